@@ -96,7 +96,7 @@ typedef int mbglu_status;
 #define MBGLU_ERR_SHAPE     2   /* M, N or K negative; M > MBGLU_MAX_M; K == 0 with the norm;
                                    add_rmsnorm_glu with one pass's rows above its shared-memory limit */
 #define MBGLU_ERR_STRIDE    3   /* a leading dimension smaller than the row it holds */
-#define MBGLU_ERR_ALIGN     4   /* a pointer not 2-byte aligned */
+#define MBGLU_ERR_ALIGN     4   /* a pointer not 2-byte aligned (or as the entry point says) */
 #define MBGLU_ERR_MODE      5   /* mode is neither FUSED nor HF */
 #define MBGLU_ERR_ALIAS     6   /* an output overlaps an input it must not overlap */
 #define MBGLU_ERR_CUDA      7   /* a CUDA runtime call failed; see mbglu_last_cuda_error() */
@@ -342,6 +342,130 @@ mbglu_status gdn_gates(const mbglu_bf16 *a, int64_t lda, const mbglu_bf16 *b, in
                        int T, int H, cudaStream_t stream);
 
 /*
+ * ---- The gated block beyond the decode batch --------------------------------
+ *
+ * glu_gemm -- glu_gemv's operation at any number of rows (a prompt, a training
+ * batch): out = SiLU(h gate_w^T) * (h up_w^T) in `mode`, both products, the
+ * activation and the product in one kernel.  No counterpart on the pages,
+ * which send such batches to a library GEMM.
+ *   h, gate_w, up_w, out, strides, mode   as glu_gemv; any M >= 0
+ *   gu      NULL, or [M][2N] fp32, row stride ldgu >= 2N: receives
+ *           g = h gate_w^T in columns [0, N) and u = h up_w^T in [N, 2N), what
+ *           glu_gemm_backward would otherwise compute again  (written)
+ * Rows beyond MBGLU_MAX_M (and any M with gu) run on the fifth-generation
+ * tensor cores where h, gate_w and up_w are 16-byte aligned with row strides
+ * that are multiples of 8 elements; other operands take a slower kernel.  Up
+ * to MBGLU_MAX_M rows without gu the call is glu_gemv.
+ * Errors as glu_gemv without the limit on M; also MBGLU_ERR_SHAPE for 2N
+ * beyond INT32_MAX, MBGLU_ERR_ALIGN for gu not 4-byte aligned and
+ * MBGLU_ERR_ALIAS where gu overlaps an operand or out.  K == 0: out = +0 and
+ * gu = 0.
+ */
+mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh,
+                      const mbglu_bf16 *gate_w, int64_t ld_gate,
+                      const mbglu_bf16 *up_w, int64_t ld_up,
+                      mbglu_bf16 *out, int64_t ldo,
+                      float *gu, int64_t ldgu,
+                      int M, int N, int K, mbglu_mode mode,
+                      cudaStream_t stream);
+
+/*
+ * glu_gemm_backward -- glu_backward's gradients at any number of rows.  g and
+ * u are read from gu (as glu_gemm wrote them) or, with gu NULL, computed again;
+ * dG = dout * u * SiLU'(g) and dU = dout * SiLU(g) are formed in fp32 and
+ * rounded once to bf16 (the tensor cores' operands); the gradients are fp32
+ * sums of their products, each rounded once to bf16.
+ *   h, gate_w, up_w, dout, grad_h, grad_gate, grad_up   as glu_backward;
+ *   any M >= 0.
+ *   workspace  device memory of glu_gemm_backward_workspace_bytes(M, N, K)
+ *              bytes, 256-byte aligned, owned by the caller; contents undefined
+ *              afterwards.  Calls that may run at the same time need different
+ *              ones.
+ * Errors as glu_backward.  Sums run in a fixed order.
+ */
+size_t glu_gemm_backward_workspace_bytes(int M, int N, int K);
+mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh,
+                               const mbglu_bf16 *gate_w, int64_t ld_gate,
+                               const mbglu_bf16 *up_w, int64_t ld_up,
+                               const mbglu_bf16 *dout, int64_t ldd,
+                               const float *gu, int64_t ldgu,
+                               mbglu_bf16 *grad_h, int64_t ldgh,
+                               mbglu_bf16 *grad_gate, int64_t ldgg,
+                               mbglu_bf16 *grad_up, int64_t ldgu_w,
+                               int M, int N, int K,
+                               void *workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
+ * The block with 8-bit operands.  e4m3 values are raw bytes; a value stands
+ * for itself times its scale, fp32.  Activations [M][K] carry a scale per row
+ * and 128 columns, [M][ceil(K/128)]; weights [N][K] one per 128 x 128 block,
+ * [ceil(N/128)][ceil(K/128)].  Row strides of scale matrices are in elements;
+ * the last dimension is contiguous everywhere.  Products accumulate in fp32
+ * within a block of 128 and are then scaled and summed in fp32; outputs are
+ * rounded once.  NaN and infinite values and scales propagate.
+ *
+ * add_rmsnorm_fp8 -- add_rmsnorm_glu's residual addition and zero-centred
+ * RMSNorm with the normed rows as e4m3:
+ *   s = bf16(x + residual)  -> residual_out
+ *   v = s (mean_k s^2 + eps)^(-1/2) (1 + norm_w)       fp32
+ *   scale = max(amax over 128 columns of |v| / 448, 2^-126),  q = e4m3(v / scale)
+ *   x, residual  [M][K] bf16, row strides ldx, ldr >= K             (read)
+ *   residual_out [M][K] bf16, row stride ldro >= K                  (written);
+ *                may be residual or x itself (same pointer and stride)
+ *   norm_w       [K] bf16
+ *   q [M][K], ldq >= K;  scale [M][ceil(K/128)], lds >= ceil(K/128)  (written)
+ *   M >= 0, K >= 1.
+ */
+mbglu_status add_rmsnorm_fp8(const mbglu_bf16 *x, int64_t ldx,
+                             const mbglu_bf16 *residual, int64_t ldr,
+                             mbglu_bf16 *residual_out, int64_t ldro,
+                             const mbglu_bf16 *norm_w, float eps,
+                             uint8_t *q, int64_t ldq,
+                             float *scale, int64_t lds,
+                             int M, int K, cudaStream_t stream);
+
+/*
+ * quantize_weight_fp8 -- a bf16 weight [N][K] to e4m3 with a scale per
+ * 128 x 128 block, by add_rmsnorm_fp8's rule for a scale.  Once per weight.
+ */
+mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw,
+                                 uint8_t *q, int64_t ldq,
+                                 float *scale, int64_t lds,
+                                 int N, int K, cudaStream_t stream);
+
+/*
+ * glu_fp8 -- out = SiLU(a gate_w^T) * (a up_w^T) of e4m3 operands, in one
+ * kernel, rounded once: to bf16 (out given, q and q_scale NULL), or to e4m3
+ * with a scale per row and 128 columns (q and q_scale given, out NULL), the
+ * operand of the down projection.  Any M, N, K >= 0; K == 0 gives +0 (scale
+ * 2^-126).  The fast kernels want a, gate_w and up_w 16-byte aligned with row
+ * strides that are multiples of 16; others take a slower kernel.
+ * MBGLU_ERR_NULL where the two output forms are mixed.
+ */
+mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas,
+                     const uint8_t *gate_w, int64_t ld_gate, const float *gate_scale, int64_t ldgs,
+                     const uint8_t *up_w, int64_t ld_up, const float *up_scale, int64_t ldus,
+                     mbglu_bf16 *out, int64_t ldo,
+                     uint8_t *q, int64_t ldq, float *q_scale, int64_t ldqs,
+                     int M, int N, int K, cudaStream_t stream);
+
+/*
+ * matmul_fp8 -- out = a w^T of e4m3 operands, bf16 [M][N]: the down
+ * projection.  The sum may be split over K into partial sums in the workspace,
+ * of matmul_fp8_workspace_bytes(M, N, K) bytes (0: none needed), 256-byte
+ * aligned, contents undefined afterwards; calls that may run at the same time
+ * need different ones.  The split depends on M, N and K alone and the partial
+ * sums are added in a fixed order.
+ */
+size_t matmul_fp8_workspace_bytes(int M, int N, int K);
+mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas,
+                        const uint8_t *w, int64_t ldw, const float *w_scale, int64_t ldws,
+                        mbglu_bf16 *out, int64_t ldo, int M, int N, int K,
+                        void *workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/*
  * Launch policy, process-wide (default MBGLU_POLICY_PREFETCH).  It decides how
  * a call's kernels are ordered after the kernel that precedes them on the
  * stream; results are identical under every policy.
@@ -359,7 +483,10 @@ mbglu_status gdn_gates(const mbglu_bf16 *a, int64_t lda, const mbglu_bf16 *b, in
  *                          dependents early (kernels that do not use
  *                          programmatic dependent launch never do: they
  *                          release at completion).  Use SERIAL or PDL around
- *                          custom early-releasing kernels that update weights.
+ *                          custom early-releasing kernels that update weights,
+ *                          and where one call's output is the very next call's
+ *                          weight: the library's kernels release early, all
+ *                          but quantize_weight_fp8's.
  * Returns MBGLU_ERR_MODE for an unknown value.
  */
 #define MBGLU_POLICY_SERIAL   0
@@ -384,7 +511,10 @@ int mbglu_last_cuda_error(void);
  * 5 silu_mul, 6 gdn_gates, 7 row blocks (a batch above MBGLU_BLOCK_M: one
  * of 1, 2, 4, 10 per block), 8 glu_backward, 9 the tcgen05 kernel (a batch
  * above MBGLU_BLOCK_M in one pass), 10 the K-slice tensor-core kernel (h's
- * fragments in registers, batch 1..16). */
+ * fragments in registers, batch 1..16); glu_gemm: 11 the CTA-pair tcgen05
+ * kernel, 12 the kernel for any alignment; 13 glu_gemm_backward, 14
+ * add_rmsnorm_fp8; e4m3 products: 15 the CTA-pair tcgen05 kernel, 16 the kernel
+ * for few rows, 17 the kernel for any alignment; 18 quantize_weight_fp8. */
 int mbglu_last_variant(void);
 
 /* Which kernels the calling thread's last glu_backward took for the
@@ -394,7 +524,9 @@ int mbglu_last_variant(void);
  * (M = 3..16; mma.sync; dG and dU enter as three bf16 terms, exact for
  * normal fp32 values).  The one-pass kernels need K % 8 == 0, 16-byte
  * aligned weights and weight gradients with row strides of whole 16-byte
- * units, and M <= 8 (CUDA cores) or M <= 16 (tensor cores). */
+ * units, and M <= 8 (CUDA cores) or M <= 16 (tensor cores).  After
+ * glu_gemm_backward: 4 the CTA-pair tcgen05 kernels, 5 the kernels for any
+ * alignment. */
 int mbglu_last_backward_path(void);
 
 /* How many row blocks of the calling thread's last add_rmsnorm_glu* call ran

@@ -8,13 +8,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmbglu.so")
-SOURCES = [os.path.join(HERE, "csrc", "mbglu_api.cu")]
-DEPS = SOURCES + [os.path.join(HERE, "csrc", f) for f in ("glu_kernels.cuh", "glu_backward.cuh", "glu_tc.cuh",
-                                                         "glu_slice.cuh", "tcgen05.cuh", "ptx.cuh")] + \
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("mbglu_api.cu", "gemm_api.cu", "fp8_api.cu")]
+DEPS = [os.path.join(HERE, "csrc", f) for f in sorted(os.listdir(os.path.join(HERE, "csrc")))] + \
     [os.path.join(ROOT, "include", "mbglu.h")]
 
 NVCC_FLAGS = [
@@ -41,10 +42,21 @@ def needs_build(out: str = LIB) -> bool:
 
 
 def build(out: str = LIB, verbose: bool = False, extra=()) -> str:
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-o", out, *SOURCES]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+    """Compiles the translation units in parallel, then links them."""
+    compile_flags = [f for f in NVCC_FLAGS if f != "-shared"]
+
+    def one(src, obj):
+        cmd = [nvcc(), *compile_flags, *extra, "-c", "-o", obj, src]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as ex:
+            for f in [ex.submit(one, s, o) for s, o in zip(SOURCES, objs)]:
+                f.result()
+        subprocess.run([nvcc(), *NVCC_FLAGS, "-o", out, *objs], check=True)
     return out
 
 

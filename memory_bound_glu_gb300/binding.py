@@ -26,6 +26,8 @@ WORKSPACE_BYTES = 256
 # Every symbol include/mbglu.h declares.
 EXPORTS = ("glu_gemv", "add_rmsnorm_glu", "add_rmsnorm_glu_ws", "add_rmsnorm_glu_strided", "add_rmsnorm_glu_noalloc",
            "silu_mul", "gdn_gates", "glu_backward", "glu_backward_workspace_bytes",
+           "glu_gemm", "glu_gemm_backward", "glu_gemm_backward_workspace_bytes", "add_rmsnorm_fp8",
+           "quantize_weight_fp8", "glu_fp8", "matmul_fp8", "matmul_fp8_workspace_bytes",
            "mbglu_set_launch_policy",
            "mbglu_get_launch_policy",
            "mbglu_status_string", "mbglu_abi_version", "mbglu_last_cuda_error", "mbglu_last_variant",
@@ -67,6 +69,24 @@ def _bind(l):
                                vp, ctypes.c_size_t, vp]
     l.glu_backward.restype = i32
     l.silu_mul.restype = i32
+    sz = ctypes.c_size_t
+    l.glu_gemm.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, vp]
+    l.glu_gemm.restype = i32
+    l.glu_gemm_backward_workspace_bytes.argtypes = [i32, i32, i32]
+    l.glu_gemm_backward_workspace_bytes.restype = sz
+    l.glu_gemm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32,
+                                    i32, vp, sz, vp]
+    l.glu_gemm_backward.restype = i32
+    l.add_rmsnorm_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, ctypes.c_float, vp, i64, vp, i64, i32, i32, vp]
+    l.add_rmsnorm_fp8.restype = i32
+    l.quantize_weight_fp8.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, vp]
+    l.quantize_weight_fp8.restype = i32
+    l.glu_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp]
+    l.glu_fp8.restype = i32
+    l.matmul_fp8_workspace_bytes.argtypes = [i32, i32, i32]
+    l.matmul_fp8_workspace_bytes.restype = sz
+    l.matmul_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, sz, vp]
+    l.matmul_fp8.restype = i32
     l.mbglu_status_string.argtypes = [i32]
     l.mbglu_status_string.restype = ctypes.c_char_p
     l.mbglu_abi_version.restype = i32
@@ -226,23 +246,36 @@ class DualWeightGlu(torch.autograd.Function):
     """out = SiLU(h @ gate_w.T) * (h @ up_w.T) with the weights read in place
     and gradients for h, gate_w and up_w ([8602/PlanB] "Plan B Design": the
     Function works on the model's own weight tensors, not on a copy, so their
-    gradients land on those tensors)."""
+    gradients land on those tensors).
+
+    Up to MAX_M rows run glu_gemv and glu_backward; more run glu_gemm, which
+    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward."""
 
     @staticmethod
     def forward(ctx, h, gate_w, up_w, mode="fused"):
+        if h.dim() == 2 and h.shape[0] > MAX_M:
+            gu = None
+            if any(ctx.needs_input_grad[:3]):
+                gu = torch.empty((h.shape[0], 2 * gate_w.shape[0]), dtype=torch.float32, device=h.device)
+            out = glu_gemm(h, gate_w, up_w, mode=mode, gu=gu)
+            ctx.save_for_backward(h, gate_w, up_w, gu)
+            return out
         ctx.save_for_backward(h, gate_w, up_w)
         return glu_gemv(h, gate_w, up_w, mode=mode)
 
     @staticmethod
     def backward(ctx, dout):
-        h, gate_w, up_w = ctx.saved_tensors
+        h, gate_w, up_w, *rest = ctx.saved_tensors
         squeeze = h.dim() == 1
         h2 = h.unsqueeze(0) if squeeze else h
         d2 = dout.reshape(h2.shape[0], -1).to(torch.bfloat16)
-        if d2.stride(-1) != 1:
+        if d2.stride(-1) != 1 or d2.stride(0) < d2.shape[1]:   # a broadcast gradient (of a sum) has stride 0
             d2 = d2.contiguous()
-        gh, gg, gu = glu_backward(h2, gate_w, up_w, d2, want_h=ctx.needs_input_grad[0],
-                                  want_w=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
+        want = dict(want_h=ctx.needs_input_grad[0], want_w=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
+        if rest:
+            gh, gg, gu = glu_gemm_backward(h2, gate_w, up_w, d2, gu=rest[0], **want)
+        else:
+            gh, gg, gu = glu_backward(h2, gate_w, up_w, d2, **want)
         if gh is not None and squeeze:
             gh = gh.view(-1)
         return gh, gg if ctx.needs_input_grad[1] else None, gu if ctx.needs_input_grad[2] else None, None
@@ -301,6 +334,252 @@ def add_rmsnorm_glu(x, residual, norm_w, eps, gate_w, up_w, out=None, mode="hf",
     if st != 0:
         raise MbgluError(st, "add_rmsnorm_glu")
     return out
+
+
+def _check_operand(t, name, dtype, shape, dev):
+    """One operand of the e4m3 (and wide bf16) calls: dtype, shape, device and
+    a contiguous last dimension; any row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+
+
+def _row_stride(t):
+    """The row stride to pass: a tensor of one row may carry any (a 1-row view's
+    stride says nothing), so it gets its row's length."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _row(t):
+    return t.data_ptr(), _row_stride(t)
+
+
+def _workspace(workspace, need, dev):
+    """(pointer, bytes) of a workspace of `need` bytes, allocated here by
+    torch's allocator on the current stream when not given."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    if workspace is None:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _allocate_on(dev, stream):
+    """Allocations of a call belong to the stream that it runs on: torch's
+    allocator hands their memory out again in that stream's order."""
+    return torch.cuda.stream(stream) if stream is not None else _on(dev)
+
+
+def glu_gemm(h, gate_w, up_w, out=None, mode="fused", gu=None, stream=None):
+    """out[M,N] = SiLU(h @ gate_w.T) * (h @ up_w.T) for any number of rows: a
+    prompt or a training batch.  Arguments as glu_gemv; gu, a float32 [M, 2N]
+    tensor, receives g and u for glu_gemm_backward.  Up to MAX_M rows without
+    gu the call is glu_gemv."""
+    bf16 = torch.bfloat16
+    squeeze = h.dim() == 1
+    h2 = h.unsqueeze(0) if squeeze else h
+    _check(h2, "h", 2)
+    _check(gate_w, "gate_w", 2)
+    M, K = h2.shape
+    N = gate_w.shape[0]
+    dev = h2.device
+    _check_operand(gate_w, "gate_w", bf16, (N, K), dev)
+    _check_operand(up_w, "up_w", bf16, (N, K), dev)
+    with _allocate_on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=bf16, device=dev)
+        out2 = out.unsqueeze(0) if out.dim() == 1 else out
+        _check_operand(out2, "out", bf16, (M, N), dev)
+        if gu is not None:
+            _check_operand(gu, "gu", torch.float32, (M, 2 * N), dev)
+        st = lib().glu_gemm(*_row(h2), *_row(gate_w), *_row(up_w), *_row(out2), *(_row(gu) if gu is not None else (None, 0)),
+                            M, N, K, _MODES[mode], _stream_handle(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "glu_gemm")
+    return out2.view(N) if squeeze else out
+
+
+def glu_gemm_backward(h, gate_w, up_w, dout, gu=None, grad_h=None, grad_gate=None, grad_up=None, want_h=True,
+                      want_w=True, workspace=None, stream=None):
+    """Gradients of glu_gemm for an upstream dout [M,N]: (grad_h, grad_gate,
+    grad_up), each None where not wanted, as glu_backward but for any number of
+    rows.  gu: what glu_gemm wrote there (computed again when not given).  The
+    workspace is a byte tensor of glu_gemm_backward_workspace_bytes(M, N, K)
+    bytes, 256-byte aligned, allocated here when not given."""
+    bf16 = torch.bfloat16
+    _check(h, "h", 2)
+    _check(gate_w, "gate_w", 2)
+    M, K = h.shape
+    N = gate_w.shape[0]
+    dev = h.device
+    _check_operand(gate_w, "gate_w", bf16, (N, K), dev)
+    _check_operand(up_w, "up_w", bf16, (N, K), dev)
+    _check_operand(dout, "dout", bf16, (M, N), dev)
+    if gu is not None:
+        _check_operand(gu, "gu", torch.float32, (M, 2 * N), dev)
+    with _allocate_on(dev, stream):
+        grads = []
+        for t, name, shape, want in ((grad_h, "grad_h", (M, K), want_h), (grad_gate, "grad_gate", (N, K), want_w),
+                                     (grad_up, "grad_up", (N, K), want_w)):
+            if not want:
+                t = None
+            elif t is None:
+                t = torch.empty(shape, dtype=bf16, device=dev)
+            else:
+                _check_operand(t, name, bf16, shape, dev)
+            grads.append(t)
+        wsp, wsb, keep = _workspace(workspace, lib().glu_gemm_backward_workspace_bytes(M, N, K), dev)
+        rows = [_row(t) if t is not None else (None, 0) for t in (gu, *grads)]
+        st = lib().glu_gemm_backward(*_row(h), *_row(gate_w), *_row(up_w), *_row(dout), *rows[0], *rows[1], *rows[2],
+                                     *rows[3], M, N, K, wsp, wsb, _stream_handle(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "glu_gemm_backward")
+    return tuple(grads)
+
+
+E4M3 = torch.float8_e4m3fn
+SCALE_BLOCK = 128   # columns (and rows, of a weight) per e4m3 scale
+
+
+def _blocks(n):
+    return -(-n // SCALE_BLOCK)
+
+
+def _empty_e4m3(M, N, dev):
+    """[M, N] e4m3 whose rows start on 16 bytes, as the products' tensor copies
+    want their operands."""
+    t = torch.empty((M, -(-N // 16) * 16), dtype=E4M3, device=dev)
+    return t if t.shape[1] == N else t[:, :N]
+
+
+def _check_scaled(t, scale, name, shape, scale_shape, dev):
+    _check_operand(t, name, E4M3, shape, dev)
+    _check_operand(scale, name + "'s scale", torch.float32, scale_shape, dev)
+
+
+def add_rmsnorm_fp8(x, residual, norm_w, eps, q=None, scale=None, residual_out=None, stream=None):
+    """residual_out <- bf16(x + residual) (in place when not given); v = its
+    zero-centred RMSNorm; returns (q, scale): v as e4m3 [M,K] with a float32
+    scale per row and 128 columns [M, ceil(K/128)]."""
+    _check(x, "x", 2)
+    M, K = x.shape
+    dev = x.device
+    if residual_out is None:
+        residual_out = residual
+    for t, name, shape in ((residual, "residual", (M, K)), (residual_out, "residual_out", (M, K)), (norm_w, "norm_w", (K,))):
+        _check_operand(t, name, torch.bfloat16, shape, dev)
+    with _allocate_on(dev, stream):
+        if q is None:
+            q = _empty_e4m3(M, K, dev)
+        if scale is None:
+            scale = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev)
+        _check_scaled(q, scale, "q", (M, K), (M, _blocks(K)), dev)
+        st = lib().add_rmsnorm_fp8(*_row(x), *_row(residual), *_row(residual_out), norm_w.data_ptr(), float(eps), *_row(q),
+                                   *_row(scale), M, K, _stream_handle(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "add_rmsnorm_fp8")
+    return q, scale
+
+
+def quantize_weight_fp8(w, q=None, scale=None, stream=None):
+    """A bf16 weight [N,K] as e4m3 with a float32 scale per 128 x 128 block:
+    returns (q, scale), scale [ceil(N/128), ceil(K/128)]."""
+    _check(w, "w", 2)
+    N, K = w.shape
+    dev = w.device
+    with _allocate_on(dev, stream):
+        if q is None:
+            q = _empty_e4m3(N, K, dev)
+        if scale is None:
+            scale = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
+        _check_scaled(q, scale, "q", (N, K), (_blocks(N), _blocks(K)), dev)
+        st = lib().quantize_weight_fp8(*_row(w), *_row(q), *_row(scale), N, K, _stream_handle(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "quantize_weight_fp8")
+    return q, scale
+
+
+def glu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale, out=None, out_scale=None, out_dtype=torch.bfloat16,
+            stream=None):
+    """SiLU(a @ gate_w.T) * (a @ up_w.T) of e4m3 operands: a [M,K] with a scale
+    per row and 128 columns (add_rmsnorm_fp8's), weights [N,K] with one per
+    128 x 128 block (quantize_weight_fp8's).  out_dtype bfloat16 returns out;
+    float8_e4m3fn returns (q, scale), the operand of matmul_fp8."""
+    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(gate_w, torch.Tensor) or gate_w.dim() != 2:
+        raise ValueError("a must be [M,K] and gate_w [N,K] tensors")
+    if out_dtype not in (torch.bfloat16, E4M3):
+        raise TypeError(f"out_dtype must be bfloat16 or float8_e4m3fn, got {out_dtype}")
+    M, K = a.shape
+    N = gate_w.shape[0]
+    dev = a.device
+    kb, nb = _blocks(K), _blocks(N)
+    _check_scaled(a, a_scale, "a", (M, K), (M, kb), dev)
+    _check_scaled(gate_w, gate_scale, "gate_w", (N, K), (nb, kb), dev)
+    _check_scaled(up_w, up_scale, "up_w", (N, K), (nb, kb), dev)
+    quant = out_dtype is E4M3
+    with _allocate_on(dev, stream):
+        if quant:
+            if out is None:
+                out = _empty_e4m3(M, N, dev)
+            if out_scale is None:
+                out_scale = torch.empty((M, nb), dtype=torch.float32, device=dev)
+            _check_scaled(out, out_scale, "out", (M, N), (M, nb), dev)
+            outs = (None, 0, *_row(out), *_row(out_scale))
+        else:
+            if out_scale is not None:
+                raise ValueError("out_scale belongs to a float8_e4m3fn output")
+            if out is None:
+                out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+            _check_operand(out, "out", torch.bfloat16, (M, N), dev)
+            outs = (*_row(out), None, 0, None, 0)
+        st = lib().glu_fp8(*_row(a), *_row(a_scale), *_row(gate_w), *_row(gate_scale), *_row(up_w), *_row(up_scale), *outs,
+                           M, N, K, _stream_handle(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "glu_fp8")
+    return (out, out_scale) if quant else out
+
+
+def matmul_fp8(a, a_scale, w, w_scale, out=None, workspace=None, stream=None):
+    """out[M,N] = a @ w.T (bf16) of e4m3 operands with the scales of glu_fp8.
+    The workspace is a byte tensor of matmul_fp8_workspace_bytes(M, N, K)
+    bytes, 256-byte aligned, allocated here when not given."""
+    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("a must be [M,K] and w [N,K] tensors")
+    M, K = a.shape
+    N = w.shape[0]
+    dev = a.device
+    kb = _blocks(K)
+    _check_scaled(a, a_scale, "a", (M, K), (M, kb), dev)
+    _check_scaled(w, w_scale, "w", (N, K), (_blocks(N), kb), dev)
+    with _allocate_on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        _check_operand(out, "out", torch.bfloat16, (M, N), dev)
+        wsp, wsb, keep = _workspace(workspace, lib().matmul_fp8_workspace_bytes(M, N, K), dev)
+        st = lib().matmul_fp8(*_row(a), *_row(a_scale), *_row(w), *_row(w_scale), *_row(out), M, N, K, wsp, wsb,
+                              _stream_handle(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "matmul_fp8")
+    return out
+
+
+def glu_gemm_backward_workspace_bytes(M, N, K):
+    """Bytes of glu_gemm_backward's workspace."""
+    return lib().glu_gemm_backward_workspace_bytes(M, N, K)
+
+
+def matmul_fp8_workspace_bytes(M, N, K):
+    """Bytes of matmul_fp8's workspace (0: none needed)."""
+    return lib().matmul_fp8_workspace_bytes(M, N, K)
 
 
 def silu_mul(x, out=None, mode="fused", stream=None):
@@ -368,14 +647,18 @@ def last_variant() -> int:
     """Kernel the calling thread's last call launched: 0 none, 1 streaming
     (CUDA-core), 2 generic, 3 zero fill, 4 tensor cores with h in shared
     memory (batch >= 3), 5 silu_mul, 6 gdn_gates, 7 row blocks, 8
-    glu_backward, 9 tcgen05, 10 the K-slice tensor-core kernel (batch 1..16)."""
+    glu_backward, 9 tcgen05, 10 the K-slice tensor-core kernel (batch 1..16),
+    11 glu_gemm on the CTA-pair tcgen05 kernel, 12 glu_gemm at any alignment,
+    13 glu_gemm_backward, 14 add_rmsnorm_fp8, 15..17 an e4m3 product (CTA pairs,
+    few rows, any alignment), 18 quantize_weight_fp8."""
     return lib().mbglu_last_variant()
 
 
 def last_backward_path() -> int:
     """The second step of the calling thread's last glu_backward: 0 none, 1
     separate kernels, 2 one pass on the CUDA cores, 3 one pass on the tensor
-    cores."""
+    cores; of glu_gemm_backward: 4 the CTA-pair tcgen05 kernels, 5 the kernels
+    for any alignment."""
     return lib().mbglu_last_backward_path()
 
 

@@ -1,0 +1,43 @@
+// dense_launch.h -- launches of the gated block's kernels beyond the decode
+// batch.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "api_internal.h"
+
+namespace mbglu_host {
+
+inline mbglu_status launched(cudaError_t e) { return e == cudaSuccess ? MBGLU_OK : cuda_fail(e); }
+
+// Launch configuration with the process's launch policy: under PDL a kernel may
+// be scheduled while its predecessor drains (every kernel here waits for the
+// predecessor before it touches global memory).
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Launch(const Launch &) = delete;   // cfg points at attr
+    Launch(dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster = 1)
+    {
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        unsigned n = 0;
+        if (launch_policy() != MBGLU_POLICY_SERIAL) {
+            attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[n].val.programmaticStreamSerializationAllowed = 1;
+            ++n;
+        }
+        if (cluster > 1) {
+            attr[n].id = cudaLaunchAttributeClusterDimension;
+            attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+            attr[n].val.clusterDim.y = 1;
+            attr[n].val.clusterDim.z = 1;
+            ++n;
+        }
+        cfg.attrs = attr;
+        cfg.numAttrs = n;
+    }
+};
+
+}  // namespace mbglu_host

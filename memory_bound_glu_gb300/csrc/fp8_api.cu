@@ -1,0 +1,210 @@
+// fp8_api.cu -- the gated block with e4m3 operands and block scales
+// (add_rmsnorm_fp8, glu_fp8, matmul_fp8, quantize_weight_fp8): host-side
+// validation, planning and launches.
+#include <algorithm>
+#include <mutex>
+
+#include "api_internal.h"
+#include "dense_generic.cuh"
+#include "dense_launch.h"
+#include "norm_fp8.cuh"
+
+namespace {
+
+using namespace mbglu_host;
+
+constexpr int64_t kBlk = mbglu::kScaleBlock;
+
+mbglu::GenOperand operand(const uint8_t *p, int64_t ld, const float *scale, int64_t lds)
+{
+    return mbglu::GenOperand{p, ld, 1, scale, lds};
+}
+
+template <int EPI, bool DUAL>
+mbglu_status launch_generic(const mbglu::GenParams &p, cudaStream_t stream)
+{
+    Launch l(mbglu::gen_grid(p.rows, p.cols), 256, 0, stream);
+    const mbglu_status st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::dense_generic_kernel<EPI, true, DUAL>, p));
+    if (st == MBGLU_OK) set_last_variant(kFp8Generic);
+    return st;
+}
+
+// One e4m3 operand with its scales: [rows][K], scales [scale_rows][blocks of K]
+struct Scaled {
+    const uint8_t *p;
+    int64_t ld;
+    const float *s;
+    int64_t lds;
+    int64_t rows, scale_rows;
+};
+
+mbglu_status check_scaled(const Scaled &o, int K)
+{
+    if (K == 0) return MBGLU_OK;
+    if (!o.p || !o.s) return MBGLU_ERR_NULL;
+    if (o.ld < K || o.lds < ceil_div(K, kBlk)) return MBGLU_ERR_STRIDE;
+    return aligned(o.s, 4) ? MBGLU_OK : MBGLU_ERR_ALIGN;
+}
+
+bool meets(const void *p, int64_t bytes, const Scaled &o, int K)
+{
+    return K > 0 && (overlaps(p, bytes, o.p, extent(o.rows, K, o.ld, 1)) ||
+                     overlaps(p, bytes, o.s, extent(o.scale_rows, ceil_div(K, kBlk), o.lds, 4)));
+}
+
+}  // namespace
+
+extern "C" {
+
+mbglu_status add_rmsnorm_fp8(const mbglu_bf16 *x, int64_t ldx, const mbglu_bf16 *residual, int64_t ldr,
+                             mbglu_bf16 *residual_out, int64_t ldro, const mbglu_bf16 *norm_w, float eps, uint8_t *q,
+                             int64_t ldq, float *scale, int64_t lds, int M, int K, cudaStream_t stream)
+{
+    set_last_variant(0);
+    if (M < 0 || K < 1) return MBGLU_ERR_SHAPE;
+    if (M == 0) return MBGLU_OK;
+    if (!x || !residual || !residual_out || !norm_w || !q || !scale) return MBGLU_ERR_NULL;
+    if (ldx < K || ldr < K || ldro < K || ldq < K || lds < ceil_div(K, kBlk)) return MBGLU_ERR_STRIDE;
+    if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(residual_out, 2) || !aligned(norm_w, 2) ||
+        !aligned(scale, 4))
+        return MBGLU_ERR_ALIGN;
+    const void *ins[3] = {x, residual, norm_w};
+    const int64_t ldi[3] = {ldx, ldr, K};
+    const int64_t inb[3] = {extent(M, K, ldx, 2), extent(M, K, ldr, 2), extent(1, K, K, 2)};
+    const void *outs[3] = {residual_out, q, scale};
+    const int64_t outb[3] = {extent(M, K, ldro, 2), extent(M, K, ldq, 1), extent(M, ceil_div(K, kBlk), lds, 4)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 3; ++j) {
+            // in place: residual_out may be x or residual itself, element by element
+            if (i == 0 && j < 2 && outs[0] == ins[j] && (ldro == ldi[j] || M == 1)) continue;
+            if (overlaps(outs[i], outb[i], ins[j], inb[j])) return MBGLU_ERR_ALIAS;
+        }
+        for (int j = i + 1; j < 3; ++j)
+            if (overlaps(outs[i], outb[i], outs[j], outb[j])) return MBGLU_ERR_ALIAS;
+    }
+    mbglu::NormFp8Params p = {x, ldx, residual, ldr, residual_out, ldro, norm_w, eps, q, ldq, scale, lds, M, K};
+    Launch l(dim3(static_cast<unsigned>(M)), 256, 0, stream);
+    const mbglu_status st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::norm_fp8_any_kernel, p));
+    if (st == MBGLU_OK) set_last_variant(kNormFp8);
+    return st;
+}
+
+mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw, uint8_t *q, int64_t ldq, float *scale, int64_t lds,
+                                 int N, int K, cudaStream_t stream)
+{
+    set_last_variant(0);
+    if (N < 0 || K < 0) return MBGLU_ERR_SHAPE;
+    if (N == 0 || K == 0) return MBGLU_OK;
+    if (!w || !q || !scale) return MBGLU_ERR_NULL;
+    if (ldw < K || ldq < K || lds < ceil_div(K, kBlk)) return MBGLU_ERR_STRIDE;
+    if (!aligned(w, 2) || !aligned(scale, 4)) return MBGLU_ERR_ALIGN;
+    const int64_t wb = extent(N, K, ldw, 2), qb = extent(N, K, ldq, 1);
+    const int64_t sb = extent(ceil_div(N, kBlk), ceil_div(K, kBlk), lds, 4);
+    if (overlaps(q, qb, w, wb) || overlaps(scale, sb, w, wb) || overlaps(q, qb, scale, sb)) return MBGLU_ERR_ALIAS;
+    const int nb = ceil_div(N, kBlk);
+    Launch l(dim3(static_cast<unsigned>(ceil_div(K, kBlk)), static_cast<unsigned>(std::min(nb, 32768))), 256, 0, stream);
+    const mbglu_status st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::quant_weight_kernel, static_cast<const uint16_t *>(w),
+                                                        ldw, q, ldq, scale, lds, N, K));
+    if (st == MBGLU_OK) set_last_variant(kQuantWeight);
+    return st;
+}
+
+size_t matmul_fp8_workspace_bytes(int M, int N, int K)
+{
+    (void)M;
+    (void)N;
+    (void)K;
+    return 0;
+}
+
+mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas, const uint8_t *w,
+                        int64_t ldw, const float *w_scale, int64_t ldws, mbglu_bf16 *out, int64_t ldo, int M, int N,
+                        int K, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    set_last_variant(0);
+    if (M < 0 || N < 0 || K < 0) return MBGLU_ERR_SHAPE;
+    if (M == 0 || N == 0) return MBGLU_OK;
+    if (!out) return MBGLU_ERR_NULL;
+    const Scaled A = {a, lda, a_scale, ldas, M, M}, W = {w, ldw, w_scale, ldws, N, ceil_div(N, kBlk)};
+    for (const Scaled *o : {&A, &W}) {
+        const mbglu_status st = check_scaled(*o, K);
+        if (st != MBGLU_OK) return st;
+    }
+    if (ldo < N) return MBGLU_ERR_STRIDE;
+    if (!aligned(out, 2)) return MBGLU_ERR_ALIGN;
+    const size_t need = matmul_fp8_workspace_bytes(M, N, K);
+    if (need && !workspace) return MBGLU_ERR_NULL;
+    if (workspace_bytes < need) return MBGLU_ERR_SHAPE;
+    if (need && !aligned(workspace, 256)) return MBGLU_ERR_ALIGN;
+    const int64_t ob = extent(M, N, ldo, 2), wsb = static_cast<int64_t>(need);
+    if (meets(out, ob, A, K) || meets(out, ob, W, K) || meets(workspace, wsb, A, K) || meets(workspace, wsb, W, K) ||
+        overlaps(out, ob, workspace, wsb))
+        return MBGLU_ERR_ALIAS;
+    mbglu::GenParams p = {};
+    p.a[0] = operand(a, lda, a_scale, ldas);
+    p.b[0] = operand(w, ldw, w_scale, ldws);
+    p.rows = M;
+    p.cols = N;
+    p.T = K;
+    p.npair = 1;
+    p.out = out;
+    p.ldo = ldo;
+    return launch_generic<mbglu::kGenPlain, false>(p, stream);
+}
+
+mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas, const uint8_t *gate_w,
+                     int64_t ld_gate, const float *gate_scale, int64_t ldgs, const uint8_t *up_w, int64_t ld_up,
+                     const float *up_scale, int64_t ldus, mbglu_bf16 *out, int64_t ldo, uint8_t *q, int64_t ldq,
+                     float *q_scale, int64_t ldqs, int M, int N, int K, cudaStream_t stream)
+{
+    set_last_variant(0);
+    if (M < 0 || N < 0 || K < 0) return MBGLU_ERR_SHAPE;
+    if (M == 0 || N == 0) return MBGLU_OK;
+    // one form of the output: bf16, or e4m3 with its scales
+    if ((out != nullptr) == (q != nullptr) || (q != nullptr) != (q_scale != nullptr)) return MBGLU_ERR_NULL;
+    const Scaled A = {a, lda, a_scale, ldas, M, M}, G = {gate_w, ld_gate, gate_scale, ldgs, N, ceil_div(N, kBlk)},
+                 U = {up_w, ld_up, up_scale, ldus, N, ceil_div(N, kBlk)};
+    for (const Scaled *o : {&A, &G, &U}) {
+        const mbglu_status st = check_scaled(*o, K);
+        if (st != MBGLU_OK) return st;
+    }
+    if (out ? ldo < N : (ldq < N || ldqs < ceil_div(N, kBlk))) return MBGLU_ERR_STRIDE;
+    if (!aligned(out, 2) || !aligned(q_scale, 4)) return MBGLU_ERR_ALIGN;
+    const int64_t ob = out ? extent(M, N, ldo, 2) : extent(M, N, ldq, 1);
+    const int64_t sb = out ? 0 : extent(M, ceil_div(N, kBlk), ldqs, 4);
+    const void *o = out ? static_cast<const void *>(out) : q;
+    for (const Scaled *in : {&A, &G, &U})
+        if (meets(o, ob, *in, K) || meets(q_scale, sb, *in, K)) return MBGLU_ERR_ALIAS;
+    if (overlaps(o, ob, q_scale, sb)) return MBGLU_ERR_ALIAS;
+    mbglu::GenParams p = {};
+    p.a[0] = operand(a, lda, a_scale, ldas);
+    p.b[0] = operand(gate_w, ld_gate, gate_scale, ldgs);
+    p.b[1] = operand(up_w, ld_up, up_scale, ldus);
+    p.rows = M;
+    p.cols = N;
+    p.T = K;
+    p.npair = 1;
+    p.mode = MBGLU_MODE_FUSED;
+    p.out = out;
+    p.ldo = ldo;
+    p.q = q;
+    p.ldq = ldq;
+    p.qs = q_scale;
+    p.ldqs = ldqs;
+    return q ? launch_generic<mbglu::kGenQuant, true>(p, stream) : launch_generic<mbglu::kGenGlu, true>(p, stream);
+}
+
+}  // extern "C"
+
+namespace mbglu_host {
+
+__device__ int g_fp8_error;
+
+cudaError_t take_fp8_error(int *w)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(w, g_fp8_error, sizeof *w);
+    const int zero = 0;
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof zero);
+}
+
+}  // namespace mbglu_host

@@ -18,6 +18,7 @@
 #include <utility>
 
 #include "mbglu.h"
+#include "api_internal.h"
 #include "glu_kernels.cuh"
 #include "glu_backward.cuh"
 #include "glu_tc.cuh"
@@ -285,15 +286,8 @@ mbglu_status device_info(const DeviceInfo **out)
     return MBGLU_OK;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// [p, p + bytes) and [q, q + bytes_q) intersect
-bool overlaps(const void *p, int64_t bytes, const void *q, int64_t bytes_q)
-{
-    if (bytes <= 0 || bytes_q <= 0) return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + static_cast<uintptr_t>(bytes_q) && b < a + static_cast<uintptr_t>(bytes);
-}
+using mbglu_host::aligned;
+using mbglu_host::overlaps;
 
 int64_t matrix_bytes(int rows, int cols, int64_t ld)
 {
@@ -557,21 +551,21 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     return fn;
 }
 
-// Tiled 2-D descriptor of a bf16 [rows][K] matrix with row stride ld, box
-// box_k x box_rows; elements past K or rows read as zero.  False if the
+// Tiled 2-D descriptor of a [rows][K] matrix (bf16, or bytes with elem_bytes
+// = 1) with row stride ld, box box_k x box_rows; elements past K or rows read as zero.  False if the
 // driver rejects it (the caller then takes a path without tensor copies).
 // The last 64 descriptors this thread encoded are kept
 // (direct-mapped on their arguments): a descriptor holds only the address,
 // the shape and the strides, so a kept one is exactly what encoding again
 // would give, whatever the memory holds now.
 bool encode_2d(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, int K, int box_k, int box_rows,
-               CUtensorMapSwizzle swizzle)
+               CUtensorMapSwizzle swizzle, int elem_bytes = 2)
 {
     static_assert(sizeof(CUtensorMap) == sizeof(mbglu::TensorMap), "tensor map size");
     struct Entry {
         const void *base = nullptr;
         int64_t ld = 0;
-        int rows = 0, K = 0, box_k = 0, box_rows = 0, swizzle = -1;
+        int rows = 0, K = 0, box_k = 0, box_rows = 0, swizzle = -1, elem_bytes = 0;
         mbglu::TensorMap map;
     };
     thread_local Entry cache[64];
@@ -580,7 +574,7 @@ bool encode_2d(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, in
                          (static_cast<uint64_t>(box_rows) << 3) ^ static_cast<uint64_t>(swizzle);
     Entry &e = cache[(hsh ^ (hsh >> 6) ^ (hsh >> 12)) & 63u];
     if (e.base == base && e.ld == ld && e.rows == rows && e.K == K && e.box_k == box_k && e.box_rows == box_rows &&
-        e.swizzle == static_cast<int>(swizzle)) {
+        e.swizzle == static_cast<int>(swizzle) && e.elem_bytes == elem_bytes) {
         *out = e.map;
         return true;
     }
@@ -588,10 +582,10 @@ bool encode_2d(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, in
     if (!fn || box_k > 256 || box_rows < 1 || box_rows > 256) return false;
     CUtensorMap m;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2u};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(elem_bytes)};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t elem_strides[2] = {1u, 1u};
-    if (fn(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, elem_strides,
+    if (fn(&m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, elem_strides,
            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
@@ -603,6 +597,7 @@ bool encode_2d(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, in
     e.box_k = box_k;
     e.box_rows = box_rows;
     e.swizzle = static_cast<int>(swizzle);
+    e.elem_bytes = elem_bytes;
     e.map = *out;
     return true;
 }
@@ -640,6 +635,25 @@ mbglu_status launch_stream(const Plan &pl, const GluParams &p, cudaStream_t stre
 #undef MBGLU_CASE
     return MBGLU_ERR_SHAPE;  // unreachable: plan_stream only produces listed tiles
 }
+
+}  // namespace
+
+namespace mbglu_host {
+
+mbglu_status cuda_fail(cudaError_t e) { return ::cuda_fail(e); }
+void set_last_variant(int v) { t_last_variant = v; }
+void set_last_backward_path(int v) { t_last_bwd = v; }
+int launch_policy() { return g_policy.load(std::memory_order_relaxed); }
+
+bool encode_tile_map(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, int cols, int box_cols,
+                     int box_rows, int elem_bytes)
+{
+    return encode_2d(out, base, ld, rows, cols, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, elem_bytes);
+}
+
+}  // namespace mbglu_host
+
+namespace {
 
 int generic_grid(const DeviceInfo &d, int N) { return std::max(1, std::min(d.sm_count * 4, (N + 7) / 8)); }
 
@@ -1932,6 +1946,11 @@ mbglu_status mbglu_read_device_error(int *word)
     if ((e = cudaMemcpyFromSymbol(&w, mbglu::g_device_error, sizeof w)) != cudaSuccess) return cuda_fail(e);
     const int zero = 0;
     if ((e = cudaMemcpyToSymbol(mbglu::g_device_error, &zero, sizeof zero)) != cudaSuccess) return cuda_fail(e);
+    for (cudaError_t (*take)(int *) : {mbglu_host::take_gemm_error, mbglu_host::take_fp8_error}) {
+        int x = 0;   // the other translation units' words
+        if ((e = take(&x)) != cudaSuccess) return cuda_fail(e);
+        if (w == 0) w = x;
+    }
     *word = w;
     return MBGLU_OK;
 }

@@ -1,0 +1,123 @@
+// norm_fp8.cuh -- residual addition, zero-centred RMSNorm and the e4m3 output
+// with a scale per 128 columns, in one pass; and the e4m3 form of a weight.
+//
+//   s = bf16(x + residual)                        (the residual stream's update)
+//   v = s (mean_k s^2 + eps)^-1/2 (1 + w)          fp32, not rounded to bf16
+//   scale = max(amax_128(|v|) / 448, 2^-126),  q = e4m3(v / scale)
+//
+// Memory-bound: 2 + 2 bytes in, 2 + 1 out per element.  A block owns a row and
+// keeps it in registers between the statistic and the output, so each byte
+// moves once.  The division by the scale is a product with 1 / scale: at most
+// 1.5 fp32 ulps before a rounding to 4 bits.
+#pragma once
+
+#include "dense_common.cuh"
+
+namespace mbglu {
+
+struct NormFp8Params {
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *residual;
+    int64_t ldr;
+    uint16_t *residual_out;
+    int64_t ldro;
+    const uint16_t *w;
+    float eps;
+    uint8_t *q;
+    int64_t ldq;
+    float *scale;
+    int64_t lds;
+    int M, K;
+};
+
+// Sum over the block (warps up to 32), the same in every thread; the order of
+// the additions is fixed.
+__device__ __forceinline__ float block_sum(float v, float *red)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int nw = blockDim.x >> 5;
+    v = 0.0f;
+    for (int i = 0; i < nw; ++i) v += red[i];
+    return v;
+}
+
+// Any K, stride and 2-byte alignment: the row is read back from residual_out
+// for the output (each block reads what it wrote itself).
+__global__ void __launch_bounds__(256) norm_fp8_any_kernel(const NormFp8Params p)
+{
+    __shared__ float red[8];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        uint16_t *ro = p.residual_out + m * p.ldro;
+        float ss = 0.0f;
+        for (int k = threadIdx.x; k < p.K; k += 256) {
+            const uint16_t s = f32_to_bf16(bf16_to_f32(p.x[m * p.ldx + k]) + bf16_to_f32(p.residual[m * p.ldr + k]));
+            ro[k] = s;
+            const float f = bf16_to_f32(s);
+            ss = fmaf(f, f, ss);
+        }
+        const float inv = rsqrtf(block_sum(ss, red) / static_cast<float>(p.K) + p.eps);
+        __syncthreads();   // the whole row is written (and red may be reused)
+        for (int g = warp; g * kScaleBlock < p.K; g += 8) {
+            float v[4], amax = 0.0f;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int k = g * kScaleBlock + lane + 32 * b;
+                v[b] = k < p.K ? bf16_to_f32(ro[k]) * inv * (1.0f + bf16_to_f32(p.w[k])) : 0.0f;
+                amax = max_nan(amax, fabsf(v[b]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float s = group_scale(amax), r = 1.0f / s;
+            if (lane == 0) p.scale[m * p.lds + g] = s;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int k = g * kScaleBlock + lane + 32 * b;
+                if (k < p.K) p.q[m * p.ldq + k] = static_cast<uint8_t>(pack_e4m3x2(v[b] * r, 0.0f));
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// A weight [N][K] bf16 to e4m3 with a scale per 128 x 128 block, one thread
+// block each.  Runs once per weight.  It does not release its dependents early:
+// what it writes is the next call's weight.
+__global__ void __launch_bounds__(256) quant_weight_kernel(const uint16_t *w, int64_t ldw, uint8_t *q, int64_t ldq,
+                                                           float *scale, int64_t lds, int N, int K)
+{
+    __shared__ float red[8];
+    grid_dependency_wait();
+    const int kb = blockIdx.x;
+    const int k0 = kb * kScaleBlock;
+    for (int64_t nb = blockIdx.y; nb * kScaleBlock < N; nb += gridDim.y) {
+        const int64_t n0 = nb * kScaleBlock;
+        float amax = 0.0f;
+        for (int e = threadIdx.x; e < kScaleBlock * kScaleBlock; e += 256) {
+            const int64_t n = n0 + e / kScaleBlock;
+            const int k = k0 + e % kScaleBlock;
+            if (n < N && k < K) amax = max_nan(amax, fabsf(bf16_to_f32(w[n * ldw + k])));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        __syncthreads();   // red of the block before is read
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+        __syncthreads();
+        for (int i = 0; i < 8; ++i) amax = max_nan(amax, red[i]);
+        const float s = group_scale(amax), r = 1.0f / s;
+        if (threadIdx.x == 0) scale[nb * lds + kb] = s;
+        for (int e = threadIdx.x; e < kScaleBlock * kScaleBlock; e += 256) {
+            const int64_t n = n0 + e / kScaleBlock;
+            const int k = k0 + e % kScaleBlock;
+            if (n < N && k < K) q[n * ldq + k] = static_cast<uint8_t>(pack_e4m3x2(bf16_to_f32(w[n * ldw + k]) * r, 0.0f));
+        }
+    }
+}
+
+}  // namespace mbglu

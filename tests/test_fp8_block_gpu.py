@@ -1,0 +1,278 @@
+"""add_rmsnorm_fp8, quantize_weight_fp8, glu_fp8 and matmul_fp8 against the
+definitions in 64 bits, alone and as the chain that a decode step runs."""
+import pytest
+import torch
+
+import dense_ref as R
+import memory_bound_glu_gb300 as mb
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+F8 = torch.float8_e4m3fn
+
+
+def rand(*shape, seed=0, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(*shape, generator=g, device=DEV) * scale
+
+
+def strided(t, pad, off=0):
+    """t's values in a wider buffer: rows `pad` elements longer, from column `off`."""
+    buf = torch.zeros((t.shape[0], t.shape[1] + pad + off), dtype=t.dtype, device=t.device)
+    view = buf[:, off:off + t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+def activations(M, K, seed=0):
+    return R.quantise_rows(rand(M, K, seed=seed).double())
+
+
+def weight(N, K, seed=0):
+    return R.quantise_blocks(rand(N, K, seed=seed, scale=K ** -0.5).double())
+
+
+def wide_rows(a, s):
+    return a.double() * R.spread_rows(s, a.shape[1])
+
+
+def wide_blocks(w, s):
+    return w.double() * R.spread_blocks(s, *w.shape)
+
+
+def check_norm(x, r, w, eps=1e-6, **kw):
+    want = (x.float() + r.float()).to(BF)
+    q, s = mb.add_rmsnorm_fp8(x, r, w, eps, **kw)
+    got = kw.get("residual_out", r)
+    assert torch.equal(got, want)
+    v = want.double()
+    h = v / torch.sqrt((v * v).mean(1, keepdim=True) + eps) * (1 + w.double())
+    # the statistic: a sum of K squares and its root, half the relative error; four more roundings
+    K = x.shape[1]
+    R.assert_e4m3(q, s, h, h.abs() * (R.acc(K) / 2 + 8 * 2.0 ** -24), "norm")
+    return q, s
+
+
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 8), (1, 127), (2, 128), (3, 129), (1, 2560), (5, 2560), (4, 4096), (2, 5000),
+                                 (3, 8192), (2, 8200), (1, 20000), (300, 640), (7, 136)])
+def test_norm_sizes(M, K):
+    check_norm(rand(M, K, seed=K).to(BF), rand(M, K, seed=K + 1, scale=3).to(BF), rand(K, seed=2, scale=0.1).to(BF))
+
+
+@pytest.mark.parametrize("pad,off", [(8, 0), (16, 8), (1, 0), (3, 1)])
+def test_norm_strides_and_separate_residual(pad, off):
+    M, K = 9, 264
+    x, r = rand(M, K, seed=1).to(BF), rand(M, K, seed=2).to(BF)
+    w = rand(K, seed=3, scale=0.1).to(BF)
+    ro = strided(torch.zeros_like(x), pad, off)
+    q = strided(torch.zeros(M, K, device=DEV), pad, off).to(F8)
+    qbuf = torch.zeros((M, K + pad + off), device=DEV).to(F8)
+    q = qbuf[:, off:off + K]
+    scale = torch.full((M, 5), 7.0, device=DEV)
+    xs, rs = strided(x, pad, off), strided(r, pad, off)
+    check_norm(xs, rs, w, residual_out=ro, q=q, scale=scale[:, :3])
+    assert torch.equal(rs, r) and (scale[:, 3:] == 7).all()
+    assert (qbuf[:, off + K:].float() == 0).all() and (qbuf[:, :off].float() == 0).all()
+    # the same as the contiguous call
+    q2, s2 = mb.add_rmsnorm_fp8(x, r.clone(), w, 1e-6)
+    assert torch.equal(q2.float(), q.float()) and torch.equal(s2, scale[:, :3])
+
+
+def test_norm_in_place_of_x():
+    x, r = rand(4, 512, seed=1).to(BF), rand(4, 512, seed=2).to(BF)
+    w = rand(512, seed=3, scale=0.1).to(BF)
+    want = check_norm(x, r, w, residual_out=torch.empty_like(x))
+    xx = x.clone()
+    got = mb.add_rmsnorm_fp8(xx, r, w, 1e-6, residual_out=xx)
+    assert torch.equal(got[0].float(), want[0].float()) and torch.equal(xx, (x.float() + r.float()).to(BF))
+
+
+def test_norm_zeros_and_not_finite():
+    x = torch.zeros(4, 384, dtype=BF, device=DEV)
+    r = torch.zeros_like(x)
+    x[1, 5] = float("nan")
+    x[2, 130] = float("inf")
+    x[3] = rand(384, seed=4).to(BF)
+    w = torch.zeros(384, dtype=BF, device=DEV)
+    q, s = mb.add_rmsnorm_fp8(x, r, w, 1e-6)
+    assert (q[0].float() == 0).all() and (s[0] == 2.0 ** -126).all()
+    assert s[1].isnan().all() and q[1].float().isnan().all()     # the statistic is NaN: so is the row
+    assert s[2, 1].isnan() and q[2, 130].float().isnan()         # inf * 0
+    assert q[3].float().isfinite().all() and s[3].isfinite().all()
+
+
+@pytest.mark.parametrize("N,K", [(1, 1), (128, 128), (129, 130), (300, 1000), (56, 264)])
+def test_quantise_weight(N, K):
+    w = rand(N, K, seed=N).to(BF)
+    w[: N // 2, : K // 2] *= 1e-3
+    q, s = mb.quantize_weight_fp8(w)
+    rq, rs = R.quantise_blocks(w.double())
+    assert ((s.double() - rs.double()).abs() <= 2.0 ** -22 * rs.double()).all()
+    ws = R.spread_blocks(s, N, K)
+    d = (q.double() * ws - w.double()).abs()
+    assert (d <= (R.EPS_E4M3 + 2.0 ** -20) * w.double().abs() + R.STEP_E4M3 * ws).all()
+    z, zs = mb.quantize_weight_fp8(torch.zeros_like(w))
+    assert (z.float() == 0).all() and (zs == 2.0 ** -126).all()
+
+
+def check_matmul(a, sa, w, sw, **kw):
+    A, W = wide_rows(a, sa), wide_blocks(w, sw)
+    out = mb.matmul_fp8(a, sa, w, sw, **kw)
+    K = a.shape[1]
+    R.assert_bf16(out, A @ W.T, R.acc(K + 4 * R.blocks(K)) * (A.abs() @ W.abs().T), "matmul")
+    assert mb.read_device_error() == 0
+    return out
+
+
+def check_glu(a, sa, g, sg, u, su, quant, **kw):
+    A, G, U = wide_rows(a, sa), wide_blocks(g, sg), wide_blocks(u, su)
+    K = a.shape[1]
+    e = R.acc(K + 4 * R.blocks(K)) * A.abs()
+    v, err = R.glu_out(A @ G.T, A @ U.T, e @ G.abs().T, e @ U.abs().T)
+    got = mb.glu_fp8(a, sa, g, sg, u, su, out_dtype=F8 if quant else BF, **kw)
+    if quant:
+        R.assert_e4m3(*got, v, err, "glu")
+    else:
+        R.assert_bf16(got, v, err, "glu")
+    assert mb.read_device_error() == 0
+    return got
+
+
+ROWS = [1, 2, 7, 8, 9, 16, 17, 31, 32, 33, 64, 65, 128, 129, 256, 257, 300]
+
+
+@pytest.mark.parametrize("M", ROWS)
+def test_matmul_rows(M):
+    check_matmul(*activations(M, 272, seed=M), *weight(200, 272, seed=1))
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("quant", [False, True])
+def test_glu_rows(M, quant):
+    check_glu(*activations(M, 272, seed=M), *weight(200, 272, seed=1), *weight(200, 272, seed=2), quant)
+
+
+@pytest.mark.parametrize("M", [3, 20, 70])
+@pytest.mark.parametrize("N,K", [(1, 16), (8, 1), (15, 128), (16, 144), (127, 256), (128, 130), (129, 384), (640, 48), (257, 1040),
+                                 (72, 4112), (1100, 112)])
+def test_columns_and_inner_dimension(M, N, K):
+    a, g, u = activations(M, K, seed=K), weight(N, K, seed=N), weight(N, K, seed=N + 1)
+    check_matmul(*a, *g)
+    check_glu(*a, *g, *u, True)
+    check_glu(*a, *g, *u, False)
+
+
+@pytest.mark.parametrize("M", [4, 40, 150])
+@pytest.mark.parametrize("pad,off", [(16, 0), (16, 16), (1, 0), (5, 3)])
+def test_operand_strides(M, pad, off):
+    K, N = 288, 136
+    (a, sa), (g, sg), (u, su) = activations(M, K), weight(N, K, seed=1), weight(N, K, seed=2)
+    a, g, u = (strided(t.view(torch.uint8), pad, off).view(F8) for t in (a, g, u))
+    sa, sg, su = (strided(t, 2, 1) for t in (sa, sg, su))
+    check_matmul(a, sa, g, sg)
+    check_glu(a, sa, g, sg, u, su, True)
+
+
+@pytest.mark.parametrize("M", [5, 40, 150])
+@pytest.mark.parametrize("pad", [0, 1, 8, 24])
+def test_what_lies_behind_the_outputs(M, pad):
+    K, N = 160, 200
+    a, g, u = activations(M, K), weight(N, K, seed=1), weight(N, K, seed=2)
+    whole = torch.full((M + 1, N + pad), 7.0, dtype=BF, device=DEV)
+    check_matmul(*a, *g, out=whole[:M, :N])
+    assert (whole[M] == 7).all() and (whole[:, N:] == 7).all()
+    q = torch.full((M + 1, N + pad), 2.0, device=DEV).to(F8)
+    s = torch.full((M + 1, 2 + pad), 7.0, device=DEV)
+    check_glu(*a, *g, *u, True, out=q[:M, :N], out_scale=s[:M, :2])
+    assert (q[M].float() == 2).all() and (q[:, N:].float() == 2).all()
+    assert (s[M] == 7).all() and (s[:, 2:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_empty_and_zero(M):
+    K, N = 256, 136
+    (a, sa), (w, sw) = activations(M, K), weight(N, K)
+    assert mb.matmul_fp8(a[:0], sa[:0], w, sw).shape == (0, N)
+    assert mb.matmul_fp8(a, sa, w[:0], sw[:0]).shape == (M, 0)
+    assert (mb.matmul_fp8(a[:, :0], sa[:, :0], w[:, :0], sw[:, :0]) == 0).all()
+    q, s = mb.glu_fp8(a[:, :0], sa[:, :0], w[:, :0], sw[:, :0], w[:, :0], sw[:, :0], out_dtype=F8)
+    assert (q.float() == 0).all() and (s == 2.0 ** -126).all()
+    z = torch.zeros_like(a)
+    q, s = mb.glu_fp8(z, sa, w, sw, w, sw, out_dtype=F8)
+    assert (q.float() == 0).all() and (s == 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("M", [3, 40, 150])
+def test_scales_of_many_sizes_and_nan(M):
+    """Scales over 60 binades, one infinite activation group, one NaN weight value."""
+    K, N = 400, 264
+    (a, sa), (w, sw) = activations(M, K), weight(N, K)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    sa = sa * torch.exp2(torch.randint(-30, 30, sa.shape, generator=gen, device=DEV).float())
+    sw = sw * torch.exp2(torch.randint(-30, 30, sw.shape, generator=gen, device=DEV).float())
+    base = check_matmul(a, sa, w, sw)
+    w2 = w.clone()
+    w2.view(torch.uint8)[130, 3] = 0x7F   # NaN
+    out = mb.matmul_fp8(a, sa, w2, sw)
+    cols = [i for i in range(N) if i != 130]
+    assert out[:, 130].isnan().all() and torch.equal(out[:, cols], base[:, cols])
+    sa2 = sa.clone()
+    sa2[1, 2] = float("nan")
+    out = mb.matmul_fp8(a, sa2, w, sw)
+    assert out[1].isnan().all() and torch.equal(out[0], base[0]) and torch.equal(out[2:], base[2:])
+
+
+@pytest.mark.parametrize("M", [1, 8, 48, 130])
+def test_decode_chain(M):
+    """norm -> gate and up -> down, as a decode step runs them, each against its
+    definition on the operands that the one before gave; then the chain once more
+    under a graph."""
+    H, N = 384, 520
+    x, r = rand(M, H, seed=1).to(BF), rand(M, H, seed=2).to(BF)
+    nw = rand(H, seed=3, scale=0.1).to(BF)
+    ws = [mb.quantize_weight_fp8((rand(*s, seed=i) * s[1] ** -0.5).to(BF)) for i, s in enumerate(((N, H), (N, H), (H, N)))]
+    ro = torch.empty_like(r)
+    q, s = check_norm(x, r, nw, residual_out=ro)
+    q2, s2 = check_glu(q, s, *ws[0], *ws[1], True)
+    y = check_matmul(q2, s2, *ws[2])
+
+    def chain():
+        q, s = mb.add_rmsnorm_fp8(x, r, nw, 1e-6, residual_out=ro)
+        return mb.matmul_fp8(*mb.glu_fp8(q, s, *ws[0], *ws[1], out_dtype=F8), *ws[2])
+
+    for _ in range(5):   # back to back, nothing waits between
+        got = chain()
+    assert torch.equal(got, y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain()
+    for _ in range(2):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, y)
+
+
+def test_two_streams_with_their_own_workspaces():
+    M, N, K = 100, 256, 4096
+    ops = [(*activations(M, K, seed=i), *weight(N, K, seed=i)) for i in (1, 2)]
+    want = [mb.matmul_fp8(*o) for o in ops]
+    streams = [torch.cuda.Stream() for _ in ops]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got = [mb.matmul_fp8(*o, stream=s) for o, s in zip(ops, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_rows_do_not_depend_on_their_place():
+    for M in (16, 48, 300):
+        a, sa = activations(M, 512, seed=3)
+        w, u = weight(264, 512, seed=4), weight(264, 512, seed=5)
+        perm = torch.randperm(M, generator=torch.Generator().manual_seed(0)).to(DEV)
+        pa = a.view(torch.uint8)[perm].view(F8)
+        assert torch.equal(mb.matmul_fp8(pa, sa[perm], *w), mb.matmul_fp8(a, sa, *w)[perm])
+        x, y = mb.glu_fp8(pa, sa[perm], *w, *u, out_dtype=F8), mb.glu_fp8(a, sa, *w, *u, out_dtype=F8)
+        assert torch.equal(x[0].float(), y[0].float()[perm]) and torch.equal(x[1], y[1][perm])

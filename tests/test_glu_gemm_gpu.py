@@ -1,0 +1,256 @@
+"""glu_gemm and glu_gemm_backward against the definitions in 64 bits: sizes
+around the tiles' edges, strides and alignments, g and u handed out, subsets of
+the gradients, differences, streams and graphs."""
+import pytest
+import torch
+
+import dense_ref as R
+import memory_bound_glu_gb300 as mb
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def rand(*shape, seed=0, scale=1.0, pad=0, off=0):
+    """bf16 normal values; pad: extra columns behind each row, off: first column of the view."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    t = (torch.randn(*shape[:-1], shape[-1] + pad + off, generator=g, device=DEV) * scale).to(BF)
+    return t[..., off:off + shape[-1]]
+
+
+def operands(M, N, K, seed=0, pad=0, off=0):
+    return (rand(M, K, seed=seed, pad=pad, off=off), rand(N, K, seed=seed + 1, scale=K ** -0.5, pad=pad, off=off),
+            rand(N, K, seed=seed + 2, scale=K ** -0.5, pad=pad, off=off))
+
+
+def check_forward(h, gw, uw, mode="fused", gu=False, out=None):
+    M, N = h.shape[0], gw.shape[0]
+    buf = torch.full((M, 2 * N), float("nan"), device=DEV) if gu else None
+    out = mb.glu_gemm(h, gw, uw, out=out, mode=mode, gu=buf)
+    g, u, eg, eu = R.glu(h.double(), gw.double(), uw.double())
+    if mode == "fused":
+        R.assert_bf16(out, *R.glu_out(g, u, eg, eu), "out")
+    else:
+        # g, u and SiLU(g) round to bf16 too: 2^-8 of each more
+        eg, eu = eg + R.EPS_BF16 * (g.abs() + eg), eu + R.EPS_BF16 * (u.abs() + eu)
+        v, e = R.glu_out(g, u, eg, eu)
+        R.assert_bf16(out, v, e + R.EPS_BF16 * (v.abs() + e), "out (hf)")
+    if gu:
+        for got, ref, err in ((buf[:, :N], g, eg), (buf[:, N:], u, eu)):
+            assert ((got.double() - ref).abs() <= err + 2.0 ** -23 * ref.abs()).all()
+    assert mb.read_device_error() == 0
+    return out
+
+
+@pytest.mark.parametrize("M", [65, 127, 128, 129, 255, 256, 257, 300, 700])
+def test_rows_around_the_tiles(M):
+    check_forward(*operands(M, 200, 136, seed=M))
+
+
+@pytest.mark.parametrize("N", [1, 2, 31, 32, 33, 64, 127, 128, 129, 257, 1000])
+def test_columns_around_the_tiles(N):
+    check_forward(*operands(100, N, 72, seed=N), gu=True)
+
+
+@pytest.mark.parametrize("K", [1, 7, 8, 16, 63, 64, 65, 128, 500, 2568])
+def test_inner_dimension(K):
+    check_forward(*operands(90, 136, K, seed=K))
+
+
+@pytest.mark.parametrize("M", [1, 2, 16, 40, 64])
+def test_few_rows(M):
+    ops = operands(M, 136, 264, seed=M)
+    out = check_forward(*ops)
+    if M <= 64:
+        assert torch.equal(out, mb.glu_gemv(*ops))
+    check_forward(*ops, gu=True)
+
+
+@pytest.mark.parametrize("mode", ["fused", "hf"])
+@pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (1, 0), (3, 2), (5, 1)])
+def test_strides_and_alignment(mode, pad, off):
+    h, gw, uw = operands(130, 96, 152, seed=pad + 10 * off, pad=pad, off=off)
+    check_forward(h, gw, uw, mode=mode)
+
+
+@pytest.mark.parametrize("pad", [0, 1, 8, 24])
+def test_output_stride_and_what_lies_behind(pad):
+    h, gw, uw = operands(130, 100, 64, seed=pad)
+    whole = torch.full((131, 100 + pad), 7.0, dtype=BF, device=DEV)
+    check_forward(h, gw, uw, out=whole[:130, :100])
+    assert (whole[:130, 100:] == 7).all() and (whole[130] == 7).all()
+
+
+def test_empty():
+    h, gw, uw = operands(70, 24, 16)
+    assert mb.glu_gemm(h[:0], gw, uw).shape == (0, 24)
+    assert mb.glu_gemm(h, gw[:0], uw[:0]).shape == (70, 0)
+    gu = torch.full((70, 48), 3.0, device=DEV)
+    out = mb.glu_gemm(h[:, :0], gw[:, :0], uw[:, :0], gu=gu)
+    assert (out == 0).all() and (gu == 0).all()
+
+
+def test_outliers_and_nan_stay_in_their_row():
+    h, gw, uw = operands(200, 136, 256, seed=4)
+    base = mb.glu_gemm(h, gw, uw)
+    h2 = h.clone()
+    h2[77, 5] = float("nan")
+    h2[100] = h2[100] * 1e30
+    out = mb.glu_gemm(h2, gw, uw)
+    rows = [i for i in range(200) if i not in (77, 100)]
+    assert torch.equal(out[rows], base[rows]) and out[77].isnan().all()
+
+
+def test_large_negative_gate():
+    h, gw, uw = operands(80, 64, 64, seed=9)
+    check_forward(h * 30, gw, uw)
+
+
+def backward_reference(h, gw, uw, d):
+    """The three gradients in 64 bits and their bounds before the last rounding."""
+    h, gw, uw, d = (t.double() for t in (h, gw, uw, d))
+    g, u, eg, eu = R.glu(h, gw, uw)
+    dg, du = d * u * R.dsilu(g), d * R.silu(g)
+    # |SiLU'| <= 1.1, |SiLU''| <= 0.5; dG and dU round to bf16
+    edg = d.abs() * (0.5 * eg * (u.abs() + eu) + 1.1 * eu) + 2.0 ** -20 * (dg.abs() + d.abs() * u.abs() * 2.0 ** -3)
+    edu = d.abs() * 1.1 * eg + 2.0 ** -20 * du.abs()
+    edg, edu = edg + R.EPS_BF16 * (dg.abs() + edg), edu + R.EPS_BF16 * (du.abs() + edu)
+    M, N = d.shape
+    gh = dg @ gw + du @ uw
+    egh = (edg + R.acc(2 * N) * dg.abs()) @ gw.abs() + (edu + R.acc(2 * N) * du.abs()) @ uw.abs()
+    ggw, egw = dg.T @ h, (edg + R.acc(M) * dg.abs()).T @ h.abs()
+    guw, euw = du.T @ h, (edu + R.acc(M) * du.abs()).T @ h.abs()
+    return (gh, egh), (ggw, egw), (guw, euw)
+
+
+def check_backward(h, gw, uw, d, gu=False, **kw):
+    buf = None
+    if gu:
+        buf = torch.empty((h.shape[0], 2 * gw.shape[0]), device=DEV)
+        mb.glu_gemm(h, gw, uw, gu=buf)
+    got = mb.glu_gemm_backward(h, gw, uw, d, gu=buf, **kw)
+    for name, x, (ref, err) in zip(("grad_h", "grad_gate", "grad_up"), got, backward_reference(h, gw, uw, d)):
+        if x is not None:
+            R.assert_bf16(x, ref, err, name)
+            # the errors are independent: in the 2-norm two roundings of half a step at most
+            rel = (x.double() - ref).norm() / ref.norm()
+            assert rel <= 2 * R.EPS_BF16, (name, rel.item())
+    assert mb.read_device_error() == 0
+    return got
+
+
+@pytest.mark.parametrize("gu", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (3, 40, 24), (65, 136, 72), (64, 64, 64), (128, 128, 256), (257, 264, 136),
+                                   (300, 1000, 520), (33, 1, 9), (100, 77, 51), (70, 129, 257), (520, 56, 64)])
+def test_backward_sizes(M, N, K, gu):
+    h, gw, uw = operands(M, N, K, seed=M + N)
+    check_backward(h, gw, uw, rand(M, N, seed=5), gu=gu)
+
+
+@pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (1, 0), (3, 2)])
+def test_backward_strides(pad, off):
+    h, gw, uw = operands(100, 96, 88, seed=pad, pad=pad, off=off)
+    d = rand(100, 96, seed=6, pad=pad, off=off)
+    outs = [torch.full((n + 1, 88 + pad), 7.0, dtype=BF, device=DEV) for n in (100, 96, 96)]
+    check_backward(h, gw, uw, d, grad_h=outs[0][:100, :88], grad_gate=outs[1][:96, :88], grad_up=outs[2][:96, :88])
+    for t in outs:
+        assert (t[-1] == 7).all() and (t[:, 88:] == 7).all()
+
+
+def test_backward_subsets():
+    h, gw, uw = operands(90, 72, 80)
+    d = rand(90, 72, seed=8)
+    whole = check_backward(h, gw, uw, d)
+    a = mb.glu_gemm_backward(h, gw, uw, d, want_w=False)
+    b = mb.glu_gemm_backward(h, gw, uw, d, want_h=False)
+    assert a[1] is None and a[2] is None and b[0] is None
+    assert torch.equal(a[0], whole[0]) and torch.equal(b[1], whole[1]) and torch.equal(b[2], whole[2])
+    assert mb.glu_gemm_backward(h, gw, uw, d, want_h=False, want_w=False) == (None, None, None)
+
+
+def test_backward_empty():
+    h, gw, uw = operands(66, 24, 16)
+    d = rand(66, 24)
+    gh, gg, gu = mb.glu_gemm_backward(h[:0], gw, uw, d[:0])
+    assert gh.shape == (0, 16) and (gg == 0).all() and (gu == 0).all()
+    gh, gg, gu = mb.glu_gemm_backward(h, gw[:0], uw[:0], d[:, :0])
+    assert (gh == 0).all() and gg.shape == (0, 16)
+
+
+def test_autograd_follows_differences():
+    """Central differences of <out, d> in 64 bits along random directions against the
+    gradients that autograd returns: two bf16 roundings of each gradient element at most."""
+    M, N, K = 80, 48, 40
+    h, gw, uw = (t.clone().requires_grad_(True) for t in operands(M, N, K, seed=3))
+    d = rand(M, N, seed=4)
+    out = mb.DualWeightGlu.apply(h, gw, uw)
+    assert torch.equal(out, mb.glu_gemm(h.detach(), gw.detach(), uw.detach()))
+    grads = torch.autograd.grad(out, (h, gw, uw), d)
+    refs = backward_reference(h.detach(), gw.detach(), uw.detach(), d)
+    f = lambda *a: (R.silu(a[0] @ a[1].T) * (a[0] @ a[2].T) * d.double()).sum()  # noqa: E731
+    base = [t.detach().double() for t in (h, gw, uw)]
+    for i, (grad, (_, err)) in enumerate(zip(grads, refs)):
+        v = torch.randn(base[i].shape, generator=torch.Generator(device=DEV).manual_seed(i), device=DEV, dtype=torch.float64)
+        t = 1e-5
+        plus, minus = list(base), list(base)
+        plus[i], minus[i] = base[i] + t * v, base[i] - t * v
+        diff = (f(*plus) - f(*minus)) / (2 * t)
+        got = (grad.double() * v).sum()
+        bound = ((err + R.EPS_BF16 * (grad.double().abs() + err)) * v.abs()).sum() + 1e-6 * diff.abs()
+        assert (got - diff).abs() <= bound
+
+
+def test_autograd_subsets_and_broadcast_gradient():
+    h, gw, uw = operands(100, 64, 48, seed=11)
+    for need in ((True, False, False), (False, True, False), (False, False, True)):
+        leaves = [t.clone().requires_grad_(n) for t, n in zip((h, gw, uw), need)]
+        mb.DualWeightGlu.apply(*leaves).float().sum().backward()   # the gradient of a sum is a broadcast
+        want = backward_reference(h, gw, uw, torch.ones(100, 64, device=DEV, dtype=BF))
+        for t, n, (ref, err) in zip(leaves, need, want):
+            assert (t.grad is not None) == n
+            if n:
+                R.assert_bf16(t.grad, ref, err)
+    col = [t.clone().requires_grad_(True) for t in (h, gw, uw)]
+    out = mb.DualWeightGlu.apply(*col)
+    (gh,) = torch.autograd.grad(out, col[0], torch.ones(1, 64, device=DEV, dtype=BF).expand(100, 64))
+    R.assert_bf16(gh, *backward_reference(h, gw, uw, torch.ones(100, 64, device=DEV, dtype=BF))[0])
+
+
+def test_deterministic_and_rows_independent():
+    h, gw, uw = operands(300, 264, 200, seed=12)
+    a, b = mb.glu_gemm(h, gw, uw), mb.glu_gemm(h, gw, uw)
+    assert torch.equal(a, b)
+    perm = torch.randperm(300, generator=torch.Generator().manual_seed(0)).to(DEV)
+    assert torch.equal(mb.glu_gemm(h[perm], gw, uw), a[perm])
+    d = rand(300, 264, seed=13)
+    for x, y in zip(mb.glu_gemm_backward(h, gw, uw, d), mb.glu_gemm_backward(h, gw, uw, d)):
+        assert torch.equal(x, y)
+
+
+def test_other_stream_and_graph():
+    h, gw, uw = operands(200, 136, 128, seed=14)
+    d = rand(200, 136, seed=15)
+    want, grads = mb.glu_gemm(h, gw, uw), mb.glu_gemm_backward(h, gw, uw, d)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = mb.glu_gemm(h, gw, uw, stream=s)
+    got = mb.glu_gemm_backward(h, gw, uw, d, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want) and all(torch.equal(x, y) for x, y in zip(got, grads))
+    out.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mb.glu_gemm(h, gw, uw, out=out)
+        got = mb.glu_gemm_backward(h, gw, uw, d)
+    h2 = rand(200, 128, seed=99)
+    keep = h.clone()
+    h.copy_(h2)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, mb.glu_gemm(h2, gw, uw))
+    assert all(torch.equal(x, y) for x, y in zip(got, mb.glu_gemm_backward(h2, gw, uw, d)))
+    h.copy_(keep)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
