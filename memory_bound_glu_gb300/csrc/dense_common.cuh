@@ -10,6 +10,9 @@
 
 namespace mbglu {
 
+// The translation unit's error word: MBGLU_ERR_TIMEOUT after a bounded wait gave up.
+static __device__ int g_dense_error;
+
 constexpr int kScaleBlock = 128;                  // columns (and, for weights, rows) per scale
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleMin = 1.17549435e-38f;      // 2^-126: the scale of a group of zeros

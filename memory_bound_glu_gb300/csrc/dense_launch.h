@@ -3,9 +3,34 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "api_internal.h"
 
 namespace mbglu_host {
+
+// The current device's SM count, after `setup` (attributes of the unit's
+// kernels) has run once on it.
+struct DeviceTable {
+    std::mutex mu;
+    int sms[64] = {};
+    mbglu_status get(int *sm_count, cudaError_t (*setup)())
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (dev < 0 || dev >= 64) return cuda_fail(cudaErrorInvalidDevice);
+        std::lock_guard<std::mutex> lk(mu);
+        if (sms[dev] == 0) {
+            int n = 0;
+            if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
+            if ((e = setup()) != cudaSuccess) return cuda_fail(e);
+            sms[dev] = n;
+        }
+        *sm_count = sms[dev];
+        return MBGLU_OK;
+    }
+};
 
 inline mbglu_status launched(cudaError_t e) { return e == cudaSuccess ? MBGLU_OK : cuda_fail(e); }
 

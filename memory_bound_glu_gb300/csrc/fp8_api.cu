@@ -198,13 +198,11 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
 
 namespace mbglu_host {
 
-__device__ int g_fp8_error;
-
 cudaError_t take_fp8_error(int *w)
 {
-    cudaError_t e = cudaMemcpyFromSymbol(w, g_fp8_error, sizeof *w);
+    cudaError_t e = cudaMemcpyFromSymbol(w, mbglu::g_dense_error, sizeof *w);
     const int zero = 0;
-    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof zero);
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(mbglu::g_dense_error, &zero, sizeof zero);
 }
 
 }  // namespace mbglu_host

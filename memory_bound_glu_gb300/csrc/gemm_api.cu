@@ -2,11 +2,11 @@
 // its backward pass (glu_gemm_backward): host-side validation, planning and
 // launches.
 #include <algorithm>
-#include <mutex>
 
 #include "api_internal.h"
 #include "dense_generic.cuh"
 #include "dense_launch.h"
+#include "pair_gemm.cuh"
 
 namespace {
 
@@ -26,6 +26,88 @@ mbglu_status launch_generic(const mbglu::GenParams &p, cudaStream_t stream)
 {
     Launch l(mbglu::gen_grid(p.rows, p.cols), 256, 0, stream);
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::dense_generic_kernel<EPI, false, DUAL>, p));
+}
+
+// ---- the CTA-pair kernels --------------------------------------------------------
+
+constexpr int kPairs = 76;   // SM pairs of the part: what a split of the inner dimension is planned for
+
+template <int EPI, int MODE, bool A_MN, bool B_MN>
+cudaError_t allow_pair()
+{
+    return cudaFuncSetAttribute(mbglu::pair_gemm_kernel<EPI, MODE, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(mbglu::kPairSmem));
+}
+
+cudaError_t setup_pair()
+{
+    cudaError_t e = allow_pair<mbglu::kPairGlu, mbglu::kPairDual, false, false>();
+    if (e == cudaSuccess) e = allow_pair<mbglu::kPairGrad, mbglu::kPairDual, false, false>();
+    if (e == cudaSuccess) e = allow_pair<mbglu::kPairPlain, mbglu::kPairSum, false, true>();
+    if (e == cudaSuccess) e = allow_pair<mbglu::kPairPlain, mbglu::kPairStack, true, true>();
+    return e;
+}
+
+mbglu_status sm_count(int *n)
+{
+    static DeviceTable table;
+    return table.get(n, setup_pair);
+}
+
+// An operand that tensor copies take: 16-byte aligned rows.
+bool copyable(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+// 2 when every row of elem-byte elements starts on 32 bytes, 1 on 16, else 0
+int row_align(const void *p, int64_t ld, int elem)
+{
+    return aligned(p, 32) && ld * elem % 32 == 0 ? 2 : aligned(p, 16) && ld * elem % 16 == 0 ? 1 : 0;
+}
+
+bool k_major(mbglu::TensorMap *m, const void *p, int64_t ld, int rows, int T)
+{
+    return encode_tile_map(m, p, ld, rows, T, 64, 128, 2);
+}
+
+// [T][cols], cols the output's index
+bool mn_major(mbglu::TensorMap *m, const void *p, int64_t ld, int T, int cols)
+{
+    return encode_tile_map(m, p, ld, T, cols, 64, 64, 2);
+}
+
+mbglu::PairPlan pair_plan(int rows, int cols, int tile_cols, int nout, int nchunk0, int nchunk, int splits)
+{
+    mbglu::PairPlan p = {};
+    p.rows = rows;
+    p.cols = cols;
+    p.mt = ceil_div(rows, mbglu::kPairTile);
+    p.nt = ceil_div(cols, tile_cols);
+    p.nout = nout;
+    p.splits = splits;
+    p.ntiles = p.mt * p.nt * nout * splits;
+    p.group = 8;
+    p.nchunk0 = nchunk0;
+    p.nchunk = nchunk;
+    return p;
+}
+
+template <int EPI, int MODE, bool A_MN, bool B_MN>
+mbglu_status launch_pair(const mbglu::PairParams &p, const mbglu::PairMaps &maps, cudaStream_t stream)
+{
+    int sms = 0;
+    const mbglu_status st = sm_count(&sms);
+    if (st != MBGLU_OK) return st;
+    Launch l(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.ntiles))), mbglu::kPairThreads, mbglu::kPairSmem,
+             stream, 2);
+    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_gemm_kernel<EPI, MODE, A_MN, B_MN>, p, maps));
+}
+
+// Ranges of the inner dimension for grad_h: where its tiles leave most SM
+// pairs idle, as many as fill them, each of at least 8 chunks.
+int grad_h_splits(int M, int N, int K)
+{
+    const int64_t tiles = static_cast<int64_t>(ceil_div(M, mbglu::kPairTile)) * ceil_div(K, mbglu::kPairTile);
+    const int64_t chunks = 2 * static_cast<int64_t>(ceil_div(N, 64));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, chunks / 8, 16})));
 }
 
 }  // namespace
@@ -56,6 +138,23 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
     // few rows: the decode kernels, which hand out no g and u
     if (M <= MBGLU_MAX_M && !gu)
         return glu_gemv(h, ldh, gate_w, ld_gate, up_w, ld_up, out, ldo, M, N, K, mode, stream);
+    mbglu::PairMaps maps;
+    if (K > 0 && copyable(h, ldh) && copyable(gate_w, ld_gate) && copyable(up_w, ld_up) && k_major(&maps.a[0], h, ldh, M, K) &&
+        k_major(&maps.b[0], gate_w, ld_gate, N, K) && k_major(&maps.b[1], up_w, ld_up, N, K)) {
+        mbglu::PairParams q = {};
+        q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), 1);
+        q.mode = static_cast<int>(mode);
+        q.out[0] = out;
+        q.ldo[0] = ldo;
+        q.out_align[0] = row_align(out, ldo, 2);
+        q.gu = gu;
+        q.ldgu = ldgu;
+        q.gu_align = gu ? row_align(gu, ldgu, 4) : 0;
+        q.gu_align_u = gu ? row_align(gu + N, ldgu, 4) : 0;
+        const mbglu_status st = launch_pair<mbglu::kPairGlu, mbglu::kPairDual, false, false>(q, maps, stream);
+        if (st == MBGLU_OK) set_last_variant(kPairGemm);
+        return st;
+    }
     mbglu::GenParams p = {};
     p.a[0] = operand(h, ldh, 1);
     p.b[0] = operand(gate_w, ld_gate, 1);
@@ -79,10 +178,14 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
 static int64_t grad_width(int N) { return (static_cast<int64_t>(N) + 63) / 64 * 64; }
 static int64_t grad_bytes(int M, int N) { return (2 * static_cast<int64_t>(M) * grad_width(N) * 2 + 255) / 256 * 256; }
 
+static int64_t part_width(int K) { return (static_cast<int64_t>(K) + 7) / 8 * 8; }
+
 size_t glu_gemm_backward_workspace_bytes(int M, int N, int K)
 {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
-    return static_cast<size_t>(grad_bytes(M, N));
+    const int splits = grad_h_splits(M, N, K);
+    const int64_t part = splits > 1 ? static_cast<int64_t>(splits) * M * part_width(K) * 4 : 0;
+    return static_cast<size_t>(grad_bytes(M, N) + part);
 }
 
 mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w, int64_t ld_gate,
@@ -135,21 +238,70 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
     const int64_t W = grad_width(N);
     uint16_t *dG = static_cast<uint16_t *>(workspace), *dU = dG + static_cast<int64_t>(M) * W;
 
-    mbglu::GenParams p = {};
-    p.a[0] = operand(h, ldh, 1);
-    p.b[0] = operand(gate_w, ld_gate, 1);
-    p.b[1] = operand(up_w, ld_up, 1);
-    p.rows = M;
-    p.cols = N;
-    p.T = K;
-    p.npair = 1;
-    p.dout = dout;
-    p.ldd = ldd;
-    p.out = dG;
-    p.out2 = dU;
-    p.ldo = W;
-    mbglu_status st = launch_generic<mbglu::kGenGrad, true>(p, stream);
-    if (st == MBGLU_OK && want_h) {   // dG Wg + dU Wu
+    const bool fast_h = copyable(h, ldh), fast_w = copyable(gate_w, ld_gate) && copyable(up_w, ld_up);
+    mbglu_status st = MBGLU_OK;
+    mbglu::PairMaps maps;
+    int path = 4;
+
+    // 1) dG, dU: from g and u as the forward kept them, or both products again
+    if (gu) {
+        const int vec = N % 8 == 0 && aligned(gu, 16) && ldgu % 4 == 0 && aligned(dout, 16) && ldd % 8 == 0;
+        const int64_t work = static_cast<int64_t>(M) * (vec ? N / 8 : N);
+        Launch l(dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, 1 << 20))), 256, 0, stream);
+        st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::glu_grad_kernel, gu, ldgu, static_cast<const uint16_t *>(dout), ldd, dG, dU,
+                                         W, M, N, vec));
+    } else if (fast_h && fast_w && k_major(&maps.a[0], h, ldh, M, K) && k_major(&maps.b[0], gate_w, ld_gate, N, K) &&
+               k_major(&maps.b[1], up_w, ld_up, N, K)) {
+        mbglu::PairParams q = {};
+        q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), 1);
+        q.out[0] = dG;
+        q.out[1] = dU;
+        q.ldo[0] = q.ldo[1] = W;
+        q.out_align[0] = row_align(dG, W, 2);
+        q.out_align[1] = row_align(dU, W, 2);
+        q.dout = dout;
+        q.ldd = ldd;
+        q.dout_align = row_align(dout, ldd, 2);
+        st = launch_pair<mbglu::kPairGrad, mbglu::kPairDual, false, false>(q, maps, stream);
+    } else {
+        path = 5;
+        mbglu::GenParams p = {};
+        p.a[0] = operand(h, ldh, 1);
+        p.b[0] = operand(gate_w, ld_gate, 1);
+        p.b[1] = operand(up_w, ld_up, 1);
+        p.rows = M;
+        p.cols = N;
+        p.T = K;
+        p.npair = 1;
+        p.dout = dout;
+        p.ldd = ldd;
+        p.out = dG;
+        p.out2 = dU;
+        p.ldo = W;
+        st = launch_generic<mbglu::kGenGrad, true>(p, stream);
+    }
+
+    // 2) grad_h = dG Wg + dU Wu: one sum over 2N
+    if (st == MBGLU_OK && want_h && fast_w && k_major(&maps.a[0], dG, W, M, N) && k_major(&maps.a[1], dU, W, M, N) &&
+        mn_major(&maps.b[0], gate_w, ld_gate, N, K) && mn_major(&maps.b[1], up_w, ld_up, N, K)) {
+        const int splits = grad_h_splits(M, N, K), chunks = ceil_div(N, 64);
+        mbglu::PairParams q = {};
+        q.plan = pair_plan(M, K, 256, 1, chunks, 2 * chunks, splits);
+        q.out[0] = grad_h;
+        q.ldo[0] = ldgh;
+        q.out_align[0] = row_align(grad_h, ldgh, 2);
+        q.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + grad_bytes(M, N));
+        q.ldp = part_width(K);
+        st = launch_pair<mbglu::kPairPlain, mbglu::kPairSum, false, true>(q, maps, stream);
+        if (st == MBGLU_OK && splits > 1) {
+            const int vec = K % 4 == 0 && aligned(grad_h, 8) && ldgh % 4 == 0;
+            const int64_t work = static_cast<int64_t>(M) * (vec ? K / 4 : K);
+            Launch l(dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, 1 << 20))), 256, 0, stream);
+            st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_join_kernel, static_cast<const float *>(q.part), splits, M, K, q.ldp,
+                                             static_cast<uint16_t *>(grad_h), ldgh, vec));
+        }
+    } else if (st == MBGLU_OK && want_h) {
+        path = 5;
         mbglu::GenParams q = {};
         q.a[0] = operand(dG, W, 1);
         q.a[1] = operand(dU, W, 1);
@@ -163,21 +315,37 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
         q.ldo = ldgh;
         st = launch_generic<mbglu::kGenPlain, false>(q, stream);
     }
-    for (int i = 0; st == MBGLU_OK && want_w && i < 2; ++i) {   // dG^T h, dU^T h
-        mbglu::GenParams q = {};
-        q.a[0] = operand(i ? dU : dG, 1, W);
-        q.b[0] = operand(h, 1, ldh);
-        q.rows = N;
-        q.cols = K;
-        q.T = M;
-        q.npair = 1;
-        q.out = i ? grad_up : grad_gate;
-        q.ldo = i ? ldgu_w : ldgg;
-        st = launch_generic<mbglu::kGenPlain, false>(q, stream);
+
+    // 3) grad_gate = dG^T h, grad_up = dU^T h: the tiles of both in one launch
+    if (st == MBGLU_OK && want_w && fast_h && mn_major(&maps.a[0], dG, W, M, N) && mn_major(&maps.a[1], dU, W, M, N) &&
+        mn_major(&maps.b[0], h, ldh, M, K)) {
+        mbglu::PairParams q = {};
+        q.plan = pair_plan(N, K, 256, 2, 0, ceil_div(M, 64), 1);
+        q.out[0] = grad_gate;
+        q.out[1] = grad_up;
+        q.ldo[0] = ldgg;
+        q.ldo[1] = ldgu_w;
+        q.out_align[0] = row_align(grad_gate, ldgg, 2);
+        q.out_align[1] = row_align(grad_up, ldgu_w, 2);
+        st = launch_pair<mbglu::kPairPlain, mbglu::kPairStack, true, true>(q, maps, stream);
+    } else if (want_w) {
+        path = 5;
+        for (int i = 0; st == MBGLU_OK && want_w && i < 2; ++i) {   // dG^T h, dU^T h
+            mbglu::GenParams q = {};
+            q.a[0] = operand(i ? dU : dG, 1, W);
+            q.b[0] = operand(h, 1, ldh);
+            q.rows = N;
+            q.cols = K;
+            q.T = M;
+            q.npair = 1;
+            q.out = i ? grad_up : grad_gate;
+            q.ldo = i ? ldgu_w : ldgg;
+            st = launch_generic<mbglu::kGenPlain, false>(q, stream);
+        }
     }
     if (st == MBGLU_OK) {
         set_last_variant(kGemmBackward);
-        set_last_backward_path(5);
+        set_last_backward_path(path);
     }
     return st;
 }
@@ -186,13 +354,11 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
 
 namespace mbglu_host {
 
-__device__ int g_gemm_error;
-
 cudaError_t take_gemm_error(int *w)
 {
-    cudaError_t e = cudaMemcpyFromSymbol(w, g_gemm_error, sizeof *w);
+    cudaError_t e = cudaMemcpyFromSymbol(w, mbglu::g_dense_error, sizeof *w);
     const int zero = 0;
-    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof zero);
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(mbglu::g_dense_error, &zero, sizeof zero);
 }
 
 }  // namespace mbglu_host

@@ -1,0 +1,427 @@
+// pair_gemm.cuh -- the pipeline of the tensor-core products on CTA pairs, and
+// the bf16 kernel on it: both projections of the gated block with their
+// epilogues, and the three gradient products.
+//
+// A cluster of two CTAs (an SM pair) owns a tile of 256 rows x 256 accumulator
+// columns; tcgen05.mma of cta_group::2 reads 128 rows of A and 128 of B from
+// each SM's shared memory, so an operand byte is brought in once per pair and
+// each SM's shared memory feeds twice the arithmetic that it would alone.  One
+// persistent cluster per SM pair walks the tiles; roles per CTA (384 threads):
+//   warp 0      tensor copies: per stage 16 KB of A and 16 KB of B
+//               (64 bf16 or 128 e4m3 of the inner dimension), 6 stages;
+//               both CTAs' copies count on the even CTA's barrier
+//   warp 1      (even CTA) issues the MMAs
+//   warp 2      owns the tensor memory: two buffers of 256 columns, so that a
+//               tile's epilogue runs under the next tile's products
+//   warps 4-11  epilogue: warp w reads lanes 32 (w % 4).., the first or second
+//               half of the columns
+// A gated tile holds 128 gate and 128 up columns of the same outputs: the even
+// CTA brings the gate rows, the odd one the up rows, and g and u of one output
+// meet in one thread.
+//
+// Tiles run along rows first within groups of `group` row tiles, so the tiles
+// in flight share operands in L2.  Every wait is bounded; after one gives up
+// each role runs its loops to the end without touching memory.
+#pragma once
+
+#include "dense_common.cuh"
+#include "tc_pair.cuh"
+
+namespace mbglu {
+
+constexpr int kPairThreads = 384;
+constexpr int kPairStages = 6;
+constexpr int kPairTile = 256;
+constexpr uint32_t kPairOperand = 16384;                   // one operand's bytes per stage and CTA
+constexpr uint32_t kPairStage = 2 * kPairOperand;
+constexpr uint32_t kPairHeader = 4096;                     // barriers, tensor-memory address, the epilogue's exchange
+constexpr uint32_t kPairExchange = 1024;                   // offset of the exchange within the header
+constexpr uint32_t kPairSmem = kPairHeader + kPairStages * kPairStage + 1024;   // + alignment
+constexpr uint32_t kPairCols = 512;
+
+// How a tile's operands are chosen.
+enum PairMode {
+    kPairDual = 0,    // b[0] rows (even CTA) and b[1] rows (odd CTA) of the same 128 outputs
+    kPairSum = 1,     // a[0] b[0] + a[1] b[1] (a[1], b[1] after nchunk0 chunks)
+    kPairStack = 2    // nout products a[o] b[0]
+};
+
+struct PairMaps {
+    TensorMap a[2], b[2];
+};
+
+struct PairPlan {
+    int rows, cols;          // of one output
+    int mt, nt, nout;        // row tiles, column tiles, outputs
+    int splits;              // ranges of the inner dimension per tile
+    int ntiles;              // mt nt nout splits
+    int group;
+    int nchunk0, nchunk;     // chunks of the first product, of all
+};
+
+struct PairTileAt {
+    int o, split, mi, ni, c0, c1;
+};
+
+__host__ __device__ inline PairTileAt pair_tile(const PairPlan &p, int t)
+{
+    PairTileAt x;
+    const int per = p.mt * p.nt;
+    x.split = t / (per * p.nout);
+    t -= x.split * per * p.nout;
+    x.o = t / per;
+    t -= x.o * per;
+    const int g = t / (p.group * p.nt), first = g * p.group;
+    const int gm = p.mt - first < p.group ? p.mt - first : p.group;
+    t -= first * p.nt;
+    x.mi = first + t % gm;
+    x.ni = t / gm;
+    x.c0 = static_cast<int>(static_cast<int64_t>(p.nchunk) * x.split / p.splits);
+    x.c1 = static_cast<int>(static_cast<int64_t>(p.nchunk) * (x.split + 1) / p.splits);
+    return x;
+}
+
+struct PairShared {
+    uint64_t *full, *empty, *acc_full, *acc_empty;
+    uint32_t *slot;
+    unsigned char *stages;
+    float *exchange;
+};
+
+__device__ __forceinline__ PairShared pair_shared(unsigned char *raw)
+{
+    unsigned char *base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    PairShared s;
+    s.full = reinterpret_cast<uint64_t *>(base);
+    s.empty = s.full + kPairStages;
+    s.acc_full = s.empty + kPairStages;
+    s.acc_empty = s.acc_full + 2;
+    s.slot = reinterpret_cast<uint32_t *>(s.acc_empty + 2);
+    s.exchange = reinterpret_cast<float *>(base + kPairExchange);
+    s.stages = base + kPairHeader;
+    return s;
+}
+
+// Barriers and tensor memory; returns the tensor-memory address.
+__device__ __forceinline__ uint32_t pair_setup(const PairShared &s, int warp)
+{
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], 16);   // the epilogue warps of both CTAs
+        }
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        pair_tmem_alloc(s.slot, kPairCols);
+        pair_tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();   // the other CTA's barriers and tensor memory exist
+    tc_fence_after();
+    return *s.slot;
+}
+
+__device__ __forceinline__ void pair_teardown(int warp, uint32_t tmem)
+{
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();   // both CTAs have read their accumulators and sent their arrivals
+    if (warp == 2) {
+        tc_fence_after();
+        pair_tmem_dealloc(tmem, kPairCols);
+    }
+}
+
+// Warp 0, one thread.  CK: elements of the inner dimension per chunk.
+template <int MODE, bool A_MN, bool B_MN, int CK>
+__device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &maps, const PairShared &s, uint32_t rank)
+{
+    bool ok = true;
+    int64_t u = 0;   // stages filled
+    for (int t = static_cast<int>(blockIdx.x >> 1); t < p.ntiles && ok; t += static_cast<int>(gridDim.x >> 1)) {
+        const PairTileAt x = pair_tile(p, t);
+        const int arow = x.mi * kPairTile + static_cast<int>(rank) * 128;
+        const int brow = MODE == kPairDual ? x.ni * 128 : x.ni * kPairTile + static_cast<int>(rank) * 128;
+        for (int c = x.c0; c < x.c1; ++c, ++u) {
+            const int st = static_cast<int>(u % kPairStages);
+            const int64_t round = u / kPairStages;
+            if (round > 0 && !mbar_wait_cluster_bounded(&s.empty[st], static_cast<uint32_t>((round - 1) & 1), kWaitLimitNs)) {
+                ok = false;
+                break;
+            }
+            const bool second = MODE == kPairSum && c >= p.nchunk0;
+            const int k = (second ? c - p.nchunk0 : c) * CK;
+            const TensorMap *ma = &maps.a[MODE == kPairSum ? second : MODE == kPairStack ? x.o : 0];
+            const TensorMap *mb = &maps.b[MODE == kPairSum ? second : MODE == kPairDual ? static_cast<int>(rank) : 0];
+            unsigned char *da = s.stages + st * kPairStage, *db = da + kPairOperand;
+            if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kPairStage);
+            const uint32_t bar = map_to_rank(&s.full[st], 0);
+            if (A_MN) {
+                pair_load_2d(da, ma, arow, k, bar);
+                pair_load_2d(da + kPairBoxBytes, ma, arow + 64, k, bar);
+            } else {
+                pair_load_2d(da, ma, k, arow, bar);
+            }
+            if (B_MN) {
+                pair_load_2d(db, mb, brow, k, bar);
+                pair_load_2d(db + kPairBoxBytes, mb, brow + 64, k, bar);
+            } else {
+                pair_load_2d(db, mb, k, brow, bar);
+            }
+        }
+    }
+    // every copy of this CTA has landed and been read, and every arrival on
+    // this CTA's barriers has come, before it may leave
+    for (int64_t v = u > kPairStages ? u - kPairStages : 0; v < u; ++v)
+        if (!mbar_wait_cluster_bounded(&s.empty[v % kPairStages], static_cast<uint32_t>((v / kPairStages) & 1), kWaitLimitNs))
+            ok = false;
+    return ok;
+}
+
+// Warp 1 of the even CTA, one thread.  PER_CHUNK: each chunk is a sum of its
+// own in the next buffer (block-scaled operands), else a tile is.
+template <bool A_MN, bool B_MN, bool E4M3, bool PER_CHUNK>
+__device__ __forceinline__ bool pair_multiply(const PairPlan &p, const PairShared &s, uint32_t tmem)
+{
+    constexpr uint32_t idesc = E4M3 ? pair_idesc_e4m3() : pair_idesc_bf16(A_MN, B_MN);
+    int64_t u = 0, v = 0;   // stages read, buffers filled
+    for (int t = static_cast<int>(blockIdx.x >> 1); t < p.ntiles; t += static_cast<int>(gridDim.x >> 1)) {
+        const PairTileAt x = pair_tile(p, t);
+        for (int c = x.c0; c < x.c1; ++c, ++u) {
+            const int buf = static_cast<int>(v & 1);
+            if ((PER_CHUNK || c == x.c0) && v >= 2 &&
+                !mbar_wait_cluster_bounded(&s.acc_empty[buf], static_cast<uint32_t>(((v >> 1) - 1) & 1), kWaitLimitNs))
+                return false;
+            const int st = static_cast<int>(u % kPairStages);
+            if (!mbar_wait_cluster_bounded(&s.full[st], static_cast<uint32_t>((u / kPairStages) & 1), kWaitLimitNs))
+                return false;
+            tc_fence_after();
+            unsigned char *da = s.stages + st * kPairStage, *db = da + kPairOperand;
+            const uint64_t ad = A_MN ? smem_desc_mn_sw128(da) : smem_desc_sw128(da);
+            const uint64_t bd = B_MN ? smem_desc_mn_sw128(db) : smem_desc_sw128(db);
+            const uint32_t d = tmem + static_cast<uint32_t>(buf) * kPairTile;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {   // 16 bf16 or 32 e4m3 each
+                const bool acc = kk > 0 || (!PER_CHUNK && c > x.c0);
+                const uint64_t a = ad + (A_MN ? 128 : 2) * kk, b = bd + (B_MN ? 128 : 2) * kk;
+                if (E4M3)
+                    pair_mma_e4m3(d, a, b, idesc, acc);
+                else
+                    pair_mma_bf16(d, a, b, idesc, acc);
+            }
+            pair_commit(&s.empty[st]);
+            if (PER_CHUNK || c == x.c1 - 1) {
+                pair_commit(&s.acc_full[buf]);
+                ++v;
+            }
+        }
+    }
+    return true;
+}
+
+enum PairEpilogue { kPairGlu = 0, kPairGrad = 1, kPairPlain = 2 };
+
+struct PairParams {
+    PairPlan plan;
+    int mode;
+    uint16_t *out[2];
+    int64_t ldo[2];
+    int out_align[2];
+    float *gu;               // g and u, [rows][2 cols], or null
+    int64_t ldgu;
+    int gu_align, gu_align_u;
+    const uint16_t *dout;
+    int64_t ldd;
+    int dout_align;
+    float *part;             // splits > 1: [splits][rows][ldp]
+    int64_t ldp;
+};
+
+template <int EPI, int MODE, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairParams p, const __grid_constant__ PairMaps maps)
+{
+    extern __shared__ unsigned char pair_raw[];
+    const PairShared s = pair_shared(pair_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t tmem = pair_setup(s, warp);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) ok = pair_produce<MODE, A_MN, B_MN, 64>(p.plan, maps, s, rank);
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) ok = pair_multiply<A_MN, B_MN, false, false>(p.plan, s, tmem);
+    } else if (warp >= 4) {
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        int64_t v = 0;
+        for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1), ++v) {
+            const PairTileAt x = pair_tile(p.plan, t);
+            const int buf = static_cast<int>(v & 1);
+            const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32 + lane;
+            const bool row = m < p.plan.rows;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&s.acc_full[buf], static_cast<uint32_t>((v >> 1) & 1), kWaitLimitNs));
+            tc_fence_after();
+            const uint32_t acc = lanes + static_cast<uint32_t>(buf) * kPairTile;
+            if constexpr (MODE == kPairDual) {
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    const int c = half * 64 + j * 32;
+                    const int n = x.ni * 128 + c, valid = p.plan.cols - n;
+                    uint32_t g[32], u[32];
+                    tmem_ld32(acc + static_cast<uint32_t>(c), g);
+                    tmem_ld32(acc + 128u + static_cast<uint32_t>(c), u);
+                    float d[32];
+                    if (EPI == kPairGrad && row && valid > 0) load_bf16_32(p.dout + m * p.ldd + n, d, valid, p.dout_align);
+                    tmem_wait_ld(g, u);
+                    if (j == 1) {   // the buffer is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(map_to_rank(&s.acc_empty[buf], 0));
+                    }
+                    if (!ok || !row || valid <= 0) continue;
+                    uint32_t w[16], w2[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
+                        const float u0 = __uint_as_float(u[2 * i]), u1 = __uint_as_float(u[2 * i + 1]);
+                        if (EPI == kPairGrad) {
+                            float dg0, du0, dg1, du1;
+                            glu_gradients(g0, u0, d[2 * i], dg0, du0);
+                            glu_gradients(g1, u1, d[2 * i + 1], dg1, du1);
+                            w[i] = pack_bf16x2(dg0, dg1);
+                            w2[i] = pack_bf16x2(du0, du1);
+                        } else if (p.mode == 0) {
+                            w[i] = pack_bf16x2(silu_f32(g0) * u0, silu_f32(g1) * u1);
+                        } else {
+                            w[i] = glu_epilogue(g0, u0, 1) | (static_cast<uint32_t>(glu_epilogue(g1, u1, 1)) << 16);
+                        }
+                    }
+                    store_bf16_32(p.out[0] + m * p.ldo[0] + n, w, valid, p.out_align[0]);
+                    if (EPI == kPairGrad) store_bf16_32(p.out[1] + m * p.ldo[1] + n, w2, valid, p.out_align[1]);
+                    if (EPI == kPairGlu && p.gu) {
+                        float f[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(g[i]);
+                        store_f32_32(p.gu + m * p.ldgu + n, f, valid, p.gu_align);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(u[i]);
+                        store_f32_32(p.gu + m * p.ldgu + p.plan.cols + n, f, valid, p.gu_align_u);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    const int c = half * 128 + j * 32;
+                    const int n = x.ni * kPairTile + c, valid = p.plan.cols - n;
+                    uint32_t r[32];
+                    tmem_ld32(acc + static_cast<uint32_t>(c), r);
+                    tmem_wait_ld(r);
+                    if (j == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(map_to_rank(&s.acc_empty[buf], 0));
+                    }
+                    if (!ok || !row || valid <= 0) continue;
+                    if (p.plan.splits > 1) {
+                        float f[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+                        store_f32_32(p.part + (static_cast<int64_t>(x.split) * p.plan.rows + m) * p.ldp + n, f, valid, 2);
+                    } else {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                        const int o = MODE == kPairStack ? x.o : 0;
+                        store_bf16_32(p.out[o] + m * p.ldo[o] + n, w, valid, p.out_align[o]);
+                    }
+                }
+            }
+        }
+    }
+    if (!ok) atomicExch(&g_dense_error, kErrTimeout);
+    pair_teardown(warp, tmem);
+}
+
+// out = bf16(sum of the splits' partial sums, in order); 4 columns per thread
+// where they lie on 8 bytes (vec), else one.
+__global__ void __launch_bounds__(256) pair_join_kernel(const float *part, int splits, int rows, int cols, int64_t ldp,
+                                                        uint16_t *out, int64_t ldo, int vec)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int per = vec ? cols / 4 : cols;
+    const int64_t total = static_cast<int64_t>(rows) * per;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t m = i / per;
+        const int c = static_cast<int>(i - m * per);
+        if (vec) {
+            float4 a = make_float4(0, 0, 0, 0);
+            for (int s = 0; s < splits; ++s) {
+                const float4 b = __ldcs(reinterpret_cast<const float4 *>(part + (s * static_cast<int64_t>(rows) + m) * ldp) + c);
+                a.x += b.x;
+                a.y += b.y;
+                a.z += b.z;
+                a.w += b.w;
+            }
+            *reinterpret_cast<uint2 *>(out + m * ldo + 4 * c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        } else {
+            float a = 0.0f;
+            for (int s = 0; s < splits; ++s) a += part[(s * static_cast<int64_t>(rows) + m) * ldp + c];
+            out[m * ldo + c] = f32_to_bf16(a);
+        }
+    }
+}
+
+// dG, dU (bf16, [rows][ldo]) from g and u as the forward kept them: one pass,
+// 8 columns per thread where everything lies on 16 bytes (vec).
+__global__ void __launch_bounds__(256) glu_grad_kernel(const float *gu, int64_t ldgu, const uint16_t *dout, int64_t ldd,
+                                                       uint16_t *dg, uint16_t *du, int64_t ldo, int rows, int cols, int vec)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int per = vec ? cols / 8 : cols;
+    const int64_t total = static_cast<int64_t>(rows) * per;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t m = i / per;
+        const int c = static_cast<int>(i - m * per);
+        if (vec) {
+            const float4 *pg = reinterpret_cast<const float4 *>(gu + m * ldgu) + 2 * c;
+            const float4 *pu = reinterpret_cast<const float4 *>(gu + m * ldgu + cols) + 2 * c;
+            const float4 g0 = __ldcs(pg), g1 = __ldcs(pg + 1), u0 = __ldcs(pu), u1 = __ldcs(pu + 1);
+            const uint4 dq = __ldcs(reinterpret_cast<const uint4 *>(dout + m * ldd) + c);
+            const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+            const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+            const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w};
+            uint32_t wg[4], wu[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a0, b0, a1, b1;
+                glu_gradients(g[2 * j], u[2 * j], bf16_lo(dw[j]), a0, b0);
+                glu_gradients(g[2 * j + 1], u[2 * j + 1], bf16_hi(dw[j]), a1, b1);
+                wg[j] = pack_bf16x2(a0, a1);
+                wu[j] = pack_bf16x2(b0, b1);
+            }
+            reinterpret_cast<uint4 *>(dg + m * ldo)[c] = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+            reinterpret_cast<uint4 *>(du + m * ldo)[c] = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+        } else {
+            float a, b;
+            glu_gradients(gu[m * ldgu + c], gu[m * ldgu + cols + c], bf16_to_f32(dout[m * ldd + c]), a, b);
+            dg[m * ldo + c] = f32_to_bf16(a);
+            du[m * ldo + c] = f32_to_bf16(b);
+        }
+    }
+}
+
+}  // namespace mbglu

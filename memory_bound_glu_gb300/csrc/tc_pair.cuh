@@ -1,0 +1,134 @@
+// tc_pair.cuh -- inline-PTX wrappers for tcgen05 on CTA pairs (cta_group::2):
+// one MMA of 256 rows spans the two SMs of a cluster of two CTAs, each holding
+// half of A's rows, half of B's rows and its own 128 accumulator lanes.
+#pragma once
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace mbglu {
+
+// Both CTAs' warps call these; the columns are taken in both SMs.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t *slot, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(ncols)
+                 : "memory");
+}
+
+__device__ __forceinline__ void pair_tmem_relinquish()
+{
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// d (+)= A B^T over both CTAs' tiles, issued by one thread of the even CTA; the
+// descriptors' addresses hold in both.
+__device__ __forceinline__ void pair_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+__device__ __forceinline__ void pair_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+// One arrival on `bar` (the same offset) in both CTAs once the MMAs that this
+// thread issued before have completed.
+__device__ __forceinline__ void pair_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// A tensor copy into this CTA's shared memory that counts its bytes on a
+// barrier of either CTA of the pair (a shared::cluster address).
+__device__ __forceinline__ void pair_load_2d(void *dst, const TensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// 32 consecutive fp32 columns of this thread's tensor-memory lane; the values
+// are there after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Waits for this warp's tensor-memory loads; the loaded registers pass through,
+// so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 :
+          "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32], uint32_t (&v)[32])
+{
+    tmem_wait_ld(r);
+    tmem_wait_ld(v);   // nothing is left to wait for: the registers' passage
+}
+
+// Shared-memory matrix descriptor of an MN-major bf16 tile in the 128-byte
+// swizzled layout: boxes of 64 MN-elements (128 bytes) x 64 K-rows, 8192 bytes
+// each, one behind the other along MN (the leading offset); groups of 8 K-rows
+// 1024 bytes apart (the stride offset).  16 K-rows further on: + 128.
+constexpr uint32_t kPairBoxBytes = 8192;
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(const void *tile)
+{
+    const uint64_t addr = smem_addr(tile);
+    return ((addr >> 4) & 0x3FFFull) | (static_cast<uint64_t>(kPairBoxBytes >> 4) << 16) | ((1024ull >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptors of a 256 x 256 tile, fp32 accumulators: bf16
+// operands, each K-major or MN-major (bits 15, 16), and e4m3 ones (K-major;
+// format code 0).
+__host__ __device__ constexpr uint32_t pair_idesc_bf16(bool a_mn, bool b_mn)
+{
+    return tc_idesc_bf16(256, 256) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+__host__ __device__ constexpr uint32_t pair_idesc_e4m3()
+{
+    return (1u << 4) | (static_cast<uint32_t>(256 >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
+}
+
+}  // namespace mbglu
