@@ -2,12 +2,13 @@
 // (add_rmsnorm_fp8, glu_fp8, matmul_fp8, quantize_weight_fp8): host-side
 // validation, planning and launches.
 #include <algorithm>
-#include <mutex>
 
 #include "api_internal.h"
 #include "dense_generic.cuh"
 #include "dense_launch.h"
+#include "fp8_pair.cuh"
 #include "norm_fp8.cuh"
+#include "pair_plan.h"
 
 namespace {
 
@@ -51,6 +52,47 @@ bool meets(const void *p, int64_t bytes, const Scaled &o, int K)
     return K > 0 && (overlaps(p, bytes, o.p, extent(o.rows, K, o.ld, 1)) ||
                      overlaps(p, bytes, o.s, extent(o.scale_rows, ceil_div(K, kBlk), o.lds, 4)));
 }
+
+template <int EPI>
+cudaError_t allow_pair()
+{
+    return cudaFuncSetAttribute(mbglu::fp8_pair_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(mbglu::kFp8Smem));
+}
+
+cudaError_t setup_fp8()
+{
+    cudaError_t e = allow_pair<mbglu::kFp8Out>();
+    if (e == cudaSuccess) e = allow_pair<mbglu::kFp8Glu>();
+    if (e == cudaSuccess) e = allow_pair<mbglu::kFp8GluQuant>();
+    return e;
+}
+
+mbglu_status sm_count(int *n)
+{
+    static DeviceTable table;
+    return table.get(n, setup_fp8);
+}
+
+bool k_major(mbglu::TensorMap *m, const Scaled &o, int K)
+{
+    return copyable(o.p, o.ld, 1) && encode_tile_map(m, o.p, o.ld, static_cast<int>(o.rows), K, 128, 128, 1);
+}
+
+template <int EPI>
+mbglu_status launch_pair(const mbglu::Fp8PairParams &p, const mbglu::PairMaps &maps, cudaStream_t stream)
+{
+    int sms = 0;
+    mbglu_status st = sm_count(&sms);
+    if (st != MBGLU_OK) return st;
+    Launch l(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.ntiles))), mbglu::kPairThreads, mbglu::kFp8Smem,
+             stream, 2);
+    st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::fp8_pair_kernel<EPI>, p, maps));
+    if (st == MBGLU_OK) set_last_variant(kFp8Pair);
+    return st;
+}
+
+int matmul_splits(int M, int N, int K) { return pair_splits(M, N, ceil_div(K, kBlk)); }
 
 }  // namespace
 
@@ -111,10 +153,9 @@ mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw, uint8_t *q, i
 
 size_t matmul_fp8_workspace_bytes(int M, int N, int K)
 {
-    (void)M;
-    (void)N;
-    (void)K;
-    return 0;
+    if (M <= 0 || N <= 0 || K <= 0) return 0;
+    const int splits = matmul_splits(M, N, K);
+    return splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(M) * static_cast<size_t>(part_width(N)) * 4 : 0;
 }
 
 mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas, const uint8_t *w,
@@ -140,6 +181,25 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
     if (meets(out, ob, A, K) || meets(out, ob, W, K) || meets(workspace, wsb, A, K) || meets(workspace, wsb, W, K) ||
         overlaps(out, ob, workspace, wsb))
         return MBGLU_ERR_ALIAS;
+    mbglu::PairMaps maps;
+    if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], W, K)) {
+        const int splits = matmul_splits(M, N, K), chunks = ceil_div(K, kBlk);
+        mbglu::Fp8PairParams q = {};
+        q.plan = pair_plan(M, N, 256, 1, chunks, chunks, splits);
+        q.as = a_scale;
+        q.ldas = ldas;
+        q.ws[0] = w_scale;
+        q.ldws[0] = ldws;
+        q.wblocks = ceil_div(N, kBlk);
+        q.out = out;
+        q.ldo = ldo;
+        q.out_align = row_align(out, ldo, 2);
+        q.part = static_cast<float *>(workspace);
+        q.ldp = part_width(N);
+        mbglu_status st = launch_pair<mbglu::kFp8Out>(q, maps, stream);
+        if (st == MBGLU_OK && splits > 1) st = launch_join(q.part, splits, M, N, out, ldo, stream);
+        return st;
+    }
     mbglu::GenParams p = {};
     p.a[0] = operand(a, lda, a_scale, ldas);
     p.b[0] = operand(w, ldw, w_scale, ldws);
@@ -176,6 +236,27 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
     for (const Scaled *in : {&A, &G, &U})
         if (meets(o, ob, *in, K) || meets(q_scale, sb, *in, K)) return MBGLU_ERR_ALIAS;
     if (overlaps(o, ob, q_scale, sb)) return MBGLU_ERR_ALIAS;
+    mbglu::PairMaps maps;
+    if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], G, K) && k_major(&maps.b[1], U, K)) {
+        mbglu::Fp8PairParams p = {};
+        p.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, kBlk), 1);
+        p.as = a_scale;
+        p.ldas = ldas;
+        p.ws[0] = gate_scale;
+        p.ldws[0] = ldgs;
+        p.ws[1] = up_scale;
+        p.ldws[1] = ldus;
+        p.wblocks = ceil_div(N, kBlk);
+        p.out = out;
+        p.ldo = ldo;
+        p.out_align = out ? row_align(out, ldo, 2) : 0;
+        p.q = q;
+        p.ldq = ldq;
+        p.q_align = q ? row_align(q, ldq, 1) : 0;
+        p.qs = q_scale;
+        p.ldqs = ldqs;
+        return q ? launch_pair<mbglu::kFp8GluQuant>(p, maps, stream) : launch_pair<mbglu::kFp8Glu>(p, maps, stream);
+    }
     mbglu::GenParams p = {};
     p.a[0] = operand(a, lda, a_scale, ldas);
     p.b[0] = operand(gate_w, ld_gate, gate_scale, ldgs);

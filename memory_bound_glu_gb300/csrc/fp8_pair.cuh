@@ -1,0 +1,264 @@
+// fp8_pair.cuh -- the products of e4m3 operands with block scales on CTA pairs:
+// the pipeline of pair_gemm.cuh with 128 bytes of the inner dimension per
+// stage, so that a stage is one scale block.
+//
+//   out[m, n] = sum_b sa[m, b] sw[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
+//
+// The inner sum of a block is formed by the tensor cores in one of two
+// tensor-memory buffers; while the next block runs into the other, the eight
+// epilogue warps read it (128 columns per thread and block), scale it and add
+// it to fp32 totals in registers.  A thread's columns lie in one 128-row block
+// of the weight (or 64 + 64 in one block of each weight), so the scale of a
+// block is one or two products per thread.  Per block and SM the MMAs take 512
+// cycles at the dense e4m3 rate, the totals' FMAs 256 (packed pairs, 2 x 64
+// per thread and scheduler) and the tensor-memory reads 256: they fit under
+// the MMAs, which is why the totals may stay out of the tensor memory.
+#pragma once
+
+#include "pair_gemm.cuh"
+
+namespace mbglu {
+
+enum Fp8Epilogue { kFp8Out = 0, kFp8Glu = 1, kFp8GluQuant = 2 };
+
+struct Fp8PairParams {
+    PairPlan plan;
+    const float *as;          // a's scales
+    int64_t ldas;
+    const float *ws[2];       // the weights' scales
+    int64_t ldws[2];
+    int wblocks;              // scale rows of a weight
+    uint16_t *out;
+    int64_t ldo;
+    int out_align;
+    uint8_t *q;
+    int64_t ldq;
+    int q_align;
+    float *qs;
+    int64_t ldqs;
+    float *part;
+    int64_t ldp;
+};
+
+// 32 e4m3 values (8 words) of one row
+__device__ __forceinline__ void store_e4m3_32(uint8_t *p, const uint32_t (&w)[8], int valid, int align)
+{
+    if (valid >= 32 && align == 2) {
+        st_global_32B(p, w);
+    } else if (valid >= 32 && align == 1) {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < valid) p[i] = static_cast<uint8_t>(w[i >> 2] >> ((i & 3) * 8));
+    }
+}
+
+// The scales of 8 blocks at a time, staged by an otherwise idle warp: a thread's
+// own row of a's scales is one line per lane and load, which costs the epilogue
+// 32 cache accesses per warp and block (4096 x 4864 x 11008: 238 us against
+// XXX us from shared memory).
+constexpr int kScaleGroup = 8;
+struct ScaleStage {
+    float a[kScaleGroup][132];   // this CTA's rows; 4 words of padding spread a load over the banks
+    float w[2][kScaleGroup];     // weights: blocks 2 ni and 2 ni + 1, or gate and up
+};
+constexpr uint32_t kFp8Smem = kPairSmem + 2 * sizeof(ScaleStage);
+
+// acc += f (lo, hi), one packed FMA.  Volatile: kept in order with the loads
+// around it, so that no more than two steps' columns are held at a time.
+__device__ __forceinline__ void scale_add(float2 &acc, uint32_t lo, uint32_t hi, float f)
+{
+    asm volatile(
+        "{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "r"(lo), "r"(hi), "f"(f));
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8PairParams p, const __grid_constant__ PairMaps maps)
+{
+    constexpr bool kDual = EPI != kFp8Out;
+    constexpr int kMode = kDual ? kPairDual : kPairSum;
+    extern __shared__ unsigned char pair_raw[];
+    const PairShared s = pair_shared(pair_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    ScaleStage *scales = reinterpret_cast<ScaleStage *>(s.stages + kPairStages * kPairStage);
+    uint64_t *scale_full = reinterpret_cast<uint64_t *>(s.slot + 2), *scale_empty = scale_full + 2;
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&scale_full[i], 1);
+            mbar_init(&scale_empty[i], 8);
+        }
+        fence_mbar_init();
+    }
+    const uint32_t tmem = pair_setup(s, warp);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    bool ok = true;
+    // three warps share a scheduler's registers: 168 each at launch; the eight
+    // epilogue warps, which hold 128 totals per thread, take what the others leave
+    // (128 x 88 + 256 x 208 registers of 384 x 168)
+    if (warp < kPairEpilogue) {
+        regs_release<88>();
+        if (warp == 0 && lane == 0) ok = pair_produce<kMode, false, false, 128>(p.plan, maps, s, rank);
+        if (warp == 1 && lane == 0 && rank == 0) ok = pair_multiply<false, false, true, true>(p.plan, s, tmem);
+        if (warp == 2) {
+            uint32_t g = 0;
+            for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1)) {
+                const PairTileAt x = pair_tile(p.plan, t);
+                const int m0 = x.mi * kPairTile + static_cast<int>(rank) * 128;
+                for (int c = x.c0; c < x.c1; c += kScaleGroup, ++g) {
+                    ScaleStage &st = scales[g & 1];
+                    float w = 0.0f;   // lanes 0-7: the first weight block, 8-15: the second
+                    {
+                        const int second = lane >> 3, b = c + (lane & 7);
+                        const int wb = kDual ? x.ni : 2 * x.ni + second;
+                        if (second < 2 && b < x.c1 && wb < p.wblocks)
+                            w = __ldg((kDual && second ? p.ws[1] + wb * p.ldws[1] : p.ws[0] + wb * p.ldws[0]) + b);
+                    }
+                    if (g >= 2 && ok) ok = __all_sync(0xffffffffu, pair_wait(&scale_empty[g & 1], ((g >> 1) - 1) & 1, kWaitLimitNs));
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 32; i0 += 16) {   // 4 rows x 8 blocks per load
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int m = m0 + 4 * (i0 + i) + (lane >> 3), b = c + (lane & 7);
+                            v[i] = m < p.plan.rows && b < x.c1 ? __ldg(p.as + m * p.ldas + b) : 0.0f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) st.a[lane & 7][4 * (i0 + i) + (lane >> 3)] = v[i];
+                    }
+                    if (lane < 16) st.w[lane >> 3][lane & 7] = w;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&scale_full[g & 1]);
+                }
+            }
+        }
+    } else {
+        regs_take<208>();
+        const int q = warp & 3, half = (warp - kPairEpilogue) >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        // this thread's accumulator columns: [c0, c0 + 64) and [c1, c1 + 64)
+        const int c0 = kDual ? half * 64 : half * 128, c1 = kDual ? 128 + half * 64 : half * 128 + 64;
+        uint32_t v = 0, tiles = 0, g = 0;
+        for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1), ++tiles) {
+            const PairTileAt x = pair_tile(p.plan, t);
+            const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32 + lane;
+            const bool row = m < p.plan.rows;
+            float2 acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int c = x.c0; c < x.c1; ++c, ++v) {
+                const int buf = static_cast<int>(v & 1), in = (c - x.c0) & (kScaleGroup - 1);
+                if (in == 0 && ok) ok = __all_sync(0xffffffffu, pair_wait(&scale_full[g & 1], (g >> 1) & 1, kWaitLimitNs));
+                const ScaleStage &sc = scales[g & 1];
+                const float sa = sc.a[in][q * 32 + lane];
+                const float f0 = sa * sc.w[kDual ? 0 : half][in], f1 = kDual ? sa * sc.w[1][in] : f0;
+                if (in == kScaleGroup - 1 || c == x.c1 - 1) {   // the group is read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&scale_empty[g & 1]);
+                    ++g;
+                }
+                if (ok)
+                    ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], (v >> 1) & 1,
+                                                                           kWaitLimitNs));
+                tc_fence_after();
+                const uint32_t from = lanes + static_cast<uint32_t>(buf) * kPairTile;
+                // a step's FMAs run while the next step's columns arrive
+                uint32_t r[2][32];
+                tmem_ld32(from + static_cast<uint32_t>(c0), r[0]);
+                tmem_wait_ld(r[0]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j < 3) tmem_ld32(from + static_cast<uint32_t>((j < 1 ? c0 : c1) + (~j & 1) * 32), r[(j + 1) & 1]);
+                    const float f = j < 2 ? f0 : f1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) scale_add(acc[16 * j + i], r[j & 1][2 * i], r[j & 1][2 * i + 1], f);
+                    if (j < 3) tmem_wait_ld(r[(j + 1) & 1]);
+                    if (j == 2) {   // the buffer is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
+                    }
+                }
+            }
+            if constexpr (EPI == kFp8Out) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = x.ni * kPairTile + c0 + 32 * j, valid = p.plan.cols - n;
+                    if (!ok || !row || valid <= 0) continue;
+                    if (p.plan.splits > 1) {
+                        float f[32];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            f[2 * i] = acc[16 * j + i].x;
+                            f[2 * i + 1] = acc[16 * j + i].y;
+                        }
+                        store_f32_32(p.part + (static_cast<int64_t>(x.split) * p.plan.rows + m) * p.ldp + n, f, valid, 2);
+                    } else {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(acc[16 * j + i].x, acc[16 * j + i].y);
+                        store_bf16_32(p.out + m * p.ldo + n, w, valid, p.out_align);
+                    }
+                }
+            } else {
+                // g in acc[0..31], u in acc[32..63]: SiLU(g) u over g
+                const int n0 = x.ni * 128 + half * 64;
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    acc[i].x = silu_f32(acc[i].x) * acc[32 + i].x;
+                    acc[i].y = silu_f32(acc[i].y) * acc[32 + i].y;
+                    // columns past the last are sums over zeros unless a scale is
+                    // not finite; they are no part of the group
+                    if (EPI == kFp8GluQuant) {
+                        if (n0 + 2 * i < p.plan.cols) amax = max_nan(amax, fabsf(acc[i].x));
+                        if (n0 + 2 * i + 1 < p.plan.cols) amax = max_nan(amax, fabsf(acc[i].y));
+                    }
+                }
+                float scale = 0.0f, inv = 0.0f;
+                if constexpr (EPI == kFp8GluQuant) {
+                    // the other 64 columns' maximum, from the warp that has them
+                    float *ex = s.exchange + (tiles & 1) * 256;
+                    ex[half * 128 + q * 32 + lane] = amax;
+                    bar_sync_named(1, 256);
+                    amax = max_nan(amax, ex[(half ^ 1) * 128 + q * 32 + lane]);
+                    scale = group_scale(amax);
+                    inv = 1.0f / scale;
+                    if (ok && row && half == 0) p.qs[m * p.ldqs + x.ni] = scale;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int n = n0 + 32 * j, valid = p.plan.cols - n;
+                    if (!ok || !row || valid <= 0) continue;
+                    if constexpr (EPI == kFp8GluQuant) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 a = acc[16 * j + 2 * i], b = acc[16 * j + 2 * i + 1];
+                            w[i] = pack_e4m3x4(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
+                        }
+                        store_e4m3_32(p.q + m * p.ldq + n, w, valid, p.q_align);
+                    } else {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(acc[16 * j + i].x, acc[16 * j + i].y);
+                        store_bf16_32(p.out + m * p.ldo + n, w, valid, p.out_align);
+                    }
+                }
+            }
+        }
+    }
+    if (!ok) atomicExch(&g_dense_error, kErrTimeout);
+    pair_teardown(warp, tmem);
+}
+
+}  // namespace mbglu

@@ -6,7 +6,9 @@
 #include "api_internal.h"
 #include "dense_generic.cuh"
 #include "dense_launch.h"
+#include "glu_grad.cuh"
 #include "pair_gemm.cuh"
+#include "pair_plan.h"
 
 namespace {
 
@@ -30,8 +32,6 @@ mbglu_status launch_generic(const mbglu::GenParams &p, cudaStream_t stream)
 
 // ---- the CTA-pair kernels --------------------------------------------------------
 
-constexpr int kPairs = 76;   // SM pairs of the part: what a split of the inner dimension is planned for
-
 template <int EPI, int MODE, bool A_MN, bool B_MN>
 cudaError_t allow_pair()
 {
@@ -54,15 +54,6 @@ mbglu_status sm_count(int *n)
     return table.get(n, setup_pair);
 }
 
-// An operand that tensor copies take: 16-byte aligned rows.
-bool copyable(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
-
-// 2 when every row of elem-byte elements starts on 32 bytes, 1 on 16, else 0
-int row_align(const void *p, int64_t ld, int elem)
-{
-    return aligned(p, 32) && ld * elem % 32 == 0 ? 2 : aligned(p, 16) && ld * elem % 16 == 0 ? 1 : 0;
-}
-
 bool k_major(mbglu::TensorMap *m, const void *p, int64_t ld, int rows, int T)
 {
     return encode_tile_map(m, p, ld, rows, T, 64, 128, 2);
@@ -72,22 +63,6 @@ bool k_major(mbglu::TensorMap *m, const void *p, int64_t ld, int rows, int T)
 bool mn_major(mbglu::TensorMap *m, const void *p, int64_t ld, int T, int cols)
 {
     return encode_tile_map(m, p, ld, T, cols, 64, 64, 2);
-}
-
-mbglu::PairPlan pair_plan(int rows, int cols, int tile_cols, int nout, int nchunk0, int nchunk, int splits)
-{
-    mbglu::PairPlan p = {};
-    p.rows = rows;
-    p.cols = cols;
-    p.mt = ceil_div(rows, mbglu::kPairTile);
-    p.nt = ceil_div(cols, tile_cols);
-    p.nout = nout;
-    p.splits = splits;
-    p.ntiles = p.mt * p.nt * nout * splits;
-    p.group = 8;
-    p.nchunk0 = nchunk0;
-    p.nchunk = nchunk;
-    return p;
 }
 
 template <int EPI, int MODE, bool A_MN, bool B_MN>
@@ -101,13 +76,9 @@ mbglu_status launch_pair(const mbglu::PairParams &p, const mbglu::PairMaps &maps
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_gemm_kernel<EPI, MODE, A_MN, B_MN>, p, maps));
 }
 
-// Ranges of the inner dimension for grad_h: where its tiles leave most SM
-// pairs idle, as many as fill them, each of at least 8 chunks.
 int grad_h_splits(int M, int N, int K)
 {
-    const int64_t tiles = static_cast<int64_t>(ceil_div(M, mbglu::kPairTile)) * ceil_div(K, mbglu::kPairTile);
-    const int64_t chunks = 2 * static_cast<int64_t>(ceil_div(N, 64));
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, chunks / 8, 16})));
+    return pair_splits(M, K, 2 * static_cast<int64_t>(ceil_div(N, 64)));
 }
 
 }  // namespace
@@ -139,7 +110,7 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
     if (M <= MBGLU_MAX_M && !gu)
         return glu_gemv(h, ldh, gate_w, ld_gate, up_w, ld_up, out, ldo, M, N, K, mode, stream);
     mbglu::PairMaps maps;
-    if (K > 0 && copyable(h, ldh) && copyable(gate_w, ld_gate) && copyable(up_w, ld_up) && k_major(&maps.a[0], h, ldh, M, K) &&
+    if (K > 0 && copyable(h, ldh, 2) && copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2) && k_major(&maps.a[0], h, ldh, M, K) &&
         k_major(&maps.b[0], gate_w, ld_gate, N, K) && k_major(&maps.b[1], up_w, ld_up, N, K)) {
         mbglu::PairParams q = {};
         q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), 1);
@@ -177,8 +148,6 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
 // starts on 128 bytes
 static int64_t grad_width(int N) { return (static_cast<int64_t>(N) + 63) / 64 * 64; }
 static int64_t grad_bytes(int M, int N) { return (2 * static_cast<int64_t>(M) * grad_width(N) * 2 + 255) / 256 * 256; }
-
-static int64_t part_width(int K) { return (static_cast<int64_t>(K) + 7) / 8 * 8; }
 
 size_t glu_gemm_backward_workspace_bytes(int M, int N, int K)
 {
@@ -238,7 +207,7 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
     const int64_t W = grad_width(N);
     uint16_t *dG = static_cast<uint16_t *>(workspace), *dU = dG + static_cast<int64_t>(M) * W;
 
-    const bool fast_h = copyable(h, ldh), fast_w = copyable(gate_w, ld_gate) && copyable(up_w, ld_up);
+    const bool fast_h = copyable(h, ldh, 2), fast_w = copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2);
     mbglu_status st = MBGLU_OK;
     mbglu::PairMaps maps;
     int path = 4;
@@ -293,13 +262,7 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
         q.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + grad_bytes(M, N));
         q.ldp = part_width(K);
         st = launch_pair<mbglu::kPairPlain, mbglu::kPairSum, false, true>(q, maps, stream);
-        if (st == MBGLU_OK && splits > 1) {
-            const int vec = K % 4 == 0 && aligned(grad_h, 8) && ldgh % 4 == 0;
-            const int64_t work = static_cast<int64_t>(M) * (vec ? K / 4 : K);
-            Launch l(dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, 1 << 20))), 256, 0, stream);
-            st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_join_kernel, static_cast<const float *>(q.part), splits, M, K, q.ldp,
-                                             static_cast<uint16_t *>(grad_h), ldgh, vec));
-        }
+        if (st == MBGLU_OK && splits > 1) st = launch_join(q.part, splits, M, K, grad_h, ldgh, stream);
     } else if (st == MBGLU_OK && want_h) {
         path = 5;
         mbglu::GenParams q = {};

@@ -10,9 +10,9 @@
 //   warp 0      tensor copies: per stage 16 KB of A and 16 KB of B
 //               (64 bf16 or 128 e4m3 of the inner dimension), 6 stages;
 //               both CTAs' copies count on the even CTA's barrier
-//   warp 1      (even CTA) issues the MMAs
-//   warp 2      owns the tensor memory: two buffers of 256 columns, so that a
-//               tile's epilogue runs under the next tile's products
+//   warp 1      owns the tensor memory -- two buffers of 256 columns, so that a
+//               tile's epilogue runs under the next tile's products -- and, in
+//               the even CTA, issues the MMAs
 //   warps 4-11  epilogue: warp w reads lanes 32 (w % 4).., the first or second
 //               half of the columns
 // A gated tile holds 128 gate and 128 up columns of the same outputs: the even
@@ -30,6 +30,7 @@
 namespace mbglu {
 
 constexpr int kPairThreads = 384;
+constexpr int kPairEpilogue = 4;                            // the first of the eight epilogue warps
 constexpr int kPairStages = 6;
 constexpr int kPairTile = 256;
 constexpr uint32_t kPairOperand = 16384;                   // one operand's bytes per stage and CTA
@@ -116,7 +117,7 @@ __device__ __forceinline__ uint32_t pair_setup(const PairShared &s, int warp)
         }
         fence_mbar_init();
     }
-    if (warp == 2) {
+    if (warp == 1) {
         pair_tmem_alloc(s.slot, kPairCols);
         pair_tmem_relinquish();
     }
@@ -134,7 +135,7 @@ __device__ __forceinline__ void pair_teardown(int warp, uint32_t tmem)
     __syncthreads();
     __syncwarp();
     cluster_sync();   // both CTAs have read their accumulators and sent their arrivals
-    if (warp == 2) {
+    if (warp == 1) {
         tc_fence_after();
         pair_tmem_dealloc(tmem, kPairCols);
     }
@@ -153,7 +154,7 @@ __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &
         for (int c = x.c0; c < x.c1; ++c, ++u) {
             const int st = static_cast<int>(u % kPairStages);
             const int64_t round = u / kPairStages;
-            if (round > 0 && !mbar_wait_cluster_bounded(&s.empty[st], static_cast<uint32_t>((round - 1) & 1), kWaitLimitNs)) {
+            if (round > 0 && !pair_wait(&s.empty[st], static_cast<uint32_t>((round - 1) & 1), kWaitLimitNs)) {
                 ok = false;
                 break;
             }
@@ -181,7 +182,7 @@ __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &
     // every copy of this CTA has landed and been read, and every arrival on
     // this CTA's barriers has come, before it may leave
     for (int64_t v = u > kPairStages ? u - kPairStages : 0; v < u; ++v)
-        if (!mbar_wait_cluster_bounded(&s.empty[v % kPairStages], static_cast<uint32_t>((v / kPairStages) & 1), kWaitLimitNs))
+        if (!pair_wait(&s.empty[v % kPairStages], static_cast<uint32_t>((v / kPairStages) & 1), kWaitLimitNs))
             ok = false;
     return ok;
 }
@@ -198,10 +199,10 @@ __device__ __forceinline__ bool pair_multiply(const PairPlan &p, const PairShare
         for (int c = x.c0; c < x.c1; ++c, ++u) {
             const int buf = static_cast<int>(v & 1);
             if ((PER_CHUNK || c == x.c0) && v >= 2 &&
-                !mbar_wait_cluster_bounded(&s.acc_empty[buf], static_cast<uint32_t>(((v >> 1) - 1) & 1), kWaitLimitNs))
+                !pair_wait(&s.acc_empty[buf], static_cast<uint32_t>(((v >> 1) - 1) & 1), kWaitLimitNs))
                 return false;
             const int st = static_cast<int>(u % kPairStages);
-            if (!mbar_wait_cluster_bounded(&s.full[st], static_cast<uint32_t>((u / kPairStages) & 1), kWaitLimitNs))
+            if (!pair_wait(&s.full[st], static_cast<uint32_t>((u / kPairStages) & 1), kWaitLimitNs))
                 return false;
             tc_fence_after();
             unsigned char *da = s.stages + st * kPairStage, *db = da + kPairOperand;
@@ -227,7 +228,7 @@ __device__ __forceinline__ bool pair_multiply(const PairPlan &p, const PairShare
     return true;
 }
 
-enum PairEpilogue { kPairGlu = 0, kPairGrad = 1, kPairPlain = 2 };
+enum PairKind { kPairGlu = 0, kPairGrad = 1, kPairPlain = 2 };
 
 struct PairParams {
     PairPlan plan;
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
         if (lane == 0) ok = pair_produce<MODE, A_MN, B_MN, 64>(p.plan, maps, s, rank);
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) ok = pair_multiply<A_MN, B_MN, false, false>(p.plan, s, tmem);
-    } else if (warp >= 4) {
-        const int q = warp & 3, half = (warp - 4) >> 2;
+    } else if (warp >= kPairEpilogue) {
+        const int q = warp & 3, half = (warp - kPairEpilogue) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
         int64_t v = 0;
         for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1), ++v) {
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
             const int buf = static_cast<int>(v & 1);
             const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32 + lane;
             const bool row = m < p.plan.rows;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&s.acc_full[buf], static_cast<uint32_t>((v >> 1) & 1), kWaitLimitNs));
+            if (ok) ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], static_cast<uint32_t>((v >> 1) & 1), kWaitLimitNs));
             tc_fence_after();
             const uint32_t acc = lanes + static_cast<uint32_t>(buf) * kPairTile;
             if constexpr (MODE == kPairDual) {
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
                     if (j == 1) {   // the buffer is read
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(map_to_rank(&s.acc_empty[buf], 0));
+                        if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
                     }
                     if (!ok || !row || valid <= 0) continue;
                     uint32_t w[16], w2[16];
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
                     if (j == 3) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(map_to_rank(&s.acc_empty[buf], 0));
+                        if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
                     }
                     if (!ok || !row || valid <= 0) continue;
                     if (p.plan.splits > 1) {
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
 
 // out = bf16(sum of the splits' partial sums, in order); 4 columns per thread
 // where they lie on 8 bytes (vec), else one.
-__global__ void __launch_bounds__(256) pair_join_kernel(const float *part, int splits, int rows, int cols, int64_t ldp,
+static __global__ void __launch_bounds__(256) pair_join_kernel(const float *part, int splits, int rows, int cols, int64_t ldp,
                                                         uint16_t *out, int64_t ldo, int vec)
 {
     grid_dependency_wait();
@@ -380,46 +381,6 @@ __global__ void __launch_bounds__(256) pair_join_kernel(const float *part, int s
             float a = 0.0f;
             for (int s = 0; s < splits; ++s) a += part[(s * static_cast<int64_t>(rows) + m) * ldp + c];
             out[m * ldo + c] = f32_to_bf16(a);
-        }
-    }
-}
-
-// dG, dU (bf16, [rows][ldo]) from g and u as the forward kept them: one pass,
-// 8 columns per thread where everything lies on 16 bytes (vec).
-__global__ void __launch_bounds__(256) glu_grad_kernel(const float *gu, int64_t ldgu, const uint16_t *dout, int64_t ldd,
-                                                       uint16_t *dg, uint16_t *du, int64_t ldo, int rows, int cols, int vec)
-{
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int per = vec ? cols / 8 : cols;
-    const int64_t total = static_cast<int64_t>(rows) * per;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t m = i / per;
-        const int c = static_cast<int>(i - m * per);
-        if (vec) {
-            const float4 *pg = reinterpret_cast<const float4 *>(gu + m * ldgu) + 2 * c;
-            const float4 *pu = reinterpret_cast<const float4 *>(gu + m * ldgu + cols) + 2 * c;
-            const float4 g0 = __ldcs(pg), g1 = __ldcs(pg + 1), u0 = __ldcs(pu), u1 = __ldcs(pu + 1);
-            const uint4 dq = __ldcs(reinterpret_cast<const uint4 *>(dout + m * ldd) + c);
-            const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-            const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-            const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w};
-            uint32_t wg[4], wu[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float a0, b0, a1, b1;
-                glu_gradients(g[2 * j], u[2 * j], bf16_lo(dw[j]), a0, b0);
-                glu_gradients(g[2 * j + 1], u[2 * j + 1], bf16_hi(dw[j]), a1, b1);
-                wg[j] = pack_bf16x2(a0, a1);
-                wu[j] = pack_bf16x2(b0, b1);
-            }
-            reinterpret_cast<uint4 *>(dg + m * ldo)[c] = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-            reinterpret_cast<uint4 *>(du + m * ldo)[c] = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-        } else {
-            float a, b;
-            glu_gradients(gu[m * ldgu + c], gu[m * ldgu + cols + c], bf16_to_f32(dout[m * ldd + c]), a, b);
-            dg[m * ldo + c] = f32_to_bf16(a);
-            du[m * ldo + c] = f32_to_bf16(b);
         }
     }
 }

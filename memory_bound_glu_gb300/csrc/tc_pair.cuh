@@ -61,6 +61,43 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar)
         : "memory");
 }
 
+// Waits for the barrier's phase with a wall-clock limit; false on timeout.  The
+// timer is read once in 256 tries: a read costs more than a chunk's products.
+__device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t phase, uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, phase)) return true;
+        if ((i & 255u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0)
+                t0 = now;
+            else if (now - t0 > limit_ns)
+                return false;
+        }
+    }
+}
+
+// Arrival on a barrier of either CTA (a shared::cluster address).  What it
+// publishes is that tensor memory has been read, which the tcgen05 fences
+// order; no plain memory is handed over.
+__device__ __forceinline__ void pair_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A warpgroup's registers per thread, below or above what it was launched with.
+template <int N>
+__device__ __forceinline__ void regs_release()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // A tensor copy into this CTA's shared memory that counts its bytes on a
 // barrier of either CTA of the pair (a shared::cluster address).
 __device__ __forceinline__ void pair_load_2d(void *dst, const TensorMap *map, int x, int y, uint32_t bar)
