@@ -145,16 +145,19 @@ __device__ __forceinline__ void pair_teardown(int warp, uint32_t tmem)
 template <int MODE, bool A_MN, bool B_MN, int CK>
 __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &maps, const PairShared &s, uint32_t rank)
 {
+    // one thread's instructions stand between a freed stage and its next copies,
+    // so the ring is walked by a stage number and a phase bit, without divisions
+    int st = 0;
+    uint32_t phase = 1;   // of empty[]: the first round's stages are free
     bool ok = true;
-    int64_t u = 0;   // stages filled
+    uint32_t filled = 0;  // up to kPairStages
+    const uint32_t full0 = map_to_rank(s.full, 0);
     for (int t = static_cast<int>(blockIdx.x >> 1); t < p.ntiles && ok; t += static_cast<int>(gridDim.x >> 1)) {
         const PairTileAt x = pair_tile(p, t);
         const int arow = x.mi * kPairTile + static_cast<int>(rank) * 128;
         const int brow = MODE == kPairDual ? x.ni * 128 : x.ni * kPairTile + static_cast<int>(rank) * 128;
-        for (int c = x.c0; c < x.c1; ++c, ++u) {
-            const int st = static_cast<int>(u % kPairStages);
-            const int64_t round = u / kPairStages;
-            if (round > 0 && !pair_wait(&s.empty[st], static_cast<uint32_t>((round - 1) & 1), kWaitLimitNs)) {
+        for (int c = x.c0; c < x.c1; ++c) {
+            if (!pair_wait(&s.empty[st], phase, kWaitLimitNs)) {
                 ok = false;
                 break;
             }
@@ -164,7 +167,7 @@ __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &
             const TensorMap *mb = &maps.b[MODE == kPairSum ? second : MODE == kPairDual ? static_cast<int>(rank) : 0];
             unsigned char *da = s.stages + st * kPairStage, *db = da + kPairOperand;
             if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kPairStage);
-            const uint32_t bar = map_to_rank(&s.full[st], 0);
+            const uint32_t bar = full0 + static_cast<uint32_t>(st) * 8u;
             if (A_MN) {
                 pair_load_2d(da, ma, arow, k, bar);
                 pair_load_2d(da + kPairBoxBytes, ma, arow + 64, k, bar);
@@ -177,13 +180,22 @@ __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &
             } else {
                 pair_load_2d(db, mb, k, brow, bar);
             }
+            filled += filled < kPairStages;
+            if (++st == kPairStages) {
+                st = 0;
+                phase ^= 1;
+            }
         }
     }
     // every copy of this CTA has landed and been read, and every arrival on
-    // this CTA's barriers has come, before it may leave
-    for (int64_t v = u > kPairStages ? u - kPairStages : 0; v < u; ++v)
-        if (!pair_wait(&s.empty[v % kPairStages], static_cast<uint32_t>((v / kPairStages) & 1), kWaitLimitNs))
-            ok = false;
+    // this CTA's barriers has come, before it may leave: the last round's
+    // stages, oldest first
+    for (uint32_t i = 0; i < filled; ++i) {
+        int at = st - static_cast<int>(filled - i);
+        const uint32_t ph = at < 0 ? phase : phase ^ 1;   // filled in the round before this one, or in this
+        if (at < 0) at += kPairStages;
+        if (!pair_wait(&s.empty[at], ph, kWaitLimitNs)) ok = false;
+    }
     return ok;
 }
 
@@ -193,22 +205,19 @@ template <bool A_MN, bool B_MN, bool E4M3, bool PER_CHUNK>
 __device__ __forceinline__ bool pair_multiply(const PairPlan &p, const PairShared &s, uint32_t tmem)
 {
     constexpr uint32_t idesc = E4M3 ? pair_idesc_e4m3() : pair_idesc_bf16(A_MN, B_MN);
-    int64_t u = 0, v = 0;   // stages read, buffers filled
+    const uint64_t a0 = A_MN ? smem_desc_mn_sw128(s.stages) : smem_desc_sw128(s.stages);
+    const uint64_t b0 = B_MN ? smem_desc_mn_sw128(s.stages + kPairOperand) : smem_desc_sw128(s.stages + kPairOperand);
+    int st = 0;
+    uint32_t phase = 0, buf = 0, acc_phase = 1;   // of full[], of acc_empty[] (both buffers start free)
     for (int t = static_cast<int>(blockIdx.x >> 1); t < p.ntiles; t += static_cast<int>(gridDim.x >> 1)) {
         const PairTileAt x = pair_tile(p, t);
-        for (int c = x.c0; c < x.c1; ++c, ++u) {
-            const int buf = static_cast<int>(v & 1);
-            if ((PER_CHUNK || c == x.c0) && v >= 2 &&
-                !pair_wait(&s.acc_empty[buf], static_cast<uint32_t>(((v >> 1) - 1) & 1), kWaitLimitNs))
-                return false;
-            const int st = static_cast<int>(u % kPairStages);
-            if (!pair_wait(&s.full[st], static_cast<uint32_t>((u / kPairStages) & 1), kWaitLimitNs))
-                return false;
+        for (int c = x.c0; c < x.c1; ++c) {
+            if ((PER_CHUNK || c == x.c0) && !pair_wait(&s.acc_empty[buf], acc_phase, kWaitLimitNs)) return false;
+            if (!pair_wait(&s.full[st], phase, kWaitLimitNs)) return false;
             tc_fence_after();
-            unsigned char *da = s.stages + st * kPairStage, *db = da + kPairOperand;
-            const uint64_t ad = A_MN ? smem_desc_mn_sw128(da) : smem_desc_sw128(da);
-            const uint64_t bd = B_MN ? smem_desc_mn_sw128(db) : smem_desc_sw128(db);
-            const uint32_t d = tmem + static_cast<uint32_t>(buf) * kPairTile;
+            const uint64_t ad = a0 + static_cast<uint32_t>(st) * (kPairStage >> 4);
+            const uint64_t bd = b0 + static_cast<uint32_t>(st) * (kPairStage >> 4);
+            const uint32_t d = tmem + buf * kPairTile;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {   // 16 bf16 or 32 e4m3 each
                 const bool acc = kk > 0 || (!PER_CHUNK && c > x.c0);
@@ -219,9 +228,14 @@ __device__ __forceinline__ bool pair_multiply(const PairPlan &p, const PairShare
                     pair_mma_bf16(d, a, b, idesc, acc);
             }
             pair_commit(&s.empty[st]);
+            if (++st == kPairStages) {
+                st = 0;
+                phase ^= 1;
+            }
             if (PER_CHUNK || c == x.c1 - 1) {
                 pair_commit(&s.acc_full[buf]);
-                ++v;
+                buf ^= 1;
+                if (buf == 0) acc_phase ^= 1;
             }
         }
     }
@@ -265,13 +279,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
     } else if (warp >= kPairEpilogue) {
         const int q = warp & 3, half = (warp - kPairEpilogue) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        int64_t v = 0;
+        uint32_t v = 0;
         for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1), ++v) {
             const PairTileAt x = pair_tile(p.plan, t);
             const int buf = static_cast<int>(v & 1);
             const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32 + lane;
             const bool row = m < p.plan.rows;
-            if (ok) ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], static_cast<uint32_t>((v >> 1) & 1), kWaitLimitNs));
+            if (ok) ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], (v >> 1) & 1, kWaitLimitNs));
             tc_fence_after();
             const uint32_t acc = lanes + static_cast<uint32_t>(buf) * kPairTile;
             if constexpr (MODE == kPairDual) {
