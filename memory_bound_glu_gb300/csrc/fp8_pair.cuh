@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
     constexpr int kMode = kDual ? kPairDual : kPairSum;
     extern __shared__ unsigned char pair_raw[];
     const PairShared s = pair_shared(pair_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     ScaleStage *scales = reinterpret_cast<ScaleStage *>(s.stages + kPairStages * kPairStage);
     uint64_t *scale_full = reinterpret_cast<uint64_t *>(s.slot + 2), *scale_empty = scale_full + 2;
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
     // (128 x 88 + 256 x 208 registers of 384 x 168)
     if (warp < kPairEpilogue) {
         regs_release<88>();
-        if (warp == 0 && lane == 0) ok = pair_produce<kMode, false, false, 128>(p.plan, maps, s, rank);
-        if (warp == 1 && lane == 0 && rank == 0) ok = pair_multiply<false, false, true, true>(p.plan, s, tmem);
+        if (warp == 0) ok = pair_produce<kMode, false, false, 128>(p.plan, maps, s, rank);
+        if (warp == 1 && rank == 0) ok = pair_multiply<false, false, true, true>(p.plan, s, tmem);
         if (warp == 2) {
             uint32_t g = 0;
             for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1)) {

@@ -126,7 +126,7 @@ __device__ __forceinline__ uint32_t pair_setup(const PairShared &s, int warp)
     __syncwarp();
     cluster_sync();   // the other CTA's barriers and tensor memory exist
     tc_fence_after();
-    return *s.slot;
+    return __shfl_sync(0xffffffffu, *s.slot, 0);
 }
 
 __device__ __forceinline__ void pair_teardown(int warp, uint32_t tmem)
@@ -141,11 +141,11 @@ __device__ __forceinline__ void pair_teardown(int warp, uint32_t tmem)
     }
 }
 
-// Warp 0, one thread.  CK: elements of the inner dimension per chunk.
+// Warp 0.  CK: elements of the inner dimension per chunk.
 template <int MODE, bool A_MN, bool B_MN, int CK>
 __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &maps, const PairShared &s, uint32_t rank)
 {
-    // one thread's instructions stand between a freed stage and its next copies,
+    // this warp's instructions stand between a freed stage and its next copies,
     // so the ring is walked by a stage number and a phase bit, without divisions
     int st = 0;
     uint32_t phase = 1;   // of empty[]: the first round's stages are free
@@ -166,20 +166,23 @@ __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &
             const TensorMap *ma = &maps.a[MODE == kPairSum ? second : MODE == kPairStack ? x.o : 0];
             const TensorMap *mb = &maps.b[MODE == kPairSum ? second : MODE == kPairDual ? static_cast<int>(rank) : 0];
             unsigned char *da = s.stages + st * kPairStage, *db = da + kPairOperand;
-            if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kPairStage);
             const uint32_t bar = full0 + static_cast<uint32_t>(st) * 8u;
-            if (A_MN) {
-                pair_load_2d(da, ma, arow, k, bar);
-                pair_load_2d(da + kPairBoxBytes, ma, arow + 64, k, bar);
-            } else {
-                pair_load_2d(da, ma, k, arow, bar);
+            if (elect_one()) {
+                if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kPairStage);
+                if (A_MN) {
+                    pair_load_2d(da, ma, arow, k, bar);
+                    pair_load_2d(da + kPairBoxBytes, ma, arow + 64, k, bar);
+                } else {
+                    pair_load_2d(da, ma, k, arow, bar);
+                }
+                if (B_MN) {
+                    pair_load_2d(db, mb, brow, k, bar);
+                    pair_load_2d(db + kPairBoxBytes, mb, brow + 64, k, bar);
+                } else {
+                    pair_load_2d(db, mb, k, brow, bar);
+                }
             }
-            if (B_MN) {
-                pair_load_2d(db, mb, brow, k, bar);
-                pair_load_2d(db + kPairBoxBytes, mb, brow + 64, k, bar);
-            } else {
-                pair_load_2d(db, mb, k, brow, bar);
-            }
+            __syncwarp();
             filled += filled < kPairStages;
             if (++st == kPairStages) {
                 st = 0;
@@ -199,7 +202,7 @@ __device__ __forceinline__ bool pair_produce(const PairPlan &p, const PairMaps &
     return ok;
 }
 
-// Warp 1 of the even CTA, one thread.  PER_CHUNK: each chunk is a sum of its
+// Warp 1 of the even CTA.  PER_CHUNK: each chunk is a sum of its
 // own in the next buffer (block-scaled operands), else a tile is.
 template <bool A_MN, bool B_MN, bool E4M3, bool PER_CHUNK>
 __device__ __forceinline__ bool pair_multiply(const PairPlan &p, const PairShared &s, uint32_t tmem)
@@ -218,22 +221,25 @@ __device__ __forceinline__ bool pair_multiply(const PairPlan &p, const PairShare
             const uint64_t ad = a0 + static_cast<uint32_t>(st) * (kPairStage >> 4);
             const uint64_t bd = b0 + static_cast<uint32_t>(st) * (kPairStage >> 4);
             const uint32_t d = tmem + buf * kPairTile;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {   // 16 bf16 or 32 e4m3 each
-                const bool acc = kk > 0 || (!PER_CHUNK && c > x.c0);
-                const uint64_t a = ad + (A_MN ? 128 : 2) * kk, b = bd + (B_MN ? 128 : 2) * kk;
-                if (E4M3)
-                    pair_mma_e4m3(d, a, b, idesc, acc);
-                else
-                    pair_mma_bf16(d, a, b, idesc, acc);
+                for (int kk = 0; kk < 4; ++kk) {   // 16 bf16 or 32 e4m3 each
+                    const bool acc = kk > 0 || (!PER_CHUNK && c > x.c0);
+                    const uint64_t a = ad + (A_MN ? 128 : 2) * kk, b = bd + (B_MN ? 128 : 2) * kk;
+                    if (E4M3)
+                        pair_mma_e4m3(d, a, b, idesc, acc);
+                    else
+                        pair_mma_bf16(d, a, b, idesc, acc);
+                }
+                pair_commit(&s.empty[st]);
+                if (PER_CHUNK || c == x.c1 - 1) pair_commit(&s.acc_full[buf]);
             }
-            pair_commit(&s.empty[st]);
+            __syncwarp();
             if (++st == kPairStages) {
                 st = 0;
                 phase ^= 1;
             }
             if (PER_CHUNK || c == x.c1 - 1) {
-                pair_commit(&s.acc_full[buf]);
                 buf ^= 1;
                 if (buf == 0) acc_phase ^= 1;
             }
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
 {
     extern __shared__ unsigned char pair_raw[];
     const PairShared s = pair_shared(pair_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const uint32_t tmem = pair_setup(s, warp);
     grid_dependency_wait();
@@ -273,9 +279,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
     bool ok = true;
 
     if (warp == 0) {
-        if (lane == 0) ok = pair_produce<MODE, A_MN, B_MN, 64>(p.plan, maps, s, rank);
+        ok = pair_produce<MODE, A_MN, B_MN, 64>(p.plan, maps, s, rank);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) ok = pair_multiply<A_MN, B_MN, false, false>(p.plan, s, tmem);
+        if (rank == 0) ok = pair_multiply<A_MN, B_MN, false, false>(p.plan, s, tmem);
     } else if (warp >= kPairEpilogue) {
         const int q = warp & 3, half = (warp - kPairEpilogue) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);

@@ -9,6 +9,20 @@
 
 namespace mbglu {
 
+// True in one lane of a converged warp.  The roles' loops are run by whole warps
+// and only the copies, products and commits by this lane, so that addresses and
+// descriptors stay in uniform registers, where tcgen05 takes them from.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Both CTAs' warps call these; the columns are taken in both SMs.
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t *slot, uint32_t ncols)
 {
