@@ -7,6 +7,7 @@
 #include "dense_generic.cuh"
 #include "dense_launch.h"
 #include "fp8_pair.cuh"
+#include "fp8_rows.cuh"
 #include "norm_fp8.cuh"
 #include "pair_plan.h"
 
@@ -92,7 +93,47 @@ mbglu_status launch_pair(const mbglu::Fp8PairParams &p, const mbglu::PairMaps &m
     return st;
 }
 
-int matmul_splits(int M, int N, int K) { return pair_splits(M, N, ceil_div(K, kBlk)); }
+bool rows_take(int M, int K) { return K > 0 && K % 16 == 0 && M <= mbglu::kRowsMax; }
+
+// Few rows: K-slices per 16 weight rows so that a warp has about five blocks of
+// its slice to stream, and rank 0 of a cluster writes a group's scale.
+template <int OUT>
+mbglu_status launch_rows(mbglu::Fp8RowsParams &p, cudaStream_t stream)
+{
+    const int kb = ceil_div(p.K, kBlk);
+    p.slices = kb >= 32 ? 8 : kb >= 8 ? 4 : kb >= 4 ? 2 : 1;
+    p.prefetch = launch_policy() == MBGLU_POLICY_PREFETCH;
+    const int R = mbglu::kRowsWarps / p.slices, cluster = OUT == 2 ? 8 / R : 1;
+    const int blocks = OUT == 2 ? ceil_div(p.N, kBlk) * cluster : ceil_div(p.N, 16 * R);
+    Launch l(dim3(static_cast<unsigned>(blocks)), mbglu::kRowsThreads, 0, stream, cluster);
+    const mbglu_status st = launched(p.M <= 8 ? cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<1, OUT>, p)
+                                              : cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<2, OUT>, p));
+    if (st == MBGLU_OK) set_last_variant(kFp8Rows);
+    return st;
+}
+
+mbglu::Fp8RowsParams rows_params(const Scaled &a, int M, int N, int K)
+{
+    mbglu::Fp8RowsParams p = {};
+    p.a = a.p;
+    p.lda = a.ld;
+    p.as = a.s;
+    p.ldas = a.lds;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    return p;
+}
+
+void rows_weight(mbglu::Fp8RowsParams &p, int d, const Scaled &w)
+{
+    p.w[d] = w.p;
+    p.ldw[d] = w.ld;
+    p.ws[d] = w.s;
+    p.ldws[d] = w.lds;
+}
+
+int matmul_splits(int M, int N, int K) { return rows_take(M, K) ? 1 : pair_splits(M, N, ceil_div(K, kBlk)); }
 
 }  // namespace
 
@@ -181,6 +222,13 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
     if (meets(out, ob, A, K) || meets(out, ob, W, K) || meets(workspace, wsb, A, K) || meets(workspace, wsb, W, K) ||
         overlaps(out, ob, workspace, wsb))
         return MBGLU_ERR_ALIAS;
+    if (rows_take(M, K) && copyable(a, lda, 1) && copyable(w, ldw, 1)) {
+        mbglu::Fp8RowsParams q = rows_params(A, M, N, K);
+        rows_weight(q, 0, W);
+        q.out = out;
+        q.ldo = ldo;
+        return launch_rows<0>(q, stream);
+    }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], W, K)) {
         const int splits = matmul_splits(M, N, K), chunks = ceil_div(K, kBlk);
@@ -236,6 +284,18 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
     for (const Scaled *in : {&A, &G, &U})
         if (meets(o, ob, *in, K) || meets(q_scale, sb, *in, K)) return MBGLU_ERR_ALIAS;
     if (overlaps(o, ob, q_scale, sb)) return MBGLU_ERR_ALIAS;
+    if (rows_take(M, K) && copyable(a, lda, 1) && copyable(gate_w, ld_gate, 1) && copyable(up_w, ld_up, 1)) {
+        mbglu::Fp8RowsParams p = rows_params(A, M, N, K);
+        rows_weight(p, 0, G);
+        rows_weight(p, 1, U);
+        p.out = out;
+        p.ldo = ldo;
+        p.q = q;
+        p.ldq = ldq;
+        p.qs = q_scale;
+        p.ldqs = ldqs;
+        return q ? launch_rows<2>(p, stream) : launch_rows<1>(p, stream);
+    }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], G, K) && k_major(&maps.b[1], U, K)) {
         mbglu::Fp8PairParams p = {};

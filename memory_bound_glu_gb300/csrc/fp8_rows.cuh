@@ -1,0 +1,218 @@
+// fp8_rows.cuh -- the e4m3 products for few rows (a decode step): bound by the
+// bytes of the weights, each read once.
+//
+// mma.sync m16n8k32 with the weights as the 16-row operand and the activations
+// as the 8 columns.  Fragments come straight from global memory: within a scale
+// block of 128 a lane owns 32 consecutive bytes of a weight row -- the order in
+// which the products take the inner index is free, as long as both operands use
+// the same -- so a weight fragment is two 16-byte loads per row and block, a
+// warp's load covers whole 128-byte lines, and nothing passes through shared
+// memory.  A warp streams one K-slice of 16 rows (of both weights where there
+// are two), one or two blocks ahead; slices are joined in shared memory in a
+// fixed order.  Eight warps per block, R groups of 16 rows x S slices = 8 warps.
+// An e4m3 output's group of 128 columns is a cluster of 8 / R blocks, which
+// exchange their maxima through distributed shared memory.
+#pragma once
+
+#include "dense_common.cuh"
+#include "tcgen05.cuh"
+
+namespace mbglu {
+
+constexpr int kRowsThreads = 256, kRowsWarps = 8;
+constexpr int kRowsMax = 16;     // activations' rows
+
+struct Fp8RowsParams {
+    const uint8_t *a;
+    int64_t lda;
+    const float *as;
+    int64_t ldas;
+    const uint8_t *w[2];
+    int64_t ldw[2];
+    const float *ws[2];
+    int64_t ldws[2];
+    int M, N, K;
+    int slices;              // S in {1, 2, 4, 8}; R = 8 / S
+    int prefetch;            // the first weight blocks are requested before the dependency wait
+    uint16_t *out;
+    int64_t ldo;
+    uint8_t *q;
+    int64_t ldq;
+    float *qs;
+    int64_t ldqs;
+};
+
+__device__ __forceinline__ uint4 ldg_stream16(const uint8_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: tiles of 8 activation rows.  OUT: 0 bf16 product, 1 bf16 gated, 2 e4m3 gated.
+template <int NT, int OUT>
+__global__ void __launch_bounds__(kRowsThreads, 2) fp8_rows_kernel(const Fp8RowsParams p)
+{
+    constexpr int MAT = OUT == 0 ? 1 : 2;
+    // scale blocks in flight per warp: what 128 registers hold (two blocks per SM)
+    constexpr int kRowsDepth = MAT == 2 && NT == 2 ? 1 : 2;
+    constexpr int MP = 8 * NT;                           // activation rows, padded
+    // one slice's sums of one group: [mat][16 rows][MP + 1]
+    constexpr int kPart = MAT * 16 * (MP + 1);
+    __shared__ float part[kRowsWarps][kPart];
+    __shared__ float vals[OUT == 2 ? MP * 128 : 1];      // the gated values, [m][columns of the block]
+    __shared__ float peaks[OUT == 2 ? 8 * MP : 1];       // [block of the cluster][m]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int S = p.slices, R = kRowsWarps / S;
+    const int group = warp / S, slice = warp % S;
+    const int kb = (p.K + kScaleBlock - 1) / kScaleBlock;
+    const int b0 = kb * slice / S, b1 = kb * (slice + 1) / S;
+    const int n0 = (static_cast<int>(blockIdx.x) * R + group) * 16;    // this warp's rows of the weights
+    const int wb = n0 / kScaleBlock;
+    const bool live = n0 < p.N;
+    const int r0 = min(n0 + g, p.N - 1), r1 = min(n0 + g + 8, p.N - 1);
+
+    const uint8_t *w0[MAT], *w1[MAT];
+#pragma unroll
+    for (int d = 0; d < MAT; ++d) {
+        w0[d] = p.w[d] + r0 * p.ldw[d] + t * 32;
+        w1[d] = p.w[d] + r1 * p.ldw[d] + t * 32;
+    }
+    uint4 w[kRowsDepth][MAT][4];
+    auto load_w = [&](uint4 (&dst)[MAT][4], int b) {
+        // K is a multiple of 16: 16 bytes lie in the row or past it, where the
+        // activations are 0 and any finite weight will do (the row's start)
+        const int k = b * kScaleBlock;
+        const int k0 = k + t * 32 < p.K ? k : -t * 32, k1 = k + t * 32 + 16 < p.K ? k + 16 : -t * 32;
+#pragma unroll
+        for (int d = 0; d < MAT; ++d) {
+            dst[d][0] = ldg_stream16(w0[d] + k0);
+            dst[d][1] = ldg_stream16(w0[d] + k1);
+            dst[d][2] = ldg_stream16(w1[d] + k0);
+            dst[d][3] = ldg_stream16(w1[d] + k1);
+        }
+    };
+    if (!p.prefetch) grid_dependency_wait();
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < kRowsDepth; ++i)
+            if (b0 + i < b1) load_w(w[i], b0 + i);
+    }
+    if (p.prefetch) grid_dependency_wait();
+    grid_launch_dependents();
+
+    float total[MAT][NT][4] = {};
+    if (live) {
+#pragma unroll 1
+        for (int b = b0; b < b1; b += kRowsDepth) {
+#pragma unroll
+            for (int i = 0; i < kRowsDepth; ++i) {
+                if (b + i >= b1) break;
+                const int k = (b + i) * kScaleBlock + t * 32;
+                float f[MAT];
+#pragma unroll
+                for (int d = 0; d < MAT; ++d) f[d] = __ldg(p.ws[d] + wb * p.ldws[d] + b + i);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int m = nt * 8 + g;
+                    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+                    if (m < p.M) {
+                        const uint4 *x = reinterpret_cast<const uint4 *>(p.a + m * p.lda + k);
+                        if (k < p.K) x0 = __ldg(x);
+                        if (k + 16 < p.K) x1 = __ldg(x + 1);
+                    }
+                    // the scales of the two activation rows of this lane's sums
+                    const int m0 = nt * 8 + 2 * t;
+                    const float s0 = m0 < p.M ? __ldg(p.as + m0 * p.ldas + b + i) : 0.0f;
+                    const float s1 = m0 + 1 < p.M ? __ldg(p.as + (m0 + 1) * p.ldas + b + i) : 0.0f;
+#pragma unroll
+                    for (int d = 0; d < MAT; ++d) {
+                        const uint4 *q = w[i][d];
+                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma_e4m3(c, q[0].x, q[2].x, q[0].y, q[2].y, x0.x, x0.y);
+                        mma_e4m3(c, q[0].z, q[2].z, q[0].w, q[2].w, x0.z, x0.w);
+                        mma_e4m3(c, q[1].x, q[3].x, q[1].y, q[3].y, x1.x, x1.y);
+                        mma_e4m3(c, q[1].z, q[3].z, q[1].w, q[3].w, x1.z, x1.w);
+                        float(&s)[4] = total[d][nt];
+                        s[0] = fmaf(f[d] * s0, c[0], s[0]);
+                        s[1] = fmaf(f[d] * s1, c[1], s[1]);
+                        s[2] = fmaf(f[d] * s0, c[2], s[2]);
+                        s[3] = fmaf(f[d] * s1, c[3], s[3]);
+                    }
+                }
+                if (b + i + kRowsDepth < b1) load_w(w[i], b + i + kRowsDepth);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < MAT; ++d)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[warp][(d * 16 + g + (i >> 1) * 8) * (MP + 1) + nt * 8 + 2 * t + (i & 1)] = total[d][nt][i];
+    __syncthreads();
+
+    // join: warp w takes activation rows w, w + 8, ..; lanes take columns
+    const int cols = 16 * R, c0 = static_cast<int>(blockIdx.x) * cols;
+    auto joined = [&](int d, int c, int m) {
+        const float *q = &part[(c >> 4) * S][(d * 16 + (c & 15)) * (MP + 1) + m];
+        float v = 0.0f;
+        for (int s = 0; s < S; ++s) v += q[s * kPart];
+        return v;
+    };
+    for (int m = warp; m < p.M; m += kRowsWarps) {
+        float amax = 0.0f;
+        for (int c = lane; c < cols; c += 32) {
+            const int n = c0 + c;
+            const float x = joined(0, c, m);
+            if (OUT == 0) {
+                if (n < p.N) p.out[m * p.ldo + n] = f32_to_bf16(x);
+            } else {
+                const float v = silu_f32(x) * joined(MAT - 1, c, m);
+                if (OUT == 1) {
+                    if (n < p.N) p.out[m * p.ldo + n] = f32_to_bf16(v);
+                } else {
+                    vals[m * 128 + c] = v;
+                    if (n < p.N) amax = max_nan(amax, fabsf(v));
+                }
+            }
+        }
+        if (OUT == 2) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const uint32_t rank = R < 8 ? cluster_ctarank() : 0u;
+            if (R < 8) {   // every block of the cluster gets it
+                if (lane < 8 / R) st_cluster_f32(map_to_rank(&peaks[rank * MP + m], static_cast<uint32_t>(lane)), amax);
+            } else if (lane == 0) {
+                peaks[m] = amax;
+            }
+        }
+    }
+    if constexpr (OUT == 2) {
+        if (R < 8)
+            cluster_sync();   // the maxima are there; nobody's memory is touched after it
+        else
+            __syncthreads();
+        const uint32_t rank = R < 8 ? cluster_ctarank() : 0u;
+        for (int m = warp; m < p.M; m += kRowsWarps) {
+            float amax = 0.0f;
+            for (int i = 0; i < 8 / R; ++i) amax = max_nan(amax, peaks[i * MP + m]);
+            const float s = group_scale(amax), inv = 1.0f / s;
+            if (rank == 0 && lane == 0) p.qs[m * p.ldqs + c0 / kScaleBlock] = s;
+            for (int c = lane; c < cols; c += 32)
+                if (c0 + c < p.N) p.q[m * p.ldq + c0 + c] = static_cast<uint8_t>(pack_e4m3x2(vals[m * 128 + c] * inv, 0.0f));
+        }
+    }
+}
+
+}  // namespace mbglu
