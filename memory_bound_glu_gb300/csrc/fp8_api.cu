@@ -95,21 +95,43 @@ mbglu_status launch_pair(const mbglu::Fp8PairParams &p, const mbglu::PairMaps &m
 
 bool rows_take(int M, int K) { return K > 0 && K % 16 == 0 && M <= mbglu::kRowsMax; }
 
-// Few rows: K-slices per 16 weight rows so that a warp has about five blocks of
-// its slice to stream, and rank 0 of a cluster writes a group's scale.
-template <int OUT>
-mbglu_status launch_rows(mbglu::Fp8RowsParams &p, cudaStream_t stream)
+template <int NT, int OUT, int WARPS, int DEPTH, int PER_SM>
+mbglu_status launch_rows(mbglu::Fp8RowsParams &p, int slices, cudaStream_t stream)
 {
-    const int kb = ceil_div(p.K, kBlk);
-    p.slices = kb >= 32 ? 8 : kb >= 8 ? 4 : kb >= 4 ? 2 : 1;
+    p.slices = slices;
     p.prefetch = launch_policy() == MBGLU_POLICY_PREFETCH;
-    const int R = mbglu::kRowsWarps / p.slices, cluster = OUT == 2 ? 8 / R : 1;
+    const int R = WARPS / slices, cluster = OUT == 2 ? 8 / R : 1;
     const int blocks = OUT == 2 ? ceil_div(p.N, kBlk) * cluster : ceil_div(p.N, 16 * R);
-    Launch l(dim3(static_cast<unsigned>(blocks)), mbglu::kRowsThreads, 0, stream, cluster);
-    const mbglu_status st = launched(p.M <= 8 ? cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<1, OUT>, p)
-                                              : cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<2, OUT>, p));
+    Launch l(dim3(static_cast<unsigned>(blocks)), WARPS * 32, 0, stream, cluster);
+    const mbglu_status st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<NT, OUT, WARPS, DEPTH, PER_SM>, p));
     if (st == MBGLU_OK) set_last_variant(kFp8Rows);
     return st;
+}
+
+// The largest number of K-slices (each of at least one scale block) that keeps
+// the blocks in one wave: more slices, more bytes in flight; a second wave
+// starts cold.
+int rows_slices(int N, int K, int warps, int most_blocks)
+{
+    int s = warps;
+    while (s > 1 && (ceil_div(N, 16 * (warps / s)) > most_blocks || ceil_div(K, kBlk) < s)) s /= 2;
+    return std::max(s, warps / 8);   // a block holds at most 128 rows
+}
+
+mbglu_status matmul_rows(mbglu::Fp8RowsParams &p, cudaStream_t stream)
+{
+    const int slices = rows_slices(p.N, p.K, 8, 4 * kPairs);
+    return p.M <= 8 ? launch_rows<1, 0, 8, 4, 2>(p, slices, stream) : launch_rows<2, 0, 8, 2, 2>(p, slices, stream);
+}
+
+// A cluster's blocks start together on one part of the chip, so that not quite
+// every place can be filled.
+template <int OUT>
+mbglu_status glu_rows(mbglu::Fp8RowsParams &p, cudaStream_t stream)
+{
+    const int places = OUT == 2 ? 7 * kPairs / 2 : 4 * kPairs;
+    return p.M <= 8 ? launch_rows<1, OUT, 8, 2, 2>(p, rows_slices(p.N, p.K, 8, places), stream)
+                    : launch_rows<2, OUT, 8, 2, 1>(p, rows_slices(p.N, p.K, 8, places / 2), stream);
 }
 
 mbglu::Fp8RowsParams rows_params(const Scaled &a, int M, int N, int K)
@@ -227,7 +249,7 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
         rows_weight(q, 0, W);
         q.out = out;
         q.ldo = ldo;
-        return launch_rows<0>(q, stream);
+        return matmul_rows(q, stream);
     }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], W, K)) {
@@ -294,7 +316,7 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
         p.ldq = ldq;
         p.qs = q_scale;
         p.ldqs = ldqs;
-        return q ? launch_rows<2>(p, stream) : launch_rows<1>(p, stream);
+        return q ? glu_rows<2>(p, stream) : glu_rows<1>(p, stream);
     }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], G, K) && k_major(&maps.b[1], U, K)) {

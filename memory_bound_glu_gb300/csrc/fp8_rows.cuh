@@ -3,13 +3,14 @@
 //
 // mma.sync m16n8k32 with the weights as the 16-row operand and the activations
 // as the 8 columns.  Fragments come straight from global memory: within a scale
-// block of 128 a lane owns 32 consecutive bytes of a weight row -- the order in
-// which the products take the inner index is free, as long as both operands use
-// the same -- so a weight fragment is two 16-byte loads per row and block, a
-// warp's load covers whole 128-byte lines, and nothing passes through shared
+// block of 128 a lane owns bytes 16 t .. and 64 + 16 t .. (16 each) of a weight
+// row -- the order in which the products take the inner index is free, as long
+// as both operands use the same -- so a weight fragment is two 16-byte loads per
+// row and block, each warp's load takes whole sectors (with 32 consecutive bytes
+// per lane every sector was asked for twice), and nothing passes through shared
 // memory.  A warp streams one K-slice of 16 rows (of both weights where there
 // are two), one or two blocks ahead; slices are joined in shared memory in a
-// fixed order.  Eight warps per block, R groups of 16 rows x S slices = 8 warps.
+// fixed order.  R groups of 16 rows x S slices = the block's warps.
 // An e4m3 output's group of 128 columns is a cluster of 8 / R blocks, which
 // exchange their maxima through distributed shared memory.
 #pragma once
@@ -19,7 +20,6 @@
 
 namespace mbglu {
 
-constexpr int kRowsThreads = 256, kRowsWarps = 8;
 constexpr int kRowsMax = 16;     // activations' rows
 
 struct Fp8RowsParams {
@@ -32,7 +32,7 @@ struct Fp8RowsParams {
     const float *ws[2];
     int64_t ldws[2];
     int M, N, K;
-    int slices;              // S in {1, 2, 4, 8}; R = 8 / S
+    int slices;              // S, a power of two up to the warps of a block; R = warps / S
     int prefetch;            // the first weight blocks are requested before the dependency wait
     uint16_t *out;
     int64_t ldo;
@@ -57,13 +57,13 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: tiles of 8 activation rows.  OUT: 0 bf16 product, 1 bf16 gated, 2 e4m3 gated.
-template <int NT, int OUT>
-__global__ void __launch_bounds__(kRowsThreads, 2) fp8_rows_kernel(const Fp8RowsParams p)
+// NT: tiles of 8 activation rows.  OUT: 0 bf16 product, 1 bf16 gated, 2 e4m3
+// gated.  WARPS per block, DEPTH scale blocks in flight per warp, and PER_SM
+// blocks per SM that the registers must allow.
+template <int NT, int OUT, int kRowsWarps, int kRowsDepth, int PER_SM>
+__global__ void __launch_bounds__(kRowsWarps * 32, PER_SM) fp8_rows_kernel(const Fp8RowsParams p)
 {
     constexpr int MAT = OUT == 0 ? 1 : 2;
-    // scale blocks in flight per warp: what 128 registers hold (two blocks per SM)
-    constexpr int kRowsDepth = MAT == 2 && NT == 2 ? 1 : 2;
     constexpr int MP = 8 * NT;                           // activation rows, padded
     // one slice's sums of one group: [mat][16 rows][MP + 1]
     constexpr int kPart = MAT * 16 * (MP + 1);
@@ -84,15 +84,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2) fp8_rows_kernel(const Fp8Rows
     const uint8_t *w0[MAT], *w1[MAT];
 #pragma unroll
     for (int d = 0; d < MAT; ++d) {
-        w0[d] = p.w[d] + r0 * p.ldw[d] + t * 32;
-        w1[d] = p.w[d] + r1 * p.ldw[d] + t * 32;
+        w0[d] = p.w[d] + r0 * p.ldw[d] + t * 16;
+        w1[d] = p.w[d] + r1 * p.ldw[d] + t * 16;
     }
     uint4 w[kRowsDepth][MAT][4];
     auto load_w = [&](uint4 (&dst)[MAT][4], int b) {
         // K is a multiple of 16: 16 bytes lie in the row or past it, where the
         // activations are 0 and any finite weight will do (the row's start)
         const int k = b * kScaleBlock;
-        const int k0 = k + t * 32 < p.K ? k : -t * 32, k1 = k + t * 32 + 16 < p.K ? k + 16 : -t * 32;
+        const int k0 = k + t * 16 < p.K ? k : -t * 16, k1 = k + t * 16 + 64 < p.K ? k + 64 : -t * 16;
 #pragma unroll
         for (int d = 0; d < MAT; ++d) {
             dst[d][0] = ldg_stream16(w0[d] + k0);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) fp8_rows_kernel(const Fp8Rows
 #pragma unroll
             for (int i = 0; i < kRowsDepth; ++i) {
                 if (b + i >= b1) break;
-                const int k = (b + i) * kScaleBlock + t * 32;
+                const int k = (b + i) * kScaleBlock + t * 16;
                 float f[MAT];
 #pragma unroll
                 for (int d = 0; d < MAT; ++d) f[d] = __ldg(p.ws[d] + wb * p.ldws[d] + b + i);
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) fp8_rows_kernel(const Fp8Rows
                     if (m < p.M) {
                         const uint4 *x = reinterpret_cast<const uint4 *>(p.a + m * p.lda + k);
                         if (k < p.K) x0 = __ldg(x);
-                        if (k + 16 < p.K) x1 = __ldg(x + 1);
+                        if (k + 64 < p.K) x1 = __ldg(x + 4);
                     }
                     // the scales of the two activation rows of this lane's sums
                     const int m0 = nt * 8 + 2 * t;
