@@ -61,11 +61,26 @@ cudaError_t allow_pair()
                                 static_cast<int>(mbglu::kFp8Smem));
 }
 
+constexpr int kRowsSmem = 196 * 1024;   // beside up to 27 KB of static shared memory
+
+template <int NT, int OUT, int WARPS, int DEPTH, int PER_SM>
+cudaError_t allow_rows()
+{
+    return cudaFuncSetAttribute(mbglu::fp8_rows_kernel<NT, OUT, WARPS, DEPTH, PER_SM>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
+}
+
 cudaError_t setup_fp8()
 {
     cudaError_t e = allow_pair<mbglu::kFp8Out>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8Glu>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8GluQuant>();
+    if (e == cudaSuccess) e = allow_rows<1, 0, 8, 4, 2>();
+    if (e == cudaSuccess) e = allow_rows<2, 0, 8, 2, 2>();
+    if (e == cudaSuccess) e = allow_rows<1, 1, 8, 2, 2>();
+    if (e == cudaSuccess) e = allow_rows<2, 1, 8, 2, 1>();
+    if (e == cudaSuccess) e = allow_rows<1, 2, 8, 2, 2>();
+    if (e == cudaSuccess) e = allow_rows<2, 2, 8, 2, 1>();
     return e;
 }
 
@@ -93,17 +108,24 @@ mbglu_status launch_pair(const mbglu::Fp8PairParams &p, const mbglu::PairMaps &m
     return st;
 }
 
-bool rows_take(int M, int K) { return K > 0 && K % 16 == 0 && M <= mbglu::kRowsMax; }
+bool rows_take(int M, int K)
+{
+    return K > 0 && K % 16 == 0 && M <= mbglu::kRowsMax && mbglu::rows_smem(M, K, 2) <= kRowsSmem;
+}
 
 template <int NT, int OUT, int WARPS, int DEPTH, int PER_SM>
 mbglu_status launch_rows(mbglu::Fp8RowsParams &p, int slices, cudaStream_t stream)
 {
+    int sms = 0;
+    mbglu_status st = sm_count(&sms);   // sets the kernels' attributes once per device
+    if (st != MBGLU_OK) return st;
     p.slices = slices;
     p.prefetch = launch_policy() == MBGLU_POLICY_PREFETCH;
     const int R = WARPS / slices, cluster = OUT == 2 ? 8 / R : 1;
     const int blocks = OUT == 2 ? ceil_div(p.N, kBlk) * cluster : ceil_div(p.N, 16 * R);
-    Launch l(dim3(static_cast<unsigned>(blocks)), WARPS * 32, 0, stream, cluster);
-    const mbglu_status st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<NT, OUT, WARPS, DEPTH, PER_SM>, p));
+    p.pitch = mbglu::rows_pitch(p.K);
+    Launch l(dim3(static_cast<unsigned>(blocks)), WARPS * 32, static_cast<size_t>(mbglu::rows_smem(p.M, p.K, OUT == 0 ? 1 : 2)), stream, cluster);
+    st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<NT, OUT, WARPS, DEPTH, PER_SM>, p));
     if (st == MBGLU_OK) set_last_variant(kFp8Rows);
     return st;
 }

@@ -32,6 +32,7 @@ struct Fp8RowsParams {
     const float *ws[2];
     int64_t ldws[2];
     int M, N, K;
+    int pitch;               // bytes between activation rows in shared memory (rows_pitch)
     int slices;              // S, a power of two up to the warps of a block; R = warps / S
     int prefetch;            // the first weight blocks are requested before the dependency wait
     uint16_t *out;
@@ -48,6 +49,19 @@ __device__ __forceinline__ uint4 ldg_stream16(const uint8_t *p)
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
+
+// Activation rows in shared memory: 64 bytes past a multiple of 128, so that
+// the two rows of a quarter-warp's load lie in different halves of the banks.
+__host__ __device__ constexpr int rows_pitch(int K) { return (K + 127) / 128 * 128 + 64; }
+
+// All activations, then their scales, then the weights' scales of one block row
+// (fp32): what a block keeps in shared memory.
+__host__ __device__ constexpr int64_t rows_smem(int M, int K, int mats)
+{
+    return static_cast<int64_t>(M) * rows_pitch(K) + (static_cast<int64_t>(M) + mats) * ((K + 127) / 128) * 4;
+}
+
+__device__ __forceinline__ bool rows_wait(uint64_t *bar) { return mbar_wait_bounded(bar, 0, kWaitLimitNs); }
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -70,6 +84,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PER_SM) fp8_rows_kernel(const
     __shared__ float part[kRowsWarps][kPart];
     __shared__ float vals[OUT == 2 ? MP * 128 : 1];      // the gated values, [m][columns of the block]
     __shared__ float peaks[OUT == 2 ? 8 * MP : 1];       // [block of the cluster][m]
+    extern __shared__ __align__(128) unsigned char rows_raw[];
+    __shared__ uint64_t xbar;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int S = p.slices, R = kRowsWarps / S;
@@ -77,7 +93,6 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PER_SM) fp8_rows_kernel(const
     const int kb = (p.K + kScaleBlock - 1) / kScaleBlock;
     const int b0 = kb * slice / S, b1 = kb * (slice + 1) / S;
     const int n0 = (static_cast<int>(blockIdx.x) * R + group) * 16;    // this warp's rows of the weights
-    const int wb = n0 / kScaleBlock;
     const bool live = n0 < p.N;
     const int r0 = min(n0 + g, p.N - 1), r1 = min(n0 + g + 8, p.N - 1);
 
@@ -101,14 +116,41 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PER_SM) fp8_rows_kernel(const
             dst[d][3] = ldg_stream16(w1[d] + k1);
         }
     };
+    unsigned char *xs = rows_raw;
+    float *sa = reinterpret_cast<float *>(rows_raw + p.M * p.pitch), *sw = sa + p.M * kb;
+    if (threadIdx.x == 0) {
+        mbar_init(&xbar, 1);
+        fence_mbar_init();
+    }
     if (!p.prefetch) grid_dependency_wait();
     if (live) {
 #pragma unroll
         for (int i = 0; i < kRowsDepth; ++i)
             if (b0 + i < b1) load_w(w[i], b0 + i);
     }
+    // a block's weight rows lie in one row of scale blocks
+    const int swrow = min(static_cast<int>(blockIdx.x) * R * 16, p.N - 1) / kScaleBlock;
+    for (int i = threadIdx.x; i < MAT * kb; i += kRowsWarps * 32) {
+        const int d = i / kb, b = i - d * kb;
+        sw[i] = __ldg(p.ws[d] + swrow * p.ldws[d] + b);
+    }
     if (p.prefetch) grid_dependency_wait();
     grid_launch_dependents();
+    // the activations once per block: the loop would else wait for L2 at every
+    // scale block
+    if (threadIdx.x == 0) {
+        mbar_arrive_expect_tx(&xbar, static_cast<uint32_t>(p.M) * static_cast<uint32_t>(p.K));
+        for (int m = 0; m < p.M; ++m) bulk_g2s_plain(xs + m * p.pitch, p.a + m * p.lda, static_cast<uint32_t>(p.K), &xbar);
+    }
+    for (int i = threadIdx.x; i < p.M * kb; i += kRowsWarps * 32) {
+        const int m = i / kb, b = i - m * kb;
+        sa[i] = p.as[m * p.ldas + b];
+    }
+    __syncthreads();
+    if (!rows_wait(&xbar)) {
+        atomicExch(&g_dense_error, kErrTimeout);
+        rows_wait(&xbar);   // no copy may be in flight when the block leaves
+    }
 
     float total[MAT][NT][4] = {};
     if (live) {
@@ -120,20 +162,20 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PER_SM) fp8_rows_kernel(const
                 const int k = (b + i) * kScaleBlock + t * 16;
                 float f[MAT];
 #pragma unroll
-                for (int d = 0; d < MAT; ++d) f[d] = __ldg(p.ws[d] + wb * p.ldws[d] + b + i);
+                for (int d = 0; d < MAT; ++d) f[d] = sw[d * kb + b + i];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int m = nt * 8 + g;
                     uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
                     if (m < p.M) {
-                        const uint4 *x = reinterpret_cast<const uint4 *>(p.a + m * p.lda + k);
-                        if (k < p.K) x0 = __ldg(x);
-                        if (k + 64 < p.K) x1 = __ldg(x + 4);
+                        const uint4 *x = reinterpret_cast<const uint4 *>(xs + m * p.pitch + k);
+                        if (k < p.K) x0 = x[0];
+                        if (k + 64 < p.K) x1 = x[4];
                     }
                     // the scales of the two activation rows of this lane's sums
                     const int m0 = nt * 8 + 2 * t;
-                    const float s0 = m0 < p.M ? __ldg(p.as + m0 * p.ldas + b + i) : 0.0f;
-                    const float s1 = m0 + 1 < p.M ? __ldg(p.as + (m0 + 1) * p.ldas + b + i) : 0.0f;
+                    const float s0 = m0 < p.M ? sa[m0 * kb + b + i] : 0.0f;
+                    const float s1 = m0 + 1 < p.M ? sa[(m0 + 1) * kb + b + i] : 0.0f;
 #pragma unroll
                     for (int d = 0; d < MAT; ++d) {
                         const uint4 *q = w[i][d];
