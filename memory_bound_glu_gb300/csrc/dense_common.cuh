@@ -17,13 +17,45 @@ constexpr int kScaleBlock = 128;                  // columns (and, for weights, 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleMin = 1.17549435e-38f;      // 2^-126: the scale of a group of zeros
 
-// dG = dout u SiLU'(g), dU = dout SiLU(g), in fp32
+// e^-|x|.  With z = |x| log2(e) rounded and r what the rounding left out,
+// e^-|x| = 2^-z (1 - r ln 2): relative error below 2^-21 over the whole range
+// (2^-z alone is off by |x| 2^-24).  |x| is capped where the result is 0 anyway,
+// so that infinities leave no inf - inf.
+__device__ __forceinline__ float exp_neg_abs(float x)
+{
+    constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const float a = fminf(fabsf(x), 200.0f);
+    const float z = a * kLog2e;
+    const float r = fmaf(a, kLog2eLow, fmaf(a, kLog2e, -z));
+    float t;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(-z));
+    return fmaf(t * r, -kLn2, t);
+}
+
+// SiLU(x), relative error below 2^-20, in a third of the instructions of the
+// precise form (silu_f32).  An epilogue that is unrolled over a thread's 64
+// outputs is bound by fetching its instructions once per tile: glu_fp8's at
+// M = 48, K = 128 took 17.0 us with the precise form.
+__device__ __forceinline__ float silu_short(float x)
+{
+    const float t = exp_neg_abs(x);
+    return __fdividef(x >= 0.0f ? x : x * t, 1.0f + t);
+}
+
+// the GLU epilogue's roundings (glu_epilogue) on silu_short
+__device__ __forceinline__ uint32_t glu_hf_short(float g, float u)
+{
+    return f32_to_bf16(round_to_bf16(silu_short(round_to_bf16(g))) * round_to_bf16(u));
+}
+
+// dG = dout u SiLU'(g), dU = dout SiLU(g), in fp32: with s the sigmoid,
+// SiLU' = s (1 + g (1 - s))
 __device__ __forceinline__ void glu_gradients(float g, float u, float d, float &dg, float &du)
 {
-    float s, ds;
-    silu_and_derivative(g, s, ds);
-    dg = d * u * ds;
-    du = d * s;
+    const float t = exp_neg_abs(g), inv = __fdividef(1.0f, 1.0f + t);
+    const float s = (g >= 0.0f ? 1.0f : t) * inv, rest = (g >= 0.0f ? t : 1.0f) * inv;
+    dg = d * u * (s * fmaf(g, rest, 1.0f));
+    du = d * (g * s);
 }
 
 // max that keeps a NaN (fmaxf drops it): a group with a NaN gets a NaN scale

@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
                 float amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    acc[i].x = silu_f32(acc[i].x) * acc[32 + i].x;
-                    acc[i].y = silu_f32(acc[i].y) * acc[32 + i].y;
+                    acc[i].x = silu_short(acc[i].x) * acc[32 + i].x;
+                    acc[i].y = silu_short(acc[i].y) * acc[32 + i].y;
                     // columns past the last are sums over zeros unless a scale is
                     // not finite; they are no part of the group
                     if (EPI == kFp8GluQuant) {

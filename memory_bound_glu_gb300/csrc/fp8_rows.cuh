@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PER_SM) fp8_rows_kernel(const
             if (OUT == 0) {
                 if (n < p.N) p.out[m * p.ldo + n] = f32_to_bf16(x);
             } else {
-                const float v = silu_f32(x) * joined(MAT - 1, c, m);
+                const float v = silu_short(x) * joined(MAT - 1, c, m);
                 if (OUT == 1) {
                     if (n < p.N) p.out[m * p.ldo + n] = f32_to_bf16(v);
                 } else {

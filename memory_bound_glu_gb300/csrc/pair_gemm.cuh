@@ -323,9 +323,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
                             w[i] = pack_bf16x2(dg0, dg1);
                             w2[i] = pack_bf16x2(du0, du1);
                         } else if (p.mode == 0) {
-                            w[i] = pack_bf16x2(silu_f32(g0) * u0, silu_f32(g1) * u1);
+                            w[i] = pack_bf16x2(silu_short(g0) * u0, silu_short(g1) * u1);
                         } else {
-                            w[i] = glu_epilogue(g0, u0, 1) | (static_cast<uint32_t>(glu_epilogue(g1, u1, 1)) << 16);
+                            w[i] = glu_hf_short(g0, u0) | (glu_hf_short(g1, u1) << 16);
                         }
                     }
                     store_bf16_32(p.out[0] + m * p.ldo[0] + n, w, valid, p.out_align[0]);
