@@ -76,7 +76,6 @@ cudaError_t setup_fp8()
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8Glu>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8GluQuant>();
     if (e == cudaSuccess) e = allow_rows<1, 0, 8, 4, 2>();
-    if (e == cudaSuccess) e = allow_rows<2, 0, 8, 2, 2>();
     if (e == cudaSuccess) e = allow_rows<1, 1, 8, 2, 2>();
     if (e == cudaSuccess) e = allow_rows<2, 1, 8, 2, 1>();
     if (e == cudaSuccess) e = allow_rows<1, 2, 8, 2, 2>();
@@ -113,6 +112,11 @@ bool rows_take(int M, int K)
     return K > 0 && K % 16 == 0 && M <= mbglu::kRowsMax && mbglu::rows_smem(M, K, 2) <= kRowsSmem;
 }
 
+// One weight gives a row kernel's warps half the bytes per activation row, and
+// beyond 8 rows the split product on CTA pairs is faster (K = 9728, N = 2560: 16.0
+// us at M = 9 against 12.9).
+bool rows_take_matmul(int M, int K) { return M <= 8 && rows_take(M, K); }
+
 template <int NT, int OUT, int WARPS, int DEPTH, int PER_SM>
 mbglu_status launch_rows(mbglu::Fp8RowsParams &p, int slices, cudaStream_t stream)
 {
@@ -142,8 +146,7 @@ int rows_slices(int N, int K, int warps, int most_blocks)
 
 mbglu_status matmul_rows(mbglu::Fp8RowsParams &p, cudaStream_t stream)
 {
-    const int slices = rows_slices(p.N, p.K, 8, 4 * kPairs);
-    return p.M <= 8 ? launch_rows<1, 0, 8, 4, 2>(p, slices, stream) : launch_rows<2, 0, 8, 2, 2>(p, slices, stream);
+    return launch_rows<1, 0, 8, 4, 2>(p, rows_slices(p.N, p.K, 8, 4 * kPairs), stream);
 }
 
 // A cluster's blocks start together on one part of the chip, so that not quite
@@ -177,7 +180,11 @@ void rows_weight(mbglu::Fp8RowsParams &p, int d, const Scaled &w)
     p.ldws[d] = w.lds;
 }
 
-int matmul_splits(int M, int N, int K) { return rows_take(M, K) ? 1 : pair_splits(M, N, ceil_div(K, kBlk)); }
+mbglu::PairPlan matmul_plan(int M, int N, int K)
+{
+    const int chunks = ceil_div(K, kBlk);
+    return pair_plan(M, N, 256, 1, chunks, chunks, true);
+}
 
 }  // namespace
 
@@ -239,8 +246,7 @@ mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw, uint8_t *q, i
 size_t matmul_fp8_workspace_bytes(int M, int N, int K)
 {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
-    const int splits = matmul_splits(M, N, K);
-    return splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(M) * static_cast<size_t>(part_width(N)) * 4 : 0;
+    return rows_take_matmul(M, K) ? 0 : static_cast<size_t>(part_bytes(matmul_plan(M, N, K)));
 }
 
 mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas, const uint8_t *w,
@@ -266,7 +272,7 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
     if (meets(out, ob, A, K) || meets(out, ob, W, K) || meets(workspace, wsb, A, K) || meets(workspace, wsb, W, K) ||
         overlaps(out, ob, workspace, wsb))
         return MBGLU_ERR_ALIAS;
-    if (rows_take(M, K) && copyable(a, lda, 1) && copyable(w, ldw, 1)) {
+    if (rows_take_matmul(M, K) && copyable(a, lda, 1) && copyable(w, ldw, 1)) {
         mbglu::Fp8RowsParams q = rows_params(A, M, N, K);
         rows_weight(q, 0, W);
         q.out = out;
@@ -275,9 +281,8 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
     }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], W, K)) {
-        const int splits = matmul_splits(M, N, K), chunks = ceil_div(K, kBlk);
         mbglu::Fp8PairParams q = {};
-        q.plan = pair_plan(M, N, 256, 1, chunks, chunks, splits);
+        q.plan = matmul_plan(M, N, K);
         q.as = a_scale;
         q.ldas = ldas;
         q.ws[0] = w_scale;
@@ -287,10 +292,10 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
         q.ldo = ldo;
         q.out_align = row_align(out, ldo, 2);
         q.part = static_cast<float *>(workspace);
-        q.ldp = part_width(N);
-        mbglu_status st = launch_pair<mbglu::kFp8Out>(q, maps, stream);
-        if (st == MBGLU_OK && splits > 1) st = launch_join(q.part, splits, M, N, out, ldo, stream);
-        return st;
+        const mbglu_status st = launch_pair<mbglu::kFp8Out>(q, maps, stream);
+        uint16_t *const outs[2] = {out, nullptr};
+        const int64_t ldos[2] = {ldo, 0};
+        return st == MBGLU_OK ? launch_join(q.plan, q.part, outs, ldos, stream) : st;
     }
     mbglu::GenParams p = {};
     p.a[0] = operand(a, lda, a_scale, ldas);
@@ -343,7 +348,7 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], G, K) && k_major(&maps.b[1], U, K)) {
         mbglu::Fp8PairParams p = {};
-        p.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, kBlk), 1);
+        p.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, kBlk), false);
         p.as = a_scale;
         p.ldas = ldas;
         p.ws[0] = gate_scale;

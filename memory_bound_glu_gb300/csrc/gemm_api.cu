@@ -76,10 +76,13 @@ mbglu_status launch_pair(const mbglu::PairParams &p, const mbglu::PairMaps &maps
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_gemm_kernel<EPI, MODE, A_MN, B_MN>, p, maps));
 }
 
-int grad_h_splits(int M, int N, int K)
+// grad_h [M, K] over 2 N; grad_gate and grad_up [N, K] over M
+mbglu::PairPlan grad_h_plan(int M, int N, int K)
 {
-    return pair_splits(M, K, 2 * static_cast<int64_t>(ceil_div(N, 64)));
+    const int chunks = ceil_div(N, 64);
+    return pair_plan(M, K, 256, 1, chunks, 2 * chunks, true);
 }
+mbglu::PairPlan grad_w_plan(int M, int N, int K) { return pair_plan(N, K, 256, 2, 0, ceil_div(M, 64), true); }
 
 }  // namespace
 
@@ -113,7 +116,7 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
     if (K > 0 && copyable(h, ldh, 2) && copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2) && k_major(&maps.a[0], h, ldh, M, K) &&
         k_major(&maps.b[0], gate_w, ld_gate, N, K) && k_major(&maps.b[1], up_w, ld_up, N, K)) {
         mbglu::PairParams q = {};
-        q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), 1);
+        q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), false);
         q.mode = static_cast<int>(mode);
         q.out[0] = out;
         q.ldo[0] = ldo;
@@ -152,9 +155,8 @@ static int64_t grad_bytes(int M, int N) { return (2 * static_cast<int64_t>(M) * 
 size_t glu_gemm_backward_workspace_bytes(int M, int N, int K)
 {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
-    const int splits = grad_h_splits(M, N, K);
-    const int64_t part = splits > 1 ? static_cast<int64_t>(splits) * M * part_width(K) * 4 : 0;
-    return static_cast<size_t>(grad_bytes(M, N) + part);
+    // the two products' partial sums, one after the other
+    return static_cast<size_t>(grad_bytes(M, N) + std::max(part_bytes(grad_h_plan(M, N, K)), part_bytes(grad_w_plan(M, N, K))));
 }
 
 mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w, int64_t ld_gate,
@@ -207,6 +209,7 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
     const int64_t W = grad_width(N);
     uint16_t *dG = static_cast<uint16_t *>(workspace), *dU = dG + static_cast<int64_t>(M) * W;
 
+    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + grad_bytes(M, N));
     const bool fast_h = copyable(h, ldh, 2), fast_w = copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2);
     mbglu_status st = MBGLU_OK;
     mbglu::PairMaps maps;
@@ -222,7 +225,7 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
     } else if (fast_h && fast_w && k_major(&maps.a[0], h, ldh, M, K) && k_major(&maps.b[0], gate_w, ld_gate, N, K) &&
                k_major(&maps.b[1], up_w, ld_up, N, K)) {
         mbglu::PairParams q = {};
-        q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), 1);
+        q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), false);
         q.out[0] = dG;
         q.out[1] = dU;
         q.ldo[0] = q.ldo[1] = W;
@@ -253,16 +256,14 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
     // 2) grad_h = dG Wg + dU Wu: one sum over 2N
     if (st == MBGLU_OK && want_h && fast_w && k_major(&maps.a[0], dG, W, M, N) && k_major(&maps.a[1], dU, W, M, N) &&
         mn_major(&maps.b[0], gate_w, ld_gate, N, K) && mn_major(&maps.b[1], up_w, ld_up, N, K)) {
-        const int splits = grad_h_splits(M, N, K), chunks = ceil_div(N, 64);
         mbglu::PairParams q = {};
-        q.plan = pair_plan(M, K, 256, 1, chunks, 2 * chunks, splits);
+        q.plan = grad_h_plan(M, N, K);
         q.out[0] = grad_h;
         q.ldo[0] = ldgh;
         q.out_align[0] = row_align(grad_h, ldgh, 2);
-        q.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + grad_bytes(M, N));
-        q.ldp = part_width(K);
+        q.part = part;
         st = launch_pair<mbglu::kPairPlain, mbglu::kPairSum, false, true>(q, maps, stream);
-        if (st == MBGLU_OK && splits > 1) st = launch_join(q.part, splits, M, K, grad_h, ldgh, stream);
+        if (st == MBGLU_OK) st = launch_join(q.plan, part, q.out, q.ldo, stream);
     } else if (st == MBGLU_OK && want_h) {
         path = 5;
         mbglu::GenParams q = {};
@@ -283,7 +284,8 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
     if (st == MBGLU_OK && want_w && fast_h && mn_major(&maps.a[0], dG, W, M, N) && mn_major(&maps.a[1], dU, W, M, N) &&
         mn_major(&maps.b[0], h, ldh, M, K)) {
         mbglu::PairParams q = {};
-        q.plan = pair_plan(N, K, 256, 2, 0, ceil_div(M, 64), 1);
+        q.plan = grad_w_plan(M, N, K);
+        q.part = part;
         q.out[0] = grad_gate;
         q.out[1] = grad_up;
         q.ldo[0] = ldgg;
@@ -291,6 +293,7 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
         q.out_align[0] = row_align(grad_gate, ldgg, 2);
         q.out_align[1] = row_align(grad_up, ldgu_w, 2);
         st = launch_pair<mbglu::kPairPlain, mbglu::kPairStack, true, true>(q, maps, stream);
+        if (st == MBGLU_OK) st = launch_join(q.plan, part, q.out, q.ldo, stream);
     } else if (want_w) {
         path = 5;
         for (int i = 0; st == MBGLU_OK && want_w && i < 2; ++i) {   // dG^T h, dU^T h

@@ -54,22 +54,22 @@ struct PairMaps {
 struct PairPlan {
     int rows, cols;          // of one output
     int mt, nt, nout;        // row tiles, column tiles, outputs
-    int splits;              // ranges of the inner dimension per tile
-    int ntiles;              // mt nt nout splits
+    int whole;               // tiles done whole: full rounds over the SM pairs
+    int rest, splits;        // the others, each in `splits` ranges of the inner dimension
+    int ntiles;              // whole + rest splits: work items
     int group;
     int nchunk0, nchunk;     // chunks of the first product, of all
 };
 
 struct PairTileAt {
-    int o, split, mi, ni, c0, c1;
+    int o, mi, ni, c0, c1;
+    int slot;   // where a range's partial sums go, or -1
 };
 
-__host__ __device__ inline PairTileAt pair_tile(const PairPlan &p, int t)
+// Tile `t` of the outputs: rows first within groups of row tiles.
+__host__ __device__ inline void pair_place(const PairPlan &p, int t, PairTileAt &x)
 {
-    PairTileAt x;
     const int per = p.mt * p.nt;
-    x.split = t / (per * p.nout);
-    t -= x.split * per * p.nout;
     x.o = t / per;
     t -= x.o * per;
     const int g = t / (p.group * p.nt), first = g * p.group;
@@ -77,10 +77,27 @@ __host__ __device__ inline PairTileAt pair_tile(const PairPlan &p, int t)
     t -= first * p.nt;
     x.mi = first + t % gm;
     x.ni = t / gm;
-    x.c0 = static_cast<int>(static_cast<int64_t>(p.nchunk) * x.split / p.splits);
-    x.c1 = static_cast<int>(static_cast<int64_t>(p.nchunk) * (x.split + 1) / p.splits);
+}
+
+__host__ __device__ inline PairTileAt pair_tile(const PairPlan &p, int t)
+{
+    PairTileAt x;
+    x.slot = t < p.whole ? -1 : t - p.whole;
+    x.c0 = 0;
+    x.c1 = p.nchunk;
+    if (x.slot >= 0) {
+        const int split = x.slot / p.rest;
+        t = p.whole + x.slot % p.rest;
+        x.c0 = static_cast<int>(static_cast<int64_t>(p.nchunk) * split / p.splits);
+        x.c1 = static_cast<int>(static_cast<int64_t>(p.nchunk) * (split + 1) / p.splits);
+        if (p.splits == 1) x.slot = -1;
+    }
+    pair_place(p, t, x);
     return x;
 }
+
+// fp32 values of one slot: a tile, row by row
+constexpr int64_t kPairSlot = static_cast<int64_t>(kPairTile) * kPairTile;
 
 struct PairShared {
     uint64_t *full, *empty, *acc_full, *acc_empty;
@@ -262,8 +279,7 @@ struct PairParams {
     const uint16_t *dout;
     int64_t ldd;
     int dout_align;
-    float *part;             // splits > 1: [splits][rows][ldp]
-    int64_t ldp;
+    float *part;             // ranges' partial sums, kPairSlot each
 };
 
 template <int EPI, int MODE, bool A_MN, bool B_MN>
@@ -354,11 +370,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
                         if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
                     }
                     if (!ok || !row || valid <= 0) continue;
-                    if (p.plan.splits > 1) {
+                    if (x.slot >= 0) {
                         float f[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-                        store_f32_32(p.part + (static_cast<int64_t>(x.split) * p.plan.rows + m) * p.ldp + n, f, valid, 2);
+                        store_f32_32(p.part + x.slot * kPairSlot + (rank * 128 + q * 32 + lane) * kPairTile + c, f, 32, 2);
                     } else {
                         uint32_t w[16];
 #pragma unroll
@@ -375,33 +391,44 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
     pair_teardown(warp, tmem);
 }
 
-// out = bf16(sum of the splits' partial sums, in order); 4 columns per thread
-// where they lie on 8 bytes (vec), else one.
-static __global__ void __launch_bounds__(256) pair_join_kernel(const float *part, int splits, int rows, int cols, int64_t ldp,
-                                                        uint16_t *out, int64_t ldo, int vec)
+struct PairJoin {
+    PairPlan plan;
+    const float *part;
+    uint16_t *out[2];
+    int64_t ldo[2];
+    int vec[2];              // rows of the output lie on 8 bytes
+};
+
+// The split tiles: out = bf16(sum of their ranges' partial sums, in order).  A
+// block of 256 threads takes 4 rows of a tile, 4 columns per thread.
+static __global__ void __launch_bounds__(256) pair_join_kernel(const PairJoin p)
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int per = vec ? cols / 4 : cols;
-    const int64_t total = static_cast<int64_t>(rows) * per;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t m = i / per;
-        const int c = static_cast<int>(i - m * per);
-        if (vec) {
-            float4 a = make_float4(0, 0, 0, 0);
-            for (int s = 0; s < splits; ++s) {
-                const float4 b = __ldcs(reinterpret_cast<const float4 *>(part + (s * static_cast<int64_t>(rows) + m) * ldp) + c);
-                a.x += b.x;
-                a.y += b.y;
-                a.z += b.z;
-                a.w += b.w;
-            }
-            *reinterpret_cast<uint2 *>(out + m * ldo + 4 * c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-        } else {
-            float a = 0.0f;
-            for (int s = 0; s < splits; ++s) a += part[(s * static_cast<int64_t>(rows) + m) * ldp + c];
-            out[m * ldo + c] = f32_to_bf16(a);
-        }
+    const int tile = blockIdx.x >> 6, r = (blockIdx.x & 63) * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
+    PairTileAt x;
+    pair_place(p.plan, p.plan.whole + tile, x);
+    const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + r;
+    const int n = x.ni * kPairTile + c, valid = p.plan.cols - n;
+    if (m >= p.plan.rows || valid <= 0) return;
+    const float *q = p.part + tile * kPairSlot + r * kPairTile + c;
+    float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int s = 0; s < p.plan.splits; ++s) {
+        const float4 b = __ldcs(reinterpret_cast<const float4 *>(q + static_cast<int64_t>(s) * p.plan.rest * kPairSlot));
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+    }
+    uint16_t *o = p.out[x.o] + m * p.ldo[x.o] + n;
+    const uint2 w = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    if (p.vec[x.o] && valid >= 4) {
+        *reinterpret_cast<uint2 *>(o) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < valid) o[i] = static_cast<uint16_t>((i < 2 ? w.x : w.y) >> ((i & 1) * 16));
     }
 }
 

@@ -19,19 +19,14 @@ inline int row_align(const void *p, int64_t ld, int elem)
     return aligned(p, 32) && ld * elem % 32 == 0 ? 2 : aligned(p, 16) && ld * elem % 16 == 0 ? 1 : 0;
 }
 
-// Ranges of the inner dimension (of `chunks` stages): where 256 x 256 tiles
-// leave most SM pairs idle, as many as fill them, each of at least 8 stages.
-// From the sizes alone, so that the sum's order does not depend on the device.
-inline int pair_splits(int rows, int cols, int64_t chunks)
-{
-    const int64_t tiles = static_cast<int64_t>(ceil_div(rows, mbglu::kPairTile)) * ceil_div(cols, mbglu::kPairTile);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, chunks / 8, 16})));
-}
-
-// Row stride of the partial sums, fp32: rows start on 32 bytes.
-inline int64_t part_width(int cols) { return (static_cast<int64_t>(cols) + 7) / 8 * 8; }
-
-inline mbglu::PairPlan pair_plan(int rows, int cols, int tile_cols, int nout, int nchunk0, int nchunk, int splits)
+// A product's tiles over the SM pairs: full rounds whole; what is left over,
+// where it fills at most half of the pairs, in as many ranges of the inner
+// dimension as fill them (each of at least 8 stages), if that shortens the
+// product by more than the join of the partial sums costs (about 24 stages'
+// time, 6 us).  From the sizes alone, so that the order of a sum does not depend
+// on the device.  M = 4096, K = 2560, 2 N = 19456: grad_h's 160 tiles and
+// their join take 218 us against 277 us in three rounds.
+inline mbglu::PairPlan pair_plan(int rows, int cols, int tile_cols, int nout, int nchunk0, int nchunk, bool may_split)
 {
     mbglu::PairPlan p = {};
     p.rows = rows;
@@ -39,21 +34,43 @@ inline mbglu::PairPlan pair_plan(int rows, int cols, int tile_cols, int nout, in
     p.mt = ceil_div(rows, mbglu::kPairTile);
     p.nt = ceil_div(cols, tile_cols);
     p.nout = nout;
-    p.splits = splits;
-    p.ntiles = p.mt * p.nt * nout * splits;
     p.group = 8;
     p.nchunk0 = nchunk0;
     p.nchunk = nchunk;
+    const int tiles = p.mt * p.nt * nout;
+    p.whole = tiles;
+    p.rest = 0;
+    p.splits = 1;
+    const int left = tiles % kPairs;
+    if (may_split && left > 0) {
+        const int s = std::min({kPairs / left, nchunk / 8, 16});
+        if (s > 1 && nchunk - nchunk / s >= 24) {
+            p.whole = tiles - left;
+            p.rest = left;
+            p.splits = s;
+        }
+    }
+    p.ntiles = p.whole + p.rest * p.splits;
     return p;
 }
 
-inline mbglu_status launch_join(const float *part, int splits, int rows, int cols, uint16_t *out, int64_t ldo,
+// Bytes of the partial sums.
+inline int64_t part_bytes(const mbglu::PairPlan &p) { return static_cast<int64_t>(p.rest) * p.splits * mbglu::kPairSlot * 4; }
+
+inline mbglu_status launch_join(const mbglu::PairPlan &plan, const float *part, uint16_t *const out[2], const int64_t ldo[2],
                                 cudaStream_t stream)
 {
-    const int vec = cols % 4 == 0 && aligned(out, 8) && ldo % 4 == 0;
-    const int64_t work = static_cast<int64_t>(rows) * (vec ? cols / 4 : cols);
-    Launch l(dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, 1 << 20))), 256, 0, stream);
-    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_join_kernel, part, splits, rows, cols, part_width(cols), out, ldo, vec));
+    if (plan.rest == 0) return MBGLU_OK;
+    mbglu::PairJoin p = {};
+    p.plan = plan;
+    p.part = part;
+    for (int o = 0; o < plan.nout; ++o) {
+        p.out[o] = out[o];
+        p.ldo[o] = ldo[o];
+        p.vec[o] = aligned(out[o], 8) && ldo[o] % 4 == 0;
+    }
+    Launch l(dim3(static_cast<unsigned>(plan.rest) * 64), 256, 0, stream);
+    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_join_kernel, p));
 }
 
 }  // namespace mbglu_host
