@@ -337,8 +337,8 @@ def add_rmsnorm_glu(x, residual, norm_w, eps, gate_w, up_w, out=None, mode="hf",
 
 
 def _check_operand(t, name, dtype, shape, dev):
-    """One operand of the e4m3 (and wide bf16) calls: dtype, shape, device and
-    a contiguous last dimension; any row stride."""
+    """One operand of the wide and the e4m3 calls: dtype, device, shape and a
+    contiguous last dimension; any row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -351,32 +351,76 @@ def _check_operand(t, name, dtype, shape, dev):
         raise ValueError(f"{name} must have a contiguous last dimension")
 
 
-def _row_stride(t):
-    """The row stride to pass: a tensor of one row may carry any (a 1-row view's
-    stride says nothing), so it gets its row's length."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _arg(t, name, dtype, rows, cols, dev):
+    """(pointer, row stride) of a checked [rows, cols] operand.  A tensor of one
+    row may carry any stride (a view's says nothing), so it gets its row's
+    length.  The common case is decided in a few attribute reads: a decode step's
+    kernels take microseconds, and so would the checks."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == (rows, cols):
+        s0, s1 = t.stride()
+        if s1 == 1:
+            return t.data_ptr(), s0 if rows > 1 else cols
+    _check_operand(t, name, dtype, (rows, cols), dev)
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 1)
 
 
-def _row(t):
-    return t.data_ptr(), _row_stride(t)
+def _dims(t, name, dtype):
+    """(rows, cols, device) of a call's first operand, a 2-D CUDA tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    return (*t.shape, t.device)
+
+
+def _out_rows(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape[0]
 
 
 def _workspace(workspace, need, dev):
-    """(pointer, bytes) of a workspace of `need` bytes, allocated here by
+    """(pointer, bytes, tensor) of a workspace of `need` bytes, allocated here by
     torch's allocator on the current stream when not given."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), need, workspace
+    if not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    if workspace is None:
-        return None, 0, None
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+_here = contextlib.nullcontext()
+_one_device = None   # whether the process sees one GPU, which then is the current one
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _allocate_on(dev, stream):
-    """Allocations of a call belong to the stream that it runs on: torch's
-    allocator hands their memory out again in that stream's order."""
-    return torch.cuda.stream(stream) if stream is not None else _on(dev)
+    """The context of a call's allocations and launch: they belong to the stream
+    that the call runs on, whose order torch's allocator then hands their memory
+    out again in."""
+    global _one_device
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    return _here if _one_device else _on(dev)
+
+
+def _stream_of(dev, stream):
+    """The handle of the stream that a call runs on."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+_NONE = (None, 0)
 
 
 def glu_gemm(h, gate_w, up_w, out=None, mode="fused", gu=None, stream=None):
@@ -385,24 +429,18 @@ def glu_gemm(h, gate_w, up_w, out=None, mode="fused", gu=None, stream=None):
     tensor, receives g and u for glu_gemm_backward.  Up to MAX_M rows without
     gu the call is glu_gemv."""
     bf16 = torch.bfloat16
-    squeeze = h.dim() == 1
+    squeeze = isinstance(h, torch.Tensor) and h.dim() == 1
     h2 = h.unsqueeze(0) if squeeze else h
-    _check(h2, "h", 2)
-    _check(gate_w, "gate_w", 2)
-    M, K = h2.shape
-    N = gate_w.shape[0]
-    dev = h2.device
-    _check_operand(gate_w, "gate_w", bf16, (N, K), dev)
-    _check_operand(up_w, "up_w", bf16, (N, K), dev)
+    M, K, dev = _dims(h2, "h", bf16)
+    N = _out_rows(gate_w, "gate_w")
+    ins = (*_arg(h2, "h", bf16, M, K, dev), *_arg(gate_w, "gate_w", bf16, N, K, dev), *_arg(up_w, "up_w", bf16, N, K, dev))
     with _allocate_on(dev, stream):
         if out is None:
             out = torch.empty((M, N), dtype=bf16, device=dev)
         out2 = out.unsqueeze(0) if out.dim() == 1 else out
-        _check_operand(out2, "out", bf16, (M, N), dev)
-        if gu is not None:
-            _check_operand(gu, "gu", torch.float32, (M, 2 * N), dev)
-        st = lib().glu_gemm(*_row(h2), *_row(gate_w), *_row(up_w), *_row(out2), *(_row(gu) if gu is not None else (None, 0)),
-                            M, N, K, _MODES[mode], _stream_handle(dev, stream))
+        st = lib().glu_gemm(*ins, *_arg(out2, "out", bf16, M, N, dev),
+                            *(_NONE if gu is None else _arg(gu, "gu", torch.float32, M, 2 * N, dev)), M, N, K, _MODES[mode],
+                            _stream_of(dev, stream))
     if st != 0:
         raise MbgluError(st, "glu_gemm")
     return out2.view(N) if squeeze else out
@@ -416,34 +454,30 @@ def glu_gemm_backward(h, gate_w, up_w, dout, gu=None, grad_h=None, grad_gate=Non
     workspace is a byte tensor of glu_gemm_backward_workspace_bytes(M, N, K)
     bytes, 256-byte aligned, allocated here when not given."""
     bf16 = torch.bfloat16
-    _check(h, "h", 2)
-    _check(gate_w, "gate_w", 2)
-    M, K = h.shape
-    N = gate_w.shape[0]
-    dev = h.device
-    _check_operand(gate_w, "gate_w", bf16, (N, K), dev)
-    _check_operand(up_w, "up_w", bf16, (N, K), dev)
-    _check_operand(dout, "dout", bf16, (M, N), dev)
-    if gu is not None:
-        _check_operand(gu, "gu", torch.float32, (M, 2 * N), dev)
+    M, K, dev = _dims(h, "h", bf16)
+    N = _out_rows(gate_w, "gate_w")
+    ins = (*_arg(h, "h", bf16, M, K, dev), *_arg(gate_w, "gate_w", bf16, N, K, dev), *_arg(up_w, "up_w", bf16, N, K, dev),
+           *_arg(dout, "dout", bf16, M, N, dev), *(_NONE if gu is None else _arg(gu, "gu", torch.float32, M, 2 * N, dev)))
     with _allocate_on(dev, stream):
-        grads = []
-        for t, name, shape, want in ((grad_h, "grad_h", (M, K), want_h), (grad_gate, "grad_gate", (N, K), want_w),
-                                     (grad_up, "grad_up", (N, K), want_w)):
-            if not want:
-                t = None
-            elif t is None:
-                t = torch.empty(shape, dtype=bf16, device=dev)
-            else:
-                _check_operand(t, name, bf16, shape, dev)
-            grads.append(t)
+        if not want_h:
+            grad_h = None
+        elif grad_h is None:
+            grad_h = torch.empty((M, K), dtype=bf16, device=dev)
+        if not want_w:
+            grad_gate = grad_up = None
+        else:
+            if grad_gate is None:
+                grad_gate = torch.empty((N, K), dtype=bf16, device=dev)
+            if grad_up is None:
+                grad_up = torch.empty((N, K), dtype=bf16, device=dev)
+        outs = (*(_arg(grad_h, "grad_h", bf16, M, K, dev) if want_h else _NONE),
+                *(_arg(grad_gate, "grad_gate", bf16, N, K, dev) if want_w else _NONE),
+                *(_arg(grad_up, "grad_up", bf16, N, K, dev) if want_w else _NONE))
         wsp, wsb, keep = _workspace(workspace, lib().glu_gemm_backward_workspace_bytes(M, N, K), dev)
-        rows = [_row(t) if t is not None else (None, 0) for t in (gu, *grads)]
-        st = lib().glu_gemm_backward(*_row(h), *_row(gate_w), *_row(up_w), *_row(dout), *rows[0], *rows[1], *rows[2],
-                                     *rows[3], M, N, K, wsp, wsb, _stream_handle(dev, stream))
+        st = lib().glu_gemm_backward(*ins, *outs, M, N, K, wsp, wsb, _stream_of(dev, stream))
     if st != 0:
         raise MbgluError(st, "glu_gemm_backward")
-    return tuple(grads)
+    return grad_h, grad_gate, grad_up
 
 
 E4M3 = torch.float8_e4m3fn
@@ -457,34 +491,33 @@ def _blocks(n):
 def _empty_e4m3(M, N, dev):
     """[M, N] e4m3 whose rows start on 16 bytes, as the products' tensor copies
     want their operands."""
-    t = torch.empty((M, -(-N // 16) * 16), dtype=E4M3, device=dev)
-    return t if t.shape[1] == N else t[:, :N]
+    if N % 16 == 0:
+        return torch.empty((M, N), dtype=E4M3, device=dev)
+    return torch.empty((M, -(-N // 16) * 16), dtype=E4M3, device=dev)[:, :N]
 
 
-def _check_scaled(t, scale, name, shape, scale_shape, dev):
-    _check_operand(t, name, E4M3, shape, dev)
-    _check_operand(scale, name + "'s scale", torch.float32, scale_shape, dev)
+def _scaled(t, scale, name, rows, cols, scale_rows, dev):
+    """(pointer, row stride) of an e4m3 operand, then of its scales."""
+    return (*_arg(t, name, E4M3, rows, cols, dev), *_arg(scale, name + "'s scale", torch.float32, scale_rows, _blocks(cols), dev))
 
 
 def add_rmsnorm_fp8(x, residual, norm_w, eps, q=None, scale=None, residual_out=None, stream=None):
     """residual_out <- bf16(x + residual) (in place when not given); v = its
     zero-centred RMSNorm; returns (q, scale): v as e4m3 [M,K] with a float32
     scale per row and 128 columns [M, ceil(K/128)]."""
-    _check(x, "x", 2)
-    M, K = x.shape
-    dev = x.device
-    if residual_out is None:
-        residual_out = residual
-    for t, name, shape in ((residual, "residual", (M, K)), (residual_out, "residual_out", (M, K)), (norm_w, "norm_w", (K,))):
-        _check_operand(t, name, torch.bfloat16, shape, dev)
+    bf16 = torch.bfloat16
+    M, K, dev = _dims(x, "x", bf16)
+    if norm_w is None or norm_w.dim() != 1 or norm_w.shape[0] != K or norm_w.dtype is not bf16 or norm_w.device != dev \
+            or not norm_w.is_contiguous():
+        raise ValueError(f"norm_w must be a contiguous bfloat16 tensor of {K} elements on {dev}")
+    ins = (*_arg(x, "x", bf16, M, K, dev), *_arg(residual, "residual", bf16, M, K, dev),
+           *_arg(residual if residual_out is None else residual_out, "residual_out", bf16, M, K, dev), norm_w.data_ptr(), eps)
     with _allocate_on(dev, stream):
         if q is None:
             q = _empty_e4m3(M, K, dev)
         if scale is None:
             scale = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev)
-        _check_scaled(q, scale, "q", (M, K), (M, _blocks(K)), dev)
-        st = lib().add_rmsnorm_fp8(*_row(x), *_row(residual), *_row(residual_out), norm_w.data_ptr(), float(eps), *_row(q),
-                                   *_row(scale), M, K, _stream_handle(dev, stream))
+        st = lib().add_rmsnorm_fp8(*ins, *_scaled(q, scale, "q", M, K, M, dev), M, K, _stream_of(dev, stream))
     if st != 0:
         raise MbgluError(st, "add_rmsnorm_fp8")
     return q, scale
@@ -493,16 +526,14 @@ def add_rmsnorm_fp8(x, residual, norm_w, eps, q=None, scale=None, residual_out=N
 def quantize_weight_fp8(w, q=None, scale=None, stream=None):
     """A bf16 weight [N,K] as e4m3 with a float32 scale per 128 x 128 block:
     returns (q, scale), scale [ceil(N/128), ceil(K/128)]."""
-    _check(w, "w", 2)
-    N, K = w.shape
-    dev = w.device
+    N, K, dev = _dims(w, "w", torch.bfloat16)
+    ins = _arg(w, "w", torch.bfloat16, N, K, dev)
     with _allocate_on(dev, stream):
         if q is None:
             q = _empty_e4m3(N, K, dev)
         if scale is None:
             scale = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
-        _check_scaled(q, scale, "q", (N, K), (_blocks(N), _blocks(K)), dev)
-        st = lib().quantize_weight_fp8(*_row(w), *_row(q), *_row(scale), N, K, _stream_handle(dev, stream))
+        st = lib().quantize_weight_fp8(*ins, *_scaled(q, scale, "q", N, K, _blocks(N), dev), N, K, _stream_of(dev, stream))
     if st != 0:
         raise MbgluError(st, "quantize_weight_fp8")
     return q, scale
@@ -514,17 +545,13 @@ def glu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale, out=None, out_scale=
     per row and 128 columns (add_rmsnorm_fp8's), weights [N,K] with one per
     128 x 128 block (quantize_weight_fp8's).  out_dtype bfloat16 returns out;
     float8_e4m3fn returns (q, scale), the operand of matmul_fp8."""
-    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(gate_w, torch.Tensor) or gate_w.dim() != 2:
-        raise ValueError("a must be [M,K] and gate_w [N,K] tensors")
-    if out_dtype not in (torch.bfloat16, E4M3):
+    if out_dtype is not torch.bfloat16 and out_dtype is not E4M3:
         raise TypeError(f"out_dtype must be bfloat16 or float8_e4m3fn, got {out_dtype}")
-    M, K = a.shape
-    N = gate_w.shape[0]
-    dev = a.device
-    kb, nb = _blocks(K), _blocks(N)
-    _check_scaled(a, a_scale, "a", (M, K), (M, kb), dev)
-    _check_scaled(gate_w, gate_scale, "gate_w", (N, K), (nb, kb), dev)
-    _check_scaled(up_w, up_scale, "up_w", (N, K), (nb, kb), dev)
+    M, K, dev = _dims(a, "a", E4M3)
+    N = _out_rows(gate_w, "gate_w")
+    nb = _blocks(N)
+    ins = (*_scaled(a, a_scale, "a", M, K, M, dev), *_scaled(gate_w, gate_scale, "gate_w", N, K, nb, dev),
+           *_scaled(up_w, up_scale, "up_w", N, K, nb, dev))
     quant = out_dtype is E4M3
     with _allocate_on(dev, stream):
         if quant:
@@ -532,17 +559,14 @@ def glu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale, out=None, out_scale=
                 out = _empty_e4m3(M, N, dev)
             if out_scale is None:
                 out_scale = torch.empty((M, nb), dtype=torch.float32, device=dev)
-            _check_scaled(out, out_scale, "out", (M, N), (M, nb), dev)
-            outs = (None, 0, *_row(out), *_row(out_scale))
+            outs = (None, 0, *_scaled(out, out_scale, "out", M, N, M, dev))
         else:
             if out_scale is not None:
                 raise ValueError("out_scale belongs to a float8_e4m3fn output")
             if out is None:
                 out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-            _check_operand(out, "out", torch.bfloat16, (M, N), dev)
-            outs = (*_row(out), None, 0, None, 0)
-        st = lib().glu_fp8(*_row(a), *_row(a_scale), *_row(gate_w), *_row(gate_scale), *_row(up_w), *_row(up_scale), *outs,
-                           M, N, K, _stream_handle(dev, stream))
+            outs = (*_arg(out, "out", torch.bfloat16, M, N, dev), None, 0, None, 0)
+        st = lib().glu_fp8(*ins, *outs, M, N, K, _stream_of(dev, stream))
     if st != 0:
         raise MbgluError(st, "glu_fp8")
     return (out, out_scale) if quant else out
@@ -552,21 +576,14 @@ def matmul_fp8(a, a_scale, w, w_scale, out=None, workspace=None, stream=None):
     """out[M,N] = a @ w.T (bf16) of e4m3 operands with the scales of glu_fp8.
     The workspace is a byte tensor of matmul_fp8_workspace_bytes(M, N, K)
     bytes, 256-byte aligned, allocated here when not given."""
-    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise ValueError("a must be [M,K] and w [N,K] tensors")
-    M, K = a.shape
-    N = w.shape[0]
-    dev = a.device
-    kb = _blocks(K)
-    _check_scaled(a, a_scale, "a", (M, K), (M, kb), dev)
-    _check_scaled(w, w_scale, "w", (N, K), (_blocks(N), kb), dev)
+    M, K, dev = _dims(a, "a", E4M3)
+    N = _out_rows(w, "w")
+    ins = (*_scaled(a, a_scale, "a", M, K, M, dev), *_scaled(w, w_scale, "w", N, K, _blocks(N), dev))
     with _allocate_on(dev, stream):
         if out is None:
             out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        _check_operand(out, "out", torch.bfloat16, (M, N), dev)
         wsp, wsb, keep = _workspace(workspace, lib().matmul_fp8_workspace_bytes(M, N, K), dev)
-        st = lib().matmul_fp8(*_row(a), *_row(a_scale), *_row(w), *_row(w_scale), *_row(out), M, N, K, wsp, wsb,
-                              _stream_handle(dev, stream))
+        st = lib().matmul_fp8(*ins, *_arg(out, "out", torch.bfloat16, M, N, dev), M, N, K, wsp, wsb, _stream_of(dev, stream))
     if st != 0:
         raise MbgluError(st, "matmul_fp8")
     return out

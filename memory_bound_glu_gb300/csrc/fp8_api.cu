@@ -217,8 +217,20 @@ mbglu_status add_rmsnorm_fp8(const mbglu_bf16 *x, int64_t ldx, const mbglu_bf16 
             if (overlaps(outs[i], outb[i], outs[j], outb[j])) return MBGLU_ERR_ALIAS;
     }
     mbglu::NormFp8Params p = {x, ldx, residual, ldr, residual_out, ldro, norm_w, eps, q, ldq, scale, lds, M, K};
-    Launch l(dim3(static_cast<unsigned>(M)), 256, 0, stream);
-    const mbglu_status st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::norm_fp8_any_kernel, p));
+    // in registers up to 16384 columns; a row's threads: a multiple of a warp, the
+    // fewest that leave a thread at most one, two, four or eight chunks of 8
+    // columns.  The same for the kernel of any alignment, which then sums in the
+    // same order.
+    const bool vec = K % 8 == 0 && K <= 16384 && aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) &&
+                     aligned(norm_w, 16) && aligned(q, 8) && ldx % 8 == 0 && ldr % 8 == 0 && ldro % 8 == 0 && ldq % 8 == 0;
+    const int chunks = ceil_div(K, 8), ch = chunks <= 256 ? 1 : chunks <= 512 ? 2 : chunks <= 1024 ? 4 : 8;
+    const int threads = std::min(256, ceil_div(ceil_div(chunks, ch), 32) * 32);
+    Launch l(dim3(static_cast<unsigned>(M)), threads, 0, stream);
+    const mbglu_status st = launched(!vec      ? cudaLaunchKernelEx(&l.cfg, mbglu::norm_fp8_any_kernel, p)
+                                     : ch == 1 ? cudaLaunchKernelEx(&l.cfg, mbglu::norm_fp8_kernel<1>, p)
+                                     : ch == 2 ? cudaLaunchKernelEx(&l.cfg, mbglu::norm_fp8_kernel<2>, p)
+                                     : ch == 4 ? cudaLaunchKernelEx(&l.cfg, mbglu::norm_fp8_kernel<4>, p)
+                                               : cudaLaunchKernelEx(&l.cfg, mbglu::norm_fp8_kernel<8>, p));
     if (st == MBGLU_OK) set_last_variant(kNormFp8);
     return st;
 }
