@@ -14,6 +14,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmbglu.so")
+QUICK = os.path.join(HERE, "_mbglu_torch.so")   # the binding's extension module
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("mbglu_api.cu", "gemm_api.cu", "fp8_api.cu")]
 DEPS = [os.path.join(HERE, "csrc", f) for f in sorted(os.listdir(os.path.join(HERE, "csrc")))] + \
     [os.path.join(ROOT, "include", "mbglu.h")]
@@ -35,14 +36,31 @@ def nvcc() -> str:
 
 
 def needs_build(out: str = LIB) -> bool:
-    if not os.path.exists(out):
+    if not os.path.exists(out) or not os.path.exists(QUICK):
         return True
-    t = os.path.getmtime(out)
+    t = min(os.path.getmtime(out), os.path.getmtime(QUICK))
     return any(os.path.getmtime(f) > t for f in DEPS)
 
 
+def build_quick(out: str = QUICK) -> str:
+    """The binding's extension module, against the torch that is installed."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(ROOT, "include"), os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
+           os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f for i in inc for f in ("-I", i)),
+                    "-o", out, os.path.join(HERE, "csrc", "bind_torch.cpp"), "-L", os.path.join(base, "lib"),
+                    "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"], check=True)
+    return out
+
+
 def build(out: str = LIB, verbose: bool = False, extra=()) -> str:
-    """Compiles the translation units in parallel, then links them."""
+    """Compiles the translation units in parallel, then links them; beside
+    them the binding's extension module."""
     compile_flags = [f for f in NVCC_FLAGS if f != "-shared"]
 
     def one(src, obj):
@@ -53,8 +71,8 @@ def build(out: str = LIB, verbose: bool = False, extra=()) -> str:
 
     with tempfile.TemporaryDirectory() as tmp:
         objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in SOURCES]
-        with ThreadPoolExecutor(len(SOURCES)) as ex:
-            for f in [ex.submit(one, s, o) for s, o in zip(SOURCES, objs)]:
+        with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+            for f in [ex.submit(build_quick)] + [ex.submit(one, s, o) for s, o in zip(SOURCES, objs)]:
                 f.result()
         subprocess.run([nvcc(), *NVCC_FLAGS, "-o", out, *objs], check=True)
     return out

@@ -2,19 +2,22 @@
 
 Argument marshalling only: tensors become device pointers, row strides and
 the current CUDA stream; every step of the computation runs in the library's
-kernels.  There is no fallback: if the library is missing or a call fails,
+kernels.  The wide and the e4m3 calls marshal their common case in an extension
+module (csrc/bind_torch.cpp).  There is no fallback: if the library is missing or a call fails,
 an exception is raised.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmbglu.so")
+QUICK_PATH = os.path.join(HERE, "_mbglu_torch.so")
 
 MODE_FUSED = 0
 MODE_HF = 1
@@ -36,6 +39,7 @@ EXPORTS = ("glu_gemv", "add_rmsnorm_glu", "add_rmsnorm_glu_ws", "add_rmsnorm_glu
 POLICY_SERIAL, POLICY_PDL, POLICY_PREFETCH = 0, 1, 2
 
 _lib = None
+_quick_module = None
 
 
 class MbgluError(RuntimeError):
@@ -113,6 +117,24 @@ def lib():
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         _lib = _bind(ctypes.CDLL(LIB_PATH))
     return _lib
+
+
+def _quick():
+    """The extension module that does the common case of the wide and the e4m3
+    calls without Python's checks (csrc/bind_torch.cpp); None from one of its
+    functions means that the call is not that case and comes here."""
+    global _quick_module
+    if _quick_module is None:
+        l = lib()
+        if not os.path.exists(QUICK_PATH):
+            raise RuntimeError(f"{QUICK_PATH} is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        m = importlib.import_module("._mbglu_torch", __package__)
+        m.bind(*(ctypes.cast(getattr(l, n), ctypes.c_void_p).value
+                 for n in ("glu_gemm", "glu_gemm_backward", "glu_gemm_backward_workspace_bytes", "add_rmsnorm_fp8", "glu_fp8",
+                           "matmul_fp8", "matmul_fp8_workspace_bytes")))
+        _quick_module = m
+    return _quick_module
 
 
 def _on(dev):
@@ -428,6 +450,12 @@ def glu_gemm(h, gate_w, up_w, out=None, mode="fused", gu=None, stream=None):
     prompt or a training batch.  Arguments as glu_gemv; gu, a float32 [M, 2N]
     tensor, receives g and u for glu_gemm_backward.  Up to MAX_M rows without
     gu the call is glu_gemv."""
+    if stream is None:
+        r = (_quick_module or _quick()).glu_gemm(h, gate_w, up_w, out, _MODES[mode], gu)
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "glu_gemm")
+            return r
     bf16 = torch.bfloat16
     squeeze = isinstance(h, torch.Tensor) and h.dim() == 1
     h2 = h.unsqueeze(0) if squeeze else h
@@ -453,6 +481,12 @@ def glu_gemm_backward(h, gate_w, up_w, dout, gu=None, grad_h=None, grad_gate=Non
     rows.  gu: what glu_gemm wrote there (computed again when not given).  The
     workspace is a byte tensor of glu_gemm_backward_workspace_bytes(M, N, K)
     bytes, 256-byte aligned, allocated here when not given."""
+    if stream is None and grad_h is None and grad_gate is None and grad_up is None and workspace is None:
+        r = (_quick_module or _quick()).glu_gemm_backward(h, gate_w, up_w, dout, gu, bool(want_h), bool(want_w))
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "glu_gemm_backward")
+            return r
     bf16 = torch.bfloat16
     M, K, dev = _dims(h, "h", bf16)
     N = _out_rows(gate_w, "gate_w")
@@ -505,6 +539,12 @@ def add_rmsnorm_fp8(x, residual, norm_w, eps, q=None, scale=None, residual_out=N
     """residual_out <- bf16(x + residual) (in place when not given); v = its
     zero-centred RMSNorm; returns (q, scale): v as e4m3 [M,K] with a float32
     scale per row and 128 columns [M, ceil(K/128)]."""
+    if stream is None:
+        r = (_quick_module or _quick()).add_rmsnorm_fp8(x, residual, norm_w, eps, q, scale, residual_out)
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "add_rmsnorm_fp8")
+            return r
     bf16 = torch.bfloat16
     M, K, dev = _dims(x, "x", bf16)
     if norm_w is None or norm_w.dim() != 1 or norm_w.shape[0] != K or norm_w.dtype is not bf16 or norm_w.device != dev \
@@ -547,6 +587,12 @@ def glu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale, out=None, out_scale=
     float8_e4m3fn returns (q, scale), the operand of matmul_fp8."""
     if out_dtype is not torch.bfloat16 and out_dtype is not E4M3:
         raise TypeError(f"out_dtype must be bfloat16 or float8_e4m3fn, got {out_dtype}")
+    if stream is None:
+        r = (_quick_module or _quick()).glu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale, out, out_scale, out_dtype is E4M3)
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "glu_fp8")
+            return r
     M, K, dev = _dims(a, "a", E4M3)
     N = _out_rows(gate_w, "gate_w")
     nb = _blocks(N)
@@ -576,6 +622,12 @@ def matmul_fp8(a, a_scale, w, w_scale, out=None, workspace=None, stream=None):
     """out[M,N] = a @ w.T (bf16) of e4m3 operands with the scales of glu_fp8.
     The workspace is a byte tensor of matmul_fp8_workspace_bytes(M, N, K)
     bytes, 256-byte aligned, allocated here when not given."""
+    if stream is None and workspace is None:
+        r = (_quick_module or _quick()).matmul_fp8(a, a_scale, w, w_scale, out)
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "matmul_fp8")
+            return r
     M, K, dev = _dims(a, "a", E4M3)
     N = _out_rows(w, "w")
     ins = (*_scaled(a, a_scale, "a", M, K, M, dev), *_scaled(w, w_scale, "w", N, K, _blocks(N), dev))

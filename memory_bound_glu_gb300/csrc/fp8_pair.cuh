@@ -65,17 +65,30 @@ struct ScaleStage {
 };
 constexpr uint32_t kFp8Smem = kPairSmem + 2 * sizeof(ScaleStage);
 
+// Two fp32 in one 64-bit register, as the packed FMA takes them.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
 // acc += f (lo, hi), one packed FMA.  Volatile: kept in order with the loads
 // around it, so that no more than two steps' columns are held at a time.
-__device__ __forceinline__ void scale_add(float2 &acc, uint32_t lo, uint32_t hi, float f)
+__device__ __forceinline__ void scale_add(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t f)
 {
     asm volatile(
-        "{\n\t.reg .b64 a, b, c;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
-        "fma.rn.f32x2 c, a, b, c;\n\t"
-        "mov.b64 {%0, %1}, c;\n\t}"
-        : "+f"(acc.x), "+f"(acc.y)
-        : "r"(lo), "r"(hi), "f"(f));
+        "{\n\t.reg .b64 a;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "fma.rn.f32x2 %0, a, %3, %0;\n\t}"
+        : "+l"(acc)
+        : "r"(lo), "r"(hi), "l"(f));
 }
 
 template <int EPI>
@@ -143,55 +156,80 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
         regs_take<208>();
         const int q = warp & 3, half = (warp - kPairEpilogue) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        // this thread's accumulator columns: [c0, c0 + 64) and [c1, c1 + 64)
-        const int c0 = kDual ? half * 64 : half * 128, c1 = kDual ? 128 + half * 64 : half * 128 + 64;
+        // this thread's accumulator columns: [col0, col0 + 64) and [col1, col1 + 64)
+        const int col0 = kDual ? half * 64 : half * 128, col1 = kDual ? 128 + half * 64 : half * 128 + 64;
         uint32_t v = 0, tiles = 0, g = 0;
         for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1), ++tiles) {
-            const PairTileAt x = pair_tile(p.plan, t);
+            int c = 0, c1 = 0;
+            {
+                const PairTileAt x = pair_tile(p.plan, t);
+                c = x.c0;
+                c1 = x.c1;
+            }
+            const int first = c;
+            uint64_t sums[64];   // pairs of columns
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sums[i] = 0;
+            // A step is 32 columns: its FMAs run while the next step's columns
+            // arrive, over the blocks' borders too, so that tensor memory is read
+            // without a pause (it gives a warp's 32 x 32 values in about 64 cycles:
+            // 512 per block for the two warps of a scheduler, as long as the MMAs take).
+            uint32_t r[2][32];
+            if (ok) ok = pair_wait(&s.acc_full[v & 1], (v >> 1) & 1, kWaitLimitNs);
+            __syncwarp();
+            tc_fence_after();
+            tmem_ld32(lanes + (v & 1) * kPairTile + static_cast<uint32_t>(col0), r[0]);
+            tmem_wait_ld(r[0]);
+#pragma unroll 1
+            for (; c < c1; ++c, ++v) {
+                const uint32_t buf = v & 1;
+                const int in = (c - first) & (kScaleGroup - 1);
+                if (in == 0 && ok) ok = pair_wait(&scale_full[g & 1], (g >> 1) & 1, kWaitLimitNs);
+                const ScaleStage &sc = scales[g & 1];
+                const float sa = sc.a[in][q * 32 + lane];
+                const float s0 = sa * sc.w[kDual ? 0 : half][in], s1 = kDual ? sa * sc.w[1][in] : s0;
+                const uint64_t f0 = pack_f32x2(s0, s0), f1 = kDual ? pack_f32x2(s1, s1) : f0;
+                __syncwarp();
+                if (in == kScaleGroup - 1 || c == c1 - 1) {   // the group is read
+                    if (lane == 0) mbar_arrive(&scale_empty[g & 1]);
+                    ++g;
+                }
+                const uint32_t from = lanes + buf * kPairTile;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    tmem_ld32(from + static_cast<uint32_t>((j < 1 ? col0 : col1) + (~j & 1) * 32), r[(j + 1) & 1]);
+                    const uint64_t f = j < 2 ? f0 : f1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) scale_add(sums[16 * j + i], r[j & 1][2 * i], r[j & 1][2 * i + 1], f);
+                    tmem_wait_ld(r[(j + 1) & 1]);
+                }
+                tc_fence_before();   // the buffer is read
+                __syncwarp();
+                if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
+                if (c + 1 < c1) {
+                    if (ok) ok = pair_wait(&s.acc_full[buf ^ 1], ((v + 1) >> 1) & 1, kWaitLimitNs);
+                    __syncwarp();
+                    tc_fence_after();
+                    tmem_ld32(lanes + (buf ^ 1) * kPairTile + static_cast<uint32_t>(col0), r[0]);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) scale_add(sums[48 + i], r[1][2 * i], r[1][2 * i + 1], f1);
+                if (c + 1 < c1) tmem_wait_ld(r[0]);
+            }
+            // where the tile lies, worked out again: the loop above needs every register
+            ok = __all_sync(0xffffffffu, ok);
+            int again = t;
+            asm volatile("" : "+r"(again));
+            const PairTileAt x = pair_tile(p.plan, again);
             const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32 + lane;
             const bool row = m < p.plan.rows;
             float2 acc[64];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-            for (int c = x.c0; c < x.c1; ++c, ++v) {
-                const int buf = static_cast<int>(v & 1), in = (c - x.c0) & (kScaleGroup - 1);
-                if (in == 0 && ok) ok = __all_sync(0xffffffffu, pair_wait(&scale_full[g & 1], (g >> 1) & 1, kWaitLimitNs));
-                const ScaleStage &sc = scales[g & 1];
-                const float sa = sc.a[in][q * 32 + lane];
-                const float f0 = sa * sc.w[kDual ? 0 : half][in], f1 = kDual ? sa * sc.w[1][in] : f0;
-                if (in == kScaleGroup - 1 || c == x.c1 - 1) {   // the group is read
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&scale_empty[g & 1]);
-                    ++g;
-                }
-                if (ok)
-                    ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], (v >> 1) & 1,
-                                                                           kWaitLimitNs));
-                tc_fence_after();
-                const uint32_t from = lanes + static_cast<uint32_t>(buf) * kPairTile;
-                // a step's FMAs run while the next step's columns arrive
-                uint32_t r[2][32];
-                tmem_ld32(from + static_cast<uint32_t>(c0), r[0]);
-                tmem_wait_ld(r[0]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j < 3) tmem_ld32(from + static_cast<uint32_t>((j < 1 ? c0 : c1) + (~j & 1) * 32), r[(j + 1) & 1]);
-                    const float f = j < 2 ? f0 : f1;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) scale_add(acc[16 * j + i], r[j & 1][2 * i], r[j & 1][2 * i + 1], f);
-                    if (j < 3) tmem_wait_ld(r[(j + 1) & 1]);
-                    if (j == 2) {   // the buffer is read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
-                    }
-                }
-            }
+            for (int i = 0; i < 64; ++i) acc[i] = unpack_f32x2(sums[i]);
             if constexpr (EPI == kFp8Out) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int n = x.ni * kPairTile + c0 + 32 * j, valid = p.plan.cols - n;
+                    const int n = x.ni * kPairTile + col0 + 32 * j, valid = p.plan.cols - n;
                     if (!ok || !row || valid <= 0) continue;
                     if (x.slot >= 0) {
                         float f[32];
@@ -200,7 +238,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
                             f[2 * i] = acc[16 * j + i].x;
                             f[2 * i + 1] = acc[16 * j + i].y;
                         }
-                        store_f32_32(p.part + x.slot * kPairSlot + (rank * 128 + q * 32 + lane) * kPairTile + c0 + 32 * j, f, 32, 2);
+                        store_f32_32(p.part + x.slot * kPairSlot + (rank * 128 + q * 32 + lane) * kPairTile + col0 + 32 * j, f, 32, 2);
                     } else {
                         uint32_t w[16];
 #pragma unroll
