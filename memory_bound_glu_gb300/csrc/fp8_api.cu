@@ -8,6 +8,7 @@
 #include "dense_launch.h"
 #include "fp8_pair.cuh"
 #include "fp8_rows.cuh"
+#include "fp8_tall.cuh"
 #include "norm_fp8.cuh"
 #include "pair_plan.h"
 
@@ -70,11 +71,14 @@ cudaError_t allow_rows()
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
 }
 
+cudaError_t setup_tall();
+
 cudaError_t setup_fp8()
 {
     cudaError_t e = allow_pair<mbglu::kFp8Out>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8Glu>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8GluQuant>();
+    if (e == cudaSuccess) e = setup_tall();
     if (e == cudaSuccess) e = allow_rows<1, 0, 8, 4, 2>();
     if (e == cudaSuccess) e = allow_rows<1, 1, 8, 2, 2>();
     if (e == cudaSuccess) e = allow_rows<2, 1, 8, 2, 1>();
@@ -179,6 +183,106 @@ void rows_weight(mbglu::Fp8RowsParams &p, int d, const Scaled &w)
     p.ws[d] = w.s;
     p.ldws[d] = w.lds;
 }
+
+// ---- some dozens of rows: fp8_tall_kernel -------------------------------------------
+
+// Clusters of ks blocks, each with an SM of its own, that the part holds at once.
+constexpr int kClusters[mbglu::kTallMaxSplit + 1] = {0, 152, 76, 46, 36, 28, 23};
+
+struct TallPlan {
+    int tn, ks;
+};
+
+// Tokens per block: the least power of two from `least` to `most` that holds
+// all, else `most`.  Ranges of the inner dimension: what makes rounds x (stages of a range +
+// what a round costs beside them, about 8 stages' time) least.
+TallPlan tall_plan(int M, int N, int K, int least, int most)
+{
+    TallPlan t = {least, 1};
+    while (t.tn < M && t.tn < most) t.tn *= 2;
+    const int64_t units = static_cast<int64_t>(ceil_div(N, mbglu::kTallRows)) * ceil_div(M, t.tn);
+    const int chunks = ceil_div(K, kBlk);
+    int64_t best = 0;
+    for (int ks = 1; ks <= std::min(mbglu::kTallMaxSplit, chunks); ++ks) {
+        const int64_t cost = (units + kClusters[ks] - 1) / kClusters[ks] * (ceil_div(chunks, ks) + 8);
+        if (ks == 1 || cost < best) {
+            best = cost;
+            t.ks = ks;
+        }
+    }
+    return t;
+}
+
+template <int TN, int OUT>
+cudaError_t allow_tall()
+{
+    return cudaFuncSetAttribute(mbglu::fp8_tall_kernel<TN, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(mbglu::TallShape<TN, OUT != 0>::kSmem));
+}
+
+cudaError_t setup_tall()
+{
+    cudaError_t e = cudaSuccess;
+#define MBGLU_ALLOW(TN, OUT) \
+    if (e == cudaSuccess) e = allow_tall<TN, OUT>();
+    MBGLU_ALLOW(16, 0) MBGLU_ALLOW(32, 0) MBGLU_ALLOW(64, 0) MBGLU_ALLOW(128, 0) MBGLU_ALLOW(256, 0)
+    MBGLU_ALLOW(32, 1) MBGLU_ALLOW(64, 1) MBGLU_ALLOW(128, 1)
+    MBGLU_ALLOW(32, 2) MBGLU_ALLOW(64, 2) MBGLU_ALLOW(128, 2)
+#undef MBGLU_ALLOW
+    return e;
+}
+
+template <int TN, int OUT>
+mbglu_status launch_tall(const TallPlan &t, const mbglu::TallParams &p, const mbglu::TallMaps &maps, cudaStream_t stream)
+{
+    const int64_t blocks = static_cast<int64_t>(p.wtiles) * ceil_div(p.M, TN) * t.ks;
+    Launch l(dim3(static_cast<unsigned>(blocks)), 384, mbglu::TallShape<TN, OUT != 0>::kSmem, stream, t.ks);
+    const mbglu_status st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::fp8_tall_kernel<TN, OUT>, p, maps));
+    if (st == MBGLU_OK) set_last_variant(kFp8Tall);
+    return st;
+}
+
+// False where a tensor map is refused (nothing is launched).
+template <int OUT>
+bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams &p, int M, int N, int K, cudaStream_t stream,
+          mbglu_status *st)
+{
+    const TallPlan t = tall_plan(M, N, K, OUT == 0 ? 16 : 32, OUT == 0 ? 256 : 128);
+    mbglu::TallMaps maps;
+    if (!k_major(&maps.w[0], w0, K) || (w1 && !k_major(&maps.w[1], *w1, K)) || !copyable(a.p, a.ld, 1) ||
+        !encode_tile_map(&maps.x, a.p, a.ld, M, K, 128, t.tn, 1))
+        return false;
+    int sms = 0;
+    if ((*st = sm_count(&sms)) != MBGLU_OK) return true;
+    p.M = M;
+    p.N = N;
+    p.nchunk = ceil_div(K, kBlk);
+    p.ks = t.ks;
+    p.wtiles = ceil_div(N, mbglu::kTallRows);
+    p.prefetch = launch_policy() == MBGLU_POLICY_PREFETCH;
+    p.as = a.s;
+    p.ldas = a.lds;
+    p.ws[0] = w0.s;
+    p.ldws[0] = w0.lds;
+    if (w1) {
+        p.ws[1] = w1->s;
+        p.ldws[1] = w1->lds;
+    }
+    if constexpr (OUT == 0) {
+        *st = t.tn == 16    ? launch_tall<16, 0>(t, p, maps, stream)
+              : t.tn == 32  ? launch_tall<32, 0>(t, p, maps, stream)
+              : t.tn == 64  ? launch_tall<64, 0>(t, p, maps, stream)
+              : t.tn == 128 ? launch_tall<128, 0>(t, p, maps, stream)
+                            : launch_tall<256, 0>(t, p, maps, stream);
+    } else {
+        *st = t.tn == 32   ? launch_tall<32, OUT>(t, p, maps, stream)
+              : t.tn == 64 ? launch_tall<64, OUT>(t, p, maps, stream)
+                           : launch_tall<128, OUT>(t, p, maps, stream);
+    }
+    return true;
+}
+
+constexpr int kTallMatmul = 512, kTallGlu = 256;   // rows up to which the tall kernel is taken
 
 mbglu::PairPlan matmul_plan(int M, int N, int K)
 {
@@ -291,6 +395,13 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
         q.ldo = ldo;
         return matmul_rows(q, stream);
     }
+    if (K > 0 && M <= kTallMatmul) {
+        mbglu::TallParams q = {};
+        q.out = out;
+        q.ldo = ldo;
+        mbglu_status st;
+        if (tall<0>(A, W, nullptr, q, M, N, K, stream, &st)) return st;
+    }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], W, K)) {
         mbglu::Fp8PairParams q = {};
@@ -356,6 +467,17 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
         p.qs = q_scale;
         p.ldqs = ldqs;
         return q ? glu_rows<2>(p, stream) : glu_rows<1>(p, stream);
+    }
+    if (K > 0 && M <= kTallGlu) {
+        mbglu::TallParams p = {};
+        p.out = out;
+        p.ldo = ldo;
+        p.q = q;
+        p.ldq = ldq;
+        p.qs = q_scale;
+        p.ldqs = ldqs;
+        mbglu_status st;
+        if (q ? tall<2>(A, G, &U, p, M, N, K, stream, &st) : tall<1>(A, G, &U, p, M, N, K, stream, &st)) return st;
     }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], G, K) && k_major(&maps.b[1], U, K)) {

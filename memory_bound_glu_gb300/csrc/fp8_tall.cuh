@@ -1,0 +1,423 @@
+// fp8_tall.cuh -- the e4m3 products of some dozens of rows (a decode batch, a
+// short chunk): too many for mma.sync fragments per weight byte, too few to fill
+// the 256-row side of a CTA pair's tile.  The weights take the MMA's 128-row
+// side and the tokens its N, so that both the products and the reading of the
+// accumulators shrink with the batch and what is left is the weights' bytes.
+//
+// A block holds 128 weight rows -- one scale block, and one group of an e4m3
+// output -- of one weight or of gate and up, TN tokens, and one of `ks` ranges
+// of the inner dimension; the ranges of a tile are the blocks of a cluster.  Per
+// 128 of the inner dimension (a scale block, a stage): one or two sums of
+// 128 x TN in tensor memory, read by eight epilogue warps, scaled by the token's
+// and the weight block's scale and added to fp32 totals in registers, while the
+// next stage's sums are formed.  At the end each block gets the totals of its
+// share of the tokens from all blocks of the cluster (distributed shared memory,
+// added in rank order) and writes them.
+//
+// Roles (384 threads): warp 0 copies, warp 1 issues the MMAs and owns the tensor
+// memory, warp 2 stages the scales, warps 4-11 are the epilogue: warp w has
+// weight rows 32 (w % 4).. and half of the tokens.
+#pragma once
+
+#include "fp8_pair.cuh"
+
+namespace mbglu {
+
+constexpr int kTallRows = 128;
+constexpr uint32_t kTallW = 16384;             // one weight's bytes per stage
+constexpr int kTallMaxStages = 8;
+constexpr uint32_t kTallHeader = 1024;
+constexpr int kTallMaxSplit = 6;
+
+template <int TN, bool DUAL>
+struct TallShape {
+    static constexpr int kMats = DUAL ? 2 : 1;
+    static constexpr uint32_t kStage = kMats * kTallW + TN * 128u;
+    // scales of 8 blocks: tokens', then the weights'; two of them
+    static constexpr uint32_t kScales = (TN * kScaleGroup + 2 * kScaleGroup) * 4u;
+    static constexpr uint32_t kRoom = 225u * 1024 - 1024 - kTallHeader - 2 * kScales;
+    static constexpr int kStages = kRoom / kStage < kTallMaxStages ? static_cast<int>(kRoom / kStage) : kTallMaxStages;
+    static constexpr uint32_t kSmem = 1024 + kTallHeader + 2 * kScales + kStages * kStage;
+    // the totals that a block gets: every rank's, of its share of the tokens
+    static constexpr uint32_t totals(int ks) { return static_cast<uint32_t>(ks * kMats * ((TN + ks - 1) / ks)) * kTallRows * 4u; }
+    static_assert(totals(1) <= kStages * kStage && totals(3) <= kStages * kStage && totals(5) <= kStages * kStage &&
+                      totals(6) <= kStages * kStage && totals(4) <= kStages * kStage,
+                  "the exchange fits the stages");
+    static_assert(kStages >= 3 && kSmem <= 227u * 1024, "shared memory");
+};
+
+struct TallMaps {
+    TensorMap w[2], x;
+};
+
+struct TallParams {
+    int M, N, nchunk, ks, wtiles;
+    int prefetch;
+    const float *as;
+    int64_t ldas;
+    const float *ws[2];
+    int64_t ldws[2];
+    uint16_t *out;
+    int64_t ldo;
+    uint8_t *q;
+    int64_t ldq;
+    float *qs;
+    int64_t ldqs;
+};
+
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+// 8 and 16 columns of this thread's lane; as tmem_ld32 and its wait
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// OUT: 0 bf16 product (one weight), 1 bf16 gated, 2 e4m3 gated.
+template <int TN, int OUT>
+__global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, const __grid_constant__ TallMaps maps)
+{
+    constexpr bool kDual = OUT != 0;
+    using Shape = TallShape<TN, kDual>;
+    constexpr int kMats = Shape::kMats, kStages = Shape::kStages;
+    constexpr int TH = TN / 2;                     // tokens per thread
+    constexpr int SW = TH < 32 ? TH : 32;          // columns per step
+    constexpr int kSteps = TH / SW;                // steps per matrix
+    extern __shared__ unsigned char tall_raw[];
+    unsigned char *base = tall_raw + ((1024u - (smem_addr(tall_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(base);
+    uint64_t *empty = full + kTallMaxStages, *acc_full = empty + kTallMaxStages, *acc_empty = acc_full + 2;
+    uint64_t *scale_full = acc_empty + 2, *scale_empty = scale_full + 2;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(scale_empty + 2);
+    float *peaks = reinterpret_cast<float *>(base + 512);   // [8 warps][..]: see the end
+    unsigned char *stages = base + kTallHeader;
+    float *scales = reinterpret_cast<float *>(stages + kStages * Shape::kStage);
+    constexpr int kScaleFloats = Shape::kScales / 4;
+    float *totals = reinterpret_cast<float *>(stages);      // after the products: [rank][mat][token][128 rows]
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int ks = p.ks;
+    const int rank = ks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int unit = static_cast<int>(blockIdx.x) / ks;
+    const int wt = unit % p.wtiles, m0 = unit / p.wtiles * TN;
+    const int c0 = p.nchunk * rank / ks, c1 = p.nchunk * (rank + 1) / ks;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 8);
+            mbar_init(&scale_full[i], 1);
+            mbar_init(&scale_empty[i], 8);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+    bool ok = true;
+    // the copies of the weights may start before the preceding kernel has ended;
+    // everything else waits for it
+    if (warp != 0 || !p.prefetch) grid_dependency_wait();
+    if (warp != 0) grid_launch_dependents();
+
+    if (warp < 4) {
+        regs_release<88>();
+        if (warp == 0) {
+            auto load_w = [&](int st, int c) {
+                unsigned char *d = stages + st * Shape::kStage;
+                mbar_arrive_expect_tx(&full[st], Shape::kStage);
+#pragma unroll
+                for (int i = 0; i < kMats; ++i)
+                    tma_load_2d(d + i * kTallW, &maps.w[i], c * 128, wt * kTallRows, &full[st], l2_policy_evict_first());
+            };
+            auto load_x = [&](int st, int c) {
+                tma_load_2d(stages + st * Shape::kStage + kMats * kTallW, &maps.x, c * 128, m0, &full[st], l2_policy_evict_last());
+            };
+            const int early = p.prefetch ? min(kStages, c1 - c0) : 0;
+            if (early > 0) {
+                if (elect_one())
+                    for (int i = 0; i < early; ++i) load_w(i, c0 + i);
+                __syncwarp();
+                grid_dependency_wait();
+                if (elect_one())
+                    for (int i = 0; i < early; ++i) load_x(i, c0 + i);
+                __syncwarp();
+            } else if (p.prefetch) {
+                grid_dependency_wait();
+            }
+            grid_launch_dependents();
+            int st = early == kStages ? 0 : early;
+            uint32_t phase = early == kStages ? 0 : 1;
+            int filled = early;
+            for (int c = c0 + early; c < c1; ++c) {
+                if (!pair_wait(&empty[st], phase, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                if (elect_one()) {
+                    load_w(st, c);
+                    load_x(st, c);
+                }
+                __syncwarp();
+                if (filled < kStages) ++filled;
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+            // every copy has landed and been read before the stages take the totals
+            for (int i = 0; i < filled; ++i) {
+                int at = st - (filled - i);
+                const uint32_t ph = at < 0 ? phase : phase ^ 1;   // filled in the round before this one, or in this
+                if (at < 0) at += kStages;
+                if (!pair_wait(&empty[at], ph, kWaitLimitNs)) ok = false;
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(TN >> 3) << 17) | (static_cast<uint32_t>(kTallRows >> 4) << 24);
+            const uint64_t d0 = smem_desc_sw128(stages);
+            int st = 0;
+            uint32_t phase = 0, buf = 0, acc_phase = 1;
+            for (int c = c0; c < c1 && ok; ++c) {
+                ok = pair_wait(&acc_empty[buf], acc_phase, kWaitLimitNs) && pair_wait(&full[st], phase, kWaitLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t w = d0 + static_cast<uint32_t>(st) * (Shape::kStage >> 4);
+                const uint64_t x = w + kMats * (kTallW >> 4);
+                const uint32_t d = tmem + buf * 256;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kMats; ++i)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_e4m3(d + i * TN, w + i * (kTallW >> 4) + 2 * kk, x + 2 * kk, idesc, kk > 0);
+                    tc_commit(&empty[st]);
+                    tc_commit(&acc_full[buf]);
+                }
+                __syncwarp();
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+                buf ^= 1;
+                if (buf == 0) acc_phase ^= 1;
+            }
+        } else if (warp == 2) {
+            uint32_t g = 0;
+            for (int c = c0; c < c1; c += kScaleGroup, ++g) {
+                float *sc = scales + (g & 1) * kScaleFloats;
+                if (g >= 2 && ok) ok = __all_sync(0xffffffffu, pair_wait(&scale_empty[g & 1], ((g >> 1) - 1) & 1, kWaitLimitNs));
+                const int b = c + (lane & 7);
+                float w = 0.0f;
+                if (lane < 8 * kMats && b < c1)
+                    w = __ldg((kDual && lane >= 8 ? p.ws[1] + wt * p.ldws[1] : p.ws[0] + wt * p.ldws[0]) + b);
+#pragma unroll 8
+                for (int i = 0; i < TN / 4; ++i) {   // 4 tokens x 8 blocks per load
+                    const int tok = 4 * i + (lane >> 3), m = m0 + tok;
+                    sc[(lane & 7) * TN + tok] = m < p.M && b < c1 ? __ldg(p.as + m * p.ldas + b) : 0.0f;
+                }
+                if (lane < 8 * kMats) sc[kScaleGroup * TN + lane] = w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&scale_full[g & 1]);
+            }
+        }
+        __syncwarp();
+        if (ks > 1) cluster_sync();   // every block's products are done: the stages are free
+        else __syncthreads();
+        if (ks > 1) cluster_sync();   // the totals have come
+        else __syncthreads();
+    } else {
+        regs_take<208>();
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * TH);
+        const int row = q * 32 + lane;
+        uint64_t sums[kMats][TH / 2];
+#pragma unroll
+        for (int d = 0; d < kMats; ++d)
+#pragma unroll
+            for (int i = 0; i < TH / 2; ++i) sums[d][i] = 0;
+        uint32_t v = 0, g = 0;
+        if (c0 < c1) {
+            uint32_t r[2][SW];
+            if (ok) ok = pair_wait(&acc_full[0], 0, kWaitLimitNs);
+            __syncwarp();
+            tc_fence_after();
+            tmem_load(lanes, r[0]);
+            tmem_wait_ld(r[0]);
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c, ++v) {
+                const uint32_t buf = v & 1;
+                const int in = (c - c0) & (kScaleGroup - 1);
+                if (in == 0 && ok) ok = pair_wait(&scale_full[g & 1], (g >> 1) & 1, kWaitLimitNs);
+                __syncwarp();
+                const float *sc = scales + (g & 1) * kScaleFloats;
+                const float *sx = sc + in * TN + half * TH;
+                uint64_t sw[kMats];
+#pragma unroll
+                for (int d = 0; d < kMats; ++d) {
+                    const float w = sc[kScaleGroup * TN + d * kScaleGroup + in];
+                    sw[d] = pack_f32x2(w, w);
+                }
+                const uint32_t from = lanes + buf * 256;
+#pragma unroll
+                for (int s = 0; s < kMats * kSteps; ++s) {
+                    const int next = s + 1;
+                    if (next < kMats * kSteps) {
+                        tmem_load(from + static_cast<uint32_t>(next / kSteps * TN + next % kSteps * SW), r[next & 1]);
+                    } else {
+                        tc_fence_before();   // the buffer is read
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                        if (c + 1 < c1) {
+                            if (ok) ok = pair_wait(&acc_full[buf ^ 1], ((v + 1) >> 1) & 1, kWaitLimitNs);
+                            __syncwarp();
+                            tc_fence_after();
+                            tmem_load(lanes + (buf ^ 1) * 256, r[next & 1]);
+                        }
+                    }
+                    const int d = s / kSteps, t0 = s % kSteps * SW;
+#pragma unroll
+                    for (int i = 0; i < SW / 4; ++i) {
+                        const float4 x = *reinterpret_cast<const float4 *>(sx + t0 + 4 * i);
+                        scale_add(sums[d][t0 / 2 + 2 * i], r[s & 1][4 * i], r[s & 1][4 * i + 1], mul_f32x2(sw[d], pack_f32x2(x.x, x.y)));
+                        scale_add(sums[d][t0 / 2 + 2 * i + 1], r[s & 1][4 * i + 2], r[s & 1][4 * i + 3],
+                                   mul_f32x2(sw[d], pack_f32x2(x.z, x.w)));
+                    }
+                    if (next < kMats * kSteps || c + 1 < c1) tmem_wait_ld(r[next & 1]);
+                }
+                if (kMats * kSteps % 2 == 1) {   // an odd number of steps: the next block's first columns are in r[1]
+#pragma unroll
+                    for (int i = 0; i < SW; ++i) r[0][i] = r[1][i];
+                }
+                if (in == kScaleGroup - 1 || c == c1 - 1) {   // the scales are read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&scale_empty[g & 1]);
+                    ++g;
+                }
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        // each token's totals to the block that writes it
+        const int share = (TN + ks - 1) / ks;
+        if (ks > 1) cluster_sync();
+        else __syncthreads();
+        fence_proxy_async_smem();
+        {
+            int owner = half * TH / share, tok = half * TH - owner * share;
+            uint32_t dst = map_to_rank(totals, static_cast<uint32_t>(owner));
+#pragma unroll
+            for (int i = 0; i < TH; ++i) {
+                const int at = (rank * kMats * share + tok) * kTallRows + row;
+#pragma unroll
+                for (int d = 0; d < kMats; ++d) {
+                    const float2 x = unpack_f32x2(sums[d][i / 2]);
+                    st_cluster_f32(dst + static_cast<uint32_t>(at + d * share * kTallRows) * 4u, i & 1 ? x.y : x.x);
+                }
+                if (++tok == share) {
+                    tok = 0;
+                    ++owner;
+                    if (i + 1 < TH) dst = map_to_rank(totals, static_cast<uint32_t>(min(owner, ks - 1)));
+                }
+            }
+        }
+        if (ks > 1) cluster_sync();
+        else __syncthreads();
+        // this block's tokens: warps 4-7 and 8-11 take alternate ones, a thread one weight row
+        const int n = wt * kTallRows + row;
+        const int first = rank * share, count = min(min(share, TN - first), p.M - m0 - first);
+        for (int t = half; t < count + (count & 1); t += 2) {   // both halves run the same rounds: there is a barrier
+            const bool live = t < count;
+            float x = 0.0f, y = 0.0f;
+            if (live) {
+                for (int s = 0; s < ks; ++s) {
+                    x += totals[(s * kMats * share + t) * kTallRows + row];
+                    if (kDual) y += totals[((s * kMats + 1) * share + t) * kTallRows + row];
+                }
+            }
+            const int64_t m = m0 + first + t;
+            const float val = kDual ? silu_short(x) * y : x;
+            if constexpr (OUT == 2) {
+                float amax = live && n < p.N ? fabsf(val) : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                // the four warps of a half hold the group; two sets of places, used in turn
+                float *pk = peaks + ((t >> 1) & 1) * 8 + half * 4;
+                if (lane == 0) pk[q] = amax;
+                bar_sync_named(1, 256);
+                amax = max_nan(max_nan(pk[0], pk[1]), max_nan(pk[2], pk[3]));
+                const float s = group_scale(amax);
+                if (live && ok) {
+                    if (row == 0) p.qs[m * p.ldqs + wt] = s;
+                    if (n < p.N) p.q[m * p.ldq + n] = static_cast<uint8_t>(pack_e4m3x2(val * (1.0f / s), 0.0f));
+                }
+            } else {
+                if (live && ok && n < p.N) p.out[m * p.ldo + n] = f32_to_bf16(val);
+            }
+        }
+    }
+    if (!ok) atomicExch(&g_dense_error, kErrTimeout);
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace mbglu
