@@ -514,8 +514,7 @@ int mbglu_last_cuda_error(void);
  * fragments in registers, batch 1..16); glu_gemm: 11 the CTA-pair tcgen05
  * kernel, 12 the kernel for any alignment; 13 glu_gemm_backward, 14
  * add_rmsnorm_fp8; e4m3 products: 15 the CTA-pair tcgen05 kernel, 16 the kernel
- * for few rows, 17 the kernel for any alignment; 18 quantize_weight_fp8;
- * 19 an e4m3 product of some dozens of rows. */
+ * for few rows, 17 the kernel for any alignment; 18 quantize_weight_fp8. */
 int mbglu_last_variant(void);
 
 /* Which kernels the calling thread's last glu_backward took for the

@@ -719,7 +719,7 @@ def last_variant() -> int:
     glu_backward, 9 tcgen05, 10 the K-slice tensor-core kernel (batch 1..16),
     11 glu_gemm on the CTA-pair tcgen05 kernel, 12 glu_gemm at any alignment,
     13 glu_gemm_backward, 14 add_rmsnorm_fp8, 15..17 an e4m3 product (CTA pairs,
-    few rows, any alignment; 19 dozens of rows), 18 quantize_weight_fp8."""
+    few rows, any alignment), 18 quantize_weight_fp8."""
     return lib().mbglu_last_variant()
 
 

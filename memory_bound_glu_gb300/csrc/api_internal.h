@@ -17,10 +17,9 @@ enum DenseVariant {
     kGemmBackward = 13,  // glu_gemm_backward
     kNormFp8 = 14,       // add_rmsnorm_fp8
     kFp8Pair = 15,       // an e4m3 product on the CTA-pair tcgen05 kernel
-    kFp8Rows = 16,       // an e4m3 product of few rows
+    kFp8Tall = 16,       // an e4m3 product of few rows
     kFp8Generic = 17,    // an e4m3 product on the kernel for any alignment
-    kQuantWeight = 18,   // quantize_weight_fp8
-    kFp8Tall = 19        // an e4m3 product of some dozens of rows
+    kQuantWeight = 18    // quantize_weight_fp8
 };
 
 mbglu_status cuda_fail(cudaError_t e);   // records e for mbglu_last_cuda_error

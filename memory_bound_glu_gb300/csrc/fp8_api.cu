@@ -7,7 +7,6 @@
 #include "dense_generic.cuh"
 #include "dense_launch.h"
 #include "fp8_pair.cuh"
-#include "fp8_rows.cuh"
 #include "fp8_tall.cuh"
 #include "norm_fp8.cuh"
 #include "pair_plan.h"
@@ -62,15 +61,6 @@ cudaError_t allow_pair()
                                 static_cast<int>(mbglu::kFp8Smem));
 }
 
-constexpr int kRowsSmem = 196 * 1024;   // beside up to 27 KB of static shared memory
-
-template <int NT, int OUT, int WARPS, int DEPTH, int PER_SM>
-cudaError_t allow_rows()
-{
-    return cudaFuncSetAttribute(mbglu::fp8_rows_kernel<NT, OUT, WARPS, DEPTH, PER_SM>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
-}
-
 cudaError_t setup_tall();
 
 cudaError_t setup_fp8()
@@ -79,11 +69,6 @@ cudaError_t setup_fp8()
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8Glu>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kFp8GluQuant>();
     if (e == cudaSuccess) e = setup_tall();
-    if (e == cudaSuccess) e = allow_rows<1, 0, 8, 4, 2>();
-    if (e == cudaSuccess) e = allow_rows<1, 1, 8, 2, 2>();
-    if (e == cudaSuccess) e = allow_rows<2, 1, 8, 2, 1>();
-    if (e == cudaSuccess) e = allow_rows<1, 2, 8, 2, 2>();
-    if (e == cudaSuccess) e = allow_rows<2, 2, 8, 2, 1>();
     return e;
 }
 
@@ -111,100 +96,28 @@ mbglu_status launch_pair(const mbglu::Fp8PairParams &p, const mbglu::PairMaps &m
     return st;
 }
 
-bool rows_take(int M, int K)
-{
-    return K > 0 && K % 16 == 0 && M <= mbglu::kRowsMax && mbglu::rows_smem(M, K, 2) <= kRowsSmem;
-}
+// ---- up to some dozens of rows: fp8_tall_kernel -------------------------------------------
 
-// One weight gives a row kernel's warps half the bytes per activation row, and
-// beyond 8 rows the split product on CTA pairs is faster (K = 9728, N = 2560: 16.0
-// us at M = 9 against 12.9).
-bool rows_take_matmul(int M, int K) { return M <= 8 && rows_take(M, K); }
-
-template <int NT, int OUT, int WARPS, int DEPTH, int PER_SM>
-mbglu_status launch_rows(mbglu::Fp8RowsParams &p, int slices, cudaStream_t stream)
-{
-    int sms = 0;
-    mbglu_status st = sm_count(&sms);   // sets the kernels' attributes once per device
-    if (st != MBGLU_OK) return st;
-    p.slices = slices;
-    p.prefetch = launch_policy() == MBGLU_POLICY_PREFETCH;
-    const int R = WARPS / slices, cluster = OUT == 2 ? 8 / R : 1;
-    const int blocks = OUT == 2 ? ceil_div(p.N, kBlk) * cluster : ceil_div(p.N, 16 * R);
-    p.pitch = mbglu::rows_pitch(p.K);
-    Launch l(dim3(static_cast<unsigned>(blocks)), WARPS * 32, static_cast<size_t>(mbglu::rows_smem(p.M, p.K, OUT == 0 ? 1 : 2)), stream, cluster);
-    st = launched(cudaLaunchKernelEx(&l.cfg, mbglu::fp8_rows_kernel<NT, OUT, WARPS, DEPTH, PER_SM>, p));
-    if (st == MBGLU_OK) set_last_variant(kFp8Rows);
-    return st;
-}
-
-// The largest number of K-slices (each of at least one scale block) that keeps
-// the blocks in one wave: more slices, more bytes in flight; a second wave
-// starts cold.
-int rows_slices(int N, int K, int warps, int most_blocks)
-{
-    int s = warps;
-    while (s > 1 && (ceil_div(N, 16 * (warps / s)) > most_blocks || ceil_div(K, kBlk) < s)) s /= 2;
-    return std::max(s, warps / 8);   // a block holds at most 128 rows
-}
-
-mbglu_status matmul_rows(mbglu::Fp8RowsParams &p, cudaStream_t stream)
-{
-    return launch_rows<1, 0, 8, 4, 2>(p, rows_slices(p.N, p.K, 8, 4 * kPairs), stream);
-}
-
-// A cluster's blocks start together on one part of the chip, so that not quite
-// every place can be filled.
-template <int OUT>
-mbglu_status glu_rows(mbglu::Fp8RowsParams &p, cudaStream_t stream)
-{
-    const int places = OUT == 2 ? 7 * kPairs / 2 : 4 * kPairs;
-    return p.M <= 8 ? launch_rows<1, OUT, 8, 2, 2>(p, rows_slices(p.N, p.K, 8, places), stream)
-                    : launch_rows<2, OUT, 8, 2, 1>(p, rows_slices(p.N, p.K, 8, places / 2), stream);
-}
-
-mbglu::Fp8RowsParams rows_params(const Scaled &a, int M, int N, int K)
-{
-    mbglu::Fp8RowsParams p = {};
-    p.a = a.p;
-    p.lda = a.ld;
-    p.as = a.s;
-    p.ldas = a.lds;
-    p.M = M;
-    p.N = N;
-    p.K = K;
-    return p;
-}
-
-void rows_weight(mbglu::Fp8RowsParams &p, int d, const Scaled &w)
-{
-    p.w[d] = w.p;
-    p.ldw[d] = w.ld;
-    p.ws[d] = w.s;
-    p.ldws[d] = w.lds;
-}
-
-// ---- some dozens of rows: fp8_tall_kernel -------------------------------------------
-
-// Clusters of ks blocks, each with an SM of its own, that the part holds at once.
-constexpr int kClusters[mbglu::kTallMaxSplit + 1] = {0, 152, 76, 46, 36, 28, 23};
+// Clusters of ks blocks, each with an SM of its own, that the part holds at once
+// (tall_per_sm: some have two per SM).
+constexpr int kClusters[mbglu::kTallMaxSplit + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 
 struct TallPlan {
     int tn, ks;
 };
 
-// Tokens per block: the least power of two from `least` to `most` that holds
-// all, else `most`.  Ranges of the inner dimension: what makes rounds x (stages of a range +
-// what a round costs beside them, about 8 stages' time) least.
-TallPlan tall_plan(int M, int N, int K, int least, int most)
+// Tokens per block: the least of 16, 32, 48, 64, 96 and 128 that holds all, else
+// 128.  Ranges of the inner dimension: what makes rounds x (stages of a range +
+// what a round costs beside them, about 16 stages' time) least.
+TallPlan tall_plan(int M, int N, int K, bool dual)
 {
-    TallPlan t = {least, 1};
-    while (t.tn < M && t.tn < most) t.tn *= 2;
+    TallPlan t = {M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : M <= 64 ? 64 : M <= 96 ? 96 : 128, 1};
     const int64_t units = static_cast<int64_t>(ceil_div(N, mbglu::kTallRows)) * ceil_div(M, t.tn);
     const int chunks = ceil_div(K, kBlk);
     int64_t best = 0;
     for (int ks = 1; ks <= std::min(mbglu::kTallMaxSplit, chunks); ++ks) {
-        const int64_t cost = (units + kClusters[ks] - 1) / kClusters[ks] * (ceil_div(chunks, ks) + 8);
+        const int places = kClusters[ks] * mbglu::tall_per_sm(t.tn, dual);
+        const int64_t cost = (units + places - 1) / places * (ceil_div(chunks, ks) + 16);
         if (ks == 1 || cost < best) {
             best = cost;
             t.ks = ks;
@@ -225,9 +138,9 @@ cudaError_t setup_tall()
     cudaError_t e = cudaSuccess;
 #define MBGLU_ALLOW(TN, OUT) \
     if (e == cudaSuccess) e = allow_tall<TN, OUT>();
-    MBGLU_ALLOW(16, 0) MBGLU_ALLOW(32, 0) MBGLU_ALLOW(64, 0) MBGLU_ALLOW(128, 0) MBGLU_ALLOW(256, 0)
-    MBGLU_ALLOW(32, 1) MBGLU_ALLOW(64, 1) MBGLU_ALLOW(128, 1)
-    MBGLU_ALLOW(32, 2) MBGLU_ALLOW(64, 2) MBGLU_ALLOW(128, 2)
+    MBGLU_ALLOW(16, 0) MBGLU_ALLOW(32, 0) MBGLU_ALLOW(48, 0) MBGLU_ALLOW(64, 0) MBGLU_ALLOW(96, 0) MBGLU_ALLOW(128, 0)
+    MBGLU_ALLOW(16, 1) MBGLU_ALLOW(32, 1) MBGLU_ALLOW(48, 1) MBGLU_ALLOW(64, 1) MBGLU_ALLOW(96, 1) MBGLU_ALLOW(128, 1)
+    MBGLU_ALLOW(16, 2) MBGLU_ALLOW(32, 2) MBGLU_ALLOW(48, 2) MBGLU_ALLOW(64, 2) MBGLU_ALLOW(96, 2) MBGLU_ALLOW(128, 2)
 #undef MBGLU_ALLOW
     return e;
 }
@@ -247,7 +160,7 @@ template <int OUT>
 bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams &p, int M, int N, int K, cudaStream_t stream,
           mbglu_status *st)
 {
-    const TallPlan t = tall_plan(M, N, K, OUT == 0 ? 16 : 32, OUT == 0 ? 256 : 128);
+    const TallPlan t = tall_plan(M, N, K, OUT != 0);
     mbglu::TallMaps maps;
     if (!k_major(&maps.w[0], w0, K) || (w1 && !k_major(&maps.w[1], *w1, K)) || !copyable(a.p, a.ld, 1) ||
         !encode_tile_map(&maps.x, a.p, a.ld, M, K, 128, t.tn, 1))
@@ -268,26 +181,24 @@ bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams
         p.ws[1] = w1->s;
         p.ldws[1] = w1->lds;
     }
-    if constexpr (OUT == 0) {
-        *st = t.tn == 16    ? launch_tall<16, 0>(t, p, maps, stream)
-              : t.tn == 32  ? launch_tall<32, 0>(t, p, maps, stream)
-              : t.tn == 64  ? launch_tall<64, 0>(t, p, maps, stream)
-              : t.tn == 128 ? launch_tall<128, 0>(t, p, maps, stream)
-                            : launch_tall<256, 0>(t, p, maps, stream);
-    } else {
-        *st = t.tn == 32   ? launch_tall<32, OUT>(t, p, maps, stream)
-              : t.tn == 64 ? launch_tall<64, OUT>(t, p, maps, stream)
-                           : launch_tall<128, OUT>(t, p, maps, stream);
-    }
+    *st = t.tn == 16   ? launch_tall<16, OUT>(t, p, maps, stream)
+          : t.tn == 32 ? launch_tall<32, OUT>(t, p, maps, stream)
+          : t.tn == 48 ? launch_tall<48, OUT>(t, p, maps, stream)
+          : t.tn == 64 ? launch_tall<64, OUT>(t, p, maps, stream)
+          : t.tn == 96 ? launch_tall<96, OUT>(t, p, maps, stream)
+                       : launch_tall<128, OUT>(t, p, maps, stream);
     return true;
 }
 
-constexpr int kTallMatmul = 512, kTallGlu = 256;   // rows up to which the tall kernel is taken
+// Rows up to which the tall kernel is taken (chained, cold L2; against CTA pairs):
+// K = 9728, N = 2560: 14.9 and 20.0 us at M = 128, 20.4 and 20.4 at 200; two weights
+// of K = 2560, N = 9728: 15.4 and 18.0 us at M = 48, 21.6 and 17.3 at 96.
+constexpr int kTallMatmul = 128, kTallGlu = 64;
 
 mbglu::PairPlan matmul_plan(int M, int N, int K)
 {
     const int chunks = ceil_div(K, kBlk);
-    return pair_plan(M, N, 256, 1, chunks, chunks, true);
+    return pair_plan(M, N, 256, 1, chunks, chunks, M > kTallMatmul);   // fewer rows have no workspace
 }
 
 }  // namespace
@@ -362,7 +273,7 @@ mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw, uint8_t *q, i
 size_t matmul_fp8_workspace_bytes(int M, int N, int K)
 {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
-    return rows_take_matmul(M, K) ? 0 : static_cast<size_t>(part_bytes(matmul_plan(M, N, K)));
+    return static_cast<size_t>(part_bytes(matmul_plan(M, N, K)));
 }
 
 mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas, const uint8_t *w,
@@ -388,13 +299,6 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
     if (meets(out, ob, A, K) || meets(out, ob, W, K) || meets(workspace, wsb, A, K) || meets(workspace, wsb, W, K) ||
         overlaps(out, ob, workspace, wsb))
         return MBGLU_ERR_ALIAS;
-    if (rows_take_matmul(M, K) && copyable(a, lda, 1) && copyable(w, ldw, 1)) {
-        mbglu::Fp8RowsParams q = rows_params(A, M, N, K);
-        rows_weight(q, 0, W);
-        q.out = out;
-        q.ldo = ldo;
-        return matmul_rows(q, stream);
-    }
     if (K > 0 && M <= kTallMatmul) {
         mbglu::TallParams q = {};
         q.out = out;
@@ -456,18 +360,6 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
     for (const Scaled *in : {&A, &G, &U})
         if (meets(o, ob, *in, K) || meets(q_scale, sb, *in, K)) return MBGLU_ERR_ALIAS;
     if (overlaps(o, ob, q_scale, sb)) return MBGLU_ERR_ALIAS;
-    if (rows_take(M, K) && copyable(a, lda, 1) && copyable(gate_w, ld_gate, 1) && copyable(up_w, ld_up, 1)) {
-        mbglu::Fp8RowsParams p = rows_params(A, M, N, K);
-        rows_weight(p, 0, G);
-        rows_weight(p, 1, U);
-        p.out = out;
-        p.ldo = ldo;
-        p.q = q;
-        p.ldq = ldq;
-        p.qs = q_scale;
-        p.ldqs = ldqs;
-        return q ? glu_rows<2>(p, stream) : glu_rows<1>(p, stream);
-    }
     if (K > 0 && M <= kTallGlu) {
         mbglu::TallParams p = {};
         p.out = out;

@@ -1,6 +1,6 @@
-// fp8_tall.cuh -- the e4m3 products of some dozens of rows (a decode batch, a
-// short chunk): too many for mma.sync fragments per weight byte, too few to fill
-// the 256-row side of a CTA pair's tile.  The weights take the MMA's 128-row
+// fp8_tall.cuh -- the e4m3 products of a token up to some dozens of rows (a
+// decode step): too few to fill the 256-row side of a CTA pair's tile, bound by
+// the bytes of the weights.  The weights take the MMA's 128-row
 // side and the tokens its N, so that both the products and the reading of the
 // accumulators shrink with the batch and what is left is the weights' bytes.
 //
@@ -27,7 +27,9 @@ constexpr int kTallRows = 128;
 constexpr uint32_t kTallW = 16384;             // one weight's bytes per stage
 constexpr int kTallMaxStages = 8;
 constexpr uint32_t kTallHeader = 1024;
-constexpr int kTallMaxSplit = 6;
+constexpr int kTallMaxSplit = 8;
+
+__host__ __device__ constexpr int tall_per_sm(int tn, bool dual) { return tn <= 16 || (dual && tn <= 32) ? 2 : 1; }
 
 template <int TN, bool DUAL>
 struct TallShape {
@@ -35,13 +37,22 @@ struct TallShape {
     static constexpr uint32_t kStage = kMats * kTallW + TN * 128u;
     // scales of 8 blocks: tokens', then the weights'; two of them
     static constexpr uint32_t kScales = (TN * kScaleGroup + 2 * kScaleGroup) * 4u;
-    static constexpr uint32_t kRoom = 225u * 1024 - 1024 - kTallHeader - 2 * kScales;
+    // Small sums leave registers and tensor memory for two blocks per SM: one
+    // block's start and end then lie under another's stream, and the next call's
+    // first weights under this call's last (two weights of K = 4096, N = 11008,
+    // chained: 18.0 us against 22.3 at M = 16, 21.3 against 26.1 at M = 32; one
+    // weight at M = 32: 8.8 against 8.4, so not there).
+    static constexpr int kPerSm = tall_per_sm(TN, DUAL);
+    static constexpr uint32_t kRoom = (kPerSm == 2 ? 113u : 225u) * 1024 - 1024 - kTallHeader - 2 * kScales;
     static constexpr int kStages = kRoom / kStage < kTallMaxStages ? static_cast<int>(kRoom / kStage) : kTallMaxStages;
     static constexpr uint32_t kSmem = 1024 + kTallHeader + 2 * kScales + kStages * kStage;
     // the totals that a block gets: every rank's, of its share of the tokens
     static constexpr uint32_t totals(int ks) { return static_cast<uint32_t>(ks * kMats * ((TN + ks - 1) / ks)) * kTallRows * 4u; }
+    // tensor-memory columns of one of the two buffers
+    static constexpr uint32_t cols(uint32_t n) { return n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+    static constexpr uint32_t kCols = cols(kMats * TN);
     static_assert(totals(1) <= kStages * kStage && totals(3) <= kStages * kStage && totals(5) <= kStages * kStage &&
-                      totals(6) <= kStages * kStage && totals(4) <= kStages * kStage,
+                      totals(6) <= kStages * kStage && totals(7) <= kStages * kStage,
                   "the exchange fits the stages");
     static_assert(kStages >= 3 && kSmem <= 227u * 1024, "shared memory");
 };
@@ -118,13 +129,13 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
 
 // OUT: 0 bf16 product (one weight), 1 bf16 gated, 2 e4m3 gated.
 template <int TN, int OUT>
-__global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, const __grid_constant__ TallMaps maps)
+__global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kernel(const TallParams p, const __grid_constant__ TallMaps maps)
 {
     constexpr bool kDual = OUT != 0;
     using Shape = TallShape<TN, kDual>;
     constexpr int kMats = Shape::kMats, kStages = Shape::kStages;
     constexpr int TH = TN / 2;                     // tokens per thread
-    constexpr int SW = TH < 32 ? TH : 32;          // columns per step
+    constexpr int SW = TH % 32 == 0 ? 32 : TH % 16 == 0 ? 16 : 8;   // columns per step
     constexpr int kSteps = TH / SW;                // steps per matrix
     extern __shared__ unsigned char tall_raw[];
     unsigned char *base = tall_raw + ((1024u - (smem_addr(tall_raw) & 1023u)) & 1023u);
@@ -132,7 +143,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
     uint64_t *empty = full + kTallMaxStages, *acc_full = empty + kTallMaxStages, *acc_empty = acc_full + 2;
     uint64_t *scale_full = acc_empty + 2, *scale_empty = scale_full + 2;
     uint32_t *slot = reinterpret_cast<uint32_t *>(scale_empty + 2);
-    float *peaks = reinterpret_cast<float *>(base + 512);   // [8 warps][..]: see the end
+    float *peaks = reinterpret_cast<float *>(base + 512);   // 2 x 8 warps x 4 tokens
     unsigned char *stages = base + kTallHeader;
     float *scales = reinterpret_cast<float *>(stages + kStages * Shape::kStage);
     constexpr int kScaleFloats = Shape::kScales / 4;
@@ -159,7 +170,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(slot, 512);
+        tmem_alloc(slot, 2 * Shape::kCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
     if (warp != 0) grid_launch_dependents();
 
     if (warp < 4) {
-        regs_release<88>();
+        if (Shape::kPerSm == 1) regs_release<88>();
         if (warp == 0) {
             auto load_w = [&](int st, int c) {
                 unsigned char *d = stages + st * Shape::kStage;
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
                 tc_fence_after();
                 const uint64_t w = d0 + static_cast<uint32_t>(st) * (Shape::kStage >> 4);
                 const uint64_t x = w + kMats * (kTallW >> 4);
-                const uint32_t d = tmem + buf * 256;
+                const uint32_t d = tmem + buf * Shape::kCols;
                 if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < kMats; ++i)
@@ -282,7 +293,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
         if (ks > 1) cluster_sync();   // the totals have come
         else __syncthreads();
     } else {
-        regs_take<208>();
+        if (Shape::kPerSm == 1) regs_take<208>();
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * TH);
         const int row = q * 32 + lane;
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
                     const float w = sc[kScaleGroup * TN + d * kScaleGroup + in];
                     sw[d] = pack_f32x2(w, w);
                 }
-                const uint32_t from = lanes + buf * 256;
+                const uint32_t from = lanes + buf * Shape::kCols;
 #pragma unroll
                 for (int s = 0; s < kMats * kSteps; ++s) {
                     const int next = s + 1;
@@ -327,7 +338,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
                             if (ok) ok = pair_wait(&acc_full[buf ^ 1], ((v + 1) >> 1) & 1, kWaitLimitNs);
                             __syncwarp();
                             tc_fence_after();
-                            tmem_load(lanes + (buf ^ 1) * 256, r[next & 1]);
+                            tmem_load(lanes + (buf ^ 1) * Shape::kCols, r[next & 1]);
                         }
                     }
                     const int d = s / kSteps, t0 = s % kSteps * SW;
@@ -377,36 +388,51 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
         }
         if (ks > 1) cluster_sync();
         else __syncthreads();
-        // this block's tokens: warps 4-7 and 8-11 take alternate ones, a thread one weight row
+        // this block's tokens: warps 4-7 and 8-11 take groups of four in turn (four
+        // chains of loads, SiLUs and shuffles at once), a thread one weight row
+        constexpr int kGroup = 4;
         const int n = wt * kTallRows + row;
         const int first = rank * share, count = min(min(share, TN - first), p.M - m0 - first);
-        for (int t = half; t < count + (count & 1); t += 2) {   // both halves run the same rounds: there is a barrier
-            const bool live = t < count;
-            float x = 0.0f, y = 0.0f;
-            if (live) {
-                for (int s = 0; s < ks; ++s) {
-                    x += totals[(s * kMats * share + t) * kTallRows + row];
-                    if (kDual) y += totals[((s * kMats + 1) * share + t) * kTallRows + row];
-                }
-            }
-            const int64_t m = m0 + first + t;
-            const float val = kDual ? silu_short(x) * y : x;
-            if constexpr (OUT == 2) {
-                float amax = live && n < p.N ? fabsf(val) : 0.0f;
+        for (int g0 = 0; g0 < count; g0 += 2 * kGroup) {   // both halves run the same rounds: there is a barrier
+            const int t0 = g0 + half * kGroup;
+            float val[kGroup];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            for (int u = 0; u < kGroup; ++u) {
+                float x = 0.0f, y = 0.0f;
+                if (t0 + u < count) {
+                    for (int s = 0; s < ks; ++s) {
+                        x += totals[(s * kMats * share + t0 + u) * kTallRows + row];
+                        if (kDual) y += totals[((s * kMats + 1) * share + t0 + u) * kTallRows + row];
+                    }
+                }
+                val[u] = kDual ? silu_short(x) * y : x;
+            }
+            const int64_t m = m0 + first + t0;
+            if constexpr (OUT == 2) {
+                float amax[kGroup];
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) amax[u] = n < p.N ? fabsf(val[u]) : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                    for (int u = 0; u < kGroup; ++u) amax[u] = max_nan(amax[u], __shfl_xor_sync(0xffffffffu, amax[u], o));
                 // the four warps of a half hold the group; two sets of places, used in turn
-                float *pk = peaks + ((t >> 1) & 1) * 8 + half * 4;
-                if (lane == 0) pk[q] = amax;
+                float *pk = peaks + ((g0 / (2 * kGroup)) & 1) * 8 * kGroup + half * 4 * kGroup;
+                if (lane == 0) *reinterpret_cast<float4 *>(pk + q * kGroup) = make_float4(amax[0], amax[1], amax[2], amax[3]);
                 bar_sync_named(1, 256);
-                amax = max_nan(max_nan(pk[0], pk[1]), max_nan(pk[2], pk[3]));
-                const float s = group_scale(amax);
-                if (live && ok) {
-                    if (row == 0) p.qs[m * p.ldqs + wt] = s;
-                    if (n < p.N) p.q[m * p.ldq + n] = static_cast<uint8_t>(pack_e4m3x2(val * (1.0f / s), 0.0f));
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {
+                    const float a = max_nan(max_nan(pk[u], pk[kGroup + u]), max_nan(pk[2 * kGroup + u], pk[3 * kGroup + u]));
+                    const float s = group_scale(a);
+                    if (t0 + u < count && ok) {
+                        if (row == 0) p.qs[(m + u) * p.ldqs + wt] = s;
+                        if (n < p.N) p.q[(m + u) * p.ldq + n] = static_cast<uint8_t>(pack_e4m3x2(val[u] * (1.0f / s), 0.0f));
+                    }
                 }
             } else {
-                if (live && ok && n < p.N) p.out[m * p.ldo + n] = f32_to_bf16(val);
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u)
+                    if (t0 + u < count && ok && n < p.N) p.out[(m + u) * p.ldo + n] = f32_to_bf16(val[u]);
             }
         }
     }
@@ -416,7 +442,7 @@ __global__ void __launch_bounds__(384, 1) fp8_tall_kernel(const TallParams p, co
     __syncwarp();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, 2 * Shape::kCols);
     }
 }
 
