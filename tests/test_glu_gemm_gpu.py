@@ -58,6 +58,20 @@ def test_inner_dimension(K):
     check_forward(*operands(90, 136, K, seed=K))
 
 
+@pytest.mark.parametrize("M,N,K,pad,variant", [(2000, 4801, 1104, 0, 11), (2001, 4864, 1099, 5, 11), (1000, 9728, 2048, 0, 11),
+                                               (2000, 4800, 1100, 3, 12)])
+def test_each_kernel(M, N, K, pad, variant):
+    """Sizes that each of the kernels takes: CTA pairs (several rounds, ragged in
+    every dimension), any alignment."""
+    h, gw, uw = operands(M, N, K, seed=M, pad=pad)
+    if variant == 12:
+        h, gw, uw = h[:100], gw[:200], uw[:200]   # the slow kernel: a corner of it
+    check_forward(h, gw, uw)
+    assert mb.last_variant() == variant
+    if variant != 12:
+        check_forward(h, gw, uw, mode="hf", gu=True)
+
+
 @pytest.mark.parametrize("M", [1, 2, 16, 40, 64])
 def test_few_rows(M):
     ops = operands(M, 136, 264, seed=M)
@@ -142,7 +156,8 @@ def check_backward(h, gw, uw, d, gu=False, **kw):
 
 @pytest.mark.parametrize("gu", [False, True])
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (3, 40, 24), (65, 136, 72), (64, 64, 64), (128, 128, 256), (257, 264, 136),
-                                   (300, 1000, 520), (33, 1, 9), (100, 77, 51), (70, 129, 257), (520, 56, 64)])
+                                   (300, 1000, 520), (33, 1, 9), (100, 77, 51), (70, 129, 257), (520, 56, 64),
+                                   (2000, 4801, 1104)])
 def test_backward_sizes(M, N, K, gu):
     h, gw, uw = operands(M, N, K, seed=M + N)
     check_backward(h, gw, uw, rand(M, N, seed=5), gu=gu)
