@@ -474,12 +474,13 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
  *                          scheduled while the preceding kernel drains, but
  *                          read and write nothing in global memory before it
  *                          has completed.
- *   MBGLU_POLICY_PREFETCH  as PDL, and the first weight stages (gate_w and
- *                          up_w only) are requested before that wait, so a
+ *   MBGLU_POLICY_PREFETCH  as PDL, and the first weight stages (gate_w, up_w
+ *                          and matmul_fp8's w only; not their scales) are
+ *                          requested before that wait, so a
  *                          decode step's back-to-back calls overlap one call's
  *                          tail with the next call's ramp.  Contract: the
  *                          kernel immediately preceding a call on its stream
- *                          must not write gate_w / up_w after releasing its
+ *                          must not write those weights after releasing its
  *                          dependents early (kernels that do not use
  *                          programmatic dependent launch never do: they
  *                          release at completion).  Use SERIAL or PDL around

@@ -271,14 +271,21 @@ class DualWeightGlu(torch.autograd.Function):
     gradients land on those tensors).
 
     Up to MAX_M rows run glu_gemv and glu_backward; more run glu_gemm, which
-    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward."""
+    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward.  Where no gradient
+    can follow, apply is the forward call alone.  To capture a training step
+    into a CUDA graph, run it on the capture's stream first and let no eager
+    graph over the same leaves live meanwhile, as for any autograd Function."""
+
+    @classmethod
+    def apply(cls, h, gate_w, up_w, mode="fused"):
+        if not (torch.is_grad_enabled() and (h.requires_grad or gate_w.requires_grad or up_w.requires_grad)):
+            return (glu_gemm if h.dim() == 2 and h.shape[0] > MAX_M else glu_gemv)(h, gate_w, up_w, mode=mode)
+        return super().apply(h, gate_w, up_w, mode)
 
     @staticmethod
     def forward(ctx, h, gate_w, up_w, mode="fused"):
         if h.dim() == 2 and h.shape[0] > MAX_M:
-            gu = None
-            if any(ctx.needs_input_grad[:3]):
-                gu = torch.empty((h.shape[0], 2 * gate_w.shape[0]), dtype=torch.float32, device=h.device)
+            gu = torch.empty((h.shape[0], 2 * gate_w.shape[0]), dtype=torch.float32, device=h.device)
             out = glu_gemm(h, gate_w, up_w, mode=mode, gu=gu)
             ctx.save_for_backward(h, gate_w, up_w, gu)
             return out
@@ -396,12 +403,16 @@ def _dims(t, name, dtype):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    if max(t.shape) > _MOST:
+        raise ValueError(f"{name} has more than {_MOST} rows or columns: {tuple(t.shape)}")
     return (*t.shape, t.device)
 
 
 def _out_rows(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
+    if t.shape[0] > _MOST:
+        raise ValueError(f"{name} has more than {_MOST} rows: {tuple(t.shape)}")
     return t.shape[0]
 
 
@@ -443,6 +454,7 @@ def _stream_of(dev, stream):
 
 
 _NONE = (None, 0)
+_MOST = 2 ** 31 - 1   # the C entry points take int sizes
 
 
 def glu_gemm(h, gate_w, up_w, out=None, mode="fused", gu=None, stream=None):

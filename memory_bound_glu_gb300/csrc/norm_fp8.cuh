@@ -158,8 +158,10 @@ __global__ void __launch_bounds__(256) norm_fp8_kernel(const NormFp8Params p)
 }
 
 // A weight [N][K] bf16 to e4m3 with a scale per 128 x 128 block, one thread
-// block each.  Runs once per weight.  It does not release its dependents early:
-// what it writes is the next call's weight.
+// block each.  Runs once per weight.  What it writes may be the very next call's
+// weight, which that call's kernel copies before its dependency wait: so it does
+// not release its dependents early, and its stores are performed, for
+// asynchronous copies too, before a block ends.
 __global__ void __launch_bounds__(256) quant_weight_kernel(const uint16_t *w, int64_t ldw, uint8_t *q, int64_t ldq,
                                                            float *scale, int64_t lds, int N, int K)
 {
@@ -189,6 +191,8 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const uint16_t *w, in
             if (n < N && k < K) q[n * ldq + k] = static_cast<uint8_t>(pack_e4m3x2(bf16_to_f32(w[n * ldw + k]) * r, 0.0f));
         }
     }
+    __threadfence();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
 }  // namespace mbglu

@@ -276,3 +276,81 @@ def test_rows_do_not_depend_on_their_place():
         assert torch.equal(mb.matmul_fp8(pa, sa[perm], *w), mb.matmul_fp8(a, sa, *w)[perm])
         x, y = mb.glu_fp8(pa, sa[perm], *w, *u, out_dtype=F8), mb.glu_fp8(a, sa, *w, *u, out_dtype=F8)
         assert torch.equal(x[0].float(), y[0].float()[perm]) and torch.equal(x[1], y[1][perm])
+
+
+def test_weight_quantised_right_before_its_use():
+    """The next call's kernel may copy its weight before its predecessor is waited for."""
+    a, sa = activations(4, 2048)
+    w = [(rand(2048, 2048, seed=i) * 2048 ** -0.5).to(BF) for i in range(6)]
+    q, s = (torch.empty(2048, 2048, device=DEV).to(F8), torch.empty(16, 16, device=DEV))
+    want = [mb.matmul_fp8(a, sa, *mb.quantize_weight_fp8(x)) for x in w]
+    for _ in range(3):
+        got = []
+        for x in w:
+            mb.quantize_weight_fp8(x, q=q, scale=s)
+            got.append(mb.matmul_fp8(a, sa, q, s))
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_given_outputs_workspace_and_stream():
+    a, w, u = activations(150, 4096), weight(300, 4096, seed=1), weight(300, 4096, seed=2)
+    want, (wq, ws) = mb.matmul_fp8(*a, *w), mb.glu_fp8(*a, *w, *u, out_dtype=F8)
+    need = mb.matmul_fp8_workspace_bytes(150, 300, 4096)
+    assert need > 0
+    out = torch.zeros(150, 300, dtype=BF, device=DEV)
+    q, s = torch.zeros(150, 300, device=DEV).to(F8), torch.zeros(150, 3, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ws1 = torch.empty(need, dtype=torch.uint8, device=DEV)
+    assert mb.matmul_fp8(*a, *w, out=out, workspace=ws1, stream=side) is out
+    r = mb.glu_fp8(*a, *w, *u, out=q, out_scale=s, out_dtype=F8, stream=side)
+    side.synchronize()
+    assert r[0] is q and r[1] is s
+    assert torch.equal(out, want) and torch.equal(q.float(), wq.float()) and torch.equal(s, ws)
+    with pytest.raises(mb.MbgluError):
+        mb.matmul_fp8(*a, *w, workspace=ws1[: need - 256])
+    with pytest.raises(ValueError):
+        mb.glu_fp8(*a, *w, *u, out_scale=s)
+    with pytest.raises((TypeError, ValueError)):
+        mb.glu_fp8(*a, *w, *u, out=out, out_dtype=F8)
+    with pytest.raises((TypeError, ValueError)):
+        mb.matmul_fp8(a[0], a[1][:, :1], *w)
+    with pytest.raises((TypeError, ValueError)):
+        mb.add_rmsnorm_fp8(out, out, torch.zeros(299, dtype=BF, device=DEV), 1e-6)
+
+
+def test_launch_policies_agree():
+    old = mb.get_launch_policy()
+    ops = [(activations(m, 1024, seed=m), weight(400, 1024, seed=1), weight(400, 1024, seed=2)) for m in (3, 70, 200)]
+    try:
+        got = []
+        for policy in (mb.POLICY_SERIAL, mb.POLICY_PDL, mb.POLICY_PREFETCH):
+            mb.set_launch_policy(policy)
+            got.append([(mb.matmul_fp8(*a, *w), *mb.glu_fp8(*a, *w, *u, out_dtype=F8)) for a, w, u in ops])
+        for other in got[1:]:
+            for x, y in zip(got[0], other):
+                assert all(torch.equal(i.float(), j.float()) for i, j in zip(x, y))
+    finally:
+        mb.set_launch_policy(old)
+
+
+def test_captured_calls_of_two_graphs_share_nothing():
+    """Two graphs with calls that need workspaces, replayed at the same time."""
+    ops = [(*activations(140, 4096, seed=i), *weight(300, 4096, seed=i)) for i in (1, 2)]
+    want = [mb.matmul_fp8(*o) for o in ops]
+    graphs, outs = [], []
+    for o in ops:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(mb.matmul_fp8(*o))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in ops]
+    for _ in range(5):
+        for x in outs:
+            x.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))

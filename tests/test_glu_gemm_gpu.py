@@ -269,3 +269,74 @@ def test_other_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_apply_without_gradients_keeps_nothing():
+    h, gw, uw = operands(300, 520, 64, seed=20)
+    want = mb.glu_gemm(h, gw, uw)
+    leaves = [t.clone().requires_grad_(True) for t in (gw, uw)]
+    with torch.no_grad():
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        out = mb.DualWeightGlu.apply(h, *leaves)
+        assert torch.cuda.memory_allocated() - before < 300 * 520 * 8   # out, no g and u
+    assert torch.equal(out, want) and not out.requires_grad
+    assert torch.equal(mb.DualWeightGlu.apply(h, gw, uw), want)
+    assert torch.equal(mb.DualWeightGlu.apply(h[:5], gw, uw), mb.glu_gemv(h[:5], gw, uw))
+    assert mb.DualWeightGlu.apply(h, *leaves).requires_grad
+
+
+def test_training_step_in_a_graph():
+    """Forward and backward captured together, replayed on new values."""
+    ops = operands(200, 136, 72, seed=21)
+    d = rand(200, 136, seed=22)
+    leaves = [t.clone().requires_grad_(True) for t in ops]
+
+    def step():
+        out = mb.DualWeightGlu.apply(*leaves)
+        return (out.detach(), *torch.autograd.grad(out, leaves, d))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    new = operands(200, 136, 72, seed=23)
+    with torch.no_grad():
+        for t, n in zip(leaves, new):
+            t.copy_(n)
+    g.replay()
+    torch.cuda.synchronize()
+    want = step()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_same_tensor_twice_and_broadcast_rows():
+    h, gw, _ = operands(130, 96, 96, seed=24)
+    check_forward(h, gw, gw)
+    check_forward(h, h[:96], h[:96])
+    with pytest.raises(mb.MbgluError):
+        mb.glu_gemm(h[:1].expand(130, 96), gw, gw)            # rows of stride 0
+    with pytest.raises(mb.MbgluError):
+        mb.glu_gemm(h, gw, gw, out=h[:, :96])                 # in place
+    with pytest.raises(ValueError):
+        mb.glu_gemm(h.t(), gw[:, :1].expand(96, 130), gw[:, :1].expand(96, 130))
+
+
+def test_operands_on_the_cpu_or_of_other_types_are_refused():
+    h, gw, uw = operands(70, 32, 32)
+    for bad in (gw.cpu(), gw.float(), gw[:, :31], gw[0]):
+        with pytest.raises((TypeError, ValueError)):
+            mb.glu_gemm(h, bad, uw)
+    with pytest.raises((TypeError, ValueError)):
+        mb.glu_gemm(h, gw, uw, gu=torch.zeros(70, 64, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises((TypeError, ValueError)):
+        mb.glu_gemm_backward(h, gw, uw, rand(69, 32))
+    with pytest.raises(ValueError):
+        mb.glu_gemm_backward(h, gw, uw, rand(70, 32), workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+    with pytest.raises(mb.MbgluError):
+        mb.glu_gemm_backward(h, gw, uw, rand(70, 32), workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
