@@ -280,6 +280,10 @@ class DualWeightGlu(torch.autograd.Function):
     def apply(cls, h, gate_w, up_w, mode="fused"):
         if not (torch.is_grad_enabled() and (h.requires_grad or gate_w.requires_grad or up_w.requires_grad)):
             return (glu_gemm if h.dim() == 2 and h.shape[0] > MAX_M else glu_gemv)(h, gate_w, up_w, mode=mode)
+        if h.dim() == 2 and h.shape[0] > MAX_M:   # the same node without Python, in its common case
+            out = (_quick_module or _quick()).wide_glu(h, gate_w, up_w, _MODES[mode])
+            if out is not None:
+                return out
         return super().apply(h, gate_w, up_w, mode)
 
     @staticmethod

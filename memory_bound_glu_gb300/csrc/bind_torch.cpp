@@ -13,6 +13,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mbglu.h"
@@ -142,6 +143,86 @@ PyObject *py_gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
                                        static_cast<float *>(gu.p), gu.ld, static_cast<int>(M), static_cast<int>(N),
                                        static_cast<int>(K), static_cast<mbglu_mode>(mode), stream_of(dev));
         return st ? status(st) : result(a[3], made);
+    });
+}
+
+// The autograd node of DualWeightGlu above the decode batch: forward keeps g and u
+// in fp32, backward runs without the interpreter (a Python node costs the engine's
+// thread two hand-overs of the interpreter lock).  A failing status becomes an
+// exception, which autograd hands to the caller.
+void must(mbglu_status st, const char *what)
+{
+    TORCH_CHECK(st == MBGLU_OK, what, ": status ", st);
+}
+
+struct WideGlu : torch::autograd::Function<WideGlu> {
+    static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &h, const at::Tensor &gate, const at::Tensor &up,
+                              int64_t mode)
+    {
+        const int64_t M = h.size(0), K = h.size(1), N = gate.size(0);
+        const int dev = h.get_device();
+        Operand a, g, u;
+        TORCH_CHECK(operand(h, kBf16, M, K, dev, a) && operand(gate, kBf16, N, K, dev, g) && operand(up, kBf16, N, K, dev, u),
+                    "glu_gemm: operands");
+        at::Tensor out = empty(M, N, kBf16, dev), gu = empty(M, 2 * N, kF32, dev);
+        must(f_gemm(static_cast<mbglu_bf16 *>(a.p), a.ld, static_cast<mbglu_bf16 *>(g.p), g.ld, static_cast<mbglu_bf16 *>(u.p), u.ld,
+                    static_cast<mbglu_bf16 *>(out.data_ptr()), N, static_cast<float *>(gu.data_ptr()), 2 * N, static_cast<int>(M),
+                    static_cast<int>(N), static_cast<int>(K), static_cast<mbglu_mode>(mode), stream_of(dev)),
+             "glu_gemm");
+        ctx->save_for_backward({h, gate, up, gu});
+        return out;
+    }
+
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, torch::autograd::variable_list grads)
+    {
+        const auto saved = ctx->get_saved_variables();
+        const at::Tensor &h = saved[0], &gate = saved[1], &up = saved[2], &gu = saved[3];
+        const int64_t M = h.size(0), K = h.size(1), N = gate.size(0);
+        const int dev = h.get_device();
+        torch::autograd::variable_list out(4);
+        if (!grads[0].defined()) return out;
+        at::Tensor d = grads[0].to(kBf16);
+        if (d.stride(1) != 1 || d.stride(0) < N) d = d.contiguous();   // a broadcast gradient (of a sum) has stride 0
+        Operand a, g, u, dd, oh, og, ou;
+        TORCH_CHECK(operand(h, kBf16, M, K, dev, a) && operand(gate, kBf16, N, K, dev, g) && operand(up, kBf16, N, K, dev, u) &&
+                        operand(d, kBf16, M, N, dev, dd),
+                    "glu_gemm_backward: operands");
+        const bool want_w = ctx->needs_input_grad(1) || ctx->needs_input_grad(2);
+        at::Tensor gh, gg, gw, ws;
+        if (ctx->needs_input_grad(0)) output(Py_None, kBf16, M, K, dev, oh, gh);
+        if (want_w) {
+            output(Py_None, kBf16, N, K, dev, og, gg);
+            output(Py_None, kBf16, N, K, dev, ou, gw);
+        }
+        const size_t need = f_gemm_backward_ws(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K));
+        if (need) ws = empty(1, static_cast<int64_t>(need), ScalarType::Byte, dev);
+        must(f_gemm_backward(static_cast<mbglu_bf16 *>(a.p), a.ld, static_cast<mbglu_bf16 *>(g.p), g.ld, static_cast<mbglu_bf16 *>(u.p),
+                             u.ld, static_cast<mbglu_bf16 *>(dd.p), dd.ld, static_cast<float *>(gu.data_ptr()), 2 * N,
+                             static_cast<mbglu_bf16 *>(oh.p), oh.ld, static_cast<mbglu_bf16 *>(og.p), og.ld,
+                             static_cast<mbglu_bf16 *>(ou.p), ou.ld, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
+                             need ? ws.data_ptr() : nullptr, need, stream_of(dev)),
+             "glu_gemm_backward");
+        out[0] = gh;
+        if (ctx->needs_input_grad(1)) out[1] = gg;
+        if (ctx->needs_input_grad(2)) out[2] = gw;
+        return out;
+    }
+};
+
+// (h, gate_w, up_w, mode): with an autograd node
+PyObject *py_wide_glu(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        int64_t M, K, N, K2;
+        int dev, dev2;
+        if (n != 4 || !first(a[0], kBf16, M, K, dev) || !first(a[1], kBf16, N, K2, dev2) || M == 0 || N == 0 || K == 0)
+            Py_RETURN_NONE;
+        Operand o;
+        for (int i = 0; i < 3; ++i)
+            if (!operand(a[i], kBf16, i ? N : M, K, dev, o)) Py_RETURN_NONE;
+        const long mode = PyLong_AsLong(a[3]);
+        return THPVariable_Wrap(WideGlu::apply(THPVariable_Unpack(a[0]), THPVariable_Unpack(a[1]), THPVariable_Unpack(a[2]),
+                                               static_cast<int64_t>(mode)));
     });
 }
 
@@ -290,6 +371,7 @@ PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 #define MBGLU_METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     MBGLU_METHOD("bind", py_bind),         MBGLU_METHOD("glu_gemm", py_gemm),
+    MBGLU_METHOD("wide_glu", py_wide_glu),
     MBGLU_METHOD("glu_gemm_backward", py_gemm_backward), MBGLU_METHOD("add_rmsnorm_fp8", py_norm),
     MBGLU_METHOD("glu_fp8", py_glu),       MBGLU_METHOD("matmul_fp8", py_matmul),
     {nullptr, nullptr, 0, nullptr}};
