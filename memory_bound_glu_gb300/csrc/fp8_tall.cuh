@@ -28,6 +28,7 @@ constexpr uint32_t kTallW = 16384;             // one weight's bytes per stage
 constexpr int kTallMaxStages = 8;
 constexpr uint32_t kTallHeader = 1024;
 constexpr int kTallMaxSplit = 8;
+constexpr int kTallGroup = 4;                  // scale blocks staged at a time
 
 __host__ __device__ constexpr int tall_per_sm(int tn, bool dual) { return tn <= 16 || (dual && tn <= 32) ? 2 : 1; }
 
@@ -35,8 +36,8 @@ template <int TN, bool DUAL>
 struct TallShape {
     static constexpr int kMats = DUAL ? 2 : 1;
     static constexpr uint32_t kStage = kMats * kTallW + TN * 128u;
-    // scales of 8 blocks: tokens', then the weights'; two of them
-    static constexpr uint32_t kScales = (TN * kScaleGroup + 2 * kScaleGroup) * 4u;
+    // the products of a token's and a weight's scale, of 4 blocks; two of them
+    static constexpr uint32_t kScales = kMats * TN * kTallGroup * 4u;
     // Small sums leave registers and tensor memory for two blocks per SM: one
     // block's start and end then lie under another's stream, and the next call's
     // first weights under this call's last (two weights of K = 4096, N = 11008,
@@ -119,13 +120,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
                  : "memory");
 }
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
-
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // OUT: 0 bf16 product (one weight), 1 bf16 gated, 2 e4m3 gated.
 template <int TN, int OUT>
@@ -270,19 +264,20 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
             }
         } else if (warp == 2) {
             uint32_t g = 0;
-            for (int c = c0; c < c1; c += kScaleGroup, ++g) {
+            for (int c = c0; c < c1; c += kTallGroup, ++g) {
                 float *sc = scales + (g & 1) * kScaleFloats;
+                const int in = lane & 3, b = c + in;
+                float w[kMats];
+#pragma unroll
+                for (int d = 0; d < kMats; ++d) w[d] = b < c1 ? __ldg(p.ws[d] + wt * p.ldws[d] + b) : 0.0f;
                 if (g >= 2 && ok) ok = __all_sync(0xffffffffu, pair_wait(&scale_empty[g & 1], ((g >> 1) - 1) & 1, kWaitLimitNs));
-                const int b = c + (lane & 7);
-                float w = 0.0f;
-                if (lane < 8 * kMats && b < c1)
-                    w = __ldg((kDual && lane >= 8 ? p.ws[1] + wt * p.ldws[1] : p.ws[0] + wt * p.ldws[0]) + b);
 #pragma unroll 8
-                for (int i = 0; i < TN / 4; ++i) {   // 4 tokens x 8 blocks per load
-                    const int tok = 4 * i + (lane >> 3), m = m0 + tok;
-                    sc[(lane & 7) * TN + tok] = m < p.M && b < c1 ? __ldg(p.as + m * p.ldas + b) : 0.0f;
+                for (int i = 0; i < TN / 8; ++i) {   // 8 tokens x 4 blocks per load
+                    const int tok = 8 * i + (lane >> 2), m = m0 + tok;
+                    const float x = m < p.M && b < c1 ? __ldg(p.as + m * p.ldas + b) : 0.0f;
+#pragma unroll
+                    for (int d = 0; d < kMats; ++d) sc[(d * kTallGroup + in) * TN + tok] = x * w[d];
                 }
-                if (lane < 8 * kMats) sc[kScaleGroup * TN + lane] = w;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&scale_full[g & 1]);
             }
@@ -313,17 +308,11 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
 #pragma unroll 1
             for (int c = c0; c < c1; ++c, ++v) {
                 const uint32_t buf = v & 1;
-                const int in = (c - c0) & (kScaleGroup - 1);
+                const int in = (c - c0) & (kTallGroup - 1);
                 if (in == 0 && ok) ok = pair_wait(&scale_full[g & 1], (g >> 1) & 1, kWaitLimitNs);
                 __syncwarp();
                 const float *sc = scales + (g & 1) * kScaleFloats;
                 const float *sx = sc + in * TN + half * TH;
-                uint64_t sw[kMats];
-#pragma unroll
-                for (int d = 0; d < kMats; ++d) {
-                    const float w = sc[kScaleGroup * TN + d * kScaleGroup + in];
-                    sw[d] = pack_f32x2(w, w);
-                }
                 const uint32_t from = lanes + buf * Shape::kCols;
 #pragma unroll
                 for (int s = 0; s < kMats * kSteps; ++s) {
@@ -344,10 +333,9 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
                     const int d = s / kSteps, t0 = s % kSteps * SW;
 #pragma unroll
                     for (int i = 0; i < SW / 4; ++i) {
-                        const float4 x = *reinterpret_cast<const float4 *>(sx + t0 + 4 * i);
-                        scale_add(sums[d][t0 / 2 + 2 * i], r[s & 1][4 * i], r[s & 1][4 * i + 1], mul_f32x2(sw[d], pack_f32x2(x.x, x.y)));
-                        scale_add(sums[d][t0 / 2 + 2 * i + 1], r[s & 1][4 * i + 2], r[s & 1][4 * i + 3],
-                                   mul_f32x2(sw[d], pack_f32x2(x.z, x.w)));
+                        const float4 f = *reinterpret_cast<const float4 *>(sx + d * kTallGroup * TN + t0 + 4 * i);
+                        scale_add(sums[d][t0 / 2 + 2 * i], r[s & 1][4 * i], r[s & 1][4 * i + 1], pack_f32x2(f.x, f.y));
+                        scale_add(sums[d][t0 / 2 + 2 * i + 1], r[s & 1][4 * i + 2], r[s & 1][4 * i + 3], pack_f32x2(f.z, f.w));
                     }
                     if (next < kMats * kSteps || c + 1 < c1) tmem_wait_ld(r[next & 1]);
                 }
@@ -355,7 +343,7 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
 #pragma unroll
                     for (int i = 0; i < SW; ++i) r[0][i] = r[1][i];
                 }
-                if (in == kScaleGroup - 1 || c == c1 - 1) {   // the scales are read
+                if (in == kTallGroup - 1 || c == c1 - 1) {   // the scales are read
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&scale_empty[g & 1]);
                     ++g;
