@@ -1,5 +1,7 @@
 // dense_common.cuh -- device helpers of the gated block beyond the decode
-// batch: the gradients of the GLU, e4m3 conversions and a group's scale, and
+// batch.  Its kernels may start before the one ahead of them has ended and then
+// wait for it, so what that one may have written is read with plain loads, never
+// with read-only ones, whose data may not change while a kernel runs.  Here: the gradients of the GLU, e4m3 conversions and a group's scale, and
 // stores of 32 consecutive columns of one row.
 #pragma once
 #include <cuda_fp16.h>
@@ -143,7 +145,7 @@ __device__ __forceinline__ void load_bf16_32(const uint16_t *p, float (&v)[32], 
     if (valid >= 32 && align >= 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -153,7 +155,7 @@ __device__ __forceinline__ void load_bf16_32(const uint16_t *p, float (&v)[32], 
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < valid ? bf16_to_f32(__ldg(p + i)) : 0.0f;
+        for (int i = 0; i < 32; ++i) v[i] = i < valid ? bf16_to_f32(p[i]) : 0.0f;
     }
 }
 

@@ -269,12 +269,12 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
                 const int in = lane & 3, b = c + in;
                 float w[kMats];
 #pragma unroll
-                for (int d = 0; d < kMats; ++d) w[d] = b < c1 ? __ldg(p.ws[d] + wt * p.ldws[d] + b) : 0.0f;
+                for (int d = 0; d < kMats; ++d) w[d] = b < c1 ? p.ws[d][wt * p.ldws[d] + b] : 0.0f;
                 if (g >= 2 && ok) ok = __all_sync(0xffffffffu, pair_wait(&scale_empty[g & 1], ((g >> 1) - 1) & 1, kWaitLimitNs));
 #pragma unroll 8
                 for (int i = 0; i < TN / 8; ++i) {   // 8 tokens x 4 blocks per load
                     const int tok = 8 * i + (lane >> 2), m = m0 + tok;
-                    const float x = m < p.M && b < c1 ? __ldg(p.as + m * p.ldas + b) : 0.0f;
+                    const float x = m < p.M && b < c1 ? p.as[m * p.ldas + b] : 0.0f;
 #pragma unroll
                     for (int d = 0; d < kMats; ++d) sc[(d * kTallGroup + in) * TN + tok] = x * w[d];
                 }

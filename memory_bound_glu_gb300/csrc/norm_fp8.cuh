@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) norm_fp8_kernel(const NormFp8Params p)
         if (c < chunks) {   // residual_out may be x or residual: plain loads
             xs[j] = x[c];
             rs[j] = r[c];
-            ws[j] = __ldg(w + c);
+            ws[j] = w[c];
         }
     }
     float v[CH][8], ss = 0.0f;

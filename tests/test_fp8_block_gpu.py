@@ -354,3 +354,48 @@ def test_captured_calls_of_two_graphs_share_nothing():
                 g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+@pytest.mark.parametrize("M", [1, 40, 150])
+def test_buffers_used_again_by_the_next_step(M):
+    """Steps back to back through the same q and scale buffers, each on other values:
+    every kernel sees what the one before it wrote, not what an earlier one did."""
+    H, N = 512, 640
+    ws = [mb.quantize_weight_fp8((rand(*s, seed=i) * s[1] ** -0.5).to(BF)) for i, s in enumerate(((N, H), (N, H), (H, N)))]
+    nw = rand(H, seed=3, scale=0.1).to(BF)
+    xs = [rand(M, H, seed=10 + i, scale=4.0 ** (i - 3)).to(BF) for i in range(6)]
+    r = rand(M, H, seed=9).to(BF)
+
+    def step(x, bufs):
+        q, s, q2, s2, ro, y = bufs
+        mb.add_rmsnorm_fp8(x, r, nw, 1e-6, q=q, scale=s, residual_out=ro)
+        mb.glu_fp8(q, s, *ws[0], *ws[1], out=q2, out_scale=s2, out_dtype=F8)
+        return mb.matmul_fp8(q2, s2, *ws[2], out=y)
+
+    def buffers():
+        e = lambda *s: torch.empty(*s, device=DEV)   # noqa: E731
+        return (e(M, H).to(F8), e(M, 4), e(M, N).to(F8), e(M, 5), e(M, H).to(BF), e(M, H).to(BF))
+
+    want = []
+    for x in xs:
+        want.append(step(x, buffers()).clone())
+        torch.cuda.synchronize()
+    one = buffers()
+    for _ in range(3):
+        ys = [torch.empty(M, H, dtype=BF, device=DEV) for _ in xs]
+        for x, y in zip(xs, ys):
+            step(x, (*one[:5], y))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ys, want))
+    # and within one graph
+    ys = [torch.empty(M, H, dtype=BF, device=DEV) for _ in xs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for x, y in zip(xs, ys):
+            step(x, (*one[:5], y))
+    for _ in range(3):
+        for y in ys:
+            y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ys, want))

@@ -340,3 +340,24 @@ def test_operands_on_the_cpu_or_of_other_types_are_refused():
         mb.glu_gemm_backward(h, gw, uw, rand(70, 32), workspace=torch.zeros(1 << 20, dtype=torch.uint8))
     with pytest.raises(mb.MbgluError):
         mb.glu_gemm_backward(h, gw, uw, rand(70, 32), workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
+
+
+def test_workspace_and_gu_used_again_by_the_next_step():
+    """Training steps back to back through the same g/u buffer and workspace."""
+    M, N, K = 300, 264, 136
+    steps = [(operands(M, N, K, seed=30 + i), rand(M, N, seed=40 + i)) for i in range(4)]
+    want = []
+    for (h, gw, uw), d in steps:
+        gu = torch.empty(M, 2 * N, device=DEV)
+        mb.glu_gemm(h, gw, uw, gu=gu)
+        want.append(mb.glu_gemm_backward(h, gw, uw, d, gu=gu))
+        torch.cuda.synchronize()
+    gu = torch.empty(M, 2 * N, device=DEV)
+    ws = torch.empty(mb.glu_gemm_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        got = []
+        for (h, gw, uw), d in steps:
+            mb.glu_gemm(h, gw, uw, gu=gu)
+            got.append(mb.glu_gemm_backward(h, gw, uw, d, gu=gu, workspace=ws))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for a, b in zip(got, want) for x, y in zip(a, b))
