@@ -52,7 +52,7 @@ bool first(PyObject *o, ScalarType type, int64_t &rows, int64_t &cols, int &devi
 bool operand(const at::Tensor &t, ScalarType type, int64_t rows, int64_t cols, int device, Operand &out)
 {
     if (!t.is_cuda() || t.get_device() != device || t.dim() != 2 || t.scalar_type() != type || t.size(0) != rows ||
-        t.size(1) != cols || t.stride(1) != 1)
+        t.size(1) != cols || t.stride(1) != 1 || (rows > 1 && t.stride(0) < cols))
         return false;
     out.p = t.data_ptr();
     out.ld = rows > 1 ? t.stride(0) : cols;

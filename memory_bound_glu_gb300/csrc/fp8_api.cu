@@ -78,9 +78,12 @@ mbglu_status sm_count(int *n)
     return table.get(n, setup_fp8);
 }
 
-bool k_major(mbglu::TensorMap *m, const Scaled &o, int K)
+// A map of 128 columns x box_rows; false where tensor copies do not take the
+// operand.  The stride of a single row is never used: any multiple of 16 does.
+bool k_major(mbglu::TensorMap *m, const Scaled &o, int K, int box_rows = 128)
 {
-    return copyable(o.p, o.ld, 1) && encode_tile_map(m, o.p, o.ld, static_cast<int>(o.rows), K, 128, 128, 1);
+    const int64_t ld = o.rows == 1 ? (o.ld + 15) / 16 * 16 : o.ld;
+    return copyable(o.p, ld, 1) && encode_tile_map(m, o.p, ld, static_cast<int>(o.rows), K, 128, box_rows, 1);
 }
 
 template <int EPI>
@@ -162,8 +165,7 @@ bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams
 {
     const TallPlan t = tall_plan(M, N, K, OUT != 0);
     mbglu::TallMaps maps;
-    if (!k_major(&maps.w[0], w0, K) || (w1 && !k_major(&maps.w[1], *w1, K)) || !copyable(a.p, a.ld, 1) ||
-        !encode_tile_map(&maps.x, a.p, a.ld, M, K, 128, t.tn, 1))
+    if (!k_major(&maps.w[0], w0, K) || (w1 && !k_major(&maps.w[1], *w1, K)) || !k_major(&maps.x, a, K, t.tn))
         return false;
     int sms = 0;
     if ((*st = sm_count(&sms)) != MBGLU_OK) return true;
@@ -190,9 +192,10 @@ bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams
     return true;
 }
 
-// Rows up to which the tall kernel is taken (chained, cold L2; against CTA pairs):
-// K = 9728, N = 2560: 14.9 and 20.0 us at M = 128, 20.4 and 20.4 at 200; two weights
-// of K = 2560, N = 9728: 15.4 and 18.0 us at M = 48, 21.6 and 17.3 at 96.
+// Rows up to which the tall kernel is taken (chained, cold L2; against CTA pairs).
+// One weight: 13.5 and 20.0 us at M = 128, 18.6 and 20.8 at 256 (K = 9728, N = 2560);
+// 16.4 and 23.5, 25.9 and 24.4 (K = 11008, N = 4096).  Two: 15.3 and 17.4 at M = 48, 21.4
+// and 17.2 at 96 (K = 2560, N = 9728); 30.1 and 35.4 at 64 (K = 4096, N = 11008).
 constexpr int kTallMatmul = 128, kTallGlu = 64;
 
 mbglu::PairPlan matmul_plan(int M, int N, int K)

@@ -1,0 +1,146 @@
+"""CPU models of the wide and the e4m3 kernels' plans: every tile of a CTA-pair
+product is done once and whole, rings of stages wait on the right phases, and the
+few-row kernel's exchange puts each total where its reader looks, inside its
+stages."""
+import pytest
+
+PAIRS, TILE = 76, 256
+
+
+def ceil_div(a, b):
+    return -(-a // b)
+
+
+def pair_plan(rows, cols, tile_cols, nout, nchunk, may_split):
+    mt, nt = ceil_div(rows, TILE), ceil_div(cols, tile_cols)
+    tiles = mt * nt * nout
+    plan = dict(mt=mt, nt=nt, nout=nout, whole=tiles, rest=0, splits=1, group=8, nchunk=nchunk)
+    left = tiles % PAIRS
+    if may_split and left:
+        s = min(PAIRS // left, nchunk // 8, 16)
+        if s > 1 and nchunk - nchunk // s >= 24:
+            plan.update(whole=tiles - left, rest=left, splits=s)
+    plan["ntiles"] = plan["whole"] + plan["rest"] * plan["splits"]
+    return plan
+
+
+def place(p, t):
+    per = p["mt"] * p["nt"]
+    o, t = divmod(t, per)
+    g = t // (p["group"] * p["nt"])
+    first = g * p["group"]
+    gm = min(p["mt"] - first, p["group"])
+    t -= first * p["nt"]
+    return o, first + t % gm, t // gm
+
+
+def tile_at(p, t):
+    slot, c0, c1 = (-1 if t < p["whole"] else t - p["whole"]), 0, p["nchunk"]
+    if slot >= 0:
+        split = slot // p["rest"]
+        t = p["whole"] + slot % p["rest"]
+        c0, c1 = p["nchunk"] * split // p["splits"], p["nchunk"] * (split + 1) // p["splits"]
+    return place(p, t), slot, c0, c1
+
+
+@pytest.mark.parametrize("rows", [1, 256, 257, 333, 2100, 4096, 20000])
+@pytest.mark.parametrize("cols,tile_cols,nout", [(1, 256, 1), (2560, 256, 1), (9728, 128, 1), (1000, 256, 2), (14336, 256, 2)])
+@pytest.mark.parametrize("nchunk", [1, 8, 31, 76, 304])
+def test_every_tile_once_and_whole(rows, cols, tile_cols, nout, nchunk):
+    p = pair_plan(rows, cols, tile_cols, nout, nchunk, True)
+    seen = {}
+    for t in range(p["ntiles"]):
+        at, slot, c0, c1 = tile_at(p, t)
+        o, mi, ni = at
+        assert o < nout and mi < p["mt"] and ni < p["nt"] and 0 <= c0 < c1 <= nchunk
+        seen.setdefault(at, []).append((c0, c1, slot))
+    assert len(seen) == p["mt"] * p["nt"] * nout
+    slots = set()
+    for parts in seen.values():
+        parts.sort()
+        assert parts[0][0] == 0 and parts[-1][1] == nchunk
+        assert all(a[1] == b[0] for a, b in zip(parts, parts[1:]))
+        if len(parts) == 1:
+            assert parts[0][2] == -1
+        else:
+            assert all(c1 - c0 >= 8 for c0, c1, _ in parts)
+            slots.update(x[2] for x in parts)
+    assert slots == set(range(p["rest"] * p["splits"])) and len(slots) <= PAIRS
+    # the join finds the ranges of leftover tile i at slots i, i + rest, ..
+    for i in range(p["rest"]):
+        for s in range(p["splits"]):
+            assert tile_at(p, p["whole"] + s * p["rest"] + i)[0] == place(p, p["whole"] + i)
+
+
+@pytest.mark.parametrize("S", [3, 4, 6, 8])
+@pytest.mark.parametrize("total", list(range(0, 30)))
+@pytest.mark.parametrize("early", [False, True])
+def test_ring_phases(S, total, early):
+    """The producer's walk: a stage is filled again only after its products were read
+    (barrier phase by phase), and the drain waits for the last fill of each stage.
+    early: the first stages are filled before the loop."""
+    done = [0] * S                                # completions of empty[] so far
+
+    def passes(i, parity):                        # try_wait.parity: that phase has completed
+        return (done[i] & 1) != parity
+
+    pre = min(S, total) if early else 0
+    fills = [0] * S
+    for i in range(pre):
+        fills[i] += 1
+        done[i] += 1                              # read at once in this model
+    st, phase, filled = (0, 0, pre) if pre == S else (pre, 1, pre)
+    for _ in range(pre, total):
+        assert passes(st, phase)
+        if fills[st]:                             # not before its last fill was read
+            done[st] -= 1
+            assert not passes(st, phase)
+            done[st] += 1
+        fills[st] += 1
+        done[st] += 1
+        filled = min(S, filled + 1)
+        st += 1
+        if st == S:
+            st, phase = 0, phase ^ 1
+    for i in range(filled):
+        at = st - (filled - i)
+        parity = phase if at < 0 else phase ^ 1
+        at %= S
+        assert passes(at, parity)
+        done[at] -= 1
+        assert not passes(at, parity)
+        done[at] += 1
+
+
+@pytest.mark.parametrize("tn", [16, 32, 48, 64, 96, 128])
+@pytest.mark.parametrize("mats", [1, 2])
+def test_few_row_exchange(tn, mats):
+    per_sm = 2 if tn <= 16 or (mats == 2 and tn <= 32) else 1
+    stage = mats * 16384 + tn * 128
+    scales = mats * tn * 4 * 4
+    room = (113 if per_sm == 2 else 225) * 1024 - 1024 - 1024 - 2 * scales
+    stages = min(8, room // stage)
+    smem = 1024 + 1024 + 2 * scales + stages * stage
+    assert stages >= 3 and smem <= 227 * 1024 and per_sm * (smem + 1024) <= 228 * 1024
+    assert stage % 1024 == 0                       # every tile of a stage on the swizzle's 1024 bytes
+    half_tokens = tn // 2
+    for ks in range(1, 9):
+        share = ceil_div(tn, ks)
+        assert ks * mats * share * 128 * 4 <= stages * stage
+        seen = {}
+        for rank in range(ks):
+            for half in (0, 1):
+                owner, tok = divmod(half * half_tokens, share)
+                for i in range(half_tokens):
+                    for d in range(mats):
+                        at = rank * mats * share + tok + d * share
+                        assert owner < ks and at < ks * mats * share and (owner, at) not in seen
+                        seen[owner, at] = (rank, d, half * half_tokens + i)
+                    tok += 1
+                    if tok == share:
+                        owner, tok = owner + 1, 0
+        for r in range(ks):                        # the reader's indexes
+            for t in range(max(0, min(share, tn - r * share))):
+                for s in range(ks):
+                    for d in range(mats):
+                        assert seen[r, (s * mats + d) * share + t] == (s, d, r * share + t)

@@ -399,3 +399,17 @@ def test_buffers_used_again_by_the_next_step(M):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ys, want))
+
+
+@pytest.mark.parametrize("K", [128, 130, 1000, 2567])
+def test_one_row_needs_no_stride(K):
+    """A single row has no row stride to be a multiple of anything."""
+    pad = -K % 16
+    a, sa = activations(1, K, seed=K)
+    (g, sg), (u, su) = weight(200, K, seed=1), weight(200, K, seed=2)
+    g, u = (strided(t.view(torch.uint8), pad).view(F8) for t in (g, u))
+    check_matmul(a, sa, g, sg)
+    assert mb.last_variant() == 16
+    check_glu(a, sa, g, sg, u, su, True)
+    assert mb.last_variant() == 16
+    check_glu(a.expand(1, K), sa, g, sg, u, su, False)

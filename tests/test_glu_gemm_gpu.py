@@ -322,6 +322,8 @@ def test_same_tensor_twice_and_broadcast_rows():
     with pytest.raises(mb.MbgluError):
         mb.glu_gemm(h[:1].expand(130, 96), gw, gw)            # rows of stride 0
     with pytest.raises(mb.MbgluError):
+        mb.DualWeightGlu.apply(h[:1].clone().requires_grad_(True).expand(130, 96), gw, gw)
+    with pytest.raises(mb.MbgluError):
         mb.glu_gemm(h, gw, gw, out=h[:, :96])                 # in place
     with pytest.raises(ValueError):
         mb.glu_gemm(h.t(), gw[:, :1].expand(96, 130), gw[:, :1].expand(96, 130))
