@@ -102,60 +102,130 @@ __device__ __forceinline__ void st_global_32B(void *p, const uint32_t *w)
                  : "memory");
 }
 
-// 32 bf16 values (16 words, two per word) of one row to p[0..31], of which the
-// first `valid` exist.  align: 2 when the row is 32-byte aligned, 1 when 16.
-// A thread owns a row, so a warp's stores of one word each touch 32 rows: the
-// 32-byte form writes whole sectors.
-__device__ __forceinline__ void store_bf16_32(uint16_t *p, const uint32_t (&w)[16], int valid, int align)
+// ---- a warp's 32 rows x 32 columns, a thread per row ------------------------------
+//
+// Rows that lie on 16 bytes move by their own threads: a store of one word each
+// touches 32 rows, the 32-byte form writes whole sectors.  Others -- an odd row
+// length, the last columns -- go through `buf` (shared memory, kRowBuf words per
+// warp), a row at a time with consecutive columns in consecutive lanes: 32 two-byte
+// stores to 32 rows each took 869 x 12359 outputs 123 us, this way 29.
+//
+// p: the warp's first row, first column; rows: how many of the 32 exist (may be 0
+// or less); valid: columns (1 or more); align: 2 where every row lies on 32 bytes, 1
+// on 16.  The whole warp calls.
+constexpr int kRowBuf = 32 * 17;
+
+__device__ __forceinline__ void warp_store_bf16(uint32_t *buf, uint16_t *p, int64_t ld, const uint32_t (&w)[16], int rows,
+                                                int valid, int align)
 {
-    if (valid >= 32 && align == 2) {
-        st_global_32B(p, &w[0]);
-        st_global_32B(p + 16, &w[8]);
-    } else if (valid >= 32 && align == 1) {
+    const int lane = threadIdx.x & 31;
+    if (align > 0 && valid >= 32) {
+        if (lane >= rows) return;
+        uint16_t *q = p + lane * ld;
+        if (align == 2) {
+            st_global_32B(q, &w[0]);
+            st_global_32B(q + 16, &w[8]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else {
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4 *>(q)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < valid) p[i] = static_cast<uint16_t>(w[i >> 1] >> ((i & 1) * 16));
+    for (int i = 0; i < 16; ++i) buf[lane * 17 + i] = w[i];
+    __syncwarp();
+    const int n = min(rows, 32);
+#pragma unroll 4
+    for (int r = 0; r < n; ++r)
+        if (lane < valid) p[r * ld + lane] = static_cast<uint16_t>(buf[r * 17 + (lane >> 1)] >> ((lane & 1) * 16));
+    __syncwarp();
+}
+
+__device__ __forceinline__ void warp_store_f32(uint32_t *buf, float *p, int64_t ld, const uint32_t (&v)[32], int rows, int valid,
+                                               int align)
+{
+    const int lane = threadIdx.x & 31;
+    if (align > 0 && valid >= 32) {
+        if (lane >= rows) return;
+        float *q = p + lane * ld;
+        if (align == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_32B(q + 8 * i, &v[8 * i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4 *>(q)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        return;
+    }
+    const int n = min(rows, 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // 16 columns at a time, two rows per store
+#pragma unroll
+        for (int i = 0; i < 16; ++i) buf[lane * 17 + i] = v[16 * h + i];
+        __syncwarp();
+        const int c = lane & 15;
+#pragma unroll 4
+        for (int r = lane >> 4; r < n; r += 2)
+            if (16 * h + c < valid) p[r * ld + 16 * h + c] = __uint_as_float(buf[r * 17 + c]);
+        __syncwarp();
     }
 }
 
-// 32 fp32 values of one row; align as above
-__device__ __forceinline__ void store_f32_32(float *p, const float (&v)[32], int valid, int align)
+__device__ __forceinline__ void warp_store_e4m3(uint32_t *buf, uint8_t *p, int64_t ld, const uint32_t (&w)[8], int rows, int valid,
+                                                int align)
 {
-    if (valid >= 32 && align == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st_global_32B(p + 8 * i, reinterpret_cast<const uint32_t *>(&v[8 * i]));
-    } else if (valid >= 32 && align == 1) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < valid) p[i] = v[i];
+    const int lane = threadIdx.x & 31;
+    if (align > 0 && valid >= 32) {
+        if (lane >= rows) return;
+        uint8_t *q = p + lane * ld;
+        if (align == 2) {
+            st_global_32B(q, w);
+        } else {
+            reinterpret_cast<uint4 *>(q)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4 *>(q)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) buf[lane * 9 + i] = w[i];
+    __syncwarp();
+    const int n = min(rows, 32);
+#pragma unroll 4
+    for (int r = 0; r < n; ++r)
+        if (lane < valid) p[r * ld + lane] = static_cast<uint8_t>(buf[r * 9 + (lane >> 2)] >> ((lane & 3) * 8));
+    __syncwarp();
 }
 
-// 32 bf16 values of one row into floats; missing ones (past valid) are 0
-__device__ __forceinline__ void load_bf16_32(const uint16_t *p, float (&v)[32], int valid, int align)
+// This thread's row as floats; what does not exist is 0.
+__device__ __forceinline__ void warp_load_bf16(uint32_t *buf, const uint16_t *p, int64_t ld, float (&v)[32], int rows, int valid,
+                                               int align)
 {
-    if (valid >= 32 && align >= 1) {
+    const int lane = threadIdx.x & 31;
+    uint32_t w[16];
+    if (align > 0 && valid >= 32) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[8 * i + 2 * j] = bf16_to_f32(static_cast<uint16_t>(w[j]));
-                v[8 * i + 2 * j + 1] = bf16_to_f32(static_cast<uint16_t>(w[j] >> 16));
-            }
+            const uint4 q = lane < rows ? reinterpret_cast<const uint4 *>(p + lane * ld)[i] : make_uint4(0, 0, 0, 0);
+            w[4 * i] = q.x;
+            w[4 * i + 1] = q.y;
+            w[4 * i + 2] = q.z;
+            w[4 * i + 3] = q.w;
         }
     } else {
+        uint16_t *half = reinterpret_cast<uint16_t *>(buf);   // rows of 34
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) half[r * 34 + lane] = r < rows && lane < valid ? p[r * ld + lane] : static_cast<uint16_t>(0);
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < valid ? bf16_to_f32(p[i]) : 0.0f;
+        for (int i = 0; i < 16; ++i) w[i] = buf[lane * 17 + i];
+        __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
     }
 }
 

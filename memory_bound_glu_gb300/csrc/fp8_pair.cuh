@@ -42,21 +42,6 @@ struct Fp8PairParams {
     float *part;
 };
 
-// 32 e4m3 values (8 words) of one row
-__device__ __forceinline__ void store_e4m3_32(uint8_t *p, const uint32_t (&w)[8], int valid, int align)
-{
-    if (valid >= 32 && align == 2) {
-        st_global_32B(p, w);
-    } else if (valid >= 32 && align == 1) {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < valid) p[i] = static_cast<uint8_t>(w[i >> 2] >> ((i & 3) * 8));
-    }
-}
-
 // The scales of 8 blocks at a time, staged by an otherwise idle warp: a thread's
 // own row of a's scales is one line per lane and load, which costs the epilogue
 // 32 cache accesses per warp and block (4096 x 4864 x 11008: 238 us against
@@ -103,7 +88,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
     const PairShared s = pair_shared(pair_raw);
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    ScaleStage *scales = reinterpret_cast<ScaleStage *>(s.stages + kPairStages * kPairStage);
+    ScaleStage *scales = reinterpret_cast<ScaleStage *>(s.row_bufs + kPairRowBufs / 4);
     uint64_t *scale_full = reinterpret_cast<uint64_t *>(s.slot + 2), *scale_empty = scale_full + 2;
     if (threadIdx.x == 32) {
         for (int i = 0; i < 2; ++i) {
@@ -224,8 +209,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
             int again = t;
             asm volatile("" : "+r"(again));
             const PairTileAt x = pair_tile(p.plan, again);
-            const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32 + lane;
-            const bool row = m < p.plan.rows;
+            const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32;   // the warp's first row
+            const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.plan.rows - m));
+            uint32_t *buf32 = s.row_bufs + (warp - kPairEpilogue) * kRowBuf;
             float2 acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = unpack_f32x2(sums[i]);
@@ -233,20 +219,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int n = x.ni * kPairTile + col0 + 32 * j, valid = p.plan.cols - n;
-                    if (!ok || !row || valid <= 0) continue;
+                    if (!ok || rows <= 0 || valid <= 0) continue;   // the whole warp
                     if (x.slot >= 0) {
-                        float f[32];
+                        uint32_t f[32];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            f[2 * i] = acc[16 * j + i].x;
-                            f[2 * i + 1] = acc[16 * j + i].y;
+                            f[2 * i] = __float_as_uint(acc[16 * j + i].x);
+                            f[2 * i + 1] = __float_as_uint(acc[16 * j + i].y);
                         }
-                        store_f32_32(p.part + x.slot * kPairSlot + (rank * 128 + q * 32 + lane) * kPairTile + col0 + 32 * j, f, 32, 2);
+                        warp_store_f32(buf32, p.part + x.slot * kPairSlot + (rank * 128 + q * 32) * kPairTile + col0 + 32 * j, kPairTile, f,
+                                       rows, 32, 2);
                     } else {
                         uint32_t w[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(acc[16 * j + i].x, acc[16 * j + i].y);
-                        store_bf16_32(p.out + m * p.ldo + n, w, valid, p.out_align);
+                        warp_store_bf16(buf32, p.out + m * p.ldo + n, p.ldo, w, rows, valid, p.out_align);
                     }
                 }
             } else {
@@ -273,12 +260,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
                     amax = max_nan(amax, ex[(half ^ 1) * 128 + q * 32 + lane]);
                     scale = group_scale(amax);
                     inv = 1.0f / scale;
-                    if (ok && row && half == 0) p.qs[m * p.ldqs + x.ni] = scale;
+                    if (ok && lane < rows && half == 0) p.qs[(m + lane) * p.ldqs + x.ni] = scale;
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int n = n0 + 32 * j, valid = p.plan.cols - n;
-                    if (!ok || !row || valid <= 0) continue;
+                    if (!ok || rows <= 0 || valid <= 0) continue;   // the whole warp
                     if constexpr (EPI == kFp8GluQuant) {
                         uint32_t w[8];
 #pragma unroll
@@ -286,12 +273,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const Fp8Pair
                             const float2 a = acc[16 * j + 2 * i], b = acc[16 * j + 2 * i + 1];
                             w[i] = pack_e4m3x4(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
                         }
-                        store_e4m3_32(p.q + m * p.ldq + n, w, valid, p.q_align);
+                        warp_store_e4m3(buf32, p.q + m * p.ldq + n, p.ldq, w, rows, valid, p.q_align);
                     } else {
                         uint32_t w[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(acc[16 * j + i].x, acc[16 * j + i].y);
-                        store_bf16_32(p.out + m * p.ldo + n, w, valid, p.out_align);
+                        warp_store_bf16(buf32, p.out + m * p.ldo + n, p.ldo, w, rows, valid, p.out_align);
                     }
                 }
             }

@@ -37,7 +37,8 @@ constexpr uint32_t kPairOperand = 16384;                   // one operand's byte
 constexpr uint32_t kPairStage = 2 * kPairOperand;
 constexpr uint32_t kPairHeader = 4096;                     // barriers, tensor-memory address, the epilogue's exchange
 constexpr uint32_t kPairExchange = 1024;                   // offset of the exchange within the header
-constexpr uint32_t kPairSmem = kPairHeader + kPairStages * kPairStage + 1024;   // + alignment
+constexpr uint32_t kPairRowBufs = 8 * kRowBuf * 4;         // the epilogue warps' buffers for unaligned rows
+constexpr uint32_t kPairSmem = kPairHeader + kPairStages * kPairStage + kPairRowBufs + 1024;   // + alignment
 constexpr uint32_t kPairCols = 512;
 
 // How a tile's operands are chosen.
@@ -103,6 +104,7 @@ struct PairShared {
     uint64_t *full, *empty, *acc_full, *acc_empty;
     uint32_t *slot;
     unsigned char *stages;
+    uint32_t *row_bufs;
     float *exchange;
 };
 
@@ -117,6 +119,7 @@ __device__ __forceinline__ PairShared pair_shared(unsigned char *raw)
     s.slot = reinterpret_cast<uint32_t *>(s.acc_empty + 2);
     s.exchange = reinterpret_cast<float *>(base + kPairExchange);
     s.stages = base + kPairHeader;
+    s.row_bufs = reinterpret_cast<uint32_t *>(s.stages + kPairStages * kPairStage);
     return s;
 }
 
@@ -305,8 +308,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
         for (int t = static_cast<int>(blockIdx.x >> 1); t < p.plan.ntiles; t += static_cast<int>(gridDim.x >> 1), ++v) {
             const PairTileAt x = pair_tile(p.plan, t);
             const int buf = static_cast<int>(v & 1);
-            const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32 + lane;
-            const bool row = m < p.plan.rows;
+            const int64_t m = static_cast<int64_t>(x.mi) * kPairTile + rank * 128 + q * 32;   // the warp's first row
+            const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.plan.rows - m));
+            uint32_t *buf32 = s.row_bufs + (warp - kPairEpilogue) * kRowBuf;
             if (ok) ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], (v >> 1) & 1, kWaitLimitNs));
             tc_fence_after();
             const uint32_t acc = lanes + static_cast<uint32_t>(buf) * kPairTile;
@@ -319,14 +323,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
                     tmem_ld32(acc + static_cast<uint32_t>(c), g);
                     tmem_ld32(acc + 128u + static_cast<uint32_t>(c), u);
                     float d[32];
-                    if (EPI == kPairGrad && row && valid > 0) load_bf16_32(p.dout + m * p.ldd + n, d, valid, p.dout_align);
+                    if (EPI == kPairGrad && rows > 0 && valid > 0) warp_load_bf16(buf32, p.dout + m * p.ldd + n, p.ldd, d, rows, valid, p.dout_align);
                     tmem_wait_ld(g, u);
                     if (j == 1) {   // the buffer is read
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
                     }
-                    if (!ok || !row || valid <= 0) continue;
+                    if (!ok || rows <= 0 || valid <= 0) continue;   // the whole warp
                     uint32_t w[16], w2[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -344,16 +348,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
                             w[i] = glu_hf_short(g0, u0) | (glu_hf_short(g1, u1) << 16);
                         }
                     }
-                    store_bf16_32(p.out[0] + m * p.ldo[0] + n, w, valid, p.out_align[0]);
-                    if (EPI == kPairGrad) store_bf16_32(p.out[1] + m * p.ldo[1] + n, w2, valid, p.out_align[1]);
+                    warp_store_bf16(buf32, p.out[0] + m * p.ldo[0] + n, p.ldo[0], w, rows, valid, p.out_align[0]);
+                    if (EPI == kPairGrad) warp_store_bf16(buf32, p.out[1] + m * p.ldo[1] + n, p.ldo[1], w2, rows, valid, p.out_align[1]);
                     if (EPI == kPairGlu && p.gu) {
-                        float f[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(g[i]);
-                        store_f32_32(p.gu + m * p.ldgu + n, f, valid, p.gu_align);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(u[i]);
-                        store_f32_32(p.gu + m * p.ldgu + p.plan.cols + n, f, valid, p.gu_align_u);
+                        warp_store_f32(buf32, p.gu + m * p.ldgu + n, p.ldgu, g, rows, valid, p.gu_align);
+                        warp_store_f32(buf32, p.gu + m * p.ldgu + p.plan.cols + n, p.ldgu, u, rows, valid, p.gu_align_u);
                     }
                 }
             } else {
@@ -369,19 +368,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_gemm_kernel(const PairPa
                         __syncwarp();
                         if (lane == 0) pair_arrive(map_to_rank(&s.acc_empty[buf], 0));
                     }
-                    if (!ok || !row || valid <= 0) continue;
+                    if (!ok || rows <= 0 || valid <= 0) continue;   // the whole warp
                     if (x.slot >= 0) {
-                        float f[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-                        store_f32_32(p.part + x.slot * kPairSlot + (rank * 128 + q * 32 + lane) * kPairTile + c, f, 32, 2);
+                        warp_store_f32(buf32, p.part + x.slot * kPairSlot + (rank * 128 + q * 32) * kPairTile + c, kPairTile, r, rows, 32, 2);
                     } else {
                         uint32_t w[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
                         const int o = MODE == kPairStack ? x.o : 0;
-                        store_bf16_32(p.out[o] + m * p.ldo[o] + n, w, valid, p.out_align[o]);
+                        warp_store_bf16(buf32, p.out[o] + m * p.ldo[o] + n, p.ldo[o], w, rows, valid, p.out_align[o]);
                     }
                 }
             }
