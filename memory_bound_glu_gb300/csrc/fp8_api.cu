@@ -194,8 +194,8 @@ bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams
 
 // Rows up to which the tall kernel is taken (chained, cold L2; against CTA pairs).
 // One weight: 13.5 and 20.0 us at M = 128, 18.6 and 20.8 at 256 (K = 9728, N = 2560);
-// 16.4 and 23.5, 25.9 and 24.4 (K = 11008, N = 4096).  Two: 15.3 and 17.4 at M = 48, 21.4
-// and 17.2 at 96 (K = 2560, N = 9728); 30.1 and 35.4 at 64 (K = 4096, N = 11008).
+// 16.4 and 23.5, 25.9 and 24.4 (K = 11008, N = 4096).  Two: 15.9 and 17.2 at M = 64, 21.4
+// and 17.2 at 96 (K = 2560, N = 9728); 27.0 and 35.4 at 64 (K = 4096, N = 11008).
 constexpr int kTallMatmul = 128, kTallGlu = 64;
 
 mbglu::PairPlan matmul_plan(int M, int N, int K)

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
     uint64_t *empty = full + kTallMaxStages, *acc_full = empty + kTallMaxStages, *acc_empty = acc_full + 2;
     uint64_t *scale_full = acc_empty + 2, *scale_empty = scale_full + 2;
     uint32_t *slot = reinterpret_cast<uint32_t *>(scale_empty + 2);
-    float *peaks = reinterpret_cast<float *>(base + 512);   // 2 x 8 warps x 4 tokens
+    float *peaks = reinterpret_cast<float *>(base + 512);   // 2 x 8 warps x 8 tokens
     unsigned char *stages = base + kTallHeader;
     float *scales = reinterpret_cast<float *>(stages + kStages * Shape::kStage);
     constexpr int kScaleFloats = Shape::kScales / 4;
@@ -376,24 +376,31 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
         }
         if (ks > 1) cluster_sync();
         else __syncthreads();
-        // this block's tokens: warps 4-7 and 8-11 take groups of four in turn (four
-        // chains of loads, SiLUs and shuffles at once), a thread one weight row
-        constexpr int kGroup = 4;
+        // this block's tokens: warps 4-7 and 8-11 take groups of kGroup in turn (as many
+        // chains of loads, SiLUs and shuffles at once), a thread one weight row.  A tile
+        // of few tokens has small groups: code that runs once is bound by its fetching
+        // (one weight of K = 9728, N = 2560 at M = 8: 7.0 us with groups of one, 7.6 of
+        // four; two of K = 4096, N = 11008 at M = 64: 27.0 with eight, 29.8 with four).
+        constexpr int kGroup = TN <= 16 ? (OUT == 0 ? 1 : 2) : TN <= 32 && OUT == 0 ? 4 : 8;
         const int n = wt * kTallRows + row;
         const int first = rank * share, count = min(min(share, TN - first), p.M - m0 - first);
         for (int g0 = 0; g0 < count; g0 += 2 * kGroup) {   // both halves run the same rounds: there is a barrier
             const int t0 = g0 + half * kGroup;
-            float val[kGroup];
+            float val[kGroup], up[kGroup];
 #pragma unroll
-            for (int u = 0; u < kGroup; ++u) {
-                float x = 0.0f, y = 0.0f;
-                if (t0 + u < count) {
-                    for (int s = 0; s < ks; ++s) {
-                        x += totals[(s * kMats * share + t0 + u) * kTallRows + row];
-                        if (kDual) y += totals[((s * kMats + 1) * share + t0 + u) * kTallRows + row];
-                    }
+            for (int u = 0; u < kGroup; ++u) val[u] = up[u] = 0.0f;
+            const float *from = totals + t0 * kTallRows + row;
+            for (int s = 0; s < ks; ++s, from += kMats * share * kTallRows) {
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {
+                    if (t0 + u >= count) break;
+                    val[u] += from[u * kTallRows];
+                    if (kDual) up[u] += from[(share + u) * kTallRows];
                 }
-                val[u] = kDual ? silu_short(x) * y : x;
+            }
+            if (kDual) {
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) val[u] = silu_short(val[u]) * up[u];
             }
             const int64_t m = m0 + first + t0;
             if constexpr (OUT == 2) {
@@ -406,7 +413,10 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
                     for (int u = 0; u < kGroup; ++u) amax[u] = max_nan(amax[u], __shfl_xor_sync(0xffffffffu, amax[u], o));
                 // the four warps of a half hold the group; two sets of places, used in turn
                 float *pk = peaks + ((g0 / (2 * kGroup)) & 1) * 8 * kGroup + half * 4 * kGroup;
-                if (lane == 0) *reinterpret_cast<float4 *>(pk + q * kGroup) = make_float4(amax[0], amax[1], amax[2], amax[3]);
+                if (lane == 0) {
+#pragma unroll
+                    for (int u = 0; u < kGroup; ++u) pk[q * kGroup + u] = amax[u];
+                }
                 bar_sync_named(1, 256);
 #pragma unroll
                 for (int u = 0; u < kGroup; ++u) {
