@@ -99,34 +99,90 @@ mbglu_status launch_pair(const mbglu::Fp8PairParams &p, const mbglu::PairMaps &m
     return st;
 }
 
-// ---- up to some dozens of rows: fp8_tall_kernel -------------------------------------------
+// ---- few rows, or few tiles: fp8_tall_kernel ----------------------------------------------
 
 // Clusters of ks blocks, each with an SM of its own, that the part holds at once
 // (tall_per_sm: some have two per SM).
 constexpr int kClusters[mbglu::kTallMaxSplit + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 
+constexpr int kTallTokens[] = {16, 32, 48, 64, 80, 96, 112, 128};   // two weights: up to 48
+
+// Which kernel, tokens per block (tn) and ranges of the inner dimension (ks): what
+// makes the estimate of a call's time in a chain of calls least.  From the sizes
+// alone, so that the order of a sum does not depend on the device.  The constants
+// (ns) are fitted to 2,500 measured combinations of tn and ks, 16 to 768 rows, six
+// shapes of one weight and five of two.  There the choice is within 1% of the fastest
+// combination on average and 10% at worst, and so it is at eleven other shapes of 333
+// to 4096 rows.  It is faster by 20% (one weight) and 17% (two) on average than the
+// least tn that holds all rows, up to 128 (two weights: 64), and CTA pairs beyond; slower
+// by 2% or more at three points: two weights of K = 4096, N = 11008 and 48 and 64 rows
+// (26.6 and 30.2 us against 26.0 and 28.1), K = 2048, N = 4096 and 16 rows (7.2 and 6.8).
+struct TallCost {
+    int64_t start, stage, stage_col, col, round, paired, rank, block;
+};
+struct PairCost {
+    int64_t start, stage, stage_full, join, join_slot;
+};
+constexpr TallCost kTallCost[2] = {{500, 210, 1, 50, 300, 350, 75, 1100}, {1000, 290, 2, 57, 0, 2500, 276, 820}};
+constexpr PairCost kPairCost[2] = {{5300, 360, 130, 1800, 95}, {6600, 330, 160, 0, 0}};
+
 struct TallPlan {
     int tn, ks;
+    int64_t ns;
 };
 
-// Tokens per block: the least of 16, 32, 48, 64, 96 and 128 that holds all, else
-// 128.  Ranges of the inner dimension: what makes rounds x (stages of a range +
-// what a round costs beside them, about 16 stages' time) least.
 TallPlan tall_plan(int M, int N, int K, bool dual)
 {
-    TallPlan t = {M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : M <= 64 ? 64 : M <= 96 ? 96 : 128, 1};
-    const int64_t units = static_cast<int64_t>(ceil_div(N, mbglu::kTallRows)) * ceil_div(M, t.tn);
+    const TallCost &c = kTallCost[dual];
+    const int64_t wtiles = ceil_div(N, mbglu::kTallRows);
     const int chunks = ceil_div(K, kBlk);
-    int64_t best = 0;
-    for (int ks = 1; ks <= std::min(mbglu::kTallMaxSplit, chunks); ++ks) {
-        const int places = kClusters[ks] * mbglu::tall_per_sm(t.tn, dual);
-        const int64_t cost = (units + places - 1) / places * (ceil_div(chunks, ks) + 16);
-        if (ks == 1 || cost < best) {
-            best = cost;
-            t.ks = ks;
+    TallPlan t = {};
+    for (const int tn : kTallTokens) {
+        if (dual && tn > 48) break;   // would hardly ever be the least
+        const int64_t units = wtiles * ceil_div(M, tn), cols = (dual ? 2 : 1) * tn;
+        const int per_sm = mbglu::tall_per_sm(tn, dual);
+        for (int ks = 1; ks <= std::min(mbglu::kTallMaxSplit, chunks); ++ks) {
+            const int places = kClusters[ks] * per_sm;
+            const int64_t round = ceil_div(chunks, ks) * (c.stage + c.stage_col * cols) + c.col * cols + c.round +
+                                  (per_sm == 2 ? c.paired : 0);
+            const int64_t ns = c.start + (units + places - 1) / places * round + c.rank * ks + c.block * units * ks / (2 * kPairs);
+            if (t.tn == 0 || ns < t.ns) t = {tn, ks, ns};
         }
+        if (tn >= M) break;   // wider tiles would only be emptier
     }
     return t;
+}
+
+int64_t pair_ns(const mbglu::PairPlan &p, bool dual)
+{
+    const PairCost &c = kPairCost[dual];
+    const int64_t stages = static_cast<int64_t>(ceil_div(p.whole, kPairs)) * p.nchunk + (p.rest ? ceil_div(p.nchunk, p.splits) : 0);
+    return c.start + stages * (c.stage + c.stage_full * std::min(p.ntiles, kPairs) / kPairs) +
+           (p.rest ? c.join + c.join_slot * p.rest * p.splits : 0);
+}
+
+// One weight: every stage is of a[0] and b[0], the only maps that are filled in.
+mbglu::PairPlan fp8_pair_plan(int M, int N, int K, bool dual, bool may_split)
+{
+    const int chunks = ceil_div(K, kBlk);
+    return pair_plan(M, N, dual ? 128 : 256, 1, chunks, chunks, may_split);
+}
+
+struct Fp8Plan {
+    TallPlan tall;
+    mbglu::PairPlan pair;
+    bool use_tall;
+};
+
+Fp8Plan fp8_plan(int M, int N, int K, bool dual)
+{
+    Fp8Plan f = {};
+    f.pair = fp8_pair_plan(M, N, K, dual, !dual);
+    if (K > 0) {
+        f.tall = tall_plan(M, N, K, dual);
+        f.use_tall = f.tall.ns < pair_ns(f.pair, dual);
+    }
+    return f;
 }
 
 template <int TN, int OUT>
@@ -141,9 +197,10 @@ cudaError_t setup_tall()
     cudaError_t e = cudaSuccess;
 #define MBGLU_ALLOW(TN, OUT) \
     if (e == cudaSuccess) e = allow_tall<TN, OUT>();
-    MBGLU_ALLOW(16, 0) MBGLU_ALLOW(32, 0) MBGLU_ALLOW(48, 0) MBGLU_ALLOW(64, 0) MBGLU_ALLOW(96, 0) MBGLU_ALLOW(128, 0)
-    MBGLU_ALLOW(16, 1) MBGLU_ALLOW(32, 1) MBGLU_ALLOW(48, 1) MBGLU_ALLOW(64, 1) MBGLU_ALLOW(96, 1) MBGLU_ALLOW(128, 1)
-    MBGLU_ALLOW(16, 2) MBGLU_ALLOW(32, 2) MBGLU_ALLOW(48, 2) MBGLU_ALLOW(64, 2) MBGLU_ALLOW(96, 2) MBGLU_ALLOW(128, 2)
+    MBGLU_ALLOW(16, 0) MBGLU_ALLOW(32, 0) MBGLU_ALLOW(48, 0) MBGLU_ALLOW(64, 0)
+    MBGLU_ALLOW(80, 0) MBGLU_ALLOW(96, 0) MBGLU_ALLOW(112, 0) MBGLU_ALLOW(128, 0)
+    MBGLU_ALLOW(16, 1) MBGLU_ALLOW(32, 1) MBGLU_ALLOW(48, 1)
+    MBGLU_ALLOW(16, 2) MBGLU_ALLOW(32, 2) MBGLU_ALLOW(48, 2)
 #undef MBGLU_ALLOW
     return e;
 }
@@ -160,10 +217,9 @@ mbglu_status launch_tall(const TallPlan &t, const mbglu::TallParams &p, const mb
 
 // False where a tensor map is refused (nothing is launched).
 template <int OUT>
-bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams &p, int M, int N, int K, cudaStream_t stream,
-          mbglu_status *st)
+bool tall(const TallPlan &t, const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams &p, int M, int N, int K,
+          cudaStream_t stream, mbglu_status *st)
 {
-    const TallPlan t = tall_plan(M, N, K, OUT != 0);
     mbglu::TallMaps maps;
     if (!k_major(&maps.w[0], w0, K) || (w1 && !k_major(&maps.w[1], *w1, K)) || !k_major(&maps.x, a, K, t.tn))
         return false;
@@ -183,26 +239,23 @@ bool tall(const Scaled &a, const Scaled &w0, const Scaled *w1, mbglu::TallParams
         p.ws[1] = w1->s;
         p.ldws[1] = w1->lds;
     }
+    if constexpr (OUT == 0) {
+        if (t.tn > 48) {
+            *st = t.tn == 64    ? launch_tall<64, OUT>(t, p, maps, stream)
+                  : t.tn == 80  ? launch_tall<80, OUT>(t, p, maps, stream)
+                  : t.tn == 96  ? launch_tall<96, OUT>(t, p, maps, stream)
+                  : t.tn == 112 ? launch_tall<112, OUT>(t, p, maps, stream)
+                                : launch_tall<128, OUT>(t, p, maps, stream);
+            return true;
+        }
+    }
     *st = t.tn == 16   ? launch_tall<16, OUT>(t, p, maps, stream)
           : t.tn == 32 ? launch_tall<32, OUT>(t, p, maps, stream)
-          : t.tn == 48 ? launch_tall<48, OUT>(t, p, maps, stream)
-          : t.tn == 64 ? launch_tall<64, OUT>(t, p, maps, stream)
-          : t.tn == 96 ? launch_tall<96, OUT>(t, p, maps, stream)
-                       : launch_tall<128, OUT>(t, p, maps, stream);
+                       : launch_tall<48, OUT>(t, p, maps, stream);
     return true;
 }
 
-// Rows up to which the tall kernel is taken (chained, cold L2; against CTA pairs).
-// One weight: 13.5 and 20.0 us at M = 128, 18.6 and 20.8 at 256 (K = 9728, N = 2560);
-// 16.4 and 23.5, 25.9 and 24.4 (K = 11008, N = 4096).  Two: 15.9 and 17.2 at M = 64, 21.4
-// and 17.2 at 96 (K = 2560, N = 9728); 27.0 and 35.4 at 64 (K = 4096, N = 11008).
-constexpr int kTallMatmul = 128, kTallGlu = 64;
-
-mbglu::PairPlan matmul_plan(int M, int N, int K)
-{
-    const int chunks = ceil_div(K, kBlk);
-    return pair_plan(M, N, 256, 1, chunks, chunks, M > kTallMatmul);   // fewer rows have no workspace
-}
+size_t workspace_of(const Fp8Plan &f) { return f.use_tall ? 0 : static_cast<size_t>(part_bytes(f.pair)); }
 
 }  // namespace
 
@@ -276,7 +329,7 @@ mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw, uint8_t *q, i
 size_t matmul_fp8_workspace_bytes(int M, int N, int K)
 {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
-    return static_cast<size_t>(part_bytes(matmul_plan(M, N, K)));
+    return workspace_of(fp8_plan(M, N, K, false));
 }
 
 mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas, const uint8_t *w,
@@ -294,7 +347,8 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
     }
     if (ldo < N) return MBGLU_ERR_STRIDE;
     if (!aligned(out, 2)) return MBGLU_ERR_ALIGN;
-    const size_t need = matmul_fp8_workspace_bytes(M, N, K);
+    const Fp8Plan plan = fp8_plan(M, N, K, false);
+    const size_t need = workspace_of(plan);
     if (need && !workspace) return MBGLU_ERR_NULL;
     if (workspace_bytes < need) return MBGLU_ERR_SHAPE;
     if (need && !aligned(workspace, 256)) return MBGLU_ERR_ALIGN;
@@ -302,17 +356,18 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
     if (meets(out, ob, A, K) || meets(out, ob, W, K) || meets(workspace, wsb, A, K) || meets(workspace, wsb, W, K) ||
         overlaps(out, ob, workspace, wsb))
         return MBGLU_ERR_ALIAS;
-    if (K > 0 && M <= kTallMatmul) {
+    if (plan.use_tall) {
         mbglu::TallParams q = {};
         q.out = out;
         q.ldo = ldo;
         mbglu_status st;
-        if (tall<0>(A, W, nullptr, q, M, N, K, stream, &st)) return st;
+        if (tall<0>(plan.tall, A, W, nullptr, q, M, N, K, stream, &st)) return st;
     }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], W, K)) {
         mbglu::Fp8PairParams q = {};
-        q.plan = matmul_plan(M, N, K);
+        q.plan = plan.pair;
+        if (plan.use_tall) q.plan = fp8_pair_plan(M, N, K, false, false);   // there is no workspace
         q.as = a_scale;
         q.ldas = ldas;
         q.ws[0] = w_scale;
@@ -363,7 +418,8 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
     for (const Scaled *in : {&A, &G, &U})
         if (meets(o, ob, *in, K) || meets(q_scale, sb, *in, K)) return MBGLU_ERR_ALIAS;
     if (overlaps(o, ob, q_scale, sb)) return MBGLU_ERR_ALIAS;
-    if (K > 0 && M <= kTallGlu) {
+    const Fp8Plan plan = fp8_plan(M, N, K, true);
+    if (plan.use_tall) {
         mbglu::TallParams p = {};
         p.out = out;
         p.ldo = ldo;
@@ -372,12 +428,13 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
         p.qs = q_scale;
         p.ldqs = ldqs;
         mbglu_status st;
-        if (q ? tall<2>(A, G, &U, p, M, N, K, stream, &st) : tall<1>(A, G, &U, p, M, N, K, stream, &st)) return st;
+        if (q ? tall<2>(plan.tall, A, G, &U, p, M, N, K, stream, &st) : tall<1>(plan.tall, A, G, &U, p, M, N, K, stream, &st))
+            return st;
     }
     mbglu::PairMaps maps;
     if (K > 0 && k_major(&maps.a[0], A, K) && k_major(&maps.b[0], G, K) && k_major(&maps.b[1], U, K)) {
         mbglu::Fp8PairParams p = {};
-        p.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, kBlk), false);
+        p.plan = plan.pair;
         p.as = a_scale;
         p.ldas = ldas;
         p.ws[0] = gate_scale;

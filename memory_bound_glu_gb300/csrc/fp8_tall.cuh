@@ -1,8 +1,16 @@
 // fp8_tall.cuh -- the e4m3 products of a token up to some dozens of rows (a
-// decode step): too few to fill the 256-row side of a CTA pair's tile, bound by
-// the bytes of the weights.  The weights take the MMA's 128-row
-// side and the tokens its N, so that both the products and the reading of the
-// accumulators shrink with the batch and what is left is the weights' bytes.
+// decode step), and of any number of rows where the product has few tiles: too
+// few to fill the 256-row side of a CTA pair's tile, or the part with such tiles.
+// The weights take the MMA's 128-row side and the tokens its N, so that both the
+// products and the reading of the accumulators shrink with the batch and what is
+// left is the weights' bytes.
+//
+// More tokens than a tile holds are further tiles, which read the weights again,
+// from L2.  Narrow tiles on more SMs are often the faster ones all the same (one
+// weight of K = 4096, N = 1000 at M = 128: 6.1 us in tiles of 32 tokens, 8.9 in one
+// of 128; K = 9728, N = 2560 at M = 333: 21.5 us in tiles of 112 and two ranges, 24.4
+// on CTA pairs).  A stage of 128 tokens takes about 340 ns: 32 KB into every SM, 14.6
+// TB/s in all, so L2 bounds what is not bound by a call's start and end.
 //
 // A block holds 128 weight rows -- one scale block, and one group of an e4m3
 // output -- of one weight or of gate and up, TN tokens, and one of `ks` ranges
@@ -380,7 +388,7 @@ __global__ void __launch_bounds__(384, tall_per_sm(TN, OUT != 0)) fp8_tall_kerne
         // chains of loads, SiLUs and shuffles at once), a thread one weight row.  A tile
         // of few tokens has small groups: code that runs once is bound by its fetching
         // (one weight of K = 9728, N = 2560 at M = 8: 7.0 us with groups of one, 7.6 of
-        // four; two of K = 4096, N = 11008 at M = 64: 27.0 with eight, 29.8 with four).
+        // four; two of K = 4096, N = 11008 in tiles of 64 tokens: 27.0 with eight, 29.8 with four).
         constexpr int kGroup = TN <= 16 ? (OUT == 0 ? 1 : 2) : TN <= 32 && OUT == 0 ? 4 : 8;
         const int n = wt * kTallRows + row;
         const int first = rank * share, count = min(min(share, TN - first), p.M - m0 - first);

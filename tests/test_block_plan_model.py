@@ -112,7 +112,7 @@ def test_ring_phases(S, total, early):
         done[at] += 1
 
 
-@pytest.mark.parametrize("tn", [16, 32, 48, 64, 96, 128])
+@pytest.mark.parametrize("tn", [16, 32, 48, 64, 80, 96, 112, 128])
 @pytest.mark.parametrize("mats", [1, 2])
 def test_few_row_exchange(tn, mats):
     per_sm = 2 if tn <= 16 or (mats == 2 and tn <= 32) else 1
@@ -144,3 +144,62 @@ def test_few_row_exchange(tn, mats):
                 for s in range(ks):
                     for d in range(mats):
                         assert seen[r, (s * mats + d) * share + t] == (s, d, r * share + t)
+
+
+CLUSTERS = [0, 152, 76, 46, 36, 28, 23, 15, 15]
+TALL_COST = [(500, 210, 1, 50, 300, 350, 75, 1100), (1000, 290, 2, 57, 0, 2500, 276, 820)]
+PAIR_COST = [(5300, 360, 130, 1800, 95), (6600, 330, 160, 0, 0)]
+
+
+def tall_plan(M, N, K, dual):
+    start, stage, stage_col, col, rnd, paired, rank, block = TALL_COST[dual]
+    best = None
+    for tn in (16, 32, 48) if dual else (16, 32, 48, 64, 80, 96, 112, 128):
+        units, cols, chunks = ceil_div(N, 128) * ceil_div(M, tn), (1 + dual) * tn, ceil_div(K, 128)
+        per_sm = 2 if tn <= 16 or (dual and tn <= 32) else 1
+        for ks in range(1, min(8, chunks) + 1):
+            ns = start + ceil_div(units, CLUSTERS[ks] * per_sm) * (
+                ceil_div(chunks, ks) * (stage + stage_col * cols) + col * cols + rnd + (paired if per_sm == 2 else 0))
+            ns += rank * ks + block * units * ks // 152
+            if best is None or ns < best[0]:
+                best = ns, tn, ks
+        if tn >= M:
+            break
+    return best
+
+
+def fp8_plan(M, N, K, dual):
+    """("tall", tn, ks) or ("pair", plan)"""
+    p = pair_plan(M, N, 128 if dual else 256, 1, ceil_div(K, 128), not dual)
+    start, stage, full, join, join_slot = PAIR_COST[dual]
+    stages = ceil_div(p["whole"], PAIRS) * p["nchunk"] + (ceil_div(p["nchunk"], p["splits"]) if p["rest"] else 0)
+    ns = start + stages * (stage + full * min(p["ntiles"], PAIRS) // PAIRS)
+    if p["rest"]:
+        ns += join + join_slot * p["rest"] * p["splits"]
+    tall = tall_plan(M, N, K, dual)
+    return ("tall", *tall[1:]) if tall[0] < ns else ("pair", p)
+
+
+def test_the_library_plans_as_the_model():
+    """A product's workspace follows from its plan: none with the few-row kernel."""
+    import memory_bound_glu_gb300 as mb
+    seen = set()
+    for M in (1, 16, 17, 64, 129, 333, 448, 500, 768, 1024, 2100, 4096):
+        for N in (1, 300, 1000, 2000, 2560, 4096, 11008):
+            for K in (128, 2048, 8192, 9728, 11008):
+                kind, *rest = fp8_plan(M, N, K, 0)
+                want = rest[0]["rest"] * rest[0]["splits"] * TILE * TILE * 4 if kind == "pair" else 0
+                assert mb.matmul_fp8_workspace_bytes(M, N, K) == want, (M, N, K)
+                seen.add((kind, want > 0))
+    assert seen == {("tall", False), ("pair", False), ("pair", True)}
+
+
+@pytest.mark.parametrize("dual", [0, 1])
+def test_few_row_plans_are_launchable(dual):
+    for M in (1, 8, 17, 100, 333, 1000, 5000, 100000):
+        for N in (1, 128, 1000, 9728, 100000):
+            for K in (1, 128, 129, 1000, 4096, 100000):
+                ns, tn, ks = tall_plan(M, N, K, dual)
+                assert ns > 0 and 1 <= ks <= min(8, ceil_div(K, 128)) and tn % 16 == 0 and tn <= 128
+                c = ceil_div(K, 128)
+                assert all(c * r // ks < c * (r + 1) // ks for r in range(ks))   # no block without a stage

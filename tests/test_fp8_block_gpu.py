@@ -10,6 +10,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 BF = torch.bfloat16
 F8 = torch.float8_e4m3fn
+SPLIT = (500, 2560, 8192)   # M, N, K of a product whose inner dimension is split between CTA pairs
 
 
 def rand(*shape, seed=0, scale=1.0):
@@ -153,6 +154,42 @@ def test_glu_rows(M, quant):
     check_glu(*activations(M, 272, seed=M), *weight(200, 272, seed=1), *weight(200, 272, seed=2), quant)
 
 
+# several tiles of tokens: every width of the few-row kernel's tile, ranges of the inner
+# dimension, a last tile of one row
+@pytest.mark.parametrize("M,N,K", [(33, 300, 2048), (97, 300, 2048), (129, 1000, 4096), (161, 4096, 1040), (200, 2560, 4096),
+                                   (241, 2560, 2048), (333, 2560, 9728), (385, 1000, 4096), (512, 520, 2048), (769, 1000, 1040),
+                                   (410, 520, 2656), (193, 4096, 2512), (374, 4096, 1616), (369, 2560, 4112), (208, 200, 4064)])
+def test_tiles_of_tokens(M, N, K):
+    a, g = activations(M, K, seed=K), weight(N, K, seed=N)
+    check_matmul(*a, *g)
+    assert mb.last_variant() == 16
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 300, 4096), (97, 1000, 2560), (160, 1000, 2064), (65, 2300, 1040), (333, 300, 4096),
+                                   (513, 300, 4096), (769, 200, 2048), (49, 4100, 272),
+                                   (479, 1000, 3248), (68, 11008, 2048), (274, 300, 2304)])
+@pytest.mark.parametrize("quant", [False, True])
+def test_gated_tiles_of_tokens(M, N, K, quant):
+    a, g, u = activations(M, K, seed=K), weight(N, K, seed=N), weight(N, K, seed=N + 1)
+    check_glu(*a, *g, *u, quant)
+    assert mb.last_variant() == 16
+
+
+@pytest.mark.parametrize("M,N,K", [(777, 2056, 128), (1100, 1501, 272), (1537, 1000, 400), (2100, 520, 16), (257, 9000, 144),
+                                   (500, 2560, 8192), (1025, 2301, 8208)])
+def test_pairs(M, N, K):
+    check_matmul(*activations(M, K, seed=K), *weight(N, K, seed=N))
+    assert mb.last_variant() == 15
+
+
+@pytest.mark.parametrize("M,N,K", [(1100, 257, 400), (1500, 130, 128), (777, 392, 272), (513, 1000, 16), (300, 2100, 1040),
+                                   (256, 9000, 144), (4097, 1, 272)])
+@pytest.mark.parametrize("quant", [False, True])
+def test_gated_pairs(M, N, K, quant):
+    check_glu(*activations(M, K, seed=K), *weight(N, K, seed=N), *weight(N, K, seed=N + 1), quant)
+    assert mb.last_variant() == 15
+
+
 @pytest.mark.parametrize("M", [3, 20, 70])
 @pytest.mark.parametrize("N,K", [(1, 16), (8, 1), (15, 128), (16, 144), (127, 256), (128, 130), (129, 384), (640, 48), (257, 1040),
                                  (72, 4112), (1100, 112)])
@@ -163,7 +200,7 @@ def test_columns_and_inner_dimension(M, N, K):
     check_glu(*a, *g, *u, False)
 
 
-@pytest.mark.parametrize("M", [4, 40, 150])
+@pytest.mark.parametrize("M", [4, 40, 150, 12300])
 @pytest.mark.parametrize("pad,off", [(16, 0), (16, 16), (1, 0), (5, 3)])
 def test_operand_strides(M, pad, off):
     K, N = 288, 136
@@ -174,7 +211,7 @@ def test_operand_strides(M, pad, off):
     check_glu(a, sa, g, sg, u, su, True)
 
 
-@pytest.mark.parametrize("M", [5, 40, 150])
+@pytest.mark.parametrize("M", [5, 40, 150, 12300])
 @pytest.mark.parametrize("pad", [0, 1, 8, 24])
 def test_what_lies_behind_the_outputs(M, pad):
     K, N = 160, 200
@@ -203,7 +240,7 @@ def test_empty_and_zero(M):
     assert (q.float() == 0).all() and (s == 2.0 ** -126).all()
 
 
-@pytest.mark.parametrize("M", [3, 40, 150])
+@pytest.mark.parametrize("M", [3, 40, 150, 4100])
 def test_scales_of_many_sizes_and_nan(M):
     """Scales over 60 binades, one infinite activation group, one NaN weight value."""
     K, N = 400, 264
@@ -223,7 +260,7 @@ def test_scales_of_many_sizes_and_nan(M):
     assert out[1].isnan().all() and torch.equal(out[0], base[0]) and torch.equal(out[2:], base[2:])
 
 
-@pytest.mark.parametrize("M", [1, 8, 48, 130])
+@pytest.mark.parametrize("M", [1, 8, 48, 130, 4100])
 def test_decode_chain(M):
     """norm -> gate and up -> down, as a decode step runs them, each against its
     definition on the operands that the one before gave; then the chain once more
@@ -255,7 +292,8 @@ def test_decode_chain(M):
 
 
 def test_two_streams_with_their_own_workspaces():
-    M, N, K = 100, 256, 4096
+    M, N, K = SPLIT
+    assert mb.matmul_fp8_workspace_bytes(*SPLIT) > 0
     ops = [(*activations(M, K, seed=i), *weight(N, K, seed=i)) for i in (1, 2)]
     want = [mb.matmul_fp8(*o) for o in ops]
     streams = [torch.cuda.Stream() for _ in ops]
@@ -293,12 +331,13 @@ def test_weight_quantised_right_before_its_use():
 
 
 def test_given_outputs_workspace_and_stream():
-    a, w, u = activations(150, 4096), weight(300, 4096, seed=1), weight(300, 4096, seed=2)
+    M, N, K = SPLIT
+    a, w, u = activations(M, K), weight(N, K, seed=1), weight(N, K, seed=2)
     want, (wq, ws) = mb.matmul_fp8(*a, *w), mb.glu_fp8(*a, *w, *u, out_dtype=F8)
-    need = mb.matmul_fp8_workspace_bytes(150, 300, 4096)
+    need = mb.matmul_fp8_workspace_bytes(M, N, K)
     assert need > 0
-    out = torch.zeros(150, 300, dtype=BF, device=DEV)
-    q, s = torch.zeros(150, 300, device=DEV).to(F8), torch.zeros(150, 3, device=DEV)
+    out = torch.zeros(M, N, dtype=BF, device=DEV)
+    q, s = torch.zeros(M, N, device=DEV).to(F8), torch.zeros(M, N // 128, device=DEV)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     ws1 = torch.empty(need, dtype=torch.uint8, device=DEV)
@@ -316,12 +355,12 @@ def test_given_outputs_workspace_and_stream():
     with pytest.raises((TypeError, ValueError)):
         mb.matmul_fp8(a[0], a[1][:, :1], *w)
     with pytest.raises((TypeError, ValueError)):
-        mb.add_rmsnorm_fp8(out, out, torch.zeros(299, dtype=BF, device=DEV), 1e-6)
+        mb.add_rmsnorm_fp8(out, out, torch.zeros(N - 1, dtype=BF, device=DEV), 1e-6)
 
 
 def test_launch_policies_agree():
     old = mb.get_launch_policy()
-    ops = [(activations(m, 1024, seed=m), weight(400, 1024, seed=1), weight(400, 1024, seed=2)) for m in (3, 70, 200)]
+    ops = [(activations(m, 1024, seed=m), weight(400, 1024, seed=1), weight(400, 1024, seed=2)) for m in (3, 70, 200, 4100)]
     try:
         got = []
         for policy in (mb.POLICY_SERIAL, mb.POLICY_PDL, mb.POLICY_PREFETCH):
@@ -336,7 +375,8 @@ def test_launch_policies_agree():
 
 def test_captured_calls_of_two_graphs_share_nothing():
     """Two graphs with calls that need workspaces, replayed at the same time."""
-    ops = [(*activations(140, 4096, seed=i), *weight(300, 4096, seed=i)) for i in (1, 2)]
+    M, N, K = SPLIT
+    ops = [(*activations(M, K, seed=i), *weight(N, K, seed=i)) for i in (1, 2)]
     want = [mb.matmul_fp8(*o) for o in ops]
     graphs, outs = [], []
     for o in ops:
@@ -356,7 +396,7 @@ def test_captured_calls_of_two_graphs_share_nothing():
         assert all(torch.equal(x, y) for x, y in zip(outs, want))
 
 
-@pytest.mark.parametrize("M", [1, 40, 150])
+@pytest.mark.parametrize("M", [1, 40, 150, 4100])
 def test_buffers_used_again_by_the_next_step(M):
     """Steps back to back through the same q and scale buffers, each on other values:
     every kernel sees what the one before it wrote, not what an earlier one did."""
