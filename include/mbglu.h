@@ -357,7 +357,8 @@ mbglu_status gdn_gates(const mbglu_bf16 *a, int64_t lda, const mbglu_bf16 *b, in
  * that are multiples of 8 elements; other operands take a slower kernel.  Up
  * to MBGLU_MAX_M rows without gu the call is glu_gemv.
  * Errors as glu_gemv without the limit on M; also MBGLU_ERR_SHAPE for 2N
- * beyond INT32_MAX, MBGLU_ERR_ALIGN for gu not 4-byte aligned and
+ * beyond INT32_MAX and M or K beyond INT32_MAX - 511 (here and in the functions
+ * below, for every size), MBGLU_ERR_ALIGN for gu not 4-byte aligned and
  * MBGLU_ERR_ALIAS where gu overlaps an operand or out.  K == 0: out = +0 and
  * gu = 0.
  */
@@ -455,8 +456,9 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
  * projection.  The sum may be split over K into partial sums in the workspace,
  * of matmul_fp8_workspace_bytes(M, N, K) bytes (0: none needed), 256-byte
  * aligned, contents undefined afterwards; calls that may run at the same time
- * need different ones.  The split depends on M, N and K alone and the partial
- * sums are added in a fixed order.
+ * need different ones.  Kernel, tiles and split depend on M, N and K alone (and
+ * on whether the operands are aligned) and the partial sums are added in a fixed
+ * order: the same call gives the same bits.
  */
 size_t matmul_fp8_workspace_bytes(int M, int N, int K);
 mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ldas,

@@ -3,11 +3,18 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cstdint>
 #include <mutex>
 
 #include "api_internal.h"
 
 namespace mbglu_host {
+
+// The largest size these entry points take: the kernels' 32-bit indexes run up to
+// the end of the last tile.
+constexpr int kMostSize = INT32_MAX - 511;
+inline bool bad_sizes(int a, int b, int c = 0) { return std::min({a, b, c}) < 0 || std::max({a, b, c}) > kMostSize; }
 
 // The current device's SM count, after `setup` (attributes of the unit's
 // kernels) has run once on it.

@@ -266,7 +266,7 @@ mbglu_status add_rmsnorm_fp8(const mbglu_bf16 *x, int64_t ldx, const mbglu_bf16 
                              int64_t ldq, float *scale, int64_t lds, int M, int K, cudaStream_t stream)
 {
     set_last_variant(0);
-    if (M < 0 || K < 1) return MBGLU_ERR_SHAPE;
+    if (bad_sizes(M, K) || K < 1) return MBGLU_ERR_SHAPE;
     if (M == 0) return MBGLU_OK;
     if (!x || !residual || !residual_out || !norm_w || !q || !scale) return MBGLU_ERR_NULL;
     if (ldx < K || ldr < K || ldro < K || ldq < K || lds < ceil_div(K, kBlk)) return MBGLU_ERR_STRIDE;
@@ -310,7 +310,7 @@ mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw, uint8_t *q, i
                                  int N, int K, cudaStream_t stream)
 {
     set_last_variant(0);
-    if (N < 0 || K < 0) return MBGLU_ERR_SHAPE;
+    if (bad_sizes(N, K)) return MBGLU_ERR_SHAPE;
     if (N == 0 || K == 0) return MBGLU_OK;
     if (!w || !q || !scale) return MBGLU_ERR_NULL;
     if (ldw < K || ldq < K || lds < ceil_div(K, kBlk)) return MBGLU_ERR_STRIDE;
@@ -328,7 +328,7 @@ mbglu_status quantize_weight_fp8(const mbglu_bf16 *w, int64_t ldw, uint8_t *q, i
 
 size_t matmul_fp8_workspace_bytes(int M, int N, int K)
 {
-    if (M <= 0 || N <= 0 || K <= 0) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || bad_sizes(M, N, K)) return 0;
     return workspace_of(fp8_plan(M, N, K, false));
 }
 
@@ -337,7 +337,7 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
                         int K, void *workspace, size_t workspace_bytes, cudaStream_t stream)
 {
     set_last_variant(0);
-    if (M < 0 || N < 0 || K < 0) return MBGLU_ERR_SHAPE;
+    if (bad_sizes(M, N, K)) return MBGLU_ERR_SHAPE;
     if (M == 0 || N == 0) return MBGLU_OK;
     if (!out) return MBGLU_ERR_NULL;
     const Scaled A = {a, lda, a_scale, ldas, M, M}, W = {w, ldw, w_scale, ldws, N, ceil_div(N, kBlk)};
@@ -400,7 +400,7 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
                      float *q_scale, int64_t ldqs, int M, int N, int K, cudaStream_t stream)
 {
     set_last_variant(0);
-    if (M < 0 || N < 0 || K < 0) return MBGLU_ERR_SHAPE;
+    if (bad_sizes(M, N, K)) return MBGLU_ERR_SHAPE;
     if (M == 0 || N == 0) return MBGLU_OK;
     // one form of the output: bf16, or e4m3 with its scales
     if ((out != nullptr) == (q != nullptr) || (q != nullptr) != (q_scale != nullptr)) return MBGLU_ERR_NULL;

@@ -94,7 +94,7 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
 {
     set_last_variant(0);
     if (mode != MBGLU_MODE_FUSED && mode != MBGLU_MODE_HF) return MBGLU_ERR_MODE;
-    if (M < 0 || N < 0 || K < 0 || N > INT32_MAX / 2) return MBGLU_ERR_SHAPE;
+    if (bad_sizes(M, N, K) || N > INT32_MAX / 2) return MBGLU_ERR_SHAPE;
     if (M == 0 || N == 0) return MBGLU_OK;
     if (!out || (K > 0 && (!h || !gate_w || !up_w))) return MBGLU_ERR_NULL;
     if (ldo < N || (gu && ldgu < 2 * static_cast<int64_t>(N)) || (K > 0 && (ldh < K || ld_gate < K || ld_up < K)))
@@ -154,7 +154,7 @@ static int64_t grad_bytes(int M, int N) { return (2 * static_cast<int64_t>(M) * 
 
 size_t glu_gemm_backward_workspace_bytes(int M, int N, int K)
 {
-    if (M <= 0 || N <= 0 || K <= 0) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || bad_sizes(M, N, K)) return 0;
     // the two products' partial sums, one after the other
     return static_cast<size_t>(grad_bytes(M, N) + std::max(part_bytes(grad_h_plan(M, N, K)), part_bytes(grad_w_plan(M, N, K))));
 }
@@ -167,7 +167,7 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
 {
     set_last_variant(0);
     set_last_backward_path(0);
-    if (M < 0 || N < 0 || K < 0 || N > INT32_MAX / 2) return MBGLU_ERR_SHAPE;
+    if (bad_sizes(M, N, K) || N > INT32_MAX / 2) return MBGLU_ERR_SHAPE;
     const bool want_h = grad_h != nullptr, want_w = grad_gate != nullptr || grad_up != nullptr;
     if (want_w && (!grad_gate || !grad_up)) return MBGLU_ERR_NULL;
     if (K == 0) return MBGLU_OK;   // every gradient has K columns

@@ -5,6 +5,7 @@ import torch
 
 import memory_bound_glu_gb300 as mb
 
+HUGE = 2 ** 31 - 511   # one more than the largest size
 OK, NULL, SHAPE, STRIDE, ALIGN, MODE, ALIAS = range(7)
 A, G, U, O, D, GH, GG, GU, WS, S1, S2, S3, S4, Q = (0x7F0000000000 + i * (1 << 36) for i in range(14))
 
@@ -20,6 +21,7 @@ def gemm(h=A, ldh=64, g=G, ldg=64, u=U, ldu=64, o=O, ldo=32, gu=0, ldgu=64, M=20
     (dict(h=A + 1), ALIGN), (dict(g=G + 1), ALIGN), (dict(u=U + 1), ALIGN), (dict(o=O + 1), ALIGN), (dict(gu=GU + 2), ALIGN),
     (dict(o=A + 2 * 64 * 199), ALIAS), (dict(o=G), ALIAS), (dict(o=U + 64), ALIAS), (dict(gu=O + 4), ALIAS), (dict(gu=G), ALIAS),
     (dict(M=0), OK), (dict(N=0), OK), (dict(M=0, h=0, g=0, u=0, o=0), OK),
+    (dict(M=HUGE), SHAPE), (dict(K=HUGE), SHAPE),
 ])
 def test_glu_gemm(kw, code):
     assert gemm(**kw) == code
@@ -40,6 +42,7 @@ def bwd(h=A, ldh=64, g=G, ldg=64, u=U, ldu=64, d=D, ldd=32, gu=0, ldgu=64, gh=GH
     (dict(gh=A), ALIAS), (dict(gg=G + 64), ALIAS), (dict(gw=D), ALIAS), (dict(ws=GG), ALIAS), (dict(gw=GG + 2 * 64 * 31), ALIAS),
     (dict(gu=GH), ALIAS),
     (dict(K=0), OK), (dict(M=0, N=0), OK), (dict(gh=0, gg=0, gw=0), OK),
+    (dict(M=HUGE), SHAPE), (dict(K=HUGE), SHAPE),
 ])
 def test_glu_gemm_backward(kw, code):
     assert bwd(**kw) == code
@@ -51,7 +54,7 @@ def norm(x=A, ldx=256, r=G, ldr=256, ro=G, ldro=256, w=U, q=Q, ldq=256, s=S1, ld
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(M=-1), SHAPE), (dict(K=0), SHAPE),
+    (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(M=HUGE), SHAPE), (dict(K=HUGE), SHAPE),
     (dict(x=0), NULL), (dict(r=0), NULL), (dict(ro=0), NULL), (dict(w=0), NULL), (dict(q=0), NULL), (dict(s=0), NULL),
     (dict(ldx=255), STRIDE), (dict(ldr=255, ro=O), STRIDE), (dict(ldro=255, ro=O), STRIDE), (dict(ldq=255), STRIDE), (dict(lds=1), STRIDE),
     (dict(x=A + 1), ALIGN), (dict(w=U + 1), ALIGN), (dict(s=S1 + 2), ALIGN),
@@ -69,7 +72,7 @@ def matmul(a=A, lda=256, sa=S1, ldsa=2, w=G, ldw=256, sw=S2, ldsw=2, o=O, ldo=20
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-1), SHAPE),
+    (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-1), SHAPE), (dict(M=HUGE), SHAPE), (dict(N=HUGE), SHAPE), (dict(K=HUGE), SHAPE),
     (dict(a=0), NULL), (dict(sa=0), NULL), (dict(w=0), NULL), (dict(sw=0), NULL), (dict(o=0), NULL),
     (dict(lda=255), STRIDE), (dict(ldw=255), STRIDE), (dict(ldsa=1), STRIDE), (dict(ldsw=1), STRIDE), (dict(ldo=199), STRIDE),
     (dict(sa=S1 + 2), ALIGN), (dict(sw=S2 + 1), ALIGN), (dict(o=O + 1), ALIGN),
@@ -87,7 +90,7 @@ def glu(a=A, lda=256, sa=S1, ldsa=2, g=G, ldg=256, sg=S2, ldsg=2, u=U, ldu=256, 
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-1), SHAPE),
+    (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-1), SHAPE), (dict(M=HUGE), SHAPE), (dict(N=HUGE), SHAPE), (dict(K=HUGE), SHAPE),
     (dict(o=O), NULL), (dict(q=0), NULL), (dict(qs=0), NULL), (dict(q=0, qs=0), NULL), (dict(o=O, q=0), NULL),
     (dict(a=0), NULL), (dict(sg=0), NULL), (dict(u=0), NULL),
     (dict(lda=255), STRIDE), (dict(ldg=255), STRIDE), (dict(ldsu=1), STRIDE), (dict(ldq=199), STRIDE), (dict(ldqs=1), STRIDE),
@@ -106,7 +109,7 @@ def quant(w=A, ldw=256, q=Q, ldq=256, s=S1, lds=2, N=200, K=256):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(N=-1), SHAPE), (dict(K=-1), SHAPE), (dict(w=0), NULL), (dict(q=0), NULL), (dict(s=0), NULL),
+    (dict(N=-1), SHAPE), (dict(K=-1), SHAPE), (dict(N=HUGE), SHAPE), (dict(K=HUGE), SHAPE), (dict(w=0), NULL), (dict(q=0), NULL), (dict(s=0), NULL),
     (dict(ldw=255), STRIDE), (dict(ldq=255), STRIDE), (dict(lds=1), STRIDE), (dict(w=A + 1), ALIGN), (dict(s=S1 + 2), ALIGN),
     (dict(q=A + 5), ALIAS), (dict(s=A), ALIAS), (dict(s=Q + 4), ALIAS), (dict(N=0), OK), (dict(K=0), OK),
 ])
@@ -120,7 +123,7 @@ def test_workspace_bytes():
     # dG and dU in bf16, rows padded to 64 elements, at least
     assert lib.glu_gemm_backward_workspace_bytes(100, 100, 64) >= 2 * 100 * 128 * 2
     for f in (lib.glu_gemm_backward_workspace_bytes, lib.matmul_fp8_workspace_bytes):
-        assert f(0, 10, 10) == 0 and f(10, 0, 10) == 0 and f(-1, 10, 10) == 0
+        assert f(0, 10, 10) == 0 and f(10, 0, 10) == 0 and f(-1, 10, 10) == 0 and f(HUGE, 10, 10) == 0
 
 
 def test_binding_refuses():
