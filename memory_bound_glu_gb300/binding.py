@@ -271,10 +271,11 @@ class DualWeightGlu(torch.autograd.Function):
     gradients land on those tensors).
 
     Up to MAX_M rows run glu_gemv and glu_backward; more run glu_gemm, which
-    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward.  Where no gradient
-    can follow, apply is the forward call alone.  To capture a training step
-    into a CUDA graph, run it on the capture's stream first and let no eager
-    graph over the same leaves live meanwhile, as for any autograd Function."""
+    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward.  There is no second
+    derivative: asking for it raises a RuntimeError.  Where no gradient can
+    follow, apply is the forward call alone.  To capture a training step into a
+    CUDA graph, run it on the capture's stream first and let no eager graph over
+    the same leaves live meanwhile, as for any autograd Function."""
 
     @classmethod
     def apply(cls, h, gate_w, up_w, mode="fused"):
@@ -297,6 +298,7 @@ class DualWeightGlu(torch.autograd.Function):
         return glu_gemv(h, gate_w, up_w, mode=mode)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         h, gate_w, up_w, *rest = ctx.saved_tensors
         squeeze = h.dim() == 1
@@ -458,7 +460,7 @@ def _stream_of(dev, stream):
 
 
 _NONE = (None, 0)
-_MOST = 2 ** 31 - 1   # the C entry points take int sizes
+_MOST = 2 ** 31 - 512   # what the C entry points take
 
 
 def glu_gemm(h, gate_w, up_w, out=None, mode="fused", gu=None, stream=None):

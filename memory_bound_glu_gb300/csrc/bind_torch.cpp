@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mbglu.h"
@@ -205,6 +206,13 @@ struct WideGlu : torch::autograd::Function<WideGlu> {
         out[0] = gh;
         if (ctx->needs_input_grad(1)) out[1] = gg;
         if (ctx->needs_input_grad(2)) out[2] = gw;
+        if (at::GradMode::is_enabled()) {   // create_graph: a second derivative is an error, not a zero
+            for (at::Tensor &x : out)
+                if (x.defined()) x.set_requires_grad(true);
+            const auto error = std::make_shared<torch::autograd::DelayedError>(
+                "DualWeightGlu has no second derivative: its backward is differentiable once", static_cast<int64_t>(out.size()));
+            return (*error)(std::move(out));
+        }
         return out;
     }
 };

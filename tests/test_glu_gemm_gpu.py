@@ -232,6 +232,18 @@ def test_autograd_subsets_and_broadcast_gradient():
     R.assert_bf16(gh, *backward_reference(h, gw, uw, torch.ones(100, 64, device=DEV, dtype=BF))[0])
 
 
+@pytest.mark.parametrize("M", [40, 100])
+def test_a_second_derivative_is_an_error(M):
+    """create_graph gives the first derivative; its own is refused, not taken as zero."""
+    leaves = [t.requires_grad_(True) for t in operands(M, 64, 48, seed=11)]
+    plain = torch.autograd.grad(mb.DualWeightGlu.apply(*leaves).float().square().sum(), leaves)
+    first = torch.autograd.grad(mb.DualWeightGlu.apply(*leaves).float().square().sum(), leaves, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(plain, first))
+    for g in first:
+        with pytest.raises(RuntimeError):
+            g.float().square().sum().backward(retain_graph=True)
+
+
 def test_deterministic_and_rows_independent():
     h, gw, uw = operands(300, 264, 200, seed=12)
     a, b = mb.glu_gemm(h, gw, uw), mb.glu_gemm(h, gw, uw)
