@@ -9,6 +9,7 @@
 #include "glu_grad.cuh"
 #include "pair_gemm.cuh"
 #include "pair_plan.h"
+#include "pair_tall.cuh"
 
 namespace {
 
@@ -45,6 +46,8 @@ cudaError_t setup_pair()
     if (e == cudaSuccess) e = allow_pair<mbglu::kPairGrad, mbglu::kPairDual, false, false>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kPairPlain, mbglu::kPairSum, false, true>();
     if (e == cudaSuccess) e = allow_pair<mbglu::kPairPlain, mbglu::kPairStack, true, true>();
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(mbglu::pair_tall_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kPairSmem));
     return e;
 }
 
@@ -54,9 +57,9 @@ mbglu_status sm_count(int *n)
     return table.get(n, setup_pair);
 }
 
-bool k_major(mbglu::TensorMap *m, const void *p, int64_t ld, int rows, int T)
+bool k_major(mbglu::TensorMap *m, const void *p, int64_t ld, int rows, int T, int box_rows = 128)
 {
-    return encode_tile_map(m, p, ld, rows, T, 64, 128, 2);
+    return encode_tile_map(m, p, ld, rows, T, 64, box_rows, 2);
 }
 
 // [T][cols], cols the output's index
@@ -74,6 +77,38 @@ mbglu_status launch_pair(const mbglu::PairParams &p, const mbglu::PairMaps &maps
     Launch l(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.ntiles))), mbglu::kPairThreads, mbglu::kPairSmem,
              stream, 2);
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_gemm_kernel<EPI, MODE, A_MN, B_MN>, p, maps));
+}
+
+// Tokens per tile of pair_tall_kernel, or 0 where pair_gemm_kernel is estimated to
+// be faster.  From the sizes alone.  The constants (ns) are fitted to 600 measured
+// calls in chains: seven shapes, 65 to 1000 rows, every tn.  There the choice is
+// within 1% of the fastest on average, 7% at worst, never slower than
+// pair_gemm_kernel and 24% faster on average (K = 2560, N = 9728 at M = 333: 29.2 us
+// against 31.2; K = 1000, N = 2504: 9.9 and 11.3; K = 4096, N = 300: 13.0 and 22.9).
+int tall_tokens(int M, int N, int K)
+{
+    const int64_t chunks = ceil_div(K, 64), nt = ceil_div(N, 128), tiles = nt * ceil_div(M, mbglu::kPairTile);
+    int64_t best = 5760 + (tiles + kPairs - 1) / kPairs * chunks * (253 + 88 * std::min<int64_t>(tiles, kPairs) / kPairs);
+    int tn = 0;
+    for (int t = 32; t < mbglu::kPairTile; t += 32) {
+        const int64_t n = nt * ceil_div(M, t);
+        const int64_t round = chunks * (77 + 59 * std::min<int64_t>(n, kPairs) / kPairs) + chunks * t * 7 / 10 + t * 31 / 2;
+        const int64_t ns = 4240 + (n + kPairs - 1) / kPairs * round;
+        if (ns < best) {
+            best = ns;
+            tn = t;
+        }
+    }
+    return tn;
+}
+
+mbglu_status launch_pair_tall(const mbglu::PairTallParams &p, const mbglu::PairMaps &maps, cudaStream_t stream)
+{
+    int sms = 0;
+    const mbglu_status st = sm_count(&sms);
+    if (st != MBGLU_OK) return st;
+    Launch l(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.ntiles))), mbglu::kPairThreads, mbglu::kPairSmem, stream, 2);
+    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_tall_kernel, p, maps));
 }
 
 // grad_h [M, K] over 2 N; grad_gate and grad_up [N, K] over M
@@ -113,7 +148,25 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
     if (M <= MBGLU_MAX_M && !gu)
         return glu_gemv(h, ldh, gate_w, ld_gate, up_w, ld_up, out, ldo, M, N, K, mode, stream);
     mbglu::PairMaps maps;
-    if (K > 0 && copyable(h, ldh, 2) && copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2) && k_major(&maps.a[0], h, ldh, M, K) &&
+    const bool fast = K > 0 && copyable(h, ldh, 2) && copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2);
+    const int tn = fast && !gu ? tall_tokens(M, N, K) : 0;
+    if (tn && k_major(&maps.a[0], gate_w, ld_gate, N, K, 64) && k_major(&maps.a[1], up_w, ld_up, N, K, 64) &&
+        k_major(&maps.b[0], h, ldh, M, K, tn / 2)) {
+        mbglu::PairTallParams q = {};
+        q.M = M;
+        q.N = N;
+        q.nchunk = ceil_div(K, 64);
+        q.tn = tn;
+        q.ttiles = ceil_div(M, tn);
+        q.ntiles = q.ttiles * ceil_div(N, 128);
+        q.mode = static_cast<int>(mode);
+        q.out = out;
+        q.ldo = ldo;
+        const mbglu_status st = launch_pair_tall(q, maps, stream);
+        if (st == MBGLU_OK) set_last_variant(kPairGemm);
+        return st;
+    }
+    if (fast && k_major(&maps.a[0], h, ldh, M, K) &&
         k_major(&maps.b[0], gate_w, ld_gate, N, K) && k_major(&maps.b[1], up_w, ld_up, N, K)) {
         mbglu::PairParams q = {};
         q.plan = pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), false);

@@ -203,3 +203,47 @@ def test_few_row_plans_are_launchable(dual):
                 assert ns > 0 and 1 <= ks <= min(8, ceil_div(K, 128)) and tn % 16 == 0 and tn <= 128
                 c = ceil_div(K, 128)
                 assert all(c * r // ks < c * (r + 1) // ks for r in range(ks))   # no block without a stage
+
+
+def gemm_tokens(M, N, K):
+    chunks, nt = ceil_div(K, 64), ceil_div(N, 128)
+    tiles = nt * ceil_div(M, TILE)
+    best, tn = 5760 + ceil_div(tiles, PAIRS) * chunks * (253 + 88 * min(tiles, PAIRS) // PAIRS), 0
+    for t in range(32, TILE, 32):
+        n = nt * ceil_div(M, t)
+        ns = 4240 + ceil_div(n, PAIRS) * (chunks * (77 + 59 * min(n, PAIRS) // PAIRS) + chunks * t * 7 // 10 + t * 31 // 2)
+        if ns < best:
+            best, tn = ns, t
+    return tn
+
+
+def test_wide_forward_plan():
+    """Narrow tiles for few rows and few tiles, 256-row tiles for long prompts."""
+    assert {gemm_tokens(M, N, K) for M in (65, 100, 160, 200, 333, 400, 565, 700) for N in (300, 2500, 9728)
+            for K in (264, 1000, 1528, 2560, 4096)} == {0, 32, 64, 96, 128, 160, 192, 224}
+    for M in (1024, 2048, 2100, 4096, 8192):
+        for N, K in ((9728, 2560), (14336, 4096), (4096, 2048), (11008, 4096)):
+            assert gemm_tokens(M, N, K) == 0
+
+
+@pytest.mark.parametrize("tn", range(32, 256, 32))
+def test_wide_forward_exchange(tn):
+    """A warp of g and its warp of u: each of the tile's values is used once, in the
+    buffers' space, and every output has one writer."""
+    seen = set()
+    for half in (0, 1):
+        for q in range(4):
+            side, pairing = q >> 1, half * 2 + (q & 1)
+            sets = 0
+            for j in range(0, tn // 2, 16):
+                mine = {pairing * 1024 + (sets & 1) * 512 + side * 256 + i * 32 + lane for i in range(8) for lane in (0, 31)}
+                assert max(mine) < 8 * 32 * 17 and len(mine) == 16
+                for i in range(8):
+                    for lane in (0, 31):
+                        at = (half * (tn // 2) + j + side * 8 + i, (q & 1) * 32 + lane)
+                        assert at not in seen and at[0] < tn
+                        seen.add(at)
+                # what this warp hands over: the other side's eight
+                assert (8 if side == 0 else 0) == (side ^ 1) * 8
+                sets += 1
+    assert len(seen) == tn * 4

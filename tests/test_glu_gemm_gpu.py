@@ -72,6 +72,17 @@ def test_each_kernel(M, N, K, pad, variant):
         check_forward(h, gw, uw, mode="hf", gu=True)
 
 
+# tiles of 32 to 224 tokens, several rounds of them, ragged in every dimension; the
+# last two with 256 rows
+@pytest.mark.parametrize("M,N,K", [(479, 520, 2048), (459, 1000, 152), (289, 2500, 352), (330, 2500, 1064), (160, 9729, 1000),
+                                   (565, 2500, 1528), (333, 9728, 2560), (400, 9730, 2568), (66, 14336, 264), (1100, 2500, 136),
+                                   (2100, 1300, 264)])
+@pytest.mark.parametrize("mode", ["fused", "hf"])
+def test_tiles_of_tokens(M, N, K, mode):
+    check_forward(*operands(M, N, K, seed=M), mode=mode)
+    assert mb.last_variant() == 11
+
+
 @pytest.mark.parametrize("M", [1, 2, 16, 40, 64])
 def test_few_rows(M):
     ops = operands(M, 136, 264, seed=M)
@@ -88,12 +99,13 @@ def test_strides_and_alignment(mode, pad, off):
     check_forward(h, gw, uw, mode=mode)
 
 
+@pytest.mark.parametrize("M,N,K", [(130, 100, 64), (1100, 2500, 136)])
 @pytest.mark.parametrize("pad", [0, 1, 8, 24])
-def test_output_stride_and_what_lies_behind(pad):
-    h, gw, uw = operands(130, 100, 64, seed=pad)
-    whole = torch.full((131, 100 + pad), 7.0, dtype=BF, device=DEV)
-    check_forward(h, gw, uw, out=whole[:130, :100])
-    assert (whole[:130, 100:] == 7).all() and (whole[130] == 7).all()
+def test_output_stride_and_what_lies_behind(pad, M, N, K):
+    h, gw, uw = operands(M, N, K, seed=pad)
+    whole = torch.full((M + 1, N + pad), 7.0, dtype=BF, device=DEV)
+    check_forward(h, gw, uw, out=whole[:M, :N])
+    assert (whole[:M, N:] == 7).all() and (whole[M] == 7).all()
 
 
 def test_empty():
