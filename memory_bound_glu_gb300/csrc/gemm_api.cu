@@ -83,8 +83,8 @@ mbglu_status launch_pair(const mbglu::PairParams &p, const mbglu::PairMaps &maps
 // be faster.  From the sizes alone.  The constants (ns) are fitted to 600 measured
 // calls in chains: seven shapes, 65 to 1000 rows, every tn.  There the choice is
 // within 1% of the fastest on average, 7% at worst, never slower than
-// pair_gemm_kernel and 24% faster on average (K = 2560, N = 9728 at M = 333: 29.2 us
-// against 31.2; K = 1000, N = 2504: 9.9 and 11.3; K = 4096, N = 300: 13.0 and 22.9).
+// pair_gemm_kernel and 24% faster on average (K = 2560, N = 9728 at M = 333: 27.9 us
+// against 31.2; K = 1000, N = 2504: 9.2 and 11.3; K = 4096, N = 300: 13.0 and 22.9).
 int tall_tokens(int M, int N, int K)
 {
     const int64_t chunks = ceil_div(K, 64), nt = ceil_div(N, 128), tiles = nt * ceil_div(M, mbglu::kPairTile);

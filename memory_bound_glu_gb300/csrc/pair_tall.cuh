@@ -10,8 +10,11 @@
 // pair_gemm.cuh.
 //
 // What bounds it: the weights' bytes up to about 128 tokens (K = 2560, N = 9728 at M =
-// 96: 21.3 us, 14.7 of them the bytes at the copy rate), the MMAs beyond, and a call's
-// start and end (4 us) where there are few tiles.
+// 96: 20.8 us, 14.7 of them the bytes at the copy rate), the MMAs beyond (333: 27.9 us,
+// the tensor pipe active for 54%), and a call's start and end (4 us) where there are
+// few tiles.  The last tile's epilogue is part of that end and bound by its
+// instructions: one pointer stepped by a row, and SiLUs apart from the stores, took
+// 29.0 to 27.9 us.  Loading the next 16 columns ahead brought nothing.
 #pragma once
 
 #include "pair_gemm.cuh"
@@ -134,14 +137,26 @@ static __global__ void __launch_bounds__(kPairThreads, 1) pair_tall_kernel(const
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mine[i * 32] = __uint_as_float(side ? r[i] : r[8 + i]);
                 bar_sync_named(1 + pairing, 64);
-                const int m = m0 + j + side * 8;
+                const int m = m0 + j + side * 8, left = n < p.N && ok ? p.M - m : 0;
+                uint16_t *o = p.out + static_cast<int64_t>(m) * p.ldo + n;
+                float g[8], u[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float x = theirs[i * 32], own = __uint_as_float(side ? r[8 + i] : r[i]);
-                    const float g = side ? x : own, u = side ? own : x;
-                    const uint16_t y = p.mode == 0 ? f32_to_bf16(silu_short(g) * u) : static_cast<uint16_t>(glu_hf_short(g, u));
-                    if (ok && m + i < p.M && n < p.N) p.out[static_cast<int64_t>(m + i) * p.ldo + n] = y;
+                    g[i] = side ? x : own;
+                    u[i] = side ? own : x;
                 }
+                uint16_t y[8];
+                if (p.mode == 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = f32_to_bf16(silu_short(g[i]) * u[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = static_cast<uint16_t>(glu_hf_short(g[i], u[i]));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i, o += p.ldo)
+                    if (i < left) *o = y[i];
             }
         }
     }
