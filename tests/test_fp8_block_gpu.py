@@ -453,3 +453,28 @@ def test_one_row_needs_no_stride(K):
     check_glu(a, sa, g, sg, u, su, True)
     assert mb.last_variant() == 16
     check_glu(a.expand(1, K), sa, g, sg, u, su, False)
+
+
+def far(t, odd=0):
+    """t's values in rows so far apart that the last lies beyond 2^31 elements."""
+    step = (2 ** 31 // (t.shape[0] - 1) + 64) // 64 * 64 + odd
+    raw = t.view(torch.uint8) if t.dtype == F8 else t
+    v = torch.empty((t.shape[0] - 1) * step + t.shape[1], dtype=raw.dtype, device=DEV).as_strided(t.shape, (step, 1))
+    assert (t.shape[0] - 1) * step > 2 ** 31 - 64
+    return v.copy_(raw).view(t.dtype)
+
+
+@pytest.mark.parametrize("M,N,K,odd", [(33, 300, 272, 0), (150, 136, 400, 0), (2100, 1000, 272, 0), (40, 72, 136, 1)])
+def test_offsets_beyond_32_bits(M, N, K, odd):
+    (a, sa), (g, sg), (u, su) = activations(M, K), weight(N, K, seed=1), weight(N, K, seed=2)
+    a, sa, g, u = (far(t, odd) for t in (a, sa, g, u))
+    check_matmul(a, sa, g, sg, out=far(torch.zeros(M, N, dtype=BF, device=DEV), odd))
+    q, s = far(torch.zeros(M, N, device=DEV).to(F8), odd), far(torch.zeros(M, -(-N // 128), device=DEV), odd)
+    check_glu(a, sa, g, sg, u, su, True, out=q, out_scale=s)
+    check_glu(a, sa, g, sg, u, su, False, out=far(torch.zeros(M, N, dtype=BF, device=DEV), odd))
+    x, r = far(rand(M, K, seed=3).to(BF), odd), far(rand(M, K, seed=4).to(BF), odd)
+    q, s = far(torch.zeros(M, K, device=DEV).to(F8), odd), far(torch.zeros(M, -(-K // 128), device=DEV), odd)
+    check_norm(x, r, rand(K, seed=5, scale=0.1).to(BF), q=q, scale=s, residual_out=far(torch.zeros(M, K, dtype=BF, device=DEV), odd))
+    wq, ws = mb.quantize_weight_fp8(far(rand(N, K, seed=6).to(BF), odd), q=far(torch.zeros(N, K, device=DEV).to(F8), odd))
+    rq, rs = mb.quantize_weight_fp8(rand(N, K, seed=6).to(BF))
+    assert torch.equal(wq.float(), rq.float()) and torch.equal(ws, rs)

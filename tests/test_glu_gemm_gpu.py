@@ -387,3 +387,27 @@ def test_workspace_and_gu_used_again_by_the_next_step():
             got.append(mb.glu_gemm_backward(h, gw, uw, d, gu=gu, workspace=ws))
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for a, b in zip(got, want) for x, y in zip(a, b))
+
+
+def far(t, odd=0):
+    """t's values in rows so far apart that the last lies beyond 2^31 elements."""
+    step = (2 ** 31 // (t.shape[0] - 1) + 64) // 64 * 64 + odd
+    v = torch.empty((t.shape[0] - 1) * step + t.shape[1], dtype=t.dtype, device=DEV).as_strided(t.shape, (step, 1))
+    assert (t.shape[0] - 1) * step > 2 ** 31 - 64
+    return v.copy_(t)
+
+
+@pytest.mark.parametrize("M,N,K,odd", [(200, 136, 72, 0), (1100, 2500, 136, 0), (90, 40, 24, 1)])
+def test_offsets_beyond_32_bits(M, N, K, odd):
+    h, gw, uw = (far(t, odd) for t in operands(M, N, K, seed=1))
+    out, gu = far(torch.zeros(M, N, dtype=BF, device=DEV), odd), far(torch.zeros(M, 2 * N, device=DEV), odd)
+    check_forward(h, gw, uw, out=out)
+    mb.glu_gemm(h, gw, uw, gu=gu)
+    d = far(rand(M, N, seed=5), odd)
+    grads = [far(torch.zeros(n, K, dtype=BF, device=DEV), odd) for n in (M, N, N)]
+    kw = dict(zip(("grad_h", "grad_gate", "grad_up"), grads))
+    check_backward(h, gw, uw, d, **kw)
+    first = [g.clone() for g in grads]
+    mb.glu_gemm_backward(h, gw, uw, d, gu=gu, **kw)
+    assert all(((a.double() - b.double()).norm() <= 4 * R.EPS_BF16 * a.double().norm()) for a, b in zip(first, grads))
+    assert mb.read_device_error() == 0
