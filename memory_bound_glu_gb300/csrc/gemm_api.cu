@@ -149,7 +149,7 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
         return glu_gemv(h, ldh, gate_w, ld_gate, up_w, ld_up, out, ldo, M, N, K, mode, stream);
     mbglu::PairMaps maps;
     const bool fast = K > 0 && copyable(h, ldh, 2) && copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2);
-    const int tn = fast && !gu ? tall_tokens(M, N, K) : 0;
+    const int tn = fast ? tall_tokens(M, N, K) : 0;
     if (tn && k_major(&maps.a[0], gate_w, ld_gate, N, K, 64) && k_major(&maps.a[1], up_w, ld_up, N, K, 64) &&
         k_major(&maps.b[0], h, ldh, M, K, tn / 2)) {
         mbglu::PairTallParams q = {};
@@ -162,6 +162,8 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
         q.mode = static_cast<int>(mode);
         q.out = out;
         q.ldo = ldo;
+        q.gu = gu;
+        q.ldgu = ldgu;
         const mbglu_status st = launch_pair_tall(q, maps, stream);
         if (st == MBGLU_OK) set_last_variant(kPairGemm);
         return st;
