@@ -352,10 +352,10 @@ mbglu_status gdn_gates(const mbglu_bf16 *a, int64_t lda, const mbglu_bf16 *b, in
  *   gu      NULL, or [M][2N] fp32, row stride ldgu >= 2N: receives
  *           g = h gate_w^T in columns [0, N) and u = h up_w^T in [N, 2N), what
  *           glu_gemm_backward would otherwise compute again  (written)
- * Rows beyond MBGLU_MAX_M (and any M with gu) run on the fifth-generation
- * tensor cores where h, gate_w and up_w are 16-byte aligned with row strides
- * that are multiples of 8 elements; other operands take a slower kernel.  Up
- * to MBGLU_MAX_M rows without gu the call is glu_gemv.
+ * More than 16 rows (and any M with gu) run on the fifth-generation tensor
+ * cores where h, gate_w and up_w are 16-byte aligned with row strides that are
+ * multiples of 8 elements; other operands take a slower kernel.  Without gu, up
+ * to 16 rows, and up to MBGLU_MAX_M of other operands, the call is glu_gemv.
  * Errors as glu_gemv without the limit on M; also MBGLU_ERR_SHAPE for 2N
  * beyond INT32_MAX and M or K beyond INT32_MAX - 511 (here and in the functions
  * below, for every size), MBGLU_ERR_ALIGN for gu not 4-byte aligned and

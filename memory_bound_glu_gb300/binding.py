@@ -466,8 +466,8 @@ _MOST = 2 ** 31 - 512   # what the C entry points take
 def glu_gemm(h, gate_w, up_w, out=None, mode="fused", gu=None, stream=None):
     """out[M,N] = SiLU(h @ gate_w.T) * (h @ up_w.T) for any number of rows: a
     prompt or a training batch.  Arguments as glu_gemv; gu, a float32 [M, 2N]
-    tensor, receives g and u for glu_gemm_backward.  Up to MAX_M rows without
-    gu the call is glu_gemv."""
+    tensor, receives g and u for glu_gemm_backward.  Without gu, up to 16 rows
+    (up to MAX_M of operands that are not 16-byte aligned) the call is glu_gemv."""
     if stream is None:
         r = (_quick_module or _quick()).glu_gemm(h, gate_w, up_w, out, _MODES[mode], gu)
         if r is not None:

@@ -79,6 +79,8 @@ mbglu_status launch_pair(const mbglu::PairParams &p, const mbglu::PairMaps &maps
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::pair_gemm_kernel<EPI, MODE, A_MN, B_MN>, p, maps));
 }
 
+constexpr int kDecodeRows = 16;   // glu_gemv's, at any alignment
+
 // Tokens per tile of pair_tall_kernel, or 0 where pair_gemm_kernel is estimated to
 // be faster.  From the sizes alone.  The constants (ns) are fitted to 600 measured
 // calls in chains: seven shapes, 65 to 1000 rows, every tn.  There the choice is
@@ -144,11 +146,14 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
         for (int i = 0; i < 3; ++i)
             if (overlaps(out, ob, ins[i], inb[i]) || overlaps(gu, gb, ins[i], inb[i])) return MBGLU_ERR_ALIAS;
     }
-    // few rows: the decode kernels, which hand out no g and u
-    if (M <= MBGLU_MAX_M && !gu)
+    // few rows: the decode kernels, which hand out no g and u.  From 17 rows on
+    // pair_tall_kernel is faster wherever it applies: 19.1 us against 23.3 at 17 rows
+    // and 19.7 against 29.4 at 64 (K = 2560, N = 9728), 6.5 against 20.9 at 64 (K = 1000,
+    // N = 2504); at 16, 18.8 and 20.1, 10.1 and 6.5 (K = 2560, N = 1000).
+    const bool fast = K > 0 && copyable(h, ldh, 2) && copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2);
+    if (!gu && (M <= kDecodeRows || (M <= MBGLU_MAX_M && !fast)))
         return glu_gemv(h, ldh, gate_w, ld_gate, up_w, ld_up, out, ldo, M, N, K, mode, stream);
     mbglu::PairMaps maps;
-    const bool fast = K > 0 && copyable(h, ldh, 2) && copyable(gate_w, ld_gate, 2) && copyable(up_w, ld_up, 2);
     const int tn = fast ? tall_tokens(M, N, K) : 0;
     if (tn && k_major(&maps.a[0], gate_w, ld_gate, N, K, 64) && k_major(&maps.a[1], up_w, ld_up, N, K, 64) &&
         k_major(&maps.b[0], h, ldh, M, K, tn / 2)) {

@@ -83,13 +83,22 @@ def test_tiles_of_tokens(M, N, K, mode):
     assert mb.last_variant() == 11
 
 
-@pytest.mark.parametrize("M", [1, 2, 16, 40, 64])
-def test_few_rows(M):
-    ops = operands(M, 136, 264, seed=M)
-    out = check_forward(*ops)
-    if M <= 64:
-        assert torch.equal(out, mb.glu_gemv(*ops))
-    check_forward(*ops, gu=True)
+@pytest.mark.parametrize("mode", ["fused", "hf"])
+@pytest.mark.parametrize("M", [1, 2, 16, 17, 31, 33, 40, 64])
+@pytest.mark.parametrize("N,K", [(136, 264), (2500, 1000), (1, 8), (129, 4104)])
+def test_few_rows(M, N, K, mode):
+    ops = operands(M, N, K, seed=M)
+    out = check_forward(*ops, mode=mode)
+    assert (mb.last_variant() == 11) == (M > 16)
+    if M <= 16:
+        assert torch.equal(out, mb.glu_gemv(*ops, mode=mode))
+    check_forward(*ops, mode=mode, gu=True)
+
+
+@pytest.mark.parametrize("M", [17, 64])
+def test_few_rows_of_any_alignment(M):
+    ops = operands(M, 136, 264, seed=M, pad=1)
+    assert torch.equal(check_forward(*ops), mb.glu_gemv(*ops))
 
 
 @pytest.mark.parametrize("mode", ["fused", "hf"])
