@@ -104,6 +104,19 @@ int tall_tokens(int M, int N, int K)
     return tn;
 }
 
+// Outputs per tile: 80 or 96 where that needs no more rounds over the SM pairs than
+// 128 does, so that a round brings fewer weights.  K = 4096, N = 11008: 34.6 us with 80
+// against 40.0 with 128 at M = 17, 37.7 and 42.6 at 100, 39.0 and 43.4 at 160; where the
+// least such width is 112, up to 2.6% slower, so not there; nor narrower than 80 (K =
+// 1024, N = 640 at M = 160: 4.9 us, 5.2 with 64).
+int tall_outputs(int M, int N, int tn)
+{
+    const int64_t tt = ceil_div(M, tn), places = (ceil_div(N, 128) * tt + kPairs - 1) / kPairs * kPairs;
+    for (const int wt : {80, 96})
+        if (ceil_div(N, wt) * tt <= places) return wt;
+    return 128;
+}
+
 mbglu_status launch_pair_tall(const mbglu::PairTallParams &p, const mbglu::PairMaps &maps, cudaStream_t stream)
 {
     int sms = 0;
@@ -155,7 +168,8 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
         return glu_gemv(h, ldh, gate_w, ld_gate, up_w, ld_up, out, ldo, M, N, K, mode, stream);
     mbglu::PairMaps maps;
     const int tn = fast ? tall_tokens(M, N, K) : 0;
-    if (tn && k_major(&maps.a[0], gate_w, ld_gate, N, K, 64) && k_major(&maps.a[1], up_w, ld_up, N, K, 64) &&
+    const int wt = tn ? tall_outputs(M, N, tn) : 0;
+    if (tn && k_major(&maps.a[0], gate_w, ld_gate, N, K, wt / 2) && k_major(&maps.a[1], up_w, ld_up, N, K, wt / 2) &&
         k_major(&maps.b[0], h, ldh, M, K, tn / 2)) {
         mbglu::PairTallParams q = {};
         q.M = M;
@@ -163,7 +177,8 @@ mbglu_status glu_gemm(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w
         q.nchunk = ceil_div(K, 64);
         q.tn = tn;
         q.ttiles = ceil_div(M, tn);
-        q.ntiles = q.ttiles * ceil_div(N, 128);
+        q.ntiles = q.ttiles * ceil_div(N, wt);
+        q.wt = wt;
         q.mode = static_cast<int>(mode);
         q.out = out;
         q.ldo = ldo;

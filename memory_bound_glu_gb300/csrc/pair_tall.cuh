@@ -2,9 +2,12 @@
 // 256-row side and the tokens on the other: for batches that fill 256-row tiles
 // badly (a chunk of some hundred tokens), and products of few tiles.
 //
-// A tile is 128 outputs x tn tokens, tn any multiple of 32 up to 256.  The even
-// CTA's 128 rows are the gate and up rows of outputs 0-63, the odd one's those of
-// 64-127, so g lies in lanes 0-63 of a CTA's tensor memory and u in lanes 64-127.
+// A tile is wt outputs x tn tokens, wt a multiple of 16 up to 128, tn of 32 up to
+// 256.  The even CTA's rows are the gate and up rows of the first wt / 2 outputs, the
+// odd one's those of the others: g lies from lane 0 of a CTA's tensor memory on, u
+// from lane 64.  Below 128 outputs the lanes between hold products of whatever the
+// stage holds there, and nobody reads them; such tiles are for even rounds (N = 11008
+// is 86 tiles of 128, a second round for ten pairs of 76, or 138 of 80).
 // A warp of g and the warp that has u of the same outputs swap halves: of 16
 // tokens the first works on 8, the second on the others.  Pipeline and roles as
 // pair_gemm.cuh.
@@ -24,7 +27,8 @@ namespace mbglu {
 
 struct PairTallParams {
     int M, N, nchunk;
-    int tn, ttiles, ntiles;   // tokens per tile, tiles along the tokens, in all
+    int wt, tn;               // outputs and tokens per tile
+    int ttiles, ntiles;       // tiles along the tokens, in all
     int mode;
     uint16_t *out;
     int64_t ldo;
@@ -50,11 +54,11 @@ static __global__ void __launch_bounds__(kPairThreads, 1) pair_tall_kernel(const
 
     if (warp == 0) {
         const uint32_t full0 = map_to_rank(s.full, 0);
-        const uint32_t bytes = 2 * (kPairOperand + static_cast<uint32_t>(p.tn) * 64u);   // both CTAs'
+        const uint32_t bytes = 2 * (static_cast<uint32_t>(p.wt) * 128u + static_cast<uint32_t>(p.tn) * 64u);   // both CTAs'
         int st = 0, filled = 0;
         uint32_t phase = 1;
         for (int t = first; t < p.ntiles && ok; t += step) {
-            const int n0 = t / p.ttiles * 128 + rank * 64, m0 = t % p.ttiles * p.tn + rank * (p.tn / 2);
+            const int n0 = t / p.ttiles * p.wt + rank * (p.wt / 2), m0 = t % p.ttiles * p.tn + rank * (p.tn / 2);
             for (int c = 0; c < p.nchunk; ++c) {
                 if (!pair_wait(&s.empty[st], phase, kWaitLimitNs)) {
                     ok = false;
@@ -121,7 +125,8 @@ static __global__ void __launch_bounds__(kPairThreads, 1) pair_tall_kernel(const
         uint32_t v = 0, sets = 0;
         for (int t = first; t < p.ntiles; t += step, ++v) {
             const uint32_t buf = v & 1;
-            const int n = t / p.ttiles * 128 + rank * 64 + (q & 1) * 32 + lane;
+            const int row = (q & 1) * 32 + lane;
+            const int n = row < p.wt / 2 ? t / p.ttiles * p.wt + rank * (p.wt / 2) + row : p.N;   // p.N: none
             const int m0 = t % p.ttiles * p.tn + half * (p.tn / 2);
             if (ok) ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], (v >> 1) & 1, kWaitLimitNs));
             tc_fence_after();

@@ -247,3 +247,22 @@ def test_wide_forward_exchange(tn):
                 assert (8 if side == 0 else 0) == (side ^ 1) * 8
                 sets += 1
     assert len(seen) == tn * 4
+
+
+def gemm_outputs(M, N, tn):
+    tt = ceil_div(M, tn)
+    places = ceil_div(ceil_div(N, 128) * tt, PAIRS) * PAIRS
+    return next((wt for wt in (80, 96) if ceil_div(N, wt) * tt <= places), 128)
+
+
+def test_wide_forward_outputs():
+    """Every output in one lane of one tile, whatever the width; never more rounds."""
+    assert {gemm_outputs(M, N, tn) for M in (17, 100, 333) for N in (300, 2504, 7000, 9728, 11008) for tn in (32, 128, 192)} == {80, 96, 128}
+    for N in (1, 79, 80, 81, 300, 2504, 9728, 11008):
+        for tn in (32, 192):
+            wt = gemm_outputs(100, N, tn)
+            assert ceil_div(ceil_div(N, wt) * ceil_div(100, tn), PAIRS) == ceil_div(ceil_div(N, 128) * ceil_div(100, tn), PAIRS)
+            seen = [t * wt + rank * (wt // 2) + row for t in range(ceil_div(N, wt)) for rank in (0, 1) for row in range(64)
+                    if row < wt // 2]
+            assert sorted(n for n in seen if n < N) == list(range(N))
+            assert wt // 2 % 8 == 0 and wt // 2 <= 64   # whole groups of the swizzle

@@ -72,11 +72,12 @@ def test_each_kernel(M, N, K, pad, variant):
         check_forward(h, gw, uw, mode="hf", gu=True)
 
 
-# tiles of 32 to 224 tokens, several rounds of them, ragged in every dimension; the
-# last two with 256 rows
+# tiles of 32 to 224 tokens and of 80, 96 and 128 outputs, several rounds of them, ragged
+# in every dimension; (1100, ..) and (2100, ..) with 256 rows
 @pytest.mark.parametrize("M,N,K", [(479, 520, 2048), (459, 1000, 152), (289, 2500, 352), (330, 2500, 1064), (160, 9729, 1000),
                                    (565, 2500, 1528), (333, 9728, 2560), (400, 9730, 2568), (66, 14336, 264), (1100, 2500, 136),
-                                   (2100, 1300, 264)])
+                                   (2100, 1300, 264), (17, 11008, 1096), (100, 10999, 2056), (130, 6999, 2056), (66, 13000, 1032),
+                                   (333, 3300, 2056), (200, 300, 4096)])
 @pytest.mark.parametrize("mode", ["fused", "hf"])
 def test_tiles_of_tokens(M, N, K, mode):
     check_forward(*operands(M, N, K, seed=M), mode=mode)
