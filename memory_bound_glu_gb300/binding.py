@@ -272,29 +272,33 @@ class DualWeightGlu(torch.autograd.Function):
 
     Up to MAX_M rows run glu_gemv and glu_backward; more run glu_gemm, which
     keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward.  There is no second
-    derivative: asking for it raises a RuntimeError.  Where no gradient can
-    follow, apply is the forward call alone.  To capture a training step into a
+    derivative and no forward-mode one: asking for either raises.  Where no
+    gradient can follow, nothing is kept.  To capture a training step into a
     CUDA graph, run it on the capture's stream first and let no eager graph over
     the same leaves live meanwhile, as for any autograd Function."""
 
     @classmethod
-    def apply(cls, h, gate_w, up_w, mode="fused"):
-        if not (torch.is_grad_enabled() and (h.requires_grad or gate_w.requires_grad or up_w.requires_grad)):
-            return (glu_gemm if h.dim() == 2 and h.shape[0] > MAX_M else glu_gemv)(h, gate_w, up_w, mode=mode)
-        if h.dim() == 2 and h.shape[0] > MAX_M:   # the same node without Python, in its common case
+    def apply(cls, h, gate_w, up_w, mode="fused", keep=None):
+        # keep: whether a backward can follow, which forward cannot see (grad mode is
+        # off inside it).  Decided here, whatever was passed: a trace calls apply
+        # again with the arguments that it recorded.
+        keep = torch.is_grad_enabled() and (h.requires_grad or gate_w.requires_grad or up_w.requires_grad)
+        if keep and h.dim() == 2 and h.shape[0] > MAX_M:   # the same node without Python, in its common case
             out = (_quick_module or _quick()).wide_glu(h, gate_w, up_w, _MODES[mode])
             if out is not None:
                 return out
-        return super().apply(h, gate_w, up_w, mode)
+        return super().apply(h, gate_w, up_w, mode, keep)
 
     @staticmethod
-    def forward(ctx, h, gate_w, up_w, mode="fused"):
+    def forward(ctx, h, gate_w, up_w, mode="fused", keep=True):
         if h.dim() == 2 and h.shape[0] > MAX_M:
-            gu = torch.empty((h.shape[0], 2 * gate_w.shape[0]), dtype=torch.float32, device=h.device)
+            gu = torch.empty((h.shape[0], 2 * gate_w.shape[0]), dtype=torch.float32, device=h.device) if keep else None
             out = glu_gemm(h, gate_w, up_w, mode=mode, gu=gu)
-            ctx.save_for_backward(h, gate_w, up_w, gu)
+            if keep:
+                ctx.save_for_backward(h, gate_w, up_w, gu)
             return out
-        ctx.save_for_backward(h, gate_w, up_w)
+        if keep:
+            ctx.save_for_backward(h, gate_w, up_w)
         return glu_gemv(h, gate_w, up_w, mode=mode)
 
     @staticmethod
@@ -313,7 +317,7 @@ class DualWeightGlu(torch.autograd.Function):
             gh, gg, gu = glu_backward(h2, gate_w, up_w, d2, **want)
         if gh is not None and squeeze:
             gh = gh.view(-1)
-        return gh, gg if ctx.needs_input_grad[1] else None, gu if ctx.needs_input_grad[2] else None, None
+        return gh, gg if ctx.needs_input_grad[1] else None, gu if ctx.needs_input_grad[2] else None, None, None
 
 
 def new_workspace(device=None):
