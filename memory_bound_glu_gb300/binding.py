@@ -283,7 +283,8 @@ class DualWeightGlu(torch.autograd.Function):
         # off inside it).  Decided here, whatever was passed: a trace calls apply
         # again with the arguments that it recorded.
         keep = torch.is_grad_enabled() and (h.requires_grad or gate_w.requires_grad or up_w.requires_grad)
-        if keep and h.dim() == 2 and h.shape[0] > MAX_M:   # the same node without Python, in its common case
+        # the same node without Python, in its common case; a tracer does not see it
+        if keep and not torch.jit.is_tracing() and h.dim() == 2 and h.shape[0] > MAX_M:
             out = (_quick_module or _quick()).wide_glu(h, gate_w, up_w, _MODES[mode])
             if out is not None:
                 return out
