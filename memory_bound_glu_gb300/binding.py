@@ -264,31 +264,9 @@ def glu_backward(h, gate_w, up_w, dout, grad_h=None, grad_gate=None, grad_up=Non
     return grad_h, grad_gate, grad_up
 
 
-class DualWeightGlu(torch.autograd.Function):
-    """out = SiLU(h @ gate_w.T) * (h @ up_w.T) with the weights read in place
-    and gradients for h, gate_w and up_w ([8602/PlanB] "Plan B Design": the
-    Function works on the model's own weight tensors, not on a copy, so their
-    gradients land on those tensors).
-
-    Up to MAX_M rows run glu_gemv and glu_backward; more run glu_gemm, which
-    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward.  There is no second
-    derivative and no forward-mode one: asking for either raises.  Where no
-    gradient can follow, nothing is kept.  To capture a training step into a
-    CUDA graph, run it on the capture's stream first and let no eager graph over
-    the same leaves live meanwhile, as for any autograd Function."""
-
-    @classmethod
-    def apply(cls, h, gate_w, up_w, mode="fused", keep=None):
-        # keep: whether a backward can follow, which forward cannot see (grad mode is
-        # off inside it).  Decided here, whatever was passed: a trace calls apply
-        # again with the arguments that it recorded.
-        keep = torch.is_grad_enabled() and (h.requires_grad or gate_w.requires_grad or up_w.requires_grad)
-        # the same node without Python, in its common case; a tracer does not see it
-        if keep and not torch.jit.is_tracing() and h.dim() == 2 and h.shape[0] > MAX_M:
-            out = (_quick_module or _quick()).wide_glu(h, gate_w, up_w, _MODES[mode])
-            if out is not None:
-                return out
-        return super().apply(h, gate_w, up_w, mode, keep)
+class _GluNode(torch.autograd.Function):
+    """The autograd node of DualWeightGlu.  keep: whether a backward can follow,
+    which forward cannot see (grad mode is off inside it)."""
 
     @staticmethod
     def forward(ctx, h, gate_w, up_w, mode="fused", keep=True):
@@ -319,6 +297,32 @@ class DualWeightGlu(torch.autograd.Function):
         if gh is not None and squeeze:
             gh = gh.view(-1)
         return gh, gg if ctx.needs_input_grad[1] else None, gu if ctx.needs_input_grad[2] else None, None, None
+
+
+class DualWeightGlu(_GluNode):
+    """out = SiLU(h @ gate_w.T) * (h @ up_w.T) with the weights read in place
+    and gradients for h, gate_w and up_w ([8602/PlanB] "Plan B Design": the
+    Function works on the model's own weight tensors, not on a copy, so their
+    gradients land on those tensors).
+
+    Up to MAX_M rows run glu_gemv and glu_backward; more run glu_gemm, which
+    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward.  There is no second
+    derivative and no forward-mode one: asking for either raises.  Where no
+    gradient can follow, nothing is kept.  To capture a training step into a
+    CUDA graph, run it on the capture's stream first and let no eager graph over
+    the same leaves live meanwhile, as for any autograd Function."""
+
+    @classmethod
+    def apply(cls, h, gate_w, up_w, mode="fused"):
+        tracing = torch.jit.is_tracing()   # what a trace runs on later may have gradients
+        keep = tracing or torch.is_grad_enabled() and (h.requires_grad or gate_w.requires_grad or up_w.requires_grad)
+        # the same node without Python, in its common case; a tracer does not see it and
+        # torch's compiler does not know it
+        if keep and not (tracing or torch.compiler.is_compiling()) and h.dim() == 2 and h.shape[0] > MAX_M:
+            out = (_quick_module or _quick()).wide_glu(h, gate_w, up_w, _MODES[mode])
+            if out is not None:
+                return out
+        return _GluNode.apply(h, gate_w, up_w, mode, keep)
 
 
 def new_workspace(device=None):

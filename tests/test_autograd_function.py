@@ -109,3 +109,17 @@ def test_function_transforms_are_refused(calls, M):
         torch.func.grad(lambda x: mb.DualWeightGlu.apply(x, gate_w, up_w).sum())(h)
     with pytest.raises(RuntimeError):
         torch.func.vmap(lambda x: mb.DualWeightGlu.apply(x, gate_w, up_w))(torch.stack([h, h]))
+
+
+@pytest.mark.parametrize("M", [4, 100])
+@pytest.mark.parametrize("grad", [False, True])
+def test_inside_a_compiled_function(calls, M, grad):
+    torch._dynamo.reset()
+    f = torch.compile(lambda *a: mb.DualWeightGlu.apply(*a) * 2, backend="eager")
+    for seed in (0, 1):
+        ops = operands(M, seed=seed, grad=grad)
+        out = f(*ops)
+        assert right(out / 2, ops) and out.requires_grad == grad
+        with torch.no_grad():
+            assert right(f(*ops) / 2, ops)
+    torch._dynamo.reset()
