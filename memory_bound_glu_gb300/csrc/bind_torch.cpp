@@ -183,7 +183,9 @@ struct WideGlu : torch::autograd::Function<WideGlu> {
         torch::autograd::variable_list out(4);
         if (!grads[0].defined()) return out;
         at::Tensor d = grads[0].to(kBf16);
-        if (d.stride(1) != 1 || d.stride(0) < N) d = d.contiguous();   // a broadcast gradient (of a sum) has stride 0
+        // a broadcast gradient (of a sum) has stride 0; a single column may have any, and
+        // counts as contiguous all the same: a copy has the strides of its shape
+        if (d.stride(1) != 1 || d.stride(0) < N) d = d.clone(at::MemoryFormat::Contiguous);
         Operand a, g, u, dd, oh, og, ou;
         TORCH_CHECK(operand(h, kBf16, M, K, dev, a) && operand(gate, kBf16, N, K, dev, g) && operand(up, kBf16, N, K, dev, u) &&
                         operand(d, kBf16, M, N, dev, dd),
