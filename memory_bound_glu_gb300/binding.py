@@ -287,8 +287,10 @@ class _GluNode(torch.autograd.Function):
         squeeze = h.dim() == 1
         h2 = h.unsqueeze(0) if squeeze else h
         d2 = dout.reshape(h2.shape[0], -1).to(torch.bfloat16)
-        if d2.stride(-1) != 1 or d2.stride(0) < d2.shape[1]:   # a broadcast gradient (of a sum) has stride 0
-            d2 = d2.contiguous()
+        # a broadcast gradient (of a sum) has stride 0; a single column or row may have any,
+        # and counts as contiguous all the same: a copy has the strides of its shape
+        if d2.stride(-1) != 1 or d2.stride(0) < d2.shape[1]:
+            d2 = d2.clone(memory_format=torch.contiguous_format)
         want = dict(want_h=ctx.needs_input_grad[0], want_w=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
         if rest:
             gh, gg, gu = glu_gemm_backward(h2, gate_w, up_w, d2, gu=rest[0], **want)

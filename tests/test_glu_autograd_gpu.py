@@ -16,9 +16,9 @@ def leaves_of(ops):
     return [t.clone().requires_grad_(True) for t in ops]
 
 
-@pytest.mark.parametrize("M", [100])
+@pytest.mark.parametrize("M", [1, *ROWS])
 @pytest.mark.parametrize("N", [1, 2, 40])
-@pytest.mark.parametrize("layout", ["rows", "columns", "strided", "broadcast"])
+@pytest.mark.parametrize("layout", ["rows", "columns", "strided", "broadcast", "row of any stride"])
 def test_gradients_of_any_layout(M, N, layout):
     """What arrives at the node is the caller's tensor: a transposed one, one column of
     a wider matrix, a single value for all."""
@@ -28,6 +28,8 @@ def test_gradients_of_any_layout(M, N, layout):
         d = rand(N, M, seed=7).t()
     elif layout == "strided":
         d = rand(M, 2 * N, seed=7)[:, ::2]
+    elif layout == "row of any stride":
+        d = rand(M, N, seed=7).as_strided((M, N), (1, 1)) if M == 1 else rand(M, N, seed=7)
     elif layout == "broadcast":
         d = rand(1, 1, seed=7).expand(M, N)
     else:
@@ -39,7 +41,7 @@ def test_gradients_of_any_layout(M, N, layout):
     assert mb.read_device_error() == 0
 
 
-@pytest.mark.parametrize("M", [100])
+@pytest.mark.parametrize("M", ROWS)
 def test_a_column_through_a_transposed_product(M):
     ops = operands(M, 1, 48, seed=M)
     w = rand(1, M, seed=8)
