@@ -16,8 +16,6 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmbglu.so")
 QUICK = os.path.join(HERE, "_mbglu_torch.so")   # the binding's extension module
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("mbglu_api.cu", "gemm_api.cu", "fp8_api.cu")]
-DEPS = [os.path.join(HERE, "csrc", f) for f in sorted(os.listdir(os.path.join(HERE, "csrc")))] + \
-    [os.path.join(ROOT, "include", "mbglu.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -35,14 +33,35 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def quick_stamp() -> str:
+    """What the extension module is built against: it fits no other torch or Python."""
+    import torch
+    return f"built for torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def quick_is_current() -> bool:
+    """Whether the extension module is there and fits the torch that is installed: its
+    description says what it was built against."""
+    try:
+        with open(QUICK, "rb") as f:
+            return quick_stamp().encode() + b"\0" in f.read()
+    except OSError:
+        return False
+
+
+def _sources_and_headers():
+    csrc = os.path.join(HERE, "csrc")
+    return [os.path.join(csrc, f) for f in sorted(os.listdir(csrc))] + [os.path.join(ROOT, "include", "mbglu.h")]
+
+
 def needs_build(out: str = LIB) -> bool:
-    if not os.path.exists(out) or not os.path.exists(QUICK):
+    if not os.path.exists(out) or not quick_is_current():
         return True
     t = min(os.path.getmtime(out), os.path.getmtime(QUICK))
-    return any(os.path.getmtime(f) > t for f in DEPS)
+    return any(os.path.getmtime(f) > t for f in _sources_and_headers())
 
 
-def build_quick(out: str = QUICK) -> str:
+def build_quick() -> str:
     """The binding's extension module, against the torch that is installed."""
     import sysconfig
 
@@ -51,11 +70,14 @@ def build_quick(out: str = QUICK) -> str:
     inc = [os.path.join(ROOT, "include"), os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
            os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
+    if os.path.exists(QUICK):   # a failing build leaves no old module behind
+        os.remove(QUICK)
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f'-DMBGLU_BUILT_FOR="{quick_stamp()}"',
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f for i in inc for f in ("-I", i)),
-                    "-o", out, os.path.join(HERE, "csrc", "bind_torch.cpp"), "-L", os.path.join(base, "lib"),
+                    "-o", QUICK, os.path.join(HERE, "csrc", "bind_torch.cpp"), "-L", os.path.join(base, "lib"),
                     "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"], check=True)
-    return out
+    return QUICK
 
 
 def build(out: str = LIB, verbose: bool = False, extra=()) -> str:
@@ -72,9 +94,11 @@ def build(out: str = LIB, verbose: bool = False, extra=()) -> str:
     with tempfile.TemporaryDirectory() as tmp:
         objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in SOURCES]
         with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-            for f in [ex.submit(build_quick)] + [ex.submit(one, s, o) for s, o in zip(SOURCES, objs)]:
+            quick = ex.submit(build_quick)
+            for f in [ex.submit(one, s, o) for s, o in zip(SOURCES, objs)]:
                 f.result()
         subprocess.run([nvcc(), *NVCC_FLAGS, "-o", out, *objs], check=True)
+    quick.result()
     return out
 
 

@@ -15,9 +15,10 @@ import os
 
 import torch
 
+from . import _build
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmbglu.so")
-QUICK_PATH = os.path.join(HERE, "_mbglu_torch.so")
 
 MODE_FUSED = 0
 MODE_HF = 1
@@ -122,12 +123,13 @@ def lib():
 def _quick():
     """The extension module that does the common case of the wide and the e4m3
     calls without Python's checks (csrc/bind_torch.cpp); None from one of its
-    functions means that the call is not that case and comes here."""
+    functions means that the call is not that case and comes here.  One that was
+    built against another torch is not loaded."""
     global _quick_module
     if _quick_module is None:
         l = lib()
-        if not os.path.exists(QUICK_PATH):
-            raise RuntimeError(f"{QUICK_PATH} is missing: build it with "
+        if not _build.quick_is_current():
+            raise RuntimeError(f"{_build.QUICK} is missing or was built against another torch: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         m = importlib.import_module("._mbglu_torch", __package__)
         m.bind(*(ctypes.cast(getattr(l, n), ctypes.c_void_p).value

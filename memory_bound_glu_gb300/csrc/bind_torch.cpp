@@ -386,7 +386,8 @@ PyMethodDef methods[] = {
     MBGLU_METHOD("glu_fp8", py_glu),       MBGLU_METHOD("matmul_fp8", py_matmul),
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mbglu_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// MBGLU_BUILT_FOR: the torch and the Python whose headers this was compiled with
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mbglu_torch", MBGLU_BUILT_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
