@@ -9,6 +9,7 @@ import os
 import subprocess
 import sys
 import tempfile
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -82,7 +83,9 @@ def build_quick() -> str:
 
 def build(out: str = LIB, verbose: bool = False, extra=()) -> str:
     """Compiles the translation units in parallel, then links them; beside
-    them the binding's extension module."""
+    them the binding's extension module.  That one needs Python's and torch's
+    headers and a CUDA build of torch, the library none of them: where the module
+    cannot be built, a warning says so and binding.py does without it."""
     compile_flags = [f for f in NVCC_FLAGS if f != "-shared"]
 
     def one(src, obj):
@@ -98,7 +101,11 @@ def build(out: str = LIB, verbose: bool = False, extra=()) -> str:
             for f in [ex.submit(one, s, o) for s, o in zip(SOURCES, objs)]:
                 f.result()
         subprocess.run([nvcc(), *NVCC_FLAGS, "-o", out, *objs], check=True)
-    quick.result()
+    try:
+        quick.result()
+    except Exception as e:
+        warnings.warn(f"the binding's extension module was not built ({e}): the wide and the e4m3 calls take 10 to 15 us "
+                      "more of host time")
     return out
 
 

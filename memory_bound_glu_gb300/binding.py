@@ -3,8 +3,8 @@
 Argument marshalling only: tensors become device pointers, row strides and
 the current CUDA stream; every step of the computation runs in the library's
 kernels.  The wide and the e4m3 calls marshal their common case in an extension
-module (csrc/bind_torch.cpp).  There is no fallback: if the library is missing or a call fails,
-an exception is raised.
+module (csrc/bind_torch.cpp), and here where that is not built.  There is no
+fallback for the library: if it is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import importlib
 import os
+import warnings
 
 import torch
 
@@ -120,6 +121,14 @@ def lib():
     return _lib
 
 
+class _NoModule:
+    """Stands in for the extension module where there is none: no call is its
+    common case, so binding.py does them all."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _quick():
     """The extension module that does the common case of the wide and the e4m3
     calls without Python's checks (csrc/bind_torch.cpp); None from one of its
@@ -129,8 +138,10 @@ def _quick():
     if _quick_module is None:
         l = lib()
         if not _build.quick_is_current():
-            raise RuntimeError(f"{_build.QUICK} is missing or was built against another torch: build it with "
-                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+            warnings.warn(f"{_build.QUICK} is missing or was built against another torch: calls take 10 to 15 us more of host "
+                          "time (build it with `python -c 'import __graft_entry__ as g; g.build()'`)")
+            _quick_module = _NoModule()
+            return _quick_module
         m = importlib.import_module("._mbglu_torch", __package__)
         m.bind(*(ctypes.cast(getattr(l, n), ctypes.c_void_p).value
                  for n in ("glu_gemm", "glu_gemm_backward", "glu_gemm_backward_workspace_bytes", "add_rmsnorm_fp8", "glu_fp8",

@@ -1,11 +1,12 @@
-"""The build's two products: the library, and the binding's extension module, which
-fits one torch."""
+"""The build's two products: the library, which needs nvcc alone, and the binding's
+extension module, which fits one torch and may be missing."""
 import os
 import subprocess
 
 import pytest
 import torch
 
+import memory_bound_glu_gb300 as mb
 from memory_bound_glu_gb300 import _build, binding
 
 
@@ -40,6 +41,16 @@ def test_both_products(tree):
     assert _build.quick_is_current() and not _build.needs_build(str(path / "lib.so"))
 
 
+def test_the_library_without_the_module(tree):
+    path, fails = tree
+    build(path)
+    fails.add("g++")
+    with pytest.warns(UserWarning, match="not built"):
+        build(path)
+    assert (path / "lib.so").exists()
+    assert not (path / "quick.so").exists() and not _build.quick_is_current()   # nor an old one
+
+
 def test_a_library_that_fails_is_an_error(tree):
     path, fails = tree
     fails.add("nvcc")
@@ -55,14 +66,22 @@ def test_a_module_of_another_torch_is_stale(tree, monkeypatch):
 
 
 @pytest.mark.parametrize("stale", [False, True])
-def test_the_binding_loads_no_such_module(tree, monkeypatch, stale):
+def test_the_binding_without_the_module(tree, monkeypatch, stale):
+    """Every call goes to the library through binding.py, with its own errors."""
     path, _ = tree
     if stale:
         build(path)
         monkeypatch.setattr(torch, "__version__", "1.0")
     monkeypatch.setattr(binding, "_quick_module", None)
-    with pytest.raises(RuntimeError, match="another torch"):
-        binding._quick()
+    with pytest.warns(UserWarning, match="another torch"):
+        q = binding._quick()
+    for name in ("glu_gemm", "wide_glu", "glu_gemm_backward", "add_rmsnorm_fp8", "glu_fp8", "matmul_fp8"):
+        assert getattr(q, name)(1, 2, 3) is None
+    assert binding._quick() is q
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        mb.glu_gemm(None, None, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        mb.matmul_fp8(torch.zeros(1, 128).to(mb.E4M3), None, None, None)
 
 
 def test_the_built_module_says_what_it_is_for():
