@@ -514,8 +514,8 @@ int mbglu_last_cuda_error(void);
  * 5 silu_mul, 6 gdn_gates, 7 row blocks (a batch above MBGLU_BLOCK_M: one
  * of 1, 2, 4, 10 per block), 8 glu_backward, 9 the tcgen05 kernel (a batch
  * above MBGLU_BLOCK_M in one pass), 10 the K-slice tensor-core kernel (h's
- * fragments in registers, batch 1..16); glu_gemm: 11 the CTA-pair tcgen05
- * kernel, 12 the kernel for any alignment; 13 glu_gemm_backward, 14
+ * fragments in registers, batch 1..16); glu_gemm: 11 a CTA-pair tcgen05
+ * kernel (which: mbglu_block_plan), 12 the kernel for any alignment; 13 glu_gemm_backward, 14
  * add_rmsnorm_fp8; e4m3 products: 15 the CTA-pair tcgen05 kernel, 16 the kernel
  * for few rows, 17 the kernel for any alignment; 18 quantize_weight_fp8. */
 int mbglu_last_variant(void);
@@ -536,6 +536,22 @@ int mbglu_last_backward_path(void);
  * as the single kernel (the workspace / no-allocation paths); 0 when every
  * block took the two-kernel path or the call launched nothing. */
 int mbglu_last_single_kernel_blocks(void);
+
+/* How a product of the gated block is laid out for operands that tensor copies
+ * take (host only; nothing is launched).  The six ints written at `plan`:
+ *   [0] 1 where the weights take the MMA's 128 or 256 rows (the kernels for few
+ *       rows or few tiles), 0 for 256-row tiles of tokens on CTA pairs
+ *   [1] tokens and [2] outputs per tile (of the weight gradients: N and K)
+ *   [3] tiles done whole, [4] tiles in ranges of the inner dimension, and
+ *   [5] the ranges of each (with [0] = 1 every tile's, added up in a cluster)
+ * glu_gemm: of the call with gu, or from 17 rows on.  Sizes from 1 on.
+ * MBGLU_ERR_NULL, MBGLU_ERR_MODE (an unknown product), MBGLU_ERR_SHAPE. */
+#define MBGLU_PRODUCT_GLU_GEMM   0
+#define MBGLU_PRODUCT_GRAD_H     1   /* glu_gemm_backward's grad_h */
+#define MBGLU_PRODUCT_GRAD_W     2   /* its grad_gate and grad_up */
+#define MBGLU_PRODUCT_GLU_FP8    3
+#define MBGLU_PRODUCT_MATMUL_FP8 4
+mbglu_status mbglu_block_plan(int product, int M, int N, int K, int *plan);
 
 /* Diagnostics: copies the first `count` ints of the current device's
  * add_rmsnorm_glu_noalloc scratch array to host memory `words`, after a

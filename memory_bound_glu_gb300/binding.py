@@ -36,7 +36,7 @@ EXPORTS = ("glu_gemv", "add_rmsnorm_glu", "add_rmsnorm_glu_ws", "add_rmsnorm_glu
            "mbglu_set_launch_policy",
            "mbglu_get_launch_policy",
            "mbglu_status_string", "mbglu_abi_version", "mbglu_last_cuda_error", "mbglu_last_variant",
-           "mbglu_last_single_kernel_blocks", "mbglu_noalloc_scratch_read", "mbglu_read_device_error",
+           "mbglu_last_single_kernel_blocks", "mbglu_block_plan", "mbglu_noalloc_scratch_read", "mbglu_read_device_error",
            "mbglu_last_backward_path")
 POLICY_SERIAL, POLICY_PDL, POLICY_PREFETCH = 0, 1, 2
 
@@ -100,6 +100,8 @@ def _bind(l):
     l.mbglu_last_variant.restype = i32
     l.mbglu_last_single_kernel_blocks.restype = i32
     l.mbglu_last_backward_path.restype = i32
+    l.mbglu_block_plan.argtypes = [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_int)]
+    l.mbglu_block_plan.restype = i32
     l.mbglu_noalloc_scratch_read.argtypes = [ctypes.POINTER(ctypes.c_int), i32]
     l.mbglu_noalloc_scratch_read.restype = i32
     l.mbglu_read_device_error.argtypes = [ctypes.POINTER(ctypes.c_int)]
@@ -771,6 +773,21 @@ def last_backward_path() -> int:
     cores; of glu_gemm_backward: 4 the CTA-pair tcgen05 kernels, 5 the kernels
     for any alignment."""
     return lib().mbglu_last_backward_path()
+
+
+PRODUCTS = ("glu_gemm", "grad_h", "grad_w", "glu_fp8", "matmul_fp8")
+
+
+def block_plan(product, M, N, K):
+    """How a product of the gated block (one of PRODUCTS) is laid out for operands
+    that tensor copies take: (1 for the kernels of few rows or few tiles, tokens and
+    outputs per tile, tiles done whole, tiles in ranges, ranges of each); see
+    include/mbglu.h."""
+    plan = (ctypes.c_int * 6)()
+    st = lib().mbglu_block_plan(PRODUCTS.index(product), M, N, K, plan)
+    if st != 0:
+        raise MbgluError(st, "mbglu_block_plan")
+    return tuple(plan)
 
 
 def read_device_error() -> int:

@@ -12,7 +12,7 @@ namespace mbglu_host {
 
 // mbglu_last_variant codes of the operators outside mbglu_api.cu
 enum DenseVariant {
-    kPairGemm = 11,      // glu_gemm on the CTA-pair tcgen05 kernel
+    kPairGemm = 11,      // glu_gemm on a CTA-pair tcgen05 kernel
     kGemmGeneric = 12,   // glu_gemm on the kernel for any alignment
     kGemmBackward = 13,  // glu_gemm_backward
     kNormFp8 = 14,       // add_rmsnorm_fp8
@@ -31,6 +31,9 @@ int launch_policy();
 // in 128-byte swizzled boxes; false where the driver takes no such map.
 bool encode_tile_map(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, int cols, int box_cols,
                      int box_rows, int elem_bytes);
+
+// mbglu_block_plan's answer for the e4m3 products
+void fp8_block_plan(bool dual, int M, int N, int K, int *plan);
 
 // Reads and clears the unit's device error word; the device is idle.
 cudaError_t take_gemm_error(int *w);

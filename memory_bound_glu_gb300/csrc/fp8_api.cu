@@ -474,6 +474,19 @@ mbglu_status glu_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_
 
 namespace mbglu_host {
 
+void fp8_block_plan(bool dual, int M, int N, int K, int *plan)
+{
+    const Fp8Plan f = fp8_plan(M, N, K, dual);
+    if (f.use_tall) {
+        const int tiles = ceil_div(N, mbglu::kTallRows) * ceil_div(M, f.tall.tn), split = f.tall.ks > 1;
+        const int got[6] = {1, f.tall.tn, mbglu::kTallRows, split ? 0 : tiles, split ? tiles : 0, f.tall.ks};
+        std::copy(got, got + 6, plan);
+    } else {
+        const int got[6] = {0, mbglu::kPairTile, dual ? 128 : mbglu::kPairTile, f.pair.whole, f.pair.rest, f.pair.splits};
+        std::copy(got, got + 6, plan);
+    }
+}
+
 cudaError_t take_fp8_error(int *w)
 {
     cudaError_t e = cudaMemcpyFromSymbol(w, mbglu::g_dense_error, sizeof *w);

@@ -391,6 +391,30 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf1
     return st;
 }
 
+mbglu_status mbglu_block_plan(int product, int M, int N, int K, int *plan)
+{
+    if (!plan) return MBGLU_ERR_NULL;
+    if (product < MBGLU_PRODUCT_GLU_GEMM || product > MBGLU_PRODUCT_MATMUL_FP8) return MBGLU_ERR_MODE;
+    if (bad_sizes(M, N, K) || std::min({M, N, K}) < 1 || N > INT32_MAX / 2) return MBGLU_ERR_SHAPE;
+    if (product >= MBGLU_PRODUCT_GLU_FP8) {
+        fp8_block_plan(product == MBGLU_PRODUCT_GLU_FP8, M, N, K, plan);
+        return MBGLU_OK;
+    }
+    const int tn = product == MBGLU_PRODUCT_GLU_GEMM ? tall_tokens(M, N, K) : 0;
+    if (tn) {
+        const int wt = tall_outputs(M, N, tn);
+        const int got[6] = {1, tn, wt, ceil_div(N, wt) * ceil_div(M, tn), 0, 1};
+        std::copy(got, got + 6, plan);
+        return MBGLU_OK;
+    }
+    const mbglu::PairPlan p = product == MBGLU_PRODUCT_GRAD_H   ? grad_h_plan(M, N, K)
+                              : product == MBGLU_PRODUCT_GRAD_W ? grad_w_plan(M, N, K)
+                                                                : pair_plan(M, N, 128, 1, 0, ceil_div(K, 64), false);
+    const int got[6] = {0, mbglu::kPairTile, product == MBGLU_PRODUCT_GLU_GEMM ? 128 : mbglu::kPairTile, p.whole, p.rest, p.splits};
+    std::copy(got, got + 6, plan);
+    return MBGLU_OK;
+}
+
 }  // extern "C"
 
 namespace mbglu_host {
