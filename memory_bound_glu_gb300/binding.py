@@ -323,7 +323,8 @@ class DualWeightGlu(_GluNode):
     gradients land on those tensors).
 
     Up to MAX_M rows run glu_gemv and glu_backward; more run glu_gemm, which
-    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward.  There is no second
+    keeps g and u in fp32 (8 M N bytes) for glu_gemm_backward, whose gradients carry
+    one bf16 rounding more (of the products' gradients dG and dU).  There is no second
     derivative and no forward-mode one: asking for either raises.  Where no
     gradient can follow, nothing is kept.  To capture a training step into a
     CUDA graph, run it on the capture's stream first and let no eager graph over

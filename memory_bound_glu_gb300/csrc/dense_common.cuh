@@ -1,8 +1,9 @@
 // dense_common.cuh -- device helpers of the gated block beyond the decode
 // batch.  Its kernels may start before the one ahead of them has ended and then
 // wait for it, so what that one may have written is read with plain loads, never
-// with read-only ones, whose data may not change while a kernel runs.  Here: the gradients of the GLU, e4m3 conversions and a group's scale, and
-// stores of 32 consecutive columns of one row.
+// with read-only ones, whose data may not change while a kernel runs.  Here: the
+// gradients of the GLU, e4m3 conversions and a group's scale, and stores of 32
+// consecutive columns of one row.
 #pragma once
 #include <cuda_fp16.h>
 #include <cstdint>
@@ -20,9 +21,10 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleMin = 1.17549435e-38f;      // 2^-126: the scale of a group of zeros
 
 // e^-|x|.  With z = |x| log2(e) rounded and r what the rounding left out,
-// e^-|x| = 2^-z (1 - r ln 2): relative error below 2^-21 over the whole range
-// (2^-z alone is off by |x| 2^-24).  |x| is capped where the result is 0 anyway,
-// so that infinities leave no inf - inf.
+// e^-|x| = 2^-z (1 - r ln 2): relative error below 2^-21 (2^-z alone is off by
+// |x| 2^-24) up to |x| = 87.  Beyond, the result is an fp32 subnormal of at most three
+// roundings of 2^-149 (at |x| = 100 up to a tenth of it), as expf's would be of one.
+// |x| is capped where the result is 0 anyway, so that infinities leave no inf - inf.
 __device__ __forceinline__ float exp_neg_abs(float x)
 {
     constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
@@ -34,8 +36,9 @@ __device__ __forceinline__ float exp_neg_abs(float x)
     return fmaf(t * r, -kLn2, t);
 }
 
-// SiLU(x), relative error below 2^-20, in a third of the instructions of the
-// precise form (silu_f32).  An epilogue that is unrolled over a thread's 64
+// SiLU(x) in a third of the instructions of the precise form (silu_f32): relative
+// error below 2^-20, and for x < -87 an error below |x| 2^-146, which is a bf16 step's
+// 2^-133 and more only beside results that bf16 no longer holds.  An epilogue that is unrolled over a thread's 64
 // outputs is bound by fetching its instructions once per tile: glu_fp8's at
 // M = 48, K = 128 took 17.0 us with the precise form.
 __device__ __forceinline__ float silu_short(float x)
@@ -51,7 +54,13 @@ __device__ __forceinline__ uint32_t glu_hf_short(float g, float u)
 }
 
 // dG = dout u SiLU'(g), dU = dout SiLU(g), in fp32: with s the sigmoid,
-// SiLU' = s (1 + g (1 - s))
+// SiLU' = s (1 + g (1 - s)).
+//
+// The callers round both once to bf16, because they are the tensor cores' operands in
+// the gradients' products: each gradient then carries two roundings, an error of
+// 2.35e-3 in the 2-norm where one rounding leaves 1.66e-3 (333 x 1000 x 2504).  Kept
+// whole, as three bf16 terms each (glu_backward, up to 64 rows, where the weights'
+// bytes bound it), they would triple products that are bound by the tensor cores.
 __device__ __forceinline__ void glu_gradients(float g, float u, float d, float &dg, float &du)
 {
     const float t = exp_neg_abs(g), inv = __fdividef(1.0f, 1.0f + t);

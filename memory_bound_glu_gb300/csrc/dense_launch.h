@@ -42,8 +42,11 @@ struct DeviceTable {
 inline mbglu_status launched(cudaError_t e) { return e == cudaSuccess ? MBGLU_OK : cuda_fail(e); }
 
 // Launch configuration with the process's launch policy: under PDL a kernel may
-// be scheduled while its predecessor drains (every kernel here waits for the
-// predecessor before it touches global memory).
+// be scheduled while its predecessor drains.  Every kernel launched here waits for the
+// predecessor before it touches global memory, but for fp8_tall_kernel: under the
+// prefetch policy it copies its first weights before the wait, so a kernel of the
+// library that writes weights (quant_weight_kernel) neither releases its dependents
+// early nor leaves its stores to be performed later.
 struct Launch {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

@@ -87,6 +87,14 @@ constexpr int kDecodeRows = 16;   // glu_gemv's, at any alignment
 // within 1% of the fastest on average, 7% at worst, never slower than
 // pair_gemm_kernel and 24% faster on average (K = 2560, N = 9728 at M = 333: 27.9 us
 // against 31.2; K = 1000, N = 2504: 9.2 and 11.3; K = 4096, N = 300: 13.0 and 22.9).
+// Outside the fit, over N = 300 to 14336 and K = 264 to 9728: at 17 to 64 rows (175
+// calls) within 4% of the fastest of tn = 32 to 128, and pair_gemm_kernel takes 1.05 to
+// 2.2 times as long; at 1024 to 8192 rows (245 calls) never slower than
+// pair_gemm_kernel and 25% faster on average where it takes a tn.  Where it keeps
+// pair_gemm_kernel there, a tn would be faster in a third of the calls, by 7% on average
+// (3000 x 2560 -> 2560: 50.5 us, 44.5 with tn = 160; 3000 x 264 -> 300: 8.4 and 6.5 with 128).
+// The estimate ranks kernels and is no time: it knows nothing of the weights' bytes,
+// and tall_outputs' narrower tiles are chosen after it.
 int tall_tokens(int M, int N, int K)
 {
     const int64_t chunks = ceil_div(K, 64), nt = ceil_div(N, 128), tiles = nt * ceil_div(M, mbglu::kPairTile);

@@ -3,6 +3,7 @@ and compiled functions, on both sides of the change from glu_gemv to glu_gemm.""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
+import torch.utils.checkpoint
 
 import memory_bound_glu_gb300 as mb
 from test_glu_gemm_gpu import BF, DEV, backward_reference, operands, rand
@@ -80,3 +81,56 @@ def test_trace_and_compile(M, grad):
             assert torch.equal(out, want)
             assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(out, leaves, d), torch.autograd.grad(want, plain, d)))
     torch._dynamo.reset()
+
+
+@pytest.mark.parametrize("M", ROWS)
+def test_saved_tensors_elsewhere_and_computed_again(M):
+    """Saved tensors on the host, and a forward that is run again in the backward."""
+    ops, d = operands(M, 40, 48, seed=M), rand(M, 40, seed=9)
+    leaves = leaves_of(ops)
+    want = torch.autograd.grad(mb.DualWeightGlu.apply(*leaves), leaves, d)
+    with torch.autograd.graph.save_on_cpu():
+        out = mb.DualWeightGlu.apply(*leaves)
+    runs = [torch.autograd.grad(out, leaves, d)]
+    for reentrant in (False, True):
+        out = torch.utils.checkpoint.checkpoint(mb.DualWeightGlu.apply, *leaves, use_reentrant=reentrant)
+        for t in leaves:
+            t.grad = None
+        out.backward(d)   # a reentrant checkpoint takes no other call
+        runs.append([t.grad for t in leaves])
+    for got in runs:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_an_operand_changed_before_the_backward_is_an_error(M, which):
+    leaves = leaves_of(operands(M, 40, 48, seed=M))
+    out = mb.DualWeightGlu.apply(*leaves)
+    with torch.no_grad():
+        leaves[which].add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        out.sum().backward()
+
+
+@pytest.mark.parametrize("M", ROWS)
+def test_used_twice_and_kept(M):
+    """Gradients of two uses of the same weights add up; a kept graph gives the same again
+    and a freed one is an error."""
+    ops, d = operands(M, 40, 48, seed=M), rand(M, 40, seed=9)
+    leaves = leaves_of(ops)
+    h = leaves[0]
+    out = mb.DualWeightGlu.apply(h, leaves[1], leaves[1]) + mb.DualWeightGlu.apply(h, leaves[1], leaves[2])
+    one = torch.autograd.grad(out, leaves, d, retain_graph=True)
+    two = torch.autograd.grad(out, leaves, d)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    first = backward_reference(ops[0], ops[1], ops[1], d)
+    second = backward_reference(*ops, d)
+    for got, terms in zip(one, ([first[0], second[0]], [first[1], first[2], second[1]], [second[2]])):
+        # each term rounds to bf16, and so may each partial sum of them
+        ref, err = sum(t[0] for t in terms), sum(t[1] + R.EPS_BF16 * (t[0].abs() + t[1]) for t in terms)
+        for _ in terms[1:]:
+            err = err + R.EPS_BF16 * (sum(t[0].abs() for t in terms) + err)
+        assert ((got.double() - ref).abs() <= err + 1e-37).all()
+    with pytest.raises(RuntimeError, match="second time"):
+        torch.autograd.grad(out, leaves, d)
