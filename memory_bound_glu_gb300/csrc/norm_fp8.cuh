@@ -158,7 +158,10 @@ __global__ void __launch_bounds__(256) norm_fp8_kernel(const NormFp8Params p)
 }
 
 // A weight [N][K] bf16 to e4m3 with a scale per 128 x 128 block, one thread
-// block each.  Runs once per weight.  What it writes may be the very next call's
+// block each: the weight is read twice, two bytes at a time (9728 x 2560: 52 us for
+// 75 MB, 1.44 TB/s; the bytes alone would take 11).
+// Serving runs it once per weight; training that updates the weights, once per step.
+// What it writes may be the very next call's
 // weight, which that call's kernel copies before its dependency wait: so it does
 // not release its dependents early, and its stores are performed, for
 // asynchronous copies too, before a block ends.
