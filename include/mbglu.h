@@ -550,7 +550,8 @@ int mbglu_last_single_kernel_blocks(void);
  *   [3] tiles done whole, [4] tiles in ranges of the inner dimension, and
  *   [5] the ranges of each (with [0] = 1 every tile's, added up in a cluster)
  * glu_gemm: of the call with gu, or from 17 rows on.  Sizes from 1 on.
- * MBGLU_ERR_NULL, MBGLU_ERR_MODE (an unknown product), MBGLU_ERR_SHAPE. */
+ * MBGLU_ERR_NULL, MBGLU_ERR_MODE (an unknown product), MBGLU_ERR_SHAPE (also for
+ * outputs beyond 2^37 elements). */
 #define MBGLU_PRODUCT_GLU_GEMM   0
 #define MBGLU_PRODUCT_GRAD_H     1   /* glu_gemm_backward's grad_h */
 #define MBGLU_PRODUCT_GRAD_W     2   /* its grad_gate and grad_up */

@@ -404,6 +404,10 @@ mbglu_status mbglu_block_plan(int product, int M, int N, int K, int *plan)
     if (!plan) return MBGLU_ERR_NULL;
     if (product < MBGLU_PRODUCT_GLU_GEMM || product > MBGLU_PRODUCT_MATMUL_FP8) return MBGLU_ERR_MODE;
     if (bad_sizes(M, N, K) || std::min({M, N, K}) < 1 || N > INT32_MAX / 2) return MBGLU_ERR_SHAPE;
+    // tiles are counted in 32 bits, ranges included (the smallest: 16 x 64 in 16 ranges)
+    const int64_t rows = product == MBGLU_PRODUCT_GRAD_W ? N : M;
+    const int64_t cols = product == MBGLU_PRODUCT_GRAD_H || product == MBGLU_PRODUCT_GRAD_W ? K : N;
+    if (rows / 16 + 1 > INT32_MAX / (16 * (cols / 64 + 1))) return MBGLU_ERR_SHAPE;
     if (product >= MBGLU_PRODUCT_GLU_FP8) {
         fp8_block_plan(product == MBGLU_PRODUCT_GLU_FP8, M, N, K, plan);
         return MBGLU_OK;

@@ -70,6 +70,11 @@ def test_refusals():
     assert status(product=-1) == status(product=5) == 5
     for bad in (dict(M=0), dict(N=0), dict(K=0), dict(M=-1), dict(M=2 ** 31 - 1), dict(N=2 ** 30), dict(K=2 ** 31 - 511)):
         assert status(**bad) == 2
+    for product, kw in enumerate((dict(M=2 ** 30, N=2 ** 29), dict(M=2 ** 30, K=2 ** 30), dict(N=2 ** 29, K=2 ** 30),
+                                  dict(M=2 ** 30, N=2 ** 29), dict(M=2 ** 30, N=2 ** 29))):
+        assert status(product=product, **kw) == 2
+    for product in range(5):   # 2^36 elements
+        assert status(product=product, M=2 ** 18, N=2 ** 18, K=2 ** 18) == 0
     with pytest.raises(ValueError):
         mb.block_plan("other", 1, 1, 1)
 
