@@ -408,8 +408,9 @@ mbglu_status glu_gemm_backward(const mbglu_bf16 *h, int64_t ldh,
  * the last dimension is contiguous everywhere.  Products accumulate in fp32
  * within a block of 128 and are then scaled and summed in fp32; outputs are
  * rounded once.  The two scales of a block's sum are multiplied first, in fp32: a
- * pair whose product passes the largest fp32 number or falls below the smallest
- * normal one is not served rightly.  NaN and infinite values and scales propagate.
+ * pair whose product passes the largest fp32 number counts as infinite, and below
+ * the smallest normal number the product loses bits (a group of zeros stays zero).
+ * NaN and infinite values and scales propagate.
  *
  * add_rmsnorm_fp8 -- add_rmsnorm_glu's residual addition and zero-centred
  * RMSNorm with the normed rows as e4m3:
