@@ -474,6 +474,107 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
                         cudaStream_t stream);
 
 /*
+ * ---- Rows that choose weights of their own ---------------------------------
+ *
+ * glu_lora, linear_lora -- the gated projections, and a plain one such as the down
+ * projection, of a batch of requests with low-rank adapters beside the shared
+ * weights.  With a = adapter[m] of row m and per projection
+ *   y(W, A, B)[m, n] = sum_k x[m,k] W[n,k] + sum_j p[m,j] B[a][n,j],
+ *   p[m, j]          = scale[a] sum_k x[m,k] A[a][j,k]                  j < R
+ *   glu_lora     out = SiLU(y(gate_w, gate)) * y(up_w, up) in `mode`
+ *   linear_lora  out = y(w, ab), rounded once
+ * Sums, p and the joined sum are fp32.  No counterpart on the pages.
+ *   h (x), gate_w, up_w (w), out, strides, mode   as glu_gemm; any M >= 0
+ *   gate, up (ab)  the projection's adapters: A [adapters][R][K], B
+ *                  [adapters][N][R]; strides in elements between adapters and
+ *                  between rows, the last dimension contiguous            (read)
+ *   adapter   [M] int32: the row's adapter; any value outside [0, adapters) is
+ *             none, and the row's second term is absent                   (read)
+ *   scale     [adapters] fp32, or NULL for 1                              (read)
+ *   workspace device memory of glu_lora_workspace_bytes (linear_lora_...) bytes,
+ *             256-byte aligned, contents undefined afterwards; calls that may run at
+ *             the same time need different ones
+ *   0 <= R <= MBGLU_LORA_MAX_RANK.  adapters == 0 or R == 0: the shared product
+ *   alone; gate, up, ab, adapter and workspace are not looked at.  M == 0 or N == 0:
+ *   no-op.
+ * A row's result depends on that row, its own adapter and the shared weights only:
+ * what other rows' adapters hold, infinities and NaN too, does not reach it.  Neither
+ * the batch's size nor a row's place changes which adapter it gets.  Rows of one
+ * adapter may lie anywhere; next to one another they are faster.
+ * The fast kernels want h, the weights and A 16-byte aligned with row and adapter
+ * strides that are multiples of 8 elements, B 4-byte aligned with even strides, and R
+ * a multiple of 8; other operands take slower kernels.
+ * Errors as glu_gemm: MBGLU_ERR_SHAPE also for adapters or R out of range or a
+ * workspace that is too small.
+ */
+#define MBGLU_LORA_MAX_RANK 128
+typedef struct {
+    const mbglu_bf16 *a;
+    int64_t a_adapter, lda;
+    const mbglu_bf16 *b;
+    int64_t b_adapter, ldb;
+} mbglu_adapters;
+size_t glu_lora_workspace_bytes(int M, int N, int K, int adapters, int R);
+size_t linear_lora_workspace_bytes(int M, int N, int K, int adapters, int R);
+mbglu_status glu_lora(const mbglu_bf16 *h, int64_t ldh,
+                      const mbglu_bf16 *gate_w, int64_t ld_gate,
+                      const mbglu_bf16 *up_w, int64_t ld_up,
+                      const mbglu_adapters *gate, const mbglu_adapters *up,
+                      const int32_t *adapter, const float *scale,
+                      mbglu_bf16 *out, int64_t ldo,
+                      int M, int N, int K, int adapters, int R, mbglu_mode mode,
+                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
+mbglu_status linear_lora(const mbglu_bf16 *x, int64_t ldx,
+                         const mbglu_bf16 *w, int64_t ldw,
+                         const mbglu_adapters *ab,
+                         const int32_t *adapter, const float *scale,
+                         mbglu_bf16 *out, int64_t ldo,
+                         int M, int N, int K, int adapters, int R,
+                         void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * moe_glu -- a whole mixture-of-experts layer of a decode batch: router, choice,
+ * the chosen experts' gated projections and down projections, and their weighted
+ * sum.  For token t:
+ *   l[e]   = sum_k h[t,k] router_w[e,k], the fp32 number nearest to the exact sum
+ *   chosen = the top_k experts by l, largest first, ties to the lowest index
+ *   c[j]   = softmax(l)[chosen j], or with renormalize the softmax over the chosen
+ *   out[t] = sum_j c[j] ((SiLU(h[t] gate_w[e]^T) * (h[t] up_w[e]^T)) down_w[e]^T)
+ * in fp32 with one rounding at the end; the activation enters the down projection
+ * as two bf16 terms (a relative error of 2^-17), or whole.  No counterpart on the
+ * pages.
+ *   h [T][K];  router_w [E][K];  gate_w, up_w [E][N][K];  down_w [E][K][N]: bf16,
+ *              strides in elements between experts and between rows        (read)
+ *   out [T][K] bf16;  ids [T][top_k] int32 and weights [T][top_k] fp32, contiguous,
+ *              or NULL: the chosen experts and c                        (written)
+ *   workspace  device memory of moe_glu_workspace_bytes(...) bytes, 256-byte
+ *              aligned, its first MBGLU_MOE_COUNTER_BYTES ALL ZERO before its first
+ *              use; every completed call leaves those zero, the rest undefined.  Calls
+ *              that may run at the same time need different ones.  After a call whose
+ *              bounded wait gave up (mbglu_read_device_error), zero them again.
+ *   0 <= T <= MBGLU_MAX_M, 1 <= E <= MBGLU_MOE_MAX_EXPERTS, 1 <= top_k <=
+ *   min(E, MBGLU_MOE_MAX_TOP_K), N >= 0, K >= 0.  T == 0: no-op.  N == 0: out = 0.
+ * A token's choice does not depend on the others, and neither does its result but
+ * for the order in which its sums' parts are added.  A token with a NaN logit gets
+ * NaN weights and a NaN result.
+ * One cooperative kernel where every operand is 16-byte aligned with strides that are
+ * multiples of 8 elements and N and K are multiples of 8; other operands take
+ * slower kernels.
+ */
+#define MBGLU_MOE_MAX_EXPERTS 512
+#define MBGLU_MOE_MAX_TOP_K 16
+#define MBGLU_MOE_COUNTER_BYTES 256
+size_t moe_glu_workspace_bytes(int T, int E, int top_k, int N, int K);
+mbglu_status moe_glu(const mbglu_bf16 *h, int64_t ldh,
+                     const mbglu_bf16 *router_w, int64_t ld_router,
+                     const mbglu_bf16 *gate_w, int64_t gate_expert, int64_t ld_gate,
+                     const mbglu_bf16 *up_w, int64_t up_expert, int64_t ld_up,
+                     const mbglu_bf16 *down_w, int64_t down_expert, int64_t ld_down,
+                     mbglu_bf16 *out, int64_t ldo, int32_t *ids, float *weights,
+                     int T, int E, int top_k, int N, int K, int renormalize,
+                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Launch policy, process-wide (default MBGLU_POLICY_PREFETCH).  It decides how
  * a call's kernels are ordered after the kernel that precedes them on the
  * stream; results are identical under every policy.
@@ -523,7 +624,9 @@ int mbglu_last_cuda_error(void);
  * fragments in registers, batch 1..16); glu_gemm: 11 a CTA-pair tcgen05
  * kernel (which: mbglu_block_plan), 12 the kernel for any alignment; 13 glu_gemm_backward, 14
  * add_rmsnorm_fp8; e4m3 products: 15 the CTA-pair tcgen05 kernel, 16 the kernel
- * for few rows, 17 the kernel for any alignment; 18 quantize_weight_fp8. */
+ * for few rows, 17 the kernel for any alignment; 18 quantize_weight_fp8;
+ * glu_lora and linear_lora: 19 the CTA-pair tcgen05 kernel, 20 the kernels for any
+ * alignment; moe_glu: 21 one kernel, 22 the kernels for any alignment. */
 int mbglu_last_variant(void);
 
 /* Which kernels the calling thread's last glu_backward took for the

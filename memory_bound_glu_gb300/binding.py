@@ -27,12 +27,18 @@ _MODES = {"fused": MODE_FUSED, "hf": MODE_HF, MODE_FUSED: MODE_FUSED, MODE_HF: M
 MAX_M = 64        # batch rows per call (MBGLU_MAX_M)
 BLOCK_M = 16      # batch rows per pass over the weights (MBGLU_BLOCK_M)
 WORKSPACE_BYTES = 256
+MAX_RANK = 128            # of an adapter (MBGLU_LORA_MAX_RANK)
+MOE_MAX_EXPERTS = 512     # MBGLU_MOE_MAX_EXPERTS
+MOE_MAX_TOP_K = 16        # MBGLU_MOE_MAX_TOP_K
+MOE_COUNTER_BYTES = 256   # MBGLU_MOE_COUNTER_BYTES
 
 # Every symbol include/mbglu.h declares.
 EXPORTS = ("glu_gemv", "add_rmsnorm_glu", "add_rmsnorm_glu_ws", "add_rmsnorm_glu_strided", "add_rmsnorm_glu_noalloc",
            "silu_mul", "gdn_gates", "glu_backward", "glu_backward_workspace_bytes",
            "glu_gemm", "glu_gemm_backward", "glu_gemm_backward_workspace_bytes", "add_rmsnorm_fp8",
            "quantize_weight_fp8", "glu_fp8", "matmul_fp8", "matmul_fp8_workspace_bytes",
+           "glu_lora", "glu_lora_workspace_bytes", "linear_lora", "linear_lora_workspace_bytes",
+           "moe_glu", "moe_glu_workspace_bytes",
            "mbglu_set_launch_policy",
            "mbglu_get_launch_policy",
            "mbglu_status_string", "mbglu_abi_version", "mbglu_last_cuda_error", "mbglu_last_variant",
@@ -51,6 +57,12 @@ class MbgluError(RuntimeError):
         if status == 7:
             msg += f" (cudaError {lib().mbglu_last_cuda_error()})"
         super().__init__(f"{what}: {msg}")
+
+
+class _Adapters(ctypes.Structure):
+    """mbglu_adapters: one projection's A and B with their strides."""
+    _fields_ = [("a", ctypes.c_void_p), ("a_adapter", ctypes.c_int64), ("lda", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("b_adapter", ctypes.c_int64), ("ldb", ctypes.c_int64)]
 
 
 def _bind(l):
@@ -93,6 +105,17 @@ def _bind(l):
     l.matmul_fp8_workspace_bytes.restype = sz
     l.matmul_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, sz, vp]
     l.matmul_fp8.restype = i32
+    ad = ctypes.POINTER(_Adapters)
+    l.glu_lora.argtypes = [vp, i64, vp, i64, vp, i64, ad, ad, vp, vp, vp, i64, i32, i32, i32, i32, i32, i32, vp, sz, vp]
+    l.glu_lora.restype = i32
+    l.linear_lora.argtypes = [vp, i64, vp, i64, ad, vp, vp, vp, i64, i32, i32, i32, i32, i32, vp, sz, vp]
+    l.linear_lora.restype = i32
+    l.moe_glu.argtypes = [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, i32, i32, i32, i32, i32, i32,
+                          vp, sz, vp]
+    l.moe_glu.restype = i32
+    for f in (l.glu_lora_workspace_bytes, l.linear_lora_workspace_bytes, l.moe_glu_workspace_bytes):
+        f.argtypes = [i32, i32, i32, i32, i32]
+        f.restype = sz
     l.mbglu_status_string.argtypes = [i32]
     l.mbglu_status_string.restype = ctypes.c_char_p
     l.mbglu_abi_version.restype = i32
@@ -696,6 +719,152 @@ def matmul_fp8_workspace_bytes(M, N, K):
     return lib().matmul_fp8_workspace_bytes(M, N, K)
 
 
+def _arg3(t, name, shape, dev):
+    """(pointer, outer stride, row stride) of a bf16 operand of three dimensions."""
+    _check_operand(t, name, torch.bfloat16, shape, dev)
+    count, rows, cols = shape
+    row = t.stride(1) if rows > 1 else max(cols, 1)
+    return t.data_ptr(), t.stride(0) if count > 1 else rows * row, row
+
+
+def _vector(t, name, dtype, n, dev):
+    """The pointer of a contiguous vector."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or t.shape != (n,) or n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+    return t.data_ptr()
+
+
+def _adapter_args(a, b, name, N, K, count, R, dev):
+    """One projection's adapters, A [count, R, K] and B [count, N, R]."""
+    return _Adapters(*_arg3(a, name + "_a", (count, R, K), dev), *_arg3(b, name + "_b", (count, N, R), dev))
+
+
+def _ranks(a, name):
+    """(adapters, R) of A [adapters, R, K]."""
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D tensor [adapters, rank, K]")
+    if a.shape[1] > MAX_RANK:
+        raise ValueError(f"{name}'s rank {a.shape[1]} is above {MAX_RANK}")
+    return a.shape[0], a.shape[1]
+
+
+def glu_lora(h, gate_w, up_w, gate_a, gate_b, up_a, up_b, adapter, scale=None, out=None, mode="fused", workspace=None,
+             stream=None):
+    """SiLU(g) * u, [M,N], of the gated projections with low-rank adapters beside the
+    shared weights: g = h @ gate_w.T + p @ gate_b[a].T with p = scale[a] * (h @
+    gate_a[a].T) and a = adapter[m] the row's adapter; u likewise.  Any number of
+    rows.  gate_a, up_a are [adapters,R,K], gate_b, up_b [adapters,N,R] (bf16, R <=
+    MAX_RANK); adapter is int32 [M], a value outside [0, adapters) meaning none;
+    scale float32 [adapters] or None for 1.  The workspace is a byte tensor of
+    glu_lora_workspace_bytes(M, N, K, adapters, R) bytes, 256-byte aligned, allocated
+    here when not given.  No gradients."""
+    bf16 = torch.bfloat16
+    M, K, dev = _dims(h, "h", bf16)
+    N = _out_rows(gate_w, "gate_w")
+    count, R = _ranks(gate_a, "gate_a")
+    ins = (*_arg(h, "h", bf16, M, K, dev), *_arg(gate_w, "gate_w", bf16, N, K, dev), *_arg(up_w, "up_w", bf16, N, K, dev),
+           _adapter_args(gate_a, gate_b, "gate", N, K, count, R, dev), _adapter_args(up_a, up_b, "up", N, K, count, R, dev),
+           _vector(adapter, "adapter", torch.int32, M, dev), None if scale is None else _vector(scale, "scale", torch.float32, count, dev))
+    with _allocate_on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=bf16, device=dev)
+        wsp, wsb, keep = _workspace(workspace, lib().glu_lora_workspace_bytes(M, N, K, count, R), dev)
+        st = lib().glu_lora(*ins, *_arg(out, "out", bf16, M, N, dev), M, N, K, count, R, _MODES[mode], wsp, wsb, _stream_of(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "glu_lora")
+    return out
+
+
+def linear_lora(x, w, a, b, adapter, scale=None, out=None, workspace=None, stream=None):
+    """x @ w.T + (scale[i] * (x @ a[i].T)) @ b[i].T, [M,N] bf16, with i = adapter[m]
+    the row's adapter: one projection of glu_lora, such as the down projection.
+    Arguments as there, a [adapters,R,K] and b [adapters,N,R]; the workspace is one of
+    linear_lora_workspace_bytes(M, N, K, adapters, R) bytes.  No gradients."""
+    bf16 = torch.bfloat16
+    M, K, dev = _dims(x, "x", bf16)
+    N = _out_rows(w, "w")
+    count, R = _ranks(a, "a")
+    ins = (*_arg(x, "x", bf16, M, K, dev), *_arg(w, "w", bf16, N, K, dev),
+           _Adapters(*_arg3(a, "a", (count, R, K), dev), *_arg3(b, "b", (count, N, R), dev)),
+           _vector(adapter, "adapter", torch.int32, M, dev), None if scale is None else _vector(scale, "scale", torch.float32, count, dev))
+    with _allocate_on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=bf16, device=dev)
+        wsp, wsb, keep = _workspace(workspace, lib().linear_lora_workspace_bytes(M, N, K, count, R), dev)
+        st = lib().linear_lora(*ins, *_arg(out, "out", bf16, M, N, dev), M, N, K, count, R, wsp, wsb, _stream_of(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "linear_lora")
+    return out
+
+
+def new_moe_workspace(T, E, top_k, N, K, device=None):
+    """A workspace for moe_glu calls of up to T tokens at these sizes (one per
+    concurrently running stream), its counters zeroed."""
+    need = moe_glu_workspace_bytes(T, E, top_k, N, K)
+    ws = torch.empty(max(need, MOE_COUNTER_BYTES), dtype=torch.uint8, device=device or "cuda")
+    ws[:MOE_COUNTER_BYTES].zero_()
+    return ws
+
+
+def moe_glu(h, router_w, gate_w, up_w, down_w, top_k, renormalize=True, out=None, ids=None, weights=None, workspace=None,
+            stream=None):
+    """A mixture-of-experts layer of up to MAX_M tokens: returns (out [T,K] bf16, ids
+    [T,top_k] int32, weights [T,top_k] float32).  The logits h @ router_w.T are the
+    float32 numbers nearest to the exact sums; each token takes the top_k experts
+    (ties to the lowest index) with softmax weights, renormalised over the chosen or
+    not; out is the weighted sum of (SiLU(h @ gate_w[e].T) * (h @ up_w[e].T)) @
+    down_w[e].T.  router_w is [E,K], gate_w and up_w [E,N,K], down_w [E,K,N].
+    The workspace (new_moe_workspace(T, E, top_k, N, K), which a decode loop keeps)
+    is allocated and its counters are zeroed here when not given.  No gradients."""
+    bf16 = torch.bfloat16
+    T, K, dev = _dims(h, "h", bf16)
+    if T > MAX_M:
+        raise ValueError(f"h has more than {MAX_M} tokens: {T}")
+    E = _out_rows(router_w, "router_w")
+    if not isinstance(gate_w, torch.Tensor) or gate_w.dim() != 3 or gate_w.shape[1] > _MOST:
+        raise ValueError("gate_w must be a 3-D tensor [experts, N, K]")
+    N = gate_w.shape[1]
+    top_k = int(top_k)
+    if not 1 <= E <= MOE_MAX_EXPERTS or not 1 <= top_k <= min(E, MOE_MAX_TOP_K):
+        raise ValueError(f"1 to {MOE_MAX_EXPERTS} experts and 1 to {MOE_MAX_TOP_K} of them per token, got {E} and {top_k}")
+    ins = (*_arg(h, "h", bf16, T, K, dev), *_arg(router_w, "router_w", bf16, E, K, dev), *_arg3(gate_w, "gate_w", (E, N, K), dev),
+           *_arg3(up_w, "up_w", (E, N, K), dev), *_arg3(down_w, "down_w", (E, K, N), dev))
+    with _allocate_on(dev, stream):
+        if out is None:
+            out = torch.empty((T, K), dtype=bf16, device=dev)
+        if ids is None:
+            ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        if weights is None:
+            weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        for t, name, dtype in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
+            _check_operand(t, name, dtype, (T, top_k), dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if workspace is None:
+            workspace = new_moe_workspace(T, E, top_k, N, K, dev)
+        wsp, wsb, keep = _workspace(workspace, 0, dev)
+        st = lib().moe_glu(*ins, *_arg(out, "out", bf16, T, K, dev), ids.data_ptr(), weights.data_ptr(), T, E, top_k, N, K,
+                           int(bool(renormalize)), wsp, wsb, _stream_of(dev, stream))
+    if st != 0:
+        raise MbgluError(st, "moe_glu")
+    return out, ids, weights
+
+
+def glu_lora_workspace_bytes(M, N, K, adapters, R):
+    """Bytes of glu_lora's workspace (0: none needed)."""
+    return lib().glu_lora_workspace_bytes(M, N, K, adapters, R)
+
+
+def linear_lora_workspace_bytes(M, N, K, adapters, R):
+    """Bytes of linear_lora's workspace (0: none needed)."""
+    return lib().linear_lora_workspace_bytes(M, N, K, adapters, R)
+
+
+def moe_glu_workspace_bytes(T, E, top_k, N, K):
+    """Bytes of moe_glu's workspace; what holds for T tokens holds for fewer."""
+    return lib().moe_glu_workspace_bytes(T, E, top_k, N, K)
+
+
 def silu_mul(x, out=None, mode="fused", stream=None):
     """out[M,N] = SiLU(x[:, :N]) * x[:, N:2N] on the halves layout (the gate
     projection in the first half of each row, the up projection in the second,
@@ -764,7 +933,9 @@ def last_variant() -> int:
     glu_backward, 9 tcgen05, 10 the K-slice tensor-core kernel (batch 1..16),
     11 glu_gemm on the CTA-pair tcgen05 kernel, 12 glu_gemm at any alignment,
     13 glu_gemm_backward, 14 add_rmsnorm_fp8, 15..17 an e4m3 product (CTA pairs,
-    few rows, any alignment), 18 quantize_weight_fp8."""
+    few rows, any alignment), 18 quantize_weight_fp8, 19 and 20 glu_lora and
+    linear_lora (CTA pairs, any alignment), 21 and 22 moe_glu (one kernel, any
+    alignment)."""
     return lib().mbglu_last_variant()
 
 

@@ -19,7 +19,11 @@ enum DenseVariant {
     kFp8Pair = 15,       // an e4m3 product on the CTA-pair tcgen05 kernel
     kFp8Tall = 16,       // an e4m3 product of few rows
     kFp8Generic = 17,    // an e4m3 product on the kernel for any alignment
-    kQuantWeight = 18    // quantize_weight_fp8
+    kQuantWeight = 18,   // quantize_weight_fp8
+    kLoraPair = 19,      // glu_lora, linear_lora on the CTA-pair tcgen05 kernel
+    kLoraGeneric = 20,   // on the kernels for any alignment
+    kMoeFused = 21,      // moe_glu in one kernel
+    kMoeGeneric = 22     // on the kernels for any alignment
 };
 
 mbglu_status cuda_fail(cudaError_t e);   // records e for mbglu_last_cuda_error
@@ -32,12 +36,17 @@ int launch_policy();
 bool encode_tile_map(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, int cols, int box_cols,
                      int box_rows, int elem_bytes);
 
+// As encode_tile_map for bf16 [count][rows][cols], stride elements from matrix to matrix.
+bool encode_stack_map(mbglu::TensorMap *out, const void *base, int64_t stride, int64_t ld, int count, int rows, int cols, int box_cols,
+                      int box_rows);
+
 // mbglu_block_plan's answer for the e4m3 products
 void fp8_block_plan(bool dual, int M, int N, int K, int *plan);
 
 // Reads and clears the unit's device error word; the device is idle.
 cudaError_t take_gemm_error(int *w);
 cudaError_t take_fp8_error(int *w);
+cudaError_t take_moe_error(int *w);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

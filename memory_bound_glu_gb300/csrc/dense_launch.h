@@ -16,6 +16,15 @@ namespace mbglu_host {
 constexpr int kMostSize = INT32_MAX - 511;
 inline bool bad_sizes(int a, int b, int c = 0) { return std::min({a, b, c}) < 0 || std::max({a, b, c}) > kMostSize; }
 
+// An operand that tensor copies take: 16-byte aligned rows.
+inline bool copyable(const void *p, int64_t ld, int elem) { return aligned(p, 16) && ld * elem % 16 == 0; }
+
+// 2 when every row of elem-byte elements starts on 32 bytes, 1 on 16, else 0
+inline int row_align(const void *p, int64_t ld, int elem)
+{
+    return aligned(p, 32) && ld * elem % 32 == 0 ? 2 : aligned(p, 16) && ld * elem % 16 == 0 ? 1 : 0;
+}
+
 // The current device's SM count, after `setup` (attributes of the unit's
 // kernels) has run once on it.
 struct DeviceTable {

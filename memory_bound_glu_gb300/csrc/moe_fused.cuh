@@ -1,0 +1,620 @@
+// moe_fused.cuh -- the expert layer of a decode batch in one cooperative kernel: one
+// block per SM, all resident at once, that meet at four grid barriers.
+//
+//   1  logits, a warp per expert and four tokens                        | barrier
+//   2  every block chooses the experts of all tokens for itself: nothing to hand over
+//   3  gated projections of the chosen experts                          | barrier
+//   4  activation, as two bf16 terms                                    | barrier
+//   5  down projections                                                 | barrier
+//   6  weighted sum over a token's experts
+//
+// What bounds it are the chosen experts' weights.  In 3 and 5 they are the MMA's 128-row
+// side (tcgen05, accumulators in tensor memory): a unit is a 16 KB box of 64 columns,
+// of 64 gate and 64 up rows or of 128 down rows.  The units of all tiles of all chosen
+// experts form one sequence that is cut into equal ranges, one per block, so every SM
+// reads the same number of bytes whatever was chosen; a tile that a border cuts leaves
+// parts of its sum, which whoever needs the sum adds in the order of the blocks.  The
+// side of the tokens: in 3 all tokens for every expert (a column costs nothing beside the
+// weights; only the chosen ones are written), in 5 the activation rows of the expert.
+// A token's column is its own, so what other tokens hold does not reach it.
+//
+// The copies of weights run ahead over the barriers: the first units of 5 are on their
+// way while 3 is finished and 4 runs, up to the ring's 96 to 160 KB per SM.
+//
+// Roles (384 threads): warp 0 copies weights, warp 2 the tokens' side, warp 1 owns the
+// tensor memory and issues the MMAs, warps 4-7 read accumulators, warps 4-11 do 4 and 6,
+// all warps 1 and 2.  Every wait is bounded; after one gives up each role ends without
+// touching memory and the counters keep what they hold.
+#pragma once
+#include "dense_common.cuh"
+#include "moe_route.cuh"
+#include "tc_pair.cuh"
+
+namespace mbglu {
+
+constexpr int kMoeThreads = 384;
+constexpr int kMoeWarps = kMoeThreads / 32;
+constexpr int kMoeSum = 4;                        // the first warp of those that read accumulators and add
+constexpr int kMoeMaxStages = 10;
+constexpr uint32_t kMoeUnit = 16384;              // a unit's weights
+constexpr uint32_t kMoeCols = 128;                // tensor memory: two accumulators of 64 columns
+constexpr int kMoeSlots = kMoeMaxRows * kMoeMaxTopK;
+
+struct MoeMaps {
+    TensorMap gate, up;   // [E][N][K], boxes of 64 x 64 (columns x rows)
+    TensorMap down;       // [E][K][N], 64 x 128
+    TensorMap h;          // [T][K], 64 x padded tokens
+    TensorMap act;        // [2 act_rows][N], 64 x 16
+};
+
+struct MoeParams {
+    const uint16_t *h, *router;
+    int64_t ldh, ldr, ldo;
+    uint16_t *out;
+    int32_t *ids;            // or null
+    float *weights;          // or null
+    uint32_t *counters;      // four barriers and the exit, all 0 at the start and at the end
+    float *logits;           // [T][E]
+    float *gu;               // [slots][2 N]: g, then u
+    float *y;                // [slots][K]
+    float *carry;            // [blocks][pad][128]: the part of a block's first tile that began in an earlier block
+    uint16_t *act;           // [2 act_rows][act_ld]: first terms, then second ones
+    int64_t act_ld;
+    int act_rows;
+    int T, E, top_k, N, K, renormalize;
+    int pad;                 // tokens padded to a multiple of 16
+    int stages;
+};
+
+struct alignas(16) MoeShared {
+    uint64_t weights_full[kMoeMaxStages], tokens_full[kMoeMaxStages], empty[kMoeMaxStages];
+    uint64_t acc_full[2], acc_empty[2], act_ready, done;
+    uint32_t tmem, failed;
+    int active, pad_;
+    uint64_t mask[kMoeMaxExperts];               // tokens that chose the expert
+    float weight[kMoeSlots];
+    uint16_t id[kMoeSlots];                      // [T][top_k]
+    uint16_t expert[kMoeMaxExperts], first[kMoeMaxExperts + 1];   // of the i-th chosen expert: itself, its first slot
+    uint16_t where[kMoeMaxExperts];              // an expert's place among the chosen ones
+    uint16_t of_slot[kMoeSlots];                 // a slot's place among the chosen experts
+};
+
+constexpr uint32_t kMoeHeader = (sizeof(MoeShared) + 1023) / 1024 * 1024;
+__host__ __device__ constexpr uint32_t moe_stage_bytes(int pad) { return kMoeUnit + 256u * static_cast<uint32_t>(pad); }
+constexpr uint32_t kMoeSmemMost = 227 * 1024;
+__host__ __device__ constexpr int moe_stages(int pad)
+{
+    const int n = static_cast<int>((kMoeSmemMost - kMoeHeader - 1024) / moe_stage_bytes(pad));
+    return n < kMoeMaxStages ? n : kMoeMaxStages;
+}
+__host__ __device__ constexpr uint32_t moe_smem(int pad) { return kMoeHeader + 1024 + static_cast<uint32_t>(moe_stages(pad)) * moe_stage_bytes(pad); }
+
+// A 64-column box of a stack of matrices.
+__device__ __forceinline__ void tma_load_3d(void *dst, const TensorMap *map, int x, int y, int z, uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+// Orders this thread's plain accesses to any memory against asynchronous copies'.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t add_acq_rel_gpu(uint32_t *p, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
+// One thread per block, after a barrier of the threads whose writes it publishes.
+__device__ __forceinline__ void grid_arrive(uint32_t *counter)
+{
+    __threadfence();
+    add_acq_rel_gpu(counter, 1u);
+}
+__device__ __forceinline__ bool grid_wait(const uint32_t *counter, uint64_t limit_ns)
+{
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1; ld_acquire_gpu(counter) < gridDim.x; ++i)
+        if ((i & 63u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
+    __threadfence();
+    return true;
+}
+
+// The units of a phase: `chosen` experts x `tiles` x `chunks`, cut into ranges for the
+// first `blocks` blocks.
+struct MoeUnits {
+    uint32_t tiles, chunks, total, blocks;
+};
+
+__device__ __forceinline__ MoeUnits moe_units(int chosen, int tiles, int chunks)
+{
+    MoeUnits u;
+    u.tiles = static_cast<uint32_t>(tiles);
+    u.chunks = static_cast<uint32_t>(chunks);
+    u.total = static_cast<uint32_t>(chosen) * u.tiles * u.chunks;
+    u.blocks = min(gridDim.x, u.total);
+    return u;
+}
+// block b's first unit; total * blocks fits 32 bits
+__device__ __forceinline__ uint32_t moe_begin(const MoeUnits &u, uint32_t b) { return b >= u.blocks ? u.total : u.total * b / u.blocks; }
+__device__ __forceinline__ uint32_t moe_owner(const MoeUnits &u, uint32_t unit) { return ((unit + 1) * u.blocks - 1) / u.total; }
+
+// A walk over a block's units.
+struct MoeWalk {
+    uint32_t left, chunk, tile, expert;   // expert: its place among the chosen ones
+    __device__ MoeWalk(const MoeUnits &u)
+    {
+        const uint32_t at = moe_begin(u, blockIdx.x);
+        left = moe_begin(u, blockIdx.x + 1) - at;
+        const uint32_t q = at / u.chunks;
+        chunk = at - q * u.chunks;
+        expert = q / u.tiles;
+        tile = q - expert * u.tiles;
+    }
+    __device__ void next(const MoeUnits &u)
+    {
+        --left;
+        if (++chunk == u.chunks) next_tile(u);
+    }
+    __device__ void next_tile(const MoeUnits &u)
+    {
+        chunk = 0;
+        if (++tile == u.tiles) {
+            tile = 0;
+            ++expert;
+        }
+    }
+    // units of this tile in the block's range
+    __device__ uint32_t run(const MoeUnits &u) const { return min(left, u.chunks - chunk); }
+};
+
+// Four tokens' logits of one expert (one token: four chains of one), a warp.
+template <int TOKENS>
+__device__ __forceinline__ void moe_logits(const MoeParams &p, int e, int t0)
+{
+    const int lane = threadIdx.x & 31;
+    float s[4] = {}, c[4] = {};
+    const uint16_t *w = p.router + e * p.ldr;
+    for (int k = lane * 8; k < p.K; k += 256) {
+        const uint4 b = *reinterpret_cast<const uint4 *>(w + k);
+        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) {
+            if (TOKENS > 1 && t0 + j >= p.T) continue;
+            const uint4 a = *reinterpret_cast<const uint4 *>(p.h + (t0 + j) * p.ldh + k);
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = TOKENS > 1 ? j : i;
+                two_sum(s[at], c[at], __fmul_rn(bf16_lo(aw[i]), bf16_lo(bw[i])));
+                two_sum(s[at], c[at], __fmul_rn(bf16_hi(aw[i]), bf16_hi(bw[i])));
+            }
+        }
+    }
+    if (TOKENS == 1) {
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            two_sum(s[0], c[0], s[i]);
+            c[0] = __fadd_rn(c[0], c[i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) {
+        const float v = warp_pair_sum(s[j], c[j]);
+        if (lane == 0 && t0 + j < p.T) __stcg(p.logits + (t0 + j) * p.E + e, v);
+    }
+}
+
+static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const MoeParams p, const __grid_constant__ MoeMaps maps)
+{
+    extern __shared__ unsigned char moe_raw[];
+    unsigned char *base = moe_raw + ((1024u - (smem_addr(moe_raw) & 1023u)) & 1023u);
+    MoeShared &s = *reinterpret_cast<MoeShared *>(base);
+    unsigned char *ring = base + kMoeHeader;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t stage_bytes = moe_stage_bytes(p.pad);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&s.weights_full[i], 1);
+            mbar_init(&s.tokens_full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], 4);
+        }
+        mbar_init(&s.act_ready, 1);
+        mbar_init(&s.done, 1);
+        s.failed = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&s.tmem, kMoeCols);
+        tmem_relinquish();
+    }
+    for (int e = threadIdx.x; e < p.E; e += kMoeThreads) s.mask[e] = 0;
+
+    // 1: logits
+    if (p.T == 1) {
+        for (int i = static_cast<int>(warp * gridDim.x + blockIdx.x); i < p.E; i += static_cast<int>(gridDim.x) * kMoeWarps) moe_logits<1>(p, i, 0);
+    } else {
+        const int groups = (p.T + 3) / 4;
+        for (int i = static_cast<int>(warp * gridDim.x + blockIdx.x); i < p.E * groups; i += static_cast<int>(gridDim.x) * kMoeWarps)
+            moe_logits<4>(p, i / groups, i % groups * 4);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    if (threadIdx.x == 0) {
+        grid_arrive(p.counters);
+        if (!grid_wait(p.counters, kWaitLimitNs)) s.failed = 1;
+    }
+    __syncthreads();
+    bool ok = s.failed == 0;
+
+    // 2: the choice, of all tokens in every block
+    if (ok) {
+        for (int t = warp; t < p.T; t += kMoeWarps) {
+            int id;
+            float w;
+            const float *l = p.logits + t * p.E;
+            const auto logit = [l](int e) { return __ldcg(l + e); };
+            if (p.E <= 128)
+                warp_top_k<4>(logit, p.E, p.top_k, p.renormalize != 0, id, w);
+            else
+                warp_top_k<kMoeMaxExperts / 32>(logit, p.E, p.top_k, p.renormalize != 0, id, w);
+            if (lane < p.top_k) {
+                const int at = t * p.top_k + lane;
+                s.id[at] = static_cast<uint16_t>(id);
+                s.weight[at] = w;
+                atomicOr(reinterpret_cast<unsigned long long *>(&s.mask[id]), 1ull << t);
+                if (static_cast<int>(blockIdx.x) == t) {
+                    if (p.ids) p.ids[at] = id;
+                    if (p.weights) p.weights[at] = w;
+                }
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int n = 0, slot = 0;
+            for (int e0 = 0; e0 < p.E; e0 += 32) {
+                const int e = e0 + lane;
+                const int count = e < p.E ? __popcll(s.mask[e]) : 0;
+                const uint32_t used = __ballot_sync(0xffffffffu, count > 0);
+                int before = count;   // inclusive sum over the lanes
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += v;
+                }
+                const int at = n + __popc(used & ((1u << lane) - 1));
+                if (count > 0) {
+                    s.expert[at] = static_cast<uint16_t>(e);
+                    s.first[at] = static_cast<uint16_t>(slot + before - count);
+                    s.where[e] = static_cast<uint16_t>(at);
+                    for (int i = 0; i < count; ++i) s.of_slot[slot + before - count + i] = static_cast<uint16_t>(at);
+                }
+                n += __popc(used);
+                slot += __shfl_sync(0xffffffffu, before, 31);
+            }
+            if (lane == 0) {
+                s.active = n;
+                s.first[n] = static_cast<uint16_t>(slot);
+            }
+        }
+        __syncthreads();
+    }
+    const MoeUnits gated = moe_units(ok ? s.active : 0, (p.N + 63) / 64, (p.K + 63) / 64);
+    const MoeUnits down = moe_units(ok ? s.active : 0, (p.K + 127) / 128, (p.N + 63) / 64);
+
+    if (!ok) {
+        // nothing was chosen: no role has anything to do
+    } else if (warp == 0) {
+        const uint64_t policy = l2_policy_evict_first();
+        int st = 0, issued = 0;
+        uint32_t phase = 1;
+        for (int second = 0; second < 2 && ok; ++second) {
+            const MoeUnits &units = second ? down : gated;
+            for (MoeWalk w(units); w.left > 0; w.next(units)) {
+                if (!pair_wait(&s.empty[st], phase, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    unsigned char *d = ring + st * stage_bytes;
+                    const int e = s.expert[w.expert], x = static_cast<int>(w.chunk) * 64;
+                    mbar_arrive_expect_tx(&s.weights_full[st], kMoeUnit);
+                    if (!second) {
+                        tma_load_3d(d, &maps.gate, x, static_cast<int>(w.tile) * 64, e, &s.weights_full[st], policy);
+                        tma_load_3d(d + kMoeUnit / 2, &maps.up, x, static_cast<int>(w.tile) * 64, e, &s.weights_full[st], policy);
+                    } else {
+                        tma_load_3d(d, &maps.down, x, static_cast<int>(w.tile) * 128, e, &s.weights_full[st], policy);
+                    }
+                }
+                __syncwarp();
+                issued += issued < p.stages;
+                if (++st == p.stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // no copy may be in flight when the block leaves
+        for (int i = 0; i < issued; ++i) {
+            int at = st - issued + i;
+            const uint32_t ph = at < 0 ? phase : phase ^ 1;
+            if (at < 0) at += p.stages;
+            if (!pair_wait(&s.weights_full[at], ph, kWaitLimitNs)) ok = false;
+        }
+    } else if (warp == 2) {
+        const uint64_t policy = l2_policy_evict_last();
+        int st = 0, issued = 0;
+        uint32_t phase = 1;
+        for (int second = 0; second < 2 && ok; ++second) {
+            const MoeUnits &units = second ? down : gated;
+            if (second) {
+                ok = pair_wait(&s.act_ready, 0, 2 * kWaitLimitNs) && *reinterpret_cast<volatile uint32_t *>(&s.failed) == 0;
+                fence_proxy_async_all();
+                if (!ok) break;
+            }
+            for (MoeWalk w(units); w.left > 0; w.next(units)) {
+                if (!pair_wait(&s.empty[st], phase, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    unsigned char *d = ring + st * stage_bytes + kMoeUnit;
+                    const int x = static_cast<int>(w.chunk) * 64;
+                    if (!second) {
+                        mbar_arrive_expect_tx(&s.tokens_full[st], static_cast<uint32_t>(p.pad) * 128u);
+                        tma_load_2d(d, &maps.h, x, 0, &s.tokens_full[st], policy);
+                    } else {
+                        const int first = s.first[w.expert], boxes = (s.first[w.expert + 1] - first + 15) / 16;
+                        mbar_arrive_expect_tx(&s.tokens_full[st], static_cast<uint32_t>(boxes) * 4096u);
+                        for (int i = 0; i < boxes; ++i) {
+                            tma_load_2d(d + i * 2048, &maps.act, x, first + i * 16, &s.tokens_full[st], policy);
+                            tma_load_2d(d + p.pad * 128 + i * 2048, &maps.act, x, p.act_rows + first + i * 16, &s.tokens_full[st], policy);
+                        }
+                    }
+                }
+                __syncwarp();
+                issued += issued < p.stages;
+                if (++st == p.stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        for (int i = 0; i < issued; ++i) {
+            int at = st - issued + i;
+            const uint32_t ph = at < 0 ? phase : phase ^ 1;
+            if (at < 0) at += p.stages;
+            if (!pair_wait(&s.tokens_full[at], ph, kWaitLimitNs)) ok = false;
+        }
+    } else if (warp == 1) {
+        int st = 0;
+        uint32_t phase = 0, buf = 0, acc_phase = 1;
+        for (int second = 0; second < 2 && ok; ++second) {
+            const MoeUnits &units = second ? down : gated;
+            MoeWalk w(units);
+            while (w.left > 0 && ok) {
+                const uint32_t run = w.run(units);
+                const int cols = second ? (s.first[w.expert + 1] - s.first[w.expert] + 15) / 16 * 16 : p.pad;
+                const uint32_t idesc = tc_idesc_bf16(128, 16) + (static_cast<uint32_t>((cols - 16) >> 3) << 17);
+                const uint32_t d = tmem + buf * 64u;
+                if (!pair_wait(&s.acc_empty[buf], acc_phase, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                for (uint32_t c = 0; c < run; ++c) {
+                    // the second phase's tokens come only after two barriers
+                    if (!pair_wait(&s.weights_full[st], phase, kWaitLimitNs) || !pair_wait(&s.tokens_full[st], phase, 4 * kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        unsigned char *a = ring + st * stage_bytes, *b = a + kMoeUnit;
+                        const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(b);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, c > 0 || kk > 0);
+                        if (second) {
+                            const uint64_t ld = smem_desc_sw128(b + p.pad * 128);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, ad + 2 * kk, ld + 2 * kk, idesc, true);
+                        }
+                        tc_commit(&s.empty[st]);
+                        if (c == run - 1) tc_commit(&s.acc_full[buf]);
+                    }
+                    __syncwarp();
+                    if (++st == p.stages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+                w.left -= run;
+                w.next_tile(units);
+                buf ^= 1;
+                if (buf == 0) acc_phase ^= 1;
+            }
+        }
+        // every product issued has ended before the tensor memory is given back
+        if (elect_one()) tc_commit(&s.done);
+        __syncwarp();
+        if (!pair_wait(&s.done, 0, kWaitLimitNs)) ok = false;
+    } else if (warp >= kMoeSum) {
+        const int sums = kMoeWarps - kMoeSum, me = warp - kMoeSum;
+        uint32_t buf = 0, acc_phase = 0;
+        for (int second = 0; second < 2 && ok; ++second) {
+            const MoeUnits &units = second ? down : gated;
+            if (me < 4) {
+                const uint32_t lanes = tmem + (static_cast<uint32_t>(me * 32) << 16);
+                const int row = me * 32 + lane;
+                MoeWalk w(units);
+                while (w.left > 0 && ok) {
+                    const uint32_t run = w.run(units);
+                    const bool whole = w.chunk == 0;   // the tile begins here
+                    const int first = s.first[w.expert], count = s.first[w.expert + 1] - first;
+                    if (!__all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], acc_phase, 4 * kWaitLimitNs))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    float *carry = p.carry + static_cast<int64_t>(blockIdx.x) * p.pad * 128 + row;
+                    if (!second) {
+                        const uint64_t mask = s.mask[s.expert[w.expert]];
+                        const int n = static_cast<int>(w.tile) * 64 + (row & 63);
+                        float *dst = p.gu + first * (2 * static_cast<int64_t>(p.N)) + (row >> 6) * p.N + n;
+                        int at = 0;
+                        for (int c = 0; c < p.pad; c += 16) {
+                            const uint32_t m = static_cast<uint32_t>(mask >> c) & 0xffffu;
+                            if (m == 0) continue;
+                            float v[16];
+                            __syncwarp();
+                            tmem_ld16(lanes + buf * 64u + static_cast<uint32_t>(c), v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (m >> i & 1u) {
+                                    if (!whole)
+                                        __stcg(carry + at * 128, v[i]);
+                                    else if (n < p.N)
+                                        __stcg(dst + at * (2 * static_cast<int64_t>(p.N)), v[i]);
+                                    ++at;
+                                }
+                            }
+                        }
+                    } else {
+                        const int k = static_cast<int>(w.tile) * 128 + row;
+                        float *dst = p.y + first * static_cast<int64_t>(p.K) + k;
+                        for (int c = 0; c < count; c += 16) {
+                            float v[16];
+                            __syncwarp();
+                            tmem_ld16(lanes + buf * 64u + static_cast<uint32_t>(c), v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (c + i < count) {
+                                    if (!whole)
+                                        __stcg(carry + (c + i) * 128, v[i]);
+                                    else if (k < p.K)
+                                        __stcg(dst + (c + i) * static_cast<int64_t>(p.K), v[i]);
+                                }
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.acc_empty[buf]);
+                    w.left -= run;
+                    w.next_tile(units);
+                    buf ^= 1;
+                    if (buf == 0) acc_phase ^= 1;
+                }
+            }
+            if (!ok) s.failed = 1;
+            bar_sync_named(1, sums * 32);
+            if (me == 0 && lane == 0) {
+                grid_arrive(p.counters + 1 + 2 * second);   // after a failure too: the others need not wait
+                if (!grid_wait(p.counters + 1 + 2 * second, 2 * kWaitLimitNs)) s.failed = 1;
+            }
+            bar_sync_named(1, sums * 32);
+            ok = *reinterpret_cast<volatile uint32_t *>(&s.failed) == 0;
+            if (!second) {
+                // 4: the activation; a warp per slot and tile of 64 columns
+                const int slots = s.first[s.active];
+                for (uint32_t i = blockIdx.x + gridDim.x * static_cast<uint32_t>(me); ok && i < static_cast<uint32_t>(slots) * units.tiles;
+                     i += gridDim.x * static_cast<uint32_t>(sums)) {
+                    const uint32_t slot = i / units.tiles, tile = i - slot * units.tiles;
+                    const int at = s.of_slot[slot], col = static_cast<int>(slot) - s.first[at];
+                    const uint32_t u0 = (static_cast<uint32_t>(at) * units.tiles + tile) * units.chunks;
+                    const uint32_t b0 = moe_owner(units, u0), b1 = moe_owner(units, u0 + units.chunks - 1);
+                    const int n = static_cast<int>(tile) * 64 + lane * 2;
+                    if (n >= p.N) continue;   // N is even: both columns exist, or none
+                    const float *src = p.gu + slot * (2 * static_cast<int64_t>(p.N)) + n;
+                    float2 g = __ldcg(reinterpret_cast<const float2 *>(src)), u = __ldcg(reinterpret_cast<const float2 *>(src + p.N));
+                    for (uint32_t b = b0 + 1; b <= b1; ++b) {
+                        const float *q = p.carry + (static_cast<int64_t>(b) * p.pad + col) * 128 + lane * 2;
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(q)), z = __ldcg(reinterpret_cast<const float2 *>(q + 64));
+                        g.x += x.x;
+                        g.y += x.y;
+                        u.x += z.x;
+                        u.y += z.y;
+                    }
+                    // two bf16 terms, so that the tensor cores' operand is off by 2^-18 and not by 2^-9; an
+                    // infinite one has no second term
+                    const float a0 = silu_f32(g.x) * u.x, a1 = silu_f32(g.y) * u.y;
+                    const uint32_t hi = pack_bf16x2(a0, a1);
+                    const float r0 = isfinite(bf16_lo(hi)) ? a0 - bf16_lo(hi) : 0.0f, r1 = isfinite(bf16_hi(hi)) ? a1 - bf16_hi(hi) : 0.0f;
+                    uint16_t *dst = p.act + slot * p.act_ld + n;
+                    *reinterpret_cast<uint32_t *>(dst) = hi;
+                    *reinterpret_cast<uint32_t *>(dst + p.act_rows * p.act_ld) = pack_bf16x2(r0, r1);
+                }
+                fence_proxy_async_all();
+                bar_sync_named(1, sums * 32);
+                if (me == 0 && lane == 0) {
+                    grid_arrive(p.counters + 2);
+                    if (!grid_wait(p.counters + 2, 2 * kWaitLimitNs)) s.failed = 1;
+                    fence_proxy_async_all();
+                    mbar_arrive(&s.act_ready);
+                }
+            } else {
+                // 6: the weighted sum; a warp per token and tile of 128 columns
+                for (uint32_t i = blockIdx.x + gridDim.x * static_cast<uint32_t>(me); ok && i < static_cast<uint32_t>(p.T) * units.tiles;
+                     i += gridDim.x * static_cast<uint32_t>(sums)) {
+                    const uint32_t t = i / units.tiles, tile = i - t * units.tiles;
+                    const int k = static_cast<int>(tile) * 128 + lane * 4;
+                    if (k >= p.K) continue;   // K is a multiple of 8
+                    float4 sum = make_float4(0, 0, 0, 0);
+                    for (int j = 0; j < p.top_k; ++j) {
+                        const int e = s.id[t * p.top_k + j], at = s.where[e];
+                        const int col = __popcll(s.mask[e] & ((1ull << t) - 1));
+                        const float c = s.weight[t * p.top_k + j];
+                        const uint32_t u0 = (static_cast<uint32_t>(at) * units.tiles + tile) * units.chunks;
+                        const uint32_t b0 = moe_owner(units, u0), b1 = moe_owner(units, u0 + units.chunks - 1);
+                        float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (s.first[at] + col) * static_cast<int64_t>(p.K) + k));
+                        for (uint32_t b = b0 + 1; b <= b1; ++b) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.carry + (static_cast<int64_t>(b) * p.pad + col) * 128 + lane * 4));
+                            v.x += x.x;
+                            v.y += x.y;
+                            v.z += x.z;
+                            v.w += x.w;
+                        }
+                        sum.x = fmaf(c, v.x, sum.x);
+                        sum.y = fmaf(c, v.y, sum.y);
+                        sum.z = fmaf(c, v.z, sum.z);
+                        sum.w = fmaf(c, v.w, sum.w);
+                    }
+                    *reinterpret_cast<uint2 *>(p.out + t * p.ldo + k) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                }
+            }
+        }
+    }
+    if (!ok) {
+        s.failed = 1;
+        atomicExch(&g_dense_error, kErrTimeout);
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kMoeCols);
+    }
+    // the last block to leave: everyone has passed every barrier
+    if (threadIdx.x == 0 && s.failed == 0 && add_acq_rel_gpu(p.counters + 4, 1u) == gridDim.x - 1)
+        for (int i = 0; i < 5; ++i) p.counters[i] = 0;
+}
+
+}  // namespace mbglu

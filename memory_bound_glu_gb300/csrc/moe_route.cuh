@@ -1,0 +1,111 @@
+// moe_route.cuh -- the router of the expert layer: logits whose value does not
+// depend on the order of a sum, and a warp's choice of the top experts.
+//
+// An expert is chosen or not, so a logit that is off in its last bit can exchange
+// whole experts.  Products of two bf16 numbers are exact in fp32; their sum is carried
+// as an unevaluated pair s + c (Knuth's two-sum: s the rounded sum, c the sum of the
+// roundings, each of which is exact), whose error is of second order, and rounded once.
+// The logit is then the fp32 number nearest to the exact sum, whatever the order: kernels,
+// batch sizes and grids choose alike.  Six additions for each product: 64 rows x 128
+// experts x 2048 take 118 M operations, 3 us of the part's fp32 rate.
+#pragma once
+#include "glu_math.cuh"
+#include "ptx.cuh"
+
+namespace mbglu {
+
+constexpr int kMoeMaxRows = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 16;
+
+// (s, c) += x, exactly but for c's own rounding
+__device__ __forceinline__ void two_sum(float &s, float &c, float x)
+{
+    const float t = __fadd_rn(s, x);
+    const float b = __fsub_rn(t, s);
+    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    s = t;
+}
+
+// What a warp's lanes hold as (s, c), as one rounded number in every lane.  An infinite
+// or NaN sum is the plain one: its roundings are infinity - infinity.
+__device__ __forceinline__ float warp_pair_sum(float s, float c)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float s2 = __shfl_xor_sync(0xffffffffu, s, o), c2 = __shfl_xor_sync(0xffffffffu, c, o);
+        two_sum(s, c, s2);
+        c = __fadd_rn(c, c2);
+    }
+    const float v = __fadd_rn(s, c);
+    return isfinite(s) ? v : s;
+}
+
+// Orders floats as integers; -0 counts as 0, NaN is below everything.
+__device__ __forceinline__ uint32_t order_key(float x)
+{
+    if (isnan(x)) return 0;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// One warp: the top_k of `experts` logits, largest first, ties to the lowest index, and
+// their softmax weights (over all logits, or over the chosen ones).  Lane j < top_k gets
+// the j-th.  A row with a NaN logit gets NaN weights.  PER: logits per lane, 32 PER >=
+// experts; logit(e) reads one.
+template <int PER, typename F>
+__device__ __forceinline__ void warp_top_k(F logit, int experts, int top_k, bool renormalize, int &id, float &weight)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t key[PER];
+    float v[PER], top = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = i * 32 + lane;
+        v[i] = e < experts ? logit(e) : -INFINITY;
+        nan = nan || isnan(v[i]);
+        // an expert that does not exist is below one that is NaN: keys of experts start at 1
+        key[i] = e < experts ? max(order_key(v[i]), 1u) : 0u;
+        top = fmaxf(top, v[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    nan = __any_sync(0xffffffffu, nan);
+    float sum = 0.0f;
+    if (!renormalize) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (i * 32 + lane < experts) sum += expf(v[i] - top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    id = 0;
+    float mine = 0.0f;
+    for (int j = 0; j < top_k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        uint32_t at = 0xffffffffu;
+        float val = 0.0f;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] == best) {
+                at = static_cast<uint32_t>(i * 32 + lane);
+                val = v[i];
+            }
+        const uint32_t first = __reduce_min_sync(0xffffffffu, at);
+        const float x = __shfl_sync(0xffffffffu, val, static_cast<int>(first & 31u));
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (static_cast<uint32_t>(i * 32 + lane) == first) key[i] = 0;
+        const float e = expf(x - top);
+        if (renormalize) sum += e;
+        if (lane == j) {
+            id = static_cast<int>(first);
+            mine = e;
+        }
+    }
+    weight = nan ? __uint_as_float(0x7fffffffu) : mine / sum;
+}
+
+}  // namespace mbglu

@@ -10,15 +10,6 @@ namespace mbglu_host {
 
 constexpr int kPairs = 76;   // SM pairs of the part: what a split of the inner dimension is planned for
 
-// An operand that tensor copies take: 16-byte aligned rows.
-inline bool copyable(const void *p, int64_t ld, int elem) { return aligned(p, 16) && ld * elem % 16 == 0; }
-
-// 2 when every row of elem-byte elements starts on 32 bytes, 1 on 16, else 0
-inline int row_align(const void *p, int64_t ld, int elem)
-{
-    return aligned(p, 32) && ld * elem % 32 == 0 ? 2 : aligned(p, 16) && ld * elem % 16 == 0 ? 1 : 0;
-}
-
 // A product's tiles over the SM pairs: full rounds whole; what is left over,
 // where it fills at most half of the pairs, in as many ranges of the inner
 // dimension as fill them (each of at least 8 stages), if that shortens the
