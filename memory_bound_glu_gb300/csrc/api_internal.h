@@ -46,6 +46,7 @@ void fp8_block_plan(bool dual, int M, int N, int K, int *plan);
 // Reads and clears the unit's device error word; the device is idle.
 cudaError_t take_gemm_error(int *w);
 cudaError_t take_fp8_error(int *w);
+cudaError_t take_lora_error(int *w);
 cudaError_t take_moe_error(int *w);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -5,6 +5,8 @@
 #include "api_internal.h"
 #include "dense_launch.h"
 #include "lora_generic.cuh"
+#include "lora_pair.cuh"
+#include "pair_plan.h"
 
 namespace {
 
@@ -13,7 +15,61 @@ using namespace mbglu_host;
 constexpr int64_t kAlign = 256;
 int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
-int64_t lora_space(int sides, int M, int R) { return padded(static_cast<int64_t>(M) * sides * R * 4); }
+// Up to this many rows the adapters' term is left to the join, where every (row, output)
+// has a lane of its own.
+#ifndef LORA_JOIN_ROWS_FROM
+#define LORA_JOIN_ROWS_FROM 9
+#endif
+constexpr int kJoinRows = 64;
+
+// Tiles and ranges, from the sizes alone.  The estimate (ns) of a tile's time is
+// tall_tokens' (gemm_api.cu); a join costs its launch and the partial sums' way to L2 and
+// back.
+mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, bool may_split)
+{
+    mbglu::LoraPlan best = {};
+    double least = 0;
+    const int chunks = ceil_div(K, 64), wt = sides == 2 ? 128 : 256, nt = ceil_div(N, wt);
+    for (int tn = 32; tn <= mbglu::kPairTile; tn += 32) {
+        if (tn > 32 && tn - 32 >= M) break;
+        const int64_t tiles = static_cast<int64_t>(nt) * ceil_div(M, tn);
+        if (tiles > INT32_MAX / 16) continue;
+        const auto tile_ns = [&](int64_t at_once, int64_t n) { return n * (77.0 + 59.0 * std::min<int64_t>(at_once, kPairs) / kPairs + 0.7 * tn) + 15.5 * tn; };
+        const bool join = may_split && M >= LORA_JOIN_ROWS_FROM && M <= kJoinRows;
+        for (int split = 0; split < 2; ++split) {
+            const int64_t left = join ? tiles : tiles % kPairs;
+            const int64_t s = split && left > 0 ? std::min<int64_t>({std::max<int64_t>(kPairs / left, 1), std::max(chunks / 8, 1), 16}) : 1;
+            if (split && !may_split) continue;
+            if (join ? !split : split && s < 2) continue;
+            const int64_t whole = split ? tiles - left : tiles;
+            double ns = (whole + kPairs - 1) / kPairs * tile_ns(whole, chunks);
+            if (split) ns += (left * s + kPairs - 1) / kPairs * tile_ns(left * s, (chunks + s - 1) / s) + 3000 + left * s * tn * 2048.0 / 4000;
+            if (least == 0 || ns < least) {
+                least = ns;
+                best.tn = tn;
+                best.wt = wt;
+                best.ttiles = ceil_div(M, tn);
+                best.ntiles = static_cast<int>(tiles);
+                best.whole = static_cast<int>(whole);
+                best.rest = split ? static_cast<int>(left) : 0;
+                best.splits = static_cast<int>(s);
+                best.items = static_cast<int>(whole + (split ? left * s : 0));
+                best.nchunk = chunks;
+            }
+        }
+    }
+    return best;
+}
+
+int64_t lora_p_bytes(int sides, int M, int R) { return padded(static_cast<int64_t>(M) * sides * R * 4); }
+
+int64_t lora_part_bytes(const mbglu::LoraPlan &q) { return static_cast<int64_t>(q.rest) * q.splits * q.tn * 1024; }
+
+// p, then the partial sums
+int64_t lora_space(int sides, int M, int N, int K, int R)
+{
+    return lora_p_bytes(sides, M, R) + padded(lora_part_bytes(lora_plan(sides, M, N, K, true)));
+}
 
 bool bad_rank(int adapters, int R) { return adapters < 0 || adapters > kMostSize || R < 0 || R > MBGLU_LORA_MAX_RANK; }
 
@@ -21,6 +77,83 @@ bool bad_rank(int adapters, int R) { return adapters < 0 || adapters > kMostSize
 int64_t extent3(int64_t count, int64_t rows, int64_t cols, int64_t stride, int64_t ld)
 {
     return count <= 0 || rows <= 0 || cols <= 0 ? 0 : (count - 1) * stride * 2 + extent(rows, cols, ld, 2);
+}
+
+template <int SIDES, int MT, int NT>
+mbglu_status launch_shrink(const mbglu::LoraParams &p, int side_by_side, cudaStream_t stream)
+{
+    const int64_t groups = (static_cast<int64_t>(p.M) + MT * 16 - 1) / (MT * 16);
+    Launch l(dim3(static_cast<unsigned>(SIDES * ceil_div(p.R, NT * 8)), static_cast<unsigned>(std::min<int64_t>(groups, 32768)), static_cast<unsigned>(side_by_side)),
+             mbglu::kShrinkWarps * 32, mbglu::shrink_smem<MT, NT>(), stream);
+    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::lora_shrink_kernel<SIDES, MT, NT>, p));
+}
+
+template <int SIDES>
+cudaError_t setup_pair()
+{
+    cudaError_t e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(mbglu::lora_shrink_kernel<SIDES, 2, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(mbglu::shrink_smem<2, 8>()));
+    return e;
+}
+
+// Operands that the CTA-pair kernel and lora_shrink_kernel take.
+bool fast_operands(const mbglu::LoraParams &p, int sides)
+{
+    if (p.K == 0 || !copyable(p.x, p.ldx, 2)) return false;
+    for (int d = 0; d < sides; ++d) {
+        const mbglu::LoraSide &s = p.side[d];
+        if (!copyable(s.w, s.ldw, 2)) return false;
+        if (p.adapters == 0) continue;
+        // K's last 16 bytes are read whole; of B 8 bytes at a time
+        if (p.K % 8 != 0 || p.R % 8 != 0 || !copyable(s.a, s.lda, 2) || !aligned(s.b, 8) || s.ldb % 4 != 0) return false;
+        if (p.adapters > 1 && (s.a_adapter % 8 != 0 || s.b_adapter % 4 != 0)) return false;
+    }
+    return true;
+}
+
+template <int SIDES>
+mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *taken, cudaStream_t stream)
+{
+    *taken = false;
+    if (!fast_operands(l, SIDES)) return MBGLU_OK;
+    mbglu::LoraPairParams p = {};
+    p.l = l;
+    p.plan = lora_plan(SIDES, l.M, l.N, l.K, l.adapters > 0);
+    if (p.plan.ntiles == 0) return MBGLU_OK;
+    mbglu::PairMaps maps;
+    for (int d = 0; d < SIDES; ++d)
+        if (!encode_tile_map(&maps.a[d], l.side[d].w, l.side[d].ldw, l.N, l.K, 64, p.plan.wt / 2, 2)) return MBGLU_OK;
+    if (!encode_tile_map(&maps.b[0], l.x, l.ldx, l.M, l.K, 64, p.plan.tn / 2, 2)) return MBGLU_OK;
+    static DeviceTable table;
+    int sms = 0;
+    mbglu_status st = table.get(&sms, setup_pair<SIDES>);
+    if (st != MBGLU_OK) return st;
+    *taken = true;
+    if (l.adapters > 0) {
+        // few rows: a block per adapter of a group and 8 columns; many: columns together, so
+        // that the rows are read once or twice
+        p.early = launch_policy() != MBGLU_POLICY_SERIAL;
+        if (l.M <= 64)
+            st = launch_shrink<SIDES, 1, 1>(l, std::min(l.M, 16), stream);
+        else if (l.R <= 16)
+            st = launch_shrink<SIDES, 2, 2>(l, 1, stream);
+        else if (l.R <= 32)
+            st = launch_shrink<SIDES, 2, 4>(l, 1, stream);
+        else
+            st = launch_shrink<SIDES, 2, 8>(l, 1, stream);
+        if (st != MBGLU_OK) return st;
+    }
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + lora_p_bytes(SIDES, l.M, l.R));
+    Launch c(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.items))), mbglu::kPairThreads, mbglu::kLoraSmem, stream, 2);
+    st = launched(cudaLaunchKernelEx(&c.cfg, mbglu::lora_pair_kernel<SIDES>, p, maps));
+    if (st == MBGLU_OK && p.plan.rest > 0) {
+        const int64_t warps = static_cast<int64_t>(p.plan.rest) * ceil_div(p.plan.wt, 32) * (p.plan.tn / 4);
+        Launch j(dim3(static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, 1 << 20))), 256, 0, stream);
+        st = launched(cudaLaunchKernelEx(&j.cfg, mbglu::lora_join_kernel<SIDES>, p));
+    }
+    return st;
 }
 
 template <int SIDES>
@@ -48,7 +181,7 @@ mbglu_status run(mbglu::LoraParams &p, void *workspace, size_t workspace_bytes, 
         for (int d = 0; d < SIDES; ++d) ok = ok && aligned(p.side[d].a, 2) && aligned(p.side[d].b, 2);
     }
     if (!ok) return MBGLU_ERR_ALIGN;
-    const int64_t need = adapted ? lora_space(SIDES, M, R) : 0;
+    const int64_t need = adapted ? lora_space(SIDES, M, N, K, R) : 0;
     if (workspace_bytes < static_cast<size_t>(need)) return MBGLU_ERR_SHAPE;
     const void *outs[2] = {p.out, workspace};
     const int64_t outb[2] = {extent(M, N, p.ldo, 2), need};
@@ -67,7 +200,12 @@ mbglu_status run(mbglu::LoraParams &p, void *workspace, size_t workspace_bytes, 
             return MBGLU_ERR_ALIAS;
     }
     p.p = static_cast<float *>(workspace);
-    mbglu_status st = MBGLU_OK;
+    bool taken = false;
+    mbglu_status st = launch_pair<SIDES>(p, workspace, &taken, stream);
+    if (taken || st != MBGLU_OK) {
+        if (st == MBGLU_OK) set_last_variant(kLoraPair);
+        return st;
+    }
     if (adapted) {
         const int64_t warps = static_cast<int64_t>(M) * SIDES * R;
         Launch l(dim3(static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, 1 << 20))), 256, 0, stream);
@@ -123,13 +261,13 @@ extern "C" {
 size_t glu_lora_workspace_bytes(int M, int N, int K, int adapters, int R)
 {
     if (bad_sizes(M, N, K) || N > INT32_MAX / 2 || bad_rank(adapters, R) || std::min({M, N, K, adapters, R}) == 0) return 0;
-    return static_cast<size_t>(lora_space(2, M, R));
+    return static_cast<size_t>(lora_space(2, M, N, K, R));
 }
 
 size_t linear_lora_workspace_bytes(int M, int N, int K, int adapters, int R)
 {
     if (bad_sizes(M, N, K) || N > INT32_MAX / 2 || bad_rank(adapters, R) || std::min({M, N, K, adapters, R}) == 0) return 0;
-    return static_cast<size_t>(lora_space(1, M, R));
+    return static_cast<size_t>(lora_space(1, M, N, K, R));
 }
 
 mbglu_status glu_lora(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w, int64_t ld_gate, const mbglu_bf16 *up_w, int64_t ld_up,
@@ -155,3 +293,14 @@ mbglu_status linear_lora(const mbglu_bf16 *x, int64_t ldx, const mbglu_bf16 *w, 
 }
 
 }  // extern "C"
+
+namespace mbglu_host {
+
+cudaError_t take_lora_error(int *w)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(w, mbglu::g_dense_error, sizeof *w);
+    const int zero = 0;
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(mbglu::g_dense_error, &zero, sizeof zero);
+}
+
+}  // namespace mbglu_host

@@ -1963,7 +1963,8 @@ mbglu_status mbglu_read_device_error(int *word)
     if ((e = cudaMemcpyFromSymbol(&w, mbglu::g_device_error, sizeof w)) != cudaSuccess) return cuda_fail(e);
     const int zero = 0;
     if ((e = cudaMemcpyToSymbol(mbglu::g_device_error, &zero, sizeof zero)) != cudaSuccess) return cuda_fail(e);
-    for (cudaError_t (*take)(int *) : {mbglu_host::take_gemm_error, mbglu_host::take_fp8_error, mbglu_host::take_moe_error}) {
+    for (cudaError_t (*take)(int *) : {mbglu_host::take_gemm_error, mbglu_host::take_fp8_error, mbglu_host::take_lora_error,
+                                        mbglu_host::take_moe_error}) {
         int x = 0;   // the other translation units' words
         if ((e = take(&x)) != cudaSuccess) return cuda_fail(e);
         if (w == 0) w = x;
