@@ -501,9 +501,9 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
  * what other rows' adapters hold, infinities and NaN too, does not reach it.  Neither
  * the batch's size nor a row's place changes which adapter it gets.  Rows of one
  * adapter may lie anywhere; next to one another they are faster.
- * The fast kernels want h, the weights and A 16-byte aligned with row and adapter
- * strides that are multiples of 8 elements, B 8-byte aligned with strides that are
- * multiples of 4, and K and R multiples of 8; other operands take slower kernels.
+ * The fast kernels want h, the weights, A and B 16-byte aligned with row and adapter
+ * strides that are multiples of 8 elements, and K and R multiples of 8; other
+ * operands take slower kernels.
  * Errors as glu_gemm: MBGLU_ERR_SHAPE also for adapters or R out of range or a
  * workspace that is too small.
  */

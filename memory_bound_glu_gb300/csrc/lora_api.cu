@@ -15,11 +15,8 @@ using namespace mbglu_host;
 constexpr int64_t kAlign = 256;
 int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
-// Up to this many rows the adapters' term is left to the join, where every (row, output)
-// has a lane of its own.
-#ifndef LORA_JOIN_ROWS_FROM
-#define LORA_JOIN_ROWS_FROM 9
-#endif
+// From two rows up to this many the adapters' term is left to the join, where every (row,
+// output) has a lane of its own: rows of a decode batch mostly have an adapter each.
 constexpr int kJoinRows = 64;
 
 // Tiles and ranges, from the sizes alone.  The estimate (ns) of a tile's time is
@@ -35,7 +32,7 @@ mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, bool may_split)
         const int64_t tiles = static_cast<int64_t>(nt) * ceil_div(M, tn);
         if (tiles > INT32_MAX / 16) continue;
         const auto tile_ns = [&](int64_t at_once, int64_t n) { return n * (77.0 + 59.0 * std::min<int64_t>(at_once, kPairs) / kPairs + 0.7 * tn) + 15.5 * tn; };
-        const bool join = may_split && M >= LORA_JOIN_ROWS_FROM && M <= kJoinRows;
+        const bool join = may_split && M >= 2 && M <= kJoinRows;
         for (int split = 0; split < 2; ++split) {
             const int64_t left = join ? tiles : tiles % kPairs;
             const int64_t s = split && left > 0 ? std::min<int64_t>({std::max<int64_t>(kPairs / left, 1), std::max(chunks / 8, 1), 16}) : 1;
@@ -65,11 +62,22 @@ int64_t lora_p_bytes(int sides, int M, int R) { return padded(static_cast<int64_
 
 int64_t lora_part_bytes(const mbglu::LoraPlan &q) { return static_cast<int64_t>(q.rest) * q.splits * q.tn * 1024; }
 
-// p, then the partial sums
-int64_t lora_space(int sides, int M, int N, int K, int R)
+// Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, partial sums
+struct LoraSpace {
+    int64_t terms, blocks, part, bytes;
+};
+
+LoraSpace lora_space(int sides, int M, int R, const mbglu::LoraPlan &plan)
 {
-    return lora_p_bytes(sides, M, R) + padded(lora_part_bytes(lora_plan(sides, M, N, K, true)));
+    LoraSpace s = {};
+    s.terms = lora_p_bytes(sides, M, R);
+    s.blocks = s.terms + lora_p_bytes(sides, M, R);
+    s.part = s.blocks + padded((static_cast<int64_t>(M) + mbglu::kLoraBlock - 1) / mbglu::kLoraBlock * 4);
+    s.bytes = s.part + padded(lora_part_bytes(plan));
+    return s;
 }
+
+int64_t lora_bytes(int sides, int M, int N, int K, int R) { return lora_space(sides, M, R, lora_plan(sides, M, N, K, true)).bytes; }
 
 bool bad_rank(int adapters, int R) { return adapters < 0 || adapters > kMostSize || R < 0 || R > MBGLU_LORA_MAX_RANK; }
 
@@ -79,13 +87,18 @@ int64_t extent3(int64_t count, int64_t rows, int64_t cols, int64_t stride, int64
     return count <= 0 || rows <= 0 || cols <= 0 ? 0 : (count - 1) * stride * 2 + extent(rows, cols, ld, 2);
 }
 
-template <int SIDES, int MT, int NT>
-mbglu_status launch_shrink(const mbglu::LoraParams &p, int side_by_side, cudaStream_t stream)
+// The cluster's blocks split the inner dimension: as many as leave a warp about five steps,
+// so that all of its loads are on the way together, and no more than `most` blocks in all.
+template <int SIDES, int MT, int NT, int UNROLL>
+mbglu_status launch_shrink(const mbglu::LoraParams &p, int side_by_side, int most, cudaStream_t stream)
 {
-    const int64_t groups = (static_cast<int64_t>(p.M) + MT * 16 - 1) / (MT * 16);
-    Launch l(dim3(static_cast<unsigned>(SIDES * ceil_div(p.R, NT * 8)), static_cast<unsigned>(std::min<int64_t>(groups, 32768)), static_cast<unsigned>(side_by_side)),
-             mbglu::kShrinkWarps * 32, mbglu::shrink_smem<MT, NT>(), stream);
-    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::lora_shrink_kernel<SIDES, MT, NT>, p));
+    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(p.M) + MT * 16 - 1) / (MT * 16), 32768);
+    const int64_t blocks = groups * SIDES * ceil_div(p.R, NT * 8) * side_by_side;
+    int split = 1;
+    while (split < 8 && ceil_div(p.K, 32) > 5 * mbglu::kShrinkWarps * split && blocks * split * 2 <= most) split *= 2;
+    Launch l(dim3(static_cast<unsigned>(SIDES * ceil_div(p.R, NT * 8) * split), static_cast<unsigned>(groups), static_cast<unsigned>(side_by_side)),
+             mbglu::kShrinkWarps * 32, mbglu::shrink_smem<MT, NT>(), stream, split);
+    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::lora_shrink_kernel<SIDES, MT, NT, UNROLL>, p, split));
 }
 
 template <int SIDES>
@@ -93,9 +106,17 @@ cudaError_t setup_pair()
 {
     cudaError_t e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(mbglu::lora_shrink_kernel<SIDES, 2, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(mbglu::lora_shrink_kernel<SIDES, 2, 8, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(mbglu::shrink_smem<2, 8>()));
     return e;
+}
+
+template <int SIDES, int TOKENS>
+mbglu_status launch_join(const mbglu::LoraPairParams &p, cudaStream_t stream)
+{
+    const int64_t warps = static_cast<int64_t>(p.plan.rest) * ceil_div(p.plan.wt, 32) * (p.plan.tn / TOKENS);
+    Launch j(dim3(static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, 1 << 20))), 256, 0, stream);
+    return launched(cudaLaunchKernelEx(&j.cfg, mbglu::lora_join_kernel<SIDES, TOKENS>, p));
 }
 
 // Operands that the CTA-pair kernel and lora_shrink_kernel take.
@@ -106,9 +127,10 @@ bool fast_operands(const mbglu::LoraParams &p, int sides)
         const mbglu::LoraSide &s = p.side[d];
         if (!copyable(s.w, s.ldw, 2)) return false;
         if (p.adapters == 0) continue;
-        // K's last 16 bytes are read whole; of B 8 bytes at a time
-        if (p.K % 8 != 0 || p.R % 8 != 0 || !copyable(s.a, s.lda, 2) || !aligned(s.b, 8) || s.ldb % 4 != 0) return false;
-        if (p.adapters > 1 && (s.a_adapter % 8 != 0 || s.b_adapter % 4 != 0)) return false;
+        // rows are read 16 bytes at a time, the last ones too
+        // rows are read 16 bytes at a time, the last ones too
+        if (p.K % 8 != 0 || p.R % 8 != 0 || !copyable(s.a, s.lda, 2) || !copyable(s.b, s.ldb, 2)) return false;
+        if (p.adapters > 1 && (s.a_adapter % 8 != 0 || s.b_adapter % 8 != 0)) return false;
     }
     return true;
 }
@@ -122,37 +144,52 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
     p.l = l;
     p.plan = lora_plan(SIDES, l.M, l.N, l.K, l.adapters > 0);
     if (p.plan.ntiles == 0) return MBGLU_OK;
-    mbglu::PairMaps maps;
+    char *ws = static_cast<char *>(workspace);
+    const LoraSpace space = lora_space(SIDES, l.M, l.R, p.plan);
+    const bool adapted = l.adapters > 0, whole = p.plan.whole > 0;
+    mbglu::LoraMaps maps;
     for (int d = 0; d < SIDES; ++d)
-        if (!encode_tile_map(&maps.a[d], l.side[d].w, l.side[d].ldw, l.N, l.K, 64, p.plan.wt / 2, 2)) return MBGLU_OK;
-    if (!encode_tile_map(&maps.b[0], l.x, l.ldx, l.M, l.K, 64, p.plan.tn / 2, 2)) return MBGLU_OK;
+        if (!encode_tile_map(&maps.w[d], l.side[d].w, l.side[d].ldw, l.N, l.K, 64, p.plan.wt / 2, 2)) return MBGLU_OK;
+    if (!encode_tile_map(&maps.x, l.x, l.ldx, l.M, l.K, 64, p.plan.tn / 2, 2)) return MBGLU_OK;
+    if (adapted) {
+        const int width = SIDES * l.R;
+        p.l.p = reinterpret_cast<float *>(ws);
+        p.l.terms = reinterpret_cast<uint16_t *>(ws + space.terms);
+        p.part = reinterpret_cast<float *>(ws + space.part);
+        if (whole) {   // tiles in ranges leave the adapters' term to the join
+            p.l.blocks = reinterpret_cast<int32_t *>(ws + space.blocks);
+            for (int d = 0; d < SIDES; ++d) {
+                const mbglu::LoraSide &s = l.side[d];
+                if ((l.adapters > 1 && s.b_adapter <= 0) ||
+                    !encode_stack_map(&maps.b[d], s.b, s.b_adapter, s.ldb, l.adapters, l.N, l.R, 64, p.plan.wt / 2))
+                    return MBGLU_OK;
+            }
+            for (int i = 0; i < 2; ++i)
+                if (!encode_tile_map(&maps.p[i], p.l.terms + static_cast<int64_t>(i) * l.M * width, width, l.M, width, 64, 16, 2)) return MBGLU_OK;
+        }
+    }
     static DeviceTable table;
     int sms = 0;
     mbglu_status st = table.get(&sms, setup_pair<SIDES>);
     if (st != MBGLU_OK) return st;
     *taken = true;
-    if (l.adapters > 0) {
+    if (adapted) {
         // few rows: a block per adapter of a group and 8 columns; many: columns together, so
         // that the rows are read once or twice
         p.early = launch_policy() != MBGLU_POLICY_SERIAL;
-        if (l.M <= 64)
-            st = launch_shrink<SIDES, 1, 1>(l, std::min(l.M, 16), stream);
+        if (l.M <= kJoinRows)
+            st = launch_shrink<SIDES, 1, 1, 5>(p.l, std::min(l.M, 16), 1024, stream);
         else if (l.R <= 16)
-            st = launch_shrink<SIDES, 2, 2>(l, 1, stream);
+            st = launch_shrink<SIDES, 2, 2, 2>(p.l, 1, 608, stream);
         else if (l.R <= 32)
-            st = launch_shrink<SIDES, 2, 4>(l, 1, stream);
+            st = launch_shrink<SIDES, 2, 4, 1>(p.l, 1, 304, stream);
         else
-            st = launch_shrink<SIDES, 2, 8>(l, 1, stream);
+            st = launch_shrink<SIDES, 2, 8, 1>(p.l, 1, 304, stream);
         if (st != MBGLU_OK) return st;
     }
-    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + lora_p_bytes(SIDES, l.M, l.R));
     Launch c(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.items))), mbglu::kPairThreads, mbglu::kLoraSmem, stream, 2);
     st = launched(cudaLaunchKernelEx(&c.cfg, mbglu::lora_pair_kernel<SIDES>, p, maps));
-    if (st == MBGLU_OK && p.plan.rest > 0) {
-        const int64_t warps = static_cast<int64_t>(p.plan.rest) * ceil_div(p.plan.wt, 32) * (p.plan.tn / 4);
-        Launch j(dim3(static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, 1 << 20))), 256, 0, stream);
-        st = launched(cudaLaunchKernelEx(&j.cfg, mbglu::lora_join_kernel<SIDES>, p));
-    }
+    if (st == MBGLU_OK && p.plan.rest > 0) st = l.M <= 16 ? launch_join<SIDES, 1>(p, stream) : launch_join<SIDES, 4>(p, stream);
     return st;
 }
 
@@ -181,7 +218,7 @@ mbglu_status run(mbglu::LoraParams &p, void *workspace, size_t workspace_bytes, 
         for (int d = 0; d < SIDES; ++d) ok = ok && aligned(p.side[d].a, 2) && aligned(p.side[d].b, 2);
     }
     if (!ok) return MBGLU_ERR_ALIGN;
-    const int64_t need = adapted ? lora_space(SIDES, M, N, K, R) : 0;
+    const int64_t need = adapted ? lora_bytes(SIDES, M, N, K, R) : 0;
     if (workspace_bytes < static_cast<size_t>(need)) return MBGLU_ERR_SHAPE;
     const void *outs[2] = {p.out, workspace};
     const int64_t outb[2] = {extent(M, N, p.ldo, 2), need};
@@ -199,7 +236,7 @@ mbglu_status run(mbglu::LoraParams &p, void *workspace, size_t workspace_bytes, 
                         overlaps(outs[i], outb[i], p.scale, p.scale ? static_cast<int64_t>(p.adapters) * 4 : 0)))
             return MBGLU_ERR_ALIAS;
     }
-    p.p = static_cast<float *>(workspace);
+    p.p = static_cast<float *>(workspace);   // the kernels for any alignment need no more
     bool taken = false;
     mbglu_status st = launch_pair<SIDES>(p, workspace, &taken, stream);
     if (taken || st != MBGLU_OK) {
@@ -261,13 +298,13 @@ extern "C" {
 size_t glu_lora_workspace_bytes(int M, int N, int K, int adapters, int R)
 {
     if (bad_sizes(M, N, K) || N > INT32_MAX / 2 || bad_rank(adapters, R) || std::min({M, N, K, adapters, R}) == 0) return 0;
-    return static_cast<size_t>(lora_space(2, M, N, K, R));
+    return static_cast<size_t>(lora_bytes(2, M, N, K, R));
 }
 
 size_t linear_lora_workspace_bytes(int M, int N, int K, int adapters, int R)
 {
     if (bad_sizes(M, N, K) || N > INT32_MAX / 2 || bad_rank(adapters, R) || std::min({M, N, K, adapters, R}) == 0) return 0;
-    return static_cast<size_t>(lora_space(1, M, N, K, R));
+    return static_cast<size_t>(lora_bytes(1, M, N, K, R));
 }
 
 mbglu_status glu_lora(const mbglu_bf16 *h, int64_t ldh, const mbglu_bf16 *gate_w, int64_t ld_gate, const mbglu_bf16 *up_w, int64_t ld_up,

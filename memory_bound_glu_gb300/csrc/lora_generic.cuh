@@ -23,6 +23,8 @@ struct LoraParams {
     const int32_t *adapter;
     const float *scale;      // null: 1
     float *p;                // [M][sides R]: the second side's from column R on
+    uint16_t *terms;         // [2][M][sides R]: p's two bf16 terms
+    int32_t *blocks;         // of 32 rows each: their adapter, or that they have none or several; or null
     uint16_t *out;
     int64_t ldo;
     int M, N, K, adapters, R, mode;

@@ -3,11 +3,17 @@
 // tiles and roles), and the adapters' term added where the accumulators are read.
 //
 // The adapters' term p[m] B[a]^T is not a product of matrices: every row has a B of its
-// own.  Tokens are taken eight at a time: for each adapter among them a warp's tensor
-// cores multiply its 32 rows of B with the eight tokens' p (as two bf16 terms, off by
-// 2^-18), and a token takes the product with its own adapter.  So nothing of other adapters
-// enters a token's sum, infinities neither, and eight tokens of one adapter cost one such
-// product.
+// own, and what another row's adapter holds, infinities too, must not reach it.  So:
+//   * 32 rows of one adapter, and runs of them, go through the tensor cores as the shared
+//     product does: more chunks of the inner dimension, with B as the weights and p's two
+//     bf16 terms (off by 2^-18) as the tokens, into the run's columns of the accumulator.
+//     With two projections the inner dimension is p = [gate's | up's]; a box of B that
+//     begins R columns early, or ends late, is filled with zeros there.
+//   * 32 rows of several adapters are left to the epilogue: for each adapter among 16 of
+//     them a warp's own tensor cores (mma.sync) multiply its 32 rows of B with all 16
+//     tokens' p, and a token takes the product with its own adapter.
+// A prompt's rows are nearly all of the first kind, a chunk of many short requests has the
+// second.
 //
 // Tiles that would leave SM pairs without work are cut along the inner dimension: their
 // ranges leave partial sums, and lora_join_kernel adds them, the adapters' term and the
@@ -25,6 +31,12 @@ struct LoraPlan {
     int rest, splits;        // the others, each in `splits` ranges of the inner dimension
     int items;               // whole + rest splits
     int nchunk;
+};
+
+struct LoraMaps {
+    TensorMap w[2], x;
+    TensorMap b[2];          // [adapters][N][R]
+    TensorMap p[2];          // p's terms, [M][sides R], boxes of 64 x 16
 };
 
 struct LoraPairParams {
@@ -54,64 +66,129 @@ __host__ __device__ inline LoraTile lora_tile(const LoraPlan &p, int i)
     return x;
 }
 
-// The adapters' term of 32 outputs from n0 on and eight tokens from m0 on: term[token *
-// kTermPitch + output].  The whole warp; whether there was any is returned.
+// A box of a stack of matrices into this CTA's shared memory, counted on a barrier of either
+// CTA of the pair.
+__device__ __forceinline__ void pair_load_3d(void *dst, const TensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// The runs of 32-row blocks (the least that a pair's MMA takes as columns) with one adapter in a tile of tokens; a warp walks them.
+struct LoraRuns {
+    int mine, blocks, at, first, adapter;   // run: blocks first .. at - 1
+    __device__ LoraRuns(const LoraParams &p, int m0, int tn)
+    {
+        const int lane = threadIdx.x & 31;
+        blocks = min(tn / kLoraBlock, (p.M - m0 + kLoraBlock - 1) / kLoraBlock);
+        mine = lane < blocks ? __ldcg(p.blocks + m0 / kLoraBlock + lane) : kNoAdapter;
+        at = 0;
+    }
+    __device__ bool next()
+    {
+        while (at < blocks) {
+            first = at;
+            adapter = __shfl_sync(0xffffffffu, mine, at++);
+            if (adapter < 0) continue;
+            while (at < blocks && __shfl_sync(0xffffffffu, mine, at) == adapter) ++at;
+            return true;
+        }
+        return false;
+    }
+};
+
+// The adapters' term of 32 outputs from n0 on and 16 tokens from m0 on, a warp; tile(half) is
+// called for each half of the tokens with term[token * kTermPitch + output].
 constexpr int kTermPitch = 36;
 constexpr int kTermWords = 8 * kTermPitch;
-__device__ __forceinline__ bool lora_term(const LoraParams &p, int d, int sides, int64_t m0, int n0, float *term)
+template <typename F>
+__device__ __forceinline__ void lora_term(const LoraParams &p, int d, int sides, int64_t m0, int n0, float *term, F tile)
 {
     const int lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
-    const int64_t m = m0 + row;
-    const int mine = lora_adapter(p, m);
+    // lanes 0-15 hold the tokens' adapters
+    const int mine = lane < 16 ? lora_adapter(p, m0 + lane) : -1;
     uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
-    if (!left) return false;
+    const bool used[2] = {(left >> row & 1u) != 0, (left >> (8 + row) & 1u) != 0};
     const LoraSide &side = p.side[d];
-    const float *q = p.p + m * sides * p.R + d * p.R + quad * 4;
-    float sum[2][4] = {};
+    const float *q = p.p + (m0 + row) * sides * p.R + d * p.R + quad * 4;
+    const int64_t second = 8 * static_cast<int64_t>(sides) * p.R;
+    float sum[2][2][4] = {};   // halves of the tokens, halves of the outputs
     while (left) {
-        const int a = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
-        const uint32_t match = __ballot_sync(0xffffffffu, mine == a);
-        left &= ~match;
-        float acc[2][4] = {};
-        const uint16_t *b = side.b + a * side.b_adapter + (n0 + row) * side.ldb + quad * 4;
-#pragma unroll 2
+        // two adapters at a time, so that their rows are on the way together
+        int a[2];
+        uint32_t match[2];
+        a[0] = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+        match[0] = __ballot_sync(0xffffffffu, mine == a[0]);
+        left &= ~match[0];
+        a[1] = __shfl_sync(0xffffffffu, mine, left ? __ffs(left) - 1 : 0);
+        a[1] = left ? a[1] : a[0];
+        match[1] = __ballot_sync(0xffffffffu, mine == a[1]);
+        left &= ~match[1];
+        float acc[2][2][2][4] = {};
+        const uint16_t *b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) b[i] = side.b + a[i] * side.b_adapter + (n0 + row) * side.ldb + quad * 4;
         for (int j = 0; j < p.R; j += 16) {
             const bool in = j + quad * 4 < p.R;
-            uint2 w[4];
+            uint2 w[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = in && n0 + row + i * 8 < p.N ? *reinterpret_cast<const uint2 *>(b + i * 8 * side.ldb + j) : make_uint2(0, 0);
-            const float4 v = in && mine >= 0 ? *reinterpret_cast<const float4 *>(q + j) : make_float4(0, 0, 0, 0);
-            const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
-            const uint32_t l0 = pack_bf16x2(v.x - bf16_lo(h0), v.y - bf16_hi(h0)), l1 = pack_bf16x2(v.z - bf16_lo(h1), v.w - bf16_hi(h1));
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint32_t wa[4] = {w[2 * t].x, w[2 * t + 1].x, w[2 * t].y, w[2 * t + 1].y};
-                mma_16816(acc[t], wa, h0, h1);
-                mma_16816(acc[t], wa, l0, l1);
+                for (int r = 0; r < 4; ++r)
+                    w[i][r] = in && n0 + row + r * 8 < p.N ? *reinterpret_cast<const uint2 *>(b[i] + r * 8 * side.ldb + j) : make_uint2(0, 0);
+            uint32_t h[2][2], l[2][2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const float4 v = in && used[g] ? *reinterpret_cast<const float4 *>(q + g * second + j) : make_float4(0, 0, 0, 0);
+                h[g][0] = pack_bf16x2(v.x, v.y);
+                h[g][1] = pack_bf16x2(v.z, v.w);
+                l[g][0] = pack_bf16x2(v.x - bf16_lo(h[g][0]), v.y - bf16_hi(h[g][0]));
+                l[g][1] = pack_bf16x2(v.z - bf16_lo(h[g][1]), v.w - bf16_hi(h[g][1]));
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t wa[4] = {w[i][2 * t].x, w[i][2 * t + 1].x, w[i][2 * t].y, w[i][2 * t + 1].y};
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        mma_16816(acc[i][g][t], wa, h[g][0], h[g][1]);
+                        mma_16816(acc[i][g][t], wa, l[g][0], l[g][1]);
+                    }
+                }
         }
-        // this lane's two tokens: quad * 2 and the next; a token's four lanes vote alike
-        const bool t0 = match >> (quad * 8) & 1u, t1 = match >> (quad * 8 + 4) & 1u;
+        // this lane's tokens of a half: quad * 2 and the next
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const bool t0 = match[i] >> (g * 8 + quad * 2) & 1u, t1 = match[i] >> (g * 8 + quad * 2 + 1) & 1u;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    sum[g][t][0] = t0 ? acc[i][g][t][0] : sum[g][t][0];
+                    sum[g][t][1] = t1 ? acc[i][g][t][1] : sum[g][t][1];
+                    sum[g][t][2] = t0 ? acc[i][g][t][2] : sum[g][t][2];
+                    sum[g][t][3] = t1 ? acc[i][g][t][3] : sum[g][t][3];
+                }
+            }
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        __syncwarp();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            sum[t][0] = t0 ? acc[t][0] : sum[t][0];
-            sum[t][1] = t1 ? acc[t][1] : sum[t][1];
-            sum[t][2] = t0 ? acc[t][2] : sum[t][2];
-            sum[t][3] = t1 ? acc[t][3] : sum[t][3];
+            float *o = term + quad * 2 * kTermPitch + t * 16 + row;
+            o[0] = sum[g][t][0];
+            o[kTermPitch] = sum[g][t][1];
+            o[8] = sum[g][t][2];
+            o[kTermPitch + 8] = sum[g][t][3];
         }
+        __syncwarp();
+        tile(g);
     }
-    __syncwarp();
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        float *o = term + quad * 2 * kTermPitch + t * 16 + row;
-        o[0] = sum[t][0];
-        o[kTermPitch] = sum[t][1];
-        o[8] = sum[t][2];
-        o[kTermPitch + 8] = sum[t][3];
-    }
-    __syncwarp();
-    return true;
 }
 
 // The exchange between the two warps of an output's g and u (as pair_tall.cuh), then the
@@ -122,7 +199,7 @@ constexpr uint32_t kLoraSmem = kPairHeader + kPairStages * kPairStage + kLoraExt
 static_assert(kLoraSmem <= 227 * 1024, "shared memory");
 
 template <int SIDES>
-__global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPairParams p, const __grid_constant__ PairMaps maps)
+__global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPairParams p, const __grid_constant__ LoraMaps maps)
 {
     extern __shared__ unsigned char pair_raw[];
     const PairShared s = pair_shared(pair_raw);
@@ -130,6 +207,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
     const int rank = static_cast<int>(cluster_ctarank());
     const uint32_t tmem = pair_setup(s, warp);
     const LoraPlan &plan = p.plan;
+    const int R = p.l.R, width = SIDES * R;
     bool ok = true;
     const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
     if (!p.early) grid_dependency_wait();
@@ -153,9 +231,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 const uint32_t bar = full0 + static_cast<uint32_t>(st) * 8u;
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
-                    pair_load_2d(d, &maps.a[0], c * 64, n0, bar);
-                    if (SIDES == 2) pair_load_2d(d + kPairOperand / 2, &maps.a[1], c * 64, n0, bar);
-                    pair_load_2d(d + kPairOperand, &maps.b[0], c * 64, m0, bar);
+                    pair_load_2d(d, &maps.w[0], c * 64, n0, bar);
+                    if (SIDES == 2) pair_load_2d(d + kPairOperand / 2, &maps.w[1], c * 64, n0, bar);
+                    pair_load_2d(d + kPairOperand, &maps.x, c * 64, m0, bar);
                 }
                 __syncwarp();
                 filled += filled < kPairStages;
@@ -163,6 +241,34 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                     st = 0;
                     phase ^= 1;
                 }
+            }
+            if (!p.l.blocks || x.slot >= 0 || !ok) continue;
+            if (p.early) grid_dependency_wait();   // p and the table
+            for (LoraRuns run(p.l, x.t % plan.ttiles * plan.tn, plan.tn); ok && run.next();) {
+                const int blocks = run.at - run.first;
+                const int row = x.t % plan.ttiles * plan.tn + run.first * kLoraBlock + rank * blocks * 16;   // each CTA brings half of the run
+                for (int c = 0; c < width && ok; c += 64)
+                    for (int term = 0; term < 2; ++term) {
+                        if (!pair_wait(&s.empty[st], phase, kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        unsigned char *d = s.stages + st * kPairStage;
+                        const uint32_t bar = full0 + static_cast<uint32_t>(st) * 8u;
+                        if (elect_one()) {
+                            if (rank == 0)
+                                mbar_arrive_expect_tx(&s.full[st], static_cast<uint32_t>(plan.wt) * (SIDES == 2 ? 256u : 128u) + static_cast<uint32_t>(blocks) * 4096u);
+                            pair_load_3d(d, &maps.b[0], c, n0, run.adapter, bar);
+                            if (SIDES == 2) pair_load_3d(d + kPairOperand / 2, &maps.b[1], c - R, n0, run.adapter, bar);
+                            for (int b = 0; b < blocks; ++b) pair_load_2d(d + kPairOperand + b * 2048, &maps.p[term], c, row + b * 16, bar);
+                        }
+                        __syncwarp();
+                        filled += filled < kPairStages;
+                        if (++st == kPairStages) {
+                            st = 0;
+                            phase ^= 1;
+                        }
+                    }
             }
         }
         for (int i = 0; i < filled; ++i) {   // as pair_produce: the last round's stages, oldest first
@@ -190,7 +296,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) pair_mma_bf16(tmem + buf * kPairTile, a + 2 * kk, b + 2 * kk, idesc, kk > 0 || c > x.c0);
                         pair_commit(&s.empty[st]);
-                        if (c == x.c1 - 1) pair_commit(&s.acc_full[buf]);
                     }
                     __syncwarp();
                     if (++st == kPairStages) {
@@ -198,6 +303,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                         phase ^= 1;
                     }
                 }
+                if (p.l.blocks && x.slot < 0 && ok) {
+                    if (p.early) grid_dependency_wait();
+                    for (LoraRuns run(p.l, x.t % plan.ttiles * plan.tn, plan.tn); ok && run.next();) {
+                        const int cols = (run.at - run.first) * kLoraBlock;
+                        const uint32_t run_idesc = tc_idesc_bf16(256, 256) - (static_cast<uint32_t>((256 - cols) >> 3) << 17);
+                        const uint32_t d = tmem + buf * kPairTile + static_cast<uint32_t>(run.first * kLoraBlock);
+                        for (int c = 0; c < width && ok; c += 64) {
+                            const int steps = min(4, (width - c + 15) / 16);
+                            for (int term = 0; term < 2; ++term) {
+                                if (!pair_wait(&s.full[st], phase, kWaitLimitNs)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                const uint64_t a = a0 + static_cast<uint32_t>(st) * (kPairStage >> 4), b = b0 + static_cast<uint32_t>(st) * (kPairStage >> 4);
+                                if (elect_one()) {
+                                    for (int kk = 0; kk < steps; ++kk) pair_mma_bf16(d, a + 2 * kk, b + 2 * kk, run_idesc, true);
+                                    pair_commit(&s.empty[st]);
+                                }
+                                __syncwarp();
+                                if (++st == kPairStages) {
+                                    st = 0;
+                                    phase ^= 1;
+                                }
+                            }
+                        }
+                    }
+                }
+                if (elect_one() && ok) pair_commit(&s.acc_full[buf]);
+                __syncwarp();
                 buf ^= 1;
                 if (buf == 0) acc_phase ^= 1;
             }
@@ -241,12 +376,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 float y[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(r[k]);
+                if (p.l.blocks && tokens > 0 && __ldcg(p.l.blocks + (m0 + j) / kLoraBlock) == kMixed)
+                    lora_term(p.l, d, SIDES, static_cast<int64_t>(m0) + j, n0, term, [&](int g) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    if (g * 8 < tokens && p.l.adapters > 0 && lora_term(p.l, d, SIDES, static_cast<int64_t>(m0) + j + g * 8, n0, term)) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[g * 8 + k] += term[k * kTermPitch + lane];
-                    }
+                        for (int k = 0; k < 16; ++k)
+                            if (k >> 3 == g) y[k] += term[(k & 7) * kTermPitch + lane];
+                    });
                 if constexpr (SIDES == 2) {
                     // two sets in turn, as in pair_tall_kernel
                     float *mine = swap + (sets & 1) * 512 + d * 256, *theirs = swap + (sets & 1) * 512 + (d ^ 1) * 256;
@@ -280,64 +415,74 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
 }
 
 // The tiles in ranges: their partial sums in order, the adapters' term and the epilogue.  A
-// warp takes 32 outputs and four tokens.
-template <int SIDES>
+// warp takes 32 outputs and TOKENS tokens, whose rows of B are on the way together.
+template <int SIDES, int TOKENS>
 __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
 {
+    const LoraPlan &plan = p.plan;
+    const int lane = threadIdx.x & 31, R = p.l.R;
+    const int groups = plan.tn / TOKENS, blocks = (plan.wt + 31) / 32;   // of a tile
+    const int64_t total = static_cast<int64_t>(plan.rest) * blocks * groups;
     grid_dependency_wait();
     grid_launch_dependents();
-    const LoraPlan &plan = p.plan;
-    const int lane = threadIdx.x & 31;
-    const int groups = plan.tn / 4, blocks = (plan.wt + 31) / 32;   // of a tile
-    const int64_t total = static_cast<int64_t>(plan.rest) * blocks * groups;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < total; i += static_cast<int64_t>(gridDim.x) * 8) {
-        const int tile = static_cast<int>(i / (blocks * groups)), rest = static_cast<int>(i % (blocks * groups));
-        const int t = plan.whole + tile, j0 = rest % groups * 4, w = rest / groups * 32 + lane;
+        // tiles' first tokens first: those behind the last row cost nothing
+        const int group = static_cast<int>(i / (plan.rest * blocks)), other = static_cast<int>(i % (plan.rest * blocks));
+        const int tile = other / blocks, j0 = group * TOKENS, w = other % blocks * 32 + lane;
+        const int t = plan.whole + tile;
         const int n = t / plan.ttiles * plan.wt + w;
         const int64_t m0 = static_cast<int64_t>(t % plan.ttiles) * plan.tn + j0;
-        const int tokens = static_cast<int>(min(static_cast<int64_t>(4), p.l.M - m0));
-        if (tokens <= 0 || w >= plan.wt || n >= p.l.N) continue;
+        if (m0 >= p.l.M || w >= plan.wt || n >= p.l.N) continue;
+        int a[TOKENS];
+#pragma unroll
+        for (int k = 0; k < TOKENS; ++k) a[k] = lora_adapter(p.l, m0 + k);
         // output w of the tile: a CTA holds wt / 2 of them, in dual tiles from lanes 0 and 64 on
         const int rank = w >= plan.wt / 2 ? 1 : 0, at = rank * 128 + w - rank * (plan.wt / 2);
-        float acc[4][SIDES] = {};
-        for (int s = 0; s < plan.splits; ++s) {
-            const float *q = p.part + ((static_cast<int64_t>(s) * plan.rest + tile) * plan.tn + j0) * 256 + at;
+        float acc[TOKENS][SIDES] = {}, term[TOKENS][SIDES] = {};
+        const float *q = p.part + (static_cast<int64_t>(tile) * plan.tn + j0) * 256 + at;
+#pragma unroll 2
+        for (int s = 0; s < plan.splits; ++s, q += static_cast<int64_t>(plan.rest) * plan.tn * 256)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < tokens) {
+            for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
-                    for (int d = 0; d < SIDES; ++d) acc[k][d] += __ldcg(q + k * 256 + d * 64);
-                }
-        }
+                for (int d = 0; d < SIDES; ++d) acc[k][d] += m0 + k < p.l.M ? __ldcg(q + k * 256 + d * 64) : 0.0f;
+        for (int j = 0; j < R; j += 8) {
+            uint2 b[TOKENS][SIDES][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k >= tokens) break;
-            const int64_t m = m0 + k;
-            const int a = lora_adapter(p.l, m);
-            if (a >= 0) {
+            for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
                 for (int d = 0; d < SIDES; ++d) {
                     const LoraSide &side = p.l.side[d];
-                    const uint16_t *b = side.b + a * side.b_adapter + n * side.ldb;
-                    const float *v = p.l.p + m * SIDES * p.l.R + d * p.l.R;
-                    float sum = 0.0f;
-#pragma unroll 4
-                    for (int j = 0; j < p.l.R; j += 4) {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(b + j);
-                        const float4 y = *reinterpret_cast<const float4 *>(v + j);
-                        sum = fmaf(bf16_lo(x.x), y.x, sum);
-                        sum = fmaf(bf16_hi(x.x), y.y, sum);
-                        sum = fmaf(bf16_lo(x.y), y.z, sum);
-                        sum = fmaf(bf16_hi(x.y), y.w, sum);
+                    const uint16_t *r = side.b + a[k] * side.b_adapter + n * side.ldb + j;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) b[k][d][h] = a[k] >= 0 ? *reinterpret_cast<const uint2 *>(r + 4 * h) : make_uint2(0, 0);
+                }
+#pragma unroll
+            for (int k = 0; k < TOKENS; ++k) {
+                if (a[k] < 0) continue;   // the whole warp
+#pragma unroll
+                for (int d = 0; d < SIDES; ++d) {
+                    const float *v = p.l.p + (m0 + k) * SIDES * R + d * R + j;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 y = *reinterpret_cast<const float4 *>(v + 4 * h);
+                        term[k][d] = fmaf(bf16_lo(b[k][d][h].x), y.x, term[k][d]);
+                        term[k][d] = fmaf(bf16_hi(b[k][d][h].x), y.y, term[k][d]);
+                        term[k][d] = fmaf(bf16_lo(b[k][d][h].y), y.z, term[k][d]);
+                        term[k][d] = fmaf(bf16_hi(b[k][d][h].y), y.w, term[k][d]);
                     }
-                    acc[k][d] += sum;
                 }
             }
-            uint16_t *o = p.l.out + m * p.l.ldo + n;
+        }
+#pragma unroll
+        for (int k = 0; k < TOKENS; ++k) {
+            if (m0 + k >= p.l.M) break;
+            uint16_t *o = p.l.out + (m0 + k) * p.l.ldo + n;
+            const float g = acc[k][0] + term[k][0], u = acc[k][SIDES - 1] + term[k][SIDES - 1];
             if constexpr (SIDES == 2)
-                *o = p.l.mode == 0 ? f32_to_bf16(silu_short(acc[k][0]) * acc[k][SIDES - 1]) : static_cast<uint16_t>(glu_hf_short(acc[k][0], acc[k][SIDES - 1]));
+                *o = p.l.mode == 0 ? f32_to_bf16(silu_short(g) * u) : static_cast<uint16_t>(glu_hf_short(g, u));
             else
-                *o = f32_to_bf16(acc[k][0]);
+                *o = f32_to_bf16(g);
         }
     }
 }

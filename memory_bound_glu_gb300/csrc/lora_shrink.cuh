@@ -1,16 +1,21 @@
 // lora_shrink.cuh -- the first half of the adapters' term: p[m, j] = scale[a] sum_k x[m, k]
 // A[a][j, k] with a = adapter[m], on the tensor cores of single warps (mma.sync).
 //
-// A block takes 16 MT rows and 8 NT of the rank's columns; its eight warps split the inner
-// dimension and add up in shared memory, in order.  For each adapter that occurs among the
-// rows it runs the product of all of them with that adapter's A and writes the rows that
-// use it: a product of an adapter's 8 columns with one row costs as much as with sixteen,
-// and rows of a decode batch mostly have an adapter of their own (few rows: a block per
-// adapter, so that they run side by side).  Which k sits in which place of a fragment is
-// free as long as both operands agree, so a lane reads 16 consecutive bytes of a row,
-// enough for two steps of 16.
+// A block takes 16 MT rows and 8 NT of the rank's columns; the warps of its cluster split
+// the inner dimension and add up in shared memory, in order.  For each adapter that occurs
+// among the rows it runs the product of all of them with that adapter's A and writes the
+// rows that use it: a product of an adapter's 8 columns with one row costs as much as with
+// sixteen, and rows of a decode batch mostly have an adapter of their own (few rows: a
+// cluster per adapter, so that they run side by side).  Which k sits in which place of a
+// fragment is free as long as both operands agree, so a lane reads 16 consecutive bytes of
+// a row, enough for two steps of 16.
+//
+// p is written in fp32, and as two bf16 terms (off by 2^-18) for the tensor cores.  Beside
+// it a table with a number for 32 rows each: their adapter where all of them have the same,
+// kNoAdapter, or kMixed.
 #pragma once
 #include "lora_generic.cuh"
+#include "tcgen05.cuh"
 
 namespace mbglu {
 
@@ -22,31 +27,50 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 }
 
 constexpr int kShrinkWarps = 8;
+constexpr int kLoraBlock = 32;                    // rows per entry of the table
+constexpr int kNoAdapter = -1, kMixed = -2;
+
+// the warps' sums, then the block's
 template <int MT, int NT>
 constexpr uint32_t shrink_smem()
 {
-    return kShrinkWarps * MT * 16 * (NT * 8 + 4) * 4;
+    return (kShrinkWarps + 1) * MT * 16 * (NT * 8 + 4) * 4;
 }
 
-// blockIdx: (column tiles of all sides, row groups, adapters side by side)
-template <int SIDES, int MT, int NT>
-__global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const LoraParams p)
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// blockIdx: (column tiles of all sides x the cluster's blocks, row groups, adapters side by side)
+template <int SIDES, int MT, int NT, int UNROLL>
+__global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const LoraParams p, const int split)
 {
     extern __shared__ float shrink_part[];
     constexpr int kRows = MT * 16, kCols = NT * 8, kPitch = kCols + 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
+    const int rank = split > 1 ? static_cast<int>(blockIdx.x) % split : 0, col = static_cast<int>(blockIdx.x) / split;
+    const int tiles = (p.R + kCols - 1) / kCols, which = SIDES == 2 && col >= tiles ? 1 : 0;
+    const LoraSide &side = p.side[which];
+    const int j0 = (col - which * tiles) * kCols, width = SIDES * p.R;
+    const int steps = (p.K + 31) / 32, warps = kShrinkWarps * split, w0 = rank * kShrinkWarps + warp;
+    const int s0 = steps * w0 / warps, s1 = steps * (w0 + 1) / warps;
+    float *total = shrink_part + kShrinkWarps * kRows * kPitch;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
-    const int tiles = (p.R + kCols - 1) / kCols;
-    const LoraSide &side = p.side[SIDES == 2 && static_cast<int>(blockIdx.x) >= tiles];
-    const int which = SIDES == 2 && static_cast<int>(blockIdx.x) >= tiles ? 1 : 0;
-    const int j0 = (static_cast<int>(blockIdx.x) - which * tiles) * kCols;
-    const int steps = (p.K + 31) / 32;
-    const int s0 = steps * warp / kShrinkWarps, s1 = steps * (warp + 1) / kShrinkWarps;
     for (int64_t group = blockIdx.y; group * kRows < p.M; group += gridDim.y) {
         const int64_t m0 = group * kRows;
         const int mine = lane < kRows ? lora_adapter(p, m0 + lane) : -1;   // kRows <= 32
         uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
+        if (p.blocks && blockIdx.x == 0 && blockIdx.z == 0 && warp == 0) {
+            // rows behind the last agree with any; groups of 16 rows: the caller's M <= 16
+            const uint32_t in = __ballot_sync(0xffffffffu, lane < kRows && m0 + lane < p.M);
+            const int a = __shfl_sync(0xffffffffu, mine, 0);
+            const uint32_t same = __ballot_sync(0xffffffffu, mine == a);
+            if (lane == 0) p.blocks[m0 / kLoraBlock] = (in & ~same) ? kMixed : a;
+        }
         for (uint32_t nth = 0; left; ++nth) {
             const int a = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
             const uint32_t rows = __ballot_sync(0xffffffffu, mine == a);
@@ -55,7 +79,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
             float acc[MT][NT][4] = {};
             const uint16_t *w = side.a + a * side.a_adapter + (j0 + row) * side.lda;
             const uint16_t *x = p.x + (m0 + row) * p.ldx;
-#pragma unroll 2
+#pragma unroll UNROLL
             for (int s = s0; s < s1; ++s) {
                 const int k = s * 32 + quad * 8;
                 uint4 xa[MT][2], wb[NT];
@@ -81,8 +105,9 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
                     }
                 }
             }
+            // the block's warps, then the cluster's blocks.  What is written here was read
+            // for the last adapter before the barriers below.
             float *part = shrink_part + warp * kRows * kPitch;
-            __syncthreads();   // the last adapter's sums have been read
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -94,15 +119,40 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
                     q[8 * kPitch + 1] = acc[i][n][3];
                 }
             __syncthreads();
-            const float scale = p.scale ? p.scale[a] : 1.0f;
+            const auto put = [&](int r, int j, float v) {
+                v *= p.scale ? p.scale[a] : 1.0f;
+                const int64_t at = (m0 + r) * width + which * p.R + j0 + j;
+                p.p[at] = v;
+                const uint16_t hi = f32_to_bf16(v);
+                p.terms[at] = hi;
+                p.terms[at + p.M * static_cast<int64_t>(width)] = f32_to_bf16(v - bf16_to_f32(hi));
+            };
             for (int e = threadIdx.x; e < kRows * kCols; e += kShrinkWarps * 32) {
                 const int r = e / kCols, j = e % kCols;
                 if (!(rows >> r & 1u) || j0 + j >= p.R) continue;
                 float v = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kShrinkWarps; ++i) v += shrink_part[(i * kRows + r) * kPitch + j];
-                p.p[(m0 + r) * SIDES * p.R + which * p.R + j0 + j] = v * scale;
+                if (split == 1)
+                    put(r, j, v);
+                else
+                    total[r * kPitch + j] = v;
             }
+            if (split == 1) {
+                __syncthreads();
+                continue;
+            }
+            __syncwarp();
+            cluster_sync();
+            for (int e = threadIdx.x * split + rank; e < kRows * kCols; e += kShrinkWarps * 32 * split) {
+                const int r = e / kCols, j = e % kCols;
+                if (!(rows >> r & 1u) || j0 + j >= p.R) continue;
+                float v = 0.0f;
+                for (int i = 0; i < split; ++i) v += ld_cluster_f32(map_to_rank(total + r * kPitch + j, static_cast<uint32_t>(i)));
+                put(r, j, v);
+            }
+            __syncwarp();
+            cluster_sync();
         }
     }
 }
