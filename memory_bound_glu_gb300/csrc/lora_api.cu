@@ -6,6 +6,7 @@
 #include "dense_launch.h"
 #include "lora_generic.cuh"
 #include "lora_pair.cuh"
+#include "lora_shrink_tc.cuh"
 #include "pair_plan.h"
 
 namespace {
@@ -62,6 +63,12 @@ int64_t lora_p_bytes(int sides, int M, int R) { return padded(static_cast<int64_
 
 int64_t lora_part_bytes(const mbglu::LoraPlan &q) { return static_cast<int64_t>(q.rest) * q.splits * q.tn * 1024; }
 
+// From this many rows on p comes from lora_shrink_tc_kernel.
+#ifndef SHRINK_TC_FROM
+#define SHRINK_TC_FROM 1024
+#endif
+constexpr int kShrinkTcFrom = SHRINK_TC_FROM, kShrinkTcSplit = 8;
+
 // Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, partial sums
 struct LoraSpace {
     int64_t terms, blocks, part, bytes;
@@ -73,7 +80,8 @@ LoraSpace lora_space(int sides, int M, int R, const mbglu::LoraPlan &plan)
     s.terms = lora_p_bytes(sides, M, R);
     s.blocks = s.terms + lora_p_bytes(sides, M, R);
     s.part = s.blocks + padded((static_cast<int64_t>(M) + mbglu::kLoraBlock - 1) / mbglu::kLoraBlock * 4);
-    s.bytes = s.part + padded(lora_part_bytes(plan));
+    // the partial sums of p and of the outputs, one after the other
+    s.bytes = s.part + padded(std::max(lora_part_bytes(plan), M >= kShrinkTcFrom ? kShrinkTcSplit * static_cast<int64_t>(M) * sides * R * 4 : 0));
     return s;
 }
 
@@ -101,13 +109,39 @@ mbglu_status launch_shrink(const mbglu::LoraParams &p, int side_by_side, int mos
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::lora_shrink_kernel<SIDES, MT, NT, UNROLL>, p, split));
 }
 
+// Blocks of a cluster split the inner dimension, so that the tiles of 128 rows fill the SMs.
+template <int SIDES>
+mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *taken, cudaStream_t stream)
+{
+    *taken = false;
+    mbglu::ShrinkTcMaps maps;
+    if (!encode_tile_map(&maps.x, p.x, p.ldx, p.M, p.K, 64, mbglu::kShrinkTcRows, 2)) return MBGLU_OK;
+    for (int d = 0; d < SIDES; ++d) {
+        const mbglu::LoraSide &s = p.side[d];
+        if ((p.adapters > 1 && s.a_adapter <= 0) || !encode_stack_map(&maps.a[d], s.a, s.a_adapter, s.lda, p.adapters, p.R, p.K, 64, p.R)) return MBGLU_OK;
+    }
+    const int tiles = ceil_div(p.M, mbglu::kShrinkTcRows);
+    if (tiles > 65535) return MBGLU_OK;
+    mbglu::ShrinkTcParams q = {};
+    q.l = p;
+    q.part = part;
+    q.nchunk = ceil_div(p.K, 64);
+    q.split = 1;
+    while (q.split < kShrinkTcSplit && tiles * q.split * 2 <= 160 && q.nchunk >= q.split * 8) q.split *= 2;
+    const uint32_t stage = mbglu::shrink_tc_stage(SIDES * p.R);
+    q.stages = std::min<int>(mbglu::kShrinkTcMaxStages, (200 * 1024) / static_cast<int>(stage));
+    *taken = true;
+    Launch l(dim3(static_cast<unsigned>(q.split), static_cast<unsigned>(tiles)), mbglu::kShrinkTcThreads, 2048 + static_cast<size_t>(q.stages) * stage, stream,
+             q.split);
+    return launched(cudaLaunchKernelEx(&l.cfg, mbglu::lora_shrink_tc_kernel<SIDES>, q, maps));
+}
+
 template <int SIDES>
 cudaError_t setup_pair()
 {
     cudaError_t e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(mbglu::lora_shrink_kernel<SIDES, 2, 8, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(mbglu::shrink_smem<2, 8>()));
+        e = cudaFuncSetAttribute(mbglu::lora_shrink_tc_kernel<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 204 * 1024);
     return e;
 }
 
@@ -177,19 +211,19 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         // few rows: a block per adapter of a group and 8 columns; many: columns together, so
         // that the rows are read once or twice
         p.early = launch_policy() != MBGLU_POLICY_SERIAL;
-        if (l.M <= kJoinRows)
-            st = launch_shrink<SIDES, 1, 1, 5>(p.l, std::min(l.M, 16), 1024, stream);
-        else if (l.R <= 16)
-            st = launch_shrink<SIDES, 2, 2, 2>(p.l, 1, 608, stream);
-        else if (l.R <= 32)
-            st = launch_shrink<SIDES, 2, 4, 1>(p.l, 1, 304, stream);
-        else
-            st = launch_shrink<SIDES, 2, 8, 1>(p.l, 1, 304, stream);
+        bool tc = false;
+        if (l.M >= kShrinkTcFrom) st = launch_shrink_tc<SIDES>(p.l, p.part, &tc, stream);
+        if (st == MBGLU_OK && !tc) {
+            if (l.M <= kJoinRows)
+                st = launch_shrink<SIDES, 1, 1, 5>(p.l, std::min(l.M, 16), 1024, stream);
+            else
+                st = launch_shrink<SIDES, 1, 4, 4>(p.l, l.M <= 1024 ? 8 : 2, 608, stream);
+        }
         if (st != MBGLU_OK) return st;
     }
     Launch c(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.items))), mbglu::kPairThreads, mbglu::kLoraSmem, stream, 2);
     st = launched(cudaLaunchKernelEx(&c.cfg, mbglu::lora_pair_kernel<SIDES>, p, maps));
-    if (st == MBGLU_OK && p.plan.rest > 0) st = l.M <= 16 ? launch_join<SIDES, 1>(p, stream) : launch_join<SIDES, 4>(p, stream);
+    if (st == MBGLU_OK && p.plan.rest > 0) st = l.M <= 16 ? launch_join<SIDES, 1>(p, stream) : launch_join<SIDES, 2>(p, stream);
     return st;
 }
 

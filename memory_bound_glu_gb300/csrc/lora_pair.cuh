@@ -337,6 +337,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 if (buf == 0) acc_phase ^= 1;
             }
         }
+    } else if (warp == 2 && p.l.adapters > 0 && plan.rest > 0) {
+        // the join reads B row by row and waits for each: its bytes come into L2 beside the
+        // weights, whose copies leave room for them
+        for (int i = max(first, plan.whole + (first - plan.whole % step + step) % step); i < plan.whole + plan.rest; i += step) {
+            const LoraTile x = lora_tile(plan, i);
+            const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2), rows = min(plan.wt / 2, p.l.N - n0);
+            for (int m = x.t % plan.ttiles * plan.tn + lane, k = lane; k < plan.tn && rows > 0; k += 32, m += 32) {
+                const int a = lora_adapter(p.l, m);
+                if (a < 0) continue;
+#pragma unroll
+                for (int d = 0; d < SIDES; ++d) {
+                    const LoraSide &side = p.l.side[d];
+                    if (side.ldb == R) bulk_prefetch_l2(side.b + a * side.b_adapter + n0 * side.ldb, static_cast<uint32_t>(rows * R * 2));
+                }
+            }
+        }
     } else if (warp >= kPairEpilogue) {
         // p, and what the join reads after this kernel, come from the kernel before
         if (p.early) grid_dependency_wait();
@@ -440,14 +456,14 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
         const int rank = w >= plan.wt / 2 ? 1 : 0, at = rank * 128 + w - rank * (plan.wt / 2);
         float acc[TOKENS][SIDES] = {}, term[TOKENS][SIDES] = {};
         const float *q = p.part + (static_cast<int64_t>(tile) * plan.tn + j0) * 256 + at;
-#pragma unroll 2
+#pragma unroll 4
         for (int s = 0; s < plan.splits; ++s, q += static_cast<int64_t>(plan.rest) * plan.tn * 256)
 #pragma unroll
             for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
                 for (int d = 0; d < SIDES; ++d) acc[k][d] += m0 + k < p.l.M ? __ldcg(q + k * 256 + d * 64) : 0.0f;
-        for (int j = 0; j < R; j += 8) {
-            uint2 b[TOKENS][SIDES][2];
+        for (int j = 0; j < R; j += 16) {
+            uint4 b[TOKENS][SIDES][2];
 #pragma unroll
             for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
@@ -455,7 +471,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
                     const LoraSide &side = p.l.side[d];
                     const uint16_t *r = side.b + a[k] * side.b_adapter + n * side.ldb + j;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) b[k][d][h] = a[k] >= 0 ? *reinterpret_cast<const uint2 *>(r + 4 * h) : make_uint2(0, 0);
+                    for (int h = 0; h < 2; ++h) b[k][d][h] = a[k] >= 0 && j + 8 * h < R ? *reinterpret_cast<const uint4 *>(r + 8 * h) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
             for (int k = 0; k < TOKENS; ++k) {
@@ -465,11 +481,18 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
                     const float *v = p.l.p + (m0 + k) * SIDES * R + d * R + j;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float4 y = *reinterpret_cast<const float4 *>(v + 4 * h);
-                        term[k][d] = fmaf(bf16_lo(b[k][d][h].x), y.x, term[k][d]);
-                        term[k][d] = fmaf(bf16_hi(b[k][d][h].x), y.y, term[k][d]);
-                        term[k][d] = fmaf(bf16_lo(b[k][d][h].y), y.z, term[k][d]);
-                        term[k][d] = fmaf(bf16_hi(b[k][d][h].y), y.w, term[k][d]);
+                        if (j + 8 * h >= R) continue;
+                        const float4 y = *reinterpret_cast<const float4 *>(v + 8 * h), z = *reinterpret_cast<const float4 *>(v + 8 * h + 4);
+                        const uint4 x = b[k][d][h];
+                        float t = term[k][d];
+                        t = fmaf(bf16_lo(x.x), y.x, t);
+                        t = fmaf(bf16_hi(x.x), y.y, t);
+                        t = fmaf(bf16_lo(x.y), y.z, t);
+                        t = fmaf(bf16_hi(x.y), y.w, t);
+                        t = fmaf(bf16_lo(x.z), z.x, t);
+                        t = fmaf(bf16_hi(x.z), z.y, t);
+                        t = fmaf(bf16_lo(x.w), z.z, t);
+                        term[k][d] = fmaf(bf16_hi(x.w), z.w, t);
                     }
                 }
             }

@@ -64,11 +64,11 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
         const int64_t m0 = group * kRows;
         const int mine = lane < kRows ? lora_adapter(p, m0 + lane) : -1;   // kRows <= 32
         uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
-        if (p.blocks && blockIdx.x == 0 && blockIdx.z == 0 && warp == 0) {
-            // rows behind the last agree with any; groups of 16 rows: the caller's M <= 16
-            const uint32_t in = __ballot_sync(0xffffffffu, lane < kRows && m0 + lane < p.M);
-            const int a = __shfl_sync(0xffffffffu, mine, 0);
-            const uint32_t same = __ballot_sync(0xffffffffu, mine == a);
+        if (p.blocks && m0 % kLoraBlock == 0 && blockIdx.x == 0 && blockIdx.z == 0 && warp == 0) {
+            // rows behind the last agree with any
+            const uint32_t in = __ballot_sync(0xffffffffu, m0 + lane < p.M);
+            const int its = lora_adapter(p, m0 + lane), a = __shfl_sync(0xffffffffu, its, 0);
+            const uint32_t same = __ballot_sync(0xffffffffu, its == a);
             if (lane == 0) p.blocks[m0 / kLoraBlock] = (in & ~same) ? kMixed : a;
         }
         for (uint32_t nth = 0; left; ++nth) {

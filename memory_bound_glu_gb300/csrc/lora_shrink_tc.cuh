@@ -1,0 +1,246 @@
+// lora_shrink_tc.cuh -- p = scale[a] x A[a]^T for many rows, on tcgen05.
+//
+// A cluster takes 128 rows, its blocks a range of the inner dimension each.  The rows are
+// the MMA's M side; the columns are the adapter's A, both projections' one behind the other
+// (up to 256).  For each adapter among the rows the block runs its range's product of all
+// rows and keeps of it the rows that use the adapter, as a partial sum in global memory
+// (which stays in L2); a row has one adapter, so no row is written twice, and one cluster
+// barrier at the end lets the blocks add up 128 / split rows each, in order.
+//
+// What bounds it is x's way in: 4096 x 2560 are 21 MB.  Rows of one request lie together, so
+// mostly there is one adapter, or two; a chunk of many short requests takes
+// lora_shrink_kernel.
+#pragma once
+#include "lora_shrink.cuh"
+#include "tc_pair.cuh"
+
+namespace mbglu {
+
+constexpr int kShrinkTcThreads = 192;
+constexpr int kShrinkTcRows = 128;
+constexpr uint32_t kShrinkTcX = kShrinkTcRows * 128;      // a chunk of 64 columns of x
+constexpr int kShrinkTcMaxStages = 8;
+
+struct ShrinkTcMaps {
+    TensorMap x;             // [M][K], boxes of 64 x 128
+    TensorMap a[2];          // [adapters][R][K], 64 x R
+};
+
+struct ShrinkTcParams {
+    LoraParams l;
+    float *part;             // [split][M][sides R]
+    int split, stages, nchunk;
+};
+
+__host__ __device__ constexpr uint32_t shrink_tc_stage(int width) { return kShrinkTcX + static_cast<uint32_t>((width + 15) / 16 * 16) * 128u; }
+
+// The adapters among 128 rows, each once; a warp walks them.
+struct LoraDistinct {
+    int id[4];
+    uint32_t left[4];
+    __device__ LoraDistinct(const LoraParams &p, int64_t m0)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            id[i] = lora_adapter(p, m0 + i * 32 + (threadIdx.x & 31));
+            left[i] = __ballot_sync(0xffffffffu, id[i] >= 0);
+        }
+    }
+    __device__ bool next(int &a)
+    {
+        a = -1;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const int v = __shfl_sync(0xffffffffu, id[i], left[i] ? __ffs(left[i]) - 1 : 0);
+            if (left[i]) a = v;
+        }
+        if (a < 0) return false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) left[i] &= ~__ballot_sync(0xffffffffu, id[i] == a);
+        return true;
+    }
+};
+
+// grid: (split, tiles of 128 rows), clusters of split
+template <int SIDES>
+__global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(const ShrinkTcParams p, const __grid_constant__ ShrinkTcMaps maps)
+{
+    extern __shared__ unsigned char shrink_raw[];
+    unsigned char *base = shrink_raw + ((1024u - (smem_addr(shrink_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(base), *empty = full + kShrinkTcMaxStages;
+    uint64_t *acc_full = empty + kShrinkTcMaxStages, *acc_empty = acc_full + 2, *done = acc_empty + 2;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(done + 1);
+    unsigned char *ring = base + 1024;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int R = p.l.R, width = SIDES * R, rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const uint32_t stage = shrink_tc_stage(width);
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kShrinkTcRows;
+    const int c0 = static_cast<int>(static_cast<int64_t>(p.nchunk) * rank / p.split), c1 = static_cast<int>(static_cast<int64_t>(p.nchunk) * (rank + 1) / p.split);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    bool ok = true;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    if (warp == 0) {
+        LoraDistinct adapters(p.l, m0);
+        int st = 0, issued = 0, a;
+        uint32_t phase = 1;
+        while (ok && adapters.next(a)) {
+            for (int c = c0; c < c1; ++c) {
+                if (!pair_wait(&empty[st], phase, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    unsigned char *d = ring + st * stage;
+                    mbar_arrive_expect_tx(&full[st], kShrinkTcX + static_cast<uint32_t>(width) * 128u);
+                    const uint64_t policy = l2_policy_evict_last();   // the shared product reads x again
+                    tma_load_2d(d, &maps.x, c * 64, static_cast<int>(m0), &full[st], policy);
+#pragma unroll
+                    for (int i = 0; i < SIDES; ++i) tma_load_3d(d + kShrinkTcX + i * R * 128, &maps.a[i], c * 64, 0, a, &full[st], policy);
+                }
+                __syncwarp();
+                issued += issued < p.stages;
+                if (++st == p.stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        for (int i = 0; i < issued; ++i) {   // no copy may be in flight when the block leaves
+            int at = st - issued + i;
+            const uint32_t ph = at < 0 ? phase : phase ^ 1;
+            if (at < 0) at += p.stages;
+            if (!pair_wait(&full[at], ph, kWaitLimitNs)) ok = false;
+        }
+    } else if (warp == 1) {
+        LoraDistinct adapters(p.l, m0);
+        const uint32_t idesc = tc_idesc_bf16(kShrinkTcRows, (width + 15) / 16 * 16);
+        int st = 0, a;
+        uint32_t phase = 0, buf = 0, acc_phase = 1;
+        while (ok && adapters.next(a)) {
+            if (!pair_wait(&acc_empty[buf], acc_phase, kWaitLimitNs)) {
+                ok = false;
+                break;
+            }
+            for (int c = c0; c < c1; ++c) {
+                if (!pair_wait(&full[st], phase, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t x = smem_desc_sw128(ring + st * stage), w = smem_desc_sw128(ring + st * stage + kShrinkTcX);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(tmem + buf * 256u, x + 2 * kk, w + 2 * kk, idesc, c > c0 || kk > 0);
+                    tc_commit(&empty[st]);
+                }
+                __syncwarp();
+                if (++st == p.stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+            if (elect_one() && ok) tc_commit(&acc_full[buf]);
+            __syncwarp();
+            buf ^= 1;
+            if (buf == 0) acc_phase ^= 1;
+        }
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+        if (!pair_wait(done, 0, kWaitLimitNs)) ok = false;
+    } else {
+        LoraDistinct adapters(p.l, m0);
+        const int q = warp & 3, row = q * 32 + lane;
+        const int mine = lora_adapter(p.l, m0 + row);
+        if (p.l.blocks && rank == 0) {   // the table: a warp has 32 rows
+            const uint32_t in = __ballot_sync(0xffffffffu, m0 + row < p.l.M);
+            const int first = __shfl_sync(0xffffffffu, mine, 0);
+            const uint32_t same = __ballot_sync(0xffffffffu, mine == first);
+            if (lane == 0 && in) p.l.blocks[m0 / kLoraBlock + q] = (in & ~same) ? kMixed : first;
+        }
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        float *dst = p.part + (static_cast<int64_t>(rank) * p.l.M + m0 + row) * width;
+        uint32_t buf = 0, acc_phase = 0;
+        int a;
+        while (ok && adapters.next(a)) {
+            if (!__all_sync(0xffffffffu, pair_wait(&acc_full[buf], acc_phase, kWaitLimitNs))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, mine == a))
+                for (int c = 0; c < width; c += 16) {
+                    float v[16];
+                    __syncwarp();
+                    tmem_ld16(lanes + buf * 256u + static_cast<uint32_t>(c), v);
+                    if (mine == a) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (c + 4 * i < width) __stcg(reinterpret_cast<float4 *>(dst + c + 4 * i), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                    }
+                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            buf ^= 1;
+            if (buf == 0) acc_phase ^= 1;
+        }
+    }
+    if (!ok) atomicExch(&g_dense_error, kErrTimeout);
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    if (p.split > 1) cluster_sync();   // the partial sums are there
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    // this block's rows of the tile; a thread has four columns at a time
+    const int rows = kShrinkTcRows / p.split, quads = width / 4;
+    for (int e = threadIdx.x; e < rows * quads; e += kShrinkTcThreads) {
+        const int64_t m = m0 + rank * rows + e / quads;
+        const int j = e % quads * 4, a = lora_adapter(p.l, m);
+        if (a < 0) continue;
+        float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int i = 0; i < p.split; ++i) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part + (static_cast<int64_t>(i) * p.l.M + m) * width + j));
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+        }
+        const float s = p.l.scale ? p.l.scale[a] : 1.0f;
+        v = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
+        const int64_t at = m * width + j;
+        *reinterpret_cast<float4 *>(p.l.p + at) = v;
+        const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
+        *reinterpret_cast<uint2 *>(p.l.terms + at) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2 *>(p.l.terms + at + p.l.M * static_cast<int64_t>(width)) =
+            make_uint2(pack_bf16x2(v.x - bf16_lo(h0), v.y - bf16_hi(h0)), pack_bf16x2(v.z - bf16_lo(h1), v.w - bf16_hi(h1)));
+    }
+}
+
+}  // namespace mbglu

@@ -89,16 +89,6 @@ __host__ __device__ constexpr int moe_stages(int pad)
 }
 __host__ __device__ constexpr uint32_t moe_smem(int pad) { return kMoeHeader + 1024 + static_cast<uint32_t>(moe_stages(pad)) * moe_stage_bytes(pad); }
 
-// A 64-column box of a stack of matrices.
-__device__ __forceinline__ void tma_load_3d(void *dst, const TensorMap *map, int x, int y, int z, uint64_t *bar, uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
-        : "memory");
-}
-
 // Orders this thread's plain accesses to any memory against asynchronous copies'.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
