@@ -16,9 +16,9 @@ using namespace mbglu_host;
 constexpr int64_t kAlign = 256;
 int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
-// From two rows up to this many the adapters' term is left to the join, where every (row,
-// output) has a lane of its own: rows of a decode batch mostly have an adapter each.
-constexpr int kJoinRows = 64;
+// Up to this many rows the rows of a block with several adapters are taken to have one each,
+// as those of a decode batch mostly do.
+constexpr int kFewRows = 64;
 
 // Tiles and ranges, from the sizes alone.  The estimate (ns) of a tile's time is
 // tall_tokens' (gemm_api.cu); a join costs its launch and the partial sums' way to L2 and
@@ -33,12 +33,11 @@ mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, bool may_split)
         const int64_t tiles = static_cast<int64_t>(nt) * ceil_div(M, tn);
         if (tiles > INT32_MAX / 16) continue;
         const auto tile_ns = [&](int64_t at_once, int64_t n) { return n * (77.0 + 59.0 * std::min<int64_t>(at_once, kPairs) / kPairs + 0.7 * tn) + 15.5 * tn; };
-        const bool join = may_split && M >= 2 && M <= kJoinRows;
         for (int split = 0; split < 2; ++split) {
-            const int64_t left = join ? tiles : tiles % kPairs;
+            const int64_t left = tiles % kPairs;
             const int64_t s = split && left > 0 ? std::min<int64_t>({std::max<int64_t>(kPairs / left, 1), std::max(chunks / 8, 1), 16}) : 1;
             if (split && !may_split) continue;
-            if (join ? !split : split && s < 2) continue;
+            if (split && s < 2) continue;
             const int64_t whole = split ? tiles - left : tiles;
             double ns = (whole + kPairs - 1) / kPairs * tile_ns(whole, chunks);
             if (split) ns += (left * s + kPairs - 1) / kPairs * tile_ns(left * s, (chunks + s - 1) / s) + 3000 + left * s * tn * 2048.0 / 4000;
@@ -64,10 +63,7 @@ int64_t lora_p_bytes(int sides, int M, int R) { return padded(static_cast<int64_
 int64_t lora_part_bytes(const mbglu::LoraPlan &q) { return static_cast<int64_t>(q.rest) * q.splits * q.tn * 1024; }
 
 // From this many rows on p comes from lora_shrink_tc_kernel.
-#ifndef SHRINK_TC_FROM
-#define SHRINK_TC_FROM 1024
-#endif
-constexpr int kShrinkTcFrom = SHRINK_TC_FROM, kShrinkTcSplit = 8;
+constexpr int kShrinkTcFrom = 1024, kShrinkTcSplit = 8;
 
 // Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, partial sums
 struct LoraSpace {
@@ -139,7 +135,9 @@ mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *tak
 template <int SIDES>
 cudaError_t setup_pair()
 {
-    cudaError_t e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
+    cudaError_t e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mbglu::lora_shrink_tc_kernel<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 204 * 1024);
     return e;
@@ -190,6 +188,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         p.l.p = reinterpret_cast<float *>(ws);
         p.l.terms = reinterpret_cast<uint16_t *>(ws + space.terms);
         p.part = reinterpret_cast<float *>(ws + space.part);
+        p.prefetch = l.M <= kFewRows;
         if (whole) {   // tiles in ranges leave the adapters' term to the join
             p.l.blocks = reinterpret_cast<int32_t *>(ws + space.blocks);
             for (int d = 0; d < SIDES; ++d) {
@@ -214,7 +213,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         bool tc = false;
         if (l.M >= kShrinkTcFrom) st = launch_shrink_tc<SIDES>(p.l, p.part, &tc, stream);
         if (st == MBGLU_OK && !tc) {
-            if (l.M <= kJoinRows)
+            if (l.M <= kFewRows)
                 st = launch_shrink<SIDES, 1, 1, 5>(p.l, std::min(l.M, 16), 1024, stream);
             else
                 st = launch_shrink<SIDES, 1, 4, 4>(p.l, l.M <= 1024 ? 8 : 2, 608, stream);
@@ -222,7 +221,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         if (st != MBGLU_OK) return st;
     }
     Launch c(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.items))), mbglu::kPairThreads, mbglu::kLoraSmem, stream, 2);
-    st = launched(cudaLaunchKernelEx(&c.cfg, mbglu::lora_pair_kernel<SIDES>, p, maps));
+    st = launched(cudaLaunchKernelEx(&c.cfg, l.M <= kFewRows ? mbglu::lora_pair_kernel<SIDES, true> : mbglu::lora_pair_kernel<SIDES, false>, p, maps));
     if (st == MBGLU_OK && p.plan.rest > 0) st = l.M <= 16 ? launch_join<SIDES, 1>(p, stream) : launch_join<SIDES, 2>(p, stream);
     return st;
 }

@@ -43,6 +43,7 @@ struct LoraPairParams {
     LoraParams l;
     LoraPlan plan;
     float *part;             // [rest splits][tn][256]: a range's accumulators, token by token
+    int prefetch;            // B into L2 ahead
     int early;               // the kernel before this one has waited for the operands
 };
 
@@ -64,6 +65,19 @@ __host__ __device__ inline LoraTile lora_tile(const LoraPlan &p, int i)
         x.c1 = static_cast<int>(static_cast<int64_t>(p.nchunk) * (split + 1) / p.splits);
     }
     return x;
+}
+
+// t + the products of eight bf16 values with eight fp32 ones
+__device__ __forceinline__ float dot8(const uint4 &x, const float4 &y, const float4 &z, float t)
+{
+    t = fmaf(bf16_lo(x.x), y.x, t);
+    t = fmaf(bf16_hi(x.x), y.y, t);
+    t = fmaf(bf16_lo(x.y), y.z, t);
+    t = fmaf(bf16_hi(x.y), y.w, t);
+    t = fmaf(bf16_lo(x.z), z.x, t);
+    t = fmaf(bf16_hi(x.z), z.y, t);
+    t = fmaf(bf16_lo(x.w), z.z, t);
+    return fmaf(bf16_hi(x.w), z.w, t);
 }
 
 // A box of a stack of matrices into this CTA's shared memory, counted on a barrier of either
@@ -131,34 +145,44 @@ __device__ __forceinline__ void lora_term(const LoraParams &p, int d, int sides,
         const uint16_t *b[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) b[i] = side.b + a[i] * side.b_adapter + (n0 + row) * side.ldb + quad * 4;
-        for (int j = 0; j < p.R; j += 16) {
-            const bool in = j + quad * 4 < p.R;
-            uint2 w[2][4];
+        for (int j0 = 0; j0 < p.R; j0 += 32) {   // two steps' loads together
+            uint2 w[2][2][4];
+            float4 v[2][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int c = 0; c < 2; ++c) {
+                const int j = j0 + c * 16;
+                const bool in = j + quad * 4 < p.R;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    w[i][r] = in && n0 + row + r * 8 < p.N ? *reinterpret_cast<const uint2 *>(b[i] + r * 8 * side.ldb + j) : make_uint2(0, 0);
-            uint32_t h[2][2], l[2][2];
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float4 v = in && used[g] ? *reinterpret_cast<const float4 *>(q + g * second + j) : make_float4(0, 0, 0, 0);
-                h[g][0] = pack_bf16x2(v.x, v.y);
-                h[g][1] = pack_bf16x2(v.z, v.w);
-                l[g][0] = pack_bf16x2(v.x - bf16_lo(h[g][0]), v.y - bf16_hi(h[g][0]));
-                l[g][1] = pack_bf16x2(v.z - bf16_lo(h[g][1]), v.w - bf16_hi(h[g][1]));
+                    for (int r = 0; r < 4; ++r)
+                        w[c][i][r] = in && n0 + row + r * 8 < p.N ? *reinterpret_cast<const uint2 *>(b[i] + r * 8 * side.ldb + j) : make_uint2(0, 0);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) v[c][g] = in && used[g] ? *reinterpret_cast<const float4 *>(q + g * second + j) : make_float4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int c = 0; c < 2; ++c) {
+                uint32_t h[2][2], l[2][2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t wa[4] = {w[i][2 * t].x, w[i][2 * t + 1].x, w[i][2 * t].y, w[i][2 * t + 1].y};
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        mma_16816(acc[i][g][t], wa, h[g][0], h[g][1]);
-                        mma_16816(acc[i][g][t], wa, l[g][0], l[g][1]);
-                    }
+                for (int g = 0; g < 2; ++g) {
+                    const float4 x = v[c][g];
+                    h[g][0] = pack_bf16x2(x.x, x.y);
+                    h[g][1] = pack_bf16x2(x.z, x.w);
+                    l[g][0] = pack_bf16x2(x.x - bf16_lo(h[g][0]), x.y - bf16_hi(h[g][0]));
+                    l[g][1] = pack_bf16x2(x.z - bf16_lo(h[g][1]), x.w - bf16_hi(h[g][1]));
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t wa[4] = {w[c][i][2 * t].x, w[c][i][2 * t + 1].x, w[c][i][2 * t].y, w[c][i][2 * t + 1].y};
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            mma_16816(acc[i][g][t], wa, h[g][0], h[g][1]);
+                            mma_16816(acc[i][g][t], wa, l[g][0], l[g][1]);
+                        }
+                    }
+            }
         }
         // this lane's tokens of a half: quad * 2 and the next
 #pragma unroll
@@ -191,6 +215,51 @@ __device__ __forceinline__ void lora_term(const LoraParams &p, int d, int sides,
     }
 }
 
+// The same for rows that mostly have an adapter each: a lane has one output n, reads its row
+// of each token's B, eight tokens' together, and adds the term to y.  p of 16 tokens and 16
+// columns is staged in shared memory (stage, 256 floats), on the way beside B.
+__device__ __forceinline__ void lora_term_rows(const LoraParams &p, int d, int sides, int64_t m0, int64_t n, float *stage, float (&y)[16])
+{
+    const int lane = threadIdx.x & 31, R = p.R;
+    const int mine = lane < 16 ? lora_adapter(p, m0 + lane) : -1;
+    const uint32_t used = __ballot_sync(0xffffffffu, mine >= 0);
+    const LoraSide &side = p.side[d];
+    // this lane stages 8 columns of token lane / 2
+    const bool has = used >> (lane >> 1) & 1u;
+    const float *q = p.p + (m0 + (lane >> 1)) * sides * R + d * R + (lane & 1) * 8;
+    float4 *mystage = reinterpret_cast<float4 *>(stage + lane * 8);
+    for (int j = 0; j < R; j += 16) {
+        const bool in = has && j + (lane & 1) * 8 < R;
+        const float4 v0 = in ? *reinterpret_cast<const float4 *>(q + j) : make_float4(0, 0, 0, 0);
+        const float4 v1 = in ? *reinterpret_cast<const float4 *>(q + j + 4) : make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint4 b[8][2];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int a = __shfl_sync(0xffffffffu, mine, 8 * g + k);
+                const uint16_t *r = side.b + a * side.b_adapter + n * side.ldb + j;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    b[k][h] = a >= 0 && n < p.N && j + 8 * h < R ? *reinterpret_cast<const uint4 *>(r + 8 * h) : make_uint4(0, 0, 0, 0);
+            }
+            if (g == 0) {
+                __syncwarp();
+                mystage[0] = v0;
+                mystage[1] = v1;
+                __syncwarp();
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 *v = reinterpret_cast<const float4 *>(stage + (8 * g + k) * 16);
+                float t = dot8(b[k][0], v[0], v[1], 0.0f);
+                y[8 * g + k] += dot8(b[k][1], v[2], v[3], t);
+            }
+        }
+    }
+    __syncwarp();
+}
+
 // The exchange between the two warps of an output's g and u (as pair_tall.cuh), then the
 // warps' terms.
 constexpr int kLoraSwap = 2 * 16 * 32;
@@ -198,7 +267,8 @@ constexpr uint32_t kLoraExtra = 4 * kLoraSwap * 4 + 8 * kTermWords * 4;
 constexpr uint32_t kLoraSmem = kPairHeader + kPairStages * kPairStage + kLoraExtra + 1024;
 static_assert(kLoraSmem <= 227 * 1024, "shared memory");
 
-template <int SIDES>
+// ROWS: 16 tokens of several adapters by lora_term_rows.
+template <int SIDES, bool ROWS>
 __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPairParams p, const __grid_constant__ LoraMaps maps)
 {
     extern __shared__ unsigned char pair_raw[];
@@ -337,10 +407,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 if (buf == 0) acc_phase ^= 1;
             }
         }
-    } else if (warp == 2 && p.l.adapters > 0 && plan.rest > 0) {
-        // the join reads B row by row and waits for each: its bytes come into L2 beside the
-        // weights, whose copies leave room for them
-        for (int i = max(first, plan.whole + (first - plan.whole % step + step) % step); i < plan.whole + plan.rest; i += step) {
+    } else if (warp == 2 && p.l.adapters > 0 && p.prefetch) {
+        // B is read row by row at the end, where nothing hides the way: its bytes come into L2
+        // beside the weights, whose copies leave room for them
+        for (int i = first; i < plan.whole + plan.rest; i += step) {
             const LoraTile x = lora_tile(plan, i);
             const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2), rows = min(plan.wt / 2, p.l.N - n0);
             for (int m = x.t % plan.ttiles * plan.tn + lane, k = lane; k < plan.tn && rows > 0; k += 32, m += 32) {
@@ -392,12 +462,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 float y[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(r[k]);
-                if (p.l.blocks && tokens > 0 && __ldcg(p.l.blocks + (m0 + j) / kLoraBlock) == kMixed)
-                    lora_term(p.l, d, SIDES, static_cast<int64_t>(m0) + j, n0, term, [&](int g) {
+                if (p.l.blocks && tokens > 0 && __ldcg(p.l.blocks + (m0 + j) / kLoraBlock) == kMixed) {
+                    if constexpr (ROWS)
+                        lora_term_rows(p.l, d, SIDES, static_cast<int64_t>(m0) + j, n, term, y);
+                    else
+                        lora_term(p.l, d, SIDES, static_cast<int64_t>(m0) + j, n0, term, [&](int g) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (k >> 3 == g) y[k] += term[(k & 7) * kTermPitch + lane];
-                    });
+                            for (int k = 0; k < 16; ++k)
+                                if (k >> 3 == g) y[k] += term[(k & 7) * kTermPitch + lane];
+                        });
+                }
                 if constexpr (SIDES == 2) {
                     // two sets in turn, as in pair_tall_kernel
                     float *mine = swap + (sets & 1) * 512 + d * 256, *theirs = swap + (sets & 1) * 512 + (d ^ 1) * 256;
@@ -474,28 +548,19 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
                     for (int h = 0; h < 2; ++h) b[k][d][h] = a[k] >= 0 && j + 8 * h < R ? *reinterpret_cast<const uint4 *>(r + 8 * h) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-            for (int k = 0; k < TOKENS; ++k) {
-                if (a[k] < 0) continue;   // the whole warp
+            for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
                 for (int d = 0; d < SIDES; ++d) {
                     const float *v = p.l.p + (m0 + k) * SIDES * R + d * R + j;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (j + 8 * h >= R) continue;
-                        const float4 y = *reinterpret_cast<const float4 *>(v + 8 * h), z = *reinterpret_cast<const float4 *>(v + 8 * h + 4);
-                        const uint4 x = b[k][d][h];
-                        float t = term[k][d];
-                        t = fmaf(bf16_lo(x.x), y.x, t);
-                        t = fmaf(bf16_hi(x.x), y.y, t);
-                        t = fmaf(bf16_lo(x.y), y.z, t);
-                        t = fmaf(bf16_hi(x.y), y.w, t);
-                        t = fmaf(bf16_lo(x.z), z.x, t);
-                        t = fmaf(bf16_hi(x.z), z.y, t);
-                        t = fmaf(bf16_lo(x.w), z.z, t);
-                        term[k][d] = fmaf(bf16_hi(x.w), z.w, t);
+                        // loads that no branch keeps behind one another
+                        const bool in = a[k] >= 0 && j + 8 * h < R;
+                        const float4 y = in ? *reinterpret_cast<const float4 *>(v + 8 * h) : make_float4(0, 0, 0, 0);
+                        const float4 z = in ? *reinterpret_cast<const float4 *>(v + 8 * h + 4) : make_float4(0, 0, 0, 0);
+                        term[k][d] = dot8(b[k][d][h], y, z, term[k][d]);
                     }
                 }
-            }
         }
 #pragma unroll
         for (int k = 0; k < TOKENS; ++k) {
