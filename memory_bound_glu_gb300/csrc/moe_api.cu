@@ -118,6 +118,8 @@ mbglu_status launch_fused(const mbglu::MoeGeneric &g, const MoeSpace &space, cha
     p.weights = g.user_weights;
     p.counters = reinterpret_cast<uint32_t *>(ws + space.counters);
     p.logits = g.logits;
+    p.chosen = g.ids;
+    p.chosen_weight = g.weights;
     p.gu = reinterpret_cast<float *>(ws + space.gu);
     p.y = reinterpret_cast<float *>(ws + space.y);
     p.carry = reinterpret_cast<float *>(ws + space.carry);

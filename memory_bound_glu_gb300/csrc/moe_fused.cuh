@@ -2,7 +2,7 @@
 // block per SM, all resident at once, that meet at four grid barriers.
 //
 //   1  logits, a warp per expert and four tokens                        | barrier
-//   2  every block chooses the experts of all tokens for itself: nothing to hand over
+//   2  the choice, by every block for itself, or of many tokens by a block each   (| barrier)
 //   3  gated projections of the chosen experts                          | barrier
 //   4  activation, as two bf16 terms                                    | barrier
 //   5  down projections                                                 | barrier
@@ -38,6 +38,7 @@ constexpr int kMoeSum = 4;                        // the first warp of those tha
 constexpr int kMoeMaxStages = 10;
 constexpr uint32_t kMoeUnit = 16384;              // a unit's weights
 constexpr uint32_t kMoeCols = 128;                // tensor memory: two accumulators of 64 columns
+constexpr int kMoeKeys = kMoeMaxExperts;          // logits that a block orders at a time
 constexpr int kMoeSlots = kMoeMaxRows * kMoeMaxTopK;
 
 struct MoeMaps {
@@ -53,7 +54,9 @@ struct MoeParams {
     uint16_t *out;
     int32_t *ids;            // or null
     float *weights;          // or null
-    uint32_t *counters;      // four barriers and the exit, all 0 at the start and at the end
+    uint32_t *counters;      // five barriers and the exit, all 0 at the start and at the end
+    int32_t *chosen;         // [T][top_k]: what the blocks choose, where each has tokens of its own
+    float *chosen_weight;
     float *logits;           // [T][E]
     float *gu;               // [slots][2 N]: g, then u
     float *y;                // [slots][K]
@@ -72,11 +75,15 @@ struct alignas(16) MoeShared {
     uint32_t tmem, failed;
     int active, pad_;
     uint64_t mask[kMoeMaxExperts];               // tokens that chose the expert
+    alignas(16) uint32_t key[kMoeKeys];          // the logits that the block orders
+    float2 pairs[kMoeWarps][4];                  // logits' parts
+    int chunk_used[kMoeMaxExperts / 32], chunk_slots[kMoeMaxExperts / 32];
     float weight[kMoeSlots];
     uint16_t id[kMoeSlots];                      // [T][top_k]
     uint16_t expert[kMoeMaxExperts], first[kMoeMaxExperts + 1];   // of the i-th chosen expert: itself, its first slot
     uint16_t where[kMoeMaxExperts];              // an expert's place among the chosen ones
     uint16_t of_slot[kMoeSlots];                 // a slot's place among the chosen experts
+    float4 sums[kMoeWarps - kMoeSum][32];        // 6: what the warps of a team add up
 };
 
 constexpr uint32_t kMoeHeader = (sizeof(MoeShared) + 1023) / 1024 * 1024;
@@ -106,18 +113,23 @@ __device__ __forceinline__ uint32_t add_acq_rel_gpu(uint32_t *p, uint32_t v)
     return old;
 }
 
-// One thread per block, after a barrier of the threads whose writes it publishes.
+// One thread per block, after a barrier of the threads whose writes it publishes; and before
+// one of those that read what the other blocks published.
 __device__ __forceinline__ void grid_arrive(uint32_t *counter)
 {
-    __threadfence();
-    add_acq_rel_gpu(counter, 1u);
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
 }
 __device__ __forceinline__ bool grid_wait(const uint32_t *counter, uint64_t limit_ns)
 {
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     for (uint32_t i = 1; ld_acquire_gpu(counter) < gridDim.x; ++i)
-        if ((i & 63u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
-    __threadfence();
+        if ((i & 63u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0)
+                t0 = now;
+            else if (now - t0 > limit_ns)
+                return false;
+        }
     return true;
 }
 
@@ -169,41 +181,227 @@ struct MoeWalk {
     __device__ uint32_t run(const MoeUnits &u) const { return min(left, u.chunks - chunk); }
 };
 
-// Four tokens' logits of one expert (one token: four chains of one), a warp.
+// Up to four tokens' logits of one expert (one token: four chains of one), as sums (s, c) over
+// every parts-th 256 columns from the part-th on; a warp.  The next columns are on the way
+// while these are summed.
 template <int TOKENS>
-__device__ __forceinline__ void moe_logits(const MoeParams &p, int e, int t0)
+__device__ __forceinline__ void moe_logits(const MoeParams &p, int e, int t0, int part, int parts, float (&s)[4], float (&c)[4])
 {
     const int lane = threadIdx.x & 31;
-    float s[4] = {}, c[4] = {};
-    const uint16_t *w = p.router + e * p.ldr;
-    for (int k = lane * 8; k < p.K; k += 256) {
-        const uint4 b = *reinterpret_cast<const uint4 *>(w + k);
+    const uint16_t *w = p.router + e * p.ldr, *h = p.h + t0 * p.ldh;
+    uint4 b, a[TOKENS];
+    const auto load = [&](int k) {
+        const bool in = k < p.K;
+        b = in ? *reinterpret_cast<const uint4 *>(w + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) a[j] = in && t0 + j < p.T ? *reinterpret_cast<const uint4 *>(h + j * p.ldh + k) : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = c[j] = 0.0f;
+    int k = part * 256 + lane * 8;
+    load(k);
+    for (int k0 = part * 256; k0 < p.K; k0 += parts * 256) {
         const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        uint32_t aw[TOKENS][4];
 #pragma unroll
         for (int j = 0; j < TOKENS; ++j) {
-            if (TOKENS > 1 && t0 + j >= p.T) continue;
-            const uint4 a = *reinterpret_cast<const uint4 *>(p.h + (t0 + j) * p.ldh + k);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = TOKENS > 1 ? j : i;
-                two_sum(s[at], c[at], __fmul_rn(bf16_lo(aw[i]), bf16_lo(bw[i])));
-                two_sum(s[at], c[at], __fmul_rn(bf16_hi(aw[i]), bf16_hi(bw[i])));
-            }
+            aw[j][0] = a[j].x;
+            aw[j][1] = a[j].y;
+            aw[j][2] = a[j].z;
+            aw[j][3] = a[j].w;
         }
+        k += parts * 256;
+        load(k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < TOKENS; ++j) {
+                const int at = TOKENS > 1 ? j : i;
+                two_sum(s[at], c[at], __fmul_rn(bf16_lo(aw[j][i]), bf16_lo(bw[i])));
+                two_sum(s[at], c[at], __fmul_rn(bf16_hi(aw[j][i]), bf16_hi(bw[i])));
+            }
     }
     if (TOKENS == 1) {
 #pragma unroll
-        for (int i = 1; i < 4; ++i) {
-            two_sum(s[0], c[0], s[i]);
-            c[0] = __fadd_rn(c[0], c[i]);
-        }
+        for (int i = 1; i < 4; ++i) two_sum(s[0], c[0], s[i], c[i]);
     }
 #pragma unroll
-    for (int j = 0; j < TOKENS; ++j) {
-        const float v = warp_pair_sum(s[j], c[j]);
-        if (lane == 0 && t0 + j < p.T) __stcg(p.logits + (t0 + j) * p.E + e, v);
+    for (int j = 0; j < TOKENS; ++j) warp_pair_sum(s[j], c[j]);
+}
+
+// The logits of all tokens, over all blocks.  Where there are fewer pairs of an expert and
+// four tokens than warps, several warps share a pair's columns.
+template <int TOKENS>
+__device__ __forceinline__ void moe_all_logits(const MoeParams &p, MoeShared &sh, int warp)
+{
+    const int lane = threadIdx.x & 31, groups = (p.T + TOKENS - 1) / TOKENS, items = p.E * groups, grid = static_cast<int>(gridDim.x);
+    int parts = 1;   // a divisor of the warps
+    if (items <= grid)
+        parts = 12;
+    else if (items <= 2 * grid)
+        parts = 6;
+    else if (items <= 3 * grid)
+        parts = 4;
+    else if (items <= 6 * grid)
+        parts = 2;
+    static_assert(kMoeWarps == 12, "parts");
+    const int part = warp % parts;
+    for (int i = warp / parts * grid + static_cast<int>(blockIdx.x); i < items; i += kMoeWarps / parts * grid) {
+        const int e = i / groups, t0 = i % groups * TOKENS;
+        float s[4], c[4];
+        moe_logits<TOKENS>(p, e, t0, part, parts, s, c);
+        if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < TOKENS; ++j) {
+                if (parts > 1)
+                    sh.pairs[warp][j] = make_float2(s[j], c[j]);
+                else if (t0 + j < p.T)
+                    __stcg(p.logits + (t0 + j) * p.E + e, pair_value(s[j], c[j]));
+            }
+        }
     }
+    if (parts == 1) return;   // the whole block
+    __syncthreads();          // with several parts there is one round of pairs
+    const int i = warp / parts * grid + static_cast<int>(blockIdx.x);
+    if (part == 0 && i < items && lane < TOKENS) {
+        const int e = i / groups, t = i % groups * TOKENS + lane;
+        float2 v = sh.pairs[warp][lane];
+        for (int w = 1; w < parts; ++w) two_sum(v.x, v.y, sh.pairs[warp + w][lane].x, sh.pairs[warp + w][lane].y);
+        if (t < p.T) __stcg(p.logits + t * p.E + e, pair_value(v.x, v.y));
+    }
+}
+
+// The choice of `tokens` tokens from t0 on, by the block.  A thread has an expert and counts
+// those before it (larger, or equal with a lower index): its place.  No step waits for
+// another, which a search for one maximum after the other does (8 of 128 by shuffles took
+// 4 us where this takes 1).
+__device__ __forceinline__ void moe_order(const MoeParams &p, MoeShared &s, int t0, int tokens, int warp)
+{
+    const int lane = threadIdx.x & 31, pitch = (p.E + 3) & ~3, total = tokens * pitch;
+    for (int i = threadIdx.x; i < total; i += kMoeThreads) {
+        const int t = i / pitch, e = i - t * pitch;
+        s.key[i] = e < p.E ? order_key(__ldcg(p.logits + (t0 + t) * p.E + e)) : 0u;   // 0: no expert
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += kMoeThreads) {
+        const int t = i / pitch, e = i - t * pitch;
+        const uint32_t mine = s.key[i];
+        const uint4 *k = reinterpret_cast<const uint4 *>(s.key + t * pitch);
+        int place = 0;
+#pragma unroll 4
+        for (int q = 0; q < pitch / 4; ++q) {
+            const uint4 v = k[q];   // no key is the largest number
+            place += (v.x + (4 * q < e) > mine) + (v.y + (4 * q + 1 < e) > mine) + (v.z + (4 * q + 2 < e) > mine) + (v.w + (4 * q + 3 < e) > mine);
+        }
+        if (mine != 0 && place < p.top_k) s.id[(t0 + t) * p.top_k + place] = static_cast<uint16_t>(e);
+    }
+    __syncthreads();
+    for (int t = warp; t < tokens; t += kMoeWarps) {
+        const uint16_t *id = s.id + (t0 + t) * p.top_k;
+        const uint32_t *k = s.key + t * pitch;
+        const float top = key_value(k[id[0]]);
+        const float e = lane < p.top_k ? expf(key_value(k[id[lane < p.top_k ? lane : 0]]) - top) : 0.0f;
+        float sum = p.renormalize ? e : 0.0f;
+        bool nan = false;
+        for (int i = lane; i < p.E; i += 32) {
+            nan = nan || k[i] == 1;
+            if (!p.renormalize) sum += expf(key_value(k[i]) - top);
+        }
+        nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane < p.top_k) s.weight[(t0 + t) * p.top_k + lane] = nan ? __uint_as_float(0x7fffffffu) : e / sum;
+    }
+    __syncthreads();
+}
+
+// 2: the choice of all tokens, and from it the tables of the chosen experts; false after a
+// wait that gave up, in every thread.
+__device__ __forceinline__ bool moe_choose(const MoeParams &p, MoeShared &s, int warp)
+{
+    const int lane = threadIdx.x & 31, slots = p.T * p.top_k;
+    const bool all = p.T * ((p.E + 3) & ~3) <= kMoeKeys;
+    if (all) {
+        moe_order(p, s, 0, p.T, warp);
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < slots; i += kMoeThreads) {
+                if (p.ids) p.ids[i] = s.id[i];
+                if (p.weights) p.weights[i] = s.weight[i];
+            }
+    } else {
+        for (int t = static_cast<int>(blockIdx.x); t < p.T; t += static_cast<int>(gridDim.x)) {
+            moe_order(p, s, t, 1, warp);
+            if (static_cast<int>(threadIdx.x) < p.top_k) {
+                const int i = t * p.top_k + static_cast<int>(threadIdx.x);
+                __stcg(p.chosen + i, static_cast<int32_t>(s.id[i]));
+                __stcg(p.chosen_weight + i, s.weight[i]);
+                if (p.ids) p.ids[i] = s.id[i];
+                if (p.weights) p.weights[i] = s.weight[i];
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            grid_arrive(p.counters + 5);
+            if (!grid_wait(p.counters + 5, kWaitLimitNs)) s.failed = 1;
+        }
+        __syncthreads();
+        if (s.failed != 0) return false;
+        for (int i = threadIdx.x; i < slots; i += kMoeThreads) {
+            s.id[i] = static_cast<uint16_t>(__ldcg(p.chosen + i));
+            s.weight[i] = __ldcg(p.chosen_weight + i);
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < slots; i += kMoeThreads)
+        atomicOr(reinterpret_cast<unsigned long long *>(&s.mask[s.id[i]]), 1ull << (i / p.top_k));
+    __syncthreads();
+    // 32 experts at a time: how many are used, by how many tokens
+    const int chunks = (p.E + 31) / 32;
+    for (int i = warp; i < chunks; i += kMoeWarps) {
+        const int e = i * 32 + lane, count = e < p.E ? __popcll(s.mask[e]) : 0;
+        const uint32_t used = __ballot_sync(0xffffffffu, count > 0);
+        const int total = __reduce_add_sync(0xffffffffu, count);
+        if (lane == 0) {
+            s.chunk_used[i] = __popc(used);
+            s.chunk_slots[i] = total;
+        }
+    }
+    __syncthreads();
+    for (int i = warp; i < chunks; i += kMoeWarps) {
+        const int e = i * 32 + lane, count = e < p.E ? __popcll(s.mask[e]) : 0;
+        const uint32_t used = __ballot_sync(0xffffffffu, count > 0);
+        // the chunks before this one
+        const int n = __reduce_add_sync(0xffffffffu, lane < i ? s.chunk_used[lane] : 0);
+        const int base = __reduce_add_sync(0xffffffffu, lane < i ? s.chunk_slots[lane] : 0);
+        int before = count;   // inclusive sum over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        const int at = n + __popc(used & ((1u << lane) - 1)), first = base + before - count;
+        if (count > 0) {
+            s.expert[at] = static_cast<uint16_t>(e);
+            s.first[at] = static_cast<uint16_t>(first);
+            s.where[e] = static_cast<uint16_t>(at);
+            for (int j = 0; j < count; ++j) s.of_slot[first + j] = static_cast<uint16_t>(at);
+        }
+        if (i == chunks - 1 && lane == 31) {
+            s.active = n + __popc(used);
+            s.first[n + __popc(used)] = static_cast<uint16_t>(base + before);
+        }
+    }
+    __syncthreads();
+    return true;
+}
+
+// The activation of two columns as two bf16 terms, so that the tensor cores' operand is off
+// by 2^-18 and not by 2^-9; an infinite one has no second term.
+__device__ __forceinline__ void moe_act(float2 g, float2 u, uint32_t &hi, uint32_t &lo)
+{
+    const float a0 = silu_f32(g.x) * u.x, a1 = silu_f32(g.y) * u.y;
+    hi = pack_bf16x2(a0, a1);
+    lo = pack_bf16x2(isfinite(bf16_lo(hi)) ? a0 - bf16_lo(hi) : 0.0f, isfinite(bf16_hi(hi)) ? a1 - bf16_hi(hi) : 0.0f);
 }
 
 static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const MoeParams p, const __grid_constant__ MoeMaps maps)
@@ -216,6 +414,12 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
     const uint32_t stage_bytes = moe_stage_bytes(p.pad);
 
     if (threadIdx.x == 0) {
+        // the descriptors are on their way before the first copies want them
+        prefetch_tensor_map(&maps.gate);
+        prefetch_tensor_map(&maps.up);
+        prefetch_tensor_map(&maps.down);
+        prefetch_tensor_map(&maps.h);
+        prefetch_tensor_map(&maps.act);
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s.weights_full[i], 1);
             mbar_init(&s.tokens_full[i], 1);
@@ -237,13 +441,10 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
     for (int e = threadIdx.x; e < p.E; e += kMoeThreads) s.mask[e] = 0;
 
     // 1: logits
-    if (p.T == 1) {
-        for (int i = static_cast<int>(warp * gridDim.x + blockIdx.x); i < p.E; i += static_cast<int>(gridDim.x) * kMoeWarps) moe_logits<1>(p, i, 0);
-    } else {
-        const int groups = (p.T + 3) / 4;
-        for (int i = static_cast<int>(warp * gridDim.x + blockIdx.x); i < p.E * groups; i += static_cast<int>(gridDim.x) * kMoeWarps)
-            moe_logits<4>(p, i / groups, i % groups * 4);
-    }
+    if (p.T == 1)
+        moe_all_logits<1>(p, s, warp);
+    else
+        moe_all_logits<4>(p, s, warp);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -255,58 +456,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
     __syncthreads();
     bool ok = s.failed == 0;
 
-    // 2: the choice, of all tokens in every block
-    if (ok) {
-        for (int t = warp; t < p.T; t += kMoeWarps) {
-            int id;
-            float w;
-            const float *l = p.logits + t * p.E;
-            const auto logit = [l](int e) { return __ldcg(l + e); };
-            if (p.E <= 128)
-                warp_top_k<4>(logit, p.E, p.top_k, p.renormalize != 0, id, w);
-            else
-                warp_top_k<kMoeMaxExperts / 32>(logit, p.E, p.top_k, p.renormalize != 0, id, w);
-            if (lane < p.top_k) {
-                const int at = t * p.top_k + lane;
-                s.id[at] = static_cast<uint16_t>(id);
-                s.weight[at] = w;
-                atomicOr(reinterpret_cast<unsigned long long *>(&s.mask[id]), 1ull << t);
-                if (static_cast<int>(blockIdx.x) == t) {
-                    if (p.ids) p.ids[at] = id;
-                    if (p.weights) p.weights[at] = w;
-                }
-            }
-        }
-        __syncthreads();
-        if (warp == 0) {
-            int n = 0, slot = 0;
-            for (int e0 = 0; e0 < p.E; e0 += 32) {
-                const int e = e0 + lane;
-                const int count = e < p.E ? __popcll(s.mask[e]) : 0;
-                const uint32_t used = __ballot_sync(0xffffffffu, count > 0);
-                int before = count;   // inclusive sum over the lanes
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, before, o);
-                    if (lane >= o) before += v;
-                }
-                const int at = n + __popc(used & ((1u << lane) - 1));
-                if (count > 0) {
-                    s.expert[at] = static_cast<uint16_t>(e);
-                    s.first[at] = static_cast<uint16_t>(slot + before - count);
-                    s.where[e] = static_cast<uint16_t>(at);
-                    for (int i = 0; i < count; ++i) s.of_slot[slot + before - count + i] = static_cast<uint16_t>(at);
-                }
-                n += __popc(used);
-                slot += __shfl_sync(0xffffffffu, before, 31);
-            }
-            if (lane == 0) {
-                s.active = n;
-                s.first[n] = static_cast<uint16_t>(slot);
-            }
-        }
-        __syncthreads();
-    }
+    if (ok) ok = moe_choose(p, s, warp);
     const MoeUnits gated = moe_units(ok ? s.active : 0, (p.N + 63) / 64, (p.K + 63) / 64);
     const MoeUnits down = moe_units(ok ? s.active : 0, (p.K + 127) / 128, (p.N + 63) / 64);
 
@@ -542,14 +692,11 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                         u.x += z.x;
                         u.y += z.y;
                     }
-                    // two bf16 terms, so that the tensor cores' operand is off by 2^-18 and not by 2^-9; an
-                    // infinite one has no second term
-                    const float a0 = silu_f32(g.x) * u.x, a1 = silu_f32(g.y) * u.y;
-                    const uint32_t hi = pack_bf16x2(a0, a1);
-                    const float r0 = isfinite(bf16_lo(hi)) ? a0 - bf16_lo(hi) : 0.0f, r1 = isfinite(bf16_hi(hi)) ? a1 - bf16_hi(hi) : 0.0f;
+                    uint32_t hi, lo;
+                    moe_act(g, u, hi, lo);
                     uint16_t *dst = p.act + slot * p.act_ld + n;
                     *reinterpret_cast<uint32_t *>(dst) = hi;
-                    *reinterpret_cast<uint32_t *>(dst + p.act_rows * p.act_ld) = pack_bf16x2(r0, r1);
+                    *reinterpret_cast<uint32_t *>(dst + p.act_rows * p.act_ld) = lo;
                 }
                 fence_proxy_async_all();
                 bar_sync_named(1, sums * 32);
@@ -560,33 +707,63 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                     mbar_arrive(&s.act_ready);
                 }
             } else {
-                // 6: the weighted sum; a warp per token and tile of 128 columns
-                for (uint32_t i = blockIdx.x + gridDim.x * static_cast<uint32_t>(me); ok && i < static_cast<uint32_t>(p.T) * units.tiles;
-                     i += gridDim.x * static_cast<uint32_t>(sums)) {
+                // 6: the weighted sum of a token's 128 columns: a team of warps, each of which takes
+                // every team-th expert, four of them at a time
+                const uint32_t items = static_cast<uint32_t>(p.T) * units.tiles;
+                const uint32_t team = items <= gridDim.x ? 8u : items <= 2 * gridDim.x ? 4u : items <= 4 * gridDim.x ? 2u : 1u;
+                const uint32_t mine = static_cast<uint32_t>(me) / team, place = static_cast<uint32_t>(me) % team;
+                static_assert(kMoeWarps - kMoeSum == 8, "teams");
+                for (uint32_t i = blockIdx.x + gridDim.x * mine; ok && i < items; i += gridDim.x * (8 / team)) {
                     const uint32_t t = i / units.tiles, tile = i - t * units.tiles;
                     const int k = static_cast<int>(tile) * 128 + lane * 4;
-                    if (k >= p.K) continue;   // K is a multiple of 8
+                    const bool in = k < p.K;   // K is a multiple of 8
                     float4 sum = make_float4(0, 0, 0, 0);
-                    for (int j = 0; j < p.top_k; ++j) {
-                        const int e = s.id[t * p.top_k + j], at = s.where[e];
-                        const int col = __popcll(s.mask[e] & ((1ull << t) - 1));
-                        const float c = s.weight[t * p.top_k + j];
-                        const uint32_t u0 = (static_cast<uint32_t>(at) * units.tiles + tile) * units.chunks;
-                        const uint32_t b0 = moe_owner(units, u0), b1 = moe_owner(units, u0 + units.chunks - 1);
-                        float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (s.first[at] + col) * static_cast<int64_t>(p.K) + k));
-                        for (uint32_t b = b0 + 1; b <= b1; ++b) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.carry + (static_cast<int64_t>(b) * p.pad + col) * 128 + lane * 4));
-                            v.x += x.x;
-                            v.y += x.y;
-                            v.z += x.z;
-                            v.w += x.w;
+                    for (uint32_t j0 = place; j0 < static_cast<uint32_t>(p.top_k); j0 += 4 * team) {
+                        float4 v[4], x[4];
+                        float c[4];
+                        uint32_t b0[4], b1[4];
+                        int col[4];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const uint32_t j = j0 + h * team;
+                            const bool has = in && j < static_cast<uint32_t>(p.top_k);
+                            const int at = static_cast<int>(t) * p.top_k + static_cast<int>(has ? j : place);
+                            const int e = s.id[at], w = s.where[e];
+                            col[h] = __popcll(s.mask[e] & ((1ull << t) - 1));
+                            c[h] = has ? s.weight[at] : 0.0f;
+                            const uint32_t u0 = (static_cast<uint32_t>(w) * units.tiles + tile) * units.chunks;
+                            b0[h] = moe_owner(units, u0);
+                            b1[h] = moe_owner(units, u0 + units.chunks - 1);
+                            const float4 none = make_float4(0, 0, 0, 0);
+                            v[h] = has ? __ldcg(reinterpret_cast<const float4 *>(p.y + (s.first[w] + col[h]) * static_cast<int64_t>(p.K) + k)) : none;
+                            x[h] = has && b1[h] > b0[h]
+                                       ? __ldcg(reinterpret_cast<const float4 *>(p.carry + (static_cast<int64_t>(b0[h] + 1) * p.pad + col[h]) * 128 + lane * 4))
+                                       : none;
+                            if (!has) b1[h] = b0[h];
                         }
-                        sum.x = fmaf(c, v.x, sum.x);
-                        sum.y = fmaf(c, v.y, sum.y);
-                        sum.z = fmaf(c, v.z, sum.z);
-                        sum.w = fmaf(c, v.w, sum.w);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            v[h] = make_float4(v[h].x + x[h].x, v[h].y + x[h].y, v[h].z + x[h].z, v[h].w + x[h].w);
+                            for (uint32_t b = b0[h] + 2; b <= b1[h]; ++b) {
+                                const float4 z = __ldcg(reinterpret_cast<const float4 *>(p.carry + (static_cast<int64_t>(b) * p.pad + col[h]) * 128 + lane * 4));
+                                v[h] = make_float4(v[h].x + z.x, v[h].y + z.y, v[h].z + z.z, v[h].w + z.w);
+                            }
+                            sum.x = fmaf(c[h], v[h].x, sum.x);
+                            sum.y = fmaf(c[h], v[h].y, sum.y);
+                            sum.z = fmaf(c[h], v[h].z, sum.z);
+                            sum.w = fmaf(c[h], v[h].w, sum.w);
+                        }
                     }
-                    *reinterpret_cast<uint2 *>(p.out + t * p.ldo + k) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                    if (team > 1) {   // one item per team and phase: no sum is written twice
+                        s.sums[me][lane] = sum;
+                        bar_sync_named(2 + static_cast<int>(mine), static_cast<int>(team) * 32);
+                        if (place != 0) break;
+                        for (uint32_t h = 1; h < team; ++h) {
+                            const float4 z = s.sums[me + h][lane];
+                            sum = make_float4(sum.x + z.x, sum.y + z.y, sum.z + z.z, sum.w + z.w);
+                        }
+                    }
+                    if (in) *reinterpret_cast<uint2 *>(p.out + t * p.ldo + k) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
                 }
             }
         }
@@ -604,7 +781,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
     }
     // the last block to leave: everyone has passed every barrier
     if (threadIdx.x == 0 && s.failed == 0 && add_acq_rel_gpu(p.counters + 4, 1u) == gridDim.x - 1)
-        for (int i = 0; i < 5; ++i) p.counters[i] = 0;
+        for (int i = 0; i < 6; ++i) p.counters[i] = 0;
 }
 
 }  // namespace mbglu

@@ -26,8 +26,8 @@ static __global__ void __launch_bounds__(256) moe_generic_logits(const MoeGeneri
     const uint16_t *a = p.h + t * p.ldh, *b = p.router + e * p.ldr;
     float s = 0.0f, c = 0.0f;
     for (int k = threadIdx.x & 31; k < p.K; k += 32) two_sum(s, c, __fmul_rn(bf16_to_f32(a[k]), bf16_to_f32(b[k])));
-    const float v = warp_pair_sum(s, c);
-    if ((threadIdx.x & 31) == 0) p.logits[i] = v;
+    warp_pair_sum(s, c);
+    if ((threadIdx.x & 31) == 0) p.logits[i] = pair_value(s, c);
 }
 
 static __global__ void __launch_bounds__(32) moe_generic_choice(const MoeGeneric p)

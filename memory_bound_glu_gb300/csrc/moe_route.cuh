@@ -25,26 +25,37 @@ __device__ __forceinline__ void two_sum(float &s, float &c, float x)
     s = t;
 }
 
-// What a warp's lanes hold as (s, c), as one rounded number in every lane.  An infinite
-// or NaN sum is the plain one: its roundings are infinity - infinity.
-__device__ __forceinline__ float warp_pair_sum(float s, float c)
+// (s, c) += (s2, c2)
+__device__ __forceinline__ void two_sum(float &s, float &c, float s2, float c2)
+{
+    two_sum(s, c, s2);
+    c = __fadd_rn(c, c2);
+}
+
+// A pair as one rounded number.  An infinite or NaN sum is the plain one: its roundings are
+// infinity - infinity.
+__device__ __forceinline__ float pair_value(float s, float c) { return isfinite(s) ? __fadd_rn(s, c) : s; }
+
+// The sum of what a warp's lanes hold, in every lane.
+__device__ __forceinline__ void warp_pair_sum(float &s, float &c)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float s2 = __shfl_xor_sync(0xffffffffu, s, o), c2 = __shfl_xor_sync(0xffffffffu, c, o);
-        two_sum(s, c, s2);
-        c = __fadd_rn(c, c2);
+        two_sum(s, c, s2, c2);
     }
-    const float v = __fadd_rn(s, c);
-    return isfinite(s) ? v : s;
 }
 
-// Orders floats as integers; -0 counts as 0, NaN is below everything.
+// Orders floats as integers; -0 counts as 0, NaN (1) is below everything.
 __device__ __forceinline__ uint32_t order_key(float x)
 {
-    if (isnan(x)) return 0;
+    if (isnan(x)) return 1;
     const uint32_t u = __float_as_uint(x + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return k == 1 ? __uint_as_float(0x7fffffffu) : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 // One warp: the top_k of `experts` logits, largest first, ties to the lowest index, and
@@ -55,57 +66,46 @@ template <int PER, typename F>
 __device__ __forceinline__ void warp_top_k(F logit, int experts, int top_k, bool renormalize, int &id, float &weight)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t key[PER];
-    float v[PER], top = -INFINITY;
+    uint32_t key[PER], best = 0, chosen = 0;
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        v[i] = e < experts ? logit(e) : -INFINITY;
-        nan = nan || isnan(v[i]);
-        // an expert that does not exist is below one that is NaN: keys of experts start at 1
-        key[i] = e < experts ? max(order_key(v[i]), 1u) : 0u;
-        top = fmaxf(top, v[i]);
+        key[i] = i * 32 + lane < experts ? order_key(logit(i * 32 + lane)) : 0u;
+        nan = nan || key[i] == 1;
+        best = max(best, key[i]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     nan = __any_sync(0xffffffffu, nan);
+    const float top = key_value(__reduce_max_sync(0xffffffffu, best));
     float sum = 0.0f;
     if (!renormalize) {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (i * 32 + lane < experts) sum += expf(v[i] - top);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (key[i] != 0) sum += expf(key_value(key[i]) - top);
     }
     id = 0;
-    float mine = 0.0f;
     for (int j = 0; j < top_k; ++j) {
-        uint32_t best = 0;
+        best = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) best = max(best, key[i]);
         best = __reduce_max_sync(0xffffffffu, best);
         uint32_t at = 0xffffffffu;
-        float val = 0.0f;
 #pragma unroll
         for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == best) {
-                at = static_cast<uint32_t>(i * 32 + lane);
-                val = v[i];
-            }
-        const uint32_t first = __reduce_min_sync(0xffffffffu, at);
-        const float x = __shfl_sync(0xffffffffu, val, static_cast<int>(first & 31u));
+            if (key[i] == best) at = static_cast<uint32_t>(i * 32 + lane);
+        at = __reduce_min_sync(0xffffffffu, at);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (static_cast<uint32_t>(i * 32 + lane) == first) key[i] = 0;
-        const float e = expf(x - top);
-        if (renormalize) sum += e;
+            if (static_cast<uint32_t>(i * 32 + lane) == at) key[i] = 0;
         if (lane == j) {
-            id = static_cast<int>(first);
-            mine = e;
+            id = static_cast<int>(at);
+            chosen = best;
         }
     }
-    weight = nan ? __uint_as_float(0x7fffffffu) : mine / sum;
+    const float e = lane < top_k ? expf(key_value(chosen) - top) : 0.0f;
+    if (renormalize) sum = e;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    weight = nan ? __uint_as_float(0x7fffffffu) : e / sum;
 }
 
 }  // namespace mbglu

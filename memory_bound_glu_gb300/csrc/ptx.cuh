@@ -116,6 +116,12 @@ struct alignas(64) TensorMap {
     uint64_t opaque[16];
 };
 
+// Asks for a descriptor ahead of the copies that use it.
+__device__ __forceinline__ void prefetch_tensor_map(const TensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Tiled tensor copy of one 2-D box at element coordinates (x, y) (x
 // innermost) into this CTA's shared memory (128-byte aligned); the whole
 // box's bytes -- elements outside the tensor arrive as zeros -- are counted
