@@ -18,6 +18,10 @@
 // weights; only the chosen ones are written), in 5 the activation rows of the expert.
 // A token's column is its own, so what other tokens hold does not reach it.
 //
+// In 5 the activation's second terms are more rows of the tokens' side, so their products
+// are more columns of the same MMA (added up where they are read) and the weights are read
+// from shared memory once: as MMAs of their own they took a unit from 0.2 to 0.3 us.
+//
 // The copies of weights run ahead over the barriers: the first units of 5 are on their
 // way while 3 is finished and 4 runs, up to the ring's 96 to 160 KB per SM.
 //
@@ -37,7 +41,8 @@ constexpr int kMoeWarps = kMoeThreads / 32;
 constexpr int kMoeSum = 4;                        // the first warp of those that read accumulators and add
 constexpr int kMoeMaxStages = 10;
 constexpr uint32_t kMoeUnit = 16384;              // a unit's weights
-constexpr uint32_t kMoeCols = 128;                // tensor memory: two accumulators of 64 columns
+constexpr uint32_t kMoeAcc = 128;                 // columns of an accumulator: 64 tokens' two terms
+constexpr uint32_t kMoeCols = 2 * kMoeAcc;
 constexpr int kMoeKeys = kMoeMaxExperts;          // logits that a block orders at a time
 constexpr int kMoeSlots = kMoeMaxRows * kMoeMaxTopK;
 
@@ -74,7 +79,7 @@ struct alignas(16) MoeShared {
     uint64_t acc_full[2], acc_empty[2], act_ready, done;
     uint32_t tmem, failed;
     int active, pad_;
-    uint64_t mask[kMoeMaxExperts];               // tokens that chose the expert
+    uint64_t mask[kMoeMaxExperts];               // tokens that chose the expert (little-endian halves are set)
     alignas(16) uint32_t key[kMoeKeys];          // the logits that the block orders
     float2 pairs[kMoeWarps][4];                  // logits' parts
     int chunk_used[kMoeMaxExperts / 32], chunk_slots[kMoeMaxExperts / 32];
@@ -275,9 +280,9 @@ __device__ __forceinline__ void moe_all_logits(const MoeParams &p, MoeShared &sh
 // those before it (larger, or equal with a lower index): its place.  No step waits for
 // another, which a search for one maximum after the other does (8 of 128 by shuffles took
 // 4 us where this takes 1).
-__device__ __forceinline__ void moe_order(const MoeParams &p, MoeShared &s, int t0, int tokens, int warp)
+__device__ __forceinline__ void moe_order(const MoeParams &p, MoeShared &s, int t0, int tokens)
 {
-    const int lane = threadIdx.x & 31, pitch = (p.E + 3) & ~3, total = tokens * pitch;
+    const int pitch = (p.E + 3) & ~3, total = tokens * pitch;
     for (int i = threadIdx.x; i < total; i += kMoeThreads) {
         const int t = i / pitch, e = i - t * pitch;
         s.key[i] = e < p.E ? order_key(__ldcg(p.logits + (t0 + t) * p.E + e)) : 0u;   // 0: no expert
@@ -296,7 +301,13 @@ __device__ __forceinline__ void moe_order(const MoeParams &p, MoeShared &s, int 
         if (mine != 0 && place < p.top_k) s.id[(t0 + t) * p.top_k + place] = static_cast<uint16_t>(e);
     }
     __syncthreads();
-    for (int t = warp; t < tokens; t += kMoeWarps) {
+}
+
+// The weights of what moe_order has chosen; a warp per token, `warps` of them.
+__device__ __forceinline__ void moe_weigh(const MoeParams &p, MoeShared &s, int t0, int tokens, int warp, int warps)
+{
+    const int lane = threadIdx.x & 31, pitch = (p.E + 3) & ~3;
+    for (int t = warp; t < tokens; t += warps) {
         const uint16_t *id = s.id + (t0 + t) * p.top_k;
         const uint32_t *k = s.key + t * pitch;
         const float top = key_value(k[id[0]]);
@@ -312,32 +323,35 @@ __device__ __forceinline__ void moe_order(const MoeParams &p, MoeShared &s, int 
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane < p.top_k) s.weight[(t0 + t) * p.top_k + lane] = nan ? __uint_as_float(0x7fffffffu) : e / sum;
     }
-    __syncthreads();
 }
+
+// Whether each block chooses for all tokens.
+__device__ __forceinline__ bool moe_choose_all(const MoeParams &p) { return p.T * ((p.E + 3) & ~3) <= kMoeKeys; }
 
 // 2: the choice of all tokens, and from it the tables of the chosen experts; false after a
 // wait that gave up, in every thread.
 __device__ __forceinline__ bool moe_choose(const MoeParams &p, MoeShared &s, int warp)
 {
     const int lane = threadIdx.x & 31, slots = p.T * p.top_k;
-    const bool all = p.T * ((p.E + 3) & ~3) <= kMoeKeys;
-    if (all) {
-        moe_order(p, s, 0, p.T, warp);
-        if (blockIdx.x == 0)
-            for (int i = threadIdx.x; i < slots; i += kMoeThreads) {
-                if (p.ids) p.ids[i] = s.id[i];
-                if (p.weights) p.weights[i] = s.weight[i];
-            }
+    if (moe_choose_all(p)) {
+        moe_order(p, s, 0, p.T);   // the weights are for 6 and come while the copies run
+        if (blockIdx.x == 0 && p.ids)
+            for (int i = threadIdx.x; i < slots; i += kMoeThreads) p.ids[i] = s.id[i];
     } else {
         for (int t = static_cast<int>(blockIdx.x); t < p.T; t += static_cast<int>(gridDim.x)) {
-            moe_order(p, s, t, 1, warp);
-            if (static_cast<int>(threadIdx.x) < p.top_k) {
-                const int i = t * p.top_k + static_cast<int>(threadIdx.x);
-                __stcg(p.chosen + i, static_cast<int32_t>(s.id[i]));
-                __stcg(p.chosen_weight + i, s.weight[i]);
-                if (p.ids) p.ids[i] = s.id[i];
-                if (p.weights) p.weights[i] = s.weight[i];
+            moe_order(p, s, t, 1);
+            if (warp == 0) {
+                moe_weigh(p, s, t, 1, 0, 1);
+                __syncwarp();
+                if (lane < p.top_k) {
+                    const int i = t * p.top_k + lane;
+                    __stcg(p.chosen + i, static_cast<int32_t>(s.id[i]));
+                    __stcg(p.chosen_weight + i, s.weight[i]);
+                    if (p.ids) p.ids[i] = s.id[i];
+                    if (p.weights) p.weights[i] = s.weight[i];
+                }
             }
+            __syncthreads();
         }
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -353,7 +367,7 @@ __device__ __forceinline__ bool moe_choose(const MoeParams &p, MoeShared &s, int
         __syncthreads();
     }
     for (int i = threadIdx.x; i < slots; i += kMoeThreads)
-        atomicOr(reinterpret_cast<unsigned long long *>(&s.mask[s.id[i]]), 1ull << (i / p.top_k));
+        atomicOr(reinterpret_cast<uint32_t *>(&s.mask[s.id[i]]) + (i / p.top_k >> 5), 1u << (i / p.top_k & 31));
     __syncthreads();
     // 32 experts at a time: how many are used, by how many tokens
     const int chunks = (p.E + 31) / 32;
@@ -526,7 +540,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                         mbar_arrive_expect_tx(&s.tokens_full[st], static_cast<uint32_t>(boxes) * 4096u);
                         for (int i = 0; i < boxes; ++i) {
                             tma_load_2d(d + i * 2048, &maps.act, x, first + i * 16, &s.tokens_full[st], policy);
-                            tma_load_2d(d + p.pad * 128 + i * 2048, &maps.act, x, p.act_rows + first + i * 16, &s.tokens_full[st], policy);
+                            tma_load_2d(d + (boxes + i) * 2048, &maps.act, x, p.act_rows + first + i * 16, &s.tokens_full[st], policy);
                         }
                     }
                 }
@@ -547,14 +561,15 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
     } else if (warp == 1) {
         int st = 0;
         uint32_t phase = 0, buf = 0, acc_phase = 1;
+        const uint64_t a0 = smem_desc_sw128(ring);
         for (int second = 0; second < 2 && ok; ++second) {
             const MoeUnits &units = second ? down : gated;
             MoeWalk w(units);
             while (w.left > 0 && ok) {
                 const uint32_t run = w.run(units);
-                const int cols = second ? (s.first[w.expert + 1] - s.first[w.expert] + 15) / 16 * 16 : p.pad;
+                const int cols = second ? (s.first[w.expert + 1] - s.first[w.expert] + 15) / 16 * 32 : p.pad;   // of both terms
                 const uint32_t idesc = tc_idesc_bf16(128, 16) + (static_cast<uint32_t>((cols - 16) >> 3) << 17);
-                const uint32_t d = tmem + buf * 64u;
+                const uint32_t d = tmem + buf * kMoeAcc;
                 if (!pair_wait(&s.acc_empty[buf], acc_phase, kWaitLimitNs)) {
                     ok = false;
                     break;
@@ -566,16 +581,10 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                         break;
                     }
                     tc_fence_after();
+                    const uint64_t ad = a0 + static_cast<uint32_t>(st) * (stage_bytes >> 4), bd = ad + (kMoeUnit >> 4);
                     if (elect_one()) {
-                        unsigned char *a = ring + st * stage_bytes, *b = a + kMoeUnit;
-                        const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(b);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, c > 0 || kk > 0);
-                        if (second) {
-                            const uint64_t ld = smem_desc_sw128(b + p.pad * 128);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, ad + 2 * kk, ld + 2 * kk, idesc, true);
-                        }
                         tc_commit(&s.empty[st]);
                         if (c == run - 1) tc_commit(&s.acc_full[buf]);
                     }
@@ -597,6 +606,13 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
         if (!pair_wait(&s.done, 0, kWaitLimitNs)) ok = false;
     } else if (warp >= kMoeSum) {
         const int sums = kMoeWarps - kMoeSum, me = warp - kMoeSum;
+        if (moe_choose_all(p) && me >= 4) {   // read after the barriers below
+            moe_weigh(p, s, 0, p.T, me - 4, 4);
+            __syncwarp();
+            if (blockIdx.x == 0 && p.weights)
+                for (int t = me - 4; t < p.T; t += 4)
+                    if (lane < p.top_k) p.weights[t * p.top_k + lane] = s.weight[t * p.top_k + lane];
+        }
         uint32_t buf = 0, acc_phase = 0;
         for (int second = 0; second < 2 && ok; ++second) {
             const MoeUnits &units = second ? down : gated;
@@ -624,7 +640,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                             if (m == 0) continue;
                             float v[16];
                             __syncwarp();
-                            tmem_ld16(lanes + buf * 64u + static_cast<uint32_t>(c), v);
+                            tmem_ld16(lanes + buf * kMoeAcc + static_cast<uint32_t>(c), v);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 if (m >> i & 1u) {
@@ -640,9 +656,12 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                         const int k = static_cast<int>(w.tile) * 128 + row;
                         float *dst = p.y + first * static_cast<int64_t>(p.K) + k;
                         for (int c = 0; c < count; c += 16) {
-                            float v[16];
+                            float v[16], x[16];
                             __syncwarp();
-                            tmem_ld16(lanes + buf * 64u + static_cast<uint32_t>(c), v);
+                            tmem_ld16(lanes + buf * kMoeAcc + static_cast<uint32_t>(c), v);
+                            tmem_ld16(lanes + buf * kMoeAcc + static_cast<uint32_t>((count + 15) / 16 * 16 + c), x);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] += x[i];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 if (c + i < count) {
@@ -684,13 +703,14 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                     if (n >= p.N) continue;   // N is even: both columns exist, or none
                     const float *src = p.gu + slot * (2 * static_cast<int64_t>(p.N)) + n;
                     float2 g = __ldcg(reinterpret_cast<const float2 *>(src)), u = __ldcg(reinterpret_cast<const float2 *>(src + p.N));
-                    for (uint32_t b = b0 + 1; b <= b1; ++b) {
-                        const float *q = p.carry + (static_cast<int64_t>(b) * p.pad + col) * 128 + lane * 2;
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(q)), z = __ldcg(reinterpret_cast<const float2 *>(q + 64));
-                        g.x += x.x;
-                        g.y += x.y;
-                        u.x += z.x;
-                        u.y += z.y;
+                    const auto part = [&](uint32_t b, int up) {
+                        const float *q = p.carry + (static_cast<int64_t>(b) * p.pad + col) * 128 + up * 64 + lane * 2;
+                        return b <= b1 ? __ldcg(reinterpret_cast<const float2 *>(q)) : make_float2(0.0f, 0.0f);
+                    };
+                    for (uint32_t b = b0 + 1; b <= b1; b += 2) {   // two on the way together
+                        const float2 x = part(b, 0), z = part(b, 1), x2 = part(b + 1, 0), z2 = part(b + 1, 1);
+                        g = make_float2(g.x + x.x + x2.x, g.y + x.y + x2.y);
+                        u = make_float2(u.x + z.x + z2.x, u.y + z.y + z2.y);
                     }
                     uint32_t hi, lo;
                     moe_act(g, u, hi, lo);
