@@ -170,7 +170,8 @@ def _quick():
         m = importlib.import_module("._mbglu_torch", __package__)
         m.bind(*(ctypes.cast(getattr(l, n), ctypes.c_void_p).value
                  for n in ("glu_gemm", "glu_gemm_backward", "glu_gemm_backward_workspace_bytes", "add_rmsnorm_fp8", "glu_fp8",
-                           "matmul_fp8", "matmul_fp8_workspace_bytes")))
+                           "matmul_fp8", "matmul_fp8_workspace_bytes", "glu_lora", "glu_lora_workspace_bytes", "linear_lora",
+                           "linear_lora_workspace_bytes", "moe_glu")))
         _quick_module = m
     return _quick_module
 
@@ -758,6 +759,12 @@ def glu_lora(h, gate_w, up_w, gate_a, gate_b, up_a, up_b, adapter, scale=None, o
     scale float32 [adapters] or None for 1.  The workspace is a byte tensor of
     glu_lora_workspace_bytes(M, N, K, adapters, R) bytes, 256-byte aligned, allocated
     here when not given.  No gradients."""
+    if stream is None:
+        r = (_quick_module or _quick()).glu_lora(h, gate_w, up_w, gate_a, gate_b, up_a, up_b, adapter, scale, out, _MODES[mode], workspace)
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "glu_lora")
+            return r
     bf16 = torch.bfloat16
     M, K, dev = _dims(h, "h", bf16)
     N = _out_rows(gate_w, "gate_w")
@@ -780,6 +787,12 @@ def linear_lora(x, w, a, b, adapter, scale=None, out=None, workspace=None, strea
     the row's adapter: one projection of glu_lora, such as the down projection.
     Arguments as there, a [adapters,R,K] and b [adapters,N,R]; the workspace is one of
     linear_lora_workspace_bytes(M, N, K, adapters, R) bytes.  No gradients."""
+    if stream is None:
+        r = (_quick_module or _quick()).linear_lora(x, w, a, b, adapter, scale, out, workspace)
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "linear_lora")
+            return r
     bf16 = torch.bfloat16
     M, K, dev = _dims(x, "x", bf16)
     N = _out_rows(w, "w")
@@ -816,6 +829,12 @@ def moe_glu(h, router_w, gate_w, up_w, down_w, top_k, renormalize=True, out=None
     down_w[e].T.  router_w is [E,K], gate_w and up_w [E,N,K], down_w [E,K,N].
     The workspace (new_moe_workspace(T, E, top_k, N, K), which a decode loop keeps)
     is allocated and its counters are zeroed here when not given.  No gradients."""
+    if stream is None:
+        r = (_quick_module or _quick()).moe_glu(h, router_w, gate_w, up_w, down_w, top_k, bool(renormalize), out, ids, weights, workspace)
+        if r is not None:
+            if type(r) is int:
+                raise MbgluError(r, "moe_glu")
+            return r
     bf16 = torch.bfloat16
     T, K, dev = _dims(h, "h", bf16)
     if T > MAX_M:

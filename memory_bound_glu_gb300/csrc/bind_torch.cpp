@@ -1,5 +1,5 @@
-// bind_torch.cpp -- the common case of the binding's wide and e4m3 calls: 2-D
-// tensors of the right type, shape and device, on the current device's current
+// bind_torch.cpp -- the common case of the binding's wide and e4m3 calls, and of
+// those whose rows choose weights of their own: tensors of the right type, shape and device, on the current device's current
 // stream.  Marshalling only, as binding.py, whose argument checks take longer
 // than a decode step's kernels.  A call that is not the common case returns
 // None and binding.py does it, with its own checks and errors.
@@ -30,6 +30,11 @@ decltype(&::add_rmsnorm_fp8) f_norm = nullptr;
 decltype(&::glu_fp8) f_glu = nullptr;
 decltype(&::matmul_fp8) f_matmul = nullptr;
 decltype(&::matmul_fp8_workspace_bytes) f_matmul_ws = nullptr;
+decltype(&::glu_lora) f_glu_lora = nullptr;
+decltype(&::glu_lora_workspace_bytes) f_glu_lora_ws = nullptr;
+decltype(&::linear_lora) f_linear_lora = nullptr;
+decltype(&::linear_lora_workspace_bytes) f_linear_lora_ws = nullptr;
+decltype(&::moe_glu) f_moe = nullptr;
 
 constexpr ScalarType kBf16 = ScalarType::BFloat16, kE4m3 = ScalarType::Float8_e4m3fn, kF32 = ScalarType::Float;
 
@@ -353,15 +358,179 @@ PyObject *py_matmul(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// A 3-D bf16 tensor [count, rows, cols]: its address and strides.
+bool stack(PyObject *o, int64_t count, int64_t rows, int64_t cols, int device, Operand &out, int64_t &outer)
+{
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.get_device() != device || t.dim() != 3 || t.scalar_type() != kBf16 || t.size(0) != count ||
+        t.size(1) != rows || t.size(2) != cols || t.stride(2) != 1)
+        return false;
+    out.p = t.data_ptr();
+    out.ld = rows > 1 ? t.stride(1) : cols;
+    outer = count > 1 ? t.stride(0) : rows * out.ld;
+    return true;
+}
+
+bool vector(PyObject *o, ScalarType type, int64_t n, int device, void *&p)
+{
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.get_device() != device || t.dim() != 1 || t.scalar_type() != type || t.size(0) != n || !t.is_contiguous())
+        return false;
+    p = t.data_ptr();
+    return true;
+}
+
+// The workspace at `given`, or a new one of `need` bytes (kept alive in `made`).
+bool workspace(PyObject *given, size_t need, int device, void *&p, size_t &bytes, at::Tensor &made)
+{
+    if (given == Py_None) {
+        if (need) made = empty(1, static_cast<int64_t>(need), ScalarType::Byte, device);
+        p = need ? made.data_ptr() : nullptr;
+        bytes = need;
+        return true;
+    }
+    if (!THPVariable_Check(given)) return false;
+    const at::Tensor &t = THPVariable_Unpack(given);
+    if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous()) return false;
+    p = t.data_ptr();
+    bytes = t.nbytes();
+    return true;
+}
+
+// (count, R) of A [count, R, K]
+bool ranks(PyObject *o, int64_t &count, int64_t &R)
+{
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (t.dim() != 3) return false;
+    count = t.size(0);
+    R = t.size(1);
+    return count <= INT32_MAX - 511 && R <= MBGLU_LORA_MAX_RANK;
+}
+
+bool adapters(PyObject *a, PyObject *b, int64_t N, int64_t K, int64_t count, int64_t R, int device, mbglu_adapters &out)
+{
+    Operand x, y;
+    if (!stack(a, count, R, K, device, x, out.a_adapter) || !stack(b, count, N, R, device, y, out.b_adapter)) return false;
+    out.a = static_cast<mbglu_bf16 *>(x.p);
+    out.lda = x.ld;
+    out.b = static_cast<mbglu_bf16 *>(y.p);
+    out.ldb = y.ld;
+    return true;
+}
+
+// (h, gate_w, up_w, gate_a, gate_b, up_a, up_b, adapter, scale, out, mode, workspace)
+PyObject *py_glu_lora(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        int64_t M, K, N, K2, count, R;
+        int dev, dev2;
+        if (n != 12 || !first(a[0], kBf16, M, K, dev) || !first(a[1], kBf16, N, K2, dev2) || !ranks(a[3], count, R)) Py_RETURN_NONE;
+        Operand h, g, u, o;
+        mbglu_adapters ga, ua;
+        void *index = nullptr, *scale = nullptr, *ws = nullptr;
+        size_t bytes = 0;
+        at::Tensor made, scratch;
+        if (!operand(a[0], kBf16, M, K, dev, h) || !operand(a[1], kBf16, N, K, dev, g) || !operand(a[2], kBf16, N, K, dev, u) ||
+            !adapters(a[3], a[4], N, K, count, R, dev, ga) || !adapters(a[5], a[6], N, K, count, R, dev, ua) ||
+            !vector(a[7], ScalarType::Int, M, dev, index) || (a[8] != Py_None && !vector(a[8], kF32, count, dev, scale)))
+            Py_RETURN_NONE;
+        const size_t need = a[11] == Py_None ? f_glu_lora_ws(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
+                                                            static_cast<int>(count), static_cast<int>(R))
+                                             : 0;
+        if (!workspace(a[11], need, dev, ws, bytes, scratch) || !output(a[9], kBf16, M, N, dev, o, made)) Py_RETURN_NONE;
+        const long mode = PyLong_AsLong(a[10]);
+        const mbglu_status st = f_glu_lora(
+            static_cast<mbglu_bf16 *>(h.p), h.ld, static_cast<mbglu_bf16 *>(g.p), g.ld, static_cast<mbglu_bf16 *>(u.p), u.ld, &ga, &ua,
+            static_cast<int32_t *>(index), static_cast<float *>(scale), static_cast<mbglu_bf16 *>(o.p), o.ld, static_cast<int>(M),
+            static_cast<int>(N), static_cast<int>(K), static_cast<int>(count), static_cast<int>(R), static_cast<mbglu_mode>(mode), ws,
+            bytes, stream_of(dev));
+        return st ? status(st) : result(a[9], made);
+    });
+}
+
+// (x, w, a, b, adapter, scale, out, workspace)
+PyObject *py_linear_lora(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        int64_t M, K, N, K2, count, R;
+        int dev, dev2;
+        if (n != 8 || !first(a[0], kBf16, M, K, dev) || !first(a[1], kBf16, N, K2, dev2) || !ranks(a[2], count, R)) Py_RETURN_NONE;
+        Operand x, w, o;
+        mbglu_adapters ab;
+        void *index = nullptr, *scale = nullptr, *ws = nullptr;
+        size_t bytes = 0;
+        at::Tensor made, scratch;
+        if (!operand(a[0], kBf16, M, K, dev, x) || !operand(a[1], kBf16, N, K, dev, w) ||
+            !adapters(a[2], a[3], N, K, count, R, dev, ab) || !vector(a[4], ScalarType::Int, M, dev, index) ||
+            (a[5] != Py_None && !vector(a[5], kF32, count, dev, scale)))
+            Py_RETURN_NONE;
+        const size_t need = a[7] == Py_None ? f_linear_lora_ws(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
+                                                              static_cast<int>(count), static_cast<int>(R))
+                                            : 0;
+        if (!workspace(a[7], need, dev, ws, bytes, scratch) || !output(a[6], kBf16, M, N, dev, o, made)) Py_RETURN_NONE;
+        const mbglu_status st =
+            f_linear_lora(static_cast<mbglu_bf16 *>(x.p), x.ld, static_cast<mbglu_bf16 *>(w.p), w.ld, &ab, static_cast<int32_t *>(index),
+                          static_cast<float *>(scale), static_cast<mbglu_bf16 *>(o.p), o.ld, static_cast<int>(M), static_cast<int>(N),
+                          static_cast<int>(K), static_cast<int>(count), static_cast<int>(R), ws, bytes, stream_of(dev));
+        return st ? status(st) : result(a[6], made);
+    });
+}
+
+// (h, router_w, gate_w, up_w, down_w, top_k, renormalize, out, ids, weights, workspace): with a workspace
+PyObject *py_moe(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        int64_t T, K, E, K2, N;
+        int dev, dev2;
+        if (n != 11 || a[10] == Py_None || !PyLong_CheckExact(a[5]) || !first(a[0], kBf16, T, K, dev) || !first(a[1], kBf16, E, K2, dev2) ||
+            !THPVariable_Check(a[2]) || THPVariable_Unpack(a[2]).dim() != 3)
+            Py_RETURN_NONE;
+        N = THPVariable_Unpack(a[2]).size(1);
+        const long k = PyLong_AsLong(a[5]);
+        if (PyErr_Occurred()) {   // beyond a long: the checks in Python say so
+            PyErr_Clear();
+            Py_RETURN_NONE;
+        }
+        if (T > MBGLU_MAX_M || E < 1 || E > MBGLU_MOE_MAX_EXPERTS || k < 1 || k > E || k > MBGLU_MOE_MAX_TOP_K || N > INT32_MAX - 511)
+            Py_RETURN_NONE;
+        Operand h, r, g, u, d, o, ids, w;
+        int64_t ge, ue, de;
+        void *ws = nullptr;
+        size_t bytes = 0;
+        at::Tensor made, made_ids, made_w, scratch;
+        if (!operand(a[0], kBf16, T, K, dev, h) || !operand(a[1], kBf16, E, K, dev, r) || !stack(a[2], E, N, K, dev, g, ge) ||
+            !stack(a[3], E, N, K, dev, u, ue) || !stack(a[4], E, K, N, dev, d, de) || !workspace(a[10], 0, dev, ws, bytes, scratch) ||
+            !output(a[7], kBf16, T, K, dev, o, made) || !output(a[8], ScalarType::Int, T, k, dev, ids, made_ids) ||
+            !output(a[9], kF32, T, k, dev, w, made_w) || ids.ld != k || w.ld != k)
+            Py_RETURN_NONE;
+        const mbglu_status st = f_moe(
+            static_cast<mbglu_bf16 *>(h.p), h.ld, static_cast<mbglu_bf16 *>(r.p), r.ld, static_cast<mbglu_bf16 *>(g.p), ge, g.ld,
+            static_cast<mbglu_bf16 *>(u.p), ue, u.ld, static_cast<mbglu_bf16 *>(d.p), de, d.ld, static_cast<mbglu_bf16 *>(o.p), o.ld,
+            static_cast<int32_t *>(ids.p), static_cast<float *>(w.p), static_cast<int>(T), static_cast<int>(E), static_cast<int>(k),
+            static_cast<int>(N), static_cast<int>(K), a[6] == Py_True, ws, bytes, stream_of(dev));
+        if (st) return status(st);
+        PyObject *x = result(a[7], made), *y = result(a[8], made_ids), *z = result(a[9], made_w);
+        PyObject *t = x && y && z ? PyTuple_Pack(3, x, y, z) : nullptr;
+        Py_XDECREF(x);
+        Py_XDECREF(y);
+        Py_XDECREF(z);
+        return t;
+    });
+}
+
 // The addresses of the library's entry points, in this order.
 PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 7) {
-        PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
+    constexpr int kEntries = 12;
+    if (n != kEntries) {
+        PyErr_SetString(PyExc_TypeError, "bind takes twelve addresses");
         return nullptr;
     }
-    void *p[7];
-    for (int i = 0; i < 7; ++i) {
+    void *p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
@@ -375,6 +544,11 @@ PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     f_glu = reinterpret_cast<decltype(f_glu)>(p[4]);
     f_matmul = reinterpret_cast<decltype(f_matmul)>(p[5]);
     f_matmul_ws = reinterpret_cast<decltype(f_matmul_ws)>(p[6]);
+    f_glu_lora = reinterpret_cast<decltype(f_glu_lora)>(p[7]);
+    f_glu_lora_ws = reinterpret_cast<decltype(f_glu_lora_ws)>(p[8]);
+    f_linear_lora = reinterpret_cast<decltype(f_linear_lora)>(p[9]);
+    f_linear_lora_ws = reinterpret_cast<decltype(f_linear_lora_ws)>(p[10]);
+    f_moe = reinterpret_cast<decltype(f_moe)>(p[11]);
     Py_RETURN_NONE;
 }
 
@@ -384,6 +558,8 @@ PyMethodDef methods[] = {
     MBGLU_METHOD("wide_glu", py_wide_glu),
     MBGLU_METHOD("glu_gemm_backward", py_gemm_backward), MBGLU_METHOD("add_rmsnorm_fp8", py_norm),
     MBGLU_METHOD("glu_fp8", py_glu),       MBGLU_METHOD("matmul_fp8", py_matmul),
+    MBGLU_METHOD("glu_lora", py_glu_lora), MBGLU_METHOD("linear_lora", py_linear_lora),
+    MBGLU_METHOD("moe_glu", py_moe),
     {nullptr, nullptr, 0, nullptr}};
 
 // MBGLU_BUILT_FOR: the torch and the Python whose headers this was compiled with
