@@ -185,11 +185,17 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
     if (!encode_tile_map(&maps.x, l.x, l.ldx, l.M, l.K, 64, p.plan.tn / 2, 2)) return MBGLU_OK;
     if (adapted) {
         const int width = SIDES * l.R;
+        // few rows: p is formed beside the products where that costs a block no more than some
+        // rounds of loads (units of eight values)
+        if (l.M <= kFewRows && !whole && static_cast<int64_t>(l.M) * width <= 8 * 4 * 2 * kPairs)
+            p.inside = mbglu::kInsideShared;
+        else if (p.plan.rest == 0 && static_cast<int64_t>(l.M) * width <= mbglu::kInsideMost)
+            p.inside = mbglu::kInsideEach;
         p.l.p = reinterpret_cast<float *>(ws);
         p.l.terms = reinterpret_cast<uint16_t *>(ws + space.terms);
         p.part = reinterpret_cast<float *>(ws + space.part);
         p.prefetch = l.M <= kFewRows;
-        if (whole) {   // tiles in ranges leave the adapters' term to the join
+        if (whole && p.inside == mbglu::kInsideNo) {   // tiles in ranges leave the adapters' term to the join
             p.l.blocks = reinterpret_cast<int32_t *>(ws + space.blocks);
             for (int d = 0; d < SIDES; ++d) {
                 const mbglu::LoraSide &s = l.side[d];
@@ -206,7 +212,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
     mbglu_status st = table.get(&sms, setup_pair<SIDES>);
     if (st != MBGLU_OK) return st;
     *taken = true;
-    if (adapted) {
+    if (adapted && p.inside == mbglu::kInsideNo) {
         // few rows: a block per adapter of a group and 8 columns; many: columns together, so
         // that the rows are read once or twice
         p.early = launch_policy() != MBGLU_POLICY_SERIAL;

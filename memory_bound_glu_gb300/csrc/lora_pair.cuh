@@ -15,6 +15,10 @@
 // A prompt's rows are nearly all of the first kind, a chunk of many short requests has the
 // second.
 //
+// For few rows no kernel of its own forms p: the epilogue's warps do, while the products run
+// (lora_dot8).  Where the join uses p, the blocks share the work; where a block needs it itself
+// and it is small (a token or some), every block forms all of it from L2.
+//
 // Tiles that would leave SM pairs without work are cut along the inner dimension: their
 // ranges leave partial sums, and lora_join_kernel adds them, the adapters' term and the
 // epilogue.  There a lane has one output and reads its row of B, the term in fp32 FMAs.
@@ -33,6 +37,9 @@ struct LoraPlan {
     int nchunk;
 };
 
+enum LoraInside { kInsideNo = 0, kInsideEach = 1, kInsideShared = 2 };   // a kernel before, each block all, the blocks together
+constexpr int kInsideMost = 64;   // values of p that each block forms for itself
+
 struct LoraMaps {
     TensorMap w[2], x;
     TensorMap b[2];          // [adapters][N][R]
@@ -44,6 +51,7 @@ struct LoraPairParams {
     LoraPlan plan;
     float *part;             // [rest splits][tn][256]: a range's accumulators, token by token
     int prefetch;            // B into L2 ahead
+    int inside;              // who forms p: LoraInside
     int early;               // the kernel before this one has waited for the operands
 };
 
@@ -215,10 +223,84 @@ __device__ __forceinline__ void lora_term(const LoraParams &p, int d, int sides,
     }
 }
 
+// Eight columns of p[m] from j0 on (adapter a, before its scale), summed over steps s0 .. s1 - 1
+// of 256; a warp, every lane gets the sums.
+__device__ __forceinline__ void lora_dot8(const LoraParams &p, int d, int64_t m, int a, int j0, int s0, int s1, float (&sum)[8])
+{
+    const int lane = threadIdx.x & 31;
+    const LoraSide &side = p.side[d];
+    const uint16_t *x = p.x + m * p.ldx, *w = side.a + a * side.a_adapter + j0 * side.lda;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+#pragma unroll 2
+    for (int s = s0; s < s1; ++s) {
+        const int k = s * 256 + lane * 8;
+        const bool in = k < p.K;
+        const uint4 v = in ? *reinterpret_cast<const uint4 *>(x + k) : make_uint4(0, 0, 0, 0);
+        uint4 r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = in ? *reinterpret_cast<const uint4 *>(w + i * side.lda + k) : make_uint4(0, 0, 0, 0);
+        const float4 lo = make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+        const float4 hi = make_float4(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = dot8(r[i], lo, hi, sum[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+}
+
+// The epilogue's eight warps (me: 0 to 7) form p: all of it at `mine`, laid out as p.p; or the
+// block's share at p.p.  scratch: 2 x 8 x 8 floats.
+template <int SIDES>
+__device__ __forceinline__ void lora_inside(const LoraParams &p, int inside, int me, float *mine, float *scratch)
+{
+    const int lane = threadIdx.x & 31, per = SIDES * p.R / 8, steps = (p.K + 255) / 256;   // units of 8 columns of a row
+    const int64_t units = static_cast<int64_t>(p.M) * per;
+    float sum[8];
+    if (inside == kInsideEach) {   // a warp per unit
+        for (int64_t u = me; u < units; u += 8) {
+            const int64_t m = u / per;
+            const int j = static_cast<int>(u % per) * 8, a = lora_adapter(p, m);
+            if (a < 0) continue;
+            const int d = SIDES == 2 && j >= p.R ? 1 : 0;
+            lora_dot8(p, d, m, a, j - d * p.R, 0, steps, sum);
+            const float scale = p.scale ? p.scale[a] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (lane == i) mine[m * SIDES * p.R + j + i] = sum[i] * scale;
+        }
+        bar_sync_named(6, 256);
+        return;
+    }
+    uint32_t turn = 0;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {   // the warps share a unit's columns
+        const int64_t m = u / per;
+        const int j = static_cast<int>(u % per) * 8, a = lora_adapter(p, m);
+        if (a < 0) continue;   // the whole block
+        const int d = SIDES == 2 && j >= p.R ? 1 : 0;
+        const float scale = p.scale ? p.scale[a] : 1.0f;
+        lora_dot8(p, d, m, a, j - d * p.R, steps * me / 8, steps * (me + 1) / 8, sum);
+        float *at = scratch + (turn++ & 1) * 64;   // written again only after the barrier behind which it was read
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (lane == i) at[me * 8 + i] = sum[i];
+        bar_sync_named(6, 256);
+        if (me == 0 && lane < 8) {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v += at[i * 8 + lane];
+            p.p[m * SIDES * p.R + j + lane] = v * scale;
+        }
+    }
+}
+
 // The same for rows that mostly have an adapter each: a lane has one output n, reads its row
 // of each token's B, eight tokens' together, and adds the term to y.  p of 16 tokens and 16
 // columns is staged in shared memory (stage, 256 floats), on the way beside B.
-__device__ __forceinline__ void lora_term_rows(const LoraParams &p, int d, int sides, int64_t m0, int64_t n, float *stage, float (&y)[16])
+__device__ __forceinline__ void lora_term_rows(const LoraParams &p, const float *all_p, int d, int sides, int64_t m0, int64_t n, float *stage,
+                                               float (&y)[16])
 {
     const int lane = threadIdx.x & 31, R = p.R;
     const int mine = lane < 16 ? lora_adapter(p, m0 + lane) : -1;
@@ -226,7 +308,7 @@ __device__ __forceinline__ void lora_term_rows(const LoraParams &p, int d, int s
     const LoraSide &side = p.side[d];
     // this lane stages 8 columns of token lane / 2
     const bool has = used >> (lane >> 1) & 1u;
-    const float *q = p.p + (m0 + (lane >> 1)) * sides * R + d * R + (lane & 1) * 8;
+    const float *q = all_p + (m0 + (lane >> 1)) * sides * R + d * R + (lane & 1) * 8;
     float4 *mystage = reinterpret_cast<float4 *>(stage + lane * 8);
     for (int j = 0; j < R; j += 16) {
         const bool in = has && j + (lane & 1) * 8 < R;
@@ -262,6 +344,7 @@ __device__ __forceinline__ void lora_term_rows(const LoraParams &p, int d, int s
 
 // The exchange between the two warps of an output's g and u (as pair_tall.cuh), then the
 // warps' terms.
+static_assert(kPairExchange + (kInsideMost + 128) * 4 <= kPairHeader, "p and its scratch lie behind the barriers");
 constexpr int kLoraSwap = 2 * 16 * 32;
 constexpr uint32_t kLoraExtra = 4 * kLoraSwap * 4 + 8 * kTermWords * 4;
 constexpr uint32_t kLoraSmem = kPairHeader + kPairStages * kPairStage + kLoraExtra + 1024;
@@ -432,6 +515,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
         float *extra = reinterpret_cast<float *>(s.row_bufs);
         float *swap = extra + pairing * kLoraSwap + lane, *term = extra + 4 * kLoraSwap + (warp - kPairEpilogue) * kTermWords;
         const int row0 = SIDES == 2 ? (q & 1) * 32 : q * 32;   // the warp's first output of the CTA's
+        const float *all_p = p.l.p;
+        if constexpr (ROWS) {
+            if (p.inside != kInsideNo) lora_inside<SIDES>(p.l, p.inside, warp - kPairEpilogue, s.exchange, s.exchange + kInsideMost);
+            if (p.inside == kInsideEach) all_p = s.exchange;
+        }
         uint32_t v = 0, sets = 0;
         for (int i = first; i < plan.items; i += step, ++v) {
             const LoraTile x = lora_tile(plan, i);
@@ -462,9 +550,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 float y[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(r[k]);
-                if (p.l.blocks && tokens > 0 && __ldcg(p.l.blocks + (m0 + j) / kLoraBlock) == kMixed) {
+                if (tokens > 0 && (p.inside == kInsideEach || (p.l.blocks && __ldcg(p.l.blocks + (m0 + j) / kLoraBlock) == kMixed))) {
                     if constexpr (ROWS)
-                        lora_term_rows(p.l, d, SIDES, static_cast<int64_t>(m0) + j, n, term, y);
+                        lora_term_rows(p.l, all_p, d, SIDES, static_cast<int64_t>(m0) + j, n, term, y);
                     else
                         lora_term(p.l, d, SIDES, static_cast<int64_t>(m0) + j, n0, term, [&](int g) {
 #pragma unroll
