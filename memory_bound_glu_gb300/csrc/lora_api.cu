@@ -127,7 +127,7 @@ mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *tak
     const uint32_t stage = mbglu::shrink_tc_stage(SIDES * p.R);
     q.stages = std::min<int>(mbglu::kShrinkTcMaxStages, (200 * 1024) / static_cast<int>(stage));
     *taken = true;
-    Launch l(dim3(static_cast<unsigned>(q.split), static_cast<unsigned>(tiles)), mbglu::kShrinkTcThreads, 2048 + static_cast<size_t>(q.stages) * stage, stream,
+    Launch l(dim3(static_cast<unsigned>(q.split), static_cast<unsigned>(tiles)), mbglu::kShrinkTcThreads, 3072 + static_cast<size_t>(q.stages) * stage, stream,
              q.split);
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::lora_shrink_tc_kernel<SIDES>, q, maps));
 }
@@ -194,7 +194,6 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         p.l.p = reinterpret_cast<float *>(ws);
         p.l.terms = reinterpret_cast<uint16_t *>(ws + space.terms);
         p.part = reinterpret_cast<float *>(ws + space.part);
-        p.prefetch = l.M <= kFewRows;
         if (whole && p.inside == mbglu::kInsideNo) {   // tiles in ranges leave the adapters' term to the join
             p.l.blocks = reinterpret_cast<int32_t *>(ws + space.blocks);
             for (int d = 0; d < SIDES; ++d) {

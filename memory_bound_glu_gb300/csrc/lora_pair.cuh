@@ -50,7 +50,6 @@ struct LoraPairParams {
     LoraParams l;
     LoraPlan plan;
     float *part;             // [rest splits][tn][256]: a range's accumulators, token by token
-    int prefetch;            // B into L2 ahead
     int inside;              // who forms p: LoraInside
     int early;               // the kernel before this one has waited for the operands
 };
@@ -490,15 +489,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 if (buf == 0) acc_phase ^= 1;
             }
         }
-    } else if (warp == 2 && p.l.adapters > 0 && p.prefetch) {
-        // B is read row by row at the end, where nothing hides the way: its bytes come into L2
-        // beside the weights, whose copies leave room for them
+    } else if (warp == 2 && p.l.adapters > 0) {
+        // B is read row by row at the end, where nothing hides the way, but for blocks of one
+        // adapter: its bytes come into L2 beside the weights, whose copies leave room for them
         for (int i = first; i < plan.whole + plan.rest; i += step) {
             const LoraTile x = lora_tile(plan, i);
             const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2), rows = min(plan.wt / 2, p.l.N - n0);
-            for (int m = x.t % plan.ttiles * plan.tn + lane, k = lane; k < plan.tn && rows > 0; k += 32, m += 32) {
-                const int a = lora_adapter(p.l, m);
-                if (a < 0) continue;
+            const int m0 = x.t % plan.ttiles * plan.tn;
+            for (int k = 0; k < plan.tn && m0 + k < p.l.M && rows > 0; k += 32) {
+                const int m = m0 + k + lane, a = lora_adapter(p.l, m);
+                const int head = __shfl_sync(0xffffffffu, a, 0), before = __shfl_up_sync(0xffffffffu, a, 1);
+                if (p.l.blocks && x.slot < 0 && __all_sync(0xffffffffu, a == head || m >= p.l.M)) continue;
+                if (a < 0 || (lane > 0 && a == before)) continue;
 #pragma unroll
                 for (int d = 0; d < SIDES; ++d) {
                     const LoraSide &side = p.l.side[d];

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
             const uint32_t rows = __ballot_sync(0xffffffffu, mine == a);
             left &= ~rows;
             if (nth % gridDim.z != blockIdx.z) continue;
+            const float scale = p.scale ? p.scale[a] : 1.0f;
             float acc[MT][NT][4] = {};
             const uint16_t *w = side.a + a * side.a_adapter + (j0 + row) * side.lda;
             const uint16_t *x = p.x + (m0 + row) * p.ldx;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
                 }
             __syncthreads();
             const auto put = [&](int r, int j, float v) {
-                v *= p.scale ? p.scale[a] : 1.0f;
+                v *= scale;
                 const int64_t at = (m0 + r) * width + which * p.R + j0 + j;
                 p.p[at] = v;
                 const uint16_t hi = f32_to_bf16(v);

@@ -70,7 +70,9 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
     uint64_t *full = reinterpret_cast<uint64_t *>(base), *empty = full + kShrinkTcMaxStages;
     uint64_t *acc_full = empty + kShrinkTcMaxStages, *acc_empty = acc_full + 2, *done = acc_empty + 2;
     uint32_t *slot = reinterpret_cast<uint32_t *>(done + 1);
-    unsigned char *ring = base + 1024;
+    float *scales = reinterpret_cast<float *>(base + 512);   // of the rows; 0 where none is used
+    int *ids = reinterpret_cast<int *>(base + 1024);
+    unsigned char *ring = base + 2048;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int R = p.l.R, width = SIDES * R, rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const uint32_t stage = shrink_tc_stage(width);
@@ -174,6 +176,8 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
         LoraDistinct adapters(p.l, m0);
         const int q = warp & 3, row = q * 32 + lane;
         const int mine = lora_adapter(p.l, m0 + row);
+        ids[row] = mine;
+        scales[row] = mine >= 0 ? (p.l.scale ? p.l.scale[mine] : 1.0f) : 0.0f;
         if (p.l.blocks && rank == 0) {   // the table: a warp has 32 rows
             const uint32_t in = __ballot_sync(0xffffffffu, m0 + row < p.l.M);
             const int first = __shfl_sync(0xffffffffu, mine, 0);
@@ -217,29 +221,39 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    // this block's rows of the tile; a thread has four columns at a time
+    // this block's rows of the tile; a thread has four columns of two rows at a time, whose parts
+    // are on the way together
     const int rows = kShrinkTcRows / p.split, quads = width / 4;
-    for (int e = threadIdx.x; e < rows * quads; e += kShrinkTcThreads) {
-        const int64_t m = m0 + rank * rows + e / quads;
-        const int j = e % quads * 4, a = lora_adapter(p.l, m);
-        if (a < 0) continue;
-        float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int i = 0; i < p.split; ++i) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part + (static_cast<int64_t>(i) * p.l.M + m) * width + j));
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
+    const int64_t stride = p.l.M * static_cast<int64_t>(width);
+    for (int e0 = threadIdx.x; e0 < rows * quads; e0 += 2 * kShrinkTcThreads) {
+        float4 v[2];
+        int row[2];
+        int64_t at[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = e0 + h * kShrinkTcThreads, r = rank * rows + e / quads;
+            row[h] = e < rows * quads && ids[r] >= 0 ? r : -1;
+            at[h] = (m0 + r) * width + e % quads * 4;
+            v[h] = make_float4(0, 0, 0, 0);
         }
-        const float s = p.l.scale ? p.l.scale[a] : 1.0f;
-        v = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
-        const int64_t at = m * width + j;
-        *reinterpret_cast<float4 *>(p.l.p + at) = v;
-        const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
-        *reinterpret_cast<uint2 *>(p.l.terms + at) = make_uint2(h0, h1);
-        *reinterpret_cast<uint2 *>(p.l.terms + at + p.l.M * static_cast<int64_t>(width)) =
-            make_uint2(pack_bf16x2(v.x - bf16_lo(h0), v.y - bf16_hi(h0)), pack_bf16x2(v.z - bf16_lo(h1), v.w - bf16_hi(h1)));
+#pragma unroll 8
+        for (int i = 0; i < p.split; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 x = row[h] >= 0 ? __ldcg(reinterpret_cast<const float4 *>(p.part + i * stride + at[h])) : make_float4(0, 0, 0, 0);
+                v[h] = make_float4(v[h].x + x.x, v[h].y + x.y, v[h].z + x.z, v[h].w + x.w);
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (row[h] < 0) continue;
+            const float s = scales[row[h]];
+            const float4 w = make_float4(v[h].x * s, v[h].y * s, v[h].z * s, v[h].w * s);
+            *reinterpret_cast<float4 *>(p.l.p + at[h]) = w;
+            const uint32_t h0 = pack_bf16x2(w.x, w.y), h1 = pack_bf16x2(w.z, w.w);
+            *reinterpret_cast<uint2 *>(p.l.terms + at[h]) = make_uint2(h0, h1);
+            *reinterpret_cast<uint2 *>(p.l.terms + at[h] + stride) =
+                make_uint2(pack_bf16x2(w.x - bf16_lo(h0), w.y - bf16_hi(h0)), pack_bf16x2(w.z - bf16_lo(h1), w.w - bf16_hi(h1)));
+        }
     }
 }
 
