@@ -16,14 +16,21 @@ using namespace mbglu_host;
 constexpr int64_t kAlign = 256;
 int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
-// Up to this many rows the rows of a block with several adapters are taken to have one each,
-// as those of a decode batch mostly do.
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 64;   // a decode batch
+
+// Who adds the terms of rows with adapters of their own (us at K = 2560, N = 9728, two projections):
+//   up to rank 16 the epilogue, a row of B per lane: at 100 rows of as many requests 40, on the
+//   tensor cores (lora_term) 59; at 500 rows of 60 requests 70 and 78; at rank 64 113 there and
+//   363 by rows;
+//   a decode batch's larger ranks the join, which has more warps: at 48 rows of rank 64 57, in
+//   the epilogue 83; of rank 32 36 and 47; at rank 16 it is the other way round, 33 and 31.
+bool by_rows(int M, int R) { return M <= kFewRows || (M < 512 && R <= 16); }
+bool by_join(int sides, int M, int R) { return M >= 2 && M <= kFewRows && R > 16 && M * sides * R > mbglu::kInsideMost; }
 
 // Tiles and ranges, from the sizes alone.  The estimate (ns) of a tile's time is
-// tall_tokens' (gemm_api.cu); a join costs its launch and the partial sums' way to L2 and
-// back.
-mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, bool may_split)
+// tall_tokens' (gemm_api.cu); a join costs its launch, the partial sums' way to L2 and
+// back and the adapters' terms (500 x 2560 outputs of R = 32: 24 us).
+mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, int R, bool may_split)
 {
     mbglu::LoraPlan best = {};
     double least = 0;
@@ -33,14 +40,15 @@ mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, bool may_split)
         const int64_t tiles = static_cast<int64_t>(nt) * ceil_div(M, tn);
         if (tiles > INT32_MAX / 16) continue;
         const auto tile_ns = [&](int64_t at_once, int64_t n) { return n * (77.0 + 59.0 * std::min<int64_t>(at_once, kPairs) / kPairs + 0.7 * tn) + 15.5 * tn; };
+        const bool join = may_split && by_join(sides, M, R);
         for (int split = 0; split < 2; ++split) {
-            const int64_t left = tiles % kPairs;
+            const int64_t left = join ? tiles : tiles % kPairs;
             const int64_t s = split && left > 0 ? std::min<int64_t>({std::max<int64_t>(kPairs / left, 1), std::max(chunks / 8, 1), 16}) : 1;
             if (split && !may_split) continue;
-            if (split && s < 2) continue;
+            if (join ? !split : split && s < 2) continue;
             const int64_t whole = split ? tiles - left : tiles;
             double ns = (whole + kPairs - 1) / kPairs * tile_ns(whole, chunks);
-            if (split) ns += (left * s + kPairs - 1) / kPairs * tile_ns(left * s, (chunks + s - 1) / s) + 3000 + left * s * tn * 2048.0 / 4000;
+            if (split) ns += (left * s + kPairs - 1) / kPairs * tile_ns(left * s, (chunks + s - 1) / s) + 3000 + left * s * tn * 2048.0 / 4000 + left * tn * 4;
             if (least == 0 || ns < least) {
                 least = ns;
                 best.tn = tn;
@@ -62,8 +70,10 @@ int64_t lora_p_bytes(int sides, int M, int R) { return padded(static_cast<int64_
 
 int64_t lora_part_bytes(const mbglu::LoraPlan &q) { return static_cast<int64_t>(q.rest) * q.splits * q.tn * 1024; }
 
-// From this many rows on p comes from lora_shrink_tc_kernel.
-constexpr int kShrinkTcFrom = 1024, kShrinkTcSplit = 8;
+// From this many rows on p comes from lora_shrink_tc_kernel: at 500 rows of 60 requests, K =
+// 9728, the whole call takes 66 us with it and 70 without, at 1000 of 10, K = 2560, 95 and 99;
+// at 333 rows of 37 31 and 23.
+constexpr int kShrinkTcFrom = 512, kShrinkTcSplit = 8;
 
 // Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, partial sums
 struct LoraSpace {
@@ -81,7 +91,7 @@ LoraSpace lora_space(int sides, int M, int R, const mbglu::LoraPlan &plan)
     return s;
 }
 
-int64_t lora_bytes(int sides, int M, int N, int K, int R) { return lora_space(sides, M, R, lora_plan(sides, M, N, K, true)).bytes; }
+int64_t lora_bytes(int sides, int M, int N, int K, int R) { return lora_space(sides, M, R, lora_plan(sides, M, N, K, R, true)).bytes; }
 
 bool bad_rank(int adapters, int R) { return adapters < 0 || adapters > kMostSize || R < 0 || R > MBGLU_LORA_MAX_RANK; }
 
@@ -135,20 +145,35 @@ mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *tak
 template <int SIDES>
 cudaError_t setup_pair()
 {
-    cudaError_t e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(mbglu::lora_pair_kernel<SIDES, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
+    cudaError_t e = cudaSuccess;
+    for (const auto kernel : {mbglu::lora_pair_kernel<SIDES, false>, mbglu::lora_pair_kernel<SIDES, true>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kLoraSmem));
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mbglu::lora_shrink_tc_kernel<SIDES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 204 * 1024);
     return e;
 }
 
-template <int SIDES, int TOKENS>
+template <int SIDES, int TOKENS, int LANES>
 mbglu_status launch_join(const mbglu::LoraPairParams &p, cudaStream_t stream)
 {
     const int64_t warps = static_cast<int64_t>(p.plan.rest) * ceil_div(p.plan.wt, 32) * (p.plan.tn / TOKENS);
     Launch j(dim3(static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, 1 << 20))), 256, 0, stream);
-    return launched(cudaLaunchKernelEx(&j.cfg, mbglu::lora_join_kernel<SIDES, TOKENS>, p));
+    return launched(cudaLaunchKernelEx(&j.cfg, mbglu::lora_join_kernel<SIDES, TOKENS, LANES>, p));
+}
+
+template <int SIDES>
+mbglu_status launch_join(const mbglu::LoraPairParams &p, cudaStream_t stream)
+{
+    const int R = p.l.R;
+    if (p.l.M <= 16) {   // more warps, each with less
+        if (R <= 16) return launch_join<SIDES, 1, 2>(p, stream);
+        if (R <= 32) return launch_join<SIDES, 1, 4>(p, stream);
+    } else {
+        if (R <= 16) return launch_join<SIDES, 2, 2>(p, stream);
+        if (R <= 32) return launch_join<SIDES, 2, 4>(p, stream);
+    }
+    if (R <= 64) return launch_join<SIDES, 1, 8>(p, stream);
+    return launch_join<SIDES, 1, 16>(p, stream);
 }
 
 // Operands that the CTA-pair kernel and lora_shrink_kernel take.
@@ -174,7 +199,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
     if (!fast_operands(l, SIDES)) return MBGLU_OK;
     mbglu::LoraPairParams p = {};
     p.l = l;
-    p.plan = lora_plan(SIDES, l.M, l.N, l.K, l.adapters > 0);
+    p.plan = lora_plan(SIDES, l.M, l.N, l.K, l.R, l.adapters > 0);
     if (p.plan.ntiles == 0) return MBGLU_OK;
     char *ws = static_cast<char *>(workspace);
     const LoraSpace space = lora_space(SIDES, l.M, l.R, p.plan);
@@ -185,11 +210,14 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
     if (!encode_tile_map(&maps.x, l.x, l.ldx, l.M, l.K, 64, p.plan.tn / 2, 2)) return MBGLU_OK;
     if (adapted) {
         const int width = SIDES * l.R;
+        // 10 MB of B or less (48 rows of rank 32, 60 MB: 40 us with and 36 without; of rank 16 31.5
+        // and 30.7)
+        p.prefetch = static_cast<int64_t>(std::min(l.M, l.adapters)) * l.N * width * 2 <= 10000000;
         // few rows: p is formed beside the products where that costs a block no more than some
         // rounds of loads (units of eight values)
         if (l.M <= kFewRows && !whole && static_cast<int64_t>(l.M) * width <= 8 * 4 * 2 * kPairs)
             p.inside = mbglu::kInsideShared;
-        else if (p.plan.rest == 0 && static_cast<int64_t>(l.M) * width <= mbglu::kInsideMost)
+        else if (by_rows(l.M, l.R) && p.plan.rest == 0 && static_cast<int64_t>(l.M) * width <= mbglu::kInsideMost)
             p.inside = mbglu::kInsideEach;
         p.l.p = reinterpret_cast<float *>(ws);
         p.l.terms = reinterpret_cast<uint16_t *>(ws + space.terms);
@@ -220,14 +248,15 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         if (st == MBGLU_OK && !tc) {
             if (l.M <= kFewRows)
                 st = launch_shrink<SIDES, 1, 1, 5>(p.l, std::min(l.M, 16), 1024, stream);
-            else
-                st = launch_shrink<SIDES, 1, 4, 4>(p.l, l.M <= 1024 ? 8 : 2, 608, stream);
+            else   // blocks without an adapter of theirs leave at once
+                st = launch_shrink<SIDES, 1, 4, 4>(p.l, 8, 608, stream);
         }
         if (st != MBGLU_OK) return st;
     }
     Launch c(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.items))), mbglu::kPairThreads, mbglu::kLoraSmem, stream, 2);
-    st = launched(cudaLaunchKernelEx(&c.cfg, l.M <= kFewRows ? mbglu::lora_pair_kernel<SIDES, true> : mbglu::lora_pair_kernel<SIDES, false>, p, maps));
-    if (st == MBGLU_OK && p.plan.rest > 0) st = l.M <= 16 ? launch_join<SIDES, 1>(p, stream) : launch_join<SIDES, 2>(p, stream);
+    const auto kernel = by_rows(l.M, l.R) ? mbglu::lora_pair_kernel<SIDES, true> : mbglu::lora_pair_kernel<SIDES, false>;
+    st = launched(cudaLaunchKernelEx(&c.cfg, kernel, p, maps));
+    if (st == MBGLU_OK && p.plan.rest > 0) st = launch_join<SIDES>(p, stream);
     return st;
 }
 

@@ -50,6 +50,7 @@ struct LoraPairParams {
     LoraParams l;
     LoraPlan plan;
     float *part;             // [rest splits][tn][256]: a range's accumulators, token by token
+    int prefetch;            // B into L2 ahead
     int inside;              // who forms p: LoraInside
     int early;               // the kernel before this one has waited for the operands
 };
@@ -101,7 +102,7 @@ __device__ __forceinline__ void pair_load_3d(void *dst, const TensorMap *map, in
 // The runs of 32-row blocks (the least that a pair's MMA takes as columns) with one adapter in a tile of tokens; a warp walks them.
 struct LoraRuns {
     int mine, blocks, at, first, adapter;   // run: blocks first .. at - 1
-    __device__ LoraRuns(const LoraParams &p, int m0, int tn)
+    __device__ void load(const LoraParams &p, int m0, int tn)
     {
         const int lane = threadIdx.x & 31;
         blocks = min(tn / kLoraBlock, (p.M - m0 + kLoraBlock - 1) / kLoraBlock);
@@ -121,20 +122,18 @@ struct LoraRuns {
     }
 };
 
-// The adapters' term of 32 outputs from n0 on and 16 tokens from m0 on, a warp; tile(half) is
-// called for each half of the tokens with term[token * kTermPitch + output].
+// The adapters' term of 32 outputs from n0 on and 16 tokens from m0 on, a warp; mine: lanes 0
+// to 15 hold the tokens' adapters, the others -1; tile(half) is called for each half of the tokens with term[token * kTermPitch + output].
 constexpr int kTermPitch = 36;
 constexpr int kTermWords = 8 * kTermPitch;
 template <typename F>
-__device__ __forceinline__ void lora_term(const LoraParams &p, int d, int sides, int64_t m0, int n0, float *term, F tile)
+__device__ __forceinline__ void lora_term(const LoraParams &p, int mine, int d, int sides, int64_t m0, int n0, float *term, F tile)
 {
     const int lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
-    // lanes 0-15 hold the tokens' adapters
-    const int mine = lane < 16 ? lora_adapter(p, m0 + lane) : -1;
     uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
     const bool used[2] = {(left >> row & 1u) != 0, (left >> (8 + row) & 1u) != 0};
     const LoraSide &side = p.side[d];
-    const float *q = p.p + (m0 + row) * sides * p.R + d * p.R + quad * 4;
+    const float *q = p.p + (m0 + row) * sides * p.R + d * p.R + quad * 8;
     const int64_t second = 8 * static_cast<int64_t>(sides) * p.R;
     float sum[2][2][4] = {};   // halves of the tokens, halves of the outputs
     while (left) {
@@ -145,50 +144,54 @@ __device__ __forceinline__ void lora_term(const LoraParams &p, int d, int sides,
         match[0] = __ballot_sync(0xffffffffu, mine == a[0]);
         left &= ~match[0];
         a[1] = __shfl_sync(0xffffffffu, mine, left ? __ffs(left) - 1 : 0);
-        a[1] = left ? a[1] : a[0];
-        match[1] = __ballot_sync(0xffffffffu, mine == a[1]);
+        a[1] = left ? a[1] : -1;
+        match[1] = left ? __ballot_sync(0xffffffffu, mine == a[1]) : 0;
         left &= ~match[1];
         float acc[2][2][2][4] = {};
         const uint16_t *b[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) b[i] = side.b + a[i] * side.b_adapter + (n0 + row) * side.ldb + quad * 4;
-        for (int j0 = 0; j0 < p.R; j0 += 32) {   // two steps' loads together
-            uint2 w[2][2][4];
+        for (int i = 0; i < 2; ++i) b[i] = side.b + a[i] * side.b_adapter + (n0 + row) * side.ldb + quad * 8;
+        // 32 columns, two steps of the tensor cores: a lane reads 16 bytes of a row, eight columns,
+        // the first four for the first step (which column sits where is free, as in the shrink)
+        for (int j = 0; j < p.R; j += 32) {
+            const bool in = j + quad * 8 < p.R;
+            uint4 w[2][4];
             float4 v[2][2];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int j = j0 + c * 16;
-                const bool in = j + quad * 4 < p.R;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int r = 0; r < 4; ++r)
+                    w[i][r] = in && a[i] >= 0 && n0 + row + r * 8 < p.N ? *reinterpret_cast<const uint4 *>(b[i] + r * 8 * side.ldb + j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        w[c][i][r] = in && n0 + row + r * 8 < p.N ? *reinterpret_cast<const uint2 *>(b[i] + r * 8 * side.ldb + j) : make_uint2(0, 0);
+            for (int g = 0; g < 2; ++g)
 #pragma unroll
-                for (int g = 0; g < 2; ++g) v[c][g] = in && used[g] ? *reinterpret_cast<const float4 *>(q + g * second + j) : make_float4(0, 0, 0, 0);
-            }
+                for (int c = 0; c < 2; ++c)
+                    v[g][c] = in && used[g] ? *reinterpret_cast<const float4 *>(q + g * second + j + 4 * c) : make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t h[2][2], l[2][2];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float4 x = v[c][g];
+                    const float4 x = v[g][c];
                     h[g][0] = pack_bf16x2(x.x, x.y);
                     h[g][1] = pack_bf16x2(x.z, x.w);
                     l[g][0] = pack_bf16x2(x.x - bf16_lo(h[g][0]), x.y - bf16_hi(h[g][0]));
                     l[g][1] = pack_bf16x2(x.z - bf16_lo(h[g][1]), x.w - bf16_hi(h[g][1]));
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i) {
+                    if (a[i] < 0) continue;   // the whole warp
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const uint32_t wa[4] = {w[c][i][2 * t].x, w[c][i][2 * t + 1].x, w[c][i][2 * t].y, w[c][i][2 * t + 1].y};
+                        const uint4 &x = w[i][2 * t], &y = w[i][2 * t + 1];
+                        const uint32_t wa[4] = {c ? x.z : x.x, c ? y.z : y.x, c ? x.w : x.y, c ? y.w : y.y};
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             mma_16816(acc[i][g][t], wa, h[g][0], h[g][1]);
                             mma_16816(acc[i][g][t], wa, l[g][0], l[g][1]);
                         }
                     }
+                }
             }
         }
         // this lane's tokens of a half: quad * 2 and the next
@@ -295,14 +298,14 @@ __device__ __forceinline__ void lora_inside(const LoraParams &p, int inside, int
     }
 }
 
-// The same for rows that mostly have an adapter each: a lane has one output n, reads its row
+// The same for rows that mostly have an adapter each, of rank 16 at most (a row of more spreads
+// a warp's load over 32 lines): a lane has one output n, reads its row
 // of each token's B, eight tokens' together, and adds the term to y.  p of 16 tokens and 16
 // columns is staged in shared memory (stage, 256 floats), on the way beside B.
-__device__ __forceinline__ void lora_term_rows(const LoraParams &p, const float *all_p, int d, int sides, int64_t m0, int64_t n, float *stage,
-                                               float (&y)[16])
+__device__ __forceinline__ void lora_term_rows(const LoraParams &p, int mine, const float *all_p, int d, int sides, int64_t m0, int64_t n,
+                                               float *stage, float (&y)[16])
 {
     const int lane = threadIdx.x & 31, R = p.R;
-    const int mine = lane < 16 ? lora_adapter(p, m0 + lane) : -1;
     const uint32_t used = __ballot_sync(0xffffffffu, mine >= 0);
     const LoraSide &side = p.side[d];
     // this lane stages 8 columns of token lane / 2
@@ -374,6 +377,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
         for (int i = first; i < plan.items && ok; i += step) {
             const LoraTile x = lora_tile(plan, i);
             const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2), m0 = x.t % plan.ttiles * plan.tn + rank * (plan.tn / 2);
+            // the table: but for the first tile, whose products do not wait for it, it comes ahead
+            const bool runs = p.l.blocks && x.slot < 0;
+            LoraRuns run;
+            if (runs && i != first) run.load(p.l, x.t % plan.ttiles * plan.tn, plan.tn);
             for (int c = x.c0; c < x.c1; ++c) {
                 if (!pair_wait(&s.empty[st], phase, kWaitLimitNs)) {
                     ok = false;
@@ -394,9 +401,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                     phase ^= 1;
                 }
             }
-            if (!p.l.blocks || x.slot >= 0 || !ok) continue;
-            if (p.early) grid_dependency_wait();   // p and the table
-            for (LoraRuns run(p.l, x.t % plan.ttiles * plan.tn, plan.tn); ok && run.next();) {
+            if (!runs || !ok) continue;
+            if (i == first) {
+                if (p.early) grid_dependency_wait();   // p and the table
+                run.load(p.l, x.t % plan.ttiles * plan.tn, plan.tn);
+            }
+            while (ok && run.next()) {
                 const int blocks = run.at - run.first;
                 const int row = x.t % plan.ttiles * plan.tn + run.first * kLoraBlock + rank * blocks * 16;   // each CTA brings half of the run
                 for (int c = 0; c < width && ok; c += 64)
@@ -437,6 +447,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
             uint32_t phase = 0, buf = 0, acc_phase = 1;
             for (int i = first; i < plan.items && ok; i += step) {
                 const LoraTile x = lora_tile(plan, i);
+                const bool runs = p.l.blocks && x.slot < 0;
+                LoraRuns run;
+                if (runs && i != first) run.load(p.l, x.t % plan.ttiles * plan.tn, plan.tn);
                 for (int c = x.c0; c < x.c1; ++c) {
                     if ((c == x.c0 && !pair_wait(&s.acc_empty[buf], acc_phase, kWaitLimitNs)) || !pair_wait(&s.full[st], phase, kWaitLimitNs)) {
                         ok = false;
@@ -455,9 +468,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                         phase ^= 1;
                     }
                 }
-                if (p.l.blocks && x.slot < 0 && ok) {
-                    if (p.early) grid_dependency_wait();
-                    for (LoraRuns run(p.l, x.t % plan.ttiles * plan.tn, plan.tn); ok && run.next();) {
+                if (runs && ok) {
+                    if (i == first) {
+                        if (p.early) grid_dependency_wait();
+                        run.load(p.l, x.t % plan.ttiles * plan.tn, plan.tn);
+                    }
+                    while (ok && run.next()) {
                         const int cols = (run.at - run.first) * kLoraBlock;
                         const uint32_t run_idesc = tc_idesc_bf16(256, 256) - (static_cast<uint32_t>((256 - cols) >> 3) << 17);
                         const uint32_t d = tmem + buf * kPairTile + static_cast<uint32_t>(run.first * kLoraBlock);
@@ -489,9 +505,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 if (buf == 0) acc_phase ^= 1;
             }
         }
-    } else if (warp == 2 && p.l.adapters > 0) {
+    } else if (warp == 2 && p.prefetch) {
         // B is read row by row at the end, where nothing hides the way, but for blocks of one
-        // adapter: its bytes come into L2 beside the weights, whose copies leave room for them
+        // adapter: where it is small its bytes come into L2 beside the weights
         for (int i = first; i < plan.whole + plan.rest; i += step) {
             const LoraTile x = lora_tile(plan, i);
             const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2), rows = min(plan.wt / 2, p.l.N - n0);
@@ -529,6 +545,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
             const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2) + row0;
             const int n = row0 + lane < plan.wt / 2 ? n0 + lane : p.l.N;   // N: none
             const int m0 = x.t % plan.ttiles * plan.tn + half * (plan.tn / 2);
+            // the tokens' adapters, a lane per token, on the way while the products run
+            int ids[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) ids[b] = p.l.adapters > 0 && b * 32 < plan.tn / 2 ? lora_adapter(p.l, static_cast<int64_t>(m0) + b * 32 + lane) : -1;
+            // and the table's entries of this half of the tile
+            const int entry = p.l.blocks && x.slot < 0 && lane < 5 && m0 / kLoraBlock + lane <= (p.l.M - 1) / kLoraBlock
+                                  ? __ldcg(p.l.blocks + m0 / kLoraBlock + lane) : kNoAdapter;
             if (ok) ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], (v >> 1) & 1, kWaitLimitNs));
             tc_fence_after();
             for (int j = 0; j < plan.tn / 2; j += 16, ++sets) {
@@ -552,11 +575,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 float y[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(r[k]);
-                if (tokens > 0 && (p.inside == kInsideEach || (p.l.blocks && __ldcg(p.l.blocks + (m0 + j) / kLoraBlock) == kMixed))) {
+                const int at32 = j >> 5, id = at32 == 0 ? ids[0] : at32 == 1 ? ids[1] : at32 == 2 ? ids[2] : ids[3];
+                int mine = __shfl_sync(0xffffffffu, id, (j & 16) + (lane & 15));   // these 16 tokens', in the first lanes
+                if (lane >= 16) mine = -1;
+                const int block = __shfl_sync(0xffffffffu, entry, (m0 + j) / kLoraBlock - m0 / kLoraBlock);
+                const bool term_here = p.inside == kInsideEach || block == kMixed;
+                if (tokens > 0 && term_here) {
                     if constexpr (ROWS)
-                        lora_term_rows(p.l, all_p, d, SIDES, static_cast<int64_t>(m0) + j, n, term, y);
+                        lora_term_rows(p.l, mine, all_p, d, SIDES, static_cast<int64_t>(m0) + j, n, term, y);
                     else
-                        lora_term(p.l, d, SIDES, static_cast<int64_t>(m0) + j, n0, term, [&](int g) {
+                        lora_term(p.l, mine, d, SIDES, static_cast<int64_t>(m0) + j, n0, term, [&](int g) {
 #pragma unroll
                             for (int k = 0; k < 16; ++k)
                                 if (k >> 3 == g) y[k] += term[(k & 7) * kTermPitch + lane];
@@ -595,12 +623,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
 }
 
 // The tiles in ranges: their partial sums in order, the adapters' term and the epilogue.  A
-// warp takes 32 outputs and TOKENS tokens, whose rows of B are on the way together.
-template <int SIDES, int TOKENS>
+// warp takes 32 outputs and TOKENS tokens.  LANES lanes share a row of B, eight columns each (R
+// <= 8 LANES), so that a load of the warp is 512 consecutive bytes; LANES - 1 shuffles leave each
+// output's sum in one lane.  Here an SM has 24 to 64 warps, beside the products it has eight
+// for this: 48 rows with adapters of rank 64 of their own took 83 us there, 57 here.
+template <int SIDES, int TOKENS, int LANES>
 __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
 {
+    constexpr int kRows = 32 / LANES;                 // rows of a load
     const LoraPlan &plan = p.plan;
-    const int lane = threadIdx.x & 31, R = p.l.R;
+    const int lane = threadIdx.x & 31, part = lane % LANES, row = lane / LANES, R = p.l.R;
+    const int from = lane % kRows * LANES + lane / kRows;   // where the sum of output `lane` ends up
     const int groups = plan.tn / TOKENS, blocks = (plan.wt + 31) / 32;   // of a tile
     const int64_t total = static_cast<int64_t>(plan.rest) * blocks * groups;
     grid_dependency_wait();
@@ -608,55 +641,65 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < total; i += static_cast<int64_t>(gridDim.x) * 8) {
         // tiles' first tokens first: those behind the last row cost nothing
         const int group = static_cast<int>(i / (plan.rest * blocks)), other = static_cast<int>(i % (plan.rest * blocks));
-        const int tile = other / blocks, j0 = group * TOKENS, w = other % blocks * 32 + lane;
-        const int t = plan.whole + tile;
-        const int n = t / plan.ttiles * plan.wt + w;
+        const int tile = other / blocks, j0 = group * TOKENS, w = other % blocks * 32;
+        const int t = plan.whole + tile, n0 = t / plan.ttiles * plan.wt + w;
         const int64_t m0 = static_cast<int64_t>(t % plan.ttiles) * plan.tn + j0;
-        if (m0 >= p.l.M || w >= plan.wt || n >= p.l.N) continue;
+        if (m0 >= p.l.M || n0 >= p.l.N) continue;   // the whole warp
+        const bool mine = w + lane < plan.wt && n0 + lane < p.l.N;
         int a[TOKENS];
 #pragma unroll
         for (int k = 0; k < TOKENS; ++k) a[k] = lora_adapter(p.l, m0 + k);
         // output w of the tile: a CTA holds wt / 2 of them, in dual tiles from lanes 0 and 64 on
-        const int rank = w >= plan.wt / 2 ? 1 : 0, at = rank * 128 + w - rank * (plan.wt / 2);
-        float acc[TOKENS][SIDES] = {}, term[TOKENS][SIDES] = {};
+        const int rank = w + lane >= plan.wt / 2 ? 1 : 0, at = rank * 128 + w + lane - rank * (plan.wt / 2);
+        float acc[TOKENS][SIDES] = {};
         const float *q = p.part + (static_cast<int64_t>(tile) * plan.tn + j0) * 256 + at;
 #pragma unroll 4
         for (int s = 0; s < plan.splits; ++s, q += static_cast<int64_t>(plan.rest) * plan.tn * 256)
 #pragma unroll
             for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
-                for (int d = 0; d < SIDES; ++d) acc[k][d] += m0 + k < p.l.M ? __ldcg(q + k * 256 + d * 64) : 0.0f;
-        for (int j = 0; j < R; j += 16) {
-            uint4 b[TOKENS][SIDES][2];
+                for (int d = 0; d < SIDES; ++d) acc[k][d] += mine && m0 + k < p.l.M ? __ldcg(q + k * 256 + d * 64) : 0.0f;
 #pragma unroll
-            for (int k = 0; k < TOKENS; ++k)
+        for (int d = 0; d < SIDES; ++d) {
+            const LoraSide &side = p.l.side[d];
+            uint4 b[TOKENS][LANES];
+            float4 v[TOKENS][2];
 #pragma unroll
-                for (int d = 0; d < SIDES; ++d) {
-                    const LoraSide &side = p.l.side[d];
-                    const uint16_t *r = side.b + a[k] * side.b_adapter + n * side.ldb + j;
+            for (int k = 0; k < TOKENS; ++k) {
+                const uint16_t *r = side.b + a[k] * side.b_adapter + (n0 + row) * static_cast<int64_t>(side.ldb) + part * 8;
+                const float *x = p.l.p + (m0 + k) * SIDES * R + d * R + part * 8;
+                const bool has = a[k] >= 0 && part * 8 < R;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) b[k][d][h] = a[k] >= 0 && j + 8 * h < R ? *reinterpret_cast<const uint4 *>(r + 8 * h) : make_uint4(0, 0, 0, 0);
-                }
+                for (int h = 0; h < LANES; ++h)
+                    b[k][h] = has && n0 + h * kRows + row < p.l.N ? *reinterpret_cast<const uint4 *>(r + h * kRows * side.ldb) : make_uint4(0, 0, 0, 0);
+                v[k][0] = has ? *reinterpret_cast<const float4 *>(x) : make_float4(0, 0, 0, 0);
+                v[k][1] = has ? *reinterpret_cast<const float4 *>(x + 4) : make_float4(0, 0, 0, 0);
+            }
 #pragma unroll
-            for (int k = 0; k < TOKENS; ++k)
+            for (int k = 0; k < TOKENS; ++k) {
+                float sum[LANES];
 #pragma unroll
-                for (int d = 0; d < SIDES; ++d) {
-                    const float *v = p.l.p + (m0 + k) * SIDES * R + d * R + j;
+                for (int h = 0; h < LANES; ++h) sum[h] = dot8(b[k][h], v[k][0], v[k][1], 0.0f);
+                // halves are exchanged until a lane has one sum: of the rows' group `part`
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // loads that no branch keeps behind one another
-                        const bool in = a[k] >= 0 && j + 8 * h < R;
-                        const float4 y = in ? *reinterpret_cast<const float4 *>(v + 8 * h) : make_float4(0, 0, 0, 0);
-                        const float4 z = in ? *reinterpret_cast<const float4 *>(v + 8 * h + 4) : make_float4(0, 0, 0, 0);
-                        term[k][d] = dot8(b[k][d][h], y, z, term[k][d]);
+                for (int o = LANES / 2; o > 0; o >>= 1) {
+                    const bool upper = part & o;
+#pragma unroll
+                    for (int h = 0; h < o; ++h) {
+                        const float theirs = __shfl_xor_sync(0xffffffffu, upper ? sum[h] : sum[h + o], o);
+                        sum[h] = (upper ? sum[h + o] : sum[h]) + theirs;
                     }
                 }
+                acc[k][d] += __shfl_sync(0xffffffffu, sum[0], from);
+            }
         }
+        __syncwarp();
+        if (!mine) continue;
 #pragma unroll
         for (int k = 0; k < TOKENS; ++k) {
             if (m0 + k >= p.l.M) break;
-            uint16_t *o = p.l.out + (m0 + k) * p.l.ldo + n;
-            const float g = acc[k][0] + term[k][0], u = acc[k][SIDES - 1] + term[k][SIDES - 1];
+            uint16_t *o = p.l.out + (m0 + k) * p.l.ldo + n0 + lane;
+            const float g = acc[k][0], u = acc[k][SIDES - 1];
             if constexpr (SIDES == 2)
                 *o = p.l.mode == 0 ? f32_to_bf16(silu_short(g) * u) : static_cast<uint16_t>(glu_hf_short(g, u));
             else
