@@ -229,3 +229,38 @@ def test_offsets_beyond_32_bits():
     idx = torch.tensor([69, -1, 69], dtype=torch.int32, device=DEV)
     y, e = Q.adapted(x, w, a[69:], b[69:], idx - 69, None)
     R.assert_bf16(mb.linear_lora(x, w, a, b, idx), y, e)
+
+
+@pytest.mark.parametrize("sides", [1, 2])
+@pytest.mark.parametrize("r", [8, 24, 32, 56, 64, 120, 128])
+@pytest.mark.parametrize("M,N,K", [(2, 300, 264), (16, 700, 1032), (50, 2500, 520)])
+def test_a_decode_batch_of_each_rank(M, N, K, r, sides):
+    check(M, N, K, r, 64, seed=M + r, how="own", sides=sides, variant=FAST)
+
+
+# tiles of 128 rows with one adapter, some and many; the inner dimension whole and in up to eight ranges
+@pytest.mark.parametrize("sides", [1, 2])
+@pytest.mark.parametrize("M,K,r,L,how", [(512, 72, 8, 3, "runs"), (600, 520, 128, 4, "runs"), (640, 1032, 40, 200, "mixed"),
+                                         (1100, 2056, 64, 7, "runs"), (1100, 264, 24, 5, "mixed")])
+def test_many_rows(M, K, r, L, how, sides):
+    check(M, 264, K, r, L, seed=M, how=how, sides=sides, variant=FAST)
+
+
+@pytest.mark.parametrize("M", [40, 100, 700])
+def test_one_adapter_for_all_but_some_rows(M):
+    """Runs of 32 rows of one adapter, and beside them blocks with single rows of another or of none."""
+    for lone in (0, 31, 32, M - 1):
+        args = list(operands(M, 264, 136, 24, 4, seed=M))
+        args[-2] = torch.full((M,), 2, dtype=torch.int32, device=DEV)
+        args[-2][lone] = 3 if lone % 2 else -1
+        Q.assert_glu_lora(mb.glu_lora(*args), args)
+
+
+def test_shared_memory_of_adapters():
+    """One adapter under every index: a stride of zero between adapters."""
+    x, w, a, b, idx, scale = operands(70, 200, 136, 16, 1, seed=3, sides=1)
+    a, b = a.expand(5, -1, -1), b.expand(5, -1, -1)
+    idx = indices(70, 5, 4)
+    scale = scale.expand(5).contiguous()
+    for M in (9, 70):
+        R.assert_bf16(mb.linear_lora(x[:M], w, a, b, idx[:M], scale), *Q.adapted(x[:M], w, a, b, idx[:M], scale))

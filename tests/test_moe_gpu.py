@@ -229,3 +229,15 @@ def test_offsets_beyond_32_bits():
     got = mb.moe_glu(h, r, g, u, d, 2)
     assert got[1].tolist() == [[269, 1]] * 2
     Q.assert_moe(got, h, r, g, u, d, 2, True)
+
+
+# as many tiles as half to all of the SMs: one per block, one token to 64
+@pytest.mark.parametrize("T,E,k,N,K", [(1, 16, 8, 768, 520), (2, 4, 4, 1600, 264), (17, 4, 4, 1608, 264), (40, 4, 4, 2056, 136), (64, 2, 2, 4872, 72)])
+def test_one_tile_per_block(T, E, k, N, K):
+    check(T, E, k, N, K, seed=T, variant=FAST)
+
+
+@pytest.mark.parametrize("T,E", [(1, 509), (1, 512), (2, 256), (2, 257), (4, 128), (5, 128), (16, 32), (64, 8), (64, 9), (64, 512)])
+def test_who_chooses(T, E):
+    """Around the number of logits up to which each block chooses for all tokens."""
+    check(T, E, min(E, 5), 72, 136, renormalize=False, seed=T + E, variant=FAST)
