@@ -1,8 +1,9 @@
 // bind_torch.cpp -- the common case of the binding's wide and e4m3 calls, and of
-// those whose rows choose weights of their own: tensors of the right type, shape and device, on the current device's current
-// stream.  Marshalling only, as binding.py, whose argument checks take longer
-// than a decode step's kernels.  A call that is not the common case returns
-// None and binding.py does it, with its own checks and errors.
+// those whose rows choose weights of their own: tensors of the right type, shape
+// and device, on the current device's current stream.  Marshalling only, as
+// binding.py, whose argument checks take longer than a decode step's kernels.  A
+// call that is not the common case returns None and binding.py does it, with its
+// own checks and errors.
 //
 // Each function returns what the Python function returns, None (not the common
 // case: nothing was launched), or a non-zero status as an int.

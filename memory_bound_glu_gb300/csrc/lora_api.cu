@@ -137,7 +137,8 @@ mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *tak
     const uint32_t stage = mbglu::shrink_tc_stage(SIDES * p.R);
     q.stages = std::min<int>(mbglu::kShrinkTcMaxStages, (200 * 1024) / static_cast<int>(stage));
     *taken = true;
-    Launch l(dim3(static_cast<unsigned>(q.split), static_cast<unsigned>(tiles)), mbglu::kShrinkTcThreads, 3072 + static_cast<size_t>(q.stages) * stage, stream,
+    Launch l(dim3(static_cast<unsigned>(q.split), static_cast<unsigned>(tiles)), mbglu::kShrinkTcThreads,
+             mbglu::kShrinkTcHeader + 1024 + static_cast<size_t>(q.stages) * stage, stream,
              q.split);
     return launched(cudaLaunchKernelEx(&l.cfg, mbglu::lora_shrink_tc_kernel<SIDES>, q, maps));
 }

@@ -20,6 +20,7 @@ constexpr int kShrinkTcThreads = 192;
 constexpr int kShrinkTcRows = 128;
 constexpr uint32_t kShrinkTcX = kShrinkTcRows * 128;      // a chunk of 64 columns of x
 constexpr int kShrinkTcMaxStages = 8;
+constexpr uint32_t kShrinkTcHeader = 2048;                // barriers; the rows' scales and adapters
 
 struct ShrinkTcMaps {
     TensorMap x;             // [M][K], boxes of 64 x 128
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
     uint32_t *slot = reinterpret_cast<uint32_t *>(done + 1);
     float *scales = reinterpret_cast<float *>(base + 512);   // of the rows; 0 where none is used
     int *ids = reinterpret_cast<int *>(base + 1024);
-    unsigned char *ring = base + 2048;
+    unsigned char *ring = base + kShrinkTcHeader;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int R = p.l.R, width = SIDES * R, rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const uint32_t stage = shrink_tc_stage(width);
