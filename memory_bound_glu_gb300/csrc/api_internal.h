@@ -36,7 +36,8 @@ int launch_policy();
 bool encode_tile_map(mbglu::TensorMap *out, const void *base, int64_t ld, int rows, int cols, int box_cols,
                      int box_rows, int elem_bytes);
 
-// As encode_tile_map for bf16 [count][rows][cols], stride elements from matrix to matrix.
+// As encode_tile_map for bf16 [count][rows][cols], stride elements from matrix to matrix
+// (stack_maps.cu).
 bool encode_stack_map(mbglu::TensorMap *out, const void *base, int64_t stride, int64_t ld, int count, int rows, int cols, int box_cols,
                       int box_rows);
 

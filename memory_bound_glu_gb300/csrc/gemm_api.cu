@@ -431,11 +431,18 @@ mbglu_status mbglu_block_plan(int product, int M, int N, int K, int *plan)
 
 namespace mbglu_host {
 
+// This unit's word, or else one of the units whose rows choose weights of their own.
 cudaError_t take_gemm_error(int *w)
 {
     cudaError_t e = cudaMemcpyFromSymbol(w, mbglu::g_dense_error, sizeof *w);
     const int zero = 0;
-    return e != cudaSuccess ? e : cudaMemcpyToSymbol(mbglu::g_dense_error, &zero, sizeof zero);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(mbglu::g_dense_error, &zero, sizeof zero);
+    for (cudaError_t (*take)(int *) : {take_lora_error, take_moe_error}) {
+        int x = 0;
+        if (e == cudaSuccess) e = take(&x);
+        if (*w == 0) *w = x;
+    }
+    return e;
 }
 
 }  // namespace mbglu_host

@@ -15,6 +15,7 @@
 // kNoAdapter, or kMixed.
 #pragma once
 #include "lora_generic.cuh"
+#include "stack_copy.cuh"
 #include "tcgen05.cuh"
 
 namespace mbglu {

@@ -651,23 +651,6 @@ bool encode_tile_map(mbglu::TensorMap *out, const void *base, int64_t ld, int ro
     return encode_2d(out, base, ld, rows, cols, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, elem_bytes);
 }
 
-bool encode_stack_map(mbglu::TensorMap *out, const void *base, int64_t stride, int64_t ld, int count, int rows, int cols, int box_cols,
-                      int box_rows)
-{
-    const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
-    if (!fn) return false;
-    CUtensorMap m;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(count > 1 ? stride : rows * ld) * 2};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u};
-    const cuuint32_t elem_strides[3] = {1u, 1u, 1u};
-    if (fn(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    std::memcpy(out, &m, sizeof m);
-    return true;
-}
-
 }  // namespace mbglu_host
 
 namespace {
@@ -1963,8 +1946,7 @@ mbglu_status mbglu_read_device_error(int *word)
     if ((e = cudaMemcpyFromSymbol(&w, mbglu::g_device_error, sizeof w)) != cudaSuccess) return cuda_fail(e);
     const int zero = 0;
     if ((e = cudaMemcpyToSymbol(mbglu::g_device_error, &zero, sizeof zero)) != cudaSuccess) return cuda_fail(e);
-    for (cudaError_t (*take)(int *) : {mbglu_host::take_gemm_error, mbglu_host::take_fp8_error, mbglu_host::take_lora_error,
-                                        mbglu_host::take_moe_error}) {
+    for (cudaError_t (*take)(int *) : {mbglu_host::take_gemm_error, mbglu_host::take_fp8_error}) {
         int x = 0;   // the other translation units' words
         if ((e = take(&x)) != cudaSuccess) return cuda_fail(e);
         if (w == 0) w = x;

@@ -35,6 +35,7 @@
 #pragma once
 #include "dense_common.cuh"
 #include "moe_route.cuh"
+#include "stack_copy.cuh"
 #include "tc_pair.cuh"
 
 namespace mbglu {

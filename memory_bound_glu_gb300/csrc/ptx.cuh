@@ -95,12 +95,6 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
         : "memory");
 }
 
-// Asks for `bytes` (a multiple of 16, the address 16-byte aligned) to be brought into L2.
-__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
 // Bulk copy without an L2 hint (small operands that every CTA reads).
 __device__ __forceinline__ void bulk_g2s_plain(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
@@ -116,12 +110,6 @@ struct alignas(64) TensorMap {
     uint64_t opaque[16];
 };
 
-// Asks for a descriptor ahead of the copies that use it.
-__device__ __forceinline__ void prefetch_tensor_map(const TensorMap *map)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
 // Tiled tensor copy of one 2-D box at element coordinates (x, y) (x
 // innermost) into this CTA's shared memory (128-byte aligned); the whole
 // box's bytes -- elements outside the tensor arrive as zeros -- are counted
@@ -133,16 +121,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const TensorMap *map, int
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy)
-        : "memory");
-}
-
-// tma_load_2d for a box of a stack of matrices (z: the matrix).
-__device__ __forceinline__ void tma_load_3d(void *dst, const TensorMap *map, int x, int y, int z, uint64_t *bar, uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
 }
 
