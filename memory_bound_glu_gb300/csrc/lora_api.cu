@@ -132,6 +132,7 @@ mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *tak
     q.l = p;
     q.part = part;
     q.nchunk = ceil_div(p.K, 64);
+    q.group = mbglu::shrink_tc_group(SIDES * p.R);
     q.split = 1;
     while (q.split < kShrinkTcSplit && tiles * q.split * 2 <= 160 && q.nchunk >= q.split * 8) q.split *= 2;
     const uint32_t stage = mbglu::shrink_tc_stage(SIDES * p.R);

@@ -1,11 +1,12 @@
 // lora_shrink_tc.cuh -- p = scale[a] x A[a]^T for many rows, on tcgen05.
 //
 // A cluster takes 128 rows, its blocks a range of the inner dimension each.  The rows are
-// the MMA's M side; the columns are the adapter's A, both projections' one behind the other
-// (up to 256).  For each adapter among the rows the block runs its range's product of all
-// rows and keeps of it the rows that use the adapter, as a partial sum in global memory
-// (which stays in L2); a row has one adapter, so no row is written twice, and one cluster
-// barrier at the end lets the blocks add up 128 / split rows each, in order.
+// the MMA's M side; the columns are the A of up to kShrinkTcGroup adapters among the rows, both
+// projections' one behind the other (256 columns at most), so that a tile with a border between
+// two requests reads x once.  The block keeps of each adapter's columns the rows that use it,
+// as a partial sum in global memory (which stays in L2); a row has one adapter, so no row is
+// written twice, and one cluster barrier at the end lets the blocks add up 128 / split rows
+// each, in order.
 //
 // What bounds it is x's way in: 4096 x 2560 are 21 MB.  Rows of one request lie together, so
 // mostly there is one adapter, or two; a chunk of many short requests takes
@@ -31,9 +32,15 @@ struct ShrinkTcParams {
     LoraParams l;
     float *part;             // [split][M][sides R]
     int split, stages, nchunk;
+    int group;               // adapters at a time
 };
 
-__host__ __device__ constexpr uint32_t shrink_tc_stage(int width) { return kShrinkTcX + static_cast<uint32_t>((width + 15) / 16 * 16) * 128u; }
+constexpr int kShrinkTcGroup = 4;
+__host__ __device__ constexpr int shrink_tc_group(int width) { return 256 / width < kShrinkTcGroup ? 256 / width : kShrinkTcGroup; }
+__host__ __device__ constexpr uint32_t shrink_tc_stage(int width)
+{
+    return kShrinkTcX + static_cast<uint32_t>((shrink_tc_group(width) * width + 15) / 16 * 16) * 128u;
+}
 
 // The adapters among 128 rows, each once; a warp walks them.
 struct LoraDistinct {
@@ -47,7 +54,18 @@ struct LoraDistinct {
             left[i] = __ballot_sync(0xffffffffu, id[i] >= 0);
         }
     }
-    __device__ bool next(int &a)
+    // up to `group` of them; how many
+    __device__ int next(int (&a)[kShrinkTcGroup], int group)
+    {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kShrinkTcGroup; ++i) {
+            a[i] = -1;
+            if (n == i && i < group && one(a[i])) ++n;
+        }
+        return n;
+    }
+    __device__ bool one(int &a)
     {
         a = -1;
 #pragma unroll
@@ -107,9 +125,9 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
 
     if (warp == 0) {
         LoraDistinct adapters(p.l, m0);
-        int st = 0, issued = 0, a;
+        int st = 0, issued = 0, a[kShrinkTcGroup], n;
         uint32_t phase = 1;
-        while (ok && adapters.next(a)) {
+        while (ok && (n = adapters.next(a, p.group)) > 0) {
             for (int c = c0; c < c1; ++c) {
                 if (!pair_wait(&empty[st], phase, kWaitLimitNs)) {
                     ok = false;
@@ -117,11 +135,14 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
                 }
                 if (elect_one()) {
                     unsigned char *d = ring + st * stage;
-                    mbar_arrive_expect_tx(&full[st], kShrinkTcX + static_cast<uint32_t>(width) * 128u);
+                    mbar_arrive_expect_tx(&full[st], kShrinkTcX + static_cast<uint32_t>(n * width) * 128u);
                     const uint64_t policy = l2_policy_evict_last();   // the shared product reads x again
                     tma_load_2d(d, &maps.x, c * 64, static_cast<int>(m0), &full[st], policy);
 #pragma unroll
-                    for (int i = 0; i < SIDES; ++i) tma_load_3d(d + kShrinkTcX + i * R * 128, &maps.a[i], c * 64, 0, a, &full[st], policy);
+                    for (int j = 0; j < kShrinkTcGroup; ++j)
+#pragma unroll
+                        for (int i = 0; i < SIDES; ++i)
+                            if (j < n) tma_load_3d(d + kShrinkTcX + (j * width + i * R) * 128, &maps.a[i], c * 64, 0, a[j], &full[st], policy);
                 }
                 __syncwarp();
                 issued += issued < p.stages;
@@ -139,10 +160,10 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
         }
     } else if (warp == 1) {
         LoraDistinct adapters(p.l, m0);
-        const uint32_t idesc = tc_idesc_bf16(kShrinkTcRows, (width + 15) / 16 * 16);
-        int st = 0, a;
+        int st = 0, a[kShrinkTcGroup], n;
         uint32_t phase = 0, buf = 0, acc_phase = 1;
-        while (ok && adapters.next(a)) {
+        while (ok && (n = adapters.next(a, p.group)) > 0) {
+            const uint32_t idesc = tc_idesc_bf16(kShrinkTcRows, 16) + (static_cast<uint32_t>((n * width + 15) / 16 * 16 - 16) >> 3 << 17);
             if (!pair_wait(&acc_empty[buf], acc_phase, kWaitLimitNs)) {
                 ok = false;
                 break;
@@ -188,24 +209,27 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
         float *dst = p.part + (static_cast<int64_t>(rank) * p.l.M + m0 + row) * width;
         uint32_t buf = 0, acc_phase = 0;
-        int a;
-        while (ok && adapters.next(a)) {
+        int a[kShrinkTcGroup];
+        while (ok && adapters.next(a, p.group) > 0) {
             if (!__all_sync(0xffffffffu, pair_wait(&acc_full[buf], acc_phase, kWaitLimitNs))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            if (__any_sync(0xffffffffu, mine == a))
+#pragma unroll
+            for (int j = 0; j < kShrinkTcGroup; ++j) {
+                if (a[j] < 0 || !__any_sync(0xffffffffu, mine == a[j])) continue;   // the whole warp
                 for (int c = 0; c < width; c += 16) {
                     float v[16];
                     __syncwarp();
-                    tmem_ld16(lanes + buf * 256u + static_cast<uint32_t>(c), v);
-                    if (mine == a) {
+                    tmem_ld16(lanes + buf * 256u + static_cast<uint32_t>(j * width + c), v);
+                    if (mine == a[j]) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (c + 4 * i < width) __stcg(reinterpret_cast<float4 *>(dst + c + 4 * i), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
                     }
                 }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[buf]);
