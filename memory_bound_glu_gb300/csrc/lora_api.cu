@@ -23,7 +23,8 @@ constexpr int kFewRows = 64;   // a decode batch
 //   tensor cores (lora_term) 59; at 500 rows of 60 requests 70 and 78; at rank 64 113 there and
 //   363 by rows;
 //   a decode batch's larger ranks the join, which has more warps: at 48 rows of rank 64 57, in
-//   the epilogue 83; of rank 32 36 and 47; at rank 16 it is the other way round, 33 and 31.
+//   the epilogue 83; of rank 32 36 and 47; at rank 16 it is the other way round, 33 and 31, and
+//   at 128 rows, 63 and 58 of rank 32.
 bool by_rows(int M, int R) { return M <= kFewRows || (M < 512 && R <= 16); }
 bool by_join(int sides, int M, int R) { return M >= 2 && M <= kFewRows && R > 16 && M * sides * R > mbglu::kInsideMost; }
 

@@ -373,6 +373,20 @@ __device__ __forceinline__ bool moe_choose(const MoeParams &p, MoeShared &s, int
         }
         __syncthreads();
     }
+    if (p.T == 1) {   // the choice is the table, in its own order
+        if (static_cast<int>(threadIdx.x) < p.top_k) {
+            const int i = static_cast<int>(threadIdx.x), e = s.id[i];
+            s.mask[e] = 1;
+            s.expert[i] = static_cast<uint16_t>(e);
+            s.where[e] = s.first[i] = s.of_slot[i] = static_cast<uint16_t>(i);
+            if (i == 0) {
+                s.active = p.top_k;
+                s.first[p.top_k] = static_cast<uint16_t>(p.top_k);
+            }
+        }
+        __syncthreads();
+        return true;
+    }
     for (int i = threadIdx.x; i < slots; i += kMoeThreads)
         atomicOr(reinterpret_cast<uint32_t *>(&s.mask[s.id[i]]) + (i / p.top_k >> 5), 1u << (i / p.top_k & 31));
     __syncthreads();
