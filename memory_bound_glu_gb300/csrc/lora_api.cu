@@ -20,12 +20,13 @@ constexpr int kFewRows = 64;   // a decode batch
 
 // Who adds the terms of rows with adapters of their own (us at K = 2560, N = 9728, two projections):
 //   up to rank 16 the epilogue, a row of B per lane: at 100 rows of as many requests 40, on the
-//   tensor cores (lora_term) 59; at 500 rows of 60 requests 70 and 78; at rank 64 113 there and
-//   363 by rows;
+//   tensor cores (lora_term) 59; at 1000 rows of 30 requests 102 and 114, at 4000 248 and 285;
+//   of rank 24 the tensor cores up to some 2000 rows and little behind from there (4000 rows of
+//   60 requests 330, by rows 322); of rank 64 500 rows of 60 requests 113, by rows 363;
 //   a decode batch's larger ranks the join, which has more warps: at 48 rows of rank 64 57, in
 //   the epilogue 83; of rank 32 36 and 47; at rank 16 it is the other way round, 33 and 31, and
 //   at 128 rows, 63 and 58 of rank 32.
-bool by_rows(int M, int R) { return M <= kFewRows || (M < 512 && R <= 16); }
+bool by_rows(int M, int R) { return M <= kFewRows || R <= 16; }
 bool by_join(int sides, int M, int R) { return M >= 2 && M <= kFewRows && R > 16 && M * sides * R > mbglu::kInsideMost; }
 
 // Tiles and ranges, from the sizes alone.  The estimate (ns) of a tile's time is
