@@ -493,7 +493,9 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
  *   scale     [adapters] fp32, or NULL for 1                              (read)
  *   workspace device memory of glu_lora_workspace_bytes (linear_lora_...) bytes,
  *             256-byte aligned, contents undefined afterwards; calls that may run at
- *             the same time need different ones
+ *             the same time need different ones.  Fewer rows may need more bytes (ranges
+ *             of the inner dimension leave partial sums): one that is kept for several
+ *             sizes has the largest of theirs
  *   0 <= R <= MBGLU_LORA_MAX_RANK.  adapters == 0 or R == 0: the shared product
  *   alone; gate, up, ab, adapter and workspace are not looked at.  M == 0 or N == 0:
  *   no-op.

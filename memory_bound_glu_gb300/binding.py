@@ -870,12 +870,14 @@ def moe_glu(h, router_w, gate_w, up_w, down_w, top_k, renormalize=True, out=None
 
 
 def glu_lora_workspace_bytes(M, N, K, adapters, R):
-    """Bytes of glu_lora's workspace (0: none needed)."""
+    """Bytes of glu_lora's workspace (0: none needed).  Fewer rows may need more: one
+    that is kept for several sizes has the largest of theirs."""
     return lib().glu_lora_workspace_bytes(M, N, K, adapters, R)
 
 
 def linear_lora_workspace_bytes(M, N, K, adapters, R):
-    """Bytes of linear_lora's workspace (0: none needed)."""
+    """Bytes of linear_lora's workspace (0: none needed).  Fewer rows may need more: one
+    that is kept for several sizes has the largest of theirs."""
     return lib().linear_lora_workspace_bytes(M, N, K, adapters, R)
 
 

@@ -189,7 +189,6 @@ bool fast_operands(const mbglu::LoraParams &p, int sides)
         if (!copyable(s.w, s.ldw, 2)) return false;
         if (p.adapters == 0) continue;
         // rows are read 16 bytes at a time, the last ones too
-        // rows are read 16 bytes at a time, the last ones too
         if (p.K % 8 != 0 || p.R % 8 != 0 || !copyable(s.a, s.lda, 2) || !copyable(s.b, s.ldb, 2)) return false;
         if (p.adapters > 1 && (s.a_adapter % 8 != 0 || s.b_adapter % 8 != 0)) return false;
     }
