@@ -586,7 +586,8 @@ mbglu_status moe_glu(const mbglu_bf16 *h, int64_t ldh,
  *                          read and write nothing in global memory before it
  *                          has completed.
  *   MBGLU_POLICY_PREFETCH  as PDL, and the first weight stages (gate_w, up_w
- *                          and matmul_fp8's w only; not their scales) are
+ *                          and the w of matmul_fp8 and linear_lora only; not
+ *                          scales, nor adapters) are
  *                          requested before that wait, so a
  *                          decode step's back-to-back calls overlap one call's
  *                          tail with the next call's ramp.  Contract: the

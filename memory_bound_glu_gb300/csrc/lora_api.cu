@@ -256,6 +256,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         }
         if (st != MBGLU_OK) return st;
     }
+    p.ahead = !p.early && launch_policy() == MBGLU_POLICY_PREFETCH;
     Launch c(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.items))), mbglu::kPairThreads, mbglu::kLoraSmem, stream, 2);
     const auto kernel = by_rows(l.M, l.R) ? mbglu::lora_pair_kernel<SIDES, true> : mbglu::lora_pair_kernel<SIDES, false>;
     st = launched(cudaLaunchKernelEx(&c.cfg, kernel, p, maps));

@@ -24,7 +24,7 @@
 // ranges leave partial sums, and lora_join_kernel adds them, the adapters' term and the
 // epilogue, the term in fp32 FMAs.  A decode batch of larger ranks has all of its tiles there.
 //
-// What bounds it: the weights' bytes for few rows (1 row, K = 2560, N = 9728, R = 16: 20 us,
+// What bounds it: the weights' bytes for few rows (1 row, K = 2560, N = 9728, R = 16: 19 us,
 // 14.8 of them the bytes at the copy rate), the MMAs for many (4096 rows, R = 64: 253 us, 92% of
 // them the shared product's), between them the terms of rows of several adapters, whose loads
 // eight warps per SM wait for (333 rows of 37 requests, K = 1000, N = 2504: 8 of 23 us).
@@ -58,6 +58,10 @@ struct LoraPairParams {
     float *part;             // [rest splits][tn][256]: a range's accumulators, token by token
     int prefetch;            // B into L2 ahead
     int inside;              // who forms p: LoraInside
+    // The first stages' weights are requested before the kernel before this one is done (not where
+    // that one forms p: such a call starts early as a whole): a token's call 20.3 to 18.9 us in a
+    // chain, 16 rows of rank 32 27.5 to 26.5, with few tiles in ranges no change.
+    int ahead;
     int early;               // the kernel before this one has waited for the operands
 };
 
@@ -371,8 +375,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
     const int R = p.l.R, width = SIDES * R;
     bool ok = true;
     const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
-    if (!p.early) grid_dependency_wait();
-    grid_launch_dependents();
+    if (!p.early && !(p.ahead && warp == 0)) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
+    if (p.early) grid_launch_dependents();
 
     if (warp == 0) {
         const uint32_t full0 = map_to_rank(s.full, 0);
@@ -380,6 +387,31 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
         const uint32_t bytes = static_cast<uint32_t>(plan.wt) * (SIDES == 2 ? 256u : 128u) + static_cast<uint32_t>(plan.tn) * 128u;
         int st = 0, filled = 0;
         uint32_t phase = 1;
+        if (p.ahead) {
+            const LoraTile x = lora_tile(plan, first);
+            const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2), m0 = x.t % plan.ttiles * plan.tn + rank * (plan.tn / 2);
+            filled = min(x.c1 - x.c0, kPairStages);
+            for (int k = 0; k < filled; ++k) {
+                unsigned char *d = s.stages + k * kPairStage;
+                const uint32_t bar = full0 + static_cast<uint32_t>(k) * 8u;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&s.full[k], bytes);
+                    pair_load_2d(d, &maps.w[0], (x.c0 + k) * 64, n0, bar);
+                    if (SIDES == 2) pair_load_2d(d + kPairOperand / 2, &maps.w[1], (x.c0 + k) * 64, n0, bar);
+                }
+                __syncwarp();
+            }
+            grid_dependency_wait();
+            grid_launch_dependents();
+            for (int k = 0; k < filled; ++k) {
+                if (elect_one())
+                    pair_load_2d(s.stages + k * kPairStage + kPairOperand, &maps.x, (x.c0 + k) * 64, m0, full0 + static_cast<uint32_t>(k) * 8u);
+                __syncwarp();
+            }
+            st = filled % kPairStages;
+            phase = filled == kPairStages ? 0 : 1;
+        }
+        const int done = filled;   // of the first tile
         for (int i = first; i < plan.items && ok; i += step) {
             const LoraTile x = lora_tile(plan, i);
             const int n0 = x.t / plan.ttiles * plan.wt + rank * (plan.wt / 2), m0 = x.t % plan.ttiles * plan.tn + rank * (plan.tn / 2);
@@ -387,7 +419,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
             const bool runs = p.l.blocks && x.slot < 0;
             LoraRuns run;
             if (runs && i != first) run.load(p.l, x.t % plan.ttiles * plan.tn, plan.tn);
-            for (int c = x.c0; c < x.c1; ++c) {
+            for (int c = x.c0 + (i == first ? done : 0); c < x.c1; ++c) {
                 if (!pair_wait(&s.empty[st], phase, kWaitLimitNs)) {
                     ok = false;
                     break;
