@@ -24,10 +24,28 @@ constexpr int kFewRows = 64;   // a decode batch
 //   of rank 24 the tensor cores up to some 2000 rows and little behind from there (4000 rows of
 //   60 requests 330, by rows 322); of rank 64 500 rows of 60 requests 113, by rows 363;
 //   a decode batch's larger ranks the join, which has more warps: at 48 rows of rank 64 57, in
-//   the epilogue 83; of rank 32 36 and 47; at rank 16 it is the other way round, 33 and 31, and
-//   at 128 rows, 63 and 58 of rank 32.
+//   the epilogue 83; of rank 32 36 and 47.
+// With all tiles in the join p needs no kernel of its own: the products hide it.  So smaller ranks
+// and larger batches go there too, if the tiles are one round at most (56 column tiles, rank 8:
+// 256 rows 55 and 57 us, 300 rows 68 and 61) and forming p takes a block no longer than its
+// products (hidden_values): linear, K = 4096, N = 4096, rank 16, joined and not: 8 rows 12.2 and
+// 17.9, 64 rows 13.6 and 24.1, 128 rows 17.0 and 30.5; gated, K = 2560, N = 9728: 16 rows 24.3
+// and 26.8, 160 rows of rank 32 64 and 70 (of rank 8 43 and 41); gated, K = 1024, N = 2816, 24
+// rows, beyond that bound, 12.0 and 11.0.
+// Rows and rank end where a chunk of few requests would lose more than a batch of many gains
+// (linear, K = 9728, N = 2560, rows of their own and of 4 requests): 160 rows of rank 32 40 and
+// 69, 34 and 35; 256 52 and 89, 47 and 37; 333 rows of rank 16 41 and 70, 38 and 37; 510 54 and
+// 89, 51 and 44.
 bool by_rows(int M, int R) { return M <= kFewRows || R <= 16; }
-bool by_join(int sides, int M, int R) { return M >= 2 && M <= kFewRows && R > 16 && M * sides * R > mbglu::kInsideMost; }
+int64_t hidden_values(int K, int column_tiles) { return static_cast<int64_t>(std::max(K / 512, 1)) * column_tiles * 16; }
+bool by_join(int sides, int M, int K, int R, int column_tiles)
+{
+    const int64_t values = static_cast<int64_t>(M) * sides * R, hidden = hidden_values(K, column_tiles);
+    if (M < 2 || values <= mbglu::kInsideMost) return false;
+    if (M <= kFewRows && R > 16) return true;
+    if (static_cast<int64_t>(column_tiles) * ceil_div(M, mbglu::kPairTile) > kPairs) return false;
+    return M <= kFewRows ? values <= hidden : M <= 320 && M * R <= 5120 && values <= 4 * hidden;
+}
 
 // Tiles and ranges, from the sizes alone.  The estimate (ns) of a tile's time is
 // tall_tokens' (gemm_api.cu); a join costs its launch, the partial sums' way to L2 and
@@ -42,7 +60,7 @@ mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, int R, bool may_split)
         const int64_t tiles = static_cast<int64_t>(nt) * ceil_div(M, tn);
         if (tiles > INT32_MAX / 16) continue;
         const auto tile_ns = [&](int64_t at_once, int64_t n) { return n * (77.0 + 59.0 * std::min<int64_t>(at_once, kPairs) / kPairs + 0.7 * tn) + 15.5 * tn; };
-        const bool join = may_split && by_join(sides, M, R);
+        const bool join = may_split && by_join(sides, M, K, R, nt);
         for (int split = 0; split < 2; ++split) {
             const int64_t left = join ? tiles : tiles % kPairs;
             const int64_t s = split && left > 0 ? std::min<int64_t>({std::max<int64_t>(kPairs / left, 1), std::max(chunks / 8, 1), 16}) : 1;
@@ -50,7 +68,8 @@ mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, int R, bool may_split)
             if (join ? !split : split && s < 2) continue;
             const int64_t whole = split ? tiles - left : tiles;
             double ns = (whole + kPairs - 1) / kPairs * tile_ns(whole, chunks);
-            if (split) ns += (left * s + kPairs - 1) / kPairs * tile_ns(left * s, (chunks + s - 1) / s) + 3000 + left * s * tn * 2048.0 / 4000 + left * tn * 4;
+            if (split) ns += (left * s + kPairs - 1) / kPairs * tile_ns(left * s, (chunks + s - 1) / s) + 3000 + left * s * std::min(tn, M) * 2048.0 / 4000 + left * std::min(tn, M) * 4;
+            if (may_split && whole > 0 && M >= 2 && M <= kFewRows && M * sides * R > mbglu::kInsideMost) ns += 4000;   // p's kernel, which nothing hides
             if (least == 0 || ns < least) {
                 least = ns;
                 best.tn = tn;
@@ -216,9 +235,12 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         // 10 MB of B or less (48 rows of rank 32, 60 MB: 40 us with and 36 without; of rank 16 31.5
         // and 30.7)
         p.prefetch = static_cast<int64_t>(std::min(l.M, l.adapters)) * l.N * width * 2 <= 10000000;
-        // few rows: p is formed beside the products where that costs a block no more than some
-        // rounds of loads (units of eight values)
-        if (l.M <= kFewRows && !whole && static_cast<int64_t>(l.M) * width <= 8 * 4 * 2 * kPairs)
+        // p is formed beside the products of a plan without whole tiles where that takes no longer
+        // than a kernel of its own: 64 rows of rank 64, K = 2560, N = 9728 62 us and 70; K = 1024, N =
+        // 2816, beyond the bound, 40 and 33
+        const int column_tiles = ceil_div(l.N, p.plan.wt);
+        if (!whole && (l.M <= kFewRows ? static_cast<int64_t>(l.M) * width <= 4 * hidden_values(l.K, column_tiles)
+                                       : by_join(SIDES, l.M, l.K, l.R, column_tiles)))
             p.inside = mbglu::kInsideShared;
         else if (by_rows(l.M, l.R) && p.plan.rest == 0 && static_cast<int64_t>(l.M) * width <= mbglu::kInsideMost)
             p.inside = mbglu::kInsideEach;
@@ -258,7 +280,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
     }
     p.ahead = !p.early && launch_policy() == MBGLU_POLICY_PREFETCH;
     Launch c(dim3(static_cast<unsigned>(2 * std::min(std::max(sms / 2, 1), p.plan.items))), mbglu::kPairThreads, mbglu::kLoraSmem, stream, 2);
-    const auto kernel = by_rows(l.M, l.R) ? mbglu::lora_pair_kernel<SIDES, true> : mbglu::lora_pair_kernel<SIDES, false>;
+    const auto kernel = by_rows(l.M, l.R) || p.inside != mbglu::kInsideNo ? mbglu::lora_pair_kernel<SIDES, true> : mbglu::lora_pair_kernel<SIDES, false>;
     st = launched(cudaLaunchKernelEx(&c.cfg, kernel, p, maps));
     if (st == MBGLU_OK && p.plan.rest > 0) st = launch_join<SIDES>(p, stream);
     return st;

@@ -22,7 +22,7 @@
 //
 // Tiles that would leave SM pairs without work are cut along the inner dimension: their
 // ranges leave partial sums, and lora_join_kernel adds them, the adapters' term and the
-// epilogue, the term in fp32 FMAs.  A decode batch of larger ranks has all of its tiles there.
+// epilogue, the term in fp32 FMAs.  Most decode batches have all of their tiles there.
 //
 // What bounds it: the weights' bytes for few rows (1 row, K = 2560, N = 9728, R = 16: 19 us,
 // 14.8 of them the bytes at the copy rate), the MMAs for many (4096 rows, R = 64: 253 us, 92% of

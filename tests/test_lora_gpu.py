@@ -238,6 +238,16 @@ def test_a_decode_batch_of_each_rank(M, N, K, r, sides):
     check(M, N, K, r, 64, seed=M + r, how="own", sides=sides, variant=FAST)
 
 
+# p beside the products and in a kernel of its own: both sides of the bounds on rows, rank and columns
+@pytest.mark.parametrize("sides", [1, 2])
+@pytest.mark.parametrize("M,N,K,r", [(3, 300, 520, 16), (24, 520, 1032, 16), (64, 2500, 2056, 8), (64, 300, 4104, 128), (65, 2500, 2056, 8),
+                                     (66, 700, 4104, 72), (100, 1000, 2568, 40), (160, 1300, 4104, 32), (161, 1300, 4104, 32),
+                                     (256, 2504, 1544, 8), (257, 264, 5128, 16), (320, 1300, 4104, 16), (321, 1300, 4104, 16)])
+@pytest.mark.parametrize("how", ["own", "mixed"])
+def test_a_large_decode_batch(M, N, K, r, sides, how):
+    check(M, N, K, r, 48, seed=M + r, how=how, sides=sides, variant=FAST)
+
+
 # tiles of 128 rows with one adapter, some and many; the inner dimension whole and in up to eight ranges
 @pytest.mark.parametrize("sides", [1, 2])
 @pytest.mark.parametrize("M,K,r,L,how", [(512, 72, 8, 3, "runs"), (600, 520, 128, 4, "runs"), (640, 1032, 40, 200, "mixed"),
