@@ -491,11 +491,13 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
  *   adapter   [M] int32: the row's adapter; any value outside [0, adapters) is
  *             none, and the row's second term is absent                   (read)
  *   scale     [adapters] fp32, or NULL for 1                              (read)
- *   workspace device memory of glu_lora_workspace_bytes (linear_lora_...) bytes,
- *             256-byte aligned, contents undefined afterwards; calls that may run at
- *             the same time need different ones.  Fewer rows may need more bytes (ranges
- *             of the inner dimension leave partial sums): one that is kept for several
- *             sizes has the largest of theirs
+ *   workspace device memory, 256-byte aligned, contents undefined afterwards; calls that
+ *             may run at the same time need different ones.  glu_lora_workspace_bytes
+ *             (linear_lora_...) is room for the fastest kernels of any number of rows up
+ *             to M, so one that is made for the most rows serves them all.  A smaller one
+ *             is taken as long as it holds p: 8 sides R M + M / 8 + 2048 bytes always are
+ *             enough (sides: 2, or 1 for linear_lora).  Then fewer products are cut along
+ *             the inner dimension, and sums are added in another order
  *   0 <= R <= MBGLU_LORA_MAX_RANK.  adapters == 0 or R == 0: the shared product
  *   alone; gate, up, ab, adapter and workspace are not looked at.  M == 0 or N == 0:
  *   no-op.

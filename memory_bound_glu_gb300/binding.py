@@ -756,9 +756,10 @@ def glu_lora(h, gate_w, up_w, gate_a, gate_b, up_a, up_b, adapter, scale=None, o
     gate_a[a].T) and a = adapter[m] the row's adapter; u likewise.  Any number of
     rows.  gate_a, up_a are [adapters,R,K], gate_b, up_b [adapters,N,R] (bf16, R <=
     MAX_RANK); adapter is int32 [M], a value outside [0, adapters) meaning none;
-    scale float32 [adapters] or None for 1.  The workspace is a byte tensor of
-    glu_lora_workspace_bytes(M, N, K, adapters, R) bytes, 256-byte aligned, allocated
-    here when not given.  No gradients."""
+    scale float32 [adapters] or None for 1.  The workspace is a byte tensor, 256-byte
+    aligned, of glu_lora_workspace_bytes(M, N, K, adapters, R) bytes (one for the most
+    rows serves fewer) or of less, down to 16 R M + M / 8 + 2048, which may take longer;
+    allocated here when not given.  No gradients."""
     if stream is None:
         r = (_quick_module or _quick()).glu_lora(h, gate_w, up_w, gate_a, gate_b, up_a, up_b, adapter, scale, out, _MODES[mode], workspace)
         if r is not None:
@@ -786,7 +787,8 @@ def linear_lora(x, w, a, b, adapter, scale=None, out=None, workspace=None, strea
     """x @ w.T + (scale[i] * (x @ a[i].T)) @ b[i].T, [M,N] bf16, with i = adapter[m]
     the row's adapter: one projection of glu_lora, such as the down projection.
     Arguments as there, a [adapters,R,K] and b [adapters,N,R]; the workspace is one of
-    linear_lora_workspace_bytes(M, N, K, adapters, R) bytes.  No gradients."""
+    linear_lora_workspace_bytes(M, N, K, adapters, R) bytes, or of at least 8 R M + M / 8 +
+    2048.  No gradients."""
     if stream is None:
         r = (_quick_module or _quick()).linear_lora(x, w, a, b, adapter, scale, out, workspace)
         if r is not None:
@@ -870,14 +872,14 @@ def moe_glu(h, router_w, gate_w, up_w, down_w, top_k, renormalize=True, out=None
 
 
 def glu_lora_workspace_bytes(M, N, K, adapters, R):
-    """Bytes of glu_lora's workspace (0: none needed).  Fewer rows may need more: one
-    that is kept for several sizes has the largest of theirs."""
+    """Bytes with which glu_lora takes its fastest kernels at any number of rows up to M
+    (0: none needed)."""
     return lib().glu_lora_workspace_bytes(M, N, K, adapters, R)
 
 
 def linear_lora_workspace_bytes(M, N, K, adapters, R):
-    """Bytes of linear_lora's workspace (0: none needed).  Fewer rows may need more: one
-    that is kept for several sizes has the largest of theirs."""
+    """Bytes with which linear_lora takes its fastest kernels at any number of rows up to
+    M (0: none needed)."""
     return lib().linear_lora_workspace_bytes(M, N, K, adapters, R)
 
 

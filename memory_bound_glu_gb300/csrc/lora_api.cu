@@ -17,6 +17,7 @@ constexpr int64_t kAlign = 256;
 int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
 constexpr int kFewRows = 64;   // a decode batch
+constexpr int kJoinRows = 320;
 
 // Who adds the terms of rows with adapters of their own (us at K = 2560, N = 9728, two projections):
 //   up to rank 16 the epilogue, a row of B per lane: at 100 rows of as many requests 40, on the
@@ -44,13 +45,20 @@ bool by_join(int sides, int M, int K, int R, int column_tiles)
     if (M < 2 || values <= mbglu::kInsideMost) return false;
     if (M <= kFewRows && R > 16) return true;
     if (static_cast<int64_t>(column_tiles) * ceil_div(M, mbglu::kPairTile) > kPairs) return false;
-    return M <= kFewRows ? values <= hidden : M <= 320 && M * R <= 5120 && values <= 4 * hidden;
+    return M <= kFewRows ? values <= hidden : M <= kJoinRows && M * R <= 5120 && values <= 4 * hidden;
 }
 
-// Tiles and ranges, from the sizes alone.  The estimate (ns) of a tile's time is
-// tall_tokens' (gemm_api.cu); a join costs its launch, the partial sums' way to L2 and
-// back and the adapters' terms (500 x 2560 outputs of R = 32: 24 us).
-mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, int R, bool may_split)
+// A range leaves the sums of a tile's rows, 256 outputs each.
+int64_t lora_part_bytes(int64_t ranges, int tn, int M) { return ranges * std::min(tn, M) * 1024; }
+
+// The most ranges that a tile is cut into: 8 chunks each
+int64_t most_ranges(int K) { return std::min(std::max(ceil_div(K, 64) / 8, 1), 16); }
+
+// Tiles and ranges, from the sizes and from the room for partial sums alone.  The estimate
+// (ns) of a tile's time is tall_tokens' (gemm_api.cu); a join costs its launch, the partial
+// sums' way to L2 and back and the adapters' terms (500 x 2560 outputs of R = 32: 24 us).
+// Plans of whole tiles need no room.
+mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, int R, bool may_split, int64_t room)
 {
     mbglu::LoraPlan best = {};
     double least = 0;
@@ -60,10 +68,10 @@ mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, int R, bool may_split)
         const int64_t tiles = static_cast<int64_t>(nt) * ceil_div(M, tn);
         if (tiles > INT32_MAX / 16) continue;
         const auto tile_ns = [&](int64_t at_once, int64_t n) { return n * (77.0 + 59.0 * std::min<int64_t>(at_once, kPairs) / kPairs + 0.7 * tn) + 15.5 * tn; };
-        const bool join = may_split && by_join(sides, M, K, R, nt);
+        const bool join = may_split && by_join(sides, M, K, R, nt) && lora_part_bytes(tiles, tn, M) <= room;
         for (int split = 0; split < 2; ++split) {
             const int64_t left = join ? tiles : tiles % kPairs;
-            const int64_t s = split && left > 0 ? std::min<int64_t>({std::max<int64_t>(kPairs / left, 1), std::max(chunks / 8, 1), 16}) : 1;
+            const int64_t s = split && left > 0 ? std::min({std::max<int64_t>(kPairs / left, 1), most_ranges(K), room / lora_part_bytes(left, tn, M)}) : 1;
             if (split && !may_split) continue;
             if (join ? !split : split && s < 2) continue;
             const int64_t whole = split ? tiles - left : tiles;
@@ -89,30 +97,47 @@ mbglu::LoraPlan lora_plan(int sides, int M, int N, int K, int R, bool may_split)
 
 int64_t lora_p_bytes(int sides, int M, int R) { return padded(static_cast<int64_t>(M) * sides * R * 4); }
 
-int64_t lora_part_bytes(const mbglu::LoraPlan &q) { return static_cast<int64_t>(q.rest) * q.splits * q.tn * 1024; }
+// The largest partial sums of any plan of up to M rows: ranges of less than a round of tiles, or
+// all tiles of the batches that by_join lets through.
+int64_t most_part_bytes(int sides, int M, int N, int K, int R)
+{
+    const int64_t nt = ceil_div(N, sides == 2 ? 128 : 256);
+    const int joined = std::min(M, nt * ceil_div(kJoinRows, mbglu::kPairTile) <= kPairs ? kJoinRows : nt <= kPairs ? mbglu::kPairTile : R > 16 ? kFewRows : 0);
+    int64_t most = 0;
+    for (int tn = 32; tn <= mbglu::kPairTile && (tn == 32 || tn - 32 < M); tn += 32) {
+        most = std::max(most, lora_part_bytes(std::min<int64_t>(kPairs, nt * ceil_div(M, tn) * most_ranges(K)), tn, M));
+        if (tn == 32 || tn - 32 < joined) most = std::max(most, lora_part_bytes(nt * ceil_div(joined, tn), tn, joined));
+    }
+    return most;
+}
 
 // From this many rows on p comes from lora_shrink_tc_kernel: at 500 rows of 60 requests, K =
 // 9728, the whole call takes 66 us with it and 70 without, at 1000 of 10, K = 2560, 95 and 99;
 // at 333 rows of 37 31 and 23.
 constexpr int kShrinkTcFrom = 512, kShrinkTcSplit = 8;
 
-// Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, partial sums
+// Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, then the
+// partial sums of p and of the outputs, one after the other, in what there is behind.
 struct LoraSpace {
-    int64_t terms, blocks, part, bytes;
+    int64_t terms, blocks, part;
 };
 
-LoraSpace lora_space(int sides, int M, int R, const mbglu::LoraPlan &plan)
+LoraSpace lora_space(int sides, int M, int R)
 {
     LoraSpace s = {};
     s.terms = lora_p_bytes(sides, M, R);
     s.blocks = s.terms + lora_p_bytes(sides, M, R);
     s.part = s.blocks + padded((static_cast<int64_t>(M) + mbglu::kLoraBlock - 1) / mbglu::kLoraBlock * 4);
-    // the partial sums of p and of the outputs, one after the other
-    s.bytes = s.part + padded(std::max(lora_part_bytes(plan), M >= kShrinkTcFrom ? kShrinkTcSplit * static_cast<int64_t>(M) * sides * R * 4 : 0));
     return s;
 }
 
-int64_t lora_bytes(int sides, int M, int N, int K, int R) { return lora_space(sides, M, R, lora_plan(sides, M, N, K, R, true)).bytes; }
+int64_t shrink_part_bytes(int sides, int M, int R, int split) { return split * static_cast<int64_t>(M) * sides * R * 4; }
+
+// Room for the fastest plan of any number of rows up to M.
+int64_t lora_bytes(int sides, int M, int N, int K, int R)
+{
+    return lora_space(sides, M, R).part + padded(std::max(most_part_bytes(sides, M, N, K, R), M >= kShrinkTcFrom ? shrink_part_bytes(sides, M, R, kShrinkTcSplit) : 0));
+}
 
 bool bad_rank(int adapters, int R) { return adapters < 0 || adapters > kMostSize || R < 0 || R > MBGLU_LORA_MAX_RANK; }
 
@@ -138,9 +163,10 @@ mbglu_status launch_shrink(const mbglu::LoraParams &p, int side_by_side, int mos
 
 // Blocks of a cluster split the inner dimension, so that the tiles of 128 rows fill the SMs.
 template <int SIDES>
-mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *taken, cudaStream_t stream)
+mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, int64_t room, bool *taken, cudaStream_t stream)
 {
     *taken = false;
+    if (shrink_part_bytes(SIDES, p.M, p.R, 1) > room) return MBGLU_OK;
     mbglu::ShrinkTcMaps maps;
     if (!encode_tile_map(&maps.x, p.x, p.ldx, p.M, p.K, 64, mbglu::kShrinkTcRows, 2)) return MBGLU_OK;
     for (int d = 0; d < SIDES; ++d) {
@@ -155,7 +181,7 @@ mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, bool *tak
     q.nchunk = ceil_div(p.K, 64);
     q.group = mbglu::shrink_tc_group(SIDES * p.R);
     q.split = 1;
-    while (q.split < kShrinkTcSplit && tiles * q.split * 2 <= 160 && q.nchunk >= q.split * 8) q.split *= 2;
+    while (q.split < kShrinkTcSplit && tiles * q.split * 2 <= 160 && q.nchunk >= q.split * 8 && shrink_part_bytes(SIDES, p.M, p.R, q.split * 2) <= room) q.split *= 2;
     const uint32_t stage = mbglu::shrink_tc_stage(SIDES * p.R);
     q.stages = std::min<int>(mbglu::kShrinkTcMaxStages, (200 * 1024) / static_cast<int>(stage));
     *taken = true;
@@ -215,16 +241,16 @@ bool fast_operands(const mbglu::LoraParams &p, int sides)
 }
 
 template <int SIDES>
-mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *taken, cudaStream_t stream)
+mbglu_status launch_pair(const mbglu::LoraParams &l, const mbglu::LoraPlan &plan, void *workspace, const LoraSpace &space, int64_t room, bool *taken,
+                         cudaStream_t stream)
 {
     *taken = false;
-    if (!fast_operands(l, SIDES)) return MBGLU_OK;
+    if (!fast_operands(l, SIDES) || plan.ntiles == 0) return MBGLU_OK;
     mbglu::LoraPairParams p = {};
     p.l = l;
-    p.plan = lora_plan(SIDES, l.M, l.N, l.K, l.R, l.adapters > 0);
-    if (p.plan.ntiles == 0) return MBGLU_OK;
+    p.plan = plan;
+    p.rows = std::min(plan.tn, l.M);
     char *ws = static_cast<char *>(workspace);
-    const LoraSpace space = lora_space(SIDES, l.M, l.R, p.plan);
     const bool adapted = l.adapters > 0, whole = p.plan.whole > 0;
     mbglu::LoraMaps maps;
     for (int d = 0; d < SIDES; ++d)
@@ -269,7 +295,7 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, void *workspace, bool *take
         // that the rows are read once or twice
         p.early = launch_policy() != MBGLU_POLICY_SERIAL;
         bool tc = false;
-        if (l.M >= kShrinkTcFrom) st = launch_shrink_tc<SIDES>(p.l, p.part, &tc, stream);
+        if (l.M >= kShrinkTcFrom) st = launch_shrink_tc<SIDES>(p.l, p.part, room, &tc, stream);
         if (st == MBGLU_OK && !tc) {
             if (l.M <= kFewRows)
                 st = launch_shrink<SIDES, 1, 1, 5>(p.l, std::min(l.M, 16), 1024, stream);
@@ -311,10 +337,12 @@ mbglu_status run(mbglu::LoraParams &p, void *workspace, size_t workspace_bytes, 
         for (int d = 0; d < SIDES; ++d) ok = ok && aligned(p.side[d].a, 2) && aligned(p.side[d].b, 2);
     }
     if (!ok) return MBGLU_ERR_ALIGN;
-    const int64_t need = adapted ? lora_bytes(SIDES, M, N, K, R) : 0;
-    if (workspace_bytes < static_cast<size_t>(need)) return MBGLU_ERR_SHAPE;
+    // p and its table have to fit; partial sums get what is left, up to what they can use
+    const LoraSpace space = lora_space(SIDES, M, R);
+    const int64_t has = adapted ? std::min<int64_t>(std::min<size_t>(workspace_bytes, INT64_MAX), lora_bytes(SIDES, M, N, K, R)) : 0;
+    if (adapted && has < space.part) return MBGLU_ERR_SHAPE;
     const void *outs[2] = {p.out, workspace};
-    const int64_t outb[2] = {extent(M, N, p.ldo, 2), need};
+    const int64_t outb[2] = {extent(M, N, p.ldo, 2), has};
     if (overlaps(outs[0], outb[0], outs[1], outb[1])) return MBGLU_ERR_ALIAS;
     for (int i = 0; i < 2; ++i) {
         if (overlaps(outs[i], outb[i], p.x, extent(M, K, p.ldx, 2))) return MBGLU_ERR_ALIAS;
@@ -331,7 +359,8 @@ mbglu_status run(mbglu::LoraParams &p, void *workspace, size_t workspace_bytes, 
     }
     p.p = static_cast<float *>(workspace);   // the kernels for any alignment need no more
     bool taken = false;
-    mbglu_status st = launch_pair<SIDES>(p, workspace, &taken, stream);
+    const int64_t room = adapted ? has - space.part : 0;
+    mbglu_status st = launch_pair<SIDES>(p, lora_plan(SIDES, M, N, K, R, adapted, room), workspace, space, room, &taken, stream);
     if (taken || st != MBGLU_OK) {
         if (st == MBGLU_OK) set_last_variant(kLoraPair);
         return st;

@@ -55,7 +55,8 @@ struct LoraMaps {
 struct LoraPairParams {
     LoraParams l;
     LoraPlan plan;
-    float *part;             // [rest splits][tn][256]: a range's accumulators, token by token
+    float *part;             // [rest splits][rows][256]: a range's accumulators, token by token
+    int rows;                // of a tile: tn, or all that there are
     int prefetch;            // B into L2 ahead
     int inside;              // who forms p: LoraInside
     // The first stages' weights are requested before the kernel before this one is done (not where
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) lora_pair_kernel(const LoraPa
                 }
                 const int tokens = ok ? p.l.M - m0 - j : 0;
                 if (x.slot >= 0) {
-                    float *o = p.part + (static_cast<int64_t>(x.slot) * plan.tn + half * (plan.tn / 2) + j) * 256 + rank * 128 + q * 32 + lane;
+                    float *o = p.part + (static_cast<int64_t>(x.slot) * p.rows + half * (plan.tn / 2) + j) * 256 + rank * 128 + q * 32 + lane;
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                         if (k < tokens) __stcg(o + k * 256, __uint_as_float(r[k]));
@@ -690,9 +691,9 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraPairParams p)
         // output w of the tile: a CTA holds wt / 2 of them, in dual tiles from lanes 0 and 64 on
         const int rank = w + lane >= plan.wt / 2 ? 1 : 0, at = rank * 128 + w + lane - rank * (plan.wt / 2);
         float acc[TOKENS][SIDES] = {};
-        const float *q = p.part + (static_cast<int64_t>(tile) * plan.tn + j0) * 256 + at;
+        const float *q = p.part + (static_cast<int64_t>(tile) * p.rows + j0) * 256 + at;
 #pragma unroll 4
-        for (int s = 0; s < plan.splits; ++s, q += static_cast<int64_t>(plan.rest) * plan.tn * 256)
+        for (int s = 0; s < plan.splits; ++s, q += static_cast<int64_t>(plan.rest) * p.rows * 256)
 #pragma unroll
             for (int k = 0; k < TOKENS; ++k)
 #pragma unroll
