@@ -114,7 +114,8 @@ int64_t most_part_bytes(int sides, int M, int N, int K, int R)
 // From this many rows on p comes from lora_shrink_tc_kernel: at 500 rows of 60 requests, K =
 // 9728, the whole call takes 66 us with it and 70 without, at 1000 of 10, K = 2560, 95 and 99;
 // at 333 rows of 37 31 and 23.
-constexpr int kShrinkTcFrom = 512, kShrinkTcSplit = 8;
+constexpr int kShrinkTcFrom = 512, kShrinkTcSplit = 8;   // blocks that share a tile
+constexpr int kShrinkTcBlocks = 160;                     // and at most in all, where tiles are shared
 
 // Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, then the
 // partial sums of p and of the outputs, one after the other, in what there is behind.
@@ -131,12 +132,15 @@ LoraSpace lora_space(int sides, int M, int R)
     return s;
 }
 
-int64_t shrink_part_bytes(int sides, int M, int R, int split) { return split * static_cast<int64_t>(M) * sides * R * 4; }
+// Partial sums of p beside the first block's, which lie where p does: of `split` blocks.
+int64_t shrink_part_bytes(int sides, int M, int R, int split) { return (split - 1) * static_cast<int64_t>(M) * sides * R * 4; }
 
 // Room for the fastest plan of any number of rows up to M.
 int64_t lora_bytes(int sides, int M, int N, int K, int R)
 {
-    return lora_space(sides, M, R).part + padded(std::max(most_part_bytes(sides, M, N, K, R), M >= kShrinkTcFrom ? shrink_part_bytes(sides, M, R, kShrinkTcSplit) : 0));
+    // of more rows fewer blocks share a tile (kShrinkTcBlocks), and their parts are less than these
+    const int rows = M < kShrinkTcFrom ? 0 : std::min(M, kShrinkTcBlocks / kShrinkTcSplit * mbglu::kShrinkTcRows);
+    return lora_space(sides, M, R).part + padded(std::max(most_part_bytes(sides, M, N, K, R), shrink_part_bytes(sides, rows, R, kShrinkTcSplit)));
 }
 
 bool bad_rank(int adapters, int R) { return adapters < 0 || adapters > kMostSize || R < 0 || R > MBGLU_LORA_MAX_RANK; }
@@ -166,7 +170,6 @@ template <int SIDES>
 mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, int64_t room, bool *taken, cudaStream_t stream)
 {
     *taken = false;
-    if (shrink_part_bytes(SIDES, p.M, p.R, 1) > room) return MBGLU_OK;
     mbglu::ShrinkTcMaps maps;
     if (!encode_tile_map(&maps.x, p.x, p.ldx, p.M, p.K, 64, mbglu::kShrinkTcRows, 2)) return MBGLU_OK;
     for (int d = 0; d < SIDES; ++d) {
@@ -181,7 +184,7 @@ mbglu_status launch_shrink_tc(const mbglu::LoraParams &p, float *part, int64_t r
     q.nchunk = ceil_div(p.K, 64);
     q.group = mbglu::shrink_tc_group(SIDES * p.R);
     q.split = 1;
-    while (q.split < kShrinkTcSplit && tiles * q.split * 2 <= 160 && q.nchunk >= q.split * 8 && shrink_part_bytes(SIDES, p.M, p.R, q.split * 2) <= room) q.split *= 2;
+    while (q.split < kShrinkTcSplit && tiles * q.split * 2 <= kShrinkTcBlocks && q.nchunk >= q.split * 8 && shrink_part_bytes(SIDES, p.M, p.R, q.split * 2) <= room) q.split *= 2;
     const uint32_t stage = mbglu::shrink_tc_stage(SIDES * p.R);
     q.stages = std::min<int>(mbglu::kShrinkTcMaxStages, (200 * 1024) / static_cast<int>(stage));
     *taken = true;

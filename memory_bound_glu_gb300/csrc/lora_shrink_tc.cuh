@@ -30,7 +30,7 @@ struct ShrinkTcMaps {
 
 struct ShrinkTcParams {
     LoraParams l;
-    float *part;             // [split][M][sides R]
+    float *part;             // [split - 1][M][sides R]: a block's partial sums; the first block's lie in p
     int split, stages, nchunk;
     int group;               // adapters at a time
 };
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
             if (lane == 0 && in) p.l.blocks[m0 / kLoraBlock + q] = (in & ~same) ? kMixed : first;
         }
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        float *dst = p.part + (static_cast<int64_t>(rank) * p.l.M + m0 + row) * width;
+        float *dst = (rank == 0 ? p.l.p : p.part + static_cast<int64_t>(rank - 1) * p.l.M * width) + (m0 + row) * width;
         uint32_t buf = 0, acc_phase = 0;
         int a[kShrinkTcGroup];
         while (ok && adapters.next(a, p.group) > 0) {
@@ -265,7 +265,9 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
         for (int i = 0; i < p.split; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float4 x = row[h] >= 0 ? __ldcg(reinterpret_cast<const float4 *>(p.part + i * stride + at[h])) : make_float4(0, 0, 0, 0);
+                // of p a thread reads what it writes itself below
+                const float *from = i == 0 ? p.l.p : p.part + (i - 1) * stride;
+                const float4 x = row[h] >= 0 ? __ldcg(reinterpret_cast<const float4 *>(from + at[h])) : make_float4(0, 0, 0, 0);
                 v[h] = make_float4(v[h].x + x.x, v[h].y + x.y, v[h].z + x.z, v[h].w + x.w);
             }
 #pragma unroll

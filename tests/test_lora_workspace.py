@@ -26,6 +26,15 @@ def test_more_rows_need_no_less(N, K, r, sides):
     assert all(s >= least(sides, M, r) - 2048 for M, s in enumerate(sizes[:699], 1))
 
 
+@pytest.mark.parametrize("sides", [1, 2])
+@pytest.mark.parametrize("r", [8, 64])
+def test_many_rows_need_room_for_p_alone(r, sides):
+    """Partial sums of p are for as many blocks as there are SMs, whatever the rows: 30000 more
+    rows need no more than their own p, its terms and entries of the table."""
+    few, many = (SIZES[sides](M, 2560, 2560, 30, r) for M in (30000, 60000))
+    assert many - few <= least(sides, 30000, r)
+
+
 def test_less_than_p_is_refused():
     """Pointers are never dereferenced: the calls end in the host's checks."""
     x, w, u, a, b, i, o, ws = (0x7F0000000000 + j * (1 << 36) for j in range(8))
