@@ -172,9 +172,9 @@ def run(state):
                                        renormalize=case["renormalize"], workspace=s["workspace"])
         return dict(out=out, ids=ids, weights=weights)
     if case["op"] == "linear_lora":
-        return dict(out=mb.linear_lora(s["x"], s["w"], s["a"], s["b"], s["adapter"], s["scale"]))
+        return dict(out=mb.linear_lora(s["x"], s["w"], s["a"], s["b"], s["adapter"], s["scale"], workspace=s["workspace"]))
     return dict(out=mb.glu_lora(s["x"], s["wgate"], s["wup"], s["agate"], s["bgate"], s["aup"], s["bup"], s["adapter"],
-                                s["scale"], mode=case["mode"]))
+                                s["scale"], mode=case["mode"], workspace=s["workspace"]))
 
 
 def work(case):
