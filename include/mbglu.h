@@ -503,7 +503,9 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
  *   no-op.
  * A row's result depends on that row, its own adapter and the shared weights only:
  * what other rows' adapters hold, infinities and NaN too, does not reach it.  Neither
- * the batch's size nor a row's place changes which adapter it gets.  Rows of one
+ * the batch's size nor a row's place changes which adapter it gets, but how rows of one
+ * adapter lie together decides how their sums are formed, and so their rounding and,
+ * where the row's own p or B[a] is infinite, whether infinity or NaN comes out.  Rows of one
  * adapter may lie anywhere; next to one another they are faster.
  * The fast kernels want h, the weights, A and B 16-byte aligned with row and adapter
  * strides that are multiples of 8 elements, and K and R multiples of 8; other

@@ -184,10 +184,8 @@ __device__ __forceinline__ void lora_term(const LoraParams &p, int mine, int d, 
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const float4 x = v[g][c];
-                    h[g][0] = pack_bf16x2(x.x, x.y);
-                    h[g][1] = pack_bf16x2(x.z, x.w);
-                    l[g][0] = pack_bf16x2(x.x - bf16_lo(h[g][0]), x.y - bf16_hi(h[g][0]));
-                    l[g][1] = pack_bf16x2(x.z - bf16_lo(h[g][1]), x.w - bf16_hi(h[g][1]));
+                    split_bf16x2(x.x, x.y, h[g][0], l[g][0]);
+                    split_bf16x2(x.z, x.w, h[g][1], l[g][1]);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {

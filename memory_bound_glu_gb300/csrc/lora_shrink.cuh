@@ -125,9 +125,10 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
                 v *= scale;
                 const int64_t at = (m0 + r) * width + which * p.R + j0 + j;
                 p.p[at] = v;
-                const uint16_t hi = f32_to_bf16(v);
-                p.terms[at] = hi;
-                p.terms[at + p.M * static_cast<int64_t>(width)] = f32_to_bf16(v - bf16_to_f32(hi));
+                uint32_t hi, lo;
+                split_bf16x2(v, 0.0f, hi, lo);
+                p.terms[at] = static_cast<uint16_t>(hi);
+                p.terms[at + p.M * static_cast<int64_t>(width)] = static_cast<uint16_t>(lo);
             };
             for (int e = threadIdx.x; e < kRows * kCols; e += kShrinkWarps * 32) {
                 const int r = e / kCols, j = e % kCols;

@@ -276,10 +276,11 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
             const float s = scales[row[h]];
             const float4 w = make_float4(v[h].x * s, v[h].y * s, v[h].z * s, v[h].w * s);
             *reinterpret_cast<float4 *>(p.l.p + at[h]) = w;
-            const uint32_t h0 = pack_bf16x2(w.x, w.y), h1 = pack_bf16x2(w.z, w.w);
-            *reinterpret_cast<uint2 *>(p.l.terms + at[h]) = make_uint2(h0, h1);
-            *reinterpret_cast<uint2 *>(p.l.terms + at[h] + stride) =
-                make_uint2(pack_bf16x2(w.x - bf16_lo(h0), w.y - bf16_hi(h0)), pack_bf16x2(w.z - bf16_lo(h1), w.w - bf16_hi(h1)));
+            uint2 hi, lo;
+            split_bf16x2(w.x, w.y, hi.x, lo.x);
+            split_bf16x2(w.z, w.w, hi.y, lo.y);
+            *reinterpret_cast<uint2 *>(p.l.terms + at[h]) = hi;
+            *reinterpret_cast<uint2 *>(p.l.terms + at[h] + stride) = lo;
         }
     }
 }
