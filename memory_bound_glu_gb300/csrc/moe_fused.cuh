@@ -431,12 +431,13 @@ __device__ __forceinline__ bool moe_choose(const MoeParams &p, MoeShared &s, int
 }
 
 // The activation as two bf16 terms, so that the tensor cores' operand is off by 2^-18 and not
-// by 2^-9; an infinite one has no second term.
+// by 2^-9.
 __device__ __forceinline__ void moe_act(float g, float u, uint16_t &hi, uint16_t &lo)
 {
-    const float a = silu_f32(g) * u;
-    hi = f32_to_bf16(a);
-    lo = f32_to_bf16(isfinite(bf16_to_f32(hi)) ? a - bf16_to_f32(hi) : 0.0f);
+    uint32_t h, l;
+    split_bf16x2(silu_f32(g) * u, 0.0f, h, l);
+    hi = static_cast<uint16_t>(h);
+    lo = static_cast<uint16_t>(l);
 }
 
 static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const MoeParams p, const __grid_constant__ MoeMaps maps)
