@@ -556,8 +556,10 @@ mbglu_status linear_lora(const mbglu_bf16 *x, int64_t ldx,
  *   workspace  device memory of moe_glu_workspace_bytes(...) bytes, 256-byte
  *              aligned, its first MBGLU_MOE_COUNTER_BYTES ALL ZERO before its first
  *              use; every completed call leaves those zero, the rest undefined.  Calls
- *              that may run at the same time need different ones.  After a call whose
- *              bounded wait gave up (mbglu_read_device_error), zero them again.
+ *              that may run at the same time need different ones.  A call that finds
+ *              other counters, or whose bounded wait gives up, sets the device error word
+ *              (mbglu_read_device_error), leaves its outputs undefined and the counters
+ *              not zero, so that later calls fail too: zero them again.
  *   0 <= T <= MBGLU_MAX_M, 1 <= E <= MBGLU_MOE_MAX_EXPERTS, 1 <= top_k <=
  *   min(E, MBGLU_MOE_MAX_TOP_K), N >= 0, K >= 0.  T == 0: no-op.  N == 0: out = 0.
  * A token's choice does not depend on the others, and neither does its result but

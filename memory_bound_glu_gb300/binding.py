@@ -814,7 +814,8 @@ def linear_lora(x, w, a, b, adapter, scale=None, out=None, workspace=None, strea
 
 def new_moe_workspace(T, E, top_k, N, K, device=None):
     """A workspace for moe_glu calls of up to T tokens at these sizes (one per
-    concurrently running stream), its counters zeroed."""
+    concurrently running stream), its counters zeroed.  After an error that
+    read_device_error reports, its first MOE_COUNTER_BYTES have to be zeroed again."""
     need = moe_glu_workspace_bytes(T, E, top_k, N, K)
     ws = torch.empty(max(need, MOE_COUNTER_BYTES), dtype=torch.uint8, device=device or "cuda")
     ws[:MOE_COUNTER_BYTES].zero_()
@@ -830,7 +831,9 @@ def moe_glu(h, router_w, gate_w, up_w, down_w, top_k, renormalize=True, out=None
     not; out is the weighted sum of (SiLU(h @ gate_w[e].T) * (h @ up_w[e].T)) @
     down_w[e].T.  router_w is [E,K], gate_w and up_w [E,N,K], down_w [E,K,N].
     The workspace (new_moe_workspace(T, E, top_k, N, K), which a decode loop keeps)
-    is allocated and its counters are zeroed here when not given.  No gradients."""
+    is allocated and its counters are zeroed here when not given; after a call that sets
+    the device error word (read_device_error) one that is kept has to be zeroed again
+    before calls on it succeed.  No gradients."""
     if stream is None:
         r = (_quick_module or _quick()).moe_glu(h, router_w, gate_w, up_w, down_w, top_k, bool(renormalize), out, ids, weights, workspace)
         if r is not None:

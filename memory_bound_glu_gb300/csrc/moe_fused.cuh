@@ -30,8 +30,8 @@
 //
 // Roles (384 threads): warp 0 copies weights, warp 2 the tokens' side, warp 1 owns the
 // tensor memory and issues the MMAs, warps 4-7 read accumulators, warps 4-11 do 4 and 6,
-// all warps 1 and 2.  Every wait is bounded; after one gives up each role ends without
-// touching memory and the counters keep what they hold.
+// all warps 1 and 2.  Every wait is bounded; after one gives up, or finds a counter that was not 0
+// at the start, each role ends without touching memory, and the counters are marked.
 #pragma once
 #include "dense_common.cuh"
 #include "moe_route.cuh"
@@ -63,7 +63,7 @@ struct MoeParams {
     uint16_t *out;
     int32_t *ids;            // or null
     float *weights;          // or null
-    uint32_t *counters;      // five barriers and the exit, all 0 at the start and at the end
+    uint32_t *counters;      // five barriers and the exit (the fifth), all 0 at the start and at the end
     int32_t *chosen;         // [T][top_k]: what the blocks choose, where each has tokens of its own
     float *chosen_weight;
     float *logits;           // [T][E]
@@ -123,7 +123,8 @@ __device__ __forceinline__ uint32_t add_acq_rel_gpu(uint32_t *p, uint32_t v)
 }
 
 // One thread per block, after a barrier of the threads whose writes it publishes; and before
-// one of those that read what the other blocks published.
+// one of those that read what the other blocks published.  A counter that goes beyond the blocks
+// did not begin at 0 (an earlier call gave up, or another use of the workspace wrote there): false.
 __device__ __forceinline__ void grid_arrive(uint32_t *counter)
 {
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
@@ -131,7 +132,9 @@ __device__ __forceinline__ void grid_arrive(uint32_t *counter)
 __device__ __forceinline__ bool grid_wait(const uint32_t *counter, uint64_t limit_ns)
 {
     uint64_t t0 = 0;
-    for (uint32_t i = 1; ld_acquire_gpu(counter) < gridDim.x; ++i)
+    for (uint32_t i = 1;; ++i) {
+        const uint32_t v = ld_acquire_gpu(counter);
+        if (v >= gridDim.x) return v == gridDim.x;
         if ((i & 63u) == 0) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0)
@@ -139,7 +142,15 @@ __device__ __forceinline__ bool grid_wait(const uint32_t *counter, uint64_t limi
             else if (now - t0 > limit_ns)
                 return false;
         }
-    return true;
+    }
+}
+
+// A block that fails marks every counter: the other blocks' barriers end at once, and so does any
+// later call on the workspace, until its counters are zeroed.
+constexpr int kMoeCounters = 6;
+__device__ __forceinline__ void grid_fail(uint32_t *counters)
+{
+    for (int i = 0; i < kMoeCounters; ++i) atomicOr(counters + i, 0x80000000u);
 }
 
 // The units of a phase: `chosen` experts x `tiles` x `chunks`, cut into ranges for the
@@ -368,7 +379,8 @@ __device__ __forceinline__ bool moe_choose(const MoeParams &p, MoeShared &s, int
         __syncthreads();
         if (s.failed != 0) return false;
         for (int i = threadIdx.x; i < slots; i += kMoeThreads) {
-            s.id[i] = static_cast<uint16_t>(__ldcg(p.chosen + i));
+            // behind a barrier that did not hold anything may lie there: an index of the tables all the same
+            s.id[i] = static_cast<uint16_t>(min(static_cast<uint32_t>(__ldcg(p.chosen + i)), static_cast<uint32_t>(p.E - 1)));
             s.weight[i] = __ldcg(p.chosen_weight + i);
         }
         __syncthreads();
@@ -864,9 +876,20 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
         tc_fence_after();
         tmem_dealloc(tmem, kMoeCols);
     }
-    // the last block to leave: everyone has passed every barrier
-    if (threadIdx.x == 0 && s.failed == 0 && add_acq_rel_gpu(p.counters + 4, 1u) == gridDim.x - 1)
-        for (int i = 0; i < 6; ++i) p.counters[i] = 0;
+    if (threadIdx.x == 0) {
+        if (s.failed != 0) {
+            grid_fail(p.counters);
+        } else {
+            // the last block to leave: everyone has passed every barrier
+            const uint32_t left = add_acq_rel_gpu(p.counters + 4, 1u);
+            if (left == gridDim.x - 1) {
+                for (int i = 0; i < kMoeCounters; ++i) p.counters[i] = 0;
+            } else if (left >= gridDim.x) {
+                atomicExch(&g_dense_error, kErrTimeout);
+                grid_fail(p.counters);
+            }
+        }
+    }
 }
 
 }  // namespace mbglu
