@@ -81,7 +81,10 @@ struct MoeParams {
 struct alignas(16) MoeShared {
     uint64_t weights_full[kMoeMaxStages], tokens_full[kMoeMaxStages], empty[kMoeMaxStages];
     uint64_t acc_full[2], acc_empty[2], act_ready, done;
-    uint32_t tmem, failed;
+    uint32_t tmem, failed;                       // failed: any thread sets it at any time
+    // The same for those that meet at named barriers and have to leave together: written only in
+    // front of the barrier behind which they read it.
+    uint32_t phase_failed, tile_failed;
     int active, pad_;
     uint64_t mask[kMoeMaxExperts];               // tokens that chose the expert (little-endian halves are set)
     alignas(16) uint32_t key[kMoeKeys];          // the logits that the block orders
@@ -452,6 +455,14 @@ __device__ __forceinline__ void moe_act(float g, float u, uint16_t &hi, uint16_t
     lo = static_cast<uint16_t>(l);
 }
 
+// A warp, before its part of 5: the activation is there, in every lane alike; false after a failure.
+// As long as the barriers of 3 and 4 take at most.
+__device__ __forceinline__ bool moe_act_ready(MoeShared &s)
+{
+    const bool there = pair_wait(&s.act_ready, 0, 4 * kWaitLimitNs);
+    return __all_sync(0xffffffffu, there && *reinterpret_cast<volatile uint32_t *>(&s.failed) == 0);
+}
+
 static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const MoeParams p, const __grid_constant__ MoeMaps maps)
 {
     extern __shared__ unsigned char moe_raw[];
@@ -479,7 +490,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
         }
         mbar_init(&s.act_ready, 1);
         mbar_init(&s.done, 1);
-        s.failed = 0;
+        s.failed = s.phase_failed = s.tile_failed = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -554,7 +565,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
         for (int second = 0; second < 2 && ok; ++second) {
             const MoeUnits &units = second ? down : gated;
             if (second) {
-                ok = pair_wait(&s.act_ready, 0, 2 * kWaitLimitNs) && *reinterpret_cast<volatile uint32_t *>(&s.failed) == 0;
+                ok = moe_act_ready(s);
                 fence_proxy_async_all();
                 if (!ok) break;
             }
@@ -598,6 +609,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
         const uint64_t a0 = smem_desc_sw128(ring);
         for (int second = 0; second < 2 && ok; ++second) {
             const MoeUnits &units = second ? down : gated;
+            if (second && !(ok = moe_act_ready(s))) break;
             MoeWalk w(units);
             while (w.left > 0 && ok) {
                 const uint32_t run = w.run(units);
@@ -609,8 +621,7 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                     break;
                 }
                 for (uint32_t c = 0; c < run; ++c) {
-                    // the second phase's tokens come only after two barriers
-                    if (!pair_wait(&s.weights_full[st], phase, kWaitLimitNs) || !pair_wait(&s.tokens_full[st], phase, 4 * kWaitLimitNs)) {
+                    if (!pair_wait(&s.weights_full[st], phase, kWaitLimitNs) || !pair_wait(&s.tokens_full[st], phase, kWaitLimitNs)) {
                         ok = false;
                         break;
                     }
@@ -660,9 +671,9 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                     const int first = s.first[w.expert], count = s.first[w.expert + 1] - first;
                     ok = __all_sync(0xffffffffu, pair_wait(&s.acc_full[buf], acc_phase, 4 * kWaitLimitNs));
                     if (!second && units.whole) {   // the four warps meet below: they go on together, or none does
-                        if (!ok) s.failed = 1;
+                        if (!ok) s.tile_failed = 1;   // the block's only tile of this phase
                         bar_sync_named(2, 128);
-                        ok = *reinterpret_cast<volatile uint32_t *>(&s.failed) == 0;
+                        ok = *reinterpret_cast<volatile uint32_t *>(&s.tile_failed) == 0;
                     }
                     if (!ok) break;
                     tc_fence_after();
@@ -758,9 +769,10 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
             if (me == 0 && lane == 0) {
                 grid_arrive(p.counters + 1 + 2 * second);   // after a failure too: the others need not wait
                 if (!grid_wait(p.counters + 1 + 2 * second, 2 * kWaitLimitNs)) s.failed = 1;
+                s.phase_failed = *reinterpret_cast<volatile uint32_t *>(&s.failed);
             }
             bar_sync_named(1, sums * 32);
-            ok = *reinterpret_cast<volatile uint32_t *>(&s.failed) == 0;
+            ok = *reinterpret_cast<volatile uint32_t *>(&s.phase_failed) == 0;
             if (!second && units.whole) {
                 if (me == 0 && lane == 0) {
                     fence_proxy_async_all();
@@ -800,9 +812,12 @@ static __global__ void __launch_bounds__(kMoeThreads, 1) moe_fused_kernel(const 
                 if (me == 0 && lane == 0) {
                     grid_arrive(p.counters + 2);
                     if (!grid_wait(p.counters + 2, 2 * kWaitLimitNs)) s.failed = 1;
+                    s.phase_failed = *reinterpret_cast<volatile uint32_t *>(&s.failed);
                     fence_proxy_async_all();
                     mbar_arrive(&s.act_ready);
                 }
+                bar_sync_named(1, sums * 32);
+                ok = *reinterpret_cast<volatile uint32_t *>(&s.phase_failed) == 0;
             } else {
                 // 6: the weighted sum of a token's 128 columns: a team of warps, each of which takes
                 // every team-th expert, four of them at a time

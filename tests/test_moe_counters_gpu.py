@@ -68,3 +68,20 @@ def test_other_calls_are_not_affected():
     Q.assert_moe(mb.moe_glu(*args, 3, workspace=good), *args, 3, True)
     Q.assert_moe(mb.moe_glu(*args, 3), *args, 3, True)
     assert mb.read_device_error() == 0
+
+
+# several pieces of a tile per block, and one tile per block; each barrier by itself: after the gated
+# products, after the activation (the first of them only), after the down products, and the exit
+@pytest.mark.parametrize("T,E,k,N,K,counter", [(40, 20, 3, 136, 264, 1), (40, 20, 3, 136, 264, 2), (40, 20, 3, 136, 264, 3), (40, 20, 3, 136, 264, 4),
+                                               (1, 16, 8, 768, 520, 1), (1, 16, 8, 768, 520, 3), (1, 16, 8, 768, 520, 4)])
+def test_each_counter(T, E, k, N, K, counter):
+    """All roles of all blocks leave together."""
+    args = operands(T, E, N, K)
+    ws = mb.new_moe_workspace(T, E, k, N, K)
+    counters = ws[:mb.MOE_COUNTER_BYTES].view(torch.int32)
+    counters[counter] = 1000
+    mb.moe_glu(*args, k, workspace=ws)
+    assert mb.read_device_error() == TIMEOUT
+    counters.zero_()
+    Q.assert_moe(mb.moe_glu(*args, k, workspace=ws), *args, k, True)
+    assert mb.read_device_error() == 0 and (counters == 0).all()
