@@ -497,7 +497,9 @@ mbglu_status matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int
  *             to M, so one that is made for the most rows serves them all.  A smaller one
  *             is taken as long as it holds p: 8 sides R M + M / 8 + 2048 bytes always are
  *             enough (sides: 2, or 1 for linear_lora).  Then fewer products are cut along
- *             the inner dimension, and sums are added in another order
+ *             the inner dimension, and sums are added in another order.  Its first
+ *             MBGLU_MOE_COUNTER_BYTES stay as they are: one buffer may serve these calls and
+ *             moe_glu's in turn on a stream
  *   0 <= R <= MBGLU_LORA_MAX_RANK.  adapters == 0 or R == 0: the shared product
  *   alone; gate, up, ab, adapter and workspace are not looked at.  M == 0 or N == 0:
  *   no-op.
@@ -556,7 +558,8 @@ mbglu_status linear_lora(const mbglu_bf16 *x, int64_t ldx,
  *   workspace  device memory of moe_glu_workspace_bytes(...) bytes, 256-byte
  *              aligned, its first MBGLU_MOE_COUNTER_BYTES ALL ZERO before its first
  *              use; every completed call leaves those zero, the rest undefined.  Calls
- *              that may run at the same time need different ones.  A call that finds
+ *              that may run at the same time need different ones, and other functions'
+ *              calls but glu_lora's and linear_lora's always do.  A call that finds
  *              other counters, or whose bounded wait gives up, sets the device error word
  *              (mbglu_read_device_error), leaves its outputs undefined and the counters
  *              not zero, so that later calls fail too: zero them again.

@@ -117,16 +117,18 @@ int64_t most_part_bytes(int sides, int M, int N, int K, int R)
 constexpr int kShrinkTcFrom = 512, kShrinkTcSplit = 8;   // blocks that share a tile
 constexpr int kShrinkTcBlocks = 160;                     // and at most in all, where tiles are shared
 
-// Places of the workspace, in bytes: p, its two terms, the table of 32-row blocks, then the
-// partial sums of p and of the outputs, one after the other, in what there is behind.
+// Places of the workspace, in bytes: moe_glu's counters, which stay as they are (a decode loop may
+// keep one buffer for both), p, its two terms, the table of 32-row blocks, then the partial sums
+// of p and of the outputs, one after the other, in what there is behind.
 struct LoraSpace {
-    int64_t terms, blocks, part;
+    int64_t p, terms, blocks, part;
 };
 
 LoraSpace lora_space(int sides, int M, int R)
 {
     LoraSpace s = {};
-    s.terms = lora_p_bytes(sides, M, R);
+    s.p = MBGLU_MOE_COUNTER_BYTES;
+    s.terms = s.p + lora_p_bytes(sides, M, R);
     s.blocks = s.terms + lora_p_bytes(sides, M, R);
     s.part = s.blocks + padded((static_cast<int64_t>(M) + mbglu::kLoraBlock - 1) / mbglu::kLoraBlock * 4);
     return s;
@@ -273,7 +275,6 @@ mbglu_status launch_pair(const mbglu::LoraParams &l, const mbglu::LoraPlan &plan
             p.inside = mbglu::kInsideShared;
         else if (by_rows(l.M, l.R) && p.plan.rest == 0 && static_cast<int64_t>(l.M) * width <= mbglu::kInsideMost)
             p.inside = mbglu::kInsideEach;
-        p.l.p = reinterpret_cast<float *>(ws);
         p.l.terms = reinterpret_cast<uint16_t *>(ws + space.terms);
         p.part = reinterpret_cast<float *>(ws + space.part);
         if (whole && p.inside == mbglu::kInsideNo) {   // tiles in ranges leave the adapters' term to the join
@@ -360,7 +361,7 @@ mbglu_status run(mbglu::LoraParams &p, void *workspace, size_t workspace_bytes, 
                         overlaps(outs[i], outb[i], p.scale, p.scale ? static_cast<int64_t>(p.adapters) * 4 : 0)))
             return MBGLU_ERR_ALIAS;
     }
-    p.p = static_cast<float *>(workspace);   // the kernels for any alignment need no more
+    p.p = adapted ? reinterpret_cast<float *>(static_cast<char *>(workspace) + space.p) : nullptr;   // the kernels for any alignment need no more
     bool taken = false;
     const int64_t room = adapted ? has - space.part : 0;
     mbglu_status st = launch_pair<SIDES>(p, lora_plan(SIDES, M, N, K, R, adapted, room), workspace, space, room, &taken, stream);

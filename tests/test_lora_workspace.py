@@ -113,3 +113,26 @@ def test_a_small_workspace_in_a_graph():
         workspace.fill_(255)
         graph.replay()
         Q.assert_glu_lora(out, (x, *w, *ab, idx, scale))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,r,pad", [(1, 264, 520, 16, 0), (8, 2560, 2056, 16, 0), (48, 2504, 264, 64, 0), (300, 264, 136, 24, 0), (700, 520, 264, 40, 0),
+                                         (20, 136, 72, 8, 1)])
+def test_the_counters_of_an_expert_layer_stay(M, N, K, r, pad):
+    """One buffer for adapters' calls and an expert layer's in turn, as a decode loop has it."""
+    E, k, n, T = 20, 3, 136, min(M, 64)
+    x, w, ab, idx, scale = operands(M, N, K, r, 20, 2, M)
+    if pad:   # odd strides: the kernels for any alignment
+        x = torch.nn.functional.pad(x, (0, 1))[:, :K]
+    layer = rand(E, K, seed=1, scale=K ** -0.5), rand(E, n, K, seed=2, scale=K ** -0.5), rand(E, n, K, seed=3, scale=K ** -0.5), rand(E, K, n, seed=4, scale=n ** -0.5)
+    size = max(mb.glu_lora_workspace_bytes(M, N, K, 20, r), mb.linear_lora_workspace_bytes(M, N, K, 20, r), mb.moe_glu_workspace_bytes(T, E, k, n, K))
+    workspace = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    counters = workspace[:mb.MOE_COUNTER_BYTES].zero_()
+    for _ in range(2):
+        Q.assert_glu_lora(mb.glu_lora(x, *w, *ab, idx, scale, workspace=workspace), (x, *w, *ab, idx, scale))
+        assert (counters == 0).all()
+        R.assert_bf16(mb.linear_lora(x, w[0], *ab[:2], idx, scale, workspace=workspace), *Q.adapted(x, w[0], *ab[:2], idx, scale))
+        assert (counters == 0).all()
+        Q.assert_moe(mb.moe_glu(x[:T], *layer, k, workspace=workspace), x[:T], *layer, k, True)
+        assert (counters == 0).all()
+    assert mb.read_device_error() == 0
