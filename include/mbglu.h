@@ -544,7 +544,8 @@ mbglu_status linear_lora(const mbglu_bf16 *x, int64_t ldx,
  * moe_glu -- a whole mixture-of-experts layer of a decode batch: router, choice,
  * the chosen experts' gated projections and down projections, and their weighted
  * sum.  For token t:
- *   l[e]   = sum_k h[t,k] router_w[e,k], the fp32 number nearest to the exact sum
+ *   l[e]   = sum_k h[t,k] router_w[e,k], rounded once to fp32 from a sum that is off by
+ *            at most (K / 32 + 32)^2 2^-48 sum_k |h[t,k] router_w[e,k]|
  *   chosen = the top_k experts by l, largest first, ties to the lowest index
  *   c[j]   = softmax(l)[chosen j], or with renormalize the softmax over the chosen
  *   out[t] = sum_j c[j] ((SiLU(h[t] gate_w[e]^T) * (h[t] up_w[e]^T)) down_w[e]^T)
@@ -565,9 +566,10 @@ mbglu_status linear_lora(const mbglu_bf16 *x, int64_t ldx,
  *              not zero, so that later calls fail too: zero them again.
  *   0 <= T <= MBGLU_MAX_M, 1 <= E <= MBGLU_MOE_MAX_EXPERTS, 1 <= top_k <=
  *   min(E, MBGLU_MOE_MAX_TOP_K), N >= 0, K >= 0.  T == 0: no-op.  N == 0: out = 0.
- * A token's choice does not depend on the others, and neither does its result but
- * for the order in which its sums' parts are added.  A token with a NaN logit gets
- * NaN weights and a NaN result.
+ * Neither a token's choice nor its result depends on the others but for the order in
+ * which the parts of sums are added, which goes by the sizes and, beyond the router, by
+ * what the others chose: it can exchange experts whose logits differ by less than the bound
+ * above.  A token with a NaN logit gets NaN weights and a NaN result.
  * One cooperative kernel where every operand is 16-byte aligned with strides that are
  * multiples of 8 elements and N and K are multiples of 8; other operands take
  * slower kernels.

@@ -825,11 +825,12 @@ def new_moe_workspace(T, E, top_k, N, K, device=None):
 def moe_glu(h, router_w, gate_w, up_w, down_w, top_k, renormalize=True, out=None, ids=None, weights=None, workspace=None,
             stream=None):
     """A mixture-of-experts layer of up to MAX_M tokens: returns (out [T,K] bf16, ids
-    [T,top_k] int32, weights [T,top_k] float32).  The logits h @ router_w.T are the
-    float32 numbers nearest to the exact sums; each token takes the top_k experts
-    (ties to the lowest index) with softmax weights, renormalised over the chosen or
-    not; out is the weighted sum of (SiLU(h @ gate_w[e].T) * (h @ up_w[e].T)) @
-    down_w[e].T.  router_w is [E,K], gate_w and up_w [E,N,K], down_w [E,K,N].
+    [T,top_k] int32, weights [T,top_k] float32).  The logits h @ router_w.T are rounded
+    once to float32, from sums that are off by (K / 32 + 32)^2 2^-48 of their products'
+    magnitudes at most; each token takes the top_k experts (ties to the lowest index) with
+    softmax weights, renormalised over the chosen or not; out is the weighted sum of
+    (SiLU(h @ gate_w[e].T) * (h @ up_w[e].T)) @ down_w[e].T.  router_w is [E,K], gate_w
+    and up_w [E,N,K], down_w [E,K,N].
     The workspace (new_moe_workspace(T, E, top_k, N, K), which a decode loop keeps)
     is allocated and its counters are zeroed here when not given; after a call that sets
     the device error word (read_device_error) one that is kept has to be zeroed again

@@ -1,13 +1,19 @@
-// moe_route.cuh -- the router of the expert layer: logits whose value does not
-// depend on the order of a sum, and a warp's choice of the top experts.
+// moe_route.cuh -- the router of the expert layer: logits whose error is of second order,
+// and a warp's choice of the top experts.
 //
 // An expert is chosen or not, so a logit that is off in its last bit can exchange
-// whole experts.  Products of two bf16 numbers are exact in fp32; their sum is carried
-// as an unevaluated pair s + c (Knuth's two-sum: s the rounded sum, c the sum of the
-// roundings, each of which is exact), whose error is of second order, and rounded once.
-// The logit is then the fp32 number nearest to the exact sum, whatever the order: kernels,
-// batch sizes and grids choose alike.  Six additions for each product: 64 rows x 128
-// experts x 2048 take 118 M operations, 3 us of the part's fp32 rate.
+// whole experts.  Products of two bf16 numbers are exact in fp32 (down to 2^-134, below which they
+// are off by 2^-150 at most); their sum is carried as an unevaluated pair s + c (Knuth's two-sum: s
+// the rounded sum, c the sum of the roundings, each of which is exact) and rounded once.  What
+// is lost are c's own roundings.  The sums that stand n additions behind the first ones have
+// magnitudes of at most S together (S: all products'), their c of n 2^-24 S, and two roundings of
+// each lose 2 n 2^-48 S.  With D additions one behind the other, K / 32 of a lane and fewer than 32
+// joins of lanes and warps, the pair is off by D (D + 1) 2^-48 S at most.  That is below half a step
+// of the logit unless products cancel to less than 2^-10 of S (K = 2048).  It differs with the order
+// of the sum, which differs between the kernels and with the number of tokens, so logits that lie
+// closer together than that may change places there.  Partial sums beyond fp32's range are
+// infinite.  Six additions for each product: 64 rows x 128 experts x 2048 take 118 M operations,
+// 3 us of the part's fp32 rate.
 #pragma once
 #include "glu_math.cuh"
 #include "ptx.cuh"
