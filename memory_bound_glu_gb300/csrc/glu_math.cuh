@@ -27,16 +27,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// x and y as two bf16 terms each, hi + lo, off by 2^-18 (each term by half a step of what is left
-// to it).  hi stops at the largest bf16 number: what is above it in fp32 is left to lo, and so is
-// an infinity, whose second term would else be inf - inf.  NaN is left to lo.
-__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t &hi, uint32_t &lo)
-{
-    constexpr float kMost = 0x1.fep127f;
-    hi = pack_bf16x2(fminf(fmaxf(x, -kMost), kMost), fminf(fmaxf(y, -kMost), kMost));
-    lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
-}
-
 // SiLU(x) = x / (1 + e^-x) = x * e^x / (1 + e^x), evaluated with t = e^-|x| so
 // that nothing overflows: for x < -88.7 the first form's e^-x is +inf in fp32
 // and would flush SiLU to -0, although x * e^x is still a normal bf16 value

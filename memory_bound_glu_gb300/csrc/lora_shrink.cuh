@@ -17,6 +17,7 @@
 #include "lora_generic.cuh"
 #include "stack_copy.cuh"
 #include "tcgen05.cuh"
+#include "two_terms.cuh"
 
 namespace mbglu {
 

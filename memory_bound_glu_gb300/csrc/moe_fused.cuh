@@ -37,6 +37,7 @@
 #include "moe_route.cuh"
 #include "stack_copy.cuh"
 #include "tc_pair.cuh"
+#include "two_terms.cuh"
 
 namespace mbglu {
 
