@@ -25,6 +25,16 @@ inline int row_align(const void *p, int64_t ld, int elem)
     return aligned(p, 32) && ld * elem % 32 == 0 ? 2 : aligned(p, 16) && ld * elem % 16 == 0 ? 1 : 0;
 }
 
+// Places in workspaces are multiples of kAlign bytes.
+constexpr int64_t kAlign = 256;
+inline int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
+
+// bytes from the first element of 16-bit [count][rows][cols] to the end of its last
+inline int64_t extent3(int64_t count, int64_t rows, int64_t cols, int64_t stride, int64_t ld)
+{
+    return count <= 0 || rows <= 0 || cols <= 0 ? 0 : (count - 1) * stride * 2 + extent(rows, cols, ld, 2);
+}
+
 // The current device's SM count, after `setup` (attributes of the unit's
 // kernels) has run once on it.
 struct DeviceTable {
@@ -52,10 +62,14 @@ inline mbglu_status launched(cudaError_t e) { return e == cudaSuccess ? MBGLU_OK
 
 // Launch configuration with the process's launch policy: under PDL a kernel may
 // be scheduled while its predecessor drains.  Every kernel launched here waits for the
-// predecessor before it touches global memory, but for fp8_tall_kernel: under the
-// prefetch policy it copies its first weights before the wait, so a kernel of the
-// library that writes weights (quant_weight_kernel) neither releases its dependents
-// early nor leaves its stores to be performed later.
+// predecessor before it touches global memory, but for two:
+//   fp8_tall_kernel and lora_pair_kernel copy their first weights before the wait under the
+//     prefetch policy, so a kernel of the library that writes weights (quant_weight_kernel)
+//     neither releases its dependents early nor leaves its stores to be performed later;
+//   lora_pair_kernel behind a kernel that forms p reads the call's operands and releases its own
+//     dependents while that one runs, which is sound because that one has waited for its
+//     predecessor before it releases: lora_shrink_kernel and lora_shrink_tc_kernel keep
+//     the release behind the wait.
 struct Launch {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

@@ -13,9 +13,6 @@ namespace {
 
 using namespace mbglu_host;
 
-constexpr int64_t kAlign = 256;
-int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
-
 constexpr int kFewRows = 64;   // a decode batch
 constexpr int kJoinRows = 320;
 
@@ -146,12 +143,6 @@ int64_t lora_bytes(int sides, int M, int N, int K, int R)
 }
 
 bool bad_rank(int adapters, int R) { return adapters < 0 || adapters > kMostSize || R < 0 || R > MBGLU_LORA_MAX_RANK; }
-
-// bytes from the first element of [count][rows][cols] to the end of its last
-int64_t extent3(int64_t count, int64_t rows, int64_t cols, int64_t stride, int64_t ld)
-{
-    return count <= 0 || rows <= 0 || cols <= 0 ? 0 : (count - 1) * stride * 2 + extent(rows, cols, ld, 2);
-}
 
 // The cluster's blocks split the inner dimension: as many as leave a warp about five steps,
 // so that all of its loads are on the way together, and no more than `most` blocks in all.

@@ -12,12 +12,13 @@
 //   * 32 rows of several adapters are left to the epilogue: for each adapter among 16 of
 //     them a warp's own tensor cores (mma.sync) multiply its 32 rows of B with all 16
 //     tokens' p, and a token takes the product with its own adapter (lora_term); up to rank
-//     16 a lane reads the row of B of its output for each token (lora_term_rows).
+//     16, and in a decode batch, a lane reads the row of B of its output for each token
+//     (lora_term_rows).
 // A prompt's rows are nearly all of the first kind, a chunk of many short requests has the
 // second.
 //
-// For few rows no kernel of its own forms p: the epilogue's warps do, while the products run
-// (lora_dot8).  Where the join uses p, the blocks share the work; where a block needs it itself
+// For most batches up to 320 rows no kernel of its own forms p: the epilogue's warps do, while
+// the products run (lora_dot8).  Where the join uses p, the blocks share the work; where a block needs it itself
 // and it is small (a token or some), every block forms all of it from L2.
 //
 // Tiles that would leave SM pairs without work are cut along the inner dimension: their
@@ -307,8 +308,9 @@ __device__ __forceinline__ void lora_inside(const LoraParams &p, int inside, int
     }
 }
 
-// The same for rows that mostly have an adapter each, of rank 16 at most (a row of more spreads
-// a warp's load over 32 lines): a lane has one output n, reads its row
+// The same for rows that mostly have an adapter each, best of rank 16 at most (a row of more
+// spreads a warp's load over 32 lines; single rows, and decode batches that the join does not
+// take, come here with more): a lane has one output n, reads its row
 // of each token's B, eight tokens' together, and adds the term to y.  p of 16 tokens and 16
 // columns is staged in shared memory (stage, 256 floats), on the way beside B.
 __device__ __forceinline__ void lora_term_rows(const LoraParams &p, int mine, const float *all_p, int d, int sides, int64_t m0, int64_t n,

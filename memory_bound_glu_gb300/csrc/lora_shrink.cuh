@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const Lo
     const int s0 = steps * w0 / warps, s1 = steps * (w0 + 1) / warps;
     float *total = shrink_part + kShrinkWarps * kRows * kPitch;
     grid_dependency_wait();
-    grid_launch_dependents();
+    grid_launch_dependents();   // behind the wait: lora_pair_kernel reads x then (LoraPairParams::early)
     for (int64_t group = blockIdx.y; group * kRows < p.M; group += gridDim.y) {
         const int64_t m0 = group * kRows;
         const int mine = lane < kRows ? lora_adapter(p, m0 + lane) : -1;   // kRows <= 32

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kShrinkTcThreads, 1) lora_shrink_tc_kernel(con
     const uint32_t tmem = *slot;
     bool ok = true;
     grid_dependency_wait();
-    grid_launch_dependents();
+    grid_launch_dependents();   // behind the wait: lora_pair_kernel reads x then (LoraPairParams::early)
 
     if (warp == 0) {
         LoraDistinct adapters(p.l, m0);

@@ -11,9 +11,6 @@ namespace {
 
 using namespace mbglu_host;
 
-constexpr int64_t kAlign = 256;
-int64_t padded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
-
 constexpr int kMostBlocks = 160;   // of the fused kernel: what the workspace has room for
 
 // Places of the workspace, in bytes.
@@ -45,12 +42,6 @@ bool bad_moe(int T, int E, int top_k, int N, int K)
            bad_sizes(N, K);
 }
 
-// bytes from the first element of [E][rows][cols] to the end of its last
-int64_t extent3(int64_t E, int64_t rows, int64_t cols, int64_t stride, int64_t ld)
-{
-    return rows <= 0 || cols <= 0 ? 0 : (E - 1) * stride * 2 + extent(rows, cols, ld, 2);
-}
-
 mbglu_status launch_generic(const mbglu::MoeGeneric &p, cudaStream_t stream)
 {
     const auto blocks = [](int64_t n) { return static_cast<unsigned>((n + 7) / 8); };
@@ -72,8 +63,7 @@ mbglu_status launch_generic(const mbglu::MoeGeneric &p, cudaStream_t stream)
 
 cudaError_t setup_fused()
 {
-    return cudaFuncSetAttribute(mbglu::moe_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(std::max(mbglu::moe_smem(16), mbglu::moe_smem(64))));
+    return cudaFuncSetAttribute(mbglu::moe_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mbglu::kMoeSmemMost));
 }
 
 bool stackable(const void *p, int64_t stride, int64_t ld, int count)

@@ -1,10 +1,10 @@
 // moe_fused.cuh -- the expert layer of a decode batch in one cooperative kernel: one
-// block per SM, all resident at once, that meet at four grid barriers.
+// block per SM, all resident at once, that meet at three to five grid barriers.
 //
 //   1  logits, a warp per expert and four tokens                        | barrier
 //   2  the choice, by every block for itself, or of many tokens by a block each   (| barrier)
 //   3  gated projections of the chosen experts                          | barrier
-//   4  activation, as two bf16 terms                                    | barrier
+//   4  activation, as two bf16 terms                                    (| barrier, unless 3 does it)
 //   5  down projections                                                 | barrier
 //   6  weighted sum over a token's experts
 //
@@ -101,7 +101,7 @@ struct alignas(16) MoeShared {
 
 constexpr uint32_t kMoeHeader = (sizeof(MoeShared) + 1023) / 1024 * 1024;
 __host__ __device__ constexpr uint32_t moe_stage_bytes(int pad) { return kMoeUnit + 256u * static_cast<uint32_t>(pad); }
-constexpr uint32_t kMoeSmemMost = 227 * 1024;
+constexpr uint32_t kMoeSmemMost = 227 * 1024;     // no number of tokens takes more
 __host__ __device__ constexpr int moe_stages(int pad)
 {
     const int n = static_cast<int>((kMoeSmemMost - kMoeHeader - 1024) / moe_stage_bytes(pad));
