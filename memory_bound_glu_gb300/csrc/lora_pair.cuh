@@ -26,8 +26,8 @@
 // epilogue, the term in fp32 FMAs.  Most decode batches have all of their tiles there.
 //
 // What bounds it: the weights' bytes for few rows (1 row, K = 2560, N = 9728, R = 16: 19 us,
-// 14.8 of them the bytes at the copy rate), the MMAs for many (4096 rows, R = 64: 253 us, 92% of
-// them the shared product's), between them the terms of rows of several adapters, whose loads
+// 14.8 of them the bytes at the copy rate), the MMAs for many (4096 rows, R = 64: 281 us, 230 of
+// them the shared product's, 20 the terms', 18 p's kernel), between them the terms of rows of several adapters, whose loads
 // eight warps per SM wait for (333 rows of 37 requests, K = 1000, N = 2504: 8 of 23 us).
 #pragma once
 #include "lora_shrink.cuh"
